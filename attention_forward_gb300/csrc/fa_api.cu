@@ -714,6 +714,35 @@ fa_status_t check_call(const void* q, const void* k, const void* v, const void* 
   return current_device(&d, nullptr);
 }
 
+fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out) {
+  DeviceState* d = nullptr;
+  const fa_status_t st = current_device(&d, nullptr);
+  if (st != FA_OK) return st;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return FA_ERR_CUDA;
+  *out = LaunchEnv{d->sm_count, d->status, g_watchdog_ns.load(),
+                   cap != cudaStreamCaptureStatusNone};
+  return FA_OK;
+}
+
+fa_status_t take_sched_slot(bool captured, unsigned long long** out) {
+  DeviceState* d = nullptr;
+  const fa_status_t st = current_device(&d, nullptr);
+  if (st != FA_OK) return st;
+  *out = sched_slot(*d, captured);
+  return FA_OK;
+}
+
+fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int heads,
+                        int box_rows, bool bf16) {
+  const fa_status_t st = get_encoder();
+  return st != FA_OK ? st : encode_3d(m, base, D, rows, heads, box_rows, bf16);
+}
+
+int choose_prefill_splits(int heads, int rows, int Skv, int sm_count) {
+  return prefill_splits(heads, rows, Skv, sm_count, 0);
+}
+
 }  // namespace fa
 
 extern "C" {

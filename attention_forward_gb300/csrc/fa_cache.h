@@ -1,0 +1,69 @@
+// fa_cache.h -- parameter blocks, limits and launch entry points of the 4-bit
+// key/value cache (internal).
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace fa {
+
+// Channels that share one scale and minimum.
+constexpr int kCacheGroup = 32;
+// Values beyond this magnitude are held as it: 15 scales above the smallest
+// minimum stay within fp16.
+constexpr float kCacheLimit = 61440.f;
+constexpr unsigned kStatusBadIndex = 1;  // FA_ERR_INVALID_ARG, from a kernel
+
+// The four arrays of a cache: rows of (page, kv head, slot).
+struct CachePool {
+  uint8_t* codes[2];    // K, V: [num_pages, Hkv, page_size, D / 2]
+  uint32_t* params[2];  // K, V: [num_pages, Hkv, page_size, D / 32] (scale, minimum) fp16 pairs
+};
+
+struct CacheCopyParams {
+  CachePool pool;
+  void* rows[2];          // K, V: [B, Hkv, S, D] 16-bit
+  const int* page_table;  // [B, max_pages]
+  const int* start;       // [B] or null (0)
+  const int* count;       // [B] or null (S)
+  unsigned* status;
+  long long n_rows;       // B * Hkv * S
+  int Hkv, S, num_pages, page_shift, max_pages;
+};
+
+struct CacheAttnParams {
+  CachePool pool;
+  const void* q;          // [B, H, Sq, D]
+  void* o;
+  float* lse;             // [B, H, Sq]
+  float* part_o;          // n_splits > 1: [n_splits, B * H * Sq, D] fp32, O / l
+  float* part_lse;        // n_splits > 1: [n_splits, B * H * Sq]
+  const int* page_table;
+  const int* length;      // [B]
+  const float* slopes;    // [H] or null
+  unsigned* status;
+  int B, H, Hkv, Sq;
+  int max_length;         // lengths past it are limited to it
+  int rows;               // (H / Hkv) * Sq query rows per kv head
+  int n_row_blocks;
+  int n_splits, keys_per_split;
+  int num_pages, page_shift, max_pages;
+  float scale;
+  float cap;              // cap > 0: score = cap * tanh(score / cap)
+  float inv_cap, cap_arg; // 1 / cap, 2 log2(e) / cap
+};
+
+cudaError_t launch_cache_write(int D, bool bf16, const CacheCopyParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(int D, bool bf16, const CacheCopyParams& p, cudaStream_t stream);
+
+// Query rows one CTA of the cache attention takes (8 or 16 by the rows per kv
+// head) and the keys it covers per round of its warps.
+int cache_attn_row_block(int rows);
+constexpr int kCacheAttnWarps = 4;
+constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;
+// Keys one split may cover: its page numbers are held in shared memory.
+constexpr int kCacheAttnMaxKeys = 16384;
+cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, cudaStream_t stream);
+
+}  // namespace fa

@@ -1,0 +1,211 @@
+// fa_cache_api.cu -- the 4-bit cache's entry points: argument checks, the key
+// split of the attention, and the launches.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "fa_cache.h"
+#include "fa_host.h"
+
+namespace {
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct PageShape {
+  int num_pages, page_size, max_pages;
+};
+
+bool pages_ok(const PageShape& s) {
+  return s.num_pages >= 1 && s.max_pages >= 1 && s.page_size >= 16 && s.page_size <= 1024 &&
+         (s.page_size & (s.page_size - 1)) == 0 &&
+         static_cast<long long>(s.max_pages) * s.page_size <= (1 << 24);
+}
+
+int shift_of(int n) {
+  int k = 0;
+  while ((1 << k) < n) ++k;
+  return k;
+}
+
+// The checks common to the three calls: sizes, pointers, then what is not
+// supported, as fa_fwd orders them.
+fa_status_t check_cache(const void* const (&pool)[4], const int* page_table, int B, int heads,
+                        int Hkv, int S, int D, const PageShape& s, int dtype) {
+  for (const void* p : pool)
+    if (!p || !aligned(p, 16)) return FA_ERR_INVALID_ARG;
+  if (!page_table || !aligned(page_table, 4)) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || heads < 1 || S < 1 || S > (1 << 24) || heads % Hkv != 0)
+    return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * heads >= 65536) return FA_ERR_INVALID_ARG;
+  if (!pages_ok(s)) return FA_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return FA_ERR_UNSUPPORTED;
+  if (dtype != FA_F16 && dtype != FA_BF16) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa::CachePool make_pool(const void* const (&pool)[4]) {
+  fa::CachePool c;
+  for (int n = 0; n < 2; ++n) {
+    c.codes[n] = static_cast<uint8_t*>(const_cast<void*>(pool[2 * n]));
+    c.params[n] = static_cast<uint32_t*>(const_cast<void*>(pool[2 * n + 1]));
+  }
+  return c;
+}
+
+fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const void* v,
+                 const int* page_table, const int* start, const int* count, int B, int Hkv, int S,
+                 int D, const PageShape& s, int dtype, cudaStream_t stream) {
+  fa_status_t st = check_cache(pool, page_table, B, Hkv, Hkv, S, D, s, dtype);
+  if (st != FA_OK) return st;
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(count, 4))
+    return FA_ERR_INVALID_ARG;
+  const long long n_rows = static_cast<long long>(B) * Hkv * S;
+  if (n_rows * (D / 8) > 256LL * 0x7fffffffLL) return FA_ERR_INVALID_ARG;  // the grid
+  fa::LaunchEnv env{};
+  if ((st = fa::launch_env(stream, &env)) != FA_OK) return st;
+  fa::CacheCopyParams p{};
+  p.pool = make_pool(pool);
+  p.rows[0] = const_cast<void*>(k);
+  p.rows[1] = const_cast<void*>(v);
+  p.page_table = page_table;
+  p.start = start;
+  p.count = count;
+  p.status = env.status;
+  p.n_rows = n_rows;
+  p.Hkv = Hkv;
+  p.S = S;
+  p.num_pages = s.num_pages;
+  p.page_shift = shift_of(s.page_size);
+  p.max_pages = s.max_pages;
+  const cudaError_t e = write ? fa::launch_cache_write(D, dtype == FA_BF16, p, stream)
+                              : fa::launch_cache_read(D, dtype == FA_BF16, p, stream);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+struct Split {
+  int n_splits, keys_per_split;
+  size_t bytes;
+};
+
+// Key ranges of the attention: enough CTAs for about two rounds over four a
+// multiprocessor, at least 256 keys each.
+Split plan_split(int B, int H, int Hkv, int Sq, int D, int max_length, int sm_count) {
+  const int rows = (H / Hkv) * Sq;
+  const int block = fa::cache_attn_row_block(rows);
+  const long long units = static_cast<long long>(B) * Hkv * ((rows + block - 1) / block);
+  const long long slots = 8LL * (sm_count > 0 ? sm_count : 152);
+  long long kps = (units * max_length + slots - 1) / slots;
+  kps = std::max<long long>(kps, 256);
+  kps = (kps + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys * fa::kCacheAttnKeys;
+  kps = std::min<long long>(kps, fa::kCacheAttnMaxKeys);
+  Split s{};
+  s.keys_per_split = static_cast<int>(kps);
+  s.n_splits = static_cast<int>((max_length + kps - 1) / kps);
+  if (s.n_splits > 1) {
+    const size_t n = static_cast<size_t>(s.n_splits) * B * H * Sq;
+    s.bytes = up256(n * D * sizeof(float)) + up256(n * sizeof(float));
+  }
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_cache_write(const void* k, const void* v, void* k_codes, void* k_params,
+                           void* v_codes, void* v_params, const int* page_table, const int* start,
+                           const int* count, int B, int Hkv, int S, int D, int num_pages,
+                           int page_size, int max_pages, int dtype, fa_stream_t stream) {
+  return copy(true, {k_codes, k_params, v_codes, v_params}, k, v, page_table, start, count, B, Hkv,
+              S, D, {num_pages, page_size, max_pages}, dtype, reinterpret_cast<cudaStream_t>(stream));
+}
+
+fa_status_t fa_cache_read(const void* k_codes, const void* k_params, const void* v_codes,
+                          const void* v_params, const int* page_table, const int* start,
+                          const int* count, void* k, void* v, int B, int Hkv, int S, int D,
+                          int num_pages, int page_size, int max_pages, int dtype,
+                          fa_stream_t stream) {
+  return copy(false, {k_codes, k_params, v_codes, v_params}, k, v, page_table, start, count, B,
+              Hkv, S, D, {num_pages, page_size, max_pages}, dtype,
+              reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D, int page_size, int max_pages,
+                                int max_length) {
+  const PageShape s{1, page_size, max_pages};
+  if (B < 1 || H < 1 || Hkv < 1 || Sq < 1 || Sq > 256 || H % Hkv != 0 || (D != 64 && D != 128) ||
+      static_cast<long long>(B) * H >= 65536 || !pages_ok(s) || max_length < 0)
+    return 0;
+  fa::LaunchEnv env{};
+  if (fa::launch_env(nullptr, &env) != FA_OK) env.sm_count = 0;
+  const int room = max_pages * page_size;
+  return plan_split(B, H, Hkv, Sq, D, max_length ? std::min(max_length, room) : room, env.sm_count)
+      .bytes;
+}
+
+fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_params,
+                         const void* v_codes, const void* v_params, const int* page_table,
+                         const int* length, void* o, float* lse, int B, int H, int Hkv, int Sq,
+                         int D, int num_pages, int page_size, int max_pages, int max_length,
+                         float scale, int dtype, float softcap, const float* slopes,
+                         void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  const PageShape s{num_pages, page_size, max_pages};
+  fa_status_t st = check_cache({k_codes, k_params, v_codes, v_params}, page_table, B, H, Hkv, Sq,
+                               D, s, dtype);
+  if (st != FA_OK) return st;
+  if (!q || !o || !lse || !length || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) ||
+      !aligned(length, 4) || !aligned(slopes, 4))
+    return FA_ERR_INVALID_ARG;
+  if (Sq > 256 || max_length < 0) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  if (!fa::softcap_ok(softcap)) return FA_ERR_INVALID_ARG;
+  cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+  fa::LaunchEnv env{};
+  if ((st = fa::launch_env(strm, &env)) != FA_OK) return st;
+  const int room = max_pages * page_size;
+  const int most = max_length ? std::min(max_length, room) : room;
+  const Split split = plan_split(B, H, Hkv, Sq, D, most, env.sm_count);
+  if (split.bytes > 0 && (!workspace || workspace_bytes < split.bytes || !aligned(workspace, 256)))
+    return FA_ERR_WORKSPACE;
+
+  fa::CacheAttnParams p{};
+  p.pool = make_pool({k_codes, k_params, v_codes, v_params});
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  if (split.n_splits > 1) {
+    const size_t n = static_cast<size_t>(split.n_splits) * B * H * Sq;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(n * D * sizeof(float)));
+  }
+  p.page_table = page_table;
+  p.length = length;
+  p.slopes = slopes;
+  p.status = env.status;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.Sq = Sq;
+  p.max_length = most;
+  p.rows = (H / Hkv) * Sq;
+  const int block = fa::cache_attn_row_block(p.rows);
+  p.n_row_blocks = (p.rows + block - 1) / block;
+  p.n_splits = split.n_splits;
+  p.keys_per_split = split.keys_per_split;
+  p.num_pages = num_pages;
+  p.page_shift = shift_of(page_size);
+  p.max_pages = max_pages;
+  p.scale = scale;
+  p.cap = softcap;
+  if (softcap > 0.f) {
+    p.inv_cap = static_cast<float>(1.0 / softcap);
+    p.cap_arg = static_cast<float>(2.8853900817779268 / softcap);
+  }
+  const long long grid = static_cast<long long>(p.n_splits) * p.n_row_blocks * B * Hkv;
+  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  return fa::launch_cache_attn(D, dtype == FA_BF16, p, strm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

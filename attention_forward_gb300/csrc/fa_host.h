@@ -1,6 +1,9 @@
 // fa_host.h -- host-side helpers of fa_api.cu that other host translation
 // units of the library use (internal; no device code).
 #pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
 #include "../../include/fa.h"
 
 namespace fa {
@@ -12,6 +15,9 @@ fa_status_t check_call(const void* q, const void* k, const void* v, const void* 
                        const void* lse, int B, int H, int Sq, int Skv, int D,
                        float scale, int dtype);
 
+// A tanh cap is off (0) or within the range that the kernels' fp32 terms cover.
+inline bool softcap_ok(float c) { return c == 0.f || (c >= 1e-6f && c <= 1e6f); }
+
 // The current device's support check alone (compute capability 10.3).
 fa_status_t check_device();
 
@@ -21,5 +27,26 @@ fa_status_t check_device();
 // cudaDeviceReset the primary context is a new one, with a new id, and every
 // cached address must be looked up again.
 unsigned long long context_id();
+
+// What a launch on the current device needs, after its support check.
+struct LaunchEnv {
+  int sm_count;
+  unsigned* status;               // device status word
+  unsigned long long timeout_ns;  // watchdog limit
+  bool captured;                  // the stream is being captured
+};
+fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out);
+
+// A scheduler slot of the current device for one persistent launch
+// (PrefillParams::sched).
+fa_status_t take_sched_slot(bool captured, unsigned long long** out);
+
+// TMA descriptor of a [heads, rows, D] 16-bit tensor, boxes of 64 columns x
+// box_rows.
+fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int heads,
+                        int box_rows, bool bf16);
+
+// The key split fa_fwd would choose for `heads` heads of `rows` query rows.
+int choose_prefill_splits(int heads, int rows, int Skv, int sm_count);
 
 }  // namespace fa

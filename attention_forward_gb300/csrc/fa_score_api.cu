@@ -1,0 +1,235 @@
+// fa_score_api.cu -- fa_fwd_score: argument checks, the plan of rows, tiles and
+// key ranges, the tanh coefficients, and the launches.
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "fa_host.h"
+#include "fa_launch.h"
+#include "fa_score.h"
+
+namespace fa {
+
+cudaError_t score_num_regs_d128(bool bf16, int* regs);
+cudaError_t score_num_regs_d64(bool bf16, int* regs);
+cudaError_t launch_score_d128(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                              const CUtensorMap&, const ScoreParams&, int, cudaStream_t);
+cudaError_t launch_score_d64(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                             const CUtensorMap&, const ScoreParams&, int, cudaStream_t);
+
+cudaError_t score_num_regs(int D, bool bf16, int* regs) {
+  return D == 128 ? score_num_regs_d128(bf16, regs) : score_num_regs_d64(bf16, regs);
+}
+cudaError_t launch_score(int D, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                         const CUtensorMap& v, const CUtensorMap& o, const ScoreParams& p,
+                         int grid, cudaStream_t stream) {
+  return D == 128 ? launch_score_d128(bf16, q, k, v, o, p, grid, stream)
+                  : launch_score_d64(bf16, q, k, v, o, p, grid, stream);
+}
+
+}  // namespace fa
+
+namespace {
+
+// Query tokens up to which the heads of a group are rows of one tile: a tile
+// of one head would be at most half full.
+constexpr int kPackTokens = 128;
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+struct Plan {
+  int packed, row_heads, rows, n_qtiles, n_key_tiles, n_stages;
+  int n_splits, tiles_per_split;
+  size_t doc_bytes, split_bytes;  // the workspace's two parts, documents first
+};
+
+Plan make_plan(int B, int H, int Hkv, int Sq, int Skv, int D, bool documents, int sm_count) {
+  Plan p{};
+  const int group = H / Hkv;
+  p.packed = group > 1 && Sq <= kPackTokens ? 1 : 0;
+  p.row_heads = p.packed ? B * Hkv : B * H;
+  p.rows = p.packed ? group * Sq : Sq;
+  p.n_qtiles = (p.rows + fa::kRowsPerCta - 1) / fa::kRowsPerCta;
+  p.n_key_tiles = (Skv + fa::kBN - 1) / fa::kBN;
+  p.n_stages = (p.rows + fa::kBM - 1) / fa::kBM;
+  const long long all_rows = static_cast<long long>(p.row_heads) * p.rows;
+  int s = fa::choose_prefill_splits(p.row_heads, p.rows, Skv, sm_count);
+  if (all_rows > 0x7fffffffLL) s = 1;  // the combine kernel counts rows in an int
+  p.tiles_per_split = (p.n_key_tiles + s - 1) / s;
+  p.n_splits = (p.n_key_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+  if (documents)
+    p.doc_bytes = up256(static_cast<size_t>(B) * p.n_key_tiles * sizeof(int)) +
+                  up256(static_cast<size_t>(B) * p.n_key_tiles * sizeof(int2)) +
+                  up256(static_cast<size_t>(B) * p.n_stages * sizeof(int2));
+  if (p.n_splits > 1) {
+    const size_t rows = static_cast<size_t>(p.n_splits) * static_cast<size_t>(all_rows);
+    p.split_bytes = up256(rows * D * sizeof(float)) + up256(rows * sizeof(float));
+  }
+  return p;
+}
+
+bool sizes_ok(int B, int H, int Hkv, int Sq, int Skv) {
+  return B >= 1 && H >= 1 && Hkv >= 1 && Sq >= 1 && Skv >= 1 && H % Hkv == 0 &&
+         static_cast<long long>(B) * H < 65536 && Sq <= (1 << 24) && Skv <= (1 << 24);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// cap tanh(s scale / cap) log2(e) = s (c0 + c1 s^2 + ... + c4 s^8) while
+// |s scale / cap| <= y_max.  The terms are the minimax fit (exchange
+// algorithm) of an odd polynomial to tanh on [-0.75, 0.75], error 2e-7.
+void plan_cap(fa::ScoreParams& p, double scale, double cap) {
+  static const double kTanh[fa::kCapTerms] = {0.99999723, -0.33323077, 0.13226092, -0.04928045,
+                                              0.01231884};
+  // |y| up to which the terms from i on stay under 2e-7
+  static const double kWithout[fa::kCapTerms] = {0.0, 0.008, 0.07, 0.17, 0.29};
+  constexpr double kLog2e = 1.4426950408889634;
+  const double k = scale / cap;
+  double y_max = fa::kCapPolyMax;
+  for (int i = 0; i < fa::kCapTerms; ++i) {
+    const double pw = std::pow(k, 2 * i);
+    if (pw * scale < 1e-36 && i > 0) {  // below fp32: the cap is far above the scores
+      p.cap_poly[i] = 0.f;
+      y_max = std::min(y_max, kWithout[i]);
+    } else {
+      p.cap_poly[i] = static_cast<float>(kTanh[i] * pw * scale * kLog2e);
+    }
+  }
+  const double u = (y_max / k) * (y_max / k);
+  p.cap_u_max = static_cast<float>(std::min(u, static_cast<double>(FLT_MAX)));
+  p.cap_arg = static_cast<float>(2.0 * kLog2e * k);
+  p.cap_log2 = static_cast<float>(cap * kLog2e);
+  // scores far above the cap: k^8 would leave fp32, and nothing is left of
+  // the polynomial's range
+  p.cap_mode = k <= 1e3 && scale <= 1e3 ? 1 : 2;
+}
+
+}  // namespace
+
+extern "C" size_t fa_score_workspace_bytes(int B, int H, int Hkv, int Sq, int Skv, int D,
+                                           int documents) {
+  if (!sizes_ok(B, H, Hkv, Sq, Skv) || (D != 64 && D != 128)) return 0;
+  fa::LaunchEnv env{};
+  if (fa::launch_env(nullptr, &env) != FA_OK) env.sm_count = 0;
+  const Plan p = make_plan(B, H, Hkv, Sq, Skv, D, documents != 0, env.sm_count);
+  return p.doc_bytes + p.split_bytes;
+}
+
+extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v, void* o,
+                                    float* lse, int B, int H, int Hkv, int Sq, int Skv, int D,
+                                    float scale, int causal, int dtype, float softcap,
+                                    const float* slopes, const int* doc_q, const int* doc_k,
+                                    const int* prefix, void* workspace, size_t workspace_bytes,
+                                    fa_stream_t stream) {
+  // the checks that fa_fwd makes, then those of what is new
+  if (!sizes_ok(B, H, Hkv, Sq, Skv)) return FA_ERR_INVALID_ARG;
+  if (!fa::softcap_ok(softcap)) return FA_ERR_INVALID_ARG;
+  if ((doc_q == nullptr) != (doc_k == nullptr)) return FA_ERR_INVALID_ARG;
+  if (prefix && !causal) return FA_ERR_INVALID_ARG;
+  if (!aligned4(slopes) || !aligned4(doc_q) || !aligned4(doc_k) || !aligned4(prefix))
+    return FA_ERR_INVALID_ARG;
+  fa_status_t st = fa::check_call(q, k, v, o, lse, B, H, Sq, Skv, D, scale, dtype);
+  if (st != FA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  fa::LaunchEnv env{};
+  if ((st = fa::launch_env(s, &env)) != FA_OK) return st;
+  const bool bf16 = dtype == FA_BF16;
+  {
+    // the kernel's register split assumes 128 registers a thread
+    static std::mutex mu;
+    static bool ok[2][2] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ok[D == 128][bf16]) {
+      int regs = 0;
+      if (fa::score_num_regs(D, bf16, &regs) != cudaSuccess) return FA_ERR_CUDA;
+      if (regs != 128) return FA_ERR_UNSUPPORTED;
+      ok[D == 128][bf16] = true;
+    }
+  }
+
+  Plan plan = make_plan(B, H, Hkv, Sq, Skv, D, doc_k != nullptr, env.sm_count);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA_ERR_WORKSPACE;
+  const size_t have = workspace ? workspace_bytes : 0;
+  if (have < plan.doc_bytes) return FA_ERR_WORKSPACE;
+  if (have < plan.doc_bytes + plan.split_bytes) {
+    plan.n_splits = 1;
+    plan.tiles_per_split = plan.n_key_tiles;
+  }
+
+  fa::ScoreParams p{};
+  p.lse = lse;
+  p.status = env.status;
+  p.timeout_ns = env.timeout_ns;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.Sq = Sq;
+  p.Skv = Skv;
+  p.packed = plan.packed;
+  p.row_heads = plan.row_heads;
+  p.rows = plan.rows;
+  p.one_stage = plan.rows <= fa::kBM ? 1 : 0;
+  p.n_qtiles = plan.n_qtiles;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  if (softcap > 0.f) plan_cap(p, scale, softcap);
+  p.slopes = slopes;
+  p.prefix = prefix;
+  p.n_splits = plan.n_splits;
+  p.tiles_per_split = plan.tiles_per_split;
+  char* ws = static_cast<char*>(workspace);
+  if (doc_k) {
+    fa::DocParams dp{};
+    dp.doc_q = doc_q;
+    dp.doc_k = doc_k;
+    dp.tile_doc = reinterpret_cast<int*>(ws);
+    ws += up256(static_cast<size_t>(B) * plan.n_key_tiles * sizeof(int));
+    dp.tile_range = reinterpret_cast<int2*>(ws);
+    ws += up256(static_cast<size_t>(B) * plan.n_key_tiles * sizeof(int2));
+    dp.stage_tiles = reinterpret_cast<int2*>(ws);
+    ws += up256(static_cast<size_t>(B) * plan.n_stages * sizeof(int2));
+    dp.B = B;
+    dp.Sq = Sq;
+    dp.Skv = Skv;
+    dp.rows = plan.rows;
+    dp.n_key_tiles = plan.n_key_tiles;
+    dp.n_stages = plan.n_stages;
+    p.doc_q = doc_q;
+    p.doc_k = doc_k;
+    p.tile_doc = dp.tile_doc;
+    p.stage_tiles = dp.stage_tiles;
+    p.n_key_tiles = plan.n_key_tiles;
+    p.n_stages = plan.n_stages;
+    if (fa::launch_doc_tiles(dp, s) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  const size_t rows = static_cast<size_t>(plan.row_heads) * static_cast<size_t>(plan.rows);
+  if (plan.n_splits > 1) {
+    p.part_o = reinterpret_cast<float*>(ws);
+    p.part_lse = reinterpret_cast<float*>(ws + up256(plan.n_splits * rows * D * sizeof(float)));
+  }
+  const long long n_items = static_cast<long long>(plan.n_qtiles) * plan.row_heads * plan.n_splits;
+  if (n_items > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
+  p.n_items = static_cast<int>(n_items);
+
+  const int kv_heads = B * Hkv;
+  CUtensorMap tq, tk, tv, to;
+  if ((st = fa::encode_rows(&tq, q, D, plan.rows, plan.row_heads, fa::kBM, bf16)) != FA_OK) return st;
+  if ((st = fa::encode_rows(&tk, k, D, Skv, kv_heads, fa::kBN, bf16)) != FA_OK) return st;
+  if ((st = fa::encode_rows(&tv, v, D, Skv, kv_heads, fa::kBN, bf16)) != FA_OK) return st;
+  if ((st = fa::encode_rows(&to, o, D, plan.rows, plan.row_heads, 32, bf16)) != FA_OK) return st;
+  if ((st = fa::take_sched_slot(env.captured, &p.sched)) != FA_OK) return st;
+  const int grid = static_cast<int>(std::min<long long>(n_items, env.sm_count > 0 ? env.sm_count : 1));
+  if (fa::launch_score(D, bf16, tq, tk, tv, to, p, grid, s) != cudaSuccess) return FA_ERR_CUDA;
+  if (plan.n_splits > 1) {
+    fa::DecodeParams c{};
+    c.o = o;
+    c.lse = lse;
+    c.part_o = p.part_o;
+    c.part_lse = p.part_lse;
+    c.BH = static_cast<int>(rows);
+    c.n_splits = plan.n_splits;
+    if (fa::launch_decode_combine(D, bf16, c, s) != cudaSuccess) return FA_ERR_CUDA;
+  }
+  return FA_OK;
+}

@@ -2,7 +2,8 @@
  * fa.h -- C ABI of the GB300 (sm_103a) fused attention forward library,
  * libfa_gb300.so.
  *
- * Operation (every entry point below computes it):
+ * Operation (the fa_fwd entry points compute it; fa_fwd_score and fa_fwd_cache
+ * compute it with the scores, masks and cache that they describe):
  *   for each batch b, head h and query row i
  *     O[b,h,i,:]  = sum_j softmax_j(scale * <Q[b,h,i,:], K[b,h,j,:]>) V[b,h,j,:]
  *     LSE[b,h,i]  = ln sum_j exp(scale * <Q[b,h,i,:], K[b,h,j,:]>)
@@ -274,6 +275,135 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
                                  void *o, float *lse, int B, int H, int Skv,
                                  int D, float scale, int dtype,
                                  fa_stream_t stream);
+
+/*
+ * fa_fwd_score -- the forward pass with modified scores, on grouped heads.
+ *   q [B, H, Sq, D], o [B, H, Sq, D], lse [B, H, Sq] as for fa_fwd;
+ *   k, v [B, Hkv, Skv, D], where Hkv divides H: query head h attends to kv
+ *   head h / (H / Hkv).
+ * With p = i + (Skv - Sq) the key position of query row i, the score of row i
+ * and key j is
+ *   x = scale * <Q[b,h,i,:], K[b,kv,j,:]>
+ *   x = softcap * tanh(x / softcap)          when softcap > 0
+ *   x = x - slopes[h] * |p - j|              when slopes is given
+ * and key j is visible when
+ *   (not causal, or j <= p, or prefix is given and j < prefix[b])  and
+ *   (no documents, or doc_q[b,i] == doc_k[b,j] >= 0).
+ *   softcap  0: no cap; else 1e-6 ... 1e6
+ *   slopes   [H] fp32 (finite), or NULL
+ *   doc_q    [B, Sq] int32, doc_k [B, Skv] int32: the document of every query
+ *            and key, both given or both NULL.  A negative id belongs to no
+ *            document: such a key is seen by no row, such a row sees no key.
+ *            Ids may come in any order; key tiles that hold none of a row
+ *            block's documents are skipped where documents lie together.
+ *   prefix   [B] int32, or NULL; with causal only
+ * These arrays are device memory, 4-byte aligned.  A row with no visible key
+ * gets O = 0 and LSE = -inf.  A masked key's K may hold anything; V must be
+ * finite in every row (a masked key's weight is an exact 0, and 0 * inf is
+ * NaN).
+ * Supported: fa_fwd's D, types and limits (B * H < 65536, Sq, Skv <= 2^24).
+ * Up to 128 query tokens, the heads of a group run as rows of one tile, so a
+ * single token of H heads reads K and V once.  Few row tiles split the keys,
+ * as fa_fwd does, when the workspace has room for the partials.
+ *   workspace  caller-owned device memory, 256-byte aligned, of
+ *              fa_score_workspace_bytes(...) bytes (`documents`: whether
+ *              doc_q and doc_k are given); used until the work on `stream`
+ *              has finished.  Smaller, or NULL: the keys are not split, and a
+ *              call with documents, whose tile lists need their part of it,
+ *              returns FA_ERR_WORKSPACE.
+ * Allocates nothing; may be captured into a CUDA graph (fa_fwd's limits on
+ * scheduler slots hold; the workspace is then the graph's to keep).
+ */
+size_t fa_score_workspace_bytes(int B, int H, int Hkv, int Sq, int Skv, int D,
+                                int documents);
+fa_status_t fa_fwd_score(const void *q, const void *k, const void *v, void *o,
+                         float *lse, int B, int H, int Hkv, int Sq, int Skv,
+                         int D, float scale, int causal, int dtype,
+                         float softcap, const float *slopes, const int *doc_q,
+                         const int *doc_k, const int *prefix, void *workspace,
+                         size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * The 4-bit key/value cache: fa_cache_write, fa_cache_read, fa_fwd_cache.
+ *
+ * A cache is four device arrays, 16-byte aligned, of pages of page_size
+ * tokens:
+ *   k_codes, v_codes    uint8 [num_pages, Hkv, page_size, D / 2]
+ *   k_params, v_params  fp16  [num_pages, Hkv, page_size, D / 32, 2]
+ * A row (one token of one kv head) is D codes of 4 bits in groups of 32
+ * channels, each with a scale s and a minimum z: value = s * code + z.  With
+ * x the group's values, limited to +-61440,
+ *   z = fp16(min x), s = fp16((max x - min x) / 15),
+ *   code = floor((x - z) / s + 1/2) limited to 0 ... 15 (0 where s is 0),
+ * rounded to nearest even where fp16 is named, the floor exact.  A NaN makes
+ * its group NaN.  The row's little-endian 32-bit word (D / 32) * t + g holds
+ * channels 32 g + 8 t ... 32 g + 8 t + 7, lowest first.
+ * 0.625 bytes a value: 80 bytes a row at D = 128, of 256 in 16 bits.
+ *
+ *   page_table  [B, max_pages] int32: token n of sequence b is in slot
+ *               n % page_size of page page_table[b, n / page_size]
+ *   page_size   a power of two, 16 ... 1024; max_pages * page_size <= 2^24
+ * A token whose place does not exist (a position below 0 or past max_pages, a
+ * page outside 0 ... num_pages - 1) is not written, reads as zeros and is
+ * seen by no query row; the call then records FA_ERR_INVALID_ARG in the
+ * device status word (fa_get_device_status).  Page numbers of tokens that a
+ * call does not reach are not looked at.
+ * D, dtypes and B * Hkv < 65536 as for fa_fwd.  All three allocate nothing
+ * and may be captured into CUDA graphs: lengths, starts, counts and page
+ * tables are read when the work runs.
+ *
+ * fa_cache_write -- quantises new tokens into the cache.
+ *   k, v   [B, Hkv, S, D] fp16 or bf16; token i of sequence b goes to
+ *          position start[b] + i, for i < count[b]
+ *   start  [B] int32, or NULL for 0;  count  [B] int32, or NULL for S
+ * No two tokens of a call may go to the same slot (pages that sequences share
+ * are for reading): which of them stays would be undefined.
+ *
+ * fa_cache_read -- the values of positions start[b] ... start[b] + count[b] -
+ * 1 into rows 0 ... count[b] - 1 of k, v [B, Hkv, S, D], rounded once to
+ * their type; count[b] past S counts as S, rows past it are left as they
+ * were.
+ */
+fa_status_t fa_cache_write(const void *k, const void *v, void *k_codes,
+                           void *k_params, void *v_codes, void *v_params,
+                           const int *page_table, const int *start,
+                           const int *count, int B, int Hkv, int S, int D,
+                           int num_pages, int page_size, int max_pages,
+                           int dtype, fa_stream_t stream);
+fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
+                          const void *v_codes, const void *v_params,
+                          const int *page_table, const int *start,
+                          const int *count, void *k, void *v, int B, int Hkv,
+                          int S, int D, int num_pages, int page_size,
+                          int max_pages, int dtype, fa_stream_t stream);
+
+/*
+ * fa_fwd_cache -- attention of the newest tokens over the cache.
+ *   q, o [B, H, Sq, D], lse [B, H, Sq]; Hkv divides H; 1 <= Sq <= 256
+ *   length  [B] int32: tokens of sequence b in the cache, these Sq included;
+ *           query row i sees keys j <= length[b] - Sq + i.  A length of 0, or
+ *           a row that comes before key 0, sees nothing (O = 0, LSE = -inf).
+ *           Lengths outside 0 ... max_length are limited to it, and
+ *           FA_ERR_INVALID_ARG is recorded.
+ *   max_length  no sequence is longer (0: max_pages * page_size).  The keys
+ *           are split over the GPU for this length.
+ *   scale, softcap, slopes  as for fa_fwd_score (p = length[b] - Sq + i)
+ *   workspace  fa_cache_workspace_bytes(...) bytes (0: may be NULL),
+ *           256-byte aligned, caller-owned; FA_ERR_WORKSPACE when missing
+ * Meant for single tokens and the few of a draft: every 8 or 16 query rows of
+ * a kv head read its keys again.  For longer blocks read the cache back and
+ * call fa_fwd_score.
+ */
+size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D,
+                                int page_size, int max_pages, int max_length);
+fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
+                         const void *k_params, const void *v_codes,
+                         const void *v_params, const int *page_table,
+                         const int *length, void *o, float *lse, int B, int H,
+                         int Hkv, int Sq, int D, int num_pages, int page_size,
+                         int max_pages, int max_length, float scale, int dtype,
+                         float softcap, const float *slopes, void *workspace,
+                         size_t workspace_bytes, fa_stream_t stream);
 
 /*
  * fa_release_workspaces -- frees the workspaces that fa_fwd keeps for split

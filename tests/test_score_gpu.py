@@ -1,0 +1,269 @@
+"""fa_fwd_score against the 64-bit form: caps, biases, documents, prefixes,
+grouped heads, from single tokens to split keys and many items, and the calls
+around it (streams, graphs, workspaces).  Bounds: ops_ref.py."""
+import math
+
+import pytest
+import torch
+
+from attention_forward_gb300 import fa
+import ops_ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+    assert torch.cuda.is_available()
+
+
+def make(B, H, Hkv, Sq, Skv, D, dt, seed=0, mult=1.0):
+    g = torch.Generator("cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    return ((n(B, H, Sq, D) * mult).to(DT[dt]), n(B, Hkv, Skv, D).to(DT[dt]),
+            n(B, Hkv, Skv, D).to(DT[dt]))
+
+
+def slopes_of(H):
+    return torch.tensor([2.0 ** (-8.0 * (h + 1) / H) for h in range(H)], device="cuda")
+
+
+def expect(q, k, v, causal=False, scale=None, softcap=0.0, slopes=None, doc_q=None, doc_k=None,
+           prefix=None):
+    seen, dist = ops_ref.score_seen(q.shape[2], k.shape[2], causal, prefix, doc_q, doc_k)
+    u = torch.finfo(q.dtype).eps / 2
+    return ops_ref.attention(q, k, v, seen, scale or q.shape[3] ** -0.5, softcap, slopes, dist,
+                             p_step=u)
+
+
+def run(q, k, v, **kw):
+    o, lse = fa.fa_fwd_score(q, k, v, **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    return o, lse
+
+
+SHAPES = [  # B, H, Hkv, Sq, Skv
+    (1, 1, 1, 1, 1), (2, 4, 2, 1, 1), (1, 8, 1, 1, 129), (1, 8, 2, 1, 700), (2, 6, 2, 1, 4096),
+    (1, 4, 4, 2, 255), (2, 8, 2, 5, 300), (1, 16, 1, 128, 128), (1, 6, 3, 100, 131),
+    (1, 4, 2, 129, 129), (2, 4, 2, 200, 450), (1, 2, 2, 256, 256), (1, 4, 1, 300, 77),
+    (2, 4, 4, 513, 640), (1, 8, 4, 1021, 1500), (1, 2, 1, 256, 4096),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_grouped_heads(shape, causal, dt, D):
+    q, k, v = make(*shape, D, dt, 1)
+    ops_ref.check(*run(q, k, v, causal=causal), expect(q, k, v, causal))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,mult", [(50.0, 1.0), (20.0, 1.0), (5.0, 4.0), (0.5, 1.0),
+                                      (1000.0, 1.0), (1e6, 2.0), (1e-6, 1.0)])
+@pytest.mark.parametrize("shape", [(1, 8, 2, 1, 700), (2, 4, 2, 200, 450), (1, 2, 2, 513, 640)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_cap(shape, cap, mult, D):
+    q, k, v = make(*shape, D, "bf16", 2, mult)
+    ops_ref.check(*run(q, k, v, causal=True, softcap=cap), expect(q, k, v, True, softcap=cap))
+
+
+def test_cap_with_one_large_score_among_small_ones():
+    """A warp leaves the polynomial's range in one tile only."""
+    q, k, v = make(1, 2, 2, 300, 520, 128, "fp16", 3)
+    k[0, 0, 130] = q[0, 0, 40] * 4
+    k[0, 1, 500] = -q[0, 1, 299] * 4
+    ops_ref.check(*run(q, k, v, softcap=20.0), expect(q, k, v, softcap=20.0))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("shape", [(1, 8, 2, 1, 700), (2, 6, 2, 3, 200), (1, 4, 4, 300, 700),
+                                   (1, 4, 2, 700, 300)], ids=lambda s: "x".join(map(str, s)))
+def test_bias(shape, cap, causal):
+    q, k, v = make(*shape, 64, "fp16", 4)
+    s = slopes_of(shape[1])
+    s[0] = -0.01  # grows with the distance
+    ops_ref.check(*run(q, k, v, causal=causal, softcap=cap, slopes=s),
+                  expect(q, k, v, causal, softcap=cap, slopes=s))
+
+
+def documents(B, Sq, Skv, cuts, seed=0, pad=0):
+    """Ids by cut positions, `pad` last keys without a document."""
+    dk = torch.zeros((B, Skv), dtype=torch.int32)
+    for c in cuts:
+        dk[:, c:] += 1
+    if pad:
+        dk[:, Skv - pad:] = -1
+    dq = torch.full((B, Sq), -1, dtype=torch.int32)
+    n = min(Sq, Skv)
+    dq[:, Sq - n:] = dk[:, Skv - n:]
+    return dq.cuda(), dk.cuda()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,Skv,cuts,pad", [
+    (640, 640, (128, 256), 0), (640, 640, (1, 2, 3, 130, 131, 600), 5), (513, 513, (), 200),
+    (300, 900, (10, 500, 899), 0), (900, 300, (100,), 0), (1, 500, (100, 400), 0),
+    (64, 500, (460,), 3), (1500, 1500, tuple(range(3, 1500, 7)), 0), (257, 257, (), 257)])
+def test_documents_that_lie_together(Sq, Skv, cuts, pad, D, causal):
+    q, k, v = make(2, 4, 2, Sq, Skv, D, "bf16", 5)
+    dq, dk = documents(2, Sq, Skv, cuts, pad=pad)
+    dk[1] = dk[1].flip(0)  # another order in the other batch row
+    ops_ref.check(*run(q, k, v, causal=causal, doc_q=dq, doc_k=dk),
+                  expect(q, k, v, causal, doc_q=dq, doc_k=dk))
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_documents_in_any_order(causal):
+    """Interleaved ids, rows whose document has no key, large ids."""
+    q, k, v = make(2, 2, 1, 700, 800, 128, "fp16", 6)
+    g = torch.Generator().manual_seed(7)
+    dk = torch.randint(-1, 6, (2, 800), generator=g, dtype=torch.int32)
+    dq = torch.randint(-2, 8, (2, 700), generator=g, dtype=torch.int32)
+    dk[dk == 5] = 2 ** 31 - 1
+    dq[dq == 5] = 2 ** 31 - 1
+    dq, dk = dq.cuda(), dk.cuda()
+    ops_ref.check(*run(q, k, v, causal=causal, doc_q=dq, doc_k=dk),
+                  expect(q, k, v, causal, doc_q=dq, doc_k=dk))
+
+
+@pytest.mark.parametrize("shape", [(3, 4, 2, 1, 300), (3, 4, 2, 60, 300), (3, 2, 2, 700, 900),
+                                   (3, 2, 1, 500, 200)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_prefix(shape, cap):
+    q, k, v = make(*shape, 128, "bf16", 8)
+    n = torch.tensor([0, shape[4] // 2, shape[4] + 100], dtype=torch.int32, device="cuda")
+    ops_ref.check(*run(q, k, v, causal=True, softcap=cap, prefix=n),
+                  expect(q, k, v, True, softcap=cap, prefix=n))
+    n = torch.tensor([-5, 1, shape[4] - 1], dtype=torch.int32, device="cuda")
+    ops_ref.check(*run(q, k, v, causal=True, prefix=n), expect(q, k, v, True, prefix=n))
+
+
+def test_all_of_it_together():
+    q, k, v = make(2, 8, 2, 600, 900, 64, "bf16", 9)
+    dq, dk = documents(2, 600, 900, (301, 640), pad=30)
+    n = torch.tensor([350, 700], dtype=torch.int32, device="cuda")
+    kw = dict(causal=True, softcap=15.0, slopes=slopes_of(8), doc_q=dq, doc_k=dk, prefix=n)
+    ops_ref.check(*run(q, k, v, **kw), expect(q, k, v, **kw))
+    kw["scale"] = 0.3
+    ops_ref.check(*run(q, k, v, **kw), expect(q, k, v, **kw))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_what_masked_keys_hold_does_not_matter(bad):
+    """K of keys past the diagonal, of other documents and of none."""
+    q, k, v = make(1, 4, 2, 300, 300, 128, "bf16", 10)
+    dq, dk = documents(1, 300, 300, (140,), pad=20)
+    ref = run(q, k, v, doc_q=dq, doc_k=dk, softcap=30.0)
+    k[:, :, 280:] = bad
+    for got, want in zip(run(q, k, v, doc_q=dq, doc_k=dk, softcap=30.0), ref):
+        assert torch.equal(got, want)
+    q, k, v = make(1, 2, 2, 200, 300, 64, "fp16", 11)
+    k[:, :, 250:] = bad
+    o, lse = run(q, k, v, causal=True, slopes=slopes_of(2))
+    ref = run(q[:, :, :150].contiguous(), k[:, :, :250].contiguous(), v[:, :, :250].contiguous(),
+              causal=True, slopes=slopes_of(2))
+    assert torch.equal(o[:, :, :150], ref[0]) and torch.equal(lse[:, :, :150], ref[1])
+
+
+def test_without_modifications_it_is_fa_fwd():
+    q, k, v = make(2, 4, 4, 400, 400, 128, "bf16", 12)
+    for causal in (False, True):
+        o, lse = run(q, k, v, causal=causal)
+        a, b = fa.fa_fwd_ex(q, k, v, causal=causal, flags=fa.FA_FLAG_SINGLE_CTA, num_splits=1)
+        ws = torch.empty(256, dtype=torch.uint8, device="cuda")
+        o1, l1 = run(q, k, v, causal=causal, workspace=ws[:0])  # no room: unsplit
+        assert torch.equal(o1, a) and torch.equal(l1, b)
+        assert (o.float() - a.float()).abs().max() < 0.02
+
+
+def test_many_items_and_long_rows():
+    q, k, v = make(1, 40, 8, 2100, 2100, 64, "bf16", 13)
+    ops_ref.check(*run(q, k, v, causal=True, softcap=50.0), expect(q, k, v, True, softcap=50.0))
+
+
+def test_workspace_too_small_for_documents():
+    q, k, v = make(1, 2, 2, 300, 300, 64, "bf16", 14)
+    dq, dk = documents(1, 300, 300, (100,))
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(fa.FAError) as e:
+        fa.fa_fwd_score(q, k, v, doc_q=dq, doc_k=dk, workspace=small)
+    assert e.value.status == fa.FA_ERR_WORKSPACE
+    need = fa.fa_score_workspace_bytes(1, 2, 2, 300, 300, 64, True)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ops_ref.check(*run(q, k, v, doc_q=dq, doc_k=dk, workspace=ws),
+                  expect(q, k, v, doc_q=dq, doc_k=dk))
+
+
+def test_split_and_unsplit_agree_and_fill_the_same_rows():
+    q, k, v = make(1, 4, 1, 3, 5000, 128, "bf16", 15)
+    need = fa.fa_score_workspace_bytes(1, 4, 1, 3, 5000, 128)
+    assert need > 0
+    ref = expect(q, k, v, True, softcap=30.0)
+    empty = torch.empty(256, dtype=torch.uint8, device="cuda")[:0]
+    for ws in (None, empty):
+        ops_ref.check(*run(q, k, v, causal=True, softcap=30.0, workspace=ws), ref)
+
+
+def test_two_streams_at_once_and_a_stream_that_is_not_current():
+    a, b = make(2, 8, 2, 500, 700, 128, "bf16", 16), make(1, 8, 2, 1, 3000, 128, "bf16", 17)
+    dq, dk = documents(2, 500, 700, (50, 300))
+    ra = run(*a, causal=True, doc_q=dq, doc_k=dk)
+    rb = run(*b, softcap=20.0)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(20):
+        got.append((fa.fa_fwd_score(*a, causal=True, doc_q=dq, doc_k=dk, stream=s1),
+                    fa.fa_fwd_score(*b, softcap=20.0, stream=s2)))
+    torch.cuda.synchronize()
+    for x, y in got:
+        assert torch.equal(x[0], ra[0]) and torch.equal(x[1], ra[1])
+        assert torch.equal(y[0], rb[0]) and torch.equal(y[1], rb[1])
+
+
+def test_graph_reads_ids_prefixes_and_inputs_at_replay():
+    q, k, v = make(2, 4, 2, 300, 400, 128, "bf16", 18)
+    dq, dk = documents(2, 300, 400, (90, 200))
+    n = torch.tensor([10, 20], dtype=torch.int32, device="cuda")
+    kw = dict(causal=True, softcap=30.0, slopes=slopes_of(4), doc_q=dq, doc_k=dk, prefix=n)
+    run(q, k, v, **kw)  # loads the kernels
+    ws = [torch.empty(fa.fa_score_workspace_bytes(2, 4, 2, 300, 400, 128, True),
+                      dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [(torch.empty_like(q), torch.empty((2, 4, 300), device="cuda")) for _ in range(2)]
+    graphs = []
+    for w, (o, lse) in zip(ws, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fa.fa_fwd_score(q, k, v, out=o, lse=lse, workspace=w, **kw)
+        graphs.append(g)
+    d2 = documents(2, 300, 400, (30, 150, 333))
+    dq.copy_(d2[0])
+    dk.copy_(d2[1])
+    n.fill_(250)
+    q.mul_(0.5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs[0].replay()
+    with torch.cuda.stream(side):
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK
+    ref = expect(q, k, v, **kw)
+    for o, lse in outs:
+        ops_ref.check(o, lse, ref)
+
+
+def test_same_inputs_give_the_same_bits():
+    q, k, v = make(1, 8, 2, 1100, 1100, 64, "bf16", 19)
+    a = run(q, k, v, causal=True, softcap=20.0, slopes=slopes_of(8))
+    for _ in range(3):
+        b = run(q, k, v, causal=True, softcap=20.0, slopes=slopes_of(8))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
