@@ -204,11 +204,14 @@ fa_status_t encode_3d(CUtensorMap* m, const void* base, int D, int S, int BH,
 }
 
 // The scheduler slot of one prefill launch (see g_launch_seq, g_capture_seq).
-unsigned long long* sched_slot(const DeviceState& d, bool captured) {
+unsigned long long* next_slot(unsigned long long* sched, bool captured) {
   const unsigned n = captured
       ? fa::kSchedSlots + g_capture_seq.fetch_add(1) % fa::kGraphSchedSlots
       : g_launch_seq.fetch_add(1) % fa::kSchedSlots;
-  return d.sched + 2 * static_cast<size_t>(n);
+  return sched + 2 * static_cast<size_t>(n);
+}
+unsigned long long* sched_slot(const DeviceState& d, bool captured) {
+  return next_slot(d.sched, captured);
 }
 
 // fa_fwd's workspace for `stream` on this device, grown to `need` bytes.
@@ -714,6 +717,12 @@ fa_status_t check_call(const void* q, const void* k, const void* v, const void* 
   return current_device(&d, nullptr);
 }
 
+fa_status_t check_args(const void* q, const void* k, const void* v, const void* o,
+                       const void* lse, int B, int H, int Sq, int Skv, int D, float scale,
+                       int dtype) {
+  return validate(q, k, v, o, lse, B, H, Sq, Skv, D, scale, dtype);
+}
+
 fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out) {
   DeviceState* d = nullptr;
   const fa_status_t st = current_device(&d, nullptr);
@@ -721,16 +730,17 @@ fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out) {
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) return FA_ERR_CUDA;
   *out = LaunchEnv{d->sm_count, d->status, g_watchdog_ns.load(),
-                   cap != cudaStreamCaptureStatusNone};
+                   cap != cudaStreamCaptureStatusNone, d->sched};
   return FA_OK;
 }
 
-fa_status_t take_sched_slot(bool captured, unsigned long long** out) {
+unsigned long long* take_sched_slot(const LaunchEnv& env) {
+  return next_slot(env.sched, env.captured);
+}
+
+int device_sms() {
   DeviceState* d = nullptr;
-  const fa_status_t st = current_device(&d, nullptr);
-  if (st != FA_OK) return st;
-  *out = sched_slot(*d, captured);
-  return FA_OK;
+  return current_device(&d, nullptr) == FA_OK ? d->sm_count : 0;
 }
 
 fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int heads,

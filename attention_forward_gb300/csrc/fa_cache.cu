@@ -4,21 +4,23 @@
 namespace fa {
 namespace {
 
-// D / 8 threads per row; the caller has checked that the grid fits.
-unsigned grid_of(int D, const CacheCopyParams& p) {
-  const long long n = p.n_rows * (D / 8);
-  return static_cast<unsigned>((n + kCacheCopyThreads - 1) / kCacheCopyThreads);
+// A grid of (token blocks, B * Hkv): fa_cache_* checks that both fit.
+template <int D>
+dim3 grid_of(const CacheCopyParams& p) {
+  constexpr int kTokens = kCacheCopyRows<D> * kCacheCopyTurns;
+  return dim3(static_cast<unsigned>((p.S + kTokens - 1) / kTokens),
+              static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv));
 }
 
 template <int D, bool BF16>
 cudaError_t write(const CacheCopyParams& p, cudaStream_t stream) {
-  fa_cache_write_kernel<D, BF16><<<grid_of(D, p), kCacheCopyThreads, 0, stream>>>(p);
+  fa_cache_write_kernel<D, BF16><<<grid_of<D>(p), kCacheCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool BF16>
 cudaError_t read(const CacheCopyParams& p, cudaStream_t stream) {
-  fa_cache_read_kernel<D, BF16><<<grid_of(D, p), kCacheCopyThreads, 0, stream>>>(p);
+  fa_cache_read_kernel<D, BF16><<<grid_of<D>(p), kCacheCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

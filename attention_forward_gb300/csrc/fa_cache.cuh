@@ -17,6 +17,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_cache.h"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 
@@ -40,131 +41,220 @@ __device__ __forceinline__ uint32_t cache_pack(float lo, float hi) {
   }
 }
 
-// Where row `row` of [B, Hkv, S] lies in the pool: its (page, kv head, slot)
-// index, or -1 when the row is not in the call (past the sequence's count) and
-// -2 when its place does not exist (a position or page out of range).
-__device__ __forceinline__ long long cache_place(const CacheCopyParams& p, long long row) {
-  if (row >= p.n_rows) return -1;
-  const long long bh = row / p.S;
-  const int i = static_cast<int>(row - bh * p.S);
-  const int b = static_cast<int>(bh / p.Hkv);
-  const int hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hkv);
-  if (p.count && i >= p.count[b]) return -1;
-  const long long pos = (p.start ? static_cast<long long>(p.start[b]) : 0ll) + i;
-  if (pos < 0) return -2;
-  const long long n = pos >> p.page_shift;
-  if (n >= p.max_pages) return -2;
-  const int page = p.page_table[static_cast<long long>(b) * p.max_pages + n];
-  if (page < 0 || page >= p.num_pages) return -2;
-  return ((static_cast<long long>(page) * p.Hkv + hk) << p.page_shift) +
-         (pos & ((1ll << p.page_shift) - 1));
+// Where token i of sequence b lies in a head's rows of the pool: its (page,
+// slot) as page << shift | slot, or -1 when its place does not exist (a
+// position or page out of range).
+__device__ __forceinline__ long long cache_place(const CacheCopyParams& p, int b, int start, int i) {
+  const long long pos = static_cast<long long>(start) + i;
+  if (pos < 0 || (pos >> p.page_shift) >= p.max_pages) return -1;
+  const int n = static_cast<int>(pos >> p.page_shift);
+  const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + n];
+  if (page < 0 || page >= p.num_pages) return -1;
+  return (static_cast<long long>(page) << p.page_shift) | (pos & ((1 << p.page_shift) - 1));
+}
+
+// min / max that a NaN goes through.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // One group's codes from 8 of its channels per lane (4 lanes of a quad hold
 // the group): the word of codes and the (scale, minimum) pair.
-__device__ __forceinline__ void cache_quantise(const float (&in)[8], uint32_t& word,
+//
+// A code is floor((x - z) / s + 1/2), decided exactly.  q = d inv + 1.5 2^23
+// leaves the nearest integer c to d / s (d = x - z, inv = 1 / s, both
+// rounded) in the low bits of q, and r = d - c s is exact in one FMA (c s has
+// 15 bits, and d is within a scale of it).  While every |r| of the lane is
+// clearly below half a scale, c is the code.  Else (a tie or next to one) the
+// lane takes the long way: err, what the subtraction lost (two-sum), joins r,
+// and the sign against half a scale says whether c moves by one.
+__device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& word,
                                                uint32_t& param) {
-  float x[8];
-  bool bad = false;
-  float lo = INFINITY, hi = -INFINITY;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    bad |= in[e] != in[e];
-    x[e] = fminf(fmaxf(in[e], -kCacheLimit), kCacheLimit);
-    lo = fminf(lo, x[e]);
-    hi = fmaxf(hi, x[e]);
-  }
+  constexpr float kMagic = 12582912.f;  // 1.5 2^23
+  float lo = min3_nan(x[0], x[1], x[2]), hi = fmax3(x[0], x[1], x[2]);
+  lo = min3_nan(lo, x[3], x[4]);
+  hi = fmax3(hi, x[3], x[4]);
+  lo = min3_nan(lo, x[5], x[6]);
+  hi = fmax3(hi, x[5], x[6]);
+  lo = min_nan(lo, x[7]);
+  hi = fmaxf(hi, x[7]);
 #pragma unroll
   for (int m = 1; m <= 2; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
     hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
   }
-  const uint32_t votes = __ballot_sync(0xffffffffu, bad);
-  // a NaN makes its whole group NaN: the scale carries it
-  bad = ((votes >> (threadIdx.x & 28u)) & 15u) != 0;
+  if (lo != lo) {  // a NaN makes its whole group NaN: the parameters carry it
+    word = 0u;
+    param = 0x7fff7fffu;
+    return;
+  }
+  // values past the limit take the codes at the ends
+  lo = fminf(fmaxf(lo, -kCacheLimit), kCacheLimit);
+  hi = fminf(fmaxf(hi, -kCacheLimit), kCacheLimit);
   const __half zh = __float2half_rn(lo);
   const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+  param = static_cast<uint32_t>(__half_as_ushort(sh)) |
+          (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
   const float z = __half2float(zh), s = __half2float(sh);
-  const float inv = s > 0.f ? __frcp_rn(s) : 0.f, half_s = 0.5f * s;
-  word = 0;
+  if (s == 0.f) {
+    word = 0u;
+    return;
+  }
+  const float inv = __frcp_rn(s);
+  float far = 0.f;
+  word = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    // floor((x - z) / s + 1/2), decided exactly: d + err is x - z (two-sum),
-    // c a nearest guess, r = d - c s exact by one FMA; r against half a
-    // scale, the lost part err included, says whether c moves by one
     const float d = x[e] - z;
-    const float bb = d - x[e];
-    const float err = (x[e] - (d - bb)) + (-z - bb);
-    float c = rintf(d * inv);
-    const float r = fmaf(-c, s, d);
-    if ((r - half_s) + err >= 0.f) c += 1.f;
-    if ((r + half_s) + err < 0.f) c -= 1.f;
-    c = s > 0.f ? fminf(fmaxf(c, 0.f), 15.f) : 0.f;
-    word |= static_cast<uint32_t>(c) << (4 * e);
+    const float q = fmaf(d, inv, kMagic);
+    const float r = fmaf(-(q - kMagic), s, d);
+    far = fmaxf(far, fabsf(r));
+    // each q's bits are the magic's and the code: the magic's share of the
+    // sum is taken off below
+    word += __float_as_uint(fminf(fmaxf(q, kMagic), kMagic + 15.f)) << (4 * e);
   }
-  if (bad) word = 0;
-  const uint32_t sz = static_cast<uint32_t>(__half_as_ushort(sh)) |
-                      (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
-  param = bad ? 0x7fff7fffu : sz;
+  constexpr uint32_t kMagicBits = 0x4b400000u;
+  word -= kMagicBits * 0x11111111u;
+  // a value past the limit leaves r = NaN or far above half a scale
+  if (!(far < s * 0.499998f)) {
+    const float half_s = 0.5f * s;
+    word = 0u;
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      float v = x[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
+      v = fminf(fmaxf(v, -kCacheLimit), kCacheLimit);
+      const float d = v - z;
+      const float bb = d - v;
+      const float err = (v - (d - bb)) + (-z - bb);
+      float c = rintf(d * inv);
+      const float r = fmaf(-c, s, d);
+      if ((r - half_s) + err >= 0.f) c += 1.f;
+      if ((r + half_s) + err < 0.f) c -= 1.f;
+      word |= static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f)) << (4 * e);
+    }
+  }
 }
 
-constexpr int kCacheCopyThreads = 256;
+// Rows per block: the lanes of a row lie side by side.  blockIdx.y is the
+// (sequence, kv head), blockIdx.x the block of its tokens; a thread takes
+// kCacheCopyTurns tokens, whose loads go out together.
+constexpr int kCacheCopyThreads = 128;
+constexpr int kCacheCopyTurns = 4;
+
+template <int D>
+constexpr int kCacheCopyRows = kCacheCopyThreads / (D / 8);
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const CacheCopyParams p) {
-  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup;
-  const long long idx = static_cast<long long>(blockIdx.x) * kCacheCopyThreads + threadIdx.x;
-  const long long row = idx / kLanes;
-  const int lane = static_cast<int>(idx - row * kLanes);  // 8 channels: group lane / 4, part lane % 4
-  const long long at = cache_place(p, row);
-  if (at == -2 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 8 lane ... + 7
+  const int bh = static_cast<int>(blockIdx.y);
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  const int i0 = static_cast<int>(blockIdx.x) * kRows * kCacheCopyTurns +
+                 static_cast<int>(threadIdx.x) / kLanes;
+  if (i0 - static_cast<int>(threadIdx.x) / kLanes >= count) return;
+  const int start = p.start ? p.start[b] : 0;
   const int g = lane >> 2, t = lane & 3;
+
+  uint4 w[kCacheCopyTurns][2];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    float x[8] = {};
-    if (at >= 0) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p.rows[n]) + idx);
-      const float2 a = cache_unpack<BF16>(w.x), b = cache_unpack<BF16>(w.y);
-      const float2 c = cache_unpack<BF16>(w.z), d = cache_unpack<BF16>(w.w);
-      x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-      x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+  for (int k = 0; k < kCacheCopyTurns; ++k) {
+    const int i = i0 + k * kRows;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      w[k][n] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < count)
+        w[k][n] = __ldcs(reinterpret_cast<const uint4*>(p.rows[n]) +
+                         (static_cast<size_t>(bh) * p.S + i) * kLanes + lane);
     }
-    uint32_t word, param;
-    cache_quantise(x, word, param);
-    if (at >= 0) {
-      reinterpret_cast<uint32_t*>(p.pool.codes[n])[at * kLanes + kGroups * t + g] = word;
-      if (t == 0) p.pool.params[n][at * kGroups + g] = param;
+  }
+#pragma unroll
+  for (int k = 0; k < kCacheCopyTurns; ++k) {
+    const int i = i0 + k * kRows;
+    const long long at = i < count ? cache_place(p, b, start, i) : -1;
+    if (i < count && at < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+    // the pool's row: pages, then heads, then slots
+    const long long page = at >> p.page_shift;
+    const size_t row = at < 0 ? 0 : static_cast<size_t>(((page * p.Hkv + hk) << p.page_shift) +
+                                                        (at & ((1 << p.page_shift) - 1)));
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float2 a = cache_unpack<BF16>(w[k][n].x), b2 = cache_unpack<BF16>(w[k][n].y);
+      const float2 c = cache_unpack<BF16>(w[k][n].z), d = cache_unpack<BF16>(w[k][n].w);
+      const float x[8] = {a.x, a.y, b2.x, b2.y, c.x, c.y, d.x, d.y};
+      uint32_t word, param;
+      cache_quantise(x, word, param);
+      if (at >= 0) {
+        reinterpret_cast<uint32_t*>(p.pool.codes[n])[row * kLanes + kGroups * t + g] = word;
+        if (t == 0) p.pool.params[n][row * kGroups + g] = param;
+      }
     }
   }
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const CacheCopyParams p) {
-  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup;
-  const long long idx = static_cast<long long>(blockIdx.x) * kCacheCopyThreads + threadIdx.x;
-  const long long row = idx / kLanes;
-  const int lane = static_cast<int>(idx - row * kLanes);  // the row's word
-  const long long at = cache_place(p, row);
-  if (at == -2 && lane == 0) atomicExch(p.status, kStatusBadIndex);
-  if (at == -1) return;
-  const int t = lane / kGroups, g = lane - t * kGroups;
+  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 8 lane ... + 7
+  const int bh = static_cast<int>(blockIdx.y);
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  const int i0 = static_cast<int>(blockIdx.x) * kRows * kCacheCopyTurns +
+                 static_cast<int>(threadIdx.x) / kLanes;
+  if (i0 >= count) return;
+  const int start = p.start ? p.start[b] : 0;
+  const int g = lane >> 2, t = lane & 3;
+
+  uint32_t word[kCacheCopyTurns][2], param[kCacheCopyTurns][2];
 #pragma unroll
-  for (int n = 0; n < 2; ++n) {
-    uint4 out = make_uint4(0u, 0u, 0u, 0u);  // a place that does not exist reads as zeros
-    if (at >= 0) {
-      const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(p.pool.codes[n]) + at * kLanes + lane);
-      const uint32_t param = __ldg(p.pool.params[n] + at * kGroups + g);
-      const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&param));
+  for (int k = 0; k < kCacheCopyTurns; ++k) {
+    const int i = i0 + k * kRows;
+    const long long at = i < count ? cache_place(p, b, start, i) : -1;
+    if (i < count && at < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+    const long long page = at >> p.page_shift;
+    const size_t row = at < 0 ? 0 : static_cast<size_t>(((page * p.Hkv + hk) << p.page_shift) +
+                                                        (at & ((1 << p.page_shift) - 1)));
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      word[k][n] = param[k][n] = 0u;  // a place that does not exist reads as zeros
+      if (at >= 0) {
+        word[k][n] = __ldg(reinterpret_cast<const uint32_t*>(p.pool.codes[n]) + row * kLanes +
+                           kGroups * t + g);
+        param[k][n] = __ldg(p.pool.params[n] + row * kGroups + g);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kCacheCopyTurns; ++k) {
+    const int i = i0 + k * kRows;
+    if (i >= count) return;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&param[k][n]));
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = fmaf(static_cast<float>((word >> (4 * e)) & 15u), sz.x, sz.y);
+      for (int e = 0; e < 8; ++e) {
+        // the code as a float: in the low bits of 2^23
+        const float c = __uint_as_float(((word[k][n] >> (4 * e)) & 15u) | 0x4b000000u) - 8388608.f;
+        x[e] = fmaf(c, sz.x, sz.y);
+      }
+      uint4 out;
       out.x = cache_pack<BF16>(x[0], x[1]);
       out.y = cache_pack<BF16>(x[2], x[3]);
       out.z = cache_pack<BF16>(x[4], x[5]);
       out.w = cache_pack<BF16>(x[6], x[7]);
+      reinterpret_cast<uint4*>(p.rows[n])[(static_cast<size_t>(bh) * p.S + i) * kLanes + lane] = out;
     }
-    reinterpret_cast<uint4*>(p.rows[n])[row * kLanes + 4 * g + t] = out;
   }
 }
 

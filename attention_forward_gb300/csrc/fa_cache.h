@@ -28,8 +28,7 @@ struct CacheCopyParams {
   const int* start;       // [B] or null (0)
   const int* count;       // [B] or null (S)
   unsigned* status;
-  long long n_rows;       // B * Hkv * S
-  int Hkv, S, num_pages, page_shift, max_pages;
+  int B, Hkv, S, num_pages, page_shift, max_pages;
 };
 
 struct CacheAttnParams {

@@ -61,8 +61,6 @@ fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const 
   if (st != FA_OK) return st;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(count, 4))
     return FA_ERR_INVALID_ARG;
-  const long long n_rows = static_cast<long long>(B) * Hkv * S;
-  if (n_rows * (D / 8) > 256LL * 0x7fffffffLL) return FA_ERR_INVALID_ARG;  // the grid
   fa::LaunchEnv env{};
   if ((st = fa::launch_env(stream, &env)) != FA_OK) return st;
   fa::CacheCopyParams p{};
@@ -73,7 +71,7 @@ fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const 
   p.start = start;
   p.count = count;
   p.status = env.status;
-  p.n_rows = n_rows;
+  p.B = B;
   p.Hkv = Hkv;
   p.S = S;
   p.num_pages = s.num_pages;
@@ -138,10 +136,9 @@ size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D, int page_s
   if (B < 1 || H < 1 || Hkv < 1 || Sq < 1 || Sq > 256 || H % Hkv != 0 || (D != 64 && D != 128) ||
       static_cast<long long>(B) * H >= 65536 || !pages_ok(s) || max_length < 0)
     return 0;
-  fa::LaunchEnv env{};
-  if (fa::launch_env(nullptr, &env) != FA_OK) env.sm_count = 0;
   const int room = max_pages * page_size;
-  return plan_split(B, H, Hkv, Sq, D, max_length ? std::min(max_length, room) : room, env.sm_count)
+  return plan_split(B, H, Hkv, Sq, D, max_length ? std::min(max_length, room) : room,
+                    fa::device_sms())
       .bytes;
 }
 

@@ -1,5 +1,6 @@
 // fa_cache_attn.cu -- launcher of the attention over the 4-bit cache.
 #include "fa_cache_attn.cuh"
+#include "fa_merge.h"
 
 namespace fa {
 namespace {
@@ -13,9 +14,9 @@ cudaError_t launch(const CacheAttnParams& p, cudaStream_t stream) {
                                       stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.n_splits == 1) return e;
-  const long long rows = static_cast<long long>(p.B) * p.H * p.Sq;
-  fa_cache_combine_kernel<D, BF16><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-  return cudaGetLastError();
+  const MergeParams m{p.part_o, p.part_lse, p.o, p.lse,
+                      static_cast<long long>(p.B) * p.H * p.Sq, p.n_splits};
+  return launch_merge(D, BF16, m, stream);
 }
 
 template <int D, bool BF16>

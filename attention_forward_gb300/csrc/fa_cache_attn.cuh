@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
   __syncthreads();
+  grid_launch_dependents();  // the merge waits for this grid's end
 
   const int slot_mask = (1 << p.page_shift) - 1;
   // the first pool row of a 16-key tile, or -1
@@ -493,36 +494,6 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
       if (ch == 0) p.part_lse[at] = lse;
     }
   }
-}
-
-// Merge the splits of each query row with weights exp(LSE_split - LSE): one
-// warp per row.  A split without keys left O = 0 and LSE = -inf.
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) fa_cache_combine_kernel(const CacheAttnParams p) {
-  constexpr int kDims = D / 32;
-  constexpr float kLog2e = 1.4426950408889634f;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long total = static_cast<long long>(p.B) * p.H * p.Sq;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + warp;
-  if (row >= total) return;
-  float M = -INFINITY;
-  for (int s = lane; s < p.n_splits; s += 32) M = fmaxf(M, p.part_lse[s * total + row]);
-#pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
-  const float mu = M == -INFINITY ? 0.f : M;
-  float W = 0.f, o[kDims] = {};
-  for (int s = 0; s < p.n_splits; ++s) {
-    const float w = ex2_approx((p.part_lse[s * total + row] - mu) * kLog2e);
-    W += w;
-    const float* po = p.part_o + (s * total + row) * D + lane * kDims;
-#pragma unroll
-    for (int d = 0; d < kDims; ++d) o[d] = fmaf(w, po[d], o[d]);
-  }
-  const float inv = W == 0.f ? 0.f : 1.f / W;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.o) + (row * D + lane * kDims) / 2;
-#pragma unroll
-  for (int d = 0; d < kDims; d += 2) out[d / 2] = cache_pack<BF16>(o[d] * inv, o[d + 1] * inv);
-  if (lane == 0) p.lse[row] = W == 0.f ? -INFINITY : M + logf(W);
 }
 
 }  // namespace fa

@@ -15,6 +15,11 @@ fa_status_t check_call(const void* q, const void* k, const void* v, const void* 
                        const void* lse, int B, int H, int Sq, int Skv, int D,
                        float scale, int dtype);
 
+// The argument checks alone (no device call).
+fa_status_t check_args(const void* q, const void* k, const void* v, const void* o,
+                       const void* lse, int B, int H, int Sq, int Skv, int D, float scale,
+                       int dtype);
+
 // A tanh cap is off (0) or within the range that the kernels' fp32 terms cover.
 inline bool softcap_ok(float c) { return c == 0.f || (c >= 1e-6f && c <= 1e6f); }
 
@@ -34,12 +39,15 @@ struct LaunchEnv {
   unsigned* status;               // device status word
   unsigned long long timeout_ns;  // watchdog limit
   bool captured;                  // the stream is being captured
+  unsigned long long* sched;      // the scheduler slots
 };
 fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out);
 
-// A scheduler slot of the current device for one persistent launch
-// (PrefillParams::sched).
-fa_status_t take_sched_slot(bool captured, unsigned long long** out);
+// A scheduler slot for one persistent launch (PrefillParams::sched).
+unsigned long long* take_sched_slot(const LaunchEnv& env);
+
+// The current device's multiprocessors; 0 without a supported device.
+int device_sms();
 
 // TMA descriptor of a [heads, rows, D] 16-bit tensor, boxes of 64 columns x
 // box_rows.

@@ -7,7 +7,7 @@
 #include <mutex>
 
 #include "fa_host.h"
-#include "fa_launch.h"
+#include "fa_merge.h"
 #include "fa_score.h"
 
 namespace fa {
@@ -56,7 +56,7 @@ Plan make_plan(int B, int H, int Hkv, int Sq, int Skv, int D, bool documents, in
   p.n_stages = (p.rows + fa::kBM - 1) / fa::kBM;
   const long long all_rows = static_cast<long long>(p.row_heads) * p.rows;
   int s = fa::choose_prefill_splits(p.row_heads, p.rows, Skv, sm_count);
-  if (all_rows > 0x7fffffffLL) s = 1;  // the combine kernel counts rows in an int
+  if (all_rows > 0x7fffffffLL) s = 1;  // the merge's grid
   p.tiles_per_split = (p.n_key_tiles + s - 1) / s;
   p.n_splits = (p.n_key_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
   if (documents)
@@ -111,9 +111,7 @@ void plan_cap(fa::ScoreParams& p, double scale, double cap) {
 extern "C" size_t fa_score_workspace_bytes(int B, int H, int Hkv, int Sq, int Skv, int D,
                                            int documents) {
   if (!sizes_ok(B, H, Hkv, Sq, Skv) || (D != 64 && D != 128)) return 0;
-  fa::LaunchEnv env{};
-  if (fa::launch_env(nullptr, &env) != FA_OK) env.sm_count = 0;
-  const Plan p = make_plan(B, H, Hkv, Sq, Skv, D, documents != 0, env.sm_count);
+  const Plan p = make_plan(B, H, Hkv, Sq, Skv, D, documents != 0, fa::device_sms());
   return p.doc_bytes + p.split_bytes;
 }
 
@@ -130,7 +128,7 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   if (prefix && !causal) return FA_ERR_INVALID_ARG;
   if (!aligned4(slopes) || !aligned4(doc_q) || !aligned4(doc_k) || !aligned4(prefix))
     return FA_ERR_INVALID_ARG;
-  fa_status_t st = fa::check_call(q, k, v, o, lse, B, H, Sq, Skv, D, scale, dtype);
+  fa_status_t st = fa::check_args(q, k, v, o, lse, B, H, Sq, Skv, D, scale, dtype);
   if (st != FA_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   fa::LaunchEnv env{};
@@ -218,18 +216,13 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   if ((st = fa::encode_rows(&tk, k, D, Skv, kv_heads, fa::kBN, bf16)) != FA_OK) return st;
   if ((st = fa::encode_rows(&tv, v, D, Skv, kv_heads, fa::kBN, bf16)) != FA_OK) return st;
   if ((st = fa::encode_rows(&to, o, D, plan.rows, plan.row_heads, 32, bf16)) != FA_OK) return st;
-  if ((st = fa::take_sched_slot(env.captured, &p.sched)) != FA_OK) return st;
+  p.sched = fa::take_sched_slot(env);
   const int grid = static_cast<int>(std::min<long long>(n_items, env.sm_count > 0 ? env.sm_count : 1));
   if (fa::launch_score(D, bf16, tq, tk, tv, to, p, grid, s) != cudaSuccess) return FA_ERR_CUDA;
   if (plan.n_splits > 1) {
-    fa::DecodeParams c{};
-    c.o = o;
-    c.lse = lse;
-    c.part_o = p.part_o;
-    c.part_lse = p.part_lse;
-    c.BH = static_cast<int>(rows);
-    c.n_splits = plan.n_splits;
-    if (fa::launch_decode_combine(D, bf16, c, s) != cudaSuccess) return FA_ERR_CUDA;
+    const fa::MergeParams m{p.part_o, p.part_lse, o, lse, static_cast<long long>(rows),
+                            plan.n_splits};
+    if (fa::launch_merge(D, bf16, m, s) != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
 }

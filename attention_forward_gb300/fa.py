@@ -235,85 +235,97 @@ def fa_fwd_decode_static(q, k, v, scale: float | None = None, out=None,
     return out, lse
 
 
-class _Call:
-    """The stream of a call on ``like``'s device, current for its length, and
-    the memory that the call makes for itself there."""
+# The raw handle of a device's current stream, without making a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
-    def __init__(self, like: torch.Tensor, stream):
-        self.device, self.given = like.device, stream
-        self.guard = torch.cuda.device(like.device)
+
+class _OnDevice:
+    """Makes a device current for the length of a call that is not on it."""
+    __slots__ = ("before",)
+
+    def __init__(self, dev: int):
+        now = torch.cuda.current_device()
+        self.before = None
+        if now != dev:
+            self.before = now
+            torch.cuda.set_device(dev)
 
     def __enter__(self):
-        self.guard.__enter__()
-        current = torch.cuda.current_stream()
-        if self.given is None:
-            self.handle, self.other = current.cuda_stream, None
-        else:
-            self.handle = _stream_handle(self.given)
-            self.other = None
-            if self.handle != current.cuda_stream:
-                self.other = (self.given if isinstance(self.given, torch.cuda.Stream)
-                              else torch.cuda.ExternalStream(self.handle, device=self.device))
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            # made on the current stream: wait for the work that last had this
-            # memory, and keep it until the call's own stream is done with it
-            self.other.wait_stream(torch.cuda.current_stream())
-            t.record_stream(self.other)
-        return t
-
-    def workspace(self, given, need: int):
-        """(tensor, pointer, bytes) of the caller's workspace, or of one made
-        for this call."""
-        if given is None:
-            given = self.empty((need,), torch.uint8) if need else None
-        if given is None:
-            return None, None, 0
-        return given, given.data_ptr(), given.numel() * given.element_size()
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+        return False
 
 
-def _cuda_tensor(t, name: str, like: torch.Tensor, dtype, shape):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != like.device:
-        raise ValueError(f"{name} must be a tensor on q's (or k's) CUDA device")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _own_memory(tensors, stream) -> None:
+    """Memory made on the current stream for work on another one: that stream
+    waits for the work that last had it, and the memory outlives the call's."""
+    handle = _stream_handle(stream)
+    if handle != _raw_stream(torch.cuda.current_device()):
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(handle)
+        stream.wait_stream(torch.cuda.current_stream())
+        for t in tensors:
+            t.record_stream(stream)
 
 
-def _optional(t, name, like, dtype, shape):
-    if t is None:
-        return None
-    _cuda_tensor(t, name, like, dtype, shape)
+def _bad(t, name: str, dev: int, dtype, shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a tensor on the call's CUDA device")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _ptr(t, name: str, dev: int, dtype, shape) -> int:
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != dev or not t.is_contiguous()):
+        _bad(t, name, dev, dtype, shape)
     return t.data_ptr()
 
 
 def _rows16(t, name: str):
+    """(device, shape) of a 4-d 16-bit CUDA tensor."""
     if not isinstance(t, torch.Tensor) or t.dim() != 4 or t.dtype not in _DTYPE:
         raise ValueError(f"{name} must be a 4-d float16 or bfloat16 tensor")
-    if not t.is_cuda or not t.is_contiguous():
+    dev = t.get_device()
+    if dev < 0 or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return dev, t.shape
 
 
-def _grouped(q, Hkv: int):
-    _rows16(q, "q")
-    if Hkv < 1 or q.shape[1] % Hkv != 0:
+def _group_check(H: int, Hkv: int) -> None:
+    if Hkv < 1 or H % Hkv != 0:
         raise ValueError("the kv heads must divide the query heads")
 
 
-def _given_outputs(call, q, out, lse):
+def _call_memory(q, dev, out, lse, workspace, need: int, stream):
+    """The outputs and the workspace of a call on q's device, made where they
+    are not given: (out, lse, workspace, their pointers, its bytes)."""
     B, H, Sq, D = q.shape
+    made = []
     if out is None:
-        out = call.empty(q.shape, q.dtype)
+        out = torch.empty_like(q)
+        made.append(out)
+    else:
+        _ptr(out, "out", dev, q.dtype, q.shape)
     if lse is None:
-        lse = call.empty((B, H, Sq), torch.float32)
-    _cuda_tensor(out, "out", q, q.dtype, q.shape)
-    _cuda_tensor(lse, "lse", q, torch.float32, (B, H, Sq))
-    return out, lse
+        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    else:
+        _ptr(lse, "lse", dev, torch.float32, (B, H, Sq))
+    if workspace is None:
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            made.append(workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's CUDA device")
+    if stream is not None and made:
+        _own_memory(made, stream)
+    if workspace is None:
+        return out, lse, None, 0
+    return out, lse, workspace, workspace.numel() * workspace.element_size()
 
 
 def fa_score_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Skv: int, D: int,
@@ -330,27 +342,31 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
     (int32 [B, Sq], [B, Skv]) keep rows to keys of their document, ``prefix``
     (int32 [B], causal only) shows the first keys to every row.  Without
     ``workspace`` the call makes its own.  Returns (o, lse)."""
-    _rows16(k, "k")
-    _grouped(q, k.shape[1])
-    B, H, Sq, D = q.shape
-    Hkv, Skv = k.shape[1], k.shape[2]
-    _cuda_tensor(k, "k", q, q.dtype, (B, Hkv, Skv, D))
-    _cuda_tensor(v, "v", q, q.dtype, (B, Hkv, Skv, D))
-    slopes_p = _optional(slopes, "slopes", q, torch.float32, (H,))
-    doc_q_p = _optional(doc_q, "doc_q", q, torch.int32, (B, Sq))
-    doc_k_p = _optional(doc_k, "doc_k", q, torch.int32, (B, Skv))
-    prefix_p = _optional(prefix, "prefix", q, torch.int32, (B,))
+    dev, (B, H, Sq, D) = _rows16(q, "q")
+    _, (_, Hkv, Skv, _) = _rows16(k, "k")
+    _group_check(H, Hkv)
+    kv = (B, Hkv, Skv, D)
+    kp, vp = _ptr(k, "k", dev, q.dtype, kv), _ptr(v, "v", dev, q.dtype, kv)
+    sp = dqp = dkp = pp = None
+    if slopes is not None:
+        sp = _ptr(slopes, "slopes", dev, torch.float32, (H,))
+    if doc_q is not None:
+        dqp = _ptr(doc_q, "doc_q", dev, torch.int32, (B, Sq))
+    if doc_k is not None:
+        dkp = _ptr(doc_k, "doc_k", dev, torch.int32, (B, Skv))
+    if prefix is not None:
+        pp = _ptr(prefix, "prefix", dev, torch.int32, (B,))
     sc = float(D) ** -0.5 if scale is None else float(scale)
-    with _Call(q, stream) as call:
-        out, lse = _given_outputs(call, q, out, lse)
+    L = load()
+    with _OnDevice(dev):
         need = 0
         if workspace is None:
-            need = fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, doc_k is not None)
-        _keep, ws_ptr, ws_bytes = call.workspace(workspace, need)
-        st = load().fa_fwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), B, H, Hkv, Sq, Skv, D, sc, int(bool(causal)),
-                                 _DTYPE[q.dtype], float(softcap), slopes_p, doc_q_p, doc_k_p,
-                                 prefix_p, ws_ptr, ws_bytes, call.handle)
+            need = L.fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, doc_k is not None)
+        out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
+        st = L.fa_fwd_score(q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq,
+                            Skv, D, sc, bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp,
+                            None if ws is None else ws.data_ptr(), ws_bytes,
+                            _raw_stream(dev) if stream is None else _stream_handle(stream))
     _check(st, "fa_fwd_score")
     return out, lse
 
@@ -366,45 +382,49 @@ def fa_cache_empty(num_pages: int, Hkv: int, page_size: int, D: int, device="cud
     return one() + one()
 
 
-def _cache(cache, like, Hkv: int, D: int):
-    """(pointers, num_pages, page_size) of a cache's arrays, checked."""
+def _cache(cache, dev: int, Hkv: int, D: int):
+    """A cache's four pointers, num_pages and page_size, checked."""
     if len(cache) != 4:
         raise ValueError("a cache is (k_codes, k_params, v_codes, v_params)")
-    codes = cache[0]
-    if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
+    kc, kp, vc, vp = cache
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4:
         raise ValueError("k_codes must be [num_pages, Hkv, page_size, D / 2]")
-    rows = (codes.shape[0], Hkv, codes.shape[2])
-    for n, side in ((0, "k"), (2, "v")):
-        _cuda_tensor(cache[n], side + "_codes", like, torch.uint8, rows + (D // 2,))
-        _cuda_tensor(cache[n + 1], side + "_params", like, torch.float16, rows + (D // 32, 2))
-    return [t.data_ptr() for t in cache], codes.shape[0], codes.shape[2]
+    pages, _, page, _ = kc.shape
+    codes, params = (pages, Hkv, page, D // 2), (pages, Hkv, page, D // 32, 2)
+    return (_ptr(kc, "k_codes", dev, torch.uint8, codes),
+            _ptr(kp, "k_params", dev, torch.float16, params),
+            _ptr(vc, "v_codes", dev, torch.uint8, codes),
+            _ptr(vp, "v_params", dev, torch.float16, params), pages, page)
 
 
-def _pages(page_table, like, B: int) -> int:
+def _pages(page_table, dev: int, B: int):
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _cuda_tensor(page_table, "page_table", like, torch.int32, (B, page_table.shape[1]))
-    return page_table.shape[1]
+    n = page_table.shape[1]
+    return _ptr(page_table, "page_table", dev, torch.int32, (B, n)), n
 
 
 def _copy_args(k, v, cache, page_table, start, count):
-    _rows16(k, "k")
-    B, Hkv, S, D = k.shape
-    _cuda_tensor(v, "v", k, k.dtype, k.shape)
-    pool, num_pages, page_size = _cache(cache, k, Hkv, D)
-    max_pages = _pages(page_table, k, B)
-    where = (page_table.data_ptr(), _optional(start, "start", k, torch.int32, (B,)),
-             _optional(count, "count", k, torch.int32, (B,)))
-    return pool, where, (B, Hkv, S, D, num_pages, page_size, max_pages, _DTYPE[k.dtype])
+    dev, (B, Hkv, S, D) = _rows16(k, "k")
+    vptr = _ptr(v, "v", dev, k.dtype, k.shape)
+    kc, kp, vc, vp, pages, page = _cache(cache, dev, Hkv, D)
+    table, per = _pages(page_table, dev, B)
+    if start is not None:
+        start = _ptr(start, "start", dev, torch.int32, (B,))
+    if count is not None:
+        count = _ptr(count, "count", dev, torch.int32, (B,))
+    return (dev, k.data_ptr(), vptr, (kc, kp, vc, vp), (table, start, count),
+            (B, Hkv, S, D, pages, page, per, _DTYPE[k.dtype]))
 
 
 def fa_cache_write(k, v, cache, page_table, start=None, count=None, stream=None) -> None:
     """Quantises k, v [B, Hkv, S, D] into the 4-bit cache: token i < count[b]
     (default S) of sequence b goes to position start[b] + i (default i) of the
     pages that page_table [B, max_pages] lists."""
-    pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
-    with _Call(k, stream) as call:
-        st = load().fa_cache_write(k.data_ptr(), v.data_ptr(), *pool, *where, *sizes, call.handle)
+    dev, kp, vp, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
+    with _OnDevice(dev):
+        st = load().fa_cache_write(kp, vp, *pool, *where, *sizes,
+                                   _raw_stream(dev) if stream is None else _stream_handle(stream))
     _check(st, "fa_cache_write")
 
 
@@ -415,9 +435,10 @@ def fa_cache_read(cache, page_table, start=None, count=None, out=None, stream=No
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (k, v) to read into")
     k, v = out
-    pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
-    with _Call(k, stream) as call:
-        st = load().fa_cache_read(*pool, *where, k.data_ptr(), v.data_ptr(), *sizes, call.handle)
+    dev, kp, vp, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
+    with _OnDevice(dev):
+        st = load().fa_cache_read(*pool, *where, kp, vp, *sizes,
+                                  _raw_stream(dev) if stream is None else _stream_handle(stream))
     _check(st, "fa_cache_read")
     return k, v
 
@@ -434,24 +455,26 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
     cache: length[b] (int32) tokens of sequence b are in it, these included.
     ``max_length``: no sequence is longer (default: what the page table can
     hold); the keys are split over the GPU for it.  Returns (o, lse)."""
+    dev, (B, H, Sq, D) = _rows16(q, "q")
     Hkv = cache[0].shape[1] if len(cache) == 4 and cache[0].dim() == 4 else 0
-    _grouped(q, Hkv)
-    B, H, Sq, D = q.shape
-    pool, num_pages, page_size = _cache(cache, q, Hkv, D)
-    max_pages = _pages(page_table, q, B)
-    _cuda_tensor(length, "length", q, torch.int32, (B,))
-    slopes_p = _optional(slopes, "slopes", q, torch.float32, (H,))
+    _group_check(H, Hkv)
+    kc, kp, vc, vp, pages, page = _cache(cache, dev, Hkv, D)
+    table, per = _pages(page_table, dev, B)
+    lp = _ptr(length, "length", dev, torch.int32, (B,))
+    sp = None
+    if slopes is not None:
+        sp = _ptr(slopes, "slopes", dev, torch.float32, (H,))
     sc = float(D) ** -0.5 if scale is None else float(scale)
-    with _Call(q, stream) as call:
-        out, lse = _given_outputs(call, q, out, lse)
+    L = load()
+    with _OnDevice(dev):
         need = 0
         if workspace is None:
-            need = fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages, max_length)
-        _keep, ws_ptr, ws_bytes = call.workspace(workspace, need)
-        st = load().fa_fwd_cache(q.data_ptr(), *pool, page_table.data_ptr(), length.data_ptr(),
-                                 out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, D, num_pages,
-                                 page_size, max_pages, int(max_length), sc, _DTYPE[q.dtype],
-                                 float(softcap), slopes_p, ws_ptr, ws_bytes, call.handle)
+            need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per, max_length)
+        out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
+        st = L.fa_fwd_cache(q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(),
+                            lse.data_ptr(), B, H, Hkv, Sq, D, pages, page, per, max_length, sc,
+                            _DTYPE[q.dtype], softcap, sp, None if ws is None else ws.data_ptr(),
+                            ws_bytes, _raw_stream(dev) if stream is None else _stream_handle(stream))
     _check(st, "fa_fwd_cache")
     return out, lse
 
