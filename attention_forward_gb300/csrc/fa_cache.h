@@ -36,17 +36,15 @@ struct CacheAttnParams {
   const void* q;          // [B, H, Sq, D]
   void* o;
   float* lse;             // [B, H, Sq]
-  float* part_o;          // n_splits > 1: [n_splits, B * H * Sq, D] fp32, O / l
-  float* part_lse;        // n_splits > 1: [n_splits, B * H * Sq]
+  float* part_o;          // [2 * grid, row block, D] fp32, O / l of a segment
+  float* part_lse;        // [2 * grid, row block]
   const int* page_table;
   const int* length;      // [B]
   const float* slopes;    // [H] or null
   unsigned* status;
   int B, H, Hkv, Sq;
-  int max_length;         // lengths past it are limited to it
   int rows;               // (H / Hkv) * Sq query rows per kv head
   int n_row_blocks;
-  int n_splits, keys_per_split;
   int num_pages, page_shift, max_pages;
   float scale;
   float cap;              // cap > 0: score = cap * tanh(score / cap)
@@ -56,13 +54,23 @@ struct CacheAttnParams {
 cudaError_t launch_cache_write(int D, bool bf16, const CacheCopyParams& p, cudaStream_t stream);
 cudaError_t launch_cache_read(int D, bool bf16, const CacheCopyParams& p, cudaStream_t stream);
 
-// Query rows one CTA of the cache attention takes (8 or 16 by the rows per kv
-// head) and the keys it covers per round of its warps.
+// Query rows that one pass of the cache attention over the keys takes: 8, or 16
+// where a kv head has more than 8.
 int cache_attn_row_block(int rows);
 constexpr int kCacheAttnWarps = 4;
-constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;
-// Keys one split may cover: its page numbers are held in shared memory.
-constexpr int kCacheAttnMaxKeys = 16384;
-cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, cudaStream_t stream);
+constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;  // a chunk of the work: a tile for each warp
+#ifndef FA_ST
+#define FA_ST 4
+#define FA_OCC1 4
+#define FA_OCC2 3
+#define FA_MIN 4
+#endif
+constexpr int kCacheMinChunks = FA_MIN;    // a CTA's least share
+constexpr int kCacheAttnStages = FA_ST;  // tiles of a warp's ring
+constexpr int kCachePiece = 4096;        // keys whose tiles' places are in shared memory at once
+// CTAs for `units` row blocks of up to `room` keys.
+int cache_attn_grid(int rows, long long units, int room, int sm_count);
+cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, int grid,
+                              cudaStream_t stream);
 
 }  // namespace fa

@@ -1,5 +1,5 @@
-// fa_cache_api.cu -- the 4-bit cache's entry points: argument checks, the key
-// split of the attention, and the launches.
+// fa_cache_api.cu -- the 4-bit cache's entry points: argument checks, the
+// attention's grid and workspace, and the launches.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
@@ -82,30 +82,24 @@ fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const 
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-struct Split {
-  int n_splits, keys_per_split;
-  size_t bytes;
+// The attention's persistent CTAs and the memory for their parts.
+struct AttnPlan {
+  int row_blocks, grid;
+  size_t o_bytes, bytes;
 };
 
-// Key ranges of the attention: enough CTAs for about two rounds over four a
-// multiprocessor, at least 256 keys each.
-Split plan_split(int B, int H, int Hkv, int Sq, int D, int max_length, int sm_count) {
-  const int rows = (H / Hkv) * Sq;
-  const int block = fa::cache_attn_row_block(rows);
-  const long long units = static_cast<long long>(B) * Hkv * ((rows + block - 1) / block);
-  const long long slots = 8LL * (sm_count > 0 ? sm_count : 152);
-  long long kps = (units * max_length + slots - 1) / slots;
-  kps = std::max<long long>(kps, 256);
-  kps = (kps + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys * fa::kCacheAttnKeys;
-  kps = std::min<long long>(kps, fa::kCacheAttnMaxKeys);
-  Split s{};
-  s.keys_per_split = static_cast<int>(kps);
-  s.n_splits = static_cast<int>((max_length + kps - 1) / kps);
-  if (s.n_splits > 1) {
-    const size_t n = static_cast<size_t>(s.n_splits) * B * H * Sq;
-    s.bytes = up256(n * D * sizeof(float)) + up256(n * sizeof(float));
+AttnPlan plan_attn(int B, int H, int Hkv, int Sq, int D, const PageShape& s, int sm_count) {
+  AttnPlan a{};
+  const int rows = (H / Hkv) * Sq, block = fa::cache_attn_row_block(rows);
+  a.row_blocks = (rows + block - 1) / block;
+  a.grid = fa::cache_attn_grid(rows, static_cast<long long>(B) * Hkv * a.row_blocks,
+                               s.max_pages * s.page_size, sm_count);
+  if (a.grid > 1) {
+    const size_t n = 2u * static_cast<size_t>(a.grid) * block;
+    a.o_bytes = up256(n * D * sizeof(float));
+    a.bytes = a.o_bytes + up256(n * sizeof(float));
   }
-  return s;
+  return a;
 }
 
 }  // namespace
@@ -130,23 +124,20 @@ fa_status_t fa_cache_read(const void* k_codes, const void* k_params, const void*
               reinterpret_cast<cudaStream_t>(stream));
 }
 
-size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D, int page_size, int max_pages,
-                                int max_length) {
+size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D, int page_size,
+                                int max_pages) {
   const PageShape s{1, page_size, max_pages};
   if (B < 1 || H < 1 || Hkv < 1 || Sq < 1 || Sq > 256 || H % Hkv != 0 || (D != 64 && D != 128) ||
-      static_cast<long long>(B) * H >= 65536 || !pages_ok(s) || max_length < 0)
+      static_cast<long long>(B) * H >= 65536 || !pages_ok(s))
     return 0;
-  const int room = max_pages * page_size;
-  return plan_split(B, H, Hkv, Sq, D, max_length ? std::min(max_length, room) : room,
-                    fa::device_sms())
-      .bytes;
+  return plan_attn(B, H, Hkv, Sq, D, s, fa::device_sms()).bytes;
 }
 
 fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_params,
                          const void* v_codes, const void* v_params, const int* page_table,
                          const int* length, void* o, float* lse, int B, int H, int Hkv, int Sq,
-                         int D, int num_pages, int page_size, int max_pages, int max_length,
-                         float scale, int dtype, float softcap, const float* slopes,
+                         int D, int num_pages, int page_size, int max_pages, float scale,
+                         int dtype, float softcap, const float* slopes,
                          void* workspace, size_t workspace_bytes, fa_stream_t stream) {
   const PageShape s{num_pages, page_size, max_pages};
   fa_status_t st = check_cache({k_codes, k_params, v_codes, v_params}, page_table, B, H, Hkv, Sq,
@@ -155,16 +146,18 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   if (!q || !o || !lse || !length || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) ||
       !aligned(length, 4) || !aligned(slopes, 4))
     return FA_ERR_INVALID_ARG;
-  if (Sq > 256 || max_length < 0) return FA_ERR_INVALID_ARG;
+  if (Sq > 256) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (!fa::softcap_ok(softcap)) return FA_ERR_INVALID_ARG;
   cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
   fa::LaunchEnv env{};
   if ((st = fa::launch_env(strm, &env)) != FA_OK) return st;
-  const int room = max_pages * page_size;
-  const int most = max_length ? std::min(max_length, room) : room;
-  const Split split = plan_split(B, H, Hkv, Sq, D, most, env.sm_count);
-  if (split.bytes > 0 && (!workspace || workspace_bytes < split.bytes || !aligned(workspace, 256)))
+  const AttnPlan plan = plan_attn(B, H, Hkv, Sq, D, s, env.sm_count);
+  // the kernel counts chunks of keys in an int
+  if (static_cast<long long>(B) * Hkv * plan.row_blocks *
+          ((max_pages * page_size + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys) > 0x7fffffffLL)
+    return FA_ERR_INVALID_ARG;
+  if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)))
     return FA_ERR_WORKSPACE;
 
   fa::CacheAttnParams p{};
@@ -172,10 +165,9 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   p.q = q;
   p.o = o;
   p.lse = lse;
-  if (split.n_splits > 1) {
-    const size_t n = static_cast<size_t>(split.n_splits) * B * H * Sq;
+  if (plan.bytes > 0) {
     p.part_o = static_cast<float*>(workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(n * D * sizeof(float)));
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
   }
   p.page_table = page_table;
   p.length = length;
@@ -185,12 +177,8 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   p.H = H;
   p.Hkv = Hkv;
   p.Sq = Sq;
-  p.max_length = most;
   p.rows = (H / Hkv) * Sq;
-  const int block = fa::cache_attn_row_block(p.rows);
-  p.n_row_blocks = (p.rows + block - 1) / block;
-  p.n_splits = split.n_splits;
-  p.keys_per_split = split.keys_per_split;
+  p.n_row_blocks = plan.row_blocks;
   p.num_pages = num_pages;
   p.page_shift = shift_of(page_size);
   p.max_pages = max_pages;
@@ -200,9 +188,8 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
     p.inv_cap = static_cast<float>(1.0 / softcap);
     p.cap_arg = static_cast<float>(2.8853900817779268 / softcap);
   }
-  const long long grid = static_cast<long long>(p.n_splits) * p.n_row_blocks * B * Hkv;
-  if (grid > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
-  return fa::launch_cache_attn(D, dtype == FA_BF16, p, strm) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return fa::launch_cache_attn(D, dtype == FA_BF16, p, plan.grid, strm) == cudaSuccess ? FA_OK
+                                                                                       : FA_ERR_CUDA;
 }
 
 }  // extern "C"

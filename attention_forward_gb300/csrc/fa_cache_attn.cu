@@ -1,37 +1,55 @@
 // fa_cache_attn.cu -- launcher of the attention over the 4-bit cache.
 #include "fa_cache_attn.cuh"
-#include "fa_merge.h"
 
 namespace fa {
 namespace {
 
-template <int D, bool BF16, int NT>
-cudaError_t launch(const CacheAttnParams& p, cudaStream_t stream) {
+template <int D, bool BF16, int NT, bool kMod>
+cudaError_t launch(const CacheAttnParams& p, int grid, cudaStream_t stream) {
   static_assert(sizeof(CacheAttnSmem<D, NT>) <= 48 * 1024, "no opt-in shared memory");
-  const unsigned grid = static_cast<unsigned>(p.n_splits) * static_cast<unsigned>(p.n_row_blocks) *
-                        static_cast<unsigned>(p.B * p.Hkv);
-  fa_cache_attn_kernel<D, BF16, NT><<<grid, kCacheAttnWarps * 32, sizeof(CacheAttnSmem<D, NT>),
-                                      stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.n_splits == 1) return e;
-  const MergeParams m{p.part_o, p.part_lse, p.o, p.lse,
-                      static_cast<long long>(p.B) * p.H * p.Sq, p.n_splits};
-  return launch_merge(D, BF16, m, stream);
+  fa_cache_attn_kernel<D, BF16, NT, kMod>
+      <<<grid, kCacheAttnThreads, sizeof(CacheAttnSmem<D, NT>), stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || grid == 1) return e;  // one CTA: nothing is shared
+  // the merge starts while the CTAs run and waits for them (programmatic
+  // dependent launch)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv) *
+                         static_cast<unsigned>(p.rows), 1, 1);
+  cfg.blockDim = dim3(kCacheAttnThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, BF16, NT>, p, grid);
 }
 
 template <int D, bool BF16>
-cudaError_t by_rows(const CacheAttnParams& p, cudaStream_t stream) {
-  return cache_attn_row_block(p.rows) == 8 ? launch<D, BF16, 1>(p, stream)
-                                           : launch<D, BF16, 2>(p, stream);
+cudaError_t by_rows(const CacheAttnParams& p, int grid, cudaStream_t stream) {
+  const bool mod = p.cap > 0.f || p.slopes;
+  if (cache_attn_row_block(p.rows) == 8)
+    return mod ? launch<D, BF16, 1, true>(p, grid, stream) : launch<D, BF16, 1, false>(p, grid, stream);
+  return mod ? launch<D, BF16, 2, true>(p, grid, stream) : launch<D, BF16, 2, false>(p, grid, stream);
 }
 
 }  // namespace
 
 int cache_attn_row_block(int rows) { return rows <= 8 ? 8 : 16; }
 
-cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, cudaStream_t stream) {
-  if (D == 128) return bf16 ? by_rows<128, true>(p, stream) : by_rows<128, false>(p, stream);
-  return bf16 ? by_rows<64, true>(p, stream) : by_rows<64, false>(p, stream);
+int cache_attn_grid(int rows, long long units, int room, int sm_count) {
+  const long long chunks = units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys);
+  const long long most = (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
+  const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
+                          (cache_attn_row_block(rows) == 8 ? FA_OCC1 : FA_OCC2);
+  return static_cast<int>(most < slots ? most : slots);
+}
+
+cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, int grid,
+                              cudaStream_t stream) {
+  if (D == 128) return bf16 ? by_rows<128, true>(p, grid, stream) : by_rows<128, false>(p, grid, stream);
+  return bf16 ? by_rows<64, true>(p, grid, stream) : by_rows<64, false>(p, grid, stream);
 }
 
 }  // namespace fa

@@ -24,19 +24,23 @@
 //     minimum: a rounding of 2^-11 of the value, an eighth of bf16's), B = p
 //     in fp16 (2^-11), turned from the score layout by movmatrix.
 //
-// Codes and parameters go from global memory straight to the registers of the
-// lane that needs them: lane (g, t) = (lane / 4, lane % 4) reads the 16 bytes
-// of keys g and g + 8 that hold its channels 8 t ... 8 t + 7 of every group, and
-// the words 2 g, 2 g + 1 of its four value tokens.  Every warp's loads cover
-// whole sectors; the next 16 keys' loads are in flight while these are
-// computed.  At the end the warps' states merge in shared memory and the CTA
-// writes O and LSE, or the split's partials for the combine kernel.
+// A warp copies its tiles (16 keys: 2560 bytes at D = 128) into a ring of its own
+// in shared memory with 16-byte asynchronous copies, kCacheAttnStages tiles
+// ahead, and reads them from there in the order its lanes need: lane (g, t) =
+// (lane / 4, lane % 4) takes the words of two keys that hold its channels 8 t
+// ... 8 t + 7 of every group, and the words 2 g, 2 g + 1 of four value tokens.
+// Nothing is shared between the warps until the end, where their states meet
+// in shared memory and the CTA writes O and LSE, or the range's partials for
+// the merge kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "fa_cache.h"
+#include <type_traits>
+
 #include "fa_cache.cuh"
+#include "fa_cache.h"
+#include "fa_merge.cuh"
 #include "sm103_ptx.cuh"
 
 namespace fa {
@@ -50,6 +54,15 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// D = A B.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit elements held two per lane.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t d;
@@ -57,22 +70,29 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const uint4* p) {
-  uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-      : "l"(p));
-  return v;
+// 16 bytes global -> shared, past L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint2 ldg_stream(const uint2* p) {
-  uint2 v;
-  asm("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t ldg_stream(const uint32_t* p) {
-  uint32_t v;
-  asm("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&v)[N], uint32_t addr) {
+  static_assert(N == 1 || N == 2 || N == 4, "one load");
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v[0]) : "r"(addr));
 }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2*>(&w); }
@@ -97,111 +117,276 @@ __device__ __forceinline__ float cap_score(float x, const CacheAttnParams& p) {
   return u < 0.0625f ? small : large;
 }
 
-// What a lane holds of 16 keys.
+// A 16-key tile in shared memory: the 16 rows' codes and parameters of K, then
+// of V, as they lie in the pool.
 template <int D>
 struct CacheTile {
-  static constexpr int G = D / kCacheGroup;
-  uint32_t kc[2][G];   // keys g, g + 8: channels 8 t ... of every group
-  uint32_t kp[2][G];   // their (scale, minimum) pairs
-  uint32_t vc[4][D / 64];  // tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9: words of lane g
-  uint32_t vp[4][D / 64];  // the pairs of those words' groups
+  static constexpr int kRow = D / 2, kPar = D / kCacheGroup * 4;
+  static constexpr int kKCodes = 0, kKParams = 16 * kRow;
+  static constexpr int kVCodes = kKParams + 16 * kPar, kVParams = kVCodes + 16 * kRow;
+  static constexpr int kBytes = kVParams + 16 * kPar;
+};
+
+// Score row r (0 ... 15) of a tile, and value slot r of its product, is token
+// tile_token(r): lane t's value tokens (rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9) are
+// then t, 4 + (t ^ 1), 8 + t, 12 + (t ^ 1), so that the four lanes of a load
+// read four neighbouring rows (with 2 t they would all fall on one half of the
+// banks), and rows g, g + 1 of the keys still fall on both halves.
+__device__ __forceinline__ int tile_token(int r) {
+  return (r & 8) + ((r & 1) ? 4 + (((r >> 1) & 3) ^ 1) : ((r >> 1) & 3));
+}
+
+// What a lane copies of a tile: 16 bytes at these places, at 512-byte steps of
+// the codes; the low lanes take K's parameters, the high lanes V's.
+struct CacheLane {
+  const uint8_t *kc, *vc, *par;
+  uint32_t par_dst;
+  bool has_par;
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(CacheTile<D>& x, const CacheAttnParams& p,
-                                          long long row0, int g, int t) {
-  constexpr int G = D / kCacheGroup;
-  const uint32_t* kc = reinterpret_cast<const uint32_t*>(p.pool.codes[0]);
-  const uint32_t* vc = reinterpret_cast<const uint32_t*>(p.pool.codes[1]);
+__device__ __forceinline__ CacheLane cache_lane(const CacheAttnParams& p, int lane) {
+  using T = CacheTile<D>;
+  CacheLane c;
+  c.kc = p.pool.codes[0] + 16 * lane;
+  c.vc = p.pool.codes[1] + 16 * lane;
+  const int l = lane & 15;
+  c.par = reinterpret_cast<const uint8_t*>(lane < 16 ? p.pool.params[0] : p.pool.params[1]) + 16 * l;
+  c.par_dst = (lane < 16 ? T::kKParams : T::kVParams) + 16 * l;
+  c.has_par = l < T::kPar;  // 16 rows of kPar bytes, 16 at a time
+  return c;
+}
+
+template <int D>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const CacheLane& c, long long row, int lane) {
+  using T = CacheTile<D>;
+  const long long off = row * T::kRow;
+  const uint32_t d = dst + 16u * static_cast<uint32_t>(lane);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const long long row = row0 + g + 8 * i;
-    if constexpr (D == 128) {
-      const uint4 c = ldg_stream(reinterpret_cast<const uint4*>(kc + row * (D / 8) + G * t));
-      const uint4 s = ldg_stream(reinterpret_cast<const uint4*>(p.pool.params[0] + row * G));
-      x.kc[i][0] = c.x; x.kc[i][1] = c.y; x.kc[i][2] = c.z; x.kc[i][3] = c.w;
-      x.kp[i][0] = s.x; x.kp[i][1] = s.y; x.kp[i][2] = s.z; x.kp[i][3] = s.w;
-    } else {
-      const uint2 c = ldg_stream(reinterpret_cast<const uint2*>(kc + row * (D / 8) + G * t));
-      const uint2 s = ldg_stream(reinterpret_cast<const uint2*>(p.pool.params[0] + row * G));
-      x.kc[i][0] = c.x; x.kc[i][1] = c.y;
-      x.kp[i][0] = s.x; x.kp[i][1] = s.y;
-    }
+  for (int k = 0; k < 16 * T::kRow / 512; ++k) {
+    cp_async16(d + T::kKCodes + 512 * k, c.kc + off + 512 * k);
+    cp_async16(d + T::kVCodes + 512 * k, c.vc + off + 512 * k);
   }
+  if (c.has_par) cp_async16(dst + c.par_dst, c.par + row * T::kPar);
+}
+
+// ---- how the work is dealt to the CTAs (the merge kernel uses it too) ----
+
+// A sequence's length, limited to what its page table can hold.
+__device__ __forceinline__ int cache_length(const CacheAttnParams& p, int b) {
+  return max(0, min(p.length[b], p.max_pages << p.page_shift));
+}
+
+// Chunks of a unit of that length; one without keys is a chunk all the same.
+__device__ __forceinline__ int cache_chunks(int len) {
+  return max(1, (len + kCacheAttnKeys - 1) / kCacheAttnKeys);
+}
+
+// All C chunks dealt to n CTAs: C / n each, the first C % n one more.  C < 2^31
+// (fa_fwd_cache checks it).
+struct CacheDeal {
+  int n, per, more;
+  __device__ __forceinline__ int begin(int x) const { return x * per + min(x, more); }
+  __device__ __forceinline__ int cta_of(int c) const {
+    const int big = more * (per + 1);  // chunks of the CTAs that have one more
+    return c < big ? c / (per + 1) : more + (c - big) / per;
+  }
+};
+
+// At least kCacheMinChunks chunks to a CTA.
+__device__ __forceinline__ CacheDeal cache_deal(int all, int grid) {
+  CacheDeal d;
+  d.n = min((all + kCacheMinChunks - 1) / kCacheMinChunks, grid);
+  d.per = all / d.n;
+  d.more = all - d.per * d.n;
+  return d;
+}
+
+constexpr int kCacheAttnThreads = kCacheAttnWarps * 32;
+
+struct CacheScan {
+  int warp_sum[kCacheAttnWarps];
+  int before, b;
+};
+
+// The block's threads take the sequences in runs of equal length and add up
+// their chunks.  Returns the chunks of all units, and a unit's of the sequences
+// before the thread's run (`upto`); `report` records lengths that had to be
+// limited.
+__device__ __forceinline__ int cache_scan(const CacheAttnParams& p, CacheScan& s, bool report,
+                                          int& upto) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
+  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int len = cache_length(p, b);
+    if (report && len != p.length[b]) atomicExch(p.status, kStatusBadIndex);
+    sum += cache_chunks(len);
+  }
+  int inc = sum;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long row = row0 + 2 * t + (i & 1) + 8 * (i >> 1);
-    if constexpr (D == 128) {  // words 2 g, 2 g + 1: groups 2 (g & 1), 2 (g & 1) + 1
-      const uint2 c = ldg_stream(reinterpret_cast<const uint2*>(vc + row * (D / 8) + 2 * g));
-      const uint2 s = ldg_stream(reinterpret_cast<const uint2*>(p.pool.params[1] + row * G + 2 * (g & 1)));
-      x.vc[i][0] = c.x; x.vc[i][1] = c.y;
-      x.vp[i][0] = s.x; x.vp[i][1] = s.y;
-    } else {  // word g: group g & 1
-      x.vc[i][0] = ldg_stream(vc + row * (D / 8) + g);
-      x.vp[i][0] = ldg_stream(p.pool.params[1] + row * G + (g & 1));
-    }
+  for (int k = 1; k < 32; k <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, k);
+    if (lane >= k) inc += o;
   }
+  if (lane == 31) s.warp_sum[warp] = inc;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kCacheAttnWarps; ++w) {
+    if (w < warp) base += s.warp_sum[w];
+    all += s.warp_sum[w];
+  }
+  upto = base + inc - sum;
+  return all * (p.Hkv * p.n_row_blocks);
+}
+
+// The sequence of chunk c, and the chunks before it (all units').
+__device__ __forceinline__ void cache_find(const CacheAttnParams& p, CacheScan& s, int upto, int c,
+                                           int& b, int& before) {
+  const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
+  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
+  const int units = p.Hkv * p.n_row_blocks;
+  int at = upto * units;
+  for (int k = b0; k < b1 && at <= c; ++k) {
+    const int n = cache_chunks(cache_length(p, k)) * units;
+    if (c < at + n) {
+      s.before = at;
+      s.b = k;
+    }
+    at += n;
+  }
+  __syncthreads();
+  b = s.b;
+  before = s.before;
 }
 
 template <int D, int NT>
 struct CacheAttnSmem {
-  // per warp: reference maximum and sum of each row, then O by (row, channel);
-  // a row's D channels are followed by one pad word
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowFloats = D + 1;
-  float m[kCacheAttnWarps][kRows];
-  float l[kCacheAttnWarps][kRows];
-  float o[kCacheAttnWarps][kRows][kRowFloats];
-  int pages[kCacheAttnMaxKeys / 16];
+  long long rows[kCachePiece / 16];  // a tile's first row in the pool, or -1
+  CacheScan scan;
+  union {
+    // the warps' rings
+    alignas(16) uint8_t ring[kCacheAttnWarps][kCacheAttnStages][CacheTile<D>::kBytes];
+    // at a segment's end, per warp: reference maximum and sum of each row, then
+    // O by (row, channel); a row's D channels are followed by one pad word
+    struct {
+      float m[kCacheAttnWarps][kRows];
+      float l[kCacheAttnWarps][kRows];
+      float o[kCacheAttnWarps][kRows][kRowFloats];
+    } end;
+  };
 };
 
-// p.n_splits ranges x p.n_row_blocks x (B * Hkv), row blocks fastest (they
-// read the same keys).
-template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
+// Persistent CTAs.  The work is counted in chunks of kCacheAttnKeys keys of a
+// unit (a row block of a kv head of a sequence), units in the order (sequence,
+// kv head, row block); the CTAs have equal shares of them
+// (CacheDeal), whatever the lengths, which are read here.  A unit that lies within one CTA is written
+// out; the parts of the others go to the workspace, the CTA's first segment to
+// part 2 x, its last to 2 x + 1, where the merge kernel finds them by the same
+// arithmetic.  kMod: the scores are capped or biased (without it those
+// instructions, issued and predicated off, were a quarter of the loop).
+template <int D, bool BF16, int NT, bool kMod>
+__global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2)
     fa_cache_attn_kernel(const CacheAttnParams p) {
   constexpr int G = D / kCacheGroup;
   constexpr int kWords = D / 64;   // value words per lane and token
   constexpr int kMmas = D / 16;    // output products: 8 per value word pair
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kBelow = 8.f, kTau = 15.f;
+  // a reference below every score that counts: -inf - kNone is -inf, so masked
+  // keys get 0 from the first tile on
+  constexpr float kNone = -3.0e38f;
+  using T = CacheTile<D>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   CacheAttnSmem<D, NT>& sm = *reinterpret_cast<CacheAttnSmem<D, NT>*>(smem_raw);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  int id = static_cast<int>(blockIdx.x);
-  const int rb = id % p.n_row_blocks;
-  id /= p.n_row_blocks;
-  const int split = id % p.n_splits;
-  const int bh = id / p.n_splits;
-  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+
+  int upto;
+  const int all_chunks = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
+  const CacheDeal deal = cache_deal(all_chunks, static_cast<int>(gridDim.x));
+  grid_launch_dependents();  // the merge waits for this grid's end
+  const int x_cta = static_cast<int>(blockIdx.x);
+  if (x_cta >= deal.n) return;
+  const int first = deal.begin(x_cta), last = deal.begin(x_cta + 1);
+  int b = 0, before = 0;  // the sequence, and the chunks of those before it
+  cache_find(p, sm.scan, upto, first, b, before);
+
+  // this lane's places in the ring's tiles and in the pool
+  const uint32_t ring = smem_u32(sm.ring[warp]);
+  const CacheLane from = cache_lane<D>(p, lane);
+  const int tok = tile_token(g);  // and tok + 8: its keys
+  const uint32_t at_kc = T::kKCodes + tok * T::kRow + t * (4 * G);
+  const uint32_t at_kp = T::kKParams + tok * T::kPar;
+  const uint32_t at_kz = at_kp + 4 * (t & (G - 1));
+  // D = 128: words 2 g, 2 g + 1, of groups 2 (g & 1), 2 (g & 1) + 1; D = 64: word
+  // g, of group g & 1
+  const uint32_t at_vc = T::kVCodes + g * (4 * kWords);
+  const uint32_t at_vp = T::kVParams + (g & 1) * (4 * kWords);
+  const int vtok[2] = {t, 4 + (t ^ 1)};  // and these + 8: its value tokens
+  const int units = p.Hkv * p.n_row_blocks;
+
+#pragma unroll 1
+  for (int cur = first; cur < last;) {
+  const int len = cache_length(p, b);
+  const int seq_chunks = cache_chunks(len);
+  const int unit = (cur - before) / seq_chunks;
+  const int chunk0 = cur - before - unit * seq_chunks;
+  const int n_chunks = min(seq_chunks - chunk0, last - cur);
+  const bool whole = n_chunks == seq_chunks;
+  const int part = 2 * x_cta + (cur == first ? 0 : 1);
+  const int hk = unit / p.n_row_blocks, rb = unit - hk * p.n_row_blocks;
   const int row0 = rb * 8 * NT;
-  const long long total_rows = static_cast<long long>(p.B) * p.H * p.Sq;
-  const long long out_row0 = static_cast<long long>(bh) * p.rows + row0;
+  const long long out_row0 = (static_cast<long long>(b) * p.Hkv + hk) * p.rows + row0;
   const int n_rows = min(8 * NT, p.rows - row0);
-
-  const int len_raw = p.length[b];
-  const int len = max(0, min(len_raw, p.max_length));  // max_length <= max_pages * page_size
-  if (len != len_raw && threadIdx.x == 0) atomicExch(p.status, kStatusBadIndex);
-  const int k_begin = min(len, split * p.keys_per_split);  // both below 2^25
-  const int k_end = min(len, k_begin + p.keys_per_split);
-
-  // this range's pages, by 16-key tile: the first row of the tile's 16 slots
-  // as a page number; -1 marks a page that does not exist
-  const int n_tiles = (k_end - k_begin + 15) >> 4;
-  for (int i = threadIdx.x; i < n_tiles; i += kCacheAttnWarps * 32) {
-    const int pg = p.page_table[static_cast<long long>(b) * p.max_pages + ((k_begin + 16 * i) >> p.page_shift)];
-    const bool bad = pg < 0 || pg >= p.num_pages;
-    if (bad) atomicExch(p.status, kStatusBadIndex);
-    sm.pages[i] = bad ? -1 : pg;
+  const int k_begin = chunk0 * kCacheAttnKeys;
+  const int k_end = min(len, k_begin + n_chunks * kCacheAttnKeys);
+  const int* pages = p.page_table + static_cast<long long>(b) * p.max_pages;
+  // on to the next segment
+  cur += n_chunks;
+  if (chunk0 + n_chunks == seq_chunks && unit == units - 1) {
+    before += seq_chunks * units;
+    ++b;
   }
+
+  // The segment's tiles in pieces whose places fit in shared memory: all the
+  // threads look the places of a piece up, then every warp starts its copies.
+  // The ring runs kCacheAttnStages - 1 tiles ahead; every turn commits one
+  // group of copies, empty past the end and for a tile that does not exist, so
+  // that the group to wait for is always the same number back.
+  int n_tiles = 0;
+  auto fetch = [&](int i, int stage) {
+    const long long row = i < n_tiles ? sm.rows[i] : -1;
+    if (row >= 0) copy_tile<D>(ring + stage * T::kBytes, from, row, lane);
+    cp_async_commit();
+  };
+  auto start_piece = [&](int piece) {
+    n_tiles = (min(k_end - piece, kCachePiece) + 15) >> 4;
+    for (int i = threadIdx.x; i < n_tiles; i += kCacheAttnThreads) {
+      const int key = piece + 16 * i;  // a 16-key tile lies within one page
+      const int pg = pages[key >> p.page_shift];
+      const bool bad = pg < 0 || pg >= p.num_pages;
+      if (bad) atomicExch(p.status, kStatusBadIndex);
+      sm.rows[i] = bad ? -1
+                       : ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_shift) +
+                             (key & ((1 << p.page_shift) - 1));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kCacheAttnStages - 1; ++k) fetch(warp + k * kCacheAttnWarps, k);
+  };
+  start_piece(k_begin);  // in flight while the queries are made ready
 
   // ---- the query rows: B operands, and per-row constants of the columns
   // this lane's accumulators hold (rows 2 t, 2 t + 1 of each block of 8)
   uint32_t qb[NT][G][4];   // [group][product 0: b0, b1; product 1: b0, b1]
   uint32_t qs[NT][2];      // (0, sum) of group t: high part, low part
-  float fac[NT][2];        // score = 2^24 (the codes') * sum * fac
+  float fac[NT][2];        // score = sum * fac
   float slope[NT][2];
   int limit[NT][2];        // keys below it are visible
   float m[NT][2], l[NT][2];
@@ -225,10 +410,10 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // up = 2^e with top * up in [2^13, 2^14); its exponent stays within what
-    // one float holds for every finite row (an all-zero row takes 1)
+    // up = 2^e with top * up in [2^13, 2^14), an all-zero row's 1.  The bounds
+    // keep up and 2^24 / up floats; a row past 2^113 overflows to NaN
     int e2 = top > 0.f && top < INFINITY ? 13 - ilogbf(top) : 0;
-    e2 = min(max(e2, -120), 120);
+    e2 = min(max(e2, -100), 120);
     const float up = __int_as_float((127 + e2) << 23);
     float part[G];
 #pragma unroll
@@ -257,16 +442,18 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
     const __half lo = __float2half_rn(sum - __half2float(hi));
     qs[n][0] = static_cast<uint32_t>(__half_as_ushort(hi)) << 16;
     qs[n][1] = static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
-    const float down = __int_as_float((127 - e2) << 23);  // 1 / up
+    // what a sum is multiplied by: 2^24 (the codes') / up, the scale, and
+    // log2(e) unless the cap comes between
+    const float down = __int_as_float((127 + 24 - e2) << 23);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int rc = 8 * n + 2 * t + c;
-      fac[n][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.scale;
+      fac[n][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * (kMod && p.cap > 0.f ? p.scale : p.scale * kLog2e);
       const int rr = min(rc, n_rows - 1) + row0;
       const int h = hk * (p.H / p.Hkv) + rr / p.Sq, i = rr % p.Sq;
-      slope[n][c] = p.slopes ? p.slopes[h] * kLog2e : 0.f;
-      limit[n][c] = rc < n_rows ? len - (p.Sq - 1 - i) : 0;
-      m[n][c] = -INFINITY;
+      slope[n][c] = kMod && p.slopes ? p.slopes[h] * kLog2e : 0.f;
+      limit[n][c] = rc < n_rows ? len - (p.Sq - 1 - i) : len;  // rows past n_rows are not stored
+      m[n][c] = kNone;
       l[n][c] = 0.f;
     }
   }
@@ -277,57 +464,42 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
     for (int i = 0; i < kMmas; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.f;
-  __syncthreads();
-  grid_launch_dependents();  // the merge waits for this grid's end
 
-  const int slot_mask = (1 << p.page_shift) - 1;
-  // the first pool row of a 16-key tile, or -1
-  auto tile_row = [&](int i) -> long long {
-    if (i >= n_tiles) return -1;
-    const int pg = sm.pages[i];
-    if (pg < 0) return -1;
-    return ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_shift) + ((k_begin + 16 * i) & slot_mask);
-  };
+  int least_limit = limit[0][0];  // over this lane's rows
+#pragma unroll
+  for (int n = 0; n < NT; ++n) least_limit = min(least_limit, min(limit[n][0], limit[n][1]));
+  least_limit = __reduce_min_sync(0xffffffffu, least_limit);
 
-  CacheTile<D> next;
-  long long next_row = tile_row(warp);
-  if (next_row >= 0) load_tile<D>(next, p, next_row, g, t);
-#pragma unroll 1
-  for (int i = warp; i < n_tiles; i += kCacheAttnWarps) {
-    CacheTile<D> x = next;
-    const bool have = next_row >= 0;
-    next_row = tile_row(i + kCacheAttnWarps);
-    if (next_row >= 0) load_tile<D>(next, p, next_row, g, t);
-    if (!have) continue;
-    const int key0 = k_begin + 16 * i;
-
+  // edge: some row does not see some key of the tile
+  auto compute = [&](uint32_t tile, int key0, auto edge) {
     // ------------------------------ scores ------------------------------
     float s[NT][4];
+    uint32_t kc[2][G], kp[2][G];
+    lds(kc[0], tile + at_kc);
+    lds(kc[1], tile + at_kc + 8 * T::kRow);
+    lds(kp[0], tile + at_kp);
+    lds(kp[1], tile + at_kp + 8 * T::kPar);
     {
-      uint32_t z0 = x.kp[0][0], z1 = x.kp[1][0];
-#pragma unroll
-      for (int gr = 1; gr < G; ++gr) {
-        z0 = t == gr ? x.kp[0][gr] : z0;
-        z1 = t == gr ? x.kp[1][gr] : z1;
-      }
-      if (G < 4 && t >= G) z0 = z1 = 0u;
+      uint32_t z0[1], z1[1];  // group t's pair (D = 64: lanes 2, 3 take weights of 0)
+      lds(z0, tile + at_kz);
+      lds(z1, tile + at_kz + 8 * T::kPar);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float z[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(z, z0, z1, z0, z1, qs[n][0], qs[n][1]);
+        float z[4];
+        mma_f16_first(z, z0[0], z1[0], z0[0], z1[0], qs[n][0], qs[n][1]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = z[e] * 1.52587890625e-5f;  // 2^8 / 2^24
       }
     }
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
-      const uint32_t w0 = x.kc[0][gr], w1 = x.kc[1][gr];
+      const uint32_t w0 = kc[0][gr], w1 = kc[1][gr];
       const uint32_t y0 = w0 >> 8, y1 = w1 >> 8;
-      const float s0 = __low2float(as_half2(x.kp[0][gr])), s1 = __low2float(as_half2(x.kp[1][gr]));
+      const float s0 = __low2float(as_half2(kp[0][gr])), s1 = __low2float(as_half2(kp[1][gr]));
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
+        float d[4];
+        mma_f16_first(d, w0 & 0x000f000fu, w1 & 0x000f000fu, w0 & 0x00f000f0u, w1 & 0x00f000f0u,
                 qb[n][gr][0], qb[n][gr][1]);
         mma_f16(d, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
                 qb[n][gr][2], qb[n][gr][3]);
@@ -342,18 +514,17 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
     uint32_t pb[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      bool over = false;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int c = e & 1, key = key0 + g + 8 * (e >> 1);
-        float v = (s[n][e] * 16777216.f) * fac[n][c];
-        if (p.cap > 0.f) v = cap_score(v, p);
-        v *= kLog2e;
-        if (p.slopes) v = fmaf(-slope[n][c], static_cast<float>(abs(limit[n][c] - 1 - key)), v);
-        v = key < limit[n][c] ? v : -INFINITY;
+        const int c = e & 1, key = key0 + tok + 8 * (e >> 1);
+        float v = s[n][e] * fac[n][c];
+        if (kMod && p.cap > 0.f) v = cap_score(v, p) * kLog2e;
+        if (kMod && p.slopes) v = fmaf(-slope[n][c], static_cast<float>(abs(limit[n][c] - 1 - key)), v);
+        if constexpr (decltype(edge)::value) v = key < limit[n][c] ? v : -INFINITY;
         s[n][e] = v;
-        over |= v > m[n][c] + kTau;
       }
+      const bool over = fmaxf(s[n][0], s[n][2]) > m[n][0] + kTau ||
+                        fmaxf(s[n][1], s[n][3]) > m[n][1] + kTau;
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -377,8 +548,8 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float mm = m[n][e & 1];
-        pr[e] = ex2_approx(s[n][e] - (mm == -INFINITY ? 0.f : mm));
+        // before the first visible key m is below every finite reference
+        pr[e] = ex2_approx(s[n][e] - m[n][e & 1]);
         l[n][e & 1] += pr[e];
       }
       pb[n][0] = movmatrix_trans(as_u32(__floats2half2_rn(pr[0], pr[1])));
@@ -386,38 +557,53 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
     }
 
     // ------------------------------ output ------------------------------
-    if (key0 + 16 > len) {  // slots past the sequence may hold anything
+    uint32_t vc[4][kWords], vp[4][kWords];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t r = vtok[k & 1] + 8 * (k >> 1);
+      lds(vc[k], tile + at_vc + r * T::kRow);
+      lds(vp[k], tile + at_vp + r * T::kPar);
+    }
+    if constexpr (decltype(edge)::value) {  // slots past the sequence may hold anything
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        if (key0 + 2 * t + (k & 1) + 8 * (k >> 1) >= len)
+        if (key0 + vtok[k & 1] + 8 * (k >> 1) >= len)
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) x.vp[k][w] = 0u;
+          for (int w = 0; w < kWords; ++w) vp[k][w] = 0u;
     }
+    // scale and minimum pairs of the token pairs
+    __half2 sc[kWords][2], mn[kWords][2];
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sc[w][k] = as_half2(__byte_perm(vp[2 * k][w], vp[2 * k + 1][w], 0x5410));
+        mn[w][k] = as_half2(__byte_perm(vp[2 * k][w], vp[2 * k + 1][w], 0x7632));
+      }
     // registers of half a word's channels (4 of 8) for both token pairs:
     // a[pair][channel]
     auto dequant = [&](int w, int half, uint32_t (&a)[2][4]) {
 #pragma unroll
-      for (int pr2 = 0; pr2 < 2; ++pr2) {
-        const uint32_t c01 = __byte_perm(x.vc[2 * pr2][w], x.vc[2 * pr2 + 1][w], half ? 0x7632 : 0x5410);
-        const __half2 sc = as_half2(__byte_perm(x.vp[2 * pr2][w], x.vp[2 * pr2 + 1][w], 0x5410));
-        const __half2 mn = as_half2(__byte_perm(x.vp[2 * pr2][w], x.vp[2 * pr2 + 1][w], 0x7632));
-        const uint32_t y = c01 >> 8;
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t c = __byte_perm(vc[2 * k][w], vc[2 * k + 1][w], half ? 0x7632 : 0x5410);
+        const uint32_t y = c >> 8;
         const __half2 k1024 = as_half2(0x64006400u), k64 = as_half2(0x54005400u);
-        const __half2 h0 = __hsub2(as_half2(and_or(c01, 0x000f000fu, 0x64006400u)), k1024);
-        const __half2 h1 = __hsub2(as_half2(and_or(c01, 0x00f000f0u, 0x54005400u)), k64);
+        const __half2 h0 = __hsub2(as_half2(and_or(c, 0x000f000fu, 0x64006400u)), k1024);
+        const __half2 h1 = __hsub2(as_half2(and_or(c, 0x00f000f0u, 0x54005400u)), k64);
         const __half2 h2 = __hsub2(as_half2(and_or(y, 0x000f000fu, 0x64006400u)), k1024);
         const __half2 h3 = __hsub2(as_half2(and_or(y, 0x00f000f0u, 0x54005400u)), k64);
-        a[pr2][0] = as_u32(__hfma2(h0, sc, mn));
-        a[pr2][1] = as_u32(__hfma2(h1, sc, mn));
-        a[pr2][2] = as_u32(__hfma2(h2, sc, mn));
-        a[pr2][3] = as_u32(__hfma2(h3, sc, mn));
+        a[k][0] = as_u32(__hfma2(h0, sc[w][k], mn[w][k]));
+        a[k][1] = as_u32(__hfma2(h1, sc[w][k], mn[w][k]));
+        a[k][2] = as_u32(__hfma2(h2, sc[w][k], mn[w][k]));
+        a[k][3] = as_u32(__hfma2(h3, sc[w][k], mn[w][k]));
       }
     };
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t a0[2][4], a1[2][4];
+      uint32_t a0[2][4];
       dequant(0, half, a0);
       if constexpr (D == 128) {
+        uint32_t a1[2][4];
         dequant(1, half, a1);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -433,7 +619,34 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
                     pb[n][1]);
       }
     }
+  };
+
+#pragma unroll 1
+  for (int piece = k_begin; piece < k_end; piece += kCachePiece) {
+    if (piece > k_begin) {
+      __syncthreads();  // every warp is done with the places before
+      start_piece(piece);
+    }
+    int stage = 0;
+#pragma unroll 1
+    for (int i = warp; i < n_tiles; i += kCacheAttnWarps) {
+      cp_async_wait<kCacheAttnStages - 2>();
+      __syncwarp();  // every lane's copies have landed, every lane is done with the stage before
+      fetch(i + (kCacheAttnStages - 1) * kCacheAttnWarps,
+            stage == 0 ? kCacheAttnStages - 1 : stage - 1);
+      if (sm.rows[i] >= 0) {
+        const int key0 = piece + 16 * i;
+        if (key0 + 16 <= least_limit)
+          compute(ring + stage * T::kBytes, key0, std::false_type{});
+        else
+          compute(ring + stage * T::kBytes, key0, std::true_type{});
+      }
+      stage = stage == kCacheAttnStages - 1 ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    __syncwarp();
   }
+  __syncthreads();  // the rings' memory is the end's
 
   // ---- the warps' states meet in shared memory ----
 #pragma unroll
@@ -446,8 +659,8 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
       sum += __shfl_xor_sync(0xffffffffu, sum, 16);
       const int r = 8 * n + 2 * t + c;
       if (g == 0) {
-        sm.m[warp][r] = m[n][c];
-        sm.l[warp][r] = sum;
+        sm.end.m[warp][r] = m[n][c];
+        sm.end.l[warp][r] = sum;
       }
 #pragma unroll
       for (int k = 0; k < kMmas; ++k)
@@ -463,7 +676,7 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
             nib = 4 * (k >> 1) + (k & 1) + 2 * e;
           }
           const int ch = 32 * (word % G) + 8 * (word / G) + nib;
-          sm.o[warp][r][ch] = acc[n][k][2 * e + c];
+          sm.end.o[warp][r][ch] = acc[n][k][2 * e + c];
         }
     }
   __syncthreads();
@@ -471,29 +684,66 @@ __global__ void __launch_bounds__(kCacheAttnWarps * 32, NT == 1 ? 4 : 3)
   constexpr int kPer = D / 2;
   for (int i = threadIdx.x; i < n_rows * kPer; i += kCacheAttnWarps * 32) {
     const int r = i / kPer, ch = 2 * (i - r * kPer);
-    float M = -INFINITY;
+    float M = kNone;
 #pragma unroll
-    for (int w = 0; w < kCacheAttnWarps; ++w) M = fmaxf(M, sm.m[w][r]);
-    const float mu = M == -INFINITY ? 0.f : M;
+    for (int w = 0; w < kCacheAttnWarps; ++w) M = fmaxf(M, sm.end.m[w][r]);
     float L = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
     for (int w = 0; w < kCacheAttnWarps; ++w) {
-      const float a = ex2_approx(sm.m[w][r] - mu);
-      L = fmaf(sm.l[w][r], a, L);
-      o0 = fmaf(sm.o[w][r][ch], a, o0);
-      o1 = fmaf(sm.o[w][r][ch + 1], a, o1);
+      const float a = ex2_approx(sm.end.m[w][r] - M);
+      L = fmaf(sm.end.l[w][r], a, L);
+      o0 = fmaf(sm.end.o[w][r][ch], a, o0);
+      o1 = fmaf(sm.end.o[w][r][ch + 1], a, o1);
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const float lse = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
-    if (p.n_splits == 1) {
+    if (whole) {
       reinterpret_cast<uint32_t*>(p.o)[((out_row0 + r) * D + ch) / 2] = cache_pack<BF16>(o0 * inv, o1 * inv);
       if (ch == 0) p.lse[out_row0 + r] = lse;
     } else {
-      const long long at = static_cast<long long>(split) * total_rows + out_row0 + r;
+      const long long at = static_cast<long long>(part) * (8 * NT) + r;
       *reinterpret_cast<float2*>(p.part_o + at * D + ch) = make_float2(o0 * inv, o1 * inv);
       if (ch == 0) p.part_lse[at] = lse;
     }
   }
+  __syncthreads();  // the end's memory is the rings' again
+  }
+}
+
+// The units that several CTAs shared: O = sum_s w_s O_s / sum_s w_s over their
+// parts, w_s = exp(LSE_s - max LSE).  A block per query row; four warps deal the
+// parts between them.
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(kCacheAttnThreads)
+    fa_cache_merge_kernel(const CacheAttnParams p, int attn_grid) {
+  __shared__ CacheScan scan;
+  __shared__ MergeSmem<D> sm;
+  const long long row = blockIdx.x;
+  const int bh = static_cast<int>(row / p.rows);
+  const int r = static_cast<int>(row - static_cast<long long>(bh) * p.rows);
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv, rb = r / (8 * NT);
+  int upto;
+  const int all = cache_scan(p, scan, false, upto);
+  const CacheDeal deal = cache_deal(all, attn_grid);
+  // chunks per unit of the sequences before b: the thread with b in its run
+  const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
+  if (b / run == static_cast<int>(threadIdx.x)) {
+    for (int k = static_cast<int>(threadIdx.x) * run; k < b; ++k)
+      upto += cache_chunks(cache_length(p, k));
+    scan.before = upto;
+  }
+  __syncthreads();
+  const int chunks = cache_chunks(cache_length(p, b));
+  const int start = scan.before * (p.Hkv * p.n_row_blocks) + (hk * p.n_row_blocks + rb) * chunks;
+  const int x0 = deal.cta_of(start), x1 = deal.cta_of(start + chunks - 1);
+  grid_dependency_wait();  // all blocks: this grid's end is then the attention's too
+  if (x0 == x1) return;
+  // a CTA's first segment, except where the unit begins inside x0
+  const int inside = deal.begin(x0) < start ? 1 : 0;
+  auto part_row = [&](int s) -> long long {
+    return (2ll * (x0 + s) + (s == 0 ? inside : 0)) * (8 * NT) + r % (8 * NT);
+  };
+  merge_row<D, BF16>(p.part_o, p.part_lse, x1 - x0 + 1, part_row, p.o, p.lse, row, sm);
 }
 
 }  // namespace fa

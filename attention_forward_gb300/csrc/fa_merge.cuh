@@ -1,0 +1,96 @@
+// fa_merge.cuh -- merge of one query row's partials over ranges of the keys:
+// O = sum_s w_s O_s / sum_s w_s with w_s = exp(LSE_s - max LSE), LSE = max LSE +
+// ln sum_s w_s.
+//
+// A block of four warps takes the row.  The parts are dealt to the warps, eight
+// loads of a lane in flight at once: the work is a chain of a few memory
+// latencies, not of bytes (4 (D + 1) a part).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sm103_ptx.cuh"
+
+namespace fa {
+
+constexpr int kMergeWarps = 4;
+
+template <int D>
+struct MergeSmem {
+  float part[kMergeWarps][D];
+  float sums[kMergeWarps];
+};
+
+// part_row(s): the row of part s in part_o [., D] (fp32, O / l) and part_lse [.];
+// LSE = -inf with O = 0 where a part has no visible key.
+template <int D, bool BF16, class PartRow>
+__device__ __forceinline__ void merge_row(const float* part_o, const float* part_lse, int n_parts,
+                                          PartRow part_row, void* o_out, float* lse_out,
+                                          long long row, MergeSmem<D>& sm) {
+  constexpr int kDims = D / 32, kAtOnce = 8;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float top = -INFINITY;
+  for (int s = lane; s < n_parts; s += 32) top = fmaxf(top, part_lse[part_row(s)]);
+#pragma unroll
+  for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f, o[kDims] = {};
+  for (int s0 = warp; s0 < n_parts; s0 += kMergeWarps * kAtOnce) {
+    float lse[kAtOnce], x[kAtOnce][kDims];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int s = s0 + k * kMergeWarps;
+      lse[k] = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) x[k][d] = 0.f;
+      if (s < n_parts) {
+        const long long at = part_row(s);
+        lse[k] = part_lse[at];
+        const float* po = part_o + at * D + lane * kDims;
+        if constexpr (kDims == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(po);
+          x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(po);
+          x[k][0] = v.x; x[k][1] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float w = ex2_approx((lse[k] - base) * kLog2e);
+      sum += w;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) o[d] = fmaf(w, x[k][d], o[d]);
+    }
+  }
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) sm.part[warp][lane * kDims + d] = o[d];
+  if (lane == 0) sm.sums[warp] = sum;
+  __syncthreads();
+  const int ch = 2 * static_cast<int>(threadIdx.x);
+  if (ch >= D) return;
+  float a = 0.f, b = 0.f;
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    a += sm.part[w][ch];
+    b += sm.part[w][ch + 1];
+    sum += sm.sums[w];
+  }
+  // no part has a key: 0; a NaN stays one
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t out;
+  if constexpr (BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a * inv, b * inv);
+    out = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(a * inv, b * inv);
+    out = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  reinterpret_cast<uint32_t*>(o_out)[(row * D + ch) / 2] = out;
+  if (ch == 0) lse_out[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+}
+
+}  // namespace fa

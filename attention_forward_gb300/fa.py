@@ -101,9 +101,9 @@ def load_path(path: str) -> ctypes.CDLL:
     L.fa_cache_write.restype = ci
     L.fa_cache_read.argtypes = [vp] * 9 + [ci] * 8 + [vp]
     L.fa_cache_read.restype = ci
-    L.fa_cache_workspace_bytes.argtypes = [ci] * 8
+    L.fa_cache_workspace_bytes.argtypes = [ci] * 7
     L.fa_cache_workspace_bytes.restype = sz
-    L.fa_fwd_cache.argtypes = [vp] * 9 + [ci] * 9 + [cf, ci, cf, vp, vp, sz, vp]
+    L.fa_fwd_cache.argtypes = [vp] * 9 + [ci] * 8 + [cf, ci, cf, vp, vp, sz, vp]
     L.fa_fwd_cache.restype = ci
     L.fa_version.argtypes = []
     L.fa_version.restype = ci
@@ -444,17 +444,16 @@ def fa_cache_read(cache, page_table, start=None, count=None, out=None, stream=No
 
 
 def fa_cache_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, D: int, page_size: int,
-                             max_pages: int, max_length: int = 0) -> int:
-    return int(load().fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages, max_length))
+                             max_pages: int) -> int:
+    return int(load().fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages))
 
 
 def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
-                 softcap: float = 0.0, slopes=None, max_length: int = 0, workspace=None,
-                 out=None, lse=None, stream=None):
+                 softcap: float = 0.0, slopes=None, workspace=None, out=None, lse=None,
+                 stream=None):
     """Attention of the newest Sq tokens, q [B, H, Sq, D], over the 4-bit
     cache: length[b] (int32) tokens of sequence b are in it, these included.
-    ``max_length``: no sequence is longer (default: what the page table can
-    hold); the keys are split over the GPU for it.  Returns (o, lse)."""
+    Returns (o, lse)."""
     dev, (B, H, Sq, D) = _rows16(q, "q")
     Hkv = cache[0].shape[1] if len(cache) == 4 and cache[0].dim() == 4 else 0
     _group_check(H, Hkv)
@@ -469,10 +468,10 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
     with _OnDevice(dev):
         need = 0
         if workspace is None:
-            need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per, max_length)
+            need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per)
         out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
         st = L.fa_fwd_cache(q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(),
-                            lse.data_ptr(), B, H, Hkv, Sq, D, pages, page, per, max_length, sc,
+                            lse.data_ptr(), B, H, Hkv, Sq, D, pages, page, per, sc,
                             _DTYPE[q.dtype], softcap, sp, None if ws is None else ws.data_ptr(),
                             ws_bytes, _raw_stream(dev) if stream is None else _stream_handle(stream))
     _check(st, "fa_fwd_cache")

@@ -383,26 +383,26 @@ fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
  *   length  [B] int32: tokens of sequence b in the cache, these Sq included;
  *           query row i sees keys j <= length[b] - Sq + i.  A length of 0, or
  *           a row that comes before key 0, sees nothing (O = 0, LSE = -inf).
- *           Lengths outside 0 ... max_length are limited to it, and
- *           FA_ERR_INVALID_ARG is recorded.
- *   max_length  no sequence is longer (0: max_pages * page_size).  The keys
- *           are split over the GPU for this length.
+ *           Lengths outside 0 ... max_pages * page_size are limited to it,
+ *           and FA_ERR_INVALID_ARG is recorded.
  *   scale, softcap, slopes  as for fa_fwd_score (p = length[b] - Sq + i)
  *   workspace  fa_cache_workspace_bytes(...) bytes (0: may be NULL),
  *           256-byte aligned, caller-owned; FA_ERR_WORKSPACE when missing
+ * The keys of all sequences are dealt evenly to the GPU's multiprocessors by
+ * the lengths that the device finds, ragged batches and replays included.
  * Meant for single tokens and the few of a draft: every 8 or 16 query rows of
  * a kv head read its keys again.  For longer blocks read the cache back and
  * call fa_fwd_score.
  */
 size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D,
-                                int page_size, int max_pages, int max_length);
+                                int page_size, int max_pages);
 fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
                          const void *k_params, const void *v_codes,
                          const void *v_params, const int *page_table,
                          const int *length, void *o, float *lse, int B, int H,
                          int Hkv, int Sq, int D, int num_pages, int page_size,
-                         int max_pages, int max_length, float scale, int dtype,
-                         float softcap, const float *slopes, void *workspace,
+                         int max_pages, float scale, int dtype, float softcap,
+                         const float *slopes, void *workspace,
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*

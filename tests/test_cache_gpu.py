@@ -293,20 +293,23 @@ def test_bad_pages_are_not_seen_and_reported():
     ok()
 
 
-def test_max_length_plans_the_split_and_limits_lengths():
-    cache, table, _, _ = cache_of(2, 3000, 2, 64, 128, "bf16", 17)
-    q = torch.randn((2, 8, 1, 128), generator=torch.Generator("cuda").manual_seed(18),
+@pytest.mark.parametrize("B,L", [(1, 20000), (2, 3000), (7, 900), (300, 70)])
+@pytest.mark.parametrize("rows", [4, 24])
+def test_ragged_batches_and_wide_tables(B, L, rows):
+    """The keys are dealt by the lengths found, not by the table's room."""
+    Hkv, Sq = 2, rows // 4
+    cache, table, _, _ = cache_of(B, L, Hkv, 64, 128, "bf16", 17)
+    q = torch.randn((B, 4 * Hkv, Sq, 128), generator=torch.Generator("cuda").manual_seed(18),
                     device="cuda").bfloat16()
-    length = ints([3000, 1111])
+    rng = random.Random(B)
+    length = ints([rng.choice([0, 1, 63, 64, 65, L // 2, L]) for _ in range(B - 1)] + [L])
+    wide = torch.cat([table, torch.full((B, 4000), -1, dtype=torch.int32, device="cuda")],
+                     1).contiguous()
     ref = expect(q, cache, table, length)
-    wide = torch.cat([table, torch.full((2, 4000), -1, dtype=torch.int32, device="cuda")], 1).contiguous()
-    for t, most in ((table, 0), (table, 3000), (wide, 0), (wide, 3000)):
-        o, lse = fa.fa_fwd_cache(q, cache, t, length, max_length=most)
+    for t in (table, wide):
+        o, lse = fa.fa_fwd_cache(q, cache, t, length)
         ok()
         ops_ref.check(o, lse, ref)
-    o, lse = fa.fa_fwd_cache(q, cache, table, length, max_length=1111)
-    assert fa.fa_get_device_status() == fa.FA_ERR_INVALID_ARG
-    ops_ref.check(o, lse, expect(q, cache, table, ints([1111, 1111])))
 
 
 def test_sequences_may_share_pages_for_reading():

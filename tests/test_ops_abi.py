@@ -71,15 +71,15 @@ def test_cache_copy_refusals(lib, kw, want):
 
 @pytest.mark.parametrize("kw,want", CACHE_REFUSALS + [
     (dict(q=0), 1), (dict(o=8), 1), (dict(lse=4), 1), (dict(length=0), 1), (dict(length=2), 1),
-    (dict(H=3), 1), (dict(Sq=0), 1), (dict(Sq=257), 1), (dict(most=-1), 1), (dict(scale=-1.0), 1),
+    (dict(H=3), 1), (dict(Sq=0), 1), (dict(Sq=257), 1), (dict(scale=-1.0), 1),
     (dict(scale=INF), 1), (dict(cap=-0.5), 1), (dict(cap=1e7), 1), (dict(slopes=1), 1)])
 def test_cache_attention_refusals(lib, kw, want):
-    a = dict(cache_args(), q=256, o=256, lse=256, length=256, H=4, Sq=1, most=0, scale=0.125,
+    a = dict(cache_args(), q=256, o=256, lse=256, length=256, H=4, Sq=1, scale=0.125,
              cap=0.0, slopes=None)
     a.update(kw)
     got = lib.fa_fwd_cache(a["q"], a["kc"], a["kp"], a["vc"], a["vp"], a["table"], a["length"],
                            a["o"], a["lse"], a["B"], a["H"], a["Hkv"], a["Sq"], a["D"], a["pages"],
-                           a["page"], a["per"], a["most"], ctypes.c_float(a["scale"]), a["dtype"],
+                           a["page"], a["per"], ctypes.c_float(a["scale"]), a["dtype"],
                            ctypes.c_float(a["cap"]), a["slopes"], None, 0, None)
     assert got == want
 
@@ -92,10 +92,11 @@ def test_workspace_sizes(lib):
     split = fa.fa_score_workspace_bytes(1, 4, 1, 1, 8192, 128)
     assert split >= 2 * 4 * 129 * 4 and split % 256 == 0
     assert fa.fa_cache_workspace_bytes(1, 4, 3, 1, 64, 16, 4) == 0
-    assert fa.fa_cache_workspace_bytes(1, 4, 2, 1, 64, 16, 16) == 0   # 256 keys: one range
-    two = fa.fa_cache_workspace_bytes(1, 4, 2, 1, 64, 16, 32)
-    assert two >= 2 * 4 * 65 * 4 and two % 256 == 0
-    assert fa.fa_cache_workspace_bytes(1, 4, 2, 1, 64, 16, 1024, 256) == 0
+    assert fa.fa_cache_workspace_bytes(1, 4, 1, 1, 64, 16, 4) == 0    # one CTA's work
+    n = fa.fa_cache_workspace_bytes(1, 4, 1, 1, 64, 16, 1024)
+    assert n >= 2 * 2 * 8 * 65 * 4 and n % 256 == 0
+    # however long: the parts of what the GPU holds at once
+    assert fa.fa_cache_workspace_bytes(64, 32, 8, 1, 64, 16, 1 << 20) <= 2 * 2000 * 16 * 65 * 4
 
 
 def test_binding_refusals():
