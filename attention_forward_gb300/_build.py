@@ -27,7 +27,8 @@ NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                      f"-I{os.path.join(ROOT, 'include')}"]
 SOURCES = ["fa_prefill_d128.cu", "fa_prefill_d64.cu", "fa_prefill_d64x3.cu", "fa_prefill_pair.cu",
            "fa_decode.cu", "fa_api.cu", "fa_noalloc.cu", "fa_diag.cu",
-           "fa_score_d128.cu", "fa_score_d64.cu", "fa_score_docs.cu", "fa_score_api.cu",
+           "fa_score_d128_bf16.cu", "fa_score_d128_f16.cu",
+           "fa_score_d64_bf16.cu", "fa_score_d64_f16.cu", "fa_score_docs.cu", "fa_score_api.cu",
            "fa_cache.cu", "fa_cache_attn.cu", "fa_cache_api.cu", "fa_merge.cu"]
 
 

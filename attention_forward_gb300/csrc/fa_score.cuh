@@ -18,13 +18,12 @@
 //            the item's rows.  Tiles inside that range without a visible key
 //            are computed and masked (documents that do not lie together).
 //   scores   Tiles where every key is visible to every row of a warp are not
-//            masked.  tanh is an odd polynomial of five terms while every
-//            |x / cap| of the warp's tile is at most 0.75 (its error is 2e-7
-//            of the cap; 6 FMA-pipe operations a score), else 1 - 2 / (1 +
-//            e^2x) (an exponential and a reciprocal: 12 cycles a warp
-//            instruction pair on the 16-lane XU against 6).  The bias is
-//            linear in the column on either side of the diagonal, one FMA
-//            with an immediate; tiles across it take |p - j|.
+//            masked.  tanh is an odd polynomial of four terms while every
+//            |x / cap| of the warp's tile is at most 0.5 (its error is 1.3e-7
+//            of the cap; 5 FMA-pipe operations a score), else 1 - 2 / (1 +
+//            e^2x) (an exponential and a reciprocal on the XU: measured 1.4
+//            times the whole kernel's time).  The bias is linear in the column
+//            on either side of the diagonal; tiles across it take |p - j|.
 //            Document masks are built as 128 bits a row, by one ballot per
 //            distinct document of the warp's rows.
 //
@@ -45,6 +44,26 @@ __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, 
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
+
+// Register split: 176 / 72 / 88 as in the prefill kernel for unmodified scores,
+// 184 / 64 / 80 with a cap or a bias (their sum is the launch allocation).
+// Measured on B4 H16 S4096 D128: 367 against 382 us without a cap, 571 against
+// 548 with one.
+constexpr int kRegsLaunch = kThreads * 128;
+template <bool kMod>
+constexpr int kRegsScoreSoftmax = kMod ? 184 : 176;
+template <bool kMod>
+constexpr int kRegsScoreEpilogue = kMod ? 64 : 72;
+template <bool kMod>
+constexpr int kRegsScoreControl = kMod ? 80 : 88;
+static_assert(128 * (2 * kRegsScoreSoftmax<true> + kRegsScoreEpilogue<true> +
+                     kRegsScoreControl<true>) == kRegsLaunch &&
+                  128 * (2 * kRegsScoreSoftmax<false> + kRegsScoreEpilogue<false> +
+                         kRegsScoreControl<false>) == kRegsLaunch,
+              "register split must equal the launch allocation");
+// How a call caps its scores: not; with the running reference maximum; with a
+// fixed reference, which the cap allows where it bounds every score enough.
+enum CapForm { kCapNone = 0, kCapRunning = 1, kCapFixed = 2 };
 
 struct ScoreItem {
   int rh, b, kvh;  // row head, its batch row, its kv head [B * Hkv]
@@ -120,48 +139,45 @@ __device__ __forceinline__ int claim_score_item(const ScoreParams& p) {
   return idx < static_cast<unsigned long long>(p.n_items) ? static_cast<int>(idx) : -1;
 }
 
-// What a softmax thread knows of its row during an item.
+// What a softmax thread knows of its row during an item, and its warp of all 32.
 struct ScoreRow {
-  int pos;         // the row's own key position
   int lim;         // keys below it are visible (documents apart)
-  int doc;         // its document (< 0 with documents: sees nothing, lim = 0)
-  bool valid;      // a row of the tensor
+  int lim_warp;    // the least of the warp's
+  int doc;         // its document (< 0: sees nothing)
+  int doc_warp;    // the warp's one document, or kDocSeveral
+  int pos;         // the row's own key position
   float slope;     // slope * log2(e)
 };
+// No tile has this "document": a warp whose rows have several.
+constexpr int kDocSeveral = kDocMixed + 1;
 
 // Scores of one tile in log2 units after the cap: x = cap log2(e) tanh(s scale
 // / cap).  The polynomial runs over the registers first; a warp with a score
 // past its range loads the tile again and takes the exponential form.
 __device__ __forceinline__ void cap_tile(uint32_t (&sr)[8][16], uint32_t tS, const ScoreParams& p) {
-  bool again = p.cap_mode == 2;
-  if (!again) {
-    float top = 0.f;
-    const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3],
-                c4 = p.cap_poly[4];
+  float top = 0.f;
+  const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3];
 #pragma unroll
-    for (int cc = 0; cc < 8; ++cc)
+  for (int cc = 0; cc < 8; ++cc)
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        const float a = __uint_as_float(sr[cc][e]), b = __uint_as_float(sr[cc][e + 1]);
-        float u0, u1, y0, y1;
-        fmul2(u0, u1, a, b, a, b);
-        top = fmax3(top, u0, u1);
-        ffma2(y0, y1, u0, u1, c4, c4, c3, c3);
-        ffma2(y0, y1, y0, y1, u0, u1, c2, c2);
-        ffma2(y0, y1, y0, y1, u0, u1, c1, c1);
-        ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
-        fmul2(y0, y1, y0, y1, a, b);
-        sr[cc][e] = __float_as_uint(y0);
-        sr[cc][e + 1] = __float_as_uint(y1);
-      }
-    again = __any_sync(0xffffffffu, top > p.cap_u_max);
-    if (!again) return;
+    for (int e = 0; e < 16; e += 2) {
+      const float a = __uint_as_float(sr[cc][e]), b = __uint_as_float(sr[cc][e + 1]);
+      float u0, u1, y0, y1;
+      fmul2(u0, u1, a, b, a, b);
+      top = fmax3(top, u0, u1);
+      ffma2(y0, y1, u0, u1, c3, c3, c2, c2);
+      ffma2(y0, y1, y0, y1, u0, u1, c1, c1);
+      ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
+      fmul2(y0, y1, y0, y1, a, b);
+      sr[cc][e] = __float_as_uint(y0);
+      sr[cc][e + 1] = __float_as_uint(y1);
+    }
+  if (!__any_sync(0xffffffffu, !(top <= p.cap_u_max))) return;
 #pragma unroll
-    for (int cc = 0; cc < 8; cc += 2) tmem_ld32(tS + cc * 16, sr[cc], sr[cc + 1]);
-    tmem_wait_ld();
+  for (int cc = 0; cc < 8; cc += 2) tmem_ld32(tS + cc * 16, sr[cc], sr[cc + 1]);
+  tmem_wait_ld();
 #pragma unroll
-    for (int cc = 0; cc < 8; ++cc) reg_fence16(sr[cc]);
-  }
+  for (int cc = 0; cc < 8; ++cc) reg_fence16(sr[cc]);
 #pragma unroll
   for (int cc = 0; cc < 8; ++cc)
 #pragma unroll
@@ -200,7 +216,7 @@ __device__ __forceinline__ void doc_columns(const ScoreParams& p, int b, int key
 // One key tile of one stage's softmax for this thread's row: softmax_tile of
 // fa_prefill.cuh with the scores modified first.  tile_doc: the id that all of
 // the tile's keys have (documents only).
-template <int D, bool BF16>
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
 __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, int b,
                                            const ScoreRow& row, const ScoreParams& p,
                                            int tile_doc, bool may_rescale, float& m, float& l) {
@@ -212,37 +228,44 @@ __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, i
 #pragma unroll
   for (int cc = 0; cc < 8; ++cc) reg_fence16(sr[cc]);
 
-  float c = p.scale_log2;
-  if (p.cap_mode) {
-    cap_tile(sr, tS, p);
-    c = 1.f;
-  }
-  if (p.slopes) {
+  // the factor of the scores in registers: with a cap or a bias they are in
+  // log2 units already
+  const float c = kCap != kCapNone || kBias ? 1.f : p.scale_log2;
+  if constexpr (kCap != kCapNone) cap_tile(sr, tS, p);
+  if constexpr (kBias) {
     // x = s c - slope |p - j|, linear in the column away from the diagonal
+    const float cs = kCap != kCapNone ? 1.f : p.scale_log2;
     const int d0 = key0 - row.pos;
     const bool left = d0 + kBN - 1 <= 0, right = d0 >= 0;
     if (__all_sync(0xffffffffu, left) || __all_sync(0xffffffffu, right)) {
-      const float step = right ? -row.slope : row.slope;
+      // the bias of 16 columns by steps of two from their first: seven
+      // additions' rounding at most
+      const float step = right ? -row.slope : row.slope, step2 = 2.f * step;
       const float base = step * static_cast<float>(d0);
 #pragma unroll
-      for (int cc = 0; cc < 8; ++cc)
+      for (int cc = 0; cc < 8; ++cc) {
+        float b0 = fmaf(step, static_cast<float>(cc * 16), base), b1 = b0 + step;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          sr[cc][e] = __float_as_uint(fmaf(__uint_as_float(sr[cc][e]), c,
-                                           fmaf(step, static_cast<float>(cc * 16 + e), base)));
+        for (int e = 0; e < 16; e += 2) {
+          float x0, x1;
+          ffma2(x0, x1, __uint_as_float(sr[cc][e]), __uint_as_float(sr[cc][e + 1]), cs, cs, b0, b1);
+          sr[cc][e] = __float_as_uint(x0);
+          sr[cc][e + 1] = __float_as_uint(x1);
+          if (e < 14) fadd2(b0, b1, b0, b1, step2, step2);
+        }
+      }
     } else {
       const float f0 = static_cast<float>(d0);
 #pragma unroll
       for (int cc = 0; cc < 8; ++cc)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          sr[cc][e] = __float_as_uint(fmaf(__uint_as_float(sr[cc][e]), c,
+          sr[cc][e] = __float_as_uint(fmaf(__uint_as_float(sr[cc][e]), cs,
                                            -row.slope * fabsf(f0 + static_cast<float>(cc * 16 + e))));
     }
-    c = 1.f;
   }
 
-  if (p.doc_k && __any_sync(0xffffffffu, row.valid && row.doc != tile_doc)) {
+  if (kDocs && row.doc_warp != tile_doc) {
     uint32_t bits[4];
     doc_columns(p, b, key0, row.doc, bits);
 #pragma unroll
@@ -255,7 +278,7 @@ __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, i
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         if (!((bits[cc >> 1] >> ((cc & 1) * 16 + e)) & 1u)) sr[cc][e] = __float_as_uint(-INFINITY);
-  } else if (__any_sync(0xffffffffu, key0 + kBN > row.lim)) {
+  } else if (key0 + kBN > row.lim_warp) {
     const int lim = row.lim - 1 - key0;
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc)
@@ -322,7 +345,101 @@ __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, i
   tmem_wait_st();
 }
 
-template <int D, bool BF16>
+// The exponentials of 32 columns under a fixed reference: p = 2^(x - ref) of the
+// capped scores x, to their 16 columns of P.
+template <bool BF16, bool kMasked>
+__device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32_t tP,
+                                              uint32_t visible, const ScoreParams& p, float& l0,
+                                              float& l1) {
+  const float neg = -p.cap_ref;
+  const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3];
+  float x[32], top = 0.f;
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float a = __uint_as_float(v[e >> 4][e & 15]), b = __uint_as_float(v[e >> 4][(e & 15) + 1]);
+    float u0, u1, y0, y1;
+    fmul2(u0, u1, a, b, a, b);
+    top = fmax3(top, u0, u1);
+    ffma2(y0, y1, u0, u1, c3, c3, c2, c2);
+    ffma2(y0, y1, y0, y1, u0, u1, c1, c1);
+    ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
+    ffma2(x[e], x[e + 1], y0, y1, a, b, neg, neg);
+  }
+  if (__any_sync(0xffffffffu, !(top <= p.cap_u_max))) {
+    const float end = p.cap_log2 + neg;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float ex = ex2_approx(__uint_as_float(v[e >> 4][e & 15]) * p.cap_arg);
+      x[e] = fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), end);
+    }
+  }
+  if constexpr (kMasked) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (!((visible >> e) & 1u)) x[e] = -INFINITY;
+  }
+  uint32_t pk[16];
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const float p0 = ex2_approx(x[e]), p1 = ex2_approx(x[e + 1]);
+    fadd2(l0, l1, l0, l1, p0, p1);
+    pk[e / 2] = pack2<BF16>(p0, p1);
+  }
+  tmem_st16(tP, pk);
+}
+
+// One key tile of one stage's softmax under a cap that bounds every score:
+// p = 2^(x - ref) with one ref for all rows and tiles, so there is no maximum
+// to find, nothing to rescale, and 32 columns at a time go from S to P, the
+// next 32 loading meanwhile (P's columns 16 h ... lie below those still to be
+// read).  bf16 holds p in 2^-120 ... 2^24 as exactly as around 1, l in fp32 too;
+// fp16 does not, and takes the running maximum.
+template <bool BF16, bool kDocs>
+__device__ __forceinline__ void score_tile_fixed(uint32_t tS, int key0, int b, const ScoreRow& row,
+                                                 const ScoreParams& p, int tile_doc, float& l) {
+  uint32_t va[2][16], vb[2][16];
+  tmem_ld32(tS, va[0], va[1]);
+  const bool docs = kDocs && row.doc_warp != tile_doc;
+  float l0 = 0.f, l1 = 0.f;
+  if (docs || key0 + kBN > row.lim_warp) {
+    uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
+    if (kDocs && docs) doc_columns(p, b, key0, row.doc, bits);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = row.lim - key0 - 32 * k;
+      bits[k] &= n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+    }
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      tmem_wait_ld();
+      reg_fence16(va[0]);
+      reg_fence16(va[1]);
+      fixed_columns<BF16, true>(va, tS + 16 * h, bits[0], p, l0, l1);
+      bits[0] = bits[1];
+      bits[1] = bits[2];
+      bits[2] = bits[3];
+      if (h < 3) tmem_ld32(tS + 32 * h + 32, va[0], va[1]);
+    }
+  } else {
+#pragma unroll 1
+    for (int h = 0; h < 4; h += 2) {
+      tmem_wait_ld();
+      reg_fence16(va[0]);
+      reg_fence16(va[1]);
+      tmem_ld32(tS + 32 * h + 32, vb[0], vb[1]);
+      fixed_columns<BF16, false>(va, tS + 16 * h, 0u, p, l0, l1);
+      tmem_wait_ld();
+      reg_fence16(vb[0]);
+      reg_fence16(vb[1]);
+      if (h == 0) tmem_ld32(tS + 64, va[0], va[1]);
+      fixed_columns<BF16, false>(vb, tS + 16 * h + 16, 0u, p, l0, l1);
+    }
+  }
+  l += l0 + l1;
+  tmem_wait_st();
+}
+
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_score_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -389,11 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int wg = warp >> 2;
   if (wg < 2) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmaxSingle));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScoreSoftmax<kCap != kCapNone || kBias>));
   } else if (wg == 2) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogueSingle));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScoreEpilogue<kCap != kCapNone || kBias>));
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControlSingle));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScoreControl<kCap != kCapNone || kBias>));
   }
 
   if (wg < 2) {
@@ -414,40 +531,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       const ScoreItem it = get_score_item(p, idx);
       const int nT = s == 0 ? it.nT0 : it.nT1;
       const int row_g = stage_row(p, it.row0, s) + r;  // row of the row head
-      ScoreRow row;
+      const bool stored = row_g < p.rows;
+      ScoreRow row{};
       {
         const int h_in = row_g / p.Sq;  // packed: the head within its group
         const int i = row_g - h_in * p.Sq;
-        row.valid = row_g < p.rows;
         row.pos = i + (p.Skv - p.Sq);
         row.lim = p.Skv;
-        row.doc = 0;
-        row.slope = 0.f;
-        if (row.valid) {
+        if (stored) {
           if (p.causal) {
             row.lim = row.pos + 1;
             if (p.prefix) row.lim = max(row.lim, p.prefix[it.b]);
             row.lim = min(max(row.lim, 0), p.Skv);
           }
-          if (p.doc_k) {
-            row.doc = p.doc_q[static_cast<size_t>(it.b) * p.Sq + i];
-            if (row.doc < 0) row.lim = 0;
-          }
-          if (p.slopes)
+          if constexpr (kBias)
             row.slope = p.slopes[p.packed ? (it.rh % p.Hkv) * (p.H / p.Hkv) + h_in : it.rh % p.H] *
                         1.4426950408889634f;
         }
+        row.lim_warp = __reduce_min_sync(0xffffffffu, row.lim);
+        if constexpr (kDocs) {
+          row.doc = stored ? p.doc_q[static_cast<size_t>(it.b) * p.Sq + i] : -1;
+          // rows past the last are not stored: any document is theirs
+          const int lo = __reduce_min_sync(0xffffffffu, stored ? row.doc : 0x7fffffff);
+          const int hi = __reduce_max_sync(0xffffffffu, stored ? row.doc : kDocMixed);
+          row.doc_warp = lo == hi && lo >= 0 ? lo : kDocSeveral;
+        }
       }
-      const int* tile_doc = p.doc_k ? p.tile_doc + static_cast<size_t>(it.b) * p.n_key_tiles + it.t0 : nullptr;
-      float m = -INFINITY;  // reference max of c*s (log2 units)
+      // reference of the scores (log2 units)
+      float m = kCap == kCapFixed ? p.cap_ref : -INFINITY;
       float l = 0.f;        // running sum of 2^(c*s - m)
 
 #pragma unroll 1
       for (int j = 0; j < nT; ++j, ++n_s) {
-        const int doc = tile_doc ? tile_doc[j] : 0;  // in flight during the wait
+        int doc = 0;  // in flight during the wait
+        if constexpr (kDocs) doc = p.tile_doc[it.b * p.n_key_tiles + it.t0 + j];
         if (!wait_bar_warp(bar(L::S_FULL + s), n_s & 1, ctl)) { ok = false; break; }
         tc_fence_after();
-        score_tile<D, BF16>(tS, tO, (it.t0 + j) * kBN, it.b, row, p, doc, j > 0, m, l);
+        if constexpr (kCap == kCapFixed)
+          score_tile_fixed<BF16, kDocs>(tS, (it.t0 + j) * kBN, it.b, row, p, doc, l);
+        else
+          score_tile<D, BF16, kCap, kBias, kDocs>(tS, tO, (it.t0 + j) * kBN, it.b, row, p, doc,
+                                                  j > 0, m, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::PV_READY + s));
@@ -456,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // end of the item: LSE straight to global, 1/l to the epilogue warps
       // once the item's last PV_s has completed (then O_s is final)
-      if (row.valid) {
+      if (stored) {
         // l = 0: no visible key; a NaN stays one
         const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
         if (p.n_splits > 1)

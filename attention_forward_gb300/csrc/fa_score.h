@@ -8,10 +8,10 @@
 
 namespace fa {
 
-// Coefficients of the tanh polynomial (odd, five terms).
-constexpr int kCapTerms = 5;
+// Terms of the tanh polynomial (odd).
+constexpr int kCapTerms = 4;
 // |score / cap| up to which it is used.
-constexpr float kCapPolyMax = 0.75f;
+constexpr float kCapPolyMax = 0.5f;
 
 struct ScoreParams {
   float* lse;                 // [B*H, Sq]
@@ -29,13 +29,13 @@ struct ScoreParams {
   int n_items;                // n_qtiles * row_heads * n_splits
   int causal;
   float scale_log2;           // scale * log2(e)
-  // tanh cap: 0 none, 1 polynomial with the exponential form behind it, 2
-  // exponential form only
-  int cap_mode;
-  float cap_u_max;            // score^2 up to which the polynomial holds
+  int capped;                 // scores have a tanh cap
+  int cap_fixed;              // with the fixed reference cap_ref
+  float cap_u_max;            // score^2 up to which the polynomial holds (< 0: none)
   float cap_poly[kCapTerms];  // log2-scaled score = s * (c0 + c1 s^2 + ...)
   float cap_arg;              // 2 log2(e) scale / cap
   float cap_log2;             // cap * log2(e)
+  float cap_ref;              // cap_log2 - 24
   const float* slopes;        // [H] or null
   const int* prefix;          // [B] or null
   const int* doc_q;           // [B, Sq] or null

@@ -12,21 +12,28 @@
 
 namespace fa {
 
-cudaError_t score_num_regs_d128(bool bf16, int* regs);
-cudaError_t score_num_regs_d64(bool bf16, int* regs);
-cudaError_t launch_score_d128(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                              const CUtensorMap&, const ScoreParams&, int, cudaStream_t);
-cudaError_t launch_score_d64(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
-                             const CUtensorMap&, const ScoreParams&, int, cudaStream_t);
+#define FA_SCORE_FORM(n)                                                                     \
+  cudaError_t score_num_regs_##n(int* regs);                                                 \
+  cudaError_t launch_score_##n(const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,   \
+                               const CUtensorMap&, const ScoreParams&, int, cudaStream_t);
+FA_SCORE_FORM(d128_bf16)
+FA_SCORE_FORM(d128_f16)
+FA_SCORE_FORM(d64_bf16)
+FA_SCORE_FORM(d64_f16)
+#undef FA_SCORE_FORM
 
 cudaError_t score_num_regs(int D, bool bf16, int* regs) {
-  return D == 128 ? score_num_regs_d128(bf16, regs) : score_num_regs_d64(bf16, regs);
+  if (D == 128) return bf16 ? score_num_regs_d128_bf16(regs) : score_num_regs_d128_f16(regs);
+  return bf16 ? score_num_regs_d64_bf16(regs) : score_num_regs_d64_f16(regs);
 }
 cudaError_t launch_score(int D, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
                          const CUtensorMap& v, const CUtensorMap& o, const ScoreParams& p,
                          int grid, cudaStream_t stream) {
-  return D == 128 ? launch_score_d128(bf16, q, k, v, o, p, grid, stream)
-                  : launch_score_d64(bf16, q, k, v, o, p, grid, stream);
+  if (D == 128)
+    return bf16 ? launch_score_d128_bf16(q, k, v, o, p, grid, stream)
+                : launch_score_d128_f16(q, k, v, o, p, grid, stream);
+  return bf16 ? launch_score_d64_bf16(q, k, v, o, p, grid, stream)
+              : launch_score_d64_f16(q, k, v, o, p, grid, stream);
 }
 
 }  // namespace fa
@@ -77,14 +84,14 @@ bool sizes_ok(int B, int H, int Hkv, int Sq, int Skv) {
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// cap tanh(s scale / cap) log2(e) = s (c0 + c1 s^2 + ... + c4 s^8) while
-// |s scale / cap| <= y_max.  The terms are the minimax fit (exchange
-// algorithm) of an odd polynomial to tanh on [-0.75, 0.75], error 2e-7.
-void plan_cap(fa::ScoreParams& p, double scale, double cap) {
-  static const double kTanh[fa::kCapTerms] = {0.99999723, -0.33323077, 0.13226092, -0.04928045,
-                                              0.01231884};
-  // |y| up to which the terms from i on stay under 2e-7
-  static const double kWithout[fa::kCapTerms] = {0.0, 0.008, 0.07, 0.17, 0.29};
+// cap tanh(s scale / cap) log2(e) = s (c0 + c1 s^2 + c2 s^4 + c3 s^6) while
+// |s scale / cap| <= y_max.  The terms are the minimax fit (exchange algorithm)
+// of an odd polynomial to tanh on [-0.5, 0.5], error 1.3e-7.
+void plan_cap(fa::ScoreParams& p, double scale, double cap, bool bf16) {
+  static const double kTanh[fa::kCapTerms] = {0.999997676, -0.333206552, 0.131451457,
+                                              -0.043372484};
+  // |y| up to which the terms before i alone are within 2e-7
+  static const double kWithout[fa::kCapTerms] = {0.0, 0.0087, 0.058, 0.172};
   constexpr double kLog2e = 1.4426950408889634;
   const double k = scale / cap;
   double y_max = fa::kCapPolyMax;
@@ -101,9 +108,17 @@ void plan_cap(fa::ScoreParams& p, double scale, double cap) {
   p.cap_u_max = static_cast<float>(std::min(u, static_cast<double>(FLT_MAX)));
   p.cap_arg = static_cast<float>(2.0 * kLog2e * k);
   p.cap_log2 = static_cast<float>(cap * kLog2e);
-  // scores far above the cap: k^8 would leave fp32, and nothing is left of
-  // the polynomial's range
-  p.cap_mode = k <= 1e3 && scale <= 1e3 ? 1 : 2;
+  // scores far above the cap: powers of k would leave fp32, and nothing is
+  // left of the polynomial's range
+  if (!(k <= 1e3 && scale <= 1e3)) {
+    std::fill(p.cap_poly, p.cap_poly + fa::kCapTerms, 0.f);
+    p.cap_u_max = -1.f;
+  }
+  p.capped = 1;
+  // p = 2^(x - ref) for |x| <= cap_log2 within bf16's normal numbers with room
+  // for sums: at most 2^24, at least 2^-120 while cap_log2 <= 72.5 (a cap of 50)
+  p.cap_ref = p.cap_log2 - 24.f;
+  p.cap_fixed = bf16 && !p.slopes && p.cap_log2 <= 72.5f ? 1 : 0;
 }
 
 }  // namespace
@@ -171,8 +186,8 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   p.n_qtiles = plan.n_qtiles;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
-  if (softcap > 0.f) plan_cap(p, scale, softcap);
   p.slopes = slopes;
+  if (softcap > 0.f) plan_cap(p, scale, softcap, bf16);
   p.prefix = prefix;
   p.n_splits = plan.n_splits;
   p.tiles_per_split = plan.tiles_per_split;

@@ -7,8 +7,8 @@
 
 namespace fa {
 
-template <int D, bool BF16>
-cudaError_t score_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
+cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& o, const ScoreParams& p, int grid,
                          cudaStream_t stream) {
   {  // the shared-memory opt-in, once per device
@@ -20,22 +20,64 @@ cudaError_t score_launch(const CUtensorMap& q, const CUtensorMap& k, const CUten
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(fa_score_kernel<D, BF16>,
+      e = cudaFuncSetAttribute(fa_score_kernel<D, BF16, kCap, kBias, kDocs>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                PrefillLayout<D>::kSmemBytes);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  fa_score_kernel<D, BF16><<<grid, kThreads, PrefillLayout<D>::kSmemBytes, stream>>>(q, k, v, o, p);
+  fa_score_kernel<D, BF16, kCap, kBias, kDocs><<<grid, kThreads, PrefillLayout<D>::kSmemBytes, stream>>>(q, k, v, o, p);
   return cudaGetLastError();
 }
 
+template <int D, bool BF16, int kCap, bool kBias>
+cudaError_t score_launch_docs(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                              const CUtensorMap& o, const ScoreParams& p, int grid,
+                              cudaStream_t stream) {
+  return p.doc_k ? score_launch_one<D, BF16, kCap, kBias, true>(q, k, v, o, p, grid, stream)
+                 : score_launch_one<D, BF16, kCap, kBias, false>(q, k, v, o, p, grid, stream);
+}
+
+template <int D, bool BF16>
+cudaError_t score_launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                         const CUtensorMap& o, const ScoreParams& p, int grid,
+                         cudaStream_t stream) {
+  if constexpr (BF16)
+    if (p.cap_fixed) return score_launch_docs<D, BF16, kCapFixed, false>(q, k, v, o, p, grid, stream);
+  if (p.capped)
+    return p.slopes ? score_launch_docs<D, BF16, kCapRunning, true>(q, k, v, o, p, grid, stream)
+                    : score_launch_docs<D, BF16, kCapRunning, false>(q, k, v, o, p, grid, stream);
+  return p.slopes ? score_launch_docs<D, BF16, kCapNone, true>(q, k, v, o, p, grid, stream)
+                  : score_launch_docs<D, BF16, kCapNone, false>(q, k, v, o, p, grid, stream);
+}
+
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
+cudaError_t score_regs_one(int* regs) {
+  cudaFuncAttributes a{};
+  const cudaError_t e = cudaFuncGetAttributes(&a, fa_score_kernel<D, BF16, kCap, kBias, kDocs>);
+  if (e == cudaSuccess && a.numRegs != 128) *regs = a.numRegs;
+  return e;
+}
+
+// Registers per thread of every form: 128, or one that differs.
 template <int D, bool BF16>
 cudaError_t score_regs(int* regs) {
-  cudaFuncAttributes a{};
-  const cudaError_t e = cudaFuncGetAttributes(&a, fa_score_kernel<D, BF16>);
-  if (e == cudaSuccess) *regs = a.numRegs;
+  *regs = 128;
+  cudaError_t e = cudaSuccess;
+  auto look = [&](cudaError_t r) { e = e == cudaSuccess ? r : e; };
+  look(score_regs_one<D, BF16, kCapNone, false, false>(regs));
+  look(score_regs_one<D, BF16, kCapNone, false, true>(regs));
+  look(score_regs_one<D, BF16, kCapNone, true, false>(regs));
+  look(score_regs_one<D, BF16, kCapNone, true, true>(regs));
+  look(score_regs_one<D, BF16, kCapRunning, false, false>(regs));
+  look(score_regs_one<D, BF16, kCapRunning, false, true>(regs));
+  look(score_regs_one<D, BF16, kCapRunning, true, false>(regs));
+  look(score_regs_one<D, BF16, kCapRunning, true, true>(regs));
+  if constexpr (BF16) {
+    look(score_regs_one<D, BF16, kCapFixed, false, false>(regs));
+    look(score_regs_one<D, BF16, kCapFixed, false, true>(regs));
+  }
   return e;
 }
 
