@@ -65,9 +65,21 @@ static_assert(128 * (2 * kRegsScoreSoftmax<true> + kRegsScoreEpilogue<true> +
 // fixed reference, which the cap allows where it bounds every score enough.
 enum CapForm { kCapNone = 0, kCapRunning = 1, kCapFixed = 2 };
 
+// One work item, worked out by the producer and handed to the other roles
+// through a ring in shared memory (worked out by each of them, its divisions
+// took 10 % of the kernel's time, 18 % at D = 64).
 struct ScoreItem {
+  int valid;       // 0: no more items
   int rh, b, kvh;  // row head, its batch row, its kv head [B * Hkv]
+  int h0;          // its query head (packed: the group's first)
   int row0, nT0, nT1, t0, split;
+};
+
+template <int D>
+struct ScoreLayout : PrefillLayout<D> {
+  static constexpr int kOffRing = PrefillLayout<D>::kOffMisc + PrefillLayout<D>::kMiscBytes;
+  static constexpr int kSmemBytes = kOffRing + kItemRing * static_cast<int>(sizeof(ScoreItem)) + 1024;
+  static_assert(kOffRing % 4 == 0 && kSmemBytes <= 232448, "shared memory budget");
 };
 
 // First row of stage s of an item.
@@ -83,8 +95,9 @@ __device__ __forceinline__ int2 stage_range(const ScoreParams& p, int b, int row
   int lo = 0, hi = n_all;
   if (p.causal) {
     const int last = min(row + kBM, p.rows) - 1;
-    // the last query token among the rows (packed: of any head)
-    const int i = row / p.Sq == last / p.Sq ? last % p.Sq : p.Sq - 1;
+    // the last query token among the rows (packed rows run through the heads)
+    int i = last;
+    if (p.packed) i = row / p.Sq == last / p.Sq ? last % p.Sq : p.Sq - 1;
     int keys = i + 1 + (p.Skv - p.Sq);
     if (p.prefix) keys = max(keys, p.prefix[b]);
     keys = min(max(keys, 0), p.Skv);
@@ -100,22 +113,26 @@ __device__ __forceinline__ int2 stage_range(const ScoreParams& p, int b, int row
 
 __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int idx) {
   ScoreItem it;
-  const int qi = idx / p.n_splits;
+  it.valid = 1;
+  const int qi = p.n_splits == 1 ? idx : idx / p.n_splits;
   it.split = idx - qi * p.n_splits;
   int qtile;
   if (p.causal) {  // heaviest first
-    qtile = p.n_qtiles - 1 - qi / p.row_heads;
-    it.rh = qi % p.row_heads;
+    const int back = qi / p.row_heads;
+    qtile = p.n_qtiles - 1 - back;
+    it.rh = qi - back * p.row_heads;
   } else {
-    qtile = qi % p.n_qtiles;
     it.rh = qi / p.n_qtiles;
+    qtile = qi - it.rh * p.n_qtiles;
   }
   if (p.packed) {
     it.b = it.rh / p.Hkv;
     it.kvh = it.rh;
+    it.h0 = (it.rh - it.b * p.Hkv) * p.group;
   } else {
     it.b = it.rh / p.H;
-    it.kvh = it.b * p.Hkv + (it.rh - it.b * p.H) / (p.H / p.Hkv);
+    it.h0 = it.rh - it.b * p.H;
+    it.kvh = it.b * p.Hkv + it.h0 / p.group;
   }
   it.row0 = qtile * kRowsPerCta;
   int2 r0 = stage_range(p, it.b, stage_row(p, it.row0, 0));
@@ -137,6 +154,20 @@ __device__ __forceinline__ int claim_score_item(const ScoreParams& p) {
   const unsigned long long ticket = atomicAdd(p.sched, 1ull);
   const unsigned long long idx = gridDim.x + ticket;
   return idx < static_cast<unsigned long long>(p.n_items) ? static_cast<int>(idx) : -1;
+}
+
+// The k-th item of this CTA, as published by the producer.
+template <unsigned kSleepNs>
+__device__ __forceinline__ ScoreItem take_score_item(const ScoreItem* ring, uint32_t full,
+                                                     uint32_t empty, uint32_t k, const Ctl& c,
+                                                     bool& ok) {
+  const uint32_t slot = k % kItemRing;
+  ok = wait_bar_warp<kSleepNs>(full + 8u * slot, (k / kItemRing) & 1, c);
+  ScoreItem it{};
+  if (ok) it = ring[slot];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(empty + 8u * slot);
+  return it;
 }
 
 // What a softmax thread knows of its row during an item, and its warp of all 32.
@@ -446,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmV,
                     const __grid_constant__ CUtensorMap tmO,
                     const ScoreParams p) {
-  using L = PrefillLayout<D>;
+  using L = ScoreLayout<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -456,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sOut = sbase + L::kOffOut;
   const uint32_t bars = sbase + L::kOffBars;
   float* inv_l_smem = reinterpret_cast<float*>(smem + L::kOffInvL);
-  volatile int* item_ring = reinterpret_cast<volatile int*>(smem + L::kOffItems);
+  ScoreItem* item_ring = reinterpret_cast<ScoreItem*>(smem + L::kOffRing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffTmemSlot);
   volatile uint32_t* abort_flag =
       reinterpret_cast<volatile uint32_t*>(smem + L::kOffAbort);
@@ -526,15 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
     for (uint32_t k = 0; ok; ++k) {
-      const int idx = take_item<0>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
-      if (!ok || idx < 0) break;
-      const ScoreItem it = get_score_item(p, idx);
+      const ScoreItem it =
+          take_score_item<0>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
+      if (!ok || !it.valid) break;
       const int nT = s == 0 ? it.nT0 : it.nT1;
       const int row_g = stage_row(p, it.row0, s) + r;  // row of the row head
       const bool stored = row_g < p.rows;
       ScoreRow row{};
       {
-        const int h_in = row_g / p.Sq;  // packed: the head within its group
+        const int h_in = p.packed ? row_g / p.Sq : 0;  // the head within its group
         const int i = row_g - h_in * p.Sq;
         row.pos = i + (p.Skv - p.Sq);
         row.lim = p.Skv;
@@ -545,8 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             row.lim = min(max(row.lim, 0), p.Skv);
           }
           if constexpr (kBias)
-            row.slope = p.slopes[p.packed ? (it.rh % p.Hkv) * (p.H / p.Hkv) + h_in : it.rh % p.H] *
-                        1.4426950408889634f;
+            row.slope = p.slopes[it.h0 + h_in] * 1.4426950408889634f;
         }
         row.lim_warp = __reduce_min_sync(0xffffffffu, row.lim);
         if constexpr (kDocs) {
@@ -611,10 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
 #pragma unroll 1
     for (uint32_t k = 0; ok; ++k) {
-      const int idx = take_item<kSleepEpilogueNs>(item_ring, bar(L::ITEM_FULL),
-                                                  bar(L::ITEM_EMPTY), k, ctl, ok);
-      if (!ok || idx < 0) break;
-      const ScoreItem it = get_score_item(p, idx);
+      const ScoreItem it = take_score_item<kSleepEpilogueNs>(item_ring, bar(L::ITEM_FULL),
+                                                             bar(L::ITEM_EMPTY), k, ctl, ok);
+      if (!ok || !it.valid) break;
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (!ok) continue;
@@ -751,10 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int kq = 0;                     // items begun (Q_FULL phase)
       int fK = 0;                     // fill of the current item's K_0
       bool ok = true;
-      const int first = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL),
-                                               bar(L::ITEM_EMPTY), 0, ctl, ok);
-      ScoreItem cur = first >= 0 ? get_score_item(p, first) : ScoreItem{};
-      if (ok && first >= 0) ok = begin(cur, 0, 0);
+      ScoreItem cur = take_score_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL),
+                                                   bar(L::ITEM_EMPTY), 0, ctl, ok);
+      if (ok && cur.valid) ok = begin(cur, 0, 0);
       else ok = false;
 #pragma unroll 1
       while (ok) {
@@ -765,10 +793,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto take_next = [&]() {
           if (taken) return;
           taken = true;
-          const int nidx = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL),
-                                                  bar(L::ITEM_EMPTY), kq + 1, ctl, ok);
-          has_next = ok && nidx >= 0;
-          if (has_next) nxt = get_score_item(p, nidx);
+          nxt = take_score_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY),
+                                             kq + 1, ctl, ok);
+          has_next = ok && nxt.valid;
         };
         const int fN = fK + 2 * cur.nT1;  // the next item's K_0
 #pragma unroll 1
@@ -898,10 +925,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        item_ring[slot] = idx;
+        const ScoreItem it = idx < 0 ? ScoreItem{} : get_score_item(p, idx);
+        item_ring[slot] = it;
         mbar_arrive(bar(L::ITEM_FULL + slot));
         if (idx < 0) break;
-        const ScoreItem it = get_score_item(p, idx);
         ok = load_q(it, 0);
 #pragma unroll 1
         for (int j = 0; ok && j < it.nT1; ++j) {

@@ -18,7 +18,7 @@ struct ScoreParams {
   unsigned long long* sched;  // this launch's scheduler slot
   unsigned* status;
   unsigned long long timeout_ns;
-  int H, Hkv, Sq, Skv;
+  int H, Hkv, group, Sq, Skv;  // group = H / Hkv
   // Rows are taken per row head: a query head's Sq rows, or, packed, the
   // group * Sq rows of the query heads that share a kv head.
   int packed;

@@ -177,6 +177,7 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   p.timeout_ns = env.timeout_ns;
   p.H = H;
   p.Hkv = Hkv;
+  p.group = H / Hkv;
   p.Sq = Sq;
   p.Skv = Skv;
   p.packed = plan.packed;

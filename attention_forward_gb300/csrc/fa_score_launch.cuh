@@ -22,12 +22,12 @@ cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
     if (!done[dev]) {
       e = cudaFuncSetAttribute(fa_score_kernel<D, BF16, kCap, kBias, kDocs>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               PrefillLayout<D>::kSmemBytes);
+                               ScoreLayout<D>::kSmemBytes);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  fa_score_kernel<D, BF16, kCap, kBias, kDocs><<<grid, kThreads, PrefillLayout<D>::kSmemBytes, stream>>>(q, k, v, o, p);
+  fa_score_kernel<D, BF16, kCap, kBias, kDocs><<<grid, kThreads, ScoreLayout<D>::kSmemBytes, stream>>>(q, k, v, o, p);
   return cudaGetLastError();
 }
 
