@@ -749,10 +749,6 @@ fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int h
   return st != FA_OK ? st : encode_3d(m, base, D, rows, heads, box_rows, bf16);
 }
 
-int choose_prefill_splits(int heads, int rows, int Skv, int sm_count) {
-  return prefill_splits(heads, rows, Skv, sm_count, 0);
-}
-
 }  // namespace fa
 
 extern "C" {

@@ -54,7 +54,4 @@ int device_sms();
 fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int heads,
                         int box_rows, bool bf16);
 
-// The key split fa_fwd would choose for `heads` heads of `rows` query rows.
-int choose_prefill_splits(int heads, int rows, int Skv, int sm_count);
-
 }  // namespace fa

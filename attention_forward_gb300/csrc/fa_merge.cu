@@ -1,25 +1,36 @@
-// fa_merge.cu -- the merge of equal key ranges of all rows, one block a row.  It
-// starts while the kernel before it still runs (programmatic dependent
-// launch).
+// fa_merge.cu -- the merge of equal key ranges of all rows.  It starts while the
+// kernel before it still runs (programmatic dependent launch).
 #include "fa_merge.cuh"
 #include "fa_merge.h"
 
 namespace fa {
 namespace {
 
-template <int D, bool BF16>
+// Parts up to which a row is one warp's: their loads go out at once.
+constexpr int kWarpParts = 8;
+
+template <int D, bool BF16, bool kByWarp>
 __global__ void __launch_bounds__(kMergeWarps * 32) fa_merge_kernel(const MergeParams p) {
-  __shared__ MergeSmem<D> sm;
-  const long long row = blockIdx.x;
   grid_dependency_wait();
-  merge_row<D, BF16>(p.part_o, p.part_lse, p.n_splits,
-                     [&](int s) -> long long { return s * p.rows + row; }, p.o, p.lse, row, sm);
+  if constexpr (kByWarp) {
+    const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    if (row >= p.rows) return;
+    merge_row_warp<D, BF16>(p.part_o, p.part_lse, p.n_splits,
+                            [&](int s) -> long long { return s * p.rows + row; }, p.o, p.lse, row);
+  } else {
+    __shared__ MergeSmem<D> sm;
+    const long long row = blockIdx.x;
+    merge_row<D, BF16>(p.part_o, p.part_lse, p.n_splits,
+                       [&](int s) -> long long { return s * p.rows + row; }, p.o, p.lse, row, sm);
+  }
 }
 
 template <int D, bool BF16>
 cudaError_t launch(const MergeParams& p, cudaStream_t stream) {
+  const bool by_warp = p.n_splits <= kWarpParts;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(by_warp ? (p.rows + kMergeWarps - 1) / kMergeWarps : p.rows),
+                     1, 1);
   cfg.blockDim = dim3(kMergeWarps * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -27,7 +38,8 @@ cudaError_t launch(const MergeParams& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_merge_kernel<D, BF16>, p);
+  return by_warp ? cudaLaunchKernelEx(&cfg, fa_merge_kernel<D, BF16, true>, p)
+                 : cudaLaunchKernelEx(&cfg, fa_merge_kernel<D, BF16, false>, p);
 }
 
 }  // namespace

@@ -46,6 +46,31 @@ constexpr int kPackTokens = 128;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Key ranges per item where the items are fewer than the SMs: the count with the
+// smallest estimated time, in quarters of a key tile (about 0.4 us): rounds of
+// one item an SM, each the tiles of a range and, split, the partials of its
+// rows written and read again (16 quarters for 256 rows of 128 fp32 channels), 4
+// to begin it,
+// and 6 for the merge.  A split has to gain an eighth.  Measured: 8 heads of one
+// token over 700 keys 15.2 us whole, 10.5 split; 8 heads of 2048 x 2048 tokens
+// 31.7 us whole, 34.0 in 2 ranges, 105 in 16.
+int choose_splits(long long n_items, int rows, int D, int n_tiles, int sm_count) {
+  const long long sms = sm_count > 0 ? sm_count : 152;
+  if (n_items >= sms) return 1;
+  const int part = 16 * std::min(rows, fa::kRowsPerCta) * D / (fa::kRowsPerCta * 128);
+  int best = 1;
+  long long best_cost = (4LL * n_tiles + 4) * 7 / 8;
+  for (int s = 2; s <= std::min(n_tiles, 64); ++s) {
+    const int tiles = (n_tiles + s - 1) / s, ranges = (n_tiles + tiles - 1) / tiles;
+    const long long cost = (n_items * ranges + sms - 1) / sms * (4 * tiles + 4 + part) + 6;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = ranges;
+    }
+  }
+  return best;
+}
+
 struct Plan {
   int packed, row_heads, rows, n_qtiles, n_key_tiles, n_stages;
   int n_splits, tiles_per_split;
@@ -62,7 +87,8 @@ Plan make_plan(int B, int H, int Hkv, int Sq, int Skv, int D, bool documents, in
   p.n_key_tiles = (Skv + fa::kBN - 1) / fa::kBN;
   p.n_stages = (p.rows + fa::kBM - 1) / fa::kBM;
   const long long all_rows = static_cast<long long>(p.row_heads) * p.rows;
-  int s = fa::choose_prefill_splits(p.row_heads, p.rows, Skv, sm_count);
+  int s = choose_splits(static_cast<long long>(p.row_heads) * p.n_qtiles, p.rows, D,
+                        p.n_key_tiles, sm_count);
   if (all_rows > 0x7fffffffLL) s = 1;  // the merge's grid
   p.tiles_per_split = (p.n_key_tiles + s - 1) / s;
   p.n_splits = (p.n_key_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
