@@ -5,23 +5,35 @@ namespace fa {
 namespace {
 
 // A grid of (token blocks, B * Hkv): fa_cache_* checks that both fit.
-template <int D>
-dim3 grid_of(const CacheCopyParams& p) {
-  constexpr int kTokens = kCacheCopyRows<D> * kCacheCopyTurns;
-  return dim3(static_cast<unsigned>((p.S + kTokens - 1) / kTokens),
+dim3 grid_of(const CacheCopyParams& p, int tokens) {
+  return dim3(static_cast<unsigned>((p.S + tokens - 1) / tokens),
               static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv));
+}
+
+// Launched to overlap the end of the kernel before, which the kernels wait for
+// (programmatic dependent launch).
+template <class Kernel>
+cudaError_t launch(Kernel kernel, const CacheCopyParams& p, int tokens, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid_of(p, tokens);
+  cfg.blockDim = dim3(kCacheCopyThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D, bool BF16>
 cudaError_t write(const CacheCopyParams& p, cudaStream_t stream) {
-  fa_cache_write_kernel<D, BF16><<<grid_of<D>(p), kCacheCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(fa_cache_write_kernel<D, BF16>, p, kCacheCopyRows<D> * kCacheWriteTurns, stream);
 }
 
 template <int D, bool BF16>
 cudaError_t read(const CacheCopyParams& p, cudaStream_t stream) {
-  fa_cache_read_kernel<D, BF16><<<grid_of<D>(p), kCacheCopyThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch(fa_cache_read_kernel<D, BF16>, p, kCacheCopyRows<D> * kCacheReadTurns, stream);
 }
 
 }  // namespace

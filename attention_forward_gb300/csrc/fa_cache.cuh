@@ -41,16 +41,17 @@ __device__ __forceinline__ uint32_t cache_pack(float lo, float hi) {
   }
 }
 
-// Where token i of sequence b lies in a head's rows of the pool: its (page,
-// slot) as page << shift | slot, or -1 when its place does not exist (a
-// position or page out of range).
-__device__ __forceinline__ long long cache_place(const CacheCopyParams& p, int b, int start, int i) {
-  const long long pos = static_cast<long long>(start) + i;
-  if (pos < 0 || (pos >> p.page_shift) >= p.max_pages) return -1;
-  const int n = static_cast<int>(pos >> p.page_shift);
+// The pool's row of the token at position `pos` of sequence b, for kv head hk
+// (pages, then heads, then slots); -1 when its place does not exist.  A
+// position below 0 is past every page table as an unsigned number.
+__device__ __forceinline__ long long cache_row(const CacheCopyParams& p, int b, int hk,
+                                               uint32_t pos) {
+  const uint32_t n = pos >> p.page_shift;
+  if (n >= static_cast<uint32_t>(p.max_pages)) return -1;
   const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + n];
   if (page < 0 || page >= p.num_pages) return -1;
-  return (static_cast<long long>(page) << p.page_shift) | (pos & ((1 << p.page_shift) - 1));
+  return ((static_cast<long long>(page) * p.Hkv + hk) << p.page_shift) +
+         (pos & ((1u << p.page_shift) - 1u));
 }
 
 // min / max that a NaN goes through.
@@ -71,10 +72,11 @@ __device__ __forceinline__ float min3_nan(float a, float b, float c) {
 // A code is floor((x - z) / s + 1/2), decided exactly.  q = d inv + 1.5 2^23
 // leaves the nearest integer c to d / s (d = x - z, inv = 1 / s, both
 // rounded) in the low bits of q, and r = d - c s is exact in one FMA (c s has
-// 15 bits, and d is within a scale of it).  While every |r| of the lane is
-// clearly below half a scale, c is the code.  Else (a tie or next to one) the
-// lane takes the long way: err, what the subtraction lost (two-sum), joins r,
-// and the sign against half a scale says whether c moves by one.
+// 15 bits, and d is within a scale of it); r >= s / 2 (a tie that went down)
+// adds one.  That is the code wherever d is x - z exactly, as it is unless x
+// has bits 2^24 below z.  Only beside a tie can the lost bits decide: there
+// the lane looks for them (two-sum), and with any of them goes through its
+// channels with err, the lost part, added to r.
 __device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& word,
                                                uint32_t& param) {
   constexpr float kMagic = 12582912.f;  // 1.5 2^23
@@ -99,7 +101,9 @@ __device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& wo
   lo = fminf(fmaxf(lo, -kCacheLimit), kCacheLimit);
   hi = fminf(fmaxf(hi, -kCacheLimit), kCacheLimit);
   const __half zh = __float2half_rn(lo);
-  const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+  // (hi - lo) / 15, correctly rounded: a product by 1/15 and its residual
+  const float range = hi - lo, near15 = range * (1.f / 15.f);
+  const __half sh = __float2half_rn(fmaf(fmaf(-15.f, near15, range), 1.f / 15.f, near15));
   param = static_cast<uint32_t>(__half_as_ushort(sh)) |
           (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
   const float z = __half2float(zh), s = __half2float(sh);
@@ -107,48 +111,83 @@ __device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& wo
     word = 0u;
     return;
   }
-  const float inv = __frcp_rn(s);
+  const float inv = __fdividef(1.f, s);  // q may miss by one: r shows it
+  const float half_s = 0.5f * s;
   float far = 0.f;
   word = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float d = x[e] - z;
-    const float q = fmaf(d, inv, kMagic);
+    float q = fmaf(d, inv, kMagic);
     const float r = fmaf(-(q - kMagic), s, d);
     far = fmaxf(far, fabsf(r));
+    q += r >= half_s ? 1.f : 0.f;
     // each q's bits are the magic's and the code: the magic's share of the
     // sum is taken off below
     word += __float_as_uint(fminf(fmaxf(q, kMagic), kMagic + 15.f)) << (4 * e);
   }
   constexpr uint32_t kMagicBits = 0x4b400000u;
   word -= kMagicBits * 0x11111111u;
-  // a value past the limit leaves r = NaN or far above half a scale
-  if (!(far < s * 0.499998f)) {
-    const float half_s = 0.5f * s;
-    word = 0u;
-#pragma unroll 1
-    for (int e = 0; e < 8; ++e) {
-      float v = x[0];
+  if (!(far < s * 0.499998f)) {  // a tie or next to one, or a value past the limit
+    bool lost = !(far <= half_s);
 #pragma unroll
-      for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
-      v = fminf(fmaxf(v, -kCacheLimit), kCacheLimit);
-      const float d = v - z;
-      const float bb = d - v;
-      const float err = (v - (d - bb)) + (-z - bb);
-      float c = rintf(d * inv);
-      const float r = fmaf(-c, s, d);
-      if ((r - half_s) + err >= 0.f) c += 1.f;
-      if ((r + half_s) + err < 0.f) c -= 1.f;
-      word |= static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f)) << (4 * e);
+    for (int e = 0; e < 8; ++e) {
+      const float d = x[e] - z, bb = d - x[e];
+      lost |= (x[e] - (d - bb)) + (-z - bb) != 0.f;
+    }
+    if (lost) {
+      word = 0u;
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        float v = x[0];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) v = e == k ? x[k] : v;
+        v = fminf(fmaxf(v, -kCacheLimit), kCacheLimit);
+        const float d = v - z;
+        const float bb = d - v;
+        const float err = (v - (d - bb)) + (-z - bb);
+        float c = rintf(d * inv);
+        const float r = fmaf(-c, s, d);
+        if ((r - half_s) + err >= 0.f) c += 1.f;
+        if ((r + half_s) + err < 0.f) c -= 1.f;
+        word |= static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f)) << (4 * e);
+      }
     }
   }
 }
 
+// The 8 values of a word, rounded once to 16 bits, in the order of their
+// channels.  Two codes at a time are cut out as fp16 pairs (channels e, e + 4):
+// a code masked into the low or high nibble of a fp16 mantissa is 1024 or 64
+// too large.
+template <bool BF16>
+__device__ __forceinline__ uint4 cache_values(uint32_t word, uint32_t param) {
+  const __half2 sz = *reinterpret_cast<const __half2*>(&param);
+  const uint32_t y = word >> 8;
+  const uint32_t bits[4] = {(word & 0x000f000fu) | 0x64006400u, (word & 0x00f000f0u) | 0x54005400u,
+                            (y & 0x000f000fu) | 0x64006400u, (y & 0x00f000f0u) | 0x54005400u};
+  uint32_t v[4];  // channels (e, e + 4)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&bits[e]),
+                              __float2half2_rn(e & 1 ? 64.f : 1024.f));
+    if constexpr (BF16) {
+      const float s = __low2float(sz), z = __high2float(sz);
+      v[e] = cache_pack<true>(fmaf(__low2float(c), s, z), fmaf(__high2float(c), s, z));
+    } else {
+      const __half2 r = __hfma2(c, __low2half2(sz), __high2half2(sz));
+      v[e] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
 // Rows per block: the lanes of a row lie side by side.  blockIdx.y is the
 // (sequence, kv head), blockIdx.x the block of its tokens; a thread takes
-// kCacheCopyTurns tokens, whose loads go out together.
+// a few tokens in turn, whose loads go out together.
 constexpr int kCacheCopyThreads = 128;
-constexpr int kCacheCopyTurns = 4;
+constexpr int kCacheWriteTurns = 2, kCacheReadTurns = 2;  // 1 ... 8 measured within 6 %
 
 template <int D>
 constexpr int kCacheCopyRows = kCacheCopyThreads / (D / 8);
@@ -156,19 +195,23 @@ constexpr int kCacheCopyRows = kCacheCopyThreads / (D / 8);
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const CacheCopyParams p) {
   constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+  constexpr int kTurns = kCacheWriteTurns;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 8 lane ... + 7
   const int bh = static_cast<int>(blockIdx.y);
   const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
-  const int count = p.count ? min(p.count[b], p.S) : p.S;
-  const int i0 = static_cast<int>(blockIdx.x) * kRows * kCacheCopyTurns +
-                 static_cast<int>(threadIdx.x) / kLanes;
-  if (i0 - static_cast<int>(threadIdx.x) / kLanes >= count) return;
+  const int first = static_cast<int>(blockIdx.x) * kRows * kTurns;
   const int start = p.start ? p.start[b] : 0;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  if (first >= count) return;
+  const int i0 = first + static_cast<int>(threadIdx.x) / kLanes;
   const int g = lane >> 2, t = lane & 3;
 
-  uint4 w[kCacheCopyTurns][2];
+  uint4 w[kTurns][2];
+  long long row[kTurns];
 #pragma unroll
-  for (int k = 0; k < kCacheCopyTurns; ++k) {
+  for (int k = 0; k < kTurns; ++k) {
     const int i = i0 + k * kRows;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -177,16 +220,11 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const
         w[k][n] = __ldcs(reinterpret_cast<const uint4*>(p.rows[n]) +
                          (static_cast<size_t>(bh) * p.S + i) * kLanes + lane);
     }
+    row[k] = i < count ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
+    if (i < count && row[k] < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
   }
 #pragma unroll
-  for (int k = 0; k < kCacheCopyTurns; ++k) {
-    const int i = i0 + k * kRows;
-    const long long at = i < count ? cache_place(p, b, start, i) : -1;
-    if (i < count && at < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
-    // the pool's row: pages, then heads, then slots
-    const long long page = at >> p.page_shift;
-    const size_t row = at < 0 ? 0 : static_cast<size_t>(((page * p.Hkv + hk) << p.page_shift) +
-                                                        (at & ((1 << p.page_shift) - 1)));
+  for (int k = 0; k < kTurns; ++k) {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const float2 a = cache_unpack<BF16>(w[k][n].x), b2 = cache_unpack<BF16>(w[k][n].y);
@@ -194,9 +232,9 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const
       const float x[8] = {a.x, a.y, b2.x, b2.y, c.x, c.y, d.x, d.y};
       uint32_t word, param;
       cache_quantise(x, word, param);
-      if (at >= 0) {
-        reinterpret_cast<uint32_t*>(p.pool.codes[n])[row * kLanes + kGroups * t + g] = word;
-        if (t == 0) p.pool.params[n][row * kGroups + g] = param;
+      if (row[k] >= 0) {
+        reinterpret_cast<uint32_t*>(p.pool.codes[n])[row[k] * kLanes + kGroups * t + g] = word;
+        if (t == 0) p.pool.params[n][row[k] * kGroups + g] = param;
       }
     }
   }
@@ -205,29 +243,30 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const CacheCopyParams p) {
   constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+  constexpr int kTurns = kCacheReadTurns;
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 8 lane ... + 7
   const int bh = static_cast<int>(blockIdx.y);
   const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int start = p.start ? p.start[b] : 0;
   const int count = p.count ? min(p.count[b], p.S) : p.S;
-  const int i0 = static_cast<int>(blockIdx.x) * kRows * kCacheCopyTurns +
+  const int i0 = static_cast<int>(blockIdx.x) * kRows * kTurns +
                  static_cast<int>(threadIdx.x) / kLanes;
   if (i0 >= count) return;
-  const int start = p.start ? p.start[b] : 0;
   const int g = lane >> 2, t = lane & 3;
 
-  uint32_t word[kCacheCopyTurns][2], param[kCacheCopyTurns][2];
+  uint32_t word[kTurns][2], param[kTurns][2];
 #pragma unroll
-  for (int k = 0; k < kCacheCopyTurns; ++k) {
+  for (int k = 0; k < kTurns; ++k) {
     const int i = i0 + k * kRows;
-    const long long at = i < count ? cache_place(p, b, start, i) : -1;
-    if (i < count && at < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
-    const long long page = at >> p.page_shift;
-    const size_t row = at < 0 ? 0 : static_cast<size_t>(((page * p.Hkv + hk) << p.page_shift) +
-                                                        (at & ((1 << p.page_shift) - 1)));
+    const long long row =
+        i < count ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
+    if (i < count && row < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       word[k][n] = param[k][n] = 0u;  // a place that does not exist reads as zeros
-      if (at >= 0) {
+      if (row >= 0) {
         word[k][n] = __ldg(reinterpret_cast<const uint32_t*>(p.pool.codes[n]) + row * kLanes +
                            kGroups * t + g);
         param[k][n] = __ldg(p.pool.params[n] + row * kGroups + g);
@@ -235,26 +274,13 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const 
     }
   }
 #pragma unroll
-  for (int k = 0; k < kCacheCopyTurns; ++k) {
+  for (int k = 0; k < kTurns; ++k) {
     const int i = i0 + k * kRows;
     if (i >= count) return;
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const float2 sz = __half22float2(*reinterpret_cast<const __half2*>(&param[k][n]));
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the code as a float: in the low bits of 2^23
-        const float c = __uint_as_float(((word[k][n] >> (4 * e)) & 15u) | 0x4b000000u) - 8388608.f;
-        x[e] = fmaf(c, sz.x, sz.y);
-      }
-      uint4 out;
-      out.x = cache_pack<BF16>(x[0], x[1]);
-      out.y = cache_pack<BF16>(x[2], x[3]);
-      out.z = cache_pack<BF16>(x[4], x[5]);
-      out.w = cache_pack<BF16>(x[6], x[7]);
-      reinterpret_cast<uint4*>(p.rows[n])[(static_cast<size_t>(bh) * p.S + i) * kLanes + lane] = out;
-    }
+    for (int n = 0; n < 2; ++n)
+      reinterpret_cast<uint4*>(p.rows[n])[(static_cast<size_t>(bh) * p.S + i) * kLanes + lane] =
+          cache_values<BF16>(word[k][n], param[k][n]);
   }
 }
 

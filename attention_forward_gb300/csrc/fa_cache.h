@@ -45,6 +45,7 @@ struct CacheAttnParams {
   int B, H, Hkv, Sq;
   int rows;               // (H / Hkv) * Sq query rows per kv head
   int n_row_blocks;
+  int whole;              // CTAs take whole units: no parts, no merge
   int num_pages, page_shift, max_pages;
   float scale;
   float cap;              // cap > 0: score = cap * tanh(score / cap)
@@ -65,9 +66,15 @@ constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;  // a chunk of the work: a 
 #define FA_OCC2 3
 #define FA_MIN 4
 #endif
+#ifndef FA_WHOLE
+#define FA_WHOLE 1024
+#endif
 constexpr int kCacheMinChunks = FA_MIN;    // a CTA's least share
 constexpr int kCacheAttnStages = FA_ST;  // tiles of a warp's ring
 constexpr int kCachePiece = 4096;        // keys whose tiles' places are in shared memory at once
+// Page tables of at most this many keys are not split: 64 kv heads of 701 keys
+// took 10.3 us split and merged, WHOLEUS whole.
+constexpr int kCacheWholeKeys = FA_WHOLE;
 // CTAs for `units` row blocks of up to `room` keys.
 int cache_attn_grid(int rows, long long units, int room, int sm_count);
 cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, int grid,

@@ -84,7 +84,7 @@ fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const 
 
 // The attention's persistent CTAs and the memory for their parts.
 struct AttnPlan {
-  int row_blocks, grid;
+  int row_blocks, grid, whole;
   size_t o_bytes, bytes;
 };
 
@@ -94,7 +94,8 @@ AttnPlan plan_attn(int B, int H, int Hkv, int Sq, int D, const PageShape& s, int
   a.row_blocks = (rows + block - 1) / block;
   a.grid = fa::cache_attn_grid(rows, static_cast<long long>(B) * Hkv * a.row_blocks,
                                s.max_pages * s.page_size, sm_count);
-  if (a.grid > 1) {
+  a.whole = s.max_pages * s.page_size <= fa::kCacheWholeKeys ? 1 : 0;
+  if (!a.whole) {
     const size_t n = 2u * static_cast<size_t>(a.grid) * block;
     a.o_bytes = up256(n * D * sizeof(float));
     a.bytes = a.o_bytes + up256(n * sizeof(float));
@@ -179,6 +180,7 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   p.Sq = Sq;
   p.rows = (H / Hkv) * Sq;
   p.n_row_blocks = plan.row_blocks;
+  p.whole = plan.whole;
   p.num_pages = num_pages;
   p.page_shift = shift_of(page_size);
   p.max_pages = max_pages;

@@ -7,22 +7,23 @@ namespace {
 template <int D, bool BF16, int NT, bool kMod>
 cudaError_t launch(const CacheAttnParams& p, int grid, cudaStream_t stream) {
   static_assert(sizeof(CacheAttnSmem<D, NT>) <= 48 * 1024, "no opt-in shared memory");
-  fa_cache_attn_kernel<D, BF16, NT, kMod>
-      <<<grid, kCacheAttnThreads, sizeof(CacheAttnSmem<D, NT>), stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || grid == 1) return e;  // one CTA: nothing is shared
-  // the merge starts while the CTAs run and waits for them (programmatic
-  // dependent launch)
+  // launched to overlap the end of the kernel before, which it waits for, as
+  // the merge overlaps this one's (programmatic dependent launch)
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv) *
-                         static_cast<unsigned>(p.rows), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(kCacheAttnThreads, 1, 1);
+  cfg.dynamicSmemBytes = sizeof(CacheAttnSmem<D, NT>);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_cache_attn_kernel<D, BF16, NT, kMod>, p);
+  if (e != cudaSuccess || p.whole) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv) *
+                         static_cast<unsigned>(p.rows), 1, 1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, BF16, NT>, p, grid);
 }
 
@@ -40,7 +41,8 @@ int cache_attn_row_block(int rows) { return rows <= 8 ? 8 : 16; }
 
 int cache_attn_grid(int rows, long long units, int room, int sm_count) {
   const long long chunks = units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys);
-  const long long most = (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
+  const long long most = room <= kCacheWholeKeys ? units
+                                                 : (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
                           (cache_attn_row_block(rows) == 8 ? FA_OCC1 : FA_OCC2);
   return static_cast<int>(most < slots ? most : slots);

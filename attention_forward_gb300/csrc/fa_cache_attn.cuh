@@ -281,8 +281,9 @@ struct CacheAttnSmem {
   };
 };
 
-// Persistent CTAs.  The work is counted in chunks of kCacheAttnKeys keys of a
-// unit (a row block of a kv head of a sequence), units in the order (sequence,
+// Persistent CTAs.  Short caches (p.whole) are dealt in whole units, a row block
+// of a kv head of a sequence each.  Otherwise the work is counted in chunks of kCacheAttnKeys keys of a
+// unit, units in the order (sequence,
 // kv head, row block); the CTAs have equal shares of them
 // (CacheDeal), whatever the lengths, which are read here.  A unit that lies within one CTA is written
 // out; the parts of the others go to the workspace, the CTA's first segment to
@@ -307,15 +308,24 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  int upto;
-  const int all_chunks = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
-  const CacheDeal deal = cache_deal(all_chunks, static_cast<int>(gridDim.x));
-  grid_launch_dependents();  // the merge waits for this grid's end
+  grid_dependency_wait();
+  grid_launch_dependents();  // the merge, and the next kernel, wait for this grid's end
   const int x_cta = static_cast<int>(blockIdx.x);
-  if (x_cta >= deal.n) return;
-  const int first = deal.begin(x_cta), last = deal.begin(x_cta + 1);
-  int b = 0, before = 0;  // the sequence, and the chunks of those before it
-  cache_find(p, sm.scan, upto, first, b, before);
+  const int units = p.Hkv * p.n_row_blocks;  // of a sequence
+  int b, before, first, last;  // the sequence, the chunks of those before it, the CTA's chunks
+  if (p.whole) {  // units x, x + grid, ...: `first` and `last` count units here
+    b = before = 0;
+    first = x_cta;
+    last = p.B * units;
+  } else {
+    int upto;
+    const int all_chunks = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
+    const CacheDeal deal = cache_deal(all_chunks, static_cast<int>(gridDim.x));
+    if (x_cta >= deal.n) return;
+    first = deal.begin(x_cta);
+    last = deal.begin(x_cta + 1);
+    cache_find(p, sm.scan, upto, first, b, before);
+  }
 
   // this lane's places in the ring's tiles and in the pool
   const uint32_t ring = smem_u32(sm.ring[warp]);
@@ -329,15 +339,16 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
   const uint32_t at_vc = T::kVCodes + g * (4 * kWords);
   const uint32_t at_vp = T::kVParams + (g & 1) * (4 * kWords);
   const int vtok[2] = {t, 4 + (t ^ 1)};  // and these + 8: its value tokens
-  const int units = p.Hkv * p.n_row_blocks;
 
 #pragma unroll 1
   for (int cur = first; cur < last;) {
+  if (p.whole) b = cur / units;
   const int len = cache_length(p, b);
+  if (p.whole && threadIdx.x == 0 && len != p.length[b]) atomicExch(p.status, kStatusBadIndex);
   const int seq_chunks = cache_chunks(len);
-  const int unit = (cur - before) / seq_chunks;
-  const int chunk0 = cur - before - unit * seq_chunks;
-  const int n_chunks = min(seq_chunks - chunk0, last - cur);
+  const int unit = p.whole ? cur - b * units : (cur - before) / seq_chunks;
+  const int chunk0 = p.whole ? 0 : cur - before - unit * seq_chunks;
+  const int n_chunks = p.whole ? seq_chunks : min(seq_chunks - chunk0, last - cur);
   const bool whole = n_chunks == seq_chunks;
   const int part = 2 * x_cta + (cur == first ? 0 : 1);
   const int hk = unit / p.n_row_blocks, rb = unit - hk * p.n_row_blocks;
@@ -348,10 +359,14 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
   const int k_end = min(len, k_begin + n_chunks * kCacheAttnKeys);
   const int* pages = p.page_table + static_cast<long long>(b) * p.max_pages;
   // on to the next segment
-  cur += n_chunks;
-  if (chunk0 + n_chunks == seq_chunks && unit == units - 1) {
-    before += seq_chunks * units;
-    ++b;
+  if (p.whole) {
+    cur += static_cast<int>(gridDim.x);
+  } else {
+    cur += n_chunks;
+    if (chunk0 + n_chunks == seq_chunks && unit == units - 1) {
+      before += seq_chunks * units;
+      ++b;
+    }
   }
 
   // The segment's tiles in pieces whose places fit in shared memory: all the

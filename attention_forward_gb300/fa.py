@@ -238,33 +238,14 @@ def fa_fwd_decode_static(q, k, v, scale: float | None = None, out=None,
 # The raw handle of a device's current stream, without making a Stream object.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-
-
-class _OnDevice:
-    """Makes a device current for the length of a call that is not on it."""
-    __slots__ = ("before",)
-
-    def __init__(self, dev: int):
-        now = torch.cuda.current_device()
-        self.before = None
-        if now != dev:
-            self.before = now
-            torch.cuda.set_device(dev)
-
-    def __enter__(self):
-        return self
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-        return False
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _own_memory(tensors, stream) -> None:
     """Memory made on the current stream for work on another one: that stream
     waits for the work that last had it, and the memory outlives the call's."""
     handle = _stream_handle(stream)
-    if handle != _raw_stream(torch.cuda.current_device()):
+    if handle != _raw_stream(_current_device()):
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(handle)
         stream.wait_stream(torch.cuda.current_stream())
@@ -279,10 +260,13 @@ def _bad(t, name: str, dev: int, dtype, shape):
 
 
 def _ptr(t, name: str, dev: int, dtype, shape) -> int:
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
-            or t.get_device() != dev or not t.is_contiguous()):
-        _bad(t, name, dev, dtype, shape)
-    return t.data_ptr()
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass  # not a tensor
+    _bad(t, name, dev, dtype, shape)
 
 
 def _rows16(t, name: str):
@@ -356,18 +340,22 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
         dkp = _ptr(doc_k, "doc_k", dev, torch.int32, (B, Skv))
     if prefix is not None:
         pp = _ptr(prefix, "prefix", dev, torch.int32, (B,))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fa_fwd_score(q, k, v, causal, scale, softcap, slopes, doc_q, doc_k, prefix,
+                                workspace, out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     L = load()
-    with _OnDevice(dev):
-        need = 0
-        if workspace is None:
-            need = L.fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, doc_k is not None)
-        out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
-        st = L.fa_fwd_score(q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq,
-                            Skv, D, sc, bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp,
-                            None if ws is None else ws.data_ptr(), ws_bytes,
-                            _raw_stream(dev) if stream is None else _stream_handle(stream))
-    _check(st, "fa_fwd_score")
+    need = 0
+    if workspace is None:
+        need = L.fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, doc_k is not None)
+    out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
+    st = L.fa_fwd_score(q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv,
+                        D, sc, bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp,
+                        None if ws is None else ws.data_ptr(), ws_bytes,
+                        _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_fwd_score")
     return out, lse
 
 
@@ -413,7 +401,7 @@ def _copy_args(k, v, cache, page_table, start, count):
         start = _ptr(start, "start", dev, torch.int32, (B,))
     if count is not None:
         count = _ptr(count, "count", dev, torch.int32, (B,))
-    return (dev, k.data_ptr(), vptr, (kc, kp, vc, vp), (table, start, count),
+    return (dev, (k.data_ptr(), vptr), (kc, kp, vc, vp), (table, start, count),
             (B, Hkv, S, D, pages, page, per, _DTYPE[k.dtype]))
 
 
@@ -421,11 +409,14 @@ def fa_cache_write(k, v, cache, page_table, start=None, count=None, stream=None)
     """Quantises k, v [B, Hkv, S, D] into the 4-bit cache: token i < count[b]
     (default S) of sequence b goes to position start[b] + i (default i) of the
     pages that page_table [B, max_pages] lists."""
-    dev, kp, vp, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
-    with _OnDevice(dev):
-        st = load().fa_cache_write(kp, vp, *pool, *where, *sizes,
-                                   _raw_stream(dev) if stream is None else _stream_handle(stream))
-    _check(st, "fa_cache_write")
+    dev, rows, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fa_cache_write(k, v, cache, page_table, start, count, stream)
+    st = load().fa_cache_write(*rows, *pool, *where, *sizes,
+                               _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_cache_write")
 
 
 def fa_cache_read(cache, page_table, start=None, count=None, out=None, stream=None):
@@ -435,11 +426,14 @@ def fa_cache_read(cache, page_table, start=None, count=None, out=None, stream=No
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (k, v) to read into")
     k, v = out
-    dev, kp, vp, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
-    with _OnDevice(dev):
-        st = load().fa_cache_read(*pool, *where, kp, vp, *sizes,
-                                  _raw_stream(dev) if stream is None else _stream_handle(stream))
-    _check(st, "fa_cache_read")
+    dev, rows, pool, where, sizes = _copy_args(k, v, cache, page_table, start, count)
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fa_cache_read(cache, page_table, start, count, out, stream)
+    st = load().fa_cache_read(*pool, *where, *rows, *sizes,
+                              _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_cache_read")
     return k, v
 
 
@@ -463,18 +457,22 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
     sp = None
     if slopes is not None:
         sp = _ptr(slopes, "slopes", dev, torch.float32, (H,))
+    if _current_device() != dev:
+        with torch.cuda.device(dev):
+            return fa_fwd_cache(q, cache, page_table, length, scale, softcap, slopes, workspace,
+                                out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     L = load()
-    with _OnDevice(dev):
-        need = 0
-        if workspace is None:
-            need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per)
-        out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
-        st = L.fa_fwd_cache(q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(),
-                            lse.data_ptr(), B, H, Hkv, Sq, D, pages, page, per, sc,
-                            _DTYPE[q.dtype], softcap, sp, None if ws is None else ws.data_ptr(),
-                            ws_bytes, _raw_stream(dev) if stream is None else _stream_handle(stream))
-    _check(st, "fa_fwd_cache")
+    need = 0
+    if workspace is None:
+        need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per)
+    out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
+    st = L.fa_fwd_cache(q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(), lse.data_ptr(),
+                        B, H, Hkv, Sq, D, pages, page, per, sc, _DTYPE[q.dtype], softcap, sp,
+                        None if ws is None else ws.data_ptr(), ws_bytes,
+                        _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_fwd_cache")
     return out, lse
 
 

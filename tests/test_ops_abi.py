@@ -92,7 +92,7 @@ def test_workspace_sizes(lib):
     split = fa.fa_score_workspace_bytes(1, 4, 1, 1, 8192, 128)
     assert split >= 2 * 4 * 129 * 4 and split % 256 == 0
     assert fa.fa_cache_workspace_bytes(1, 4, 3, 1, 64, 16, 4) == 0
-    assert fa.fa_cache_workspace_bytes(1, 4, 1, 1, 64, 16, 4) == 0    # one CTA's work
+    assert fa.fa_cache_workspace_bytes(1, 4, 1, 1, 64, 16, 4) == 0    # short: not split
     n = fa.fa_cache_workspace_bytes(1, 4, 1, 1, 64, 16, 1024)
     assert n >= 2 * 2 * 8 * 65 * 4 and n % 256 == 0
     # however long: the parts of what the GPU holds at once
