@@ -82,9 +82,9 @@ struct ScoreLayout : PrefillLayout<D> {
   static_assert(kOffRing % 4 == 0 && kSmemBytes <= 232448, "shared memory budget");
 };
 
-// First row of stage s of an item.
+// First row of stage s of an item; past the last row where the stage has none.
 __device__ __forceinline__ int stage_row(const ScoreParams& p, int row0, int s) {
-  if (p.one_stage) return s == 1 ? row0 : row0 + kBM;
+  if (p.one_stage) return s == 1 ? row0 : p.rows;
   return row0 + s * kBM;
 }
 
@@ -134,7 +134,7 @@ __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int id
     it.h0 = it.rh - it.b * p.H;
     it.kvh = it.b * p.Hkv + it.h0 / p.group;
   }
-  it.row0 = qtile * kRowsPerCta;
+  it.row0 = qtile * (p.one_stage ? kBM : kRowsPerCta);
   int2 r0 = stage_range(p, it.b, stage_row(p, it.row0, 0));
   int2 r1 = stage_range(p, it.b, stage_row(p, it.row0, 1));
   const int s0 = it.split * p.tiles_per_split, s1 = s0 + p.tiles_per_split;

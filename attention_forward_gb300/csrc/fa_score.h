@@ -24,8 +24,8 @@ struct ScoreParams {
   int packed;
   int row_heads;              // B * H, or packed B * Hkv
   int rows;                   // rows of a row head
-  int one_stage;              // rows <= 128: the item's rows are stage 1's
-  int n_qtiles;               // ceil(rows / kRowsPerCta)
+  int one_stage;              // items of 128 rows, all of them stage 1's
+  int n_qtiles;               // ceil(rows / rows of an item)
   int n_items;                // n_qtiles * row_heads * n_splits
   int causal;
   float scale_log2;           // scale * log2(e)

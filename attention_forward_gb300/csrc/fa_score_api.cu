@@ -46,33 +46,43 @@ constexpr int kPackTokens = 128;
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Key ranges per item where the items are fewer than the SMs: the count with the
-// smallest estimated time, in quarters of a key tile (about 0.4 us): rounds of
-// one item an SM, each the tiles of a range and, split, the partials of its
-// rows written and read again (16 quarters for 256 rows of 128 fp32 channels), 4
-// to begin it,
-// and 6 for the merge.  A split has to gain an eighth.  Measured: 8 heads of one
-// token over 700 keys 15.2 us whole, 10.5 split; 8 heads of 2048 x 2048 tokens
-// 31.7 us whole, 34.0 in 2 ranges, 105 in 16.
-int choose_splits(long long n_items, int rows, int D, int n_tiles, int sm_count) {
+// How the work is cut where its items are fewer than the SMs: into key ranges,
+// and into items of one 128-row stage instead of two.  The smallest estimated
+// time wins, in twentieths of the time of a key tile of 256 rows (1.7 us): rounds
+// of one item an SM, each the tiles of a range, 20 to begin it and, split, 120 for
+// 256 rows of 128 channels of partials written and read again; and 30 for the
+// merge.  A tile of 128 rows takes 19: the stages hide behind each other, and
+// items of one only pay where the SMs take them all at once.  A split has to
+// gain an eighth.  Measured: 8 heads of one token over 700 keys 15.2 us whole,
+// 10.5 split; 8 heads of 2048 x 2048 tokens 31.7 us whole, 105 in 16 ranges; of
+// 1024 x 4096 31 us in 4 ranges of 256 rows, 38 in 2 of 128.
+struct Cut {
+  int one_stage, splits;
+  long long cost;
+};
+
+Cut cut_items(int row_heads, int rows, bool one_stage, int D, int n_tiles, int sm_count) {
+  const int item_rows = one_stage ? fa::kBM : fa::kRowsPerCta;
+  const long long n = static_cast<long long>(row_heads) * ((rows + item_rows - 1) / item_rows);
   const long long sms = sm_count > 0 ? sm_count : 152;
-  if (n_items >= sms) return 1;
-  const int part = 16 * std::min(rows, fa::kRowsPerCta) * D / (fa::kRowsPerCta * 128);
-  int best = 1;
-  long long best_cost = (4LL * n_tiles + 4) * 7 / 8;
+  const int tile = one_stage ? 19 : 20;
+  const int part = 120 * std::min(rows, item_rows) * D / (256 * 128);
+  Cut c{one_stage ? 1 : 0, 1, (n + sms - 1) / sms * (tile * n_tiles + 20)};
+  if (n >= sms) return c;
+  long long best = c.cost * 7 / 8;
   for (int s = 2; s <= std::min(n_tiles, 64); ++s) {
     const int tiles = (n_tiles + s - 1) / s, ranges = (n_tiles + tiles - 1) / tiles;
-    const long long cost = (n_items * ranges + sms - 1) / sms * (4 * tiles + 4 + part) + 6;
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = ranges;
+    const long long cost = (n * ranges + sms - 1) / sms * (tile * tiles + 20 + part) + 30;
+    if (cost < best) {
+      best = c.cost = cost;
+      c.splits = ranges;
     }
   }
-  return best;
+  return c;
 }
 
 struct Plan {
-  int packed, row_heads, rows, n_qtiles, n_key_tiles, n_stages;
+  int packed, row_heads, rows, one_stage, n_qtiles, n_key_tiles, n_stages;
   int n_splits, tiles_per_split;
   size_t doc_bytes, split_bytes;  // the workspace's two parts, documents first
 };
@@ -83,13 +93,18 @@ Plan make_plan(int B, int H, int Hkv, int Sq, int Skv, int D, bool documents, in
   p.packed = group > 1 && Sq <= kPackTokens ? 1 : 0;
   p.row_heads = p.packed ? B * Hkv : B * H;
   p.rows = p.packed ? group * Sq : Sq;
-  p.n_qtiles = (p.rows + fa::kRowsPerCta - 1) / fa::kRowsPerCta;
   p.n_key_tiles = (Skv + fa::kBN - 1) / fa::kBN;
   p.n_stages = (p.rows + fa::kBM - 1) / fa::kBM;
+  Cut cut = cut_items(p.row_heads, p.rows, p.rows <= fa::kBM, D, p.n_key_tiles, sm_count);
+  if (p.rows > fa::kBM) {
+    const Cut one = cut_items(p.row_heads, p.rows, true, D, p.n_key_tiles, sm_count);
+    if (one.cost < cut.cost) cut = one;
+  }
+  p.one_stage = cut.one_stage;
+  const int item_rows = p.one_stage ? fa::kBM : fa::kRowsPerCta;
+  p.n_qtiles = (p.rows + item_rows - 1) / item_rows;
   const long long all_rows = static_cast<long long>(p.row_heads) * p.rows;
-  int s = choose_splits(static_cast<long long>(p.row_heads) * p.n_qtiles, p.rows, D,
-                        p.n_key_tiles, sm_count);
-  if (all_rows > 0x7fffffffLL) s = 1;  // the merge's grid
+  const int s = all_rows > 0x7fffffffLL ? 1 : cut.splits;  // the merge's grid
   p.tiles_per_split = (p.n_key_tiles + s - 1) / s;
   p.n_splits = (p.n_key_tiles + p.tiles_per_split - 1) / p.tiles_per_split;
   if (documents)
@@ -209,7 +224,7 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   p.packed = plan.packed;
   p.row_heads = plan.row_heads;
   p.rows = plan.rows;
-  p.one_stage = plan.rows <= fa::kBM ? 1 : 0;
+  p.one_stage = plan.one_stage;
   p.n_qtiles = plan.n_qtiles;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
