@@ -206,7 +206,7 @@ constexpr int kCacheAttnThreads = kCacheAttnWarps * 32;
 
 struct CacheScan {
   int warp_sum[kCacheAttnWarps];
-  int before, b;
+  int before, b, len;
 };
 
 // The block's threads take the sequences in runs of equal length and add up
@@ -242,23 +242,26 @@ __device__ __forceinline__ int cache_scan(const CacheAttnParams& p, CacheScan& s
   return all * (p.Hkv * p.n_row_blocks);
 }
 
-// The sequence of chunk c, and the chunks before it (all units').
+// The sequence of chunk c, its length, and the chunks before it (all units').
 __device__ __forceinline__ void cache_find(const CacheAttnParams& p, CacheScan& s, int upto, int c,
-                                           int& b, int& before) {
+                                           int& b, int& len, int& before) {
   const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
   const int units = p.Hkv * p.n_row_blocks;
   int at = upto * units;
   for (int k = b0; k < b1 && at <= c; ++k) {
-    const int n = cache_chunks(cache_length(p, k)) * units;
+    const int l = cache_length(p, k);
+    const int n = cache_chunks(l) * units;
     if (c < at + n) {
       s.before = at;
       s.b = k;
+      s.len = l;
     }
     at += n;
   }
   __syncthreads();
   b = s.b;
+  len = s.len;
   before = s.before;
 }
 
@@ -312,9 +315,10 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
   grid_launch_dependents();  // the merge, and the next kernel, wait for this grid's end
   const int x_cta = static_cast<int>(blockIdx.x);
   const int units = p.Hkv * p.n_row_blocks;  // of a sequence
-  int b, before, first, last;  // the sequence, the chunks of those before it, the CTA's chunks
+  // the sequence, its length, the chunks of those before it, the CTA's chunks
+  int b, len, before, first, last;
   if (p.whole) {  // units x, x + grid, ...: `first` and `last` count units here
-    b = before = 0;
+    b = len = before = 0;
     first = x_cta;
     last = p.B * units;
   } else {
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
     if (x_cta >= deal.n) return;
     first = deal.begin(x_cta);
     last = deal.begin(x_cta + 1);
-    cache_find(p, sm.scan, upto, first, b, before);
+    cache_find(p, sm.scan, upto, first, b, len, before);
   }
 
   // this lane's places in the ring's tiles and in the pool
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
 #pragma unroll 1
   for (int cur = first; cur < last;) {
   if (p.whole) b = cur / units;
-  const int len = cache_length(p, b);
+  if (p.whole || cur != first) len = cache_length(p, b);
   if (p.whole && threadIdx.x == 0 && len != p.length[b]) atomicExch(p.status, kStatusBadIndex);
   const int seq_chunks = cache_chunks(len);
   const int unit = p.whole ? cur - b * units : (cur - before) / seq_chunks;

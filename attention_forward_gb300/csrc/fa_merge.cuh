@@ -19,13 +19,13 @@ constexpr int kMergeWarps = 4;
 template <int D>
 struct MergeSmem {
   float part[kMergeWarps][D];
-  float sums[kMergeWarps];
+  float sums[kMergeWarps], tops[kMergeWarps];
 };
 
 // A warp's share of a row: parts first, first + step, ... of n_parts.  Returns
-// the largest LSE of all; o and sum are weighted against it.  part_row(s): the
-// row of part s in part_o [., D] (fp32, O / l) and part_lse [.]; LSE = -inf with
-// O = 0 where a part has no visible key.
+// their largest LSE, against which o and sum are weighted (-inf: none has a
+// key).  part_row(s): the row of part s in part_o [., D] (fp32, O / l) and
+// part_lse [.]; LSE = -inf with O = 0 where a part has no visible key.
 template <int D, class PartRow>
 __device__ __forceinline__ float merge_parts(const float* part_o, const float* part_lse,
                                              int n_parts, int first, int step, PartRow part_row,
@@ -34,10 +34,6 @@ __device__ __forceinline__ float merge_parts(const float* part_o, const float* p
   constexpr float kLog2e = 1.4426950408889634f;
   const int lane = threadIdx.x & 31;
   float top = -INFINITY;
-  for (int s = lane; s < n_parts; s += 32) top = fmaxf(top, part_lse[part_row(s)]);
-#pragma unroll
-  for (int k = 16; k >= 1; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  const float base = top == -INFINITY ? 0.f : top;
   sum = 0.f;
 #pragma unroll
   for (int d = 0; d < kDims; ++d) o[d] = 0.f;
@@ -62,6 +58,15 @@ __device__ __forceinline__ float merge_parts(const float* part_o, const float* p
         }
       }
     }
+    float now = top;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) now = fmaxf(now, lse[k]);
+    const float base = now == -INFINITY ? 0.f : now;
+    const float old = ex2_approx((top - base) * kLog2e);
+    top = now;
+    sum *= old;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) o[d] *= old;
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const float w = ex2_approx((lse[k] - base) * kLog2e);
@@ -92,20 +97,28 @@ __device__ __forceinline__ void merge_row(const float* part_o, const float* part
   constexpr int kDims = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float o[kDims], sum;
-  const float top = merge_parts<D>(part_o, part_lse, n_parts, warp, kMergeWarps, part_row, o, sum);
+  float top = merge_parts<D>(part_o, part_lse, n_parts, warp, kMergeWarps, part_row, o, sum);
 #pragma unroll
   for (int d = 0; d < kDims; ++d) sm.part[warp][lane * kDims + d] = o[d];
-  if (lane == 0) sm.sums[warp] = sum;
+  if (lane == 0) {
+    sm.sums[warp] = sum;
+    sm.tops[warp] = top;
+  }
   __syncthreads();
   const int ch = 2 * static_cast<int>(threadIdx.x);
   if (ch >= D) return;
   float a = 0.f, b = 0.f;
   sum = 0.f;
+  top = sm.tops[0];
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) top = fmaxf(top, sm.tops[w]);
+  const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) {
-    a += sm.part[w][ch];
-    b += sm.part[w][ch + 1];
-    sum += sm.sums[w];
+    const float f = ex2_approx((sm.tops[w] - base) * 1.4426950408889634f);
+    a = fmaf(sm.part[w][ch], f, a);
+    b = fmaf(sm.part[w][ch + 1], f, b);
+    sum = fmaf(sm.sums[w], f, sum);
   }
   // no part has a key: 0; a NaN stays one
   const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -533,6 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();
   grid_launch_dependents();  // the merge of split keys waits for this grid's end
   const Ctl ctl{abort_flag, p.status, p.timeout_ns};
 

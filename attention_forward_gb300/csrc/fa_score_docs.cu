@@ -2,35 +2,39 @@
 // tile the id all of its keys share, per 128-row stage the tiles that hold
 // documents of its rows.
 //
-// One block per batch row, two passes over its ids (4 bytes a token against
-// the attention's 4 D per key and head): the id range of every key tile, then
-// for every stage the first and last tile whose range meets the range of the
-// stage's rows.  Ranges cover any order of ids; documents that lie together
-// make them exact.
+// Two kernels of one warp a task, each a few dependent loads long (4 bytes a
+// token are read): the id ranges of every key tile and every stage's rows, then
+// for every stage the first and last tile whose range meets its own.  Ranges
+// cover any order of ids; documents that lie together make them exact.  As one
+// block per batch row they took 15 us for 16384 tokens.
 #include <climits>
 
 #include "fa_score.h"
+#include "sm103_ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kDocThreads = 1024;
+constexpr int kDocWarps = 8;
 
-__global__ void __launch_bounds__(kDocThreads) fa_doc_tiles_kernel(const DocParams p) {
-  const int b = static_cast<int>(blockIdx.x);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kWarps = kDocThreads / 32;
-  const int* dk = p.doc_k + static_cast<size_t>(b) * p.Skv;
-  const int* dq = p.doc_q + static_cast<size_t>(b) * p.Sq;
-  int* tile_doc = p.tile_doc + static_cast<size_t>(b) * p.n_key_tiles;
-  int2* range = p.tile_range + static_cast<size_t>(b) * p.n_key_tiles;
-  int2* stage = p.stage_tiles + static_cast<size_t>(b) * p.n_stages;
+__device__ __forceinline__ int2 warp_range(int lo, int hi) {
+  return make_int2(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi));
+}
 
-  for (int t = warp; t < p.n_key_tiles; t += kWarps) {
-    int lo = INT_MAX, hi = -1, least = INT_MAX;
+// Tasks 0 ... n_key_tiles - 1: the smallest and largest id >= 0 of a tile's
+// keys, and the id they all have; the others: those of a stage's rows.
+__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_ranges_kernel(const DocParams p) {
+  const int b = static_cast<int>(blockIdx.y), lane = threadIdx.x & 31;
+  const int task = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (task >= p.n_key_tiles + p.n_stages) return;
+  int lo = INT_MAX, hi = -1, least = INT_MAX;
+  if (task < p.n_key_tiles) {
+    const int* dk = p.doc_k + static_cast<size_t>(b) * p.Skv;
 #pragma unroll
     for (int k = 0; k < kBN / 32; ++k) {
-      const int key = t * kBN + 32 * k + lane;
+      const int key = task * kBN + 32 * k + lane;
       if (key < p.Skv) {
         const int d = dk[key];
         least = min(least, d);
@@ -40,54 +44,82 @@ __global__ void __launch_bounds__(kDocThreads) fa_doc_tiles_kernel(const DocPara
         }
       }
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
+    const int2 r = warp_range(lo, hi);
     least = __reduce_min_sync(0xffffffffu, least);
     if (lane == 0) {
-      range[t] = make_int2(lo, hi);
-      tile_doc[t] = lo == hi && least >= 0 ? lo : kDocMixed;
+      p.tile_range[static_cast<size_t>(b) * p.n_key_tiles + task] = r;
+      p.tile_doc[static_cast<size_t>(b) * p.n_key_tiles + task] =
+          r.x == r.y && least >= 0 ? r.x : kDocMixed;
     }
+    return;
   }
-  __syncthreads();
-
-  for (int s = warp; s < p.n_stages; s += kWarps) {
-    const int first = s * kBM, last = min(first + kBM, p.rows) - 1;
-    // the query tokens among the stage's rows (packed rows run through the
-    // group's heads: a stage across two of them has every token)
-    int i0 = first % p.Sq, i1 = last % p.Sq;
-    if (first / p.Sq != last / p.Sq) {
-      i0 = 0;
-      i1 = p.Sq - 1;
-    }
-    int lo = INT_MAX, hi = -1;
-    for (int i = i0 + lane; i <= i1; i += 32) {
+  const int* dq = p.doc_q + static_cast<size_t>(b) * p.Sq;
+  const int s = task - p.n_key_tiles, first = s * kBM, last = min(first + kBM, p.rows) - 1;
+  // the query tokens among the stage's rows (packed rows run through the
+  // group's heads: a stage across two of them has every token)
+  int i0 = first % p.Sq, i1 = last % p.Sq;
+  if (first / p.Sq != last / p.Sq) {
+    i0 = 0;
+    i1 = p.Sq - 1;
+  }
+  // at most 128 tokens: a stage has 128 rows, packed rows at most 128 tokens
+#pragma unroll
+  for (int k = 0; k < kBM / 32; ++k) {
+    const int i = i0 + 32 * k + lane;
+    if (i <= i1) {
       const int d = dq[i];
       if (d >= 0) {
         lo = min(lo, d);
         hi = max(hi, d);
       }
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    int t0 = INT_MAX, t1 = -1;
-    for (int t = lane; t < p.n_key_tiles; t += 32) {
-      const int2 r = range[t];
-      if (r.x <= hi && r.y >= lo && r.x <= r.y && lo <= hi) {
-        t0 = min(t0, t);
-        t1 = max(t1, t);
-      }
-    }
-    t0 = __reduce_min_sync(0xffffffffu, t0);
-    t1 = __reduce_max_sync(0xffffffffu, t1);
-    if (lane == 0) stage[s] = t1 < 0 ? make_int2(0, 0) : make_int2(t0, t1 + 1);
   }
+  const int2 r = warp_range(lo, hi);
+  if (lane == 0) p.stage_tiles[static_cast<size_t>(b) * p.n_stages + s] = r;
+}
+
+// A stage's range of ids, as the kernel before left it, to its range of tiles.
+__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_tiles_kernel(const DocParams p) {
+  const int b = static_cast<int>(blockIdx.y), lane = threadIdx.x & 31;
+  const int s = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (s >= p.n_stages) return;
+  int2* stage = p.stage_tiles + static_cast<size_t>(b) * p.n_stages + s;
+  const int2* range = p.tile_range + static_cast<size_t>(b) * p.n_key_tiles;
+  const int2 mine = *stage;
+  int t0 = INT_MAX, t1 = -1;
+#pragma unroll 4
+  for (int t = lane; t < p.n_key_tiles; t += 32) {
+    const int2 r = range[t];
+    if (r.x <= mine.y && r.y >= mine.x && r.x <= r.y && mine.x <= mine.y) {
+      t0 = min(t0, t);
+      t1 = max(t1, t);
+    }
+  }
+  const int2 r = warp_range(t0, t1);
+  if (lane == 0) *stage = r.y < 0 ? make_int2(0, 0) : make_int2(r.x, r.y + 1);
+}
+
+cudaError_t launch(void (*kernel)(DocParams), int tasks, const DocParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((tasks + kDocWarps - 1) / kDocWarps),
+                     static_cast<unsigned>(p.B), 1);
+  cfg.blockDim = dim3(kDocWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
 
 cudaError_t launch_doc_tiles(const DocParams& p, cudaStream_t stream) {
-  fa_doc_tiles_kernel<<<p.B, kDocThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = launch(fa_doc_ranges_kernel, p.n_key_tiles + p.n_stages, p, stream);
+  return e != cudaSuccess ? e : launch(fa_doc_tiles_kernel, p.n_stages, p, stream);
 }
 
 }  // namespace fa

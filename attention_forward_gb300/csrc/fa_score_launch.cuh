@@ -27,8 +27,19 @@ cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
       done[dev] = true;
     }
   }
-  fa_score_kernel<D, BF16, kCap, kBias, kDocs><<<grid, kThreads, ScoreLayout<D>::kSmemBytes, stream>>>(q, k, v, o, p);
-  return cudaGetLastError();
+  // its setup overlaps the end of the kernel before, which it waits for
+  // (programmatic dependent launch)
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = ScoreLayout<D>::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fa_score_kernel<D, BF16, kCap, kBias, kDocs>, q, k, v, o, p);
 }
 
 template <int D, bool BF16, int kCap, bool kBias>
