@@ -45,6 +45,7 @@ struct CacheAttnParams {
   int B, H, Hkv, Sq;
   int rows;               // (H / Hkv) * Sq query rows per kv head
   int n_row_blocks;
+  int sms;                // multiprocessors
   int whole;              // CTAs take whole units: no parts, no merge
   int num_pages, page_shift, max_pages;
   float scale;
@@ -60,21 +61,18 @@ cudaError_t launch_cache_read(int D, bool bf16, const CacheCopyParams& p, cudaSt
 int cache_attn_row_block(int rows);
 constexpr int kCacheAttnWarps = 4;
 constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;  // a chunk of the work: a tile for each warp
-#ifndef FA_ST
-#define FA_ST 4
-#define FA_OCC1 4
-#define FA_OCC2 3
-#define FA_MIN 4
-#endif
-#ifndef FA_WHOLE
-#define FA_WHOLE 1024
-#endif
-constexpr int kCacheMinChunks = FA_MIN;    // a CTA's least share
-constexpr int kCacheAttnStages = FA_ST;  // tiles of a warp's ring
-constexpr int kCachePiece = 4096;        // keys whose tiles' places are in shared memory at once
-// Page tables of at most this many keys are not split: 64 kv heads of 701 keys
-// took 10.3 us split and merged, WHOLEUS whole.
-constexpr int kCacheWholeKeys = FA_WHOLE;
+constexpr int kCacheAttnStages = 3;                   // tiles of a warp's ring
+constexpr int kCachePiece = 4096;  // keys whose tiles' places are in shared memory at once
+// CTAs an SM holds: the registers of 16 accumulated rows are more.
+constexpr int cache_attn_occupancy(int row_block) { return row_block == 8 ? 4 : 3; }
+// A CTA's least share: more parts take longer to merge than they save (one
+// sequence of 2048 keys, 8 kv heads: 7.4 us by 4 chunks, 9.0 by 8, 12.8 by 12; of
+// 32768: 18.6, 17.3, 18.7).
+constexpr int kCacheMinChunks = 4;
+// Page tables of at most this many keys are not split: 4 x 16 heads of 701 keys
+// took 10.3 us split and merged, 10.0 whole, and one launch less; 8 heads of 2048
+// keys 7.4 us split, 17.2 whole.
+constexpr int kCacheWholeKeys = 1024;
 // CTAs for `units` row blocks of up to `room` keys.
 int cache_attn_grid(int rows, long long units, int room, int sm_count);
 cudaError_t launch_cache_attn(int D, bool bf16, const CacheAttnParams& p, int grid,

@@ -181,6 +181,7 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   p.rows = (H / Hkv) * Sq;
   p.n_row_blocks = plan.row_blocks;
   p.whole = plan.whole;
+  p.sms = env.sm_count;
   p.num_pages = num_pages;
   p.page_shift = shift_of(page_size);
   p.max_pages = max_pages;

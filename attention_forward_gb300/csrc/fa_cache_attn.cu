@@ -21,10 +21,13 @@ cudaError_t launch(const CacheAttnParams& p, int grid, cudaStream_t stream) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_cache_attn_kernel<D, BF16, NT, kMod>, p);
   if (e != cudaSuccess || p.whole) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hkv) *
-                         static_cast<unsigned>(p.rows), 1, 1);
+  const long long units = static_cast<long long>(p.B) * p.Hkv * p.n_row_blocks;
+  const bool by_unit = units >= p.sms;
+  cfg.gridDim = dim3(static_cast<unsigned>(by_unit ? units : static_cast<long long>(p.B) * p.Hkv * p.rows),
+                     1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, BF16, NT>, p, grid);
+  return by_unit ? cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, BF16, NT, true>, p, grid)
+                 : cudaLaunchKernelEx(&cfg, fa_cache_merge_kernel<D, BF16, NT, false>, p, grid);
 }
 
 template <int D, bool BF16>
@@ -44,7 +47,7 @@ int cache_attn_grid(int rows, long long units, int room, int sm_count) {
   const long long most = room <= kCacheWholeKeys ? units
                                                  : (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
-                          (cache_attn_row_block(rows) == 8 ? FA_OCC1 : FA_OCC2);
+                          cache_attn_occupancy(cache_attn_row_block(rows));
   return static_cast<int>(most < slots ? most : slots);
 }
 

@@ -285,16 +285,26 @@ struct CacheAttnSmem {
 };
 
 // Persistent CTAs.  Short caches (p.whole) are dealt in whole units, a row block
-// of a kv head of a sequence each.  Otherwise the work is counted in chunks of kCacheAttnKeys keys of a
-// unit, units in the order (sequence,
-// kv head, row block); the CTAs have equal shares of them
-// (CacheDeal), whatever the lengths, which are read here.  A unit that lies within one CTA is written
+// of a kv head of a sequence each.  Otherwise the work is counted in chunks of
+// kCacheAttnKeys keys of a unit, units in the order (sequence, kv head, row
+// block), and the CTAs have equal shares of them (CacheDeal), whatever the
+// lengths, which are read here.  A unit that lies within one CTA is written
 // out; the parts of the others go to the workspace, the CTA's first segment to
 // part 2 x, its last to 2 x + 1, where the merge kernel finds them by the same
 // arithmetic.  kMod: the scores are capped or biased (without it those
 // instructions, issued and predicated off, were a quarter of the loop).
+//
+// Bound: HBM by its bytes, but the instructions that cut the codes out come
+// close: 320 a tile and warp, 504 of an SM sub-partition's cycles a tile against
+// 441 of HBM time.  Measured at 32 sequences x 8 kv heads, 4 rows, D = 128: each
+// further 8192 keys at 6.0 TB/s of 6.8 (88 %), behind 10 us to start, look the
+// lengths and pages up and merge, and 3.4 us where a CTA has two segments; 59.6
+// us for the ragged 280 MB of 8192 (4.7 TB/s).  What did not pay: tiles in
+// registers two ahead (89 us: too few bytes in flight), 3 or 5 CTAs an SM
+// instead of 4 (even, 6 % slower), 4 tiles ahead (even), the next segment's first
+// tiles fetched while this one's warps meet (62.7 us).
 template <int D, bool BF16, int NT, bool kMod>
-__global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2)
+__global__ void __launch_bounds__(kCacheAttnThreads, cache_attn_occupancy(8 * NT))
     fa_cache_attn_kernel(const CacheAttnParams p) {
   constexpr int G = D / kCacheGroup;
   constexpr int kWords = D / 64;   // value words per lane and token
@@ -730,17 +740,28 @@ __global__ void __launch_bounds__(kCacheAttnThreads, NT == 1 ? FA_OCC1 : FA_OCC2
 }
 
 // The units that several CTAs shared: O = sum_s w_s O_s / sum_s w_s over their
-// parts, w_s = exp(LSE_s - max LSE).  A block per query row; four warps deal the
-// parts between them.
-template <int D, bool BF16, int NT>
+// parts, w_s = exp(LSE_s - max LSE).  kByUnit: a block per unit, its warps taking
+// rows in turn (many units of few parts each); else a block per row, its warps
+// sharing the parts (few units of many).  A block per row of 128 x 8 x 4 rows
+// cost 6 us, mostly of finding the parts.
+template <int D, bool BF16, int NT, bool kByUnit>
 __global__ void __launch_bounds__(kCacheAttnThreads)
     fa_cache_merge_kernel(const CacheAttnParams p, int attn_grid) {
   __shared__ CacheScan scan;
-  __shared__ MergeSmem<D> sm;
-  const long long row = blockIdx.x;
-  const int bh = static_cast<int>(row / p.rows);
-  const int r = static_cast<int>(row - static_cast<long long>(bh) * p.rows);
-  const int b = bh / p.Hkv, hk = bh - b * p.Hkv, rb = r / (8 * NT);
+  int b, hk, rb, r = 0;  // r: the row within the kv head's
+  if constexpr (kByUnit) {
+    const int units = p.Hkv * p.n_row_blocks;
+    b = static_cast<int>(blockIdx.x) / units;
+    const int unit = static_cast<int>(blockIdx.x) - b * units;
+    hk = unit / p.n_row_blocks;
+    rb = unit - hk * p.n_row_blocks;
+  } else {
+    const int bh = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.rows));
+    r = static_cast<int>(blockIdx.x) - bh * p.rows;
+    b = bh / p.Hkv;
+    hk = bh - b * p.Hkv;
+    rb = r / (8 * NT);
+  }
   int upto;
   const int all = cache_scan(p, scan, false, upto);
   const CacheDeal deal = cache_deal(all, attn_grid);
@@ -759,10 +780,25 @@ __global__ void __launch_bounds__(kCacheAttnThreads)
   if (x0 == x1) return;
   // a CTA's first segment, except where the unit begins inside x0
   const int inside = deal.begin(x0) < start ? 1 : 0;
-  auto part_row = [&](int s) -> long long {
-    return (2ll * (x0 + s) + (s == 0 ? inside : 0)) * (8 * NT) + r % (8 * NT);
+  const long long row0 = (static_cast<long long>(b) * p.Hkv + hk) * p.rows;
+  auto merge = [&](int row, auto&& with) {
+    with([&](int s) -> long long {
+      return (2ll * (x0 + s) + (s == 0 ? inside : 0)) * (8 * NT) + row % (8 * NT);
+    });
   };
-  merge_row<D, BF16>(p.part_o, p.part_lse, x1 - x0 + 1, part_row, p.o, p.lse, row, sm);
+  const int n_parts = x1 - x0 + 1;
+  if constexpr (kByUnit) {
+    const int end = min(p.rows, (rb + 1) * 8 * NT);
+    for (int row = rb * 8 * NT + (static_cast<int>(threadIdx.x) >> 5); row < end; row += kMergeWarps)
+      merge(row, [&](auto part_row) {
+        merge_row_warp<D, BF16>(p.part_o, p.part_lse, n_parts, part_row, p.o, p.lse, row0 + row);
+      });
+  } else {
+    __shared__ MergeSmem<D> sm;
+    merge(r, [&](auto part_row) {
+      merge_row<D, BF16>(p.part_o, p.part_lse, n_parts, part_row, p.o, p.lse, row0 + r, sm);
+    });
+  }
 }
 
 }  // namespace fa
