@@ -738,6 +738,12 @@ unsigned long long* take_sched_slot(const LaunchEnv& env) {
   return next_slot(env.sched, env.captured);
 }
 
+fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out) {
+  DeviceState* d = nullptr;
+  const fa_status_t st = current_device(&d, nullptr);
+  return st != FA_OK ? st : stream_workspace(*d, stream, need, out);
+}
+
 int device_sms() {
   DeviceState* d = nullptr;
   return current_device(&d, nullptr) == FA_OK ? d->sm_count : 0;

@@ -158,6 +158,10 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   if (static_cast<long long>(B) * Hkv * plan.row_blocks *
           ((max_pages * page_size + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys) > 0x7fffffffLL)
     return FA_ERR_INVALID_ARG;
+  if (plan.bytes > 0 && !workspace && !env.captured) {
+    if ((st = fa::library_workspace(strm, plan.bytes, &workspace)) != FA_OK) return st;
+    workspace_bytes = plan.bytes;
+  }
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)))
     return FA_ERR_WORKSPACE;
 

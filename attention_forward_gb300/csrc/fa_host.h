@@ -46,6 +46,11 @@ fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out);
 // A scheduler slot for one persistent launch (PrefillParams::sched).
 unsigned long long* take_sched_slot(const LaunchEnv& env);
 
+// The library's workspace for `stream` on the current device, the one that
+// fa_fwd keeps for its split partials, grown to `need` bytes.  Not for captured
+// calls.
+fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out);
+
 // The current device's multiprocessors; 0 without a supported device.
 int device_sms();
 

@@ -19,8 +19,8 @@
 //            are computed and masked (documents that do not lie together).
 //   scores   Tiles where every key is visible to every row of a warp are not
 //            masked.  tanh is an odd polynomial of four terms while every
-//            |x / cap| of the warp's tile is at most 0.5 (its error is 1.3e-7
-//            of the cap; 5 FMA-pipe operations a score), else 1 - 2 / (1 +
+//            |x / cap| of the warp's tile is at most 0.5 (off by 2e-7 of the
+//            cap at most; 5 FMA-pipe operations a score), else 1 - 2 / (1 +
 //            e^2x) (an exponential and a reciprocal on the XU: measured 1.4
 //            times the whole kernel's time).  The bias is linear in the column
 //            on either side of the diagonal; tiles across it take |p - j|.

@@ -127,12 +127,12 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 // cap tanh(s scale / cap) log2(e) = s (c0 + c1 s^2 + c2 s^4 + c3 s^6) while
 // |s scale / cap| <= y_max.  The terms are the minimax fit (exchange algorithm)
-// of an odd polynomial to tanh on [-0.5, 0.5], error 1.3e-7.
+// of y + a1 y^3 + a2 y^5 + a3 y^7 to tanh on [0, 0.5]: off by 2e-7 at most, by
+// less than 1e-8 up to 0.05, where most scores are.
 void plan_cap(fa::ScoreParams& p, double scale, double cap, bool bf16) {
-  static const double kTanh[fa::kCapTerms] = {0.999997676, -0.333206552, 0.131451457,
-                                              -0.043372484};
+  static const double kTanh[fa::kCapTerms] = {1.0, -0.33326461, 0.13185862, -0.0442293};
   // |y| up to which the terms before i alone are within 2e-7
-  static const double kWithout[fa::kCapTerms] = {0.0, 0.0087, 0.058, 0.172};
+  static const double kWithout[fa::kCapTerms] = {0.0, 0.0084, 0.058, 0.17};
   constexpr double kLog2e = 1.4426950408889634;
   const double k = scale / cap;
   double y_max = fa::kCapPolyMax;
@@ -205,7 +205,12 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
 
   Plan plan = make_plan(B, H, Hkv, Sq, Skv, D, doc_k != nullptr, env.sm_count);
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA_ERR_WORKSPACE;
-  const size_t have = workspace ? workspace_bytes : 0;
+  size_t have = workspace ? workspace_bytes : 0;
+  const size_t need = plan.doc_bytes + plan.split_bytes;
+  if (!workspace && need > 0 && !env.captured) {
+    if ((st = fa::library_workspace(s, need, &workspace)) != FA_OK) return st;
+    have = need;
+  }
   if (have < plan.doc_bytes) return FA_ERR_WORKSPACE;
   if (have < plan.doc_bytes + plan.split_bytes) {
     plan.n_splits = 1;

@@ -284,9 +284,8 @@ def _group_check(H: int, Hkv: int) -> None:
         raise ValueError("the kv heads must divide the query heads")
 
 
-def _call_memory(q, dev, out, lse, workspace, need: int, stream):
-    """The outputs and the workspace of a call on q's device, made where they
-    are not given: (out, lse, workspace, their pointers, its bytes)."""
+def _outputs_on(q, dev, out, lse, stream):
+    """The outputs of a call on q's device, made where they are not given."""
     B, H, Sq, D = q.shape
     made = []
     if out is None:
@@ -299,17 +298,27 @@ def _call_memory(q, dev, out, lse, workspace, need: int, stream):
         made.append(lse)
     else:
         _ptr(lse, "lse", dev, torch.float32, (B, H, Sq))
-    if workspace is None:
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            made.append(workspace)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the call's CUDA device")
     if stream is not None and made:
         _own_memory(made, stream)
+    return out, lse
+
+
+def _workspace_of(workspace, dev):
+    """(pointer, bytes) of a caller's workspace; (None, 0) for the library's."""
     if workspace is None:
-        return out, lse, None, 0
-    return out, lse, workspace, workspace.numel() * workspace.element_size()
+        return None, 0
+    if workspace.get_device() != dev or not workspace.is_contiguous() or not workspace.numel():
+        raise ValueError("workspace must be a contiguous tensor on the call's CUDA device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _graph_workspace(call, need: int, device, stream) -> int:
+    """Repeats a captured call, which may not use the library's workspace, with
+    one of the graph's own memory."""
+    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        _own_memory([workspace], stream)
+    return call(workspace.data_ptr(), need)
 
 
 def fa_score_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Skv: int, D: int,
@@ -325,7 +334,8 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
     (float32 [H]) takes slope * distance off them, ``doc_q`` / ``doc_k``
     (int32 [B, Sq], [B, Skv]) keep rows to keys of their document, ``prefix``
     (int32 [B], causal only) shows the first keys to every row.  Without
-    ``workspace`` the call makes its own.  Returns (o, lse)."""
+    ``workspace`` the library's own for the stream serves (a captured call gets
+    one of the graph's memory).  Returns (o, lse)."""
     dev, (B, H, Sq, D) = _rows16(q, "q")
     _, (_, Hkv, Skv, _) = _rows16(k, "k")
     _group_check(H, Hkv)
@@ -346,14 +356,17 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
                                 workspace, out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     L = load()
-    need = 0
-    if workspace is None:
+    out, lse = _outputs_on(q, dev, out, lse, stream)
+    ws, ws_bytes = _workspace_of(workspace, dev)
+    args = (q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv, D, sc,
+            bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    if ws is None and torch.cuda.is_current_stream_capturing():
         need = L.fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, doc_k is not None)
-    out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
-    st = L.fa_fwd_score(q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv,
-                        D, sc, bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp,
-                        None if ws is None else ws.data_ptr(), ws_bytes,
-                        _raw_stream(dev) if stream is None else _stream_handle(stream))
+        st = _graph_workspace(lambda p, n: L.fa_fwd_score(*args, p, n, handle), need, q.device,
+                              stream)
+    else:
+        st = L.fa_fwd_score(*args, ws, ws_bytes, handle)
     if st:
         _check(st, "fa_fwd_score")
     return out, lse
@@ -463,14 +476,16 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
                                 out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     L = load()
-    need = 0
-    if workspace is None:
+    out, lse = _outputs_on(q, dev, out, lse, stream)
+    ws, ws_bytes = _workspace_of(workspace, dev)
+    args = (q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Hkv,
+            Sq, D, pages, page, per, sc, _DTYPE[q.dtype], softcap, sp)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    st = L.fa_fwd_cache(*args, ws, ws_bytes, handle)
+    if st == FA_ERR_WORKSPACE and ws is None:
         need = L.fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page, per)
-    out, lse, ws, ws_bytes = _call_memory(q, dev, out, lse, workspace, need, stream)
-    st = L.fa_fwd_cache(q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(), lse.data_ptr(),
-                        B, H, Hkv, Sq, D, pages, page, per, sc, _DTYPE[q.dtype], softcap, sp,
-                        None if ws is None else ws.data_ptr(), ws_bytes,
-                        _raw_stream(dev) if stream is None else _stream_handle(stream))
+        st = _graph_workspace(lambda p, n: L.fa_fwd_cache(*args, p, n, handle), need, q.device,
+                              stream)
     if st:
         _check(st, "fa_fwd_cache")
     return out, lse

@@ -308,11 +308,13 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  *   workspace  caller-owned device memory, 256-byte aligned, of
  *              fa_score_workspace_bytes(...) bytes (`documents`: whether
  *              doc_q and doc_k are given); used until the work on `stream`
- *              has finished.  Smaller, or NULL: the keys are not split, and a
- *              call with documents, whose tile lists need their part of it,
- *              returns FA_ERR_WORKSPACE.
- * Allocates nothing; may be captured into a CUDA graph (fa_fwd's limits on
- * scheduler slots hold; the workspace is then the graph's to keep).
+ *              has finished.  Smaller: the keys are not split, and a call with
+ *              documents, whose tile lists need their part of it, returns
+ *              FA_ERR_WORKSPACE.  NULL: the library's own for the stream, as
+ *              fa_fwd keeps it; inside a capture none.
+ * With a workspace it allocates nothing.  May be captured into a CUDA graph
+ * (fa_fwd's limits on scheduler slots hold; the workspace is then the graph's to
+ * keep).
  */
 size_t fa_score_workspace_bytes(int B, int H, int Hkv, int Sq, int Skv, int D,
                                 int documents);
@@ -348,9 +350,8 @@ fa_status_t fa_fwd_score(const void *q, const void *k, const void *v, void *o,
  * seen by no query row; the call then records FA_ERR_INVALID_ARG in the
  * device status word (fa_get_device_status).  Page numbers of tokens that a
  * call does not reach are not looked at.
- * D, dtypes and B * Hkv < 65536 as for fa_fwd.  All three allocate nothing
- * and may be captured into CUDA graphs: lengths, starts, counts and page
- * tables are read when the work runs.
+ * D, dtypes and B * Hkv < 65536 as for fa_fwd.  All three may be captured into CUDA
+ * graphs: lengths, starts, counts and page tables are read when the work runs.
  *
  * fa_cache_write -- quantises new tokens into the cache.
  *   k, v   [B, Hkv, S, D] fp16 or bf16; token i of sequence b goes to
@@ -383,11 +384,15 @@ fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
  *   length  [B] int32: tokens of sequence b in the cache, these Sq included;
  *           query row i sees keys j <= length[b] - Sq + i.  A length of 0, or
  *           a row that comes before key 0, sees nothing (O = 0, LSE = -inf).
+ *           Slots past the length may hold anything; a NaN written within it
+ *           reaches every row of its kv head.
  *           Lengths outside 0 ... max_pages * page_size are limited to it,
  *           and FA_ERR_INVALID_ARG is recorded.
  *   scale, softcap, slopes  as for fa_fwd_score (p = length[b] - Sq + i)
- *   workspace  fa_cache_workspace_bytes(...) bytes (0: may be NULL),
- *           256-byte aligned, caller-owned; FA_ERR_WORKSPACE when missing
+ *   workspace  fa_cache_workspace_bytes(...) bytes, 256-byte aligned,
+ *           caller-owned.  NULL: none where that is 0, else the library's own
+ *           for the stream, as fa_fwd keeps it; a captured call that needs one
+ *           returns FA_ERR_WORKSPACE without.
  * The keys of all sequences are dealt evenly to the GPU's multiprocessors by
  * the lengths that the device finds, ragged batches and replays included.
  * Meant for single tokens and the few of a draft: every 8 or 16 query rows of

@@ -434,6 +434,28 @@ def test_prompt_decode_and_a_further_chunk(D, dt):
     ops_ref.check(o, lse, ops_ref.attention(qc, kf, vf, seen, D ** -0.5, cap, slopes, dist, p_step=u))
 
 
+def test_captured_attention_without_a_workspace():
+    """The graph's own memory holds its parts; the library's is for direct calls."""
+    cache, table, _, _ = cache_of(2, 3000, 2, 64, 128, "bf16", 28)
+    q = torch.randn((2, 8, 1, 128), generator=torch.Generator("cuda").manual_seed(29),
+                    device="cuda").bfloat16()
+    length = ints([3000, 1111])
+    ref = fa.fa_fwd_cache(q, cache, table, length)
+    ok()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.fa_fwd_cache(q, cache, table, length)
+    fa.fa_release_workspaces()
+    side = torch.cuda.Stream()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            graph.replay()
+        direct = fa.fa_fwd_cache(q, cache, table, length)
+    ok()
+    for o, lse in (got, direct):
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
 def test_captured_write_and_read_follow_their_arrays():
     cache, table, k, v = cache_of(2, 40, 2, 16, 64, "bf16", 26)
     start, count = ints([0, 0]), ints([4, 4])

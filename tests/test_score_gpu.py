@@ -179,7 +179,7 @@ def test_without_modifications_it_is_fa_fwd():
         o, lse = run(q, k, v, causal=causal)
         a, b = fa.fa_fwd_ex(q, k, v, causal=causal, flags=fa.FA_FLAG_SINGLE_CTA, num_splits=1)
         ws = torch.empty(256, dtype=torch.uint8, device="cuda")
-        o1, l1 = run(q, k, v, causal=causal, workspace=ws[:0])  # no room: unsplit
+        o1, l1 = run(q, k, v, causal=causal, workspace=ws)  # no room: unsplit
         assert torch.equal(o1, a) and torch.equal(l1, b)
         assert (o.float() - a.float()).abs().max() < 0.02
 
@@ -207,8 +207,8 @@ def test_split_and_unsplit_agree_and_fill_the_same_rows():
     need = fa.fa_score_workspace_bytes(1, 4, 1, 3, 5000, 128)
     assert need > 0
     ref = expect(q, k, v, True, softcap=30.0)
-    empty = torch.empty(256, dtype=torch.uint8, device="cuda")[:0]
-    for ws in (None, empty):
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for ws in (None, small):
         ops_ref.check(*run(q, k, v, causal=True, softcap=30.0, workspace=ws), ref)
 
 
@@ -259,6 +259,36 @@ def test_graph_reads_ids_prefixes_and_inputs_at_replay():
     ref = expect(q, k, v, **kw)
     for o, lse in outs:
         ops_ref.check(o, lse, ref)
+
+
+def test_captured_calls_have_workspaces_of_their_own():
+    """Two graphs captured without a workspace, replayed at once on two streams
+    beside direct calls; one of a larger need frees and regrows the library's."""
+    q, k, v = make(1, 8, 1, 2, 6000, 128, "bf16", 20)
+    q2, k2, v2 = make(2, 4, 2, 300, 500, 128, "bf16", 21)
+    dq, dk = documents(2, 300, 500, (200, 333))
+    ref = run(q, k, v, softcap=20.0)
+    ref2 = run(q2, k2, v2, causal=True, doc_q=dq, doc_k=dk)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            a = fa.fa_fwd_score(q, k, v, softcap=20.0)
+            b = fa.fa_fwd_score(q2, k2, v2, causal=True, doc_q=dq, doc_k=dk)
+        graphs.append(g)
+        outs.append((a, b))
+    fa.fa_release_workspaces()
+    s1 = torch.cuda.Stream()
+    big = make(1, 16, 1, 8, 9000, 128, "bf16", 22)
+    for _ in range(5):
+        graphs[0].replay()
+        with torch.cuda.stream(s1):
+            graphs[1].replay()
+        got = fa.fa_fwd_score(q, k, v, softcap=20.0)
+        fa.fa_fwd_score(*big)
+        torch.cuda.synchronize()
+        for x, y in ((got, ref),) + tuple(z for a, b in outs for z in ((a, ref), (b, ref2))):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
 
 
 def test_same_inputs_give_the_same_bits():
