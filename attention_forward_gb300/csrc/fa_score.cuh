@@ -61,8 +61,8 @@ static_assert(128 * (2 * kRegsScoreSoftmax<true> + kRegsScoreEpilogue<true> +
                   128 * (2 * kRegsScoreSoftmax<false> + kRegsScoreEpilogue<false> +
                          kRegsScoreControl<false>) == kRegsLaunch,
               "register split must equal the launch allocation");
-// How a call caps its scores: not; with the running reference maximum; with a
-// fixed reference, which the cap allows where it bounds every score enough.
+// How a call caps its scores: not; with the running reference maximum; without
+// a reference, where the cap bounds every score enough.
 enum CapForm { kCapNone = 0, kCapRunning = 1, kCapFixed = 2 };
 
 // One work item, worked out by the producer and handed to the other roles
@@ -376,13 +376,12 @@ __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, i
   tmem_wait_st();
 }
 
-// The exponentials of 32 columns under a fixed reference: p = 2^(x - ref) of the
-// capped scores x, to their 16 columns of P.
+// The exponentials of 32 columns without a reference: p = 2^x of the capped
+// scores x, to their 16 columns of P.
 template <bool BF16, bool kMasked>
 __device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32_t tP,
                                               uint32_t visible, const ScoreParams& p, float& l0,
                                               float& l1) {
-  const float neg = -p.cap_ref;
   const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3];
   float x[32], top = 0.f;
 #pragma unroll
@@ -394,14 +393,13 @@ __device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32
     ffma2(y0, y1, u0, u1, c3, c3, c2, c2);
     ffma2(y0, y1, y0, y1, u0, u1, c1, c1);
     ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
-    ffma2(x[e], x[e + 1], y0, y1, a, b, neg, neg);
+    fmul2(x[e], x[e + 1], y0, y1, a, b);
   }
   if (__any_sync(0xffffffffu, !(top <= p.cap_u_max))) {
-    const float end = p.cap_log2 + neg;
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
       const float ex = ex2_approx(__uint_as_float(v[e >> 4][e & 15]) * p.cap_arg);
-      x[e] = fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), end);
+      x[e] = fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), p.cap_log2);
     }
   }
   if constexpr (kMasked) {
@@ -420,11 +418,12 @@ __device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32
 }
 
 // One key tile of one stage's softmax under a cap that bounds every score:
-// p = 2^(x - ref) with one ref for all rows and tiles, so there is no maximum
-// to find, nothing to rescale, and 32 columns at a time go from S to P, the
-// next 32 loading meanwhile (P's columns 16 h ... lie below those still to be
-// read).  bf16 holds p in 2^-120 ... 2^24 as exactly as around 1, l in fp32 too;
-// fp16 does not, and takes the running maximum.
+// p = 2^x, so there is no maximum to find, nothing to rescale, and 32 columns at
+// a time go from S to P, the next 32 loading meanwhile (P's columns 16 h ... lie
+// below those still to be read).  At |x| <= 72.5 bf16 holds p as exactly as
+// around 1, and the fp32 sums l (2^96 with 2^24 keys) and p v (values of 2^-50
+// ... 2^30) stay normal numbers; fp16 does not hold p, and takes the running
+// maximum.
 template <bool BF16, bool kDocs>
 __device__ __forceinline__ void score_tile_fixed(uint32_t tS, int key0, int b, const ScoreRow& row,
                                                  const ScoreParams& p, int tile_doc, float& l) {
@@ -590,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // reference of the scores (log2 units)
-      float m = kCap == kCapFixed ? p.cap_ref : -INFINITY;
+      float m = kCap == kCapFixed ? 0.f : -INFINITY;
       float l = 0.f;        // running sum of 2^(c*s - m)
 
 #pragma unroll 1

@@ -30,12 +30,11 @@ struct ScoreParams {
   int causal;
   float scale_log2;           // scale * log2(e)
   int capped;                 // scores have a tanh cap
-  int cap_fixed;              // with the fixed reference cap_ref
+  int cap_fixed;              // and the cap bounds them: no reference maximum
   float cap_u_max;            // score^2 up to which the polynomial holds (< 0: none)
   float cap_poly[kCapTerms];  // log2-scaled score = s * (c0 + c1 s^2 + ...)
   float cap_arg;              // 2 log2(e) scale / cap
   float cap_log2;             // cap * log2(e)
-  float cap_ref;              // cap_log2 - 24
   const float* slopes;        // [H] or null
   const int* prefix;          // [B] or null
   const int* doc_q;           // [B, Sq] or null

@@ -156,9 +156,7 @@ void plan_cap(fa::ScoreParams& p, double scale, double cap, bool bf16) {
     p.cap_u_max = -1.f;
   }
   p.capped = 1;
-  // p = 2^(x - ref) for |x| <= cap_log2 within bf16's normal numbers with room
-  // for sums: at most 2^24, at least 2^-120 while cap_log2 <= 72.5 (a cap of 50)
-  p.cap_ref = p.cap_log2 - 24.f;
+  // |x| <= 72.5 (a cap of 50) leaves 2^x, its sums and products normal
   p.cap_fixed = bf16 && !p.slopes && p.cap_log2 <= 72.5f ? 1 : 0;
 }
 

@@ -289,7 +289,9 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  * and key j is visible when
  *   (not causal, or j <= p, or prefix is given and j < prefix[b])  and
  *   (no documents, or doc_q[b,i] == doc_k[b,j] >= 0).
- *   softcap  0: no cap; else 1e-6 ... 1e6
+ *   softcap  0: no cap; else 1e-6 ... 1e6.  With bf16, no slopes and a cap up
+ *            to 50 (its probabilities are summed unshifted) values of V are
+ *            taken up to 2^30 in magnitude, and below 2^-50 may count as 0.
  *   slopes   [H] fp32 (finite), or NULL
  *   doc_q    [B, Sq] int32, doc_k [B, Skv] int32: the document of every query
  *            and key, both given or both NULL.  A negative id belongs to no

@@ -73,6 +73,22 @@ def test_cap(shape, cap, mult, D):
     ops_ref.check(*run(q, k, v, causal=True, softcap=cap), expect(q, k, v, True, softcap=cap))
 
 
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("v_scale", [1e-6, 1.0, 1e6])
+@pytest.mark.parametrize("dt,cap", [("bf16", 50.0), ("bf16", 60.0), ("fp16", 50.0)])
+def test_rows_whose_scores_all_lie_at_the_cap(dt, cap, sign, v_scale):
+    """Every score near +cap or -cap, with values far from 1: the probabilities'
+    common factor cancels whatever it is."""
+    if dt == "fp16" and v_scale != 1.0:
+        v_scale = 1e-3 if v_scale < 1 else 1e3
+    q, k, v = make(1, 2, 1, 200, 300, 64, dt, 30)
+    q = (q.abs() + 1) * 3
+    k = (k.abs() + 1) * sign
+    v = (v.float() * v_scale).to(DT[dt])
+    q, k = q.to(DT[dt]), k.to(DT[dt])
+    ops_ref.check(*run(q, k, v, causal=True, softcap=cap), expect(q, k, v, True, softcap=cap))
+
+
 def test_cap_with_one_large_score_among_small_ones():
     """A warp leaves the polynomial's range in one tile only."""
     q, k, v = make(1, 2, 2, 300, 520, 128, "fp16", 3)
