@@ -98,9 +98,11 @@ struct DeviceState {
     unsigned tail_epoch = 0;
   };
   std::vector<StreamWorkspace> workspaces;
+  std::vector<StreamWorkspace> call_workspaces;  // library_workspace's
 };
 
 std::mutex g_mu;
+std::mutex g_call_mu;  // taken before g_mu: see library_workspace
 DeviceState g_dev[kMaxDevices];
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
@@ -214,10 +216,11 @@ unsigned long long* sched_slot(const DeviceState& d, bool captured) {
   return next_slot(d.sched, captured);
 }
 
-// fa_fwd's workspace for `stream` on this device, grown to `need` bytes.
-fa_status_t stream_workspace(DeviceState& d, cudaStream_t stream, size_t need, void** out) {
+// The workspace for `stream` among `all` (a device's), grown to `need` bytes.
+fa_status_t stream_workspace(std::vector<DeviceState::StreamWorkspace>& all, cudaStream_t stream,
+                             size_t need, void** out) {
   std::lock_guard<std::mutex> lock(g_mu);
-  for (auto& w : d.workspaces) {
+  for (auto& w : all) {
     if (w.stream != stream) continue;
     if (w.bytes < need) {
       cudaFree(w.ptr);  // waits for the work that used it
@@ -231,7 +234,7 @@ fa_status_t stream_workspace(DeviceState& d, cudaStream_t stream, size_t need, v
   }
   void* ptr = nullptr;
   if (cudaMalloc(&ptr, need) != cudaSuccess) return FA_ERR_CUDA;
-  d.workspaces.push_back({stream, ptr, need});
+  all.push_back({stream, ptr, need});
   *out = ptr;
   return FA_OK;
 }
@@ -243,7 +246,7 @@ fa_status_t stream_workspace(DeviceState& d, cudaStream_t stream, size_t need, v
 fa_status_t stream_tail_state(DeviceState& d, cudaStream_t stream, size_t part_bytes,
                               size_t n_ctr, void** part, unsigned long long** ctr,
                               unsigned* epoch) {
-  fa_status_t st = stream_workspace(d, stream, part_bytes, part);
+  fa_status_t st = stream_workspace(d.workspaces, stream, part_bytes, part);
   if (st != FA_OK) return st;
   std::lock_guard<std::mutex> lock(g_mu);
   for (auto& w : d.workspaces) {
@@ -543,7 +546,7 @@ fa_status_t run_prefill(DeviceState& d, const void* q, const void* k, const void
   p.n_splits = n_splits;
   if (need > 0) {
     if (own_ws) {
-      if ((st = stream_workspace(d, stream, need, &ws)) != FA_OK) return st;
+      if ((st = stream_workspace(d.workspaces, stream, need, &ws)) != FA_OK) return st;
     } else if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) {
       return FA_ERR_WORKSPACE;
     }
@@ -610,7 +613,7 @@ fa_status_t run_decode(DeviceState& d, const void* q, const void* k, const void*
   const size_t need = decode_ws_bytes(BH, n_splits, D);
   if (need > 0) {
     if (own_ws) {
-      const fa_status_t wst = stream_workspace(d, stream, need, &ws);
+      const fa_status_t wst = stream_workspace(d.workspaces, stream, need, &ws);
       if (wst != FA_OK) return wst;
     } else {
       if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
@@ -738,10 +741,13 @@ unsigned long long* take_sched_slot(const LaunchEnv& env) {
   return next_slot(env.sched, env.captured);
 }
 
-fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out) {
+fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out,
+                              std::unique_lock<std::mutex>* hold) {
   DeviceState* d = nullptr;
   const fa_status_t st = current_device(&d, nullptr);
-  return st != FA_OK ? st : stream_workspace(*d, stream, need, out);
+  if (st != FA_OK) return st;
+  *hold = std::unique_lock<std::mutex>(g_call_mu);
+  return stream_workspace(d->call_workspaces, stream, need, out);
 }
 
 int device_sms() {
@@ -855,14 +861,17 @@ fa_status_t fa_release_workspaces(void) {
   DeviceState* d = nullptr;
   const fa_status_t st = current_device(&d, nullptr);
   if (st != FA_OK) return st;
+  std::lock_guard<std::mutex> calls(g_call_mu);
   if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_mu);
   fa_status_t out = FA_OK;
-  for (auto& w : d->workspaces) {
-    if (cudaFree(w.ptr) != cudaSuccess) out = FA_ERR_CUDA;
-    if (w.tail_ctr && cudaFree(w.tail_ctr) != cudaSuccess) out = FA_ERR_CUDA;
+  for (auto* all : {&d->workspaces, &d->call_workspaces}) {
+    for (auto& w : *all) {
+      if (cudaFree(w.ptr) != cudaSuccess) out = FA_ERR_CUDA;
+      if (w.tail_ctr && cudaFree(w.tail_ctr) != cudaSuccess) out = FA_ERR_CUDA;
+    }
+    all->clear();
   }
-  d->workspaces.clear();
   return out;
 }
 

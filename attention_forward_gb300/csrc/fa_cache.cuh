@@ -267,9 +267,10 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const 
     for (int n = 0; n < 2; ++n) {
       word[k][n] = param[k][n] = 0u;  // a place that does not exist reads as zeros
       if (row >= 0) {
-        word[k][n] = __ldg(reinterpret_cast<const uint32_t*>(p.pool.codes[n]) + row * kLanes +
-                           kGroups * t + g);
-        param[k][n] = __ldg(p.pool.params[n] + row * kGroups + g);
+        // from L2: the kernel may have started while the write before it ran
+        word[k][n] = __ldcg(reinterpret_cast<const uint32_t*>(p.pool.codes[n]) + row * kLanes +
+                            kGroups * t + g);
+        param[k][n] = __ldcg(p.pool.params[n] + row * kGroups + g);
       }
     }
   }

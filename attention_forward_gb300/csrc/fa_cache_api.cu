@@ -156,10 +156,11 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   const AttnPlan plan = plan_attn(B, H, Hkv, Sq, D, s, env.sm_count);
   // the kernel counts chunks of keys in an int
   if (static_cast<long long>(B) * Hkv * plan.row_blocks *
-          ((max_pages * page_size + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys) > 0x7fffffffLL)
+          ((max_pages * page_size + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys) > 0x7fffff00LL)
     return FA_ERR_INVALID_ARG;
+  std::unique_lock<std::mutex> hold;
   if (plan.bytes > 0 && !workspace && !env.captured) {
-    if ((st = fa::library_workspace(strm, plan.bytes, &workspace)) != FA_OK) return st;
+    if ((st = fa::library_workspace(strm, plan.bytes, &workspace, &hold)) != FA_OK) return st;
     workspace_bytes = plan.bytes;
   }
   if (plan.bytes > 0 && (!workspace || workspace_bytes < plan.bytes || !aligned(workspace, 256)))

@@ -4,6 +4,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <mutex>
+
 #include "../../include/fa.h"
 
 namespace fa {
@@ -46,10 +48,12 @@ fa_status_t launch_env(cudaStream_t stream, LaunchEnv* out);
 // A scheduler slot for one persistent launch (PrefillParams::sched).
 unsigned long long* take_sched_slot(const LaunchEnv& env);
 
-// The library's workspace for `stream` on the current device, the one that
-// fa_fwd keeps for its split partials, grown to `need` bytes.  Not for captured
-// calls.
-fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out);
+// The library's workspace for the score and cache calls on `stream` of the
+// current device, grown to `need` bytes.  Not for captured calls.  `hold` is
+// locked: keep it until the call's launches are all in the stream, so that no
+// other thread's call comes between them or grows the workspace under them.
+fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out,
+                              std::unique_lock<std::mutex>* hold);
 
 // The current device's multiprocessors; 0 without a supported device.
 int device_sms();

@@ -205,8 +205,9 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA_ERR_WORKSPACE;
   size_t have = workspace ? workspace_bytes : 0;
   const size_t need = plan.doc_bytes + plan.split_bytes;
+  std::unique_lock<std::mutex> hold;
   if (!workspace && need > 0 && !env.captured) {
-    if ((st = fa::library_workspace(s, need, &workspace)) != FA_OK) return st;
+    if ((st = fa::library_workspace(s, need, &workspace, &hold)) != FA_OK) return st;
     have = need;
   }
   if (have < plan.doc_bytes) return FA_ERR_WORKSPACE;

@@ -312,8 +312,9 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  *              doc_q and doc_k are given); used until the work on `stream`
  *              has finished.  Smaller: the keys are not split, and a call with
  *              documents, whose tile lists need their part of it, returns
- *              FA_ERR_WORKSPACE.  NULL: the library's own for the stream, as
- *              fa_fwd keeps it; inside a capture none.
+ *              FA_ERR_WORKSPACE.  NULL: the library's own for the stream,
+ *              also with calls of several host threads; inside a capture
+ *              none.
  * With a workspace it allocates nothing.  May be captured into a CUDA graph
  * (fa_fwd's limits on scheduler slots hold; the workspace is then the graph's to
  * keep).
@@ -393,7 +394,7 @@ fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
  *   scale, softcap, slopes  as for fa_fwd_score (p = length[b] - Sq + i)
  *   workspace  fa_cache_workspace_bytes(...) bytes, 256-byte aligned,
  *           caller-owned.  NULL: none where that is 0, else the library's own
- *           for the stream, as fa_fwd keeps it; a captured call that needs one
+ *           for the stream, as for fa_fwd_score; a captured call that needs one
  *           returns FA_ERR_WORKSPACE without.
  * The keys of all sequences are dealt evenly to the GPU's multiprocessors by
  * the lengths that the device finds, ragged batches and replays included.
@@ -413,8 +414,8 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*
- * fa_release_workspaces -- frees the workspaces that fa_fwd keeps for split
- * partials on the current device (one per stream handle it was called
+ * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score and
+ * fa_fwd_cache keep for split partials on the current device (one per stream handle it was called
  * with), after synchronising the device.  The next fa_fwd that needs one
  * allocates it again.  Returns FA_ERR_CUDA if the synchronisation or a free
  * failed (the cache is emptied either way).
