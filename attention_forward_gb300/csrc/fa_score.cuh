@@ -218,11 +218,22 @@ __device__ __forceinline__ void cap_tile(uint32_t (&sr)[8][16], uint32_t tS, con
     }
 }
 
-// The bit mask of the tile's columns whose key belongs to the row's document.
-// Lane l holds the ids of columns l, l + 32, l + 64, l + 96; each distinct
-// document of the warp's rows is one round of ballots.
-__device__ __forceinline__ void doc_columns(const ScoreParams& p, int b, int key0, int my_doc,
-                                            uint32_t (&bits)[4]) {
+// The bits of the columns below the row's limit.
+__device__ __forceinline__ void limit_columns(int lim, int key0, uint32_t (&bits)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int n = lim - key0 - 32 * k;
+    bits[k] &= n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+  }
+}
+
+// The bit mask of the tile's columns that the row sees, its document's below its
+// limit.  Lane l holds the ids of columns l, l + 32, l + 64, l + 96; each distinct
+// document of the warp's rows is one round of ballots.  Made while the warp would
+// wait for the scores.
+__device__ __forceinline__ void doc_columns(const ScoreParams& p, int b, int key0,
+                                            const ScoreRow& row, uint32_t (&bits)[4]) {
+  const int my_doc = row.doc;
   const int lane = static_cast<int>(lane_id());
   int id[4];
 #pragma unroll
@@ -242,15 +253,17 @@ __device__ __forceinline__ void doc_columns(const ScoreParams& p, int b, int key
     }
     todo &= ~__ballot_sync(0xffffffffu, mine);
   }
+  limit_columns(row.lim, key0, bits);
 }
 
 // One key tile of one stage's softmax for this thread's row: softmax_tile of
-// fa_prefill.cuh with the scores modified first.  tile_doc: the id that all of
-// the tile's keys have (documents only).
-template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
-__device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, int b,
-                                           const ScoreRow& row, const ScoreParams& p,
-                                           int tile_doc, bool may_rescale, float& m, float& l) {
+// fa_prefill.cuh with the scores modified first.  docs: only the columns in `seen`
+// are visible (made by doc_columns).
+template <int D, bool BF16, int kCap, bool kBias>
+__device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0,
+                                           const ScoreRow& row, const ScoreParams& p, bool docs,
+                                           const uint32_t (&seen)[4], bool may_rescale, float& m,
+                                           float& l) {
   constexpr float kTau = 8.f;
   uint32_t sr[8][16];
 #pragma unroll
@@ -296,19 +309,12 @@ __device__ __forceinline__ void score_tile(uint32_t tS, uint32_t tO, int key0, i
     }
   }
 
-  if (kDocs && row.doc_warp != tile_doc) {
-    uint32_t bits[4];
-    doc_columns(p, b, key0, row.doc, bits);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = row.lim - key0 - 32 * k;
-      bits[k] &= n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
-    }
+  if (docs) {
 #pragma unroll
     for (int cc = 0; cc < 8; ++cc)
 #pragma unroll
       for (int e = 0; e < 16; ++e)
-        if (!((bits[cc >> 1] >> ((cc & 1) * 16 + e)) & 1u)) sr[cc][e] = __float_as_uint(-INFINITY);
+        if (!((seen[cc >> 1] >> ((cc & 1) * 16 + e)) & 1u)) sr[cc][e] = __float_as_uint(-INFINITY);
   } else if (key0 + kBN > row.lim_warp) {
     const int lim = row.lim - 1 - key0;
 #pragma unroll
@@ -424,20 +430,20 @@ __device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32
 // around 1, and the fp32 sums l (2^96 with 2^24 keys) and p v (values of 2^-50
 // ... 2^30) stay normal numbers; fp16 does not hold p, and takes the running
 // maximum.
-template <bool BF16, bool kDocs>
-__device__ __forceinline__ void score_tile_fixed(uint32_t tS, int key0, int b, const ScoreRow& row,
-                                                 const ScoreParams& p, int tile_doc, float& l) {
+template <bool BF16>
+__device__ __forceinline__ void score_tile_fixed(uint32_t tS, int key0, const ScoreRow& row,
+                                                 const ScoreParams& p, bool docs,
+                                                 const uint32_t (&seen)[4], float& l) {
   uint32_t va[2][16], vb[2][16];
   tmem_ld32(tS, va[0], va[1]);
-  const bool docs = kDocs && row.doc_warp != tile_doc;
   float l0 = 0.f, l1 = 0.f;
   if (docs || key0 + kBN > row.lim_warp) {
     uint32_t bits[4] = {~0u, ~0u, ~0u, ~0u};
-    if (kDocs && docs) doc_columns(p, b, key0, row.doc, bits);
+    if (docs) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int n = row.lim - key0 - 32 * k;
-      bits[k] &= n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+      for (int k = 0; k < 4; ++k) bits[k] = seen[k];
+    } else {
+      limit_columns(row.lim, key0, bits);
     }
 #pragma unroll 1
     for (int h = 0; h < 4; ++h) {
@@ -565,6 +571,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row_g = stage_row(p, it.row0, s) + r;  // row of the row head
       const bool stored = row_g < p.rows;
       ScoreRow row{};
+      // the id that all keys of a tile have, of the tile to come
+      const int* docs_of = nullptr;
+      int doc = 0;
+      if constexpr (kDocs) {
+        docs_of = p.tile_doc + it.b * p.n_key_tiles + it.t0;
+        if (nT > 0) doc = docs_of[0];
+      }
       {
         const int h_in = p.packed ? row_g / p.Sq : 0;  // the head within its group
         const int i = row_g - h_in * p.Sq;
@@ -594,15 +607,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
       for (int j = 0; j < nT; ++j, ++n_s) {
-        int doc = 0;  // in flight during the wait
-        if constexpr (kDocs) doc = p.tile_doc[it.b * p.n_key_tiles + it.t0 + j];
+        const int key0 = (it.t0 + j) * kBN;
+        bool docs = false;
+        uint32_t seen[4] = {};
+        if constexpr (kDocs) {
+          docs = row.doc_warp != doc;
+          if (docs) doc_columns(p, it.b, key0, row, seen);
+          if (j + 1 < nT) doc = docs_of[j + 1];  // in flight during the tile
+        }
         if (!wait_bar_warp(bar(L::S_FULL + s), n_s & 1, ctl)) { ok = false; break; }
         tc_fence_after();
         if constexpr (kCap == kCapFixed)
-          score_tile_fixed<BF16, kDocs>(tS, (it.t0 + j) * kBN, it.b, row, p, doc, l);
+          score_tile_fixed<BF16>(tS, key0, row, p, docs, seen, l);
         else
-          score_tile<D, BF16, kCap, kBias, kDocs>(tS, tO, (it.t0 + j) * kBN, it.b, row, p, doc,
-                                                  j > 0, m, l);
+          score_tile<D, BF16, kCap, kBias>(tS, tO, key0, row, p, docs, seen, j > 0, m, l);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::PV_READY + s));
