@@ -483,6 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmO,
                     const ScoreParams p) {
   using L = ScoreLayout<D>;
+  // An item's key tiles run from the last to the first with a bias: the keys
+  // next to the rows have the largest scores, and what comes after them raises
+  // no reference maximum.  Stage 0, which lacks the last ones, then joins late.
+  // B4 H16 S4096 D128 causal, slopes 2^-0.5 ... 2^-8: 238 us, 280 from the first on.
+  constexpr bool kBack = kBias;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -576,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int doc = 0;
       if constexpr (kDocs) {
         docs_of = p.tile_doc + it.b * p.n_key_tiles + it.t0;
-        if (nT > 0) doc = docs_of[0];
+        if (nT > 0) doc = docs_of[kBack ? nT - 1 : 0];
       }
       {
         const int h_in = p.packed ? row_g / p.Sq : 0;  // the head within its group
@@ -607,13 +612,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
       for (int j = 0; j < nT; ++j, ++n_s) {
-        const int key0 = (it.t0 + j) * kBN;
+        const int key0 = (it.t0 + (kBack ? nT - 1 - j : j)) * kBN;
         bool docs = false;
         uint32_t seen[4] = {};
         if constexpr (kDocs) {
           docs = row.doc_warp != doc;
           if (docs) doc_columns(p, it.b, key0, row, seen);
-          if (j + 1 < nT) doc = docs_of[j + 1];  // in flight during the tile
+          if (j + 1 < nT) doc = docs_of[kBack ? nT - 2 - j : j + 1];  // in flight during the tile
         }
         if (!wait_bar_warp(bar(L::S_FULL + s), n_s & 1, ctl)) { ok = false; break; }
         tc_fence_after();
@@ -770,6 +775,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                          kIdescPV, acc ? 1u : 0u);
         umma_commit(bar(L::O_READY + s));
       };
+      // Stage 0's tiles are an item's steps first0 ... end0 - 1
+      auto first0 = [](const ScoreItem& it) { return kBack ? it.nT1 - it.nT0 : 0; };
+      auto end0 = [](const ScoreItem& it) { return kBack ? it.nT1 : it.nT0; };
+      auto begin0 = [&](const ScoreItem& it, int f) {
+        if (it.nT0 == 0)
+          umma_commit(bar(L::Q_EMPTY + 0));
+        else if (first0(it) == 0)
+          qk(0, f, it.nT0 == 1);
+      };
       // First QKs of an item whose Q is in buffer phase kq and whose K_0 is
       // fill f (used for the CTA's first item and after an item without keys)
       auto begin = [&](const ScoreItem& it, int kq, int f) -> bool {
@@ -778,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return false;
         if (it.nT1 > 0 && !wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(f)), par_of(f), ctl)) return false;
         tc_fence_after();
-        if (it.nT0 > 0) qk(0, f, it.nT0 == 1); else umma_commit(bar(L::Q_EMPTY + 0));
+        begin0(it, f);
         if (it.nT1 > 0) {
           qk(1, f, it.nT1 == 1);
           umma_commit(bar(L::KV_EMPTY + slot_of(f)));
@@ -817,6 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           has_next = ok && nxt.valid;
         };
         const int fN = fK + 2 * cur.nT1;  // the next item's K_0
+        const int f0 = first0(cur), e0 = end0(cur);
 #pragma unroll 1
         for (int j = 0; j < cur.nT1; ++j) {
           const bool last = j + 1 == cur.nT1;
@@ -830,26 +845,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           // once PV_0(j) is issued, so that its wait is off the path from
           // the softmax's arrival to the next PV
           bool rdy = mbar_try_wait(bar(L::KV_FULL + slot_of(fv)), par_of(fv));
-          if (j < cur.nT0) rdy &= mbar_try_wait(bar(L::PV_READY + 0), n_pv0 & 1);
+          const bool on0 = j >= f0 && j < e0;
+          if (on0) rdy &= mbar_try_wait(bar(L::PV_READY + 0), n_pv0 & 1);
           if (!__all_sync(0xffffffffu, rdy)) {
             if (!wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fv)), par_of(fv), ctl)) { ok = false; break; }
-            if (j < cur.nT0 && !wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + 0), n_pv0 & 1, ctl)) { ok = false; break; }
+            if (on0 && !wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + 0), n_pv0 & 1, ctl)) { ok = false; break; }
           }
-          if (j < cur.nT0) {  // PV_0(j), then QK_0 over P_0(j)
-            if (j == 0 && n_o0 > 0 && !wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + 0), (n_o0 - 1) & 1, ctl)) {
+          if (on0) {  // PV_0(j), then QK_0 over P_0(j)
+            if (j == f0 && n_o0 > 0 && !wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + 0), (n_o0 - 1) & 1, ctl)) {
               ok = false;
               break;
             }
             ++n_pv0;
             tc_fence_after();
-            pv(0, fv, j > 0);
+            pv(0, fv, j > f0);
           }
           if (!last && !wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fk1)), par_of(fk1), ctl)) {
             ok = false;
             break;
           }
           if (!last) {
-            if (j + 1 < cur.nT0) qk(0, fk1, j + 2 == cur.nT0);
+            if (j + 1 >= f0 && j + 1 < e0) qk(0, fk1, j + 2 == e0);
           } else if (has_next) {
             if (!wait_bar_warp<kSleepMmaNs>(bar(L::Q_FULL + 0), (kq + 1) & 1, ctl)) { ok = false; break; }
             if (nxt.nT1 > 0 && !wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fN)), par_of(fN), ctl)) {
@@ -857,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            if (nxt.nT0 > 0) qk(0, fN, nxt.nT0 == 1); else umma_commit(bar(L::Q_EMPTY + 0));
+            begin0(nxt, fN);
           }
           // PV_1(j), then QK_1 over P_1(j)
           if (!wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + 1), n_pv1 & 1, ctl)) { ok = false; break; }
@@ -929,7 +945,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int box = 0; box < D / 64; ++box)
           tma_load_3d(sKV + static_cast<uint32_t>(slot * L::kKVBytes + box * L::kBox), tm,
-                      bar(L::KV_FULL + slot), box * 64, (it.t0 + j) * kBN, it.kvh);
+                      bar(L::KV_FULL + slot), box * 64,
+                      (it.t0 + (kBack ? it.nT1 - 1 - j : j)) * kBN, it.kvh);
         last_fill[slot] = fill;
         ++fill;
         return true;
