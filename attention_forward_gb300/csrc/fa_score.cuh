@@ -483,11 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmO,
                     const ScoreParams p) {
   using L = ScoreLayout<D>;
-  // An item's key tiles run from the last to the first with a bias: the keys
-  // next to the rows have the largest scores, and what comes after them raises
-  // no reference maximum.  Stage 0, which lacks the last ones, then joins late.
-  // B4 H16 S4096 D128 causal, slopes 2^-0.5 ... 2^-8: 238 us, 280 from the first on.
-  constexpr bool kBack = kBias;
+  // Modified scores: an item's key tiles run from the last to the first, and
+  // stage 0, which lacks the last ones of a causal item, joins late.  With a bias
+  // the keys next to the rows have the largest scores, and what comes after them
+  // raises no reference maximum; all gain from the stages' start one tile apart.
+  // B4 H16 S4096 D128 causal: bias 238 us, 280 from the first tile on; cap 50: 251
+  // and 257; documents of 1000: 99 and 103.  (Unmodified scores keep the order,
+  // and with it the bits, of the prefill kernel.)
+  constexpr bool kBack = kBias || kCap != kCapNone || kDocs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
