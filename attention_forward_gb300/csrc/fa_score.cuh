@@ -11,8 +11,12 @@
 //
 //   rows     Up to 128 query tokens: the group's heads of a kv head are
 //            consecutive rows in memory, so they are taken together and K and
-//            V are read once for the group.  Where those rows fit one stage,
-//            stage 1 has them and stage 0 has no tiles.
+//            V are read once for the group.
+//   halves   Where 256-row items would leave SMs idle, an item is 128 rows, both
+//            stages have them, and the key tiles go to the stages in turn; the
+//            epilogue joins the two states.  Every tile is then a K and a V
+//            tile of its own, but a stage's softmax still hides behind the other's
+//            products: 1.0 us a tile, 1.6 with the 128 rows in one stage alone.
 //   tiles    An item walks the key tiles [t0, t0 + nT1): up to the last key
 //            that a row sees, and with documents only those that hold ids of
 //            the item's rows.  Tiles inside that range without a visible key
@@ -72,20 +76,28 @@ struct ScoreItem {
   int valid;       // 0: no more items
   int rh, b, kvh;  // row head, its batch row, its kv head [B * Hkv]
   int h0;          // its query head (packed: the group's first)
-  int row0, nT0, nT1, t0, split;
+  int row0, nT0, nT1, t0, split;  // nT_s: stage s's tiles
 };
 
 template <int D>
 struct ScoreLayout : PrefillLayout<D> {
   static constexpr int kOffRing = PrefillLayout<D>::kOffMisc + PrefillLayout<D>::kMiscBytes;
   static constexpr int kSmemBytes = kOffRing + kItemRing * static_cast<int>(sizeof(ScoreItem)) + 1024;
+  // halves: [2][2][128] reference maxima and sums, where stage 1's Q would be
+  static constexpr int kOffStates = PrefillLayout<D>::kOffQ + PrefillLayout<D>::kQBytes;
   static_assert(kOffRing % 4 == 0 && kSmemBytes <= 232448, "shared memory budget");
 };
 
-// First row of stage s of an item; past the last row where the stage has none.
+// First row of stage s of an item; p.rows where the stage has none.
+template <bool kHalves>
 __device__ __forceinline__ int stage_row(const ScoreParams& p, int row0, int s) {
-  if (p.one_stage) return s == 1 ? row0 : p.rows;
-  return row0 + s * kBM;
+  return kHalves ? row0 : min(row0 + s * kBM, p.rows);
+}
+
+// Key tiles that an item loads.
+template <bool kHalves>
+__device__ __forceinline__ int item_tiles(const ScoreItem& it) {
+  return kHalves ? it.nT0 + it.nT1 : it.nT1;
 }
 
 // The key tiles [x, y) that the 128 rows from `row` of batch row b need.
@@ -111,6 +123,7 @@ __device__ __forceinline__ int2 stage_range(const ScoreParams& p, int b, int row
   return make_int2(lo, max(lo, hi));
 }
 
+template <bool kHalves>
 __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int idx) {
   ScoreItem it;
   it.valid = 1;
@@ -134,14 +147,21 @@ __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int id
     it.h0 = it.rh - it.b * p.H;
     it.kvh = it.b * p.Hkv + it.h0 / p.group;
   }
-  it.row0 = qtile * (p.one_stage ? kBM : kRowsPerCta);
-  int2 r0 = stage_range(p, it.b, stage_row(p, it.row0, 0));
-  int2 r1 = stage_range(p, it.b, stage_row(p, it.row0, 1));
+  it.row0 = qtile * (kHalves ? kBM : kRowsPerCta);
+  int2 r0 = stage_range(p, it.b, stage_row<kHalves>(p, it.row0, 0));
+  int2 r1 = stage_range(p, it.b, stage_row<kHalves>(p, it.row0, 1));
   const int s0 = it.split * p.tiles_per_split, s1 = s0 + p.tiles_per_split;
   r0.x = max(r0.x, s0);
   r1.x = max(r1.x, s0);
   r0.y = min(r0.y, s1);
   r1.y = min(r1.y, s1);
+  if constexpr (kHalves) {
+    const int n = max(r0.y - r0.x, 0);
+    it.t0 = r0.x;
+    it.nT0 = (n + 1) >> 1;
+    it.nT1 = n >> 1;
+    return it;
+  }
   const bool h0 = r0.x < r0.y, h1 = r1.x < r1.y;
   it.t0 = h0 ? (h1 ? min(r0.x, r1.x) : r0.x) : (h1 ? r1.x : 0);
   it.nT0 = h0 ? r0.y - it.t0 : 0;
@@ -475,7 +495,7 @@ __device__ __forceinline__ void score_tile_fixed(uint32_t tS, int key0, const Sc
   tmem_wait_st();
 }
 
-template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs, bool kHalves>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_score_kernel(const __grid_constant__ CUtensorMap tmQ,
                     const __grid_constant__ CUtensorMap tmK,
@@ -500,6 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sOut = sbase + L::kOffOut;
   const uint32_t bars = sbase + L::kOffBars;
   float* inv_l_smem = reinterpret_cast<float*>(smem + L::kOffInvL);
+  float* m_smem = reinterpret_cast<float*>(smem + L::kOffStates);  // halves only
+  float* l_smem = m_smem + 2 * kBM;
   ScoreItem* item_ring = reinterpret_cast<ScoreItem*>(smem + L::kOffRing);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffTmemSlot);
   volatile uint32_t* abort_flag =
@@ -576,15 +598,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           take_score_item<0>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
       if (!ok || !it.valid) break;
       const int nT = s == 0 ? it.nT0 : it.nT1;
-      const int row_g = stage_row(p, it.row0, s) + r;  // row of the row head
+      const int row_g = stage_row<kHalves>(p, it.row0, s) + r;  // row of the row head
       const bool stored = row_g < p.rows;
       ScoreRow row{};
+      // this stage's j-th tile
+      auto tile_of = [&](int j) {
+        if constexpr (kHalves)
+          return it.t0 + (kBack ? it.nT0 + it.nT1 - 1 - s - 2 * j : s + 2 * j);
+        else
+          return it.t0 + (kBack ? nT - 1 - j : j);
+      };
       // the id that all keys of a tile have, of the tile to come
       const int* docs_of = nullptr;
       int doc = 0;
       if constexpr (kDocs) {
-        docs_of = p.tile_doc + it.b * p.n_key_tiles + it.t0;
-        if (nT > 0) doc = docs_of[kBack ? nT - 1 : 0];
+        docs_of = p.tile_doc + it.b * p.n_key_tiles;
+        if (nT > 0) doc = docs_of[tile_of(0)];
       }
       {
         const int h_in = p.packed ? row_g / p.Sq : 0;  // the head within its group
@@ -615,13 +644,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 #pragma unroll 1
       for (int j = 0; j < nT; ++j, ++n_s) {
-        const int key0 = (it.t0 + (kBack ? nT - 1 - j : j)) * kBN;
+        const int key0 = tile_of(j) * kBN;
         bool docs = false;
         uint32_t seen[4] = {};
         if constexpr (kDocs) {
           docs = row.doc_warp != doc;
           if (docs) doc_columns(p, it.b, key0, row, seen);
-          if (j + 1 < nT) doc = docs_of[kBack ? nT - 2 - j : j + 1];  // in flight during the tile
+          if (j + 1 < nT) doc = docs_of[tile_of(j + 1)];  // in flight during the tile
         }
         if (!wait_bar_warp(bar(L::S_FULL + s), n_s & 1, ctl)) { ok = false; break; }
         tc_fence_after();
@@ -637,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // end of the item: LSE straight to global, 1/l to the epilogue warps
       // once the item's last PV_s has completed (then O_s is final)
-      if (stored) {
+      if (stored && !kHalves) {
         // l = 0: no visible key; a NaN stays one
         const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
         if (p.n_splits > 1)
@@ -647,7 +676,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (nT > 0) {
         if (!wait_bar_warp(bar(L::O_READY + s), (n_s - 1) & 1, ctl)) { ok = false; break; }
-        inv_l_smem[s * kBM + r] = l == 0.f ? 0.f : 1.f / l;
+        if constexpr (kHalves) {
+          m_smem[s * kBM + r] = m;
+          l_smem[s * kBM + r] = l;
+        } else {
+          inv_l_smem[s * kBM + r] = l == 0.f ? 0.f : 1.f / l;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::ML_FULL + s));
       }
@@ -671,6 +705,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       const ScoreItem it = take_score_item<kSleepEpilogueNs>(item_ring, bar(L::ITEM_FULL),
                                                              bar(L::ITEM_EMPTY), k, ctl, ok);
       if (!ok || !it.valid) break;
+      if constexpr (kHalves) {
+        // the two stages' states of the same rows: O = sum_s f_s O_s
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int nT = s == 0 ? it.nT0 : it.nT1;
+          uint32_t& n_t = s == 0 ? n_t0 : n_t1;
+          uint32_t& n_e = s == 0 ? n_e0 : n_e1;
+          if (!ok || nT == 0) continue;
+          n_t += static_cast<uint32_t>(nT);
+          if (!wait_bar_warp<kSleepEpilogueNs>(bar(L::ML_FULL + s), n_e & 1, ctl)) { ok = false; continue; }
+          ++n_e;
+          m[s] = m_smem[s * kBM + r];
+          l[s] = l_smem[s * kBM + r];
+          if (!wait_bar_warp<kSleepEpilogueNs>(bar(L::O_READY + s), (n_t - 1) & 1, ctl)) { ok = false; continue; }
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const float top = fmaxf(m[0], m[1]), base = top == -INFINITY ? 0.f : top;
+        float f0 = ex2_approx(m[0] - base), f1 = ex2_approx(m[1] - base);
+        const float sum = fmaf(l[0], f0, l[1] * f1), inv = sum == 0.f ? 0.f : 1.f / sum;
+        f0 *= inv;
+        f1 *= inv;
+        const int row_g = it.row0 + r;
+        const bool stored = row_g < p.rows;
+        const size_t part = p.n_splits > 1 ? static_cast<size_t>(it.split) * p.row_heads : 0;
+        const size_t at = (part + it.rh) * p.rows + static_cast<size_t>(row_g);
+        if (stored)
+          (p.n_splits > 1 ? p.part_lse : p.lse)[at] =
+              sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994530942f;
+        const uint32_t tO = tmem + t_lane + static_cast<uint32_t>(L::kTmemO);
+        if (p.n_splits == 1) {
+          // the slice is free once the previous store has read it
+          if (lane == 0) bulk_wait_group_read0();
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int cc = 0; cc < D / 16; ++cc) {
+          float o[16] = {};
+          if (it.nT0 > 0) {
+            uint32_t v[16];
+            tmem_ld16(tO + cc * 16, v);
+            tmem_wait_ld();
+            reg_fence16(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(v[e]) * f0;
+          }
+          if (it.nT1 > 0) {
+            uint32_t v[16];
+            tmem_ld16(tO + D + cc * 16, v);
+            tmem_wait_ld();
+            reg_fence16(v);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(v[e]), f1, o[e]);
+          }
+          if (p.n_splits > 1) {
+            if (stored) {
+              float4* prow = reinterpret_cast<float4*>(p.part_o + at * D) + cc * 4;
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                prow[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float* x = o + 8 * h;
+              const int box = cc >> 2, chunk = (cc & 3) * 2 + h;
+              st_shared_v4(stage_buf + static_cast<uint32_t>(box * L::kOutBox + lane * 128 +
+                                                             ((chunk ^ (lane & 7)) << 4)),
+                           pack2<BF16>(x[0], x[1]), pack2<BF16>(x[2], x[3]),
+                           pack2<BF16>(x[4], x[5]), pack2<BF16>(x[6], x[7]));
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (it.nT0 > 0) mbar_arrive(bar(L::O_FREE + 0));
+          if (it.nT1 > 0) mbar_arrive(bar(L::O_FREE + 1));
+        }
+        if (p.n_splits == 1) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int warp_row0 = it.row0 + rq * 32;
+          if (lane == 0 && warp_row0 < p.rows) {
+#pragma unroll
+            for (int box = 0; box < D / 64; ++box)
+              tma_store_3d(&tmO, stage_buf + static_cast<uint32_t>(box * L::kOutBox), box * 64,
+                           warp_row0, it.rh);
+            bulk_commit_group();
+          }
+        }
+        continue;
+      }
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (!ok) continue;
@@ -690,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tO = tmem + t_lane + static_cast<uint32_t>(L::kTmemO + s * D);
         if (p.n_splits > 1) {
           // a key range: O / l of this range in fp32, one row per thread
-          const int row_g = stage_row(p, it.row0, s) + r;
+          const int row_g = stage_row<kHalves>(p, it.row0, s) + r;
           float4* prow = reinterpret_cast<float4*>(
               p.part_o + ((static_cast<size_t>(it.split) * p.row_heads + it.rh) * p.rows +
                           static_cast<size_t>(row_g)) * D);
@@ -732,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        const int warp_row0 = stage_row(p, it.row0, s) + rq * 32;
+        const int warp_row0 = stage_row<kHalves>(p, it.row0, s) + rq * 32;
         if (lane == 0 && warp_row0 < p.rows) {
 #pragma unroll
           for (int box = 0; box < D / 64; ++box)
@@ -760,7 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // QK_s with K from fill fk: one asm block, K = D, both operands K-major
       // in smem; commits S_FULL_s, and Q_EMPTY_s after the item's last QK_s
       auto qk = [&](int s, int fk, bool last_of_stage) {
-        const uint64_t da = smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes), 16, 1024);
+        const uint64_t da = smem_desc_sw128(
+            sQ + static_cast<uint32_t>(kHalves ? 0 : s * L::kQBytes), 16, 1024);
         const uint64_t db = smem_desc_sw128(sKV + static_cast<uint32_t>(slot_of(fk) * L::kKVBytes), 16, 1024);
         if constexpr (D == 128) {
           umma_f16_ss_k128(s == 0 ? tS0 : tS1, da, db, kIdescQK, 0u);
@@ -768,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           umma_f16_ss_k64(s == 0 ? tS0 : tS1, da, db, kIdescQK, 0u);
         }
         umma_commit(bar(L::S_FULL + s));
-        if (last_of_stage) umma_commit(bar(L::Q_EMPTY + s));
+        if (last_of_stage) umma_commit(bar(L::Q_EMPTY + (kHalves ? 0 : s)));
       };
       // PV_s: K = 128 keys, A = P_s from tensor memory, B = V MN-major
       auto pv = [&](int s, int fv, bool acc) {
@@ -818,8 +947,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       ScoreItem cur = take_score_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL),
                                                    bar(L::ITEM_EMPTY), 0, ctl, ok);
-      if (ok && cur.valid) ok = begin(cur, 0, 0);
-      else ok = false;
+      if (!cur.valid) ok = false;
+      if constexpr (!kHalves) {
+        if (ok) ok = begin(cur, 0, 0);
+      } else {
+        // Halves: tile q, fills f + 2 q and f + 2 q + 1, is stage q & 1's.  The
+        // order is QK(0) QK(1), then per tile PV(q) QK(q + 2).  Q_0 serves both
+        // stages: the item's last QK frees it.  (The next item begins after
+        // this one's last PV: SMs seldom take a second one.)
+        auto start = [&](const ScoreItem& it, int s, int kq, int f) -> bool {
+          const int n = it.nT0 + it.nT1;
+          if (s >= n) {
+            if (n == 0 && s == 0) {  // no tile: Q, once here, is free again
+              if (!wait_bar_warp<kSleepMmaNs>(bar(L::Q_FULL), kq & 1, ctl)) return false;
+              umma_commit(bar(L::Q_EMPTY));
+              issued = true;
+            }
+            return true;
+          }
+          const int fk = f + 2 * s;
+          if (!wait_bar_warp<kSleepMmaNs>(bar(L::Q_FULL), kq & 1, ctl) ||
+              !wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fk)), par_of(fk), ctl))
+            return false;
+          tc_fence_after();
+          qk(s, fk, s + 1 == n);
+          umma_commit(bar(L::KV_EMPTY + slot_of(fk)));
+          issued = true;
+          return true;
+        };
+        if (ok) ok = start(cur, 0, 0, 0) && start(cur, 1, 0, 0);
+#pragma unroll 1
+        while (ok) {
+          const int n = cur.nT0 + cur.nT1, fN = fK + 2 * n;
+#pragma unroll 1
+          for (int q = 0; q < n && ok; ++q) {
+            const int s = q & 1, fv = fK + 2 * q + 1, fk2 = fK + 2 * q + 4;
+            uint32_t& n_pv = s == 0 ? n_pv0 : n_pv1;
+            const uint32_t n_o = s == 0 ? n_o0 : n_o1;
+            if (!wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fv)), par_of(fv), ctl) ||
+                !wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + s), n_pv & 1, ctl) ||
+                (q < 2 && n_o > 0 &&
+                 !wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + s), (n_o - 1) & 1, ctl))) {
+              ok = false;
+              break;
+            }
+            ++n_pv;
+            tc_fence_after();
+            pv(s, fv, q >= 2);
+            umma_commit(bar(L::KV_EMPTY + slot_of(fv)));
+            if (q + 2 < n) {
+              if (!wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fk2)), par_of(fk2), ctl)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              qk(s, fk2, q + 3 == n);
+              umma_commit(bar(L::KV_EMPTY + slot_of(fk2)));
+            }
+          }
+          if (!ok) break;
+          const ScoreItem nxt = take_score_item<kSleepMmaNs>(
+              item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), kq + 1, ctl, ok);
+          if (!ok || !nxt.valid) break;
+          if (cur.nT0 > 0) ++n_o0;
+          if (cur.nT1 > 0) ++n_o1;
+          ++kq;
+          cur = nxt;
+          fK = fN;
+          ok = start(cur, 0, kq, fK) && start(cur, 1, kq, fK);
+        }
+        ok = false;  // done
+      }
 #pragma unroll 1
       while (ok) {
         // the next item is taken at this item's last key tile, once the
@@ -935,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int box = 0; box < D / 64; ++box)
           tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + box * L::kBox), &tmQ,
-                      bar(L::Q_FULL + s), box * 64, stage_row(p, it.row0, s), it.rh);
+                      bar(L::Q_FULL + s), box * 64, stage_row<kHalves>(p, it.row0, s), it.rh);
         ++nq[s];
         return true;
       };
@@ -949,7 +1147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int box = 0; box < D / 64; ++box)
           tma_load_3d(sKV + static_cast<uint32_t>(slot * L::kKVBytes + box * L::kBox), tm,
                       bar(L::KV_FULL + slot), box * 64,
-                      (it.t0 + (kBack ? it.nT1 - 1 - j : j)) * kBN, it.kvh);
+                      (it.t0 + (kBack ? item_tiles<kHalves>(it) - 1 - j : j)) * kBN, it.kvh);
         last_fill[slot] = fill;
         ++fill;
         return true;
@@ -964,18 +1162,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        const ScoreItem it = idx < 0 ? ScoreItem{} : get_score_item(p, idx);
+        const ScoreItem it = idx < 0 ? ScoreItem{} : get_score_item<kHalves>(p, idx);
         item_ring[slot] = it;
         mbar_arrive(bar(L::ITEM_FULL + slot));
         if (idx < 0) break;
         ok = load_q(it, 0);
 #pragma unroll 1
-        for (int j = 0; ok && j < it.nT1; ++j) {
+        for (int j = 0; ok && j < item_tiles<kHalves>(it); ++j) {
           ok = load_kv(it, 0, j);
-          if (ok && j == 0) ok = load_q(it, 1);
+          if (ok && j == 0 && !kHalves) ok = load_q(it, 1);
           if (ok) ok = load_kv(it, 1, j);
         }
-        if (ok && it.nT1 == 0) ok = load_q(it, 1);
+        if (ok && !kHalves && it.nT1 == 0) ok = load_q(it, 1);
         idx = claim_score_item(p);
       }
       // drain: every load issued lands before shared memory goes away

@@ -24,7 +24,7 @@ struct ScoreParams {
   int packed;
   int row_heads;              // B * H, or packed B * Hkv
   int rows;                   // rows of a row head
-  int one_stage;              // items of 128 rows, all of them stage 1's
+  int halves;                 // items of 128 rows, whose key tiles the stages share
   int n_qtiles;               // ceil(rows / rows of an item)
   int n_items;                // n_qtiles * row_heads * n_splits
   int causal;

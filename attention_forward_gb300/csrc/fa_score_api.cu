@@ -47,27 +47,28 @@ constexpr int kPackTokens = 128;
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 // How the work is cut where its items are fewer than the SMs: into key ranges,
-// and into items of one 128-row stage instead of two.  The smallest estimated
-// time wins, in twentieths of the time of a key tile of 256 rows (1.7 us): rounds
-// of one item an SM, each the tiles of a range, 20 to begin it and, split, 120 for
-// 256 rows of 128 channels of partials written and read again; and 30 for the
-// merge.  A tile of 128 rows takes 19: the stages hide behind each other, and
-// items of one only pay where the SMs take them all at once.  A split has to
-// gain an eighth.  Measured: 8 heads of one token over 700 keys 15.2 us whole,
-// 10.5 split; 8 heads of 2048 x 2048 tokens 31.7 us whole, 105 in 16 ranges; of
-// 1024 x 4096 31 us in 4 ranges of 256 rows, 38 in 2 of 128.
+// and into items of 128 rows whose key tiles the two stages share (halves)
+// instead of 128 rows a stage.  The smallest estimated time wins, in twentieths
+// of the time of a key tile of 256 rows (1.7 us): rounds of one item an SM, each
+// the tiles of a range, 20 to begin it and, split, 120 for 256 rows of 128
+// channels of partials written and read again; and 30 for the merge.  A tile of
+// an item in halves takes 12.  A split has to gain an eighth.  Measured, us, all
+// causal, with a cap: 8 heads of one token over 700 keys 12.6 whole, 9.9 split; of
+// 128 over 2048 23.0 and 12.8; 2 x 8 heads of 1021 x 1500 27.6 with 256 rows, 19.9
+// in halves; 16 of 1024 x 4096 52.6 (in 2 ranges) and 39.0; 8 of 2048 x 2048 34.1
+// and 23.5 (105 in 16 ranges).
 struct Cut {
-  int one_stage, splits;
+  int halves, splits;
   long long cost;
 };
 
-Cut cut_items(int row_heads, int rows, bool one_stage, int D, int n_tiles, int sm_count) {
-  const int item_rows = one_stage ? fa::kBM : fa::kRowsPerCta;
+Cut cut_items(int row_heads, int rows, bool halves, int D, int n_tiles, int sm_count) {
+  const int item_rows = halves ? fa::kBM : fa::kRowsPerCta;
   const long long n = static_cast<long long>(row_heads) * ((rows + item_rows - 1) / item_rows);
   const long long sms = sm_count > 0 ? sm_count : 152;
-  const int tile = one_stage ? 19 : 20;
+  const int tile = halves ? 12 : 20;
   const int part = 120 * std::min(rows, item_rows) * D / (256 * 128);
-  Cut c{one_stage ? 1 : 0, 1, (n + sms - 1) / sms * (tile * n_tiles + 20)};
+  Cut c{halves ? 1 : 0, 1, (n + sms - 1) / sms * (tile * n_tiles + 20)};
   if (n >= sms) return c;
   long long best = c.cost * 7 / 8;
   for (int s = 2; s <= std::min(n_tiles, 64); ++s) {
@@ -82,7 +83,7 @@ Cut cut_items(int row_heads, int rows, bool one_stage, int D, int n_tiles, int s
 }
 
 struct Plan {
-  int packed, row_heads, rows, one_stage, n_qtiles, n_key_tiles, n_stages;
+  int packed, row_heads, rows, halves, n_qtiles, n_key_tiles, n_stages;
   int n_splits, tiles_per_split;
   size_t doc_bytes, split_bytes;  // the workspace's two parts, documents first
 };
@@ -100,8 +101,8 @@ Plan make_plan(int B, int H, int Hkv, int Sq, int Skv, int D, bool documents, in
     const Cut one = cut_items(p.row_heads, p.rows, true, D, p.n_key_tiles, sm_count);
     if (one.cost < cut.cost) cut = one;
   }
-  p.one_stage = cut.one_stage;
-  const int item_rows = p.one_stage ? fa::kBM : fa::kRowsPerCta;
+  p.halves = cut.halves;
+  const int item_rows = p.halves ? fa::kBM : fa::kRowsPerCta;
   p.n_qtiles = (p.rows + item_rows - 1) / item_rows;
   const long long all_rows = static_cast<long long>(p.row_heads) * p.rows;
   const int s = all_rows > 0x7fffffffLL ? 1 : cut.splits;  // the merge's grid
@@ -228,7 +229,7 @@ extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v,
   p.packed = plan.packed;
   p.row_heads = plan.row_heads;
   p.rows = plan.rows;
-  p.one_stage = plan.one_stage;
+  p.halves = plan.halves;
   p.n_qtiles = plan.n_qtiles;
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;

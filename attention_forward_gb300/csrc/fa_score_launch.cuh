@@ -1,13 +1,14 @@
 // fa_score_launch.cuh -- launch of fa_score_kernel, shared by its translation
-// units (one per head dimension).
+// units (one per head dimension and type).
 #pragma once
 #include <mutex>
+#include <type_traits>
 
 #include "fa_score.cuh"
 
 namespace fa {
 
-template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs, bool kHalves>
 cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                          const CUtensorMap& o, const ScoreParams& p, int grid,
                          cudaStream_t stream) {
@@ -20,7 +21,7 @@ cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(fa_score_kernel<D, BF16, kCap, kBias, kDocs>,
+      e = cudaFuncSetAttribute(fa_score_kernel<D, BF16, kCap, kBias, kDocs, kHalves>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                ScoreLayout<D>::kSmemBytes);
       if (e != cudaSuccess) return e;
@@ -39,15 +40,20 @@ cudaError_t score_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_score_kernel<D, BF16, kCap, kBias, kDocs>, q, k, v, o, p);
+  return cudaLaunchKernelEx(&cfg, fa_score_kernel<D, BF16, kCap, kBias, kDocs, kHalves>, q, k, v, o,
+                            p);
 }
 
 template <int D, bool BF16, int kCap, bool kBias>
 cudaError_t score_launch_docs(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
                               const CUtensorMap& o, const ScoreParams& p, int grid,
                               cudaStream_t stream) {
-  return p.doc_k ? score_launch_one<D, BF16, kCap, kBias, true>(q, k, v, o, p, grid, stream)
-                 : score_launch_one<D, BF16, kCap, kBias, false>(q, k, v, o, p, grid, stream);
+  auto with = [&](auto docs) {
+    constexpr bool kDocs = decltype(docs)::value;
+    return p.halves ? score_launch_one<D, BF16, kCap, kBias, kDocs, true>(q, k, v, o, p, grid, stream)
+                    : score_launch_one<D, BF16, kCap, kBias, kDocs, false>(q, k, v, o, p, grid, stream);
+  };
+  return p.doc_k ? with(std::true_type{}) : with(std::false_type{});
 }
 
 template <int D, bool BF16>
@@ -63,11 +69,14 @@ cudaError_t score_launch(const CUtensorMap& q, const CUtensorMap& k, const CUten
                   : score_launch_docs<D, BF16, kCapNone, false>(q, k, v, o, p, grid, stream);
 }
 
-template <int D, bool BF16, int kCap, bool kBias, bool kDocs>
+template <int D, bool BF16, int kCap, bool kBias, bool kDocs, bool kHalves = false>
 cudaError_t score_regs_one(int* regs) {
   cudaFuncAttributes a{};
-  const cudaError_t e = cudaFuncGetAttributes(&a, fa_score_kernel<D, BF16, kCap, kBias, kDocs>);
+  const cudaError_t e =
+      cudaFuncGetAttributes(&a, fa_score_kernel<D, BF16, kCap, kBias, kDocs, kHalves>);
   if (e == cudaSuccess && a.numRegs != 128) *regs = a.numRegs;
+  if constexpr (!kHalves)
+    return e != cudaSuccess ? e : score_regs_one<D, BF16, kCap, kBias, kDocs, true>(regs);
   return e;
 }
 

@@ -190,14 +190,43 @@ def test_what_masked_keys_hold_does_not_matter(bad):
 
 
 def test_without_modifications_it_is_fa_fwd():
-    q, k, v = make(2, 4, 4, 400, 400, 128, "bf16", 12)
+    """Items of 256 rows take the prefill kernel's sums in its order."""
+    q, k, v = make(4, 40, 40, 400, 400, 128, "bf16", 12)
     for causal in (False, True):
-        o, lse = run(q, k, v, causal=causal)
         a, b = fa.fa_fwd_ex(q, k, v, causal=causal, flags=fa.FA_FLAG_SINGLE_CTA, num_splits=1)
-        ws = torch.empty(256, dtype=torch.uint8, device="cuda")
-        o1, l1 = run(q, k, v, causal=causal, workspace=ws)  # no room: unsplit
-        assert torch.equal(o1, a) and torch.equal(l1, b)
-        assert (o.float() - a.float()).abs().max() < 0.02
+        o, lse = run(q, k, v, causal=causal)
+        assert torch.equal(o, a) and torch.equal(lse, b)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_heads_agree_with_fa_fwd(causal):
+    """Other orders of the same sums: each is within its bound of the formula."""
+    q, k, v = make(2, 4, 4, 400, 400, 128, "bf16", 12)
+    ref = expect(q, k, v, causal)
+    ops_ref.check(*fa.fa_fwd_ex(q, k, v, causal=causal, flags=fa.FA_FLAG_SINGLE_CTA, num_splits=1),
+                  ref)
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")  # no room: unsplit
+    for ws in (None, small):
+        ops_ref.check(*run(q, k, v, causal=causal, workspace=ws), ref)
+
+
+@pytest.mark.parametrize("what", ["plain", "cap", "cap16", "bias", "docs", "docs cap", "prefix"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,Skv", [(300, 300), (257, 500), (130, 1021)])
+def test_more_heads_than_multiprocessors(Sq, Skv, D, what):
+    """Items of 256 rows, several to a CTA (fewer heads: halves)."""
+    q, k, v = make(11, 32, 16, Sq, Skv, D, "fp16" if what == "cap16" else "bf16", 31)
+    kw = {}
+    if "cap" in what:
+        kw["softcap"] = 20.0
+    if what == "bias":
+        kw["slopes"] = slopes_of(32)
+    if "docs" in what:
+        kw["doc_q"], kw["doc_k"] = documents(11, Sq, Skv, (90, 140, 290), pad=3)
+    if what == "prefix":
+        kw["prefix"] = torch.tensor([0, 1, 100, 128, 129, 200, 256, 257, 299, 300, 5000],
+                                    dtype=torch.int32, device="cuda")
+    ops_ref.check(*run(q, k, v, causal=True, **kw), expect(q, k, v, True, **kw))
 
 
 def test_many_items_and_long_rows():
