@@ -274,6 +274,37 @@ def test_two_streams_at_once_and_a_stream_that_is_not_current():
         assert torch.equal(y[0], rb[0]) and torch.equal(y[1], rb[1])
 
 
+def test_two_threads_on_one_stream():
+    """The library's workspace is one per stream: a call's launches stay together,
+    and growing it waits for what was launched with it."""
+    import threading
+    a = make(1, 4, 1, 3, 5000, 128, "bf16", 40)     # split, merged
+    b = make(1, 8, 8, 500, 900, 64, "fp16", 41)     # documents
+    c = make(2, 16, 2, 64, 9000, 128, "bf16", 42)   # split, a larger workspace
+    dq, dk = documents(1, 500, 900, (50, 300, 620))
+    calls = [lambda: run(*a, causal=True, softcap=30.0),
+             lambda: run(*b, causal=True, doc_q=dq, doc_k=dk), lambda: run(*c)]
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    fa.fa_release_workspaces()
+    got = [[] for _ in calls]
+
+    def work(n):
+        for _ in range(40):
+            got[n].append(calls[n]())
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, rows in zip(want, got):
+        assert len(rows) == 40
+        for o, lse in rows:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
 def test_graph_reads_ids_prefixes_and_inputs_at_replay():
     q, k, v = make(2, 4, 2, 300, 400, 128, "bf16", 18)
     dq, dk = documents(2, 300, 400, (90, 200))
