@@ -28,12 +28,12 @@ cudaError_t launch(Kernel kernel, const CacheCopyParams& p, int tokens, cudaStre
 
 template <int D, bool BF16>
 cudaError_t write(const CacheCopyParams& p, cudaStream_t stream) {
-  return launch(fa_cache_write_kernel<D, BF16>, p, kCacheCopyRows<D> * kCacheWriteTurns, stream);
+  return launch(fa_cache_write_kernel<D, BF16>, p, kCacheWriteRows<D> * kCacheWriteTurns, stream);
 }
 
 template <int D, bool BF16>
 cudaError_t read(const CacheCopyParams& p, cudaStream_t stream) {
-  return launch(fa_cache_read_kernel<D, BF16>, p, kCacheCopyRows<D> * kCacheReadTurns, stream);
+  return launch(fa_cache_read_kernel<D, BF16>, p, kCacheReadRows<D> * kCacheReadTurns, stream);
 }
 
 }  // namespace

@@ -9,9 +9,14 @@
 // by side.
 //
 // Both kernels only move bytes (write: 4 D in, 2 (D/2 + D/8) out per token
-// and head; read the reverse) and are bound by HBM: one thread takes 8
-// channels of K and of V, 16 bytes each on the 16-bit side and a word each on
-// the packed side, so that a row's lanes cover whole sectors on both.
+// and head; read the reverse).  The read is bound by HBM: a thread takes 8
+// channels of K and of V, a word each on the packed side and 16 bytes on the
+// other, so that a row's lanes cover whole sectors on both.  The write is bound
+// by its instructions (16 a value at first, most of them of the ALU pipe): a
+// thread takes 16 channels, so that two lanes share a group's parameters.
+// 32 x 8 heads of 4096 tokens, D = 128, 705 MB: write 144 us in bf16 (4.9 TB/s of
+// 6.8), 126 in fp16, whose grid has fewer ties; read 111 us (6.3 TB/s).  With 8
+// channels a lane, every tie and limit looked at in place: 218 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -66,55 +71,29 @@ __device__ __forceinline__ float min3_nan(float a, float b, float c) {
   return d;
 }
 
-// One group's codes from 8 of its channels per lane (4 lanes of a quad hold
-// the group): the word of codes and the (scale, minimum) pair.
-//
-// A code is floor((x - z) / s + 1/2), decided exactly.  q = d inv + 1.5 2^23
-// leaves the nearest integer c to d / s (d = x - z, inv = 1 / s, both
-// rounded) in the low bits of q, and r = d - c s is exact in one FMA (c s has
-// 15 bits, and d is within a scale of it); r >= s / 2 (a tie that went down)
-// adds one.  That is the code wherever d is x - z exactly, as it is unless x
-// has bits 2^24 below z.  Only beside a tie can the lost bits decide: there
-// the lane looks for them (two-sum), and with any of them goes through its
-// channels with err, the lost part, added to r.
-__device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& word,
-                                               uint32_t& param) {
+// The codes of a group are floor((x - z) / s + 1/2), decided exactly.  With
+// d = x - z and inv = 1 / s, both rounded, q = d inv + 1.5 2^23 leaves the nearest
+// integer c to d / s in the low bits of q, and r = d - c s is exact in one FMA
+// (c s has 15 bits, and d is within a scale of it).  |r| < 0.499998 s says that c
+// is the code wherever d is x - z to 2^-23.  A value beside a tie, a code outside
+// 0 ... 15, a value past the limit, a NaN and s = 0 go to cache_codes_slow, as ties
+// of bf16 values often do.
+
+// The word of 8 channels when any of the group's lanes found such a value.  r >=
+// s / 2, a tie that went down, adds one.  Only beside a tie can the bits that d
+// lost decide: there the lane looks for them (two-sum), and with any of them goes
+// through its channels with err, the lost part, added to r.
+// (Out of line: its registers are not the kernel's.  A template, for the linker.)
+template <int kUnused = 0>
+__device__ __noinline__ uint32_t cache_codes_slow(float x0, float x1, float x2, float x3, float x4,
+                                                  float x5, float x6, float x7, float z, float s) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
   constexpr float kMagic = 12582912.f;  // 1.5 2^23
-  float lo = min3_nan(x[0], x[1], x[2]), hi = fmax3(x[0], x[1], x[2]);
-  lo = min3_nan(lo, x[3], x[4]);
-  hi = fmax3(hi, x[3], x[4]);
-  lo = min3_nan(lo, x[5], x[6]);
-  hi = fmax3(hi, x[5], x[6]);
-  lo = min_nan(lo, x[7]);
-  hi = fmaxf(hi, x[7]);
-#pragma unroll
-  for (int m = 1; m <= 2; m <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-  }
-  if (lo != lo) {  // a NaN makes its whole group NaN: the parameters carry it
-    word = 0u;
-    param = 0x7fff7fffu;
-    return;
-  }
-  // values past the limit take the codes at the ends
-  lo = fminf(fmaxf(lo, -kCacheLimit), kCacheLimit);
-  hi = fminf(fmaxf(hi, -kCacheLimit), kCacheLimit);
-  const __half zh = __float2half_rn(lo);
-  // (hi - lo) / 15, correctly rounded: a product by 1/15 and its residual
-  const float range = hi - lo, near15 = range * (1.f / 15.f);
-  const __half sh = __float2half_rn(fmaf(fmaf(-15.f, near15, range), 1.f / 15.f, near15));
-  param = static_cast<uint32_t>(__half_as_ushort(sh)) |
-          (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
-  const float z = __half2float(zh), s = __half2float(sh);
-  if (s == 0.f) {
-    word = 0u;
-    return;
-  }
+  if (s == 0.f) return 0u;
   const float inv = __fdividef(1.f, s);  // q may miss by one: r shows it
   const float half_s = 0.5f * s;
   float far = 0.f;
-  word = 0u;
+  uint32_t word = 0u;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const float d = x[e] - z;
@@ -154,6 +133,94 @@ __device__ __forceinline__ void cache_quantise(const float (&x)[8], uint32_t& wo
       }
     }
   }
+  return word;
+}
+
+// (scale, minimum) of the values lo ... hi.
+__device__ __forceinline__ void cache_params(float lo, float hi, __half& sh, __half& zh) {
+  zh = __float2half_rn(lo);
+  // (hi - lo) / 15, correctly rounded: a product by 1/15 and its residual
+  const float range = hi - lo, near15 = range * (1.f / 15.f);
+  sh = __float2half_rn(fmaf(fmaf(-15.f, near15, range), 1.f / 15.f, near15));
+}
+
+// One group's codes from 16 of its channels per lane (the 2 lanes of a pair hold
+// the group): the two words of codes and the (scale, minimum) pair.  What takes a
+// group's time is the ALU pipe (minima, maxima, comparisons, shifts), so codes
+// are put together by FMAs, c0 + 16 c1 + 256 c2 + 4096 c3 at a time, exactly.
+__device__ __forceinline__ void cache_quantise(const float (&x)[2][8], uint32_t (&word)[2],
+                                               uint32_t& param) {
+  constexpr float kMagic = 12582912.f;  // 1.5 2^23
+  float lo = x[0][0], hi = x[0][0];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      lo = min3_nan(lo, x[h][e], x[h][e + 1]);
+      hi = fmax3(hi, x[h][e], x[h][e + 1]);
+    }
+  }
+  lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+  hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+  __half sh, zh;
+  cache_params(lo, hi, sh, zh);
+  float z = __half2float(zh), s = __half2float(sh);
+  const float inv = __fdividef(1.f, s);
+  // both words at once, in packed pairs
+  float far[2] = {0.f, 0.f}, sum[2][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float c[4][2], r[4][2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float d0, d1;
+      fadd2(d0, d1, x[0][4 * k + e], x[1][4 * k + e], -z, -z);
+      ffma2(c[e][0], c[e][1], d0, d1, inv, inv, kMagic, kMagic);
+      fadd2(c[e][0], c[e][1], c[e][0], c[e][1], -kMagic, -kMagic);
+      ffma2(r[e][0], r[e][1], c[e][0], c[e][1], -s, -s, d0, d1);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      far[h] = fmax3(far[h], fabsf(r[0][h]), fabsf(r[1][h]));
+      far[h] = fmax3(far[h], fabsf(r[2][h]), fabsf(r[3][h]));
+    }
+    fadd2(sum[k][0], sum[k][1], c[0][0], c[0][1], 8388608.f, 8388608.f);
+    ffma2(sum[k][0], sum[k][1], c[1][0], c[1][1], 16.f, 16.f, sum[k][0], sum[k][1]);
+    ffma2(sum[k][0], sum[k][1], c[2][0], c[2][1], 256.f, 256.f, sum[k][0], sum[k][1]);
+    ffma2(sum[k][0], sum[k][1], c[3][0], c[3][1], 4096.f, 4096.f, sum[k][0], sum[k][1]);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)  // 2^23 + 16 bits of codes each
+    word[h] = __byte_perm(__float_as_uint(sum[0][h]), __float_as_uint(sum[1][h]), 0x5410);
+  param = static_cast<uint32_t>(__half_as_ushort(sh)) |
+          (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+  // the extremes' codes are within 0 ... 15 (a NaN fails every comparison)
+  const bool plain = lo - z > -0.49f * s && hi - z < 15.49f * s && lo >= -kCacheLimit &&
+                     hi <= kCacheLimit;
+  if (!plain) {
+    if (lo != lo) {  // a NaN makes its whole group NaN: the parameters carry it
+      word[0] = word[1] = 0u;
+      param = 0x7fff7fffu;
+      return;
+    }
+    // values past the limit take the codes at the ends
+    cache_params(fminf(fmaxf(lo, -kCacheLimit), kCacheLimit),
+                 fminf(fmaxf(hi, -kCacheLimit), kCacheLimit), sh, zh);
+    z = __half2float(zh);
+    s = __half2float(sh);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      word[h] = cache_codes_slow<>(x[h][0], x[h][1], x[h][2], x[h][3], x[h][4], x[h][5], x[h][6],
+                                 x[h][7], z, s);
+    param = static_cast<uint32_t>(__half_as_ushort(sh)) |
+            (static_cast<uint32_t>(__half_as_ushort(zh)) << 16);
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (!(far[h] < s * 0.499998f))
+      word[h] = cache_codes_slow<>(x[h][0], x[h][1], x[h][2], x[h][3], x[h][4], x[h][5], x[h][6],
+                                 x[h][7], z, s);
 }
 
 // The 8 values of a word, rounded once to 16 bits, in the order of their
@@ -184,57 +251,73 @@ __device__ __forceinline__ uint4 cache_values(uint32_t word, uint32_t param) {
 }
 
 // Rows per block: the lanes of a row lie side by side.  blockIdx.y is the
-// (sequence, kv head), blockIdx.x the block of its tokens; a thread takes
-// a few tokens in turn, whose loads go out together.
+// (sequence, kv head), blockIdx.x the block of its tokens.  A write thread takes 4
+// tokens one after the other, which spreads its 64-bit addresses (us for the 705
+// MB: 1 token 181, 2 162, 4 154, 8 151 with a longer tail where tokens are few),
+// 8 blocks an SM (64 registers; 144 us, 7 blocks 152, 10 151).  A read thread takes
+// 2, whose loads go out together (1 ... 8 measured within 6 %).
 constexpr int kCacheCopyThreads = 128;
-constexpr int kCacheWriteTurns = 2, kCacheReadTurns = 2;  // 1 ... 8 measured within 6 %
+constexpr int kCacheWriteTurns = 4, kCacheReadTurns = 2, kCacheWriteBlocks = 8;
 
 template <int D>
-constexpr int kCacheCopyRows = kCacheCopyThreads / (D / 8);
+constexpr int kCacheWriteRows = kCacheCopyThreads / (D / 16);
+template <int D>
+constexpr int kCacheReadRows = kCacheCopyThreads / (D / 8);
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const CacheCopyParams p) {
-  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+__global__ void __launch_bounds__(kCacheCopyThreads, kCacheWriteBlocks)
+    fa_cache_write_kernel(const CacheCopyParams p) {
+  constexpr int kLanes = D / 16, kGroups = D / kCacheGroup, kRows = kCacheWriteRows<D>;
   constexpr int kTurns = kCacheWriteTurns;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 8 lane ... + 7
+  const int lane = static_cast<int>(threadIdx.x) % kLanes;  // channels 16 lane ... + 15
   const int bh = static_cast<int>(blockIdx.y);
   const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
   const int first = static_cast<int>(blockIdx.x) * kRows * kTurns;
   const int start = p.start ? p.start[b] : 0;
   const int count = p.count ? min(p.count[b], p.S) : p.S;
   if (first >= count) return;
-  const int i0 = first + static_cast<int>(threadIdx.x) / kLanes;
-  const int g = lane >> 2, t = lane & 3;
-
-  uint4 w[kTurns][2];
-  long long row[kTurns];
+  const int g = lane >> 1, t = 2 * (lane & 1);
+  const uint4* in[2];
+  uint32_t *codes[2], *params[2];
 #pragma unroll
-  for (int k = 0; k < kTurns; ++k) {
-    const int i = i0 + k * kRows;
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      w[k][n] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < count)
-        w[k][n] = __ldcs(reinterpret_cast<const uint4*>(p.rows[n]) +
-                         (static_cast<size_t>(bh) * p.S + i) * kLanes + lane);
-    }
-    row[k] = i < count ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
-    if (i < count && row[k] < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+  for (int n = 0; n < 2; ++n) {
+    in[n] = reinterpret_cast<const uint4*>(p.rows[n]) + static_cast<size_t>(bh) * p.S * (2 * kLanes) +
+            2 * lane;
+    codes[n] = reinterpret_cast<uint32_t*>(p.pool.codes[n]) + kGroups * t + g;
+    params[n] = p.pool.params[n] + g;
   }
+
+#pragma unroll 1
+  for (int i = first + static_cast<int>(threadIdx.x) / kLanes, end = min(first + kRows * kTurns, count);
+       __any_sync(0xffffffffu, i < end); i += kRows) {
+    uint4 w[2][2];
 #pragma unroll
-  for (int k = 0; k < kTurns; ++k) {
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[n][h] = i < end ? __ldcs(in[n] + static_cast<size_t>(i) * (2 * kLanes) + h)
+                          : make_uint4(0u, 0u, 0u, 0u);
+    const long long row =
+        i < end ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
+    if (i < end && row < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      const float2 a = cache_unpack<BF16>(w[k][n].x), b2 = cache_unpack<BF16>(w[k][n].y);
-      const float2 c = cache_unpack<BF16>(w[k][n].z), d = cache_unpack<BF16>(w[k][n].w);
-      const float x[8] = {a.x, a.y, b2.x, b2.y, c.x, c.y, d.x, d.y};
-      uint32_t word, param;
+      float x[2][8];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 a = cache_unpack<BF16>(w[n][h].x), b2 = cache_unpack<BF16>(w[n][h].y);
+        const float2 c = cache_unpack<BF16>(w[n][h].z), d = cache_unpack<BF16>(w[n][h].w);
+        x[h][0] = a.x; x[h][1] = a.y; x[h][2] = b2.x; x[h][3] = b2.y;
+        x[h][4] = c.x; x[h][5] = c.y; x[h][6] = d.x; x[h][7] = d.y;
+      }
+      uint32_t word[2], param;
       cache_quantise(x, word, param);
-      if (row[k] >= 0) {
-        reinterpret_cast<uint32_t*>(p.pool.codes[n])[row[k] * kLanes + kGroups * t + g] = word;
-        if (t == 0) p.pool.params[n][row[k] * kGroups + g] = param;
+      if (row >= 0) {
+        codes[n][row * (D / 8)] = word[0];
+        codes[n][row * (D / 8) + kGroups] = word[1];
+        if (t == 0) params[n][row * kGroups] = param;
       }
     }
   }
@@ -242,7 +325,7 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_write_kernel(const
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const CacheCopyParams p) {
-  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheCopyRows<D>;
+  constexpr int kLanes = D / 8, kGroups = D / kCacheGroup, kRows = kCacheReadRows<D>;
   constexpr int kTurns = kCacheReadTurns;
   grid_dependency_wait();
   grid_launch_dependents();
