@@ -49,25 +49,25 @@ __device__ __forceinline__ void fmul2(float& d0, float& d1, float a0, float a1, 
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-// Register split: 176 / 72 / 88 as in the prefill kernel for unmodified scores,
-// 184 / 64 / 80 with a cap or a bias (their sum is the launch allocation).
-// Measured on B4 H16 S4096 D128: 367 against 382 us without a cap, 571 against
-// 548 with one.
-constexpr int kRegsLaunch = kThreads * 128;
-template <bool kMod>
-constexpr int kRegsScoreSoftmax = kMod ? 184 : 176;
-template <bool kMod>
-constexpr int kRegsScoreEpilogue = kMod ? 64 : 72;
-template <bool kMod>
-constexpr int kRegsScoreControl = kMod ? 80 : 88;
-static_assert(128 * (2 * kRegsScoreSoftmax<true> + kRegsScoreEpilogue<true> +
-                     kRegsScoreControl<true>) == kRegsLaunch &&
-                  128 * (2 * kRegsScoreSoftmax<false> + kRegsScoreEpilogue<false> +
-                         kRegsScoreControl<false>) == kRegsLaunch,
-              "register split must equal the launch allocation");
 // How a call caps its scores: not; with the running reference maximum; without
 // a reference, where the cap bounds every score enough.
 enum CapForm { kCapNone = 0, kCapRunning = 1, kCapFixed = 2 };
+
+// Registers a thread of the softmax, epilogue and control warpgroups: as in the
+// prefill kernel for unmodified scores, more for the softmax of modified ones (the
+// sums are the launch's allocation).  Measured on B4 H16 S4096 D128, bf16, us, for
+// 176, 184 and 192: plain 371, 384, 384; cap 50 491, 470, 466; cap and bias 677,
+// 675, 659; a bias at B8 H16 S2048 D64 in fp16 124, 120, 127.
+constexpr int kRegsLaunch = kThreads * 128;
+template <int kCap, bool kBias>
+struct ScoreRegs {
+  static constexpr bool kMore = kCap != kCapNone || kBias;
+  static constexpr int kSoftmax = kCap == kCapRunning ? 192 : kMore ? 184 : 176;
+  static constexpr int kEpilogue = kCap == kCapRunning ? 56 : kMore ? 64 : 72;
+  static constexpr int kControl = kCap == kCapRunning ? 72 : kMore ? 80 : 88;
+  static_assert(128 * (2 * kSoftmax + kEpilogue + kControl) == kRegsLaunch,
+                "register split must equal the launch allocation");
+};
 
 // One work item, worked out by the producer and handed to the other roles
 // through a ring in shared memory (worked out by each of them, its divisions
@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ CUtensorMap tmO,
                     const ScoreParams p) {
   using L = ScoreLayout<D>;
+  using Regs = ScoreRegs<kCap, kBias>;
   // Modified scores: an item's key tiles run from the last to the first, and
   // stage 0, which lacks the last ones of a causal item, joins late.  With a bias
   // the keys next to the rows have the largest scores, and what comes after them
@@ -574,11 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int wg = warp >> 2;
   if (wg < 2) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsScoreSoftmax<kCap != kCapNone || kBias>));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs::kSoftmax));
   } else if (wg == 2) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScoreEpilogue<kCap != kCapNone || kBias>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kEpilogue));
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsScoreControl<kCap != kCapNone || kBias>));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs::kControl));
   }
 
   if (wg < 2) {
