@@ -56,8 +56,8 @@ enum CapForm { kCapNone = 0, kCapRunning = 1, kCapFixed = 2 };
 // Registers a thread of the softmax, epilogue and control warpgroups: as in the
 // prefill kernel for unmodified scores, more for the softmax of modified ones (the
 // sums are the launch's allocation).  Measured on B4 H16 S4096 D128, bf16, us, for
-// 176, 184 and 192: plain 371, 384, 384; cap 50 491, 470, 466; cap and bias 677,
-// 675, 659; a bias at B8 H16 S2048 D64 in fp16 124, 120, 127.
+// 176, 184 and 192: plain 371, 384, 384; cap 50 491, 470, 466; cap 100, causal,
+// 301, 300, 290; a bias at B8 H16 S2048 D64 in fp16 124, 120, 127.
 constexpr int kRegsLaunch = kThreads * 128;
 template <int kCap, bool kBias>
 struct ScoreRegs {
@@ -77,7 +77,33 @@ struct ScoreItem {
   int rh, b, kvh;  // row head, its batch row, its kv head [B * Hkv]
   int h0;          // its query head (packed: the group's first)
   int row0, nT0, nT1, t0, split;  // nT_s: stage s's tiles
+  int turn;                       // >= 0: both stages' first tile is t0 + turn
 };
+
+// Key tiles that an item loads.
+template <bool kHalves>
+__device__ __forceinline__ int item_tiles(const ScoreItem& it) {
+  return kHalves ? it.nT0 + it.nT1 : it.nT1;
+}
+
+// The q-th tile of an item that walks n tiles backwards: from the last to the
+// first or, with `turn`, from t0 + turn to the first and then from the last.
+template <bool kTurns>
+__device__ __forceinline__ int tile_back(const ScoreItem& it, int n, int q) {
+  if (kTurns && it.turn >= 0)
+    return it.t0 + (q <= it.turn ? it.turn - q : it.turn + n - q);
+  return it.t0 + n - 1 - q;
+}
+
+// Keys on both sides of the rows, with a bias: the tile next to the rows, whose
+// scores are the largest (B4 H16 S4096 D128: 432 us, 527 from the last tile on).
+template <bool kHalves>
+__device__ __forceinline__ int item_turn(const ScoreParams& p, const ScoreItem& it) {
+  const int n = item_tiles<kHalves>(it);
+  if (!p.slopes || p.causal || (!kHalves && it.nT0 != it.nT1)) return -1;
+  const int i = p.packed ? p.Sq - 1 : min(it.row0 + (kHalves ? kBM : kRowsPerCta), p.rows) - 1;
+  return min(max(max(i + (p.Skv - p.Sq), 0) / kBN - it.t0, 0), n - 1);
+}
 
 template <int D>
 struct ScoreLayout : PrefillLayout<D> {
@@ -92,12 +118,6 @@ struct ScoreLayout : PrefillLayout<D> {
 template <bool kHalves>
 __device__ __forceinline__ int stage_row(const ScoreParams& p, int row0, int s) {
   return kHalves ? row0 : min(row0 + s * kBM, p.rows);
-}
-
-// Key tiles that an item loads.
-template <bool kHalves>
-__device__ __forceinline__ int item_tiles(const ScoreItem& it) {
-  return kHalves ? it.nT0 + it.nT1 : it.nT1;
 }
 
 // The key tiles [x, y) that the 128 rows from `row` of batch row b need.
@@ -160,6 +180,7 @@ __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int id
     it.t0 = r0.x;
     it.nT0 = (n + 1) >> 1;
     it.nT1 = n >> 1;
+    it.turn = item_turn<kHalves>(p, it);
     return it;
   }
   const bool h0 = r0.x < r0.y, h1 = r1.x < r1.y;
@@ -167,6 +188,7 @@ __device__ __forceinline__ ScoreItem get_score_item(const ScoreParams& p, int id
   it.nT0 = h0 ? r0.y - it.t0 : 0;
   // the MMA warp steps through stage 1's tiles: stage 0 never has more
   it.nT1 = max(h1 ? r1.y - it.t0 : 0, it.nT0);
+  it.turn = item_turn<kHalves>(p, it);
   return it;
 }
 
@@ -604,10 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ScoreRow row{};
       // this stage's j-th tile
       auto tile_of = [&](int j) {
-        if constexpr (kHalves)
-          return it.t0 + (kBack ? it.nT0 + it.nT1 - 1 - s - 2 * j : s + 2 * j);
-        else
-          return it.t0 + (kBack ? nT - 1 - j : j);
+        const int q = kHalves ? s + 2 * j : j;
+        return kBack ? tile_back<kBias>(it, kHalves ? it.nT0 + it.nT1 : nT, q) : it.t0 + q;
       };
       // the id that all keys of a tile have, of the tile to come
       const int* docs_of = nullptr;
@@ -1148,7 +1168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int box = 0; box < D / 64; ++box)
           tma_load_3d(sKV + static_cast<uint32_t>(slot * L::kKVBytes + box * L::kBox), tm,
                       bar(L::KV_FULL + slot), box * 64,
-                      (it.t0 + (kBack ? item_tiles<kHalves>(it) - 1 - j : j)) * kBN, it.kvh);
+                      (kBack ? tile_back<kBias>(it, item_tiles<kHalves>(it), j) : it.t0 + j) * kBN, it.kvh);
         last_fill[slot] = fill;
         ++fill;
         return true;

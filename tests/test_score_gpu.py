@@ -210,7 +210,8 @@ def test_few_heads_agree_with_fa_fwd(causal):
         ops_ref.check(*run(q, k, v, causal=causal, workspace=ws), ref)
 
 
-@pytest.mark.parametrize("what", ["plain", "cap", "cap16", "bias", "docs", "docs cap", "prefix"])
+@pytest.mark.parametrize("what", ["plain", "cap", "cap16", "bias", "bias full", "docs",
+                                  "docs cap", "prefix"])
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Sq,Skv", [(300, 300), (257, 500), (130, 1021)])
 def test_more_heads_than_multiprocessors(Sq, Skv, D, what):
@@ -219,14 +220,15 @@ def test_more_heads_than_multiprocessors(Sq, Skv, D, what):
     kw = {}
     if "cap" in what:
         kw["softcap"] = 20.0
-    if what == "bias":
+    if "bias" in what:
         kw["slopes"] = slopes_of(32)
+    causal = "full" not in what
     if "docs" in what:
         kw["doc_q"], kw["doc_k"] = documents(11, Sq, Skv, (90, 140, 290), pad=3)
     if what == "prefix":
         kw["prefix"] = torch.tensor([0, 1, 100, 128, 129, 200, 256, 257, 299, 300, 5000],
                                     dtype=torch.int32, device="cuda")
-    ops_ref.check(*run(q, k, v, causal=True, **kw), expect(q, k, v, True, **kw))
+    ops_ref.check(*run(q, k, v, causal=causal, **kw), expect(q, k, v, causal, **kw))
 
 
 def test_many_items_and_long_rows():
