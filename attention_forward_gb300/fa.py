@@ -287,6 +287,9 @@ def _group_check(H: int, Hkv: int) -> None:
 def _outputs_on(q, dev, out, lse, stream):
     """The outputs of a call on q's device, made where they are not given."""
     B, H, Sq, D = q.shape
+    if out is None and lse is None and stream is None:
+        return (torch.empty_like(q),
+                torch.empty((B, H, Sq), dtype=torch.float32, device=q.device))
     made = []
     if out is None:
         out = torch.empty_like(q)
@@ -304,9 +307,7 @@ def _outputs_on(q, dev, out, lse, stream):
 
 
 def _workspace_of(workspace, dev):
-    """(pointer, bytes) of a caller's workspace; (None, 0) for the library's."""
-    if workspace is None:
-        return None, 0
+    """(pointer, bytes) of a caller's workspace."""
     if workspace.get_device() != dev or not workspace.is_contiguous() or not workspace.numel():
         raise ValueError("workspace must be a contiguous tensor on the call's CUDA device")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -337,10 +338,12 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
     ``workspace`` the library's own for the stream serves (a captured call gets
     one of the graph's memory).  Returns (o, lse)."""
     dev, (B, H, Sq, D) = _rows16(q, "q")
-    _, (_, Hkv, Skv, _) = _rows16(k, "k")
+    _, kv = _rows16(k, "k")
+    Hkv, Skv = kv[1], kv[2]
     _group_check(H, Hkv)
-    kv = (B, Hkv, Skv, D)
-    kp, vp = _ptr(k, "k", dev, q.dtype, kv), _ptr(v, "v", dev, q.dtype, kv)
+    if kv[0] != B or kv[3] != D or k.dtype is not q.dtype or k.get_device() != dev:
+        _bad(k, "k", dev, q.dtype, (B, Hkv, Skv, D))
+    kp, vp = k.data_ptr(), _ptr(v, "v", dev, q.dtype, kv)
     sp = dqp = dkp = pp = None
     if slopes is not None:
         sp = _ptr(slopes, "slopes", dev, torch.float32, (H,))
@@ -355,9 +358,9 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
             return fa_fwd_score(q, k, v, causal, scale, softcap, slopes, doc_q, doc_k, prefix,
                                 workspace, out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
-    L = load()
+    L = _lib or load()
     out, lse = _outputs_on(q, dev, out, lse, stream)
-    ws, ws_bytes = _workspace_of(workspace, dev)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
     args = (q.data_ptr(), kp, vp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, Skv, D, sc,
             bool(causal), _DTYPE[q.dtype], softcap, sp, dqp, dkp, pp)
     handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
@@ -406,6 +409,40 @@ def _pages(page_table, dev: int, B: int):
 
 
 def _copy_args(k, v, cache, page_table, start, count):
+    """(device, arguments) of a cache copy.  The checks in one expression, for
+    their time beside the copies' own; what it refuses is named one by one."""
+    try:
+        kc, kp, vc, vp = cache
+        dt, rows, dev = k.dtype, k.shape, k.get_device()
+        B, Hkv, S, D = rows
+        pages, _, page, _ = kc.shape
+        n, per = page_table.shape
+        codes, params = (pages, Hkv, page, D // 2), (pages, Hkv, page, D // 32, 2)
+        u8, f16, i32 = torch.uint8, torch.float16, torch.int32
+        if (dev >= 0 and k.is_contiguous() and n == B
+                and v.dtype is dt and v.shape == rows and v.get_device() == dev
+                and v.is_contiguous()
+                and kc.dtype is u8 and kc.shape == codes and kc.get_device() == dev
+                and kc.is_contiguous()
+                and kp.dtype is f16 and kp.shape == params and kp.get_device() == dev
+                and kp.is_contiguous()
+                and vc.dtype is u8 and vc.shape == codes and vc.get_device() == dev
+                and vc.is_contiguous()
+                and vp.dtype is f16 and vp.shape == params and vp.get_device() == dev
+                and vp.is_contiguous()
+                and page_table.dtype is i32 and page_table.get_device() == dev
+                and page_table.is_contiguous()
+                and (start is None or start.dtype is i32 and start.shape == (B,)
+                     and start.get_device() == dev and start.is_contiguous())
+                and (count is None or count.dtype is i32 and count.shape == (B,)
+                     and count.get_device() == dev and count.is_contiguous())):
+            return (dev, (k.data_ptr(), v.data_ptr()),
+                    (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()),
+                    (page_table.data_ptr(), None if start is None else start.data_ptr(),
+                     None if count is None else count.data_ptr()),
+                    (B, Hkv, S, D, pages, page, per, _DTYPE[dt]))
+    except (AttributeError, IndexError, KeyError, TypeError, ValueError):
+        pass
     dev, (B, Hkv, S, D) = _rows16(k, "k")
     vptr = _ptr(v, "v", dev, k.dtype, k.shape)
     kc, kp, vc, vp, pages, page = _cache(cache, dev, Hkv, D)
@@ -426,8 +463,9 @@ def fa_cache_write(k, v, cache, page_table, start=None, count=None, stream=None)
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return fa_cache_write(k, v, cache, page_table, start, count, stream)
-    st = load().fa_cache_write(*rows, *pool, *where, *sizes,
-                               _raw_stream(dev) if stream is None else _stream_handle(stream))
+    st = (_lib or load()).fa_cache_write(
+        *rows, *pool, *where, *sizes,
+        _raw_stream(dev) if stream is None else _stream_handle(stream))
     if st:
         _check(st, "fa_cache_write")
 
@@ -443,8 +481,9 @@ def fa_cache_read(cache, page_table, start=None, count=None, out=None, stream=No
     if _current_device() != dev:
         with torch.cuda.device(dev):
             return fa_cache_read(cache, page_table, start, count, out, stream)
-    st = load().fa_cache_read(*pool, *where, *rows, *sizes,
-                              _raw_stream(dev) if stream is None else _stream_handle(stream))
+    st = (_lib or load()).fa_cache_read(
+        *pool, *where, *rows, *sizes,
+        _raw_stream(dev) if stream is None else _stream_handle(stream))
     if st:
         _check(st, "fa_cache_read")
     return k, v
@@ -455,6 +494,39 @@ def fa_cache_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, D: int, page_siz
     return int(load().fa_cache_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages))
 
 
+def _attn_args(cache, page_table, length, dev: int, B: int, H: int, D: int):
+    """As _copy_args: a cache, its page table and lengths."""
+    try:
+        kc, kp, vc, vp = cache
+        pages, Hkv, page, _ = kc.shape
+        n, per = page_table.shape
+        codes, params = (pages, Hkv, page, D // 2), (pages, Hkv, page, D // 32, 2)
+        u8, f16, i32 = torch.uint8, torch.float16, torch.int32
+        if (n == B and Hkv > 0 and H % Hkv == 0
+                and kc.dtype is u8 and kc.shape == codes and kc.get_device() == dev
+                and kc.is_contiguous()
+                and kp.dtype is f16 and kp.shape == params and kp.get_device() == dev
+                and kp.is_contiguous()
+                and vc.dtype is u8 and vc.shape == codes and vc.get_device() == dev
+                and vc.is_contiguous()
+                and vp.dtype is f16 and vp.shape == params and vp.get_device() == dev
+                and vp.is_contiguous()
+                and page_table.dtype is i32 and page_table.get_device() == dev
+                and page_table.is_contiguous()
+                and length.dtype is i32 and length.shape == (B,)
+                and length.get_device() == dev and length.is_contiguous()):
+            return (Hkv, kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), pages, page,
+                    page_table.data_ptr(), per, length.data_ptr())
+    except (AttributeError, IndexError, TypeError, ValueError):
+        pass
+    Hkv = cache[0].shape[1] if len(cache) == 4 and cache[0].dim() == 4 else 0
+    _group_check(H, Hkv)
+    kc, kp, vc, vp, pages, page = _cache(cache, dev, Hkv, D)
+    table, per = _pages(page_table, dev, B)
+    return (Hkv, kc, kp, vc, vp, pages, page, table, per,
+            _ptr(length, "length", dev, torch.int32, (B,)))
+
+
 def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
                  softcap: float = 0.0, slopes=None, workspace=None, out=None, lse=None,
                  stream=None):
@@ -462,11 +534,8 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
     cache: length[b] (int32) tokens of sequence b are in it, these included.
     Returns (o, lse)."""
     dev, (B, H, Sq, D) = _rows16(q, "q")
-    Hkv = cache[0].shape[1] if len(cache) == 4 and cache[0].dim() == 4 else 0
-    _group_check(H, Hkv)
-    kc, kp, vc, vp, pages, page = _cache(cache, dev, Hkv, D)
-    table, per = _pages(page_table, dev, B)
-    lp = _ptr(length, "length", dev, torch.int32, (B,))
+    ptrs = _attn_args(cache, page_table, length, dev, B, H, D)
+    Hkv, kc, kp, vc, vp, pages, page, table, per, lp = ptrs
     sp = None
     if slopes is not None:
         sp = _ptr(slopes, "slopes", dev, torch.float32, (H,))
@@ -475,9 +544,9 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
             return fa_fwd_cache(q, cache, page_table, length, scale, softcap, slopes, workspace,
                                 out, lse, stream)
     sc = float(D) ** -0.5 if scale is None else float(scale)
-    L = load()
+    L = _lib or load()
     out, lse = _outputs_on(q, dev, out, lse, stream)
-    ws, ws_bytes = _workspace_of(workspace, dev)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
     args = (q.data_ptr(), kc, kp, vc, vp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Hkv,
             Sq, D, pages, page, per, sc, _DTYPE[q.dtype], softcap, sp)
     handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
