@@ -340,7 +340,8 @@ fa_status_t fa_fwd_score(const void *q, const void *k, const void *v, void *o,
  * x the group's values, limited to +-61440,
  *   z = fp16(min x), s = fp16((max x - min x) / 15),
  *   code = floor((x - z) / s + 1/2) limited to 0 ... 15 (0 where s is 0),
- * rounded to nearest even where fp16 is named, the floor exact.  A NaN makes
+ * rounded to nearest even where fp16 is named (the difference and its fifteenth
+ * to fp32 before), the floor exact.  A NaN makes
  * its group NaN.  The row's little-endian 32-bit word (D / 32) * t + g holds
  * channels 32 g + 8 t ... 32 g + 8 t + 7, lowest first.
  * 0.625 bytes a value: 80 bytes a row at D = 128, of 256 in 16 bits.

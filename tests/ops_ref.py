@@ -82,7 +82,8 @@ def quantise(x):
     rows x: the documented arithmetic, the floor decided in 64 bits."""
     x = x.float().clamp(-61440.0, 61440.0).unflatten(-1, (-1, 32))
     lo, hi = x.amin(-1), x.amax(-1)
-    scale, least = ((hi - lo) / 15).half(), lo.half()
+    # through 64 bits: on a GPU torch divides by 15 as a product, an ulp off at times
+    scale, least = ((hi - lo).double() / 15).float().half(), lo.half()
     s, z = scale.double()[..., None], least.double()[..., None]
     code = torch.floor((x.double() - z) / torch.where(s > 0, s, 1.0) + 0.5).clamp(0, 15)
     code = torch.where((s > 0) & ~torch.isnan(s), code, 0.0)

@@ -140,6 +140,22 @@ def test_ties_constants_extremes_and_nan(dt):
         assert not out[1].isnan().any()
 
 
+@pytest.mark.parametrize("lo,hi,scale", [
+    (-1940.0, -55.15625, 125.625),       # range / 15 = 125.65625, a tie: to even
+    (-86.5, 0.365234375, 5.7890625),     # 5.791015625, a tie
+    (-34784.0, 1711.0, 2432.0),          # 2433, a tie
+    (-61440.0, 61440.0, 8192.0), (-7.5, 7.5, 1.0), (0.0, 2.0 ** -20, 2.0 ** -24)])
+def test_scales_are_rounded_to_nearest_even(lo, hi, scale):
+    x = torch.full((1, 1, 1, 64), lo, device="cuda")
+    x[..., 5] = x[..., 60] = hi
+    x = x.half()
+    cache = fa.fa_cache_empty(1, 1, 16, 64)
+    fa.fa_cache_write(x, x, cache, ints([[0]]))
+    ok()
+    for params in (cache[1], cache[3]):
+        assert params[0, 0, 0].tolist() == [[scale, lo], [scale, lo]]
+
+
 def test_starts_counts_and_what_stays_untouched():
     B, Hkv, S, page, D = 4, 2, 20, 16, 128
     cache, table, k, v = cache_of(B, 100, Hkv, page, D, "bf16", 2)
