@@ -162,7 +162,8 @@ def load_peaks():
 # attention kernels' counters depend on.
 _HOST_ONLY = {"fa_api.cu", "fa_noalloc.cu", "fa_host.h", "fa_diag.cu",
               "fa_score.h", "fa_score.cuh", "fa_score_launch.cuh", "fa_score_d128_bf16.cu",
-              "fa_score_d128_f16.cu", "fa_score_d64_bf16.cu", "fa_score_d64_f16.cu", "fa_score_docs.cu", "fa_score_api.cu",
+              "fa_score_d128_f16.cu", "fa_score_d64_bf16.cu", "fa_score_d64_f16.cu",
+              "fa_score_docs.cu", "fa_score_api.cu",
               "fa_cache.h", "fa_cache.cuh", "fa_cache.cu", "fa_cache_attn.cuh",
               "fa_cache_attn.cu", "fa_cache_api.cu", "fa_merge.h",
               "fa_merge.cuh", "fa_merge.cu"}
