@@ -659,6 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           row.doc_warp = lo == hi && lo >= 0 ? lo : kDocSeveral;
         }
       }
+      // (worked out here: its parts would be more to keep in registers)
+      float* const lse_at =
+          p.n_splits > 1
+              ? p.part_lse + (static_cast<size_t>(it.split) * p.row_heads + it.rh) * p.rows + row_g
+              : p.lse + static_cast<size_t>(it.rh) * p.rows + row_g;
       // reference of the scores (log2 units)
       float m = kCap == kCapFixed ? 0.f : -INFINITY;
       float l = 0.f;        // running sum of 2^(c*s - m)
@@ -690,10 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (stored && !kHalves) {
         // l = 0: no visible key; a NaN stays one
         const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-        if (p.n_splits > 1)
-          p.part_lse[(static_cast<size_t>(it.split) * p.row_heads + it.rh) * p.rows + row_g] = lse;
-        else
-          p.lse[static_cast<size_t>(it.rh) * p.rows + row_g] = lse;
+        *lse_at = lse;
       }
       if (nT > 0) {
         if (!wait_bar_warp(bar(L::O_READY + s), (n_s - 1) & 1, ctl)) { ok = false; break; }
@@ -818,10 +820,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bulk_commit_group();
           }
         }
-        continue;
       }
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int s = kHalves ? 2 : 0; s < 2; ++s) {
         if (!ok) continue;
         const int nT = s == 0 ? it.nT0 : it.nT1;
         const bool have_o = nT > 0;
