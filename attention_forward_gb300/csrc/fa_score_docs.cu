@@ -2,8 +2,8 @@
 // tile the id all of its keys share, per 128-row stage the tiles that hold
 // documents of its rows.
 //
-// Two kernels of one warp a task, each a few dependent loads long (4 bytes a
-// token are read): the id ranges of every key tile and every stage's rows, then
+// One warp a task, two kernels or one (below), each a few dependent loads long (4
+// bytes a token are read): the id ranges of every key tile and every stage's rows, then
 // for every stage the first and last tile whose range meets its own.  Ranges
 // cover any order of ids; documents that lie together make them exact.  As one
 // block per batch row they took 15 us for 16384 tokens.
@@ -16,6 +16,10 @@ namespace fa {
 namespace {
 
 constexpr int kDocWarps = 8;
+// Up to 64 tasks one kernel does both, a launch less on the host: whole calls of
+// 100, 2000, 4000, 8000 tokens (2, 32, 63, 126 tasks) took 8.2, 14.0, 22.7, 28.1 us
+// with it, 8.9, 14.4, 22.4, 26.3 with two.
+constexpr int kDocOneWarps = 32, kDocOneTasks = 64;
 
 __device__ __forceinline__ int2 warp_range(int lo, int hi) {
   return make_int2(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi));
@@ -23,12 +27,7 @@ __device__ __forceinline__ int2 warp_range(int lo, int hi) {
 
 // Tasks 0 ... n_key_tiles - 1: the smallest and largest id >= 0 of a tile's
 // keys, and the id they all have; the others: those of a stage's rows.
-__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_ranges_kernel(const DocParams p) {
-  const int b = static_cast<int>(blockIdx.y), lane = threadIdx.x & 31;
-  const int task = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (task >= p.n_key_tiles + p.n_stages) return;
+__device__ __forceinline__ void doc_range(const DocParams& p, int b, int task, int lane) {
   int lo = INT_MAX, hi = -1, least = INT_MAX;
   if (task < p.n_key_tiles) {
     const int* dk = p.doc_k + static_cast<size_t>(b) * p.Skv;
@@ -78,13 +77,8 @@ __global__ void __launch_bounds__(kDocWarps * 32) fa_doc_ranges_kernel(const Doc
   if (lane == 0) p.stage_tiles[static_cast<size_t>(b) * p.n_stages + s] = r;
 }
 
-// A stage's range of ids, as the kernel before left it, to its range of tiles.
-__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_tiles_kernel(const DocParams p) {
-  const int b = static_cast<int>(blockIdx.y), lane = threadIdx.x & 31;
-  const int s = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (s >= p.n_stages) return;
+// A stage's range of ids, as its task left it, to its range of tiles.
+__device__ __forceinline__ void doc_tiles(const DocParams& p, int b, int s, int lane) {
   int2* stage = p.stage_tiles + static_cast<size_t>(b) * p.n_stages + s;
   const int2* range = p.tile_range + static_cast<size_t>(b) * p.n_key_tiles;
   const int2 mine = *stage;
@@ -101,11 +95,37 @@ __global__ void __launch_bounds__(kDocWarps * 32) fa_doc_tiles_kernel(const DocP
   if (lane == 0) *stage = r.y < 0 ? make_int2(0, 0) : make_int2(r.x, r.y + 1);
 }
 
-cudaError_t launch(void (*kernel)(DocParams), int tasks, const DocParams& p, cudaStream_t stream) {
+__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_ranges_kernel(const DocParams p) {
+  const int task = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (task < p.n_key_tiles + p.n_stages)
+    doc_range(p, static_cast<int>(blockIdx.y), task, threadIdx.x & 31);
+}
+
+__global__ void __launch_bounds__(kDocWarps * 32) fa_doc_tiles_kernel(const DocParams p) {
+  const int s = static_cast<int>(blockIdx.x) * kDocWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (s < p.n_stages) doc_tiles(p, static_cast<int>(blockIdx.y), s, threadIdx.x & 31);
+}
+
+// Both, a block to a batch row.
+__global__ void __launch_bounds__(kDocOneWarps * 32) fa_doc_one_kernel(const DocParams p) {
+  const int b = static_cast<int>(blockIdx.y), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (int task = warp; task < p.n_key_tiles + p.n_stages; task += kDocOneWarps)
+    doc_range(p, b, task, lane);
+  __syncthreads();
+  for (int s = warp; s < p.n_stages; s += kDocOneWarps) doc_tiles(p, b, s, lane);
+}
+
+cudaError_t launch(void (*kernel)(DocParams), int blocks, int warps, const DocParams& p,
+                   cudaStream_t stream) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((tasks + kDocWarps - 1) / kDocWarps),
-                     static_cast<unsigned>(p.B), 1);
-  cfg.blockDim = dim3(kDocWarps * 32, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.B), 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(warps) * 32, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -118,8 +138,11 @@ cudaError_t launch(void (*kernel)(DocParams), int tasks, const DocParams& p, cud
 }  // namespace
 
 cudaError_t launch_doc_tiles(const DocParams& p, cudaStream_t stream) {
-  const cudaError_t e = launch(fa_doc_ranges_kernel, p.n_key_tiles + p.n_stages, p, stream);
-  return e != cudaSuccess ? e : launch(fa_doc_tiles_kernel, p.n_stages, p, stream);
+  const int tasks = p.n_key_tiles + p.n_stages;
+  if (tasks <= kDocOneTasks) return launch(fa_doc_one_kernel, 1, kDocOneWarps, p, stream);
+  auto blocks = [](int n) { return (n + kDocWarps - 1) / kDocWarps; };
+  const cudaError_t e = launch(fa_doc_ranges_kernel, blocks(tasks), kDocWarps, p, stream);
+  return e != cudaSuccess ? e : launch(fa_doc_tiles_kernel, blocks(p.n_stages), kDocWarps, p, stream);
 }
 
 }  // namespace fa
