@@ -22,11 +22,11 @@
 //            the item's rows.  Tiles inside that range without a visible key
 //            are computed and masked (documents that do not lie together).
 //   scores   Tiles where every key is visible to every row of a warp are not
-//            masked.  tanh is an odd polynomial of four terms while every
-//            |x / cap| of the warp's tile is at most 0.5 (off by 2e-7 of the
-//            cap at most; 5 FMA-pipe operations a score), else 1 - 2 / (1 +
-//            e^2x) (an exponential and a reciprocal on the XU: measured 1.4
-//            times the whole kernel's time).  The bias is linear in the column
+//            masked.  tanh is an odd polynomial of four terms where |x / cap|
+//            is at most 0.5 (off by 1.0e-6 of the value at most; 5 FMA-pipe
+//            operations a score), else 1 - 2 / (1 + e^2x) (an exponential and a
+//            reciprocal on the XU: measured 1.4 times the whole kernel's time),
+//            which only tiles with such a score meet.  The bias is linear in the column
 //            on either side of the diagonal; tiles across it take |p - j|.
 //            Document masks are built as 128 bits a row, by one ballot per
 //            distinct document of the warp's rows.
@@ -224,9 +224,37 @@ struct ScoreRow {
 // No tile has this "document": a warp whose rows have several.
 constexpr int kDocSeveral = kDocMixed + 1;
 
+// The exponential form of a capped score, for |s scale / cap| past the
+// polynomial's range: off by about 1e-7 of the cap.
+__device__ __forceinline__ float cap_far(float t, const ScoreParams& p) {
+  const float ex = ex2_approx(t * p.cap_arg);
+  return fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), p.cap_log2);
+}
+
+// Two capped scores, each by the form that holds for it.  Within the polynomial's
+// range they have the bits of a tile without scores past it, so that no other
+// score, of whatever row or of a key that none sees, changes them; there the
+// exponential form would be off by the cap's last digits (0.1 in a score near 0
+// under a cap of 1e6).
+__device__ __forceinline__ void cap_pair(float& x0, float& x1, float a, float b,
+                                         const ScoreParams& p) {
+  const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3];
+  float t0, t1, u0, u1, y0, y1;
+  fmul2(t0, t1, a, b, p.cap_mul, p.cap_mul);
+  fmul2(u0, u1, t0, t1, t0, t1);
+  ffma2(y0, y1, u0, u1, c3, c3, c2, c2);
+  ffma2(y0, y1, y0, y1, u0, u1, c1, c1);
+  ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
+  fmul2(y0, y1, y0, y1, t0, t1);
+  const float f0 = cap_far(t0, p), f1 = cap_far(t1, p);
+  x0 = u0 <= p.cap_u_max ? y0 : f0;
+  x1 = u1 <= p.cap_u_max ? y1 : f1;
+}
+
 // Scores of one tile in log2 units after the cap: x = cap log2(e) tanh(s scale
 // / cap).  The polynomial runs over the registers first; a warp with a score
-// past its range loads the tile again and takes the exponential form.
+// past its range takes its tile through tensor memory once more, each score by
+// its own form.
 __device__ __forceinline__ void cap_tile(uint32_t (&sr)[8][16], uint32_t tS, const ScoreParams& p) {
   float top = 0.f;
   const float c0 = p.cap_poly[0], c1 = p.cap_poly[1], c2 = p.cap_poly[2], c3 = p.cap_poly[3];
@@ -245,19 +273,28 @@ __device__ __forceinline__ void cap_tile(uint32_t (&sr)[8][16], uint32_t tS, con
       sr[cc][e] = __float_as_uint(y0);
       sr[cc][e + 1] = __float_as_uint(y1);
     }
-  if (!__any_sync(0xffffffffu, !(top <= p.cap_u_max))) return;
+  if (!__any_sync(0xffffffffu, !(top <= p.cap_u_fast))) return;
+#pragma unroll 1
+  for (int c = 0; c < kBN; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(tS + c, v);
+    tmem_wait_ld();
+    reg_fence16(v);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {
+      float x0, x1;
+      cap_pair(x0, x1, __uint_as_float(v[e]), __uint_as_float(v[e + 1]), p);
+      v[e] = __float_as_uint(x0);
+      v[e + 1] = __float_as_uint(x1);
+    }
+    tmem_st16(tS + c, v);
+  }
+  tmem_wait_st();
 #pragma unroll
   for (int cc = 0; cc < 8; cc += 2) tmem_ld32(tS + cc * 16, sr[cc], sr[cc + 1]);
   tmem_wait_ld();
 #pragma unroll
   for (int cc = 0; cc < 8; ++cc) reg_fence16(sr[cc]);
-#pragma unroll
-  for (int cc = 0; cc < 8; ++cc)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float ex = ex2_approx(__uint_as_float(sr[cc][e]) * p.cap_arg);
-      sr[cc][e] = __float_as_uint(fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), p.cap_log2));
-    }
 }
 
 // The bits of the columns below the row's limit.
@@ -443,11 +480,14 @@ __device__ __forceinline__ void fixed_columns(const uint32_t (&v)[2][16], uint32
     ffma2(y0, y1, y0, y1, u0, u1, c0, c0);
     fmul2(x[e], x[e + 1], y0, y1, a, b);
   }
+  // (each score by its form here too: 250 us at B4 H16 S4096 D128 causal, 245
+  // with the exponential form for all of the 32 columns)
   if (__any_sync(0xffffffffu, !(top <= p.cap_u_max))) {
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-      const float ex = ex2_approx(__uint_as_float(v[e >> 4][e & 15]) * p.cap_arg);
-      x[e] = fmaf(-2.f * p.cap_log2, __fdividef(1.f, 1.f + ex), p.cap_log2);
+      const float s = __uint_as_float(v[e >> 4][e & 15]);
+      const float far = cap_far(s, p);
+      if (!(fabsf(s) <= p.cap_t_max)) x[e] = far;
     }
   }
   if constexpr (kMasked) {

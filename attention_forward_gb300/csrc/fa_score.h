@@ -31,9 +31,11 @@ struct ScoreParams {
   float scale_log2;           // scale * log2(e)
   int capped;                 // scores have a tanh cap
   int cap_fixed;              // and the cap bounds them: no reference maximum
-  float cap_u_max;            // score^2 up to which the polynomial holds (< 0: none)
-  float cap_poly[kCapTerms];  // log2-scaled score = s * (c0 + c1 s^2 + ...)
-  float cap_arg;              // 2 log2(e) scale / cap
+  float cap_mul;              // t = s * cap_mul: 1, or the scale (plan_cap)
+  float cap_poly[kCapTerms];  // log2-scaled score = t * (c0 + c1 t^2 + ...)
+  float cap_t_max, cap_u_max; // |t| and t^2 up to which the polynomial holds
+  float cap_u_fast;           // the latter where t is s itself, else -1
+  float cap_arg;              // t * cap_arg = 2 log2(e) s scale / cap
   float cap_log2;             // cap * log2(e)
   const float* slopes;        // [H] or null
   const int* prefix;          // [B] or null

@@ -1,7 +1,6 @@
 // fa_score_api.cu -- fa_fwd_score: argument checks, the plan of rows, tiles and
 // key ranges, the tanh coefficients, and the launches.
 #include <algorithm>
-#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -128,37 +127,42 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 // cap tanh(s scale / cap) log2(e) = s (c0 + c1 s^2 + c2 s^4 + c3 s^6) while
 // |s scale / cap| <= y_max.  The terms are the minimax fit (exchange algorithm)
-// of y + a1 y^3 + a2 y^5 + a3 y^7 to tanh on [0, 0.5]: off by 2e-7 at most, by
-// less than 1e-8 up to 0.05, where most scores are.
+// of y + a1 y^3 + a2 y^5 + a3 y^7 to tanh on [0, 0.5]: off by 2e-7 and 1.0e-6 of
+// the value at most, by less than 1e-8 up to 0.05, where most scores are.
 void plan_cap(fa::ScoreParams& p, double scale, double cap, bool bf16) {
   static const double kTanh[fa::kCapTerms] = {1.0, -0.33326461, 0.13185862, -0.0442293};
-  // |y| up to which the terms before i alone are within 2e-7
-  static const double kWithout[fa::kCapTerms] = {0.0, 0.0084, 0.058, 0.17};
+  // |y| up to which the first three alone are within 2e-7 (1.4e-6 of the value)
+  constexpr double kThreeMax = 0.145;
   constexpr double kLog2e = 1.4426950408889634;
   const double k = scale / cap;
-  double y_max = fa::kCapPolyMax;
+  double c[fa::kCapTerms], y_max = fa::kCapPolyMax;
+  bool held = scale < 1e36;  // fp32 holds the terms of s
   for (int i = 0; i < fa::kCapTerms; ++i) {
-    const double pw = std::pow(k, 2 * i);
-    if (pw * scale < 1e-36 && i > 0) {  // below fp32: the cap is far above the scores
-      p.cap_poly[i] = 0.f;
-      y_max = std::min(y_max, kWithout[i]);
-    } else {
-      p.cap_poly[i] = static_cast<float>(kTanh[i] * pw * scale * kLog2e);
-    }
+    c[i] = std::pow(k, 2 * i) * scale;
+    held = held && c[i] < 1e36 && (c[i] > 1e-36 || i == fa::kCapTerms - 1);
   }
-  const double u = (y_max / k) * (y_max / k);
-  p.cap_u_max = static_cast<float>(std::min(u, static_cast<double>(FLT_MAX)));
-  p.cap_arg = static_cast<float>(2.0 * kLog2e * k);
+  if (c[fa::kCapTerms - 1] <= 1e-36) {  // the cap is far above the scores
+    c[fa::kCapTerms - 1] = 0.0;
+    y_max = kThreeMax;
+  }
+  held = held && y_max / k > 1e-18 && y_max / k < 1e18;
+  // else the terms of s scale, which caps of 1e-6 ... 1e6 keep within fp32, behind
+  // a product more, where the exponentials are
+  if (!held) {
+    y_max = fa::kCapPolyMax;
+    for (int i = 0; i < fa::kCapTerms; ++i) c[i] = std::pow(cap, -2 * i);
+  }
+  for (int i = 0; i < fa::kCapTerms; ++i) p.cap_poly[i] = static_cast<float>(kTanh[i] * kLog2e * c[i]);
+  p.cap_mul = held ? 1.f : static_cast<float>(scale);
+  // the product in fp32: |t| <= cap_t_max exactly where t^2 <= cap_u_max
+  p.cap_t_max = static_cast<float>(held ? y_max / k : y_max * cap);
+  p.cap_u_max = p.cap_t_max * p.cap_t_max;
+  p.cap_u_fast = held ? p.cap_u_max : -1.f;
+  p.cap_arg = static_cast<float>(2.0 * kLog2e * (held ? k : 1.0 / cap));
   p.cap_log2 = static_cast<float>(cap * kLog2e);
-  // scores far above the cap: powers of k would leave fp32, and nothing is
-  // left of the polynomial's range
-  if (!(k <= 1e3 && scale <= 1e3)) {
-    std::fill(p.cap_poly, p.cap_poly + fa::kCapTerms, 0.f);
-    p.cap_u_max = -1.f;
-  }
   p.capped = 1;
   // |x| <= 72.5 (a cap of 50) leaves 2^x, its sums and products normal
-  p.cap_fixed = bf16 && !p.slopes && p.cap_log2 <= 72.5f ? 1 : 0;
+  p.cap_fixed = held && bf16 && !p.slopes && p.cap_log2 <= 72.5f ? 1 : 0;
 }
 
 }  // namespace
