@@ -10,12 +10,12 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
-#include <vector>
 
 #include "../../include/fa.h"
 #include "fa_host.h"
 #include "fa_internal.h"
 #include "fa_launch.h"
+#include "fa_workspace.h"
 
 namespace fa {
 
@@ -67,6 +67,17 @@ constexpr int kMaxDevices = 64;
 constexpr unsigned long long kDefaultWatchdogNs = 1000000000ull;
 std::atomic<unsigned long long> g_watchdog_ns{kDefaultWatchdogNs};
 
+struct CudaStreams {
+  using Stream = cudaStream_t;
+  static bool id(cudaStream_t s, unsigned long long* out) {
+    return cudaStreamGetId(s, out) == cudaSuccess;
+  }
+  static bool shared(cudaStream_t s) { return s == cudaStreamPerThread; }
+  static bool alloc(void** p, size_t n) { return cudaMalloc(p, n) == cudaSuccess; }
+  static bool free(void* p) { return cudaFree(p) == cudaSuccess; }
+};
+using Workspaces = fa::StreamWorkspaces<CudaStreams>;
+
 struct DeviceState {
   bool probed = false;
   unsigned long long ctx_id = 0;  // the context the addresses below belong to
@@ -84,21 +95,8 @@ struct DeviceState {
   int pair64_slots[2] = {};  // the 64-key pair kernel; 0: not usable
   bool d64x3_checked[2] = {};
   bool d64x3_ok[2] = {};     // the three-stage D = 64 kernel, per dtype
-  // fa_fwd's workspaces for split partials, one per stream handle (calls on
-  // one stream run in order; calls on different streams may overlap)
-  struct StreamWorkspace {
-    cudaStream_t stream;
-    void* ptr;
-    size_t bytes;
-    // the pair kernel's tail-split arrival counters: a block of their own
-    // (no other call writes it), zeroed when made, and the epoch of the
-    // last launch that used them on this stream
-    unsigned long long* tail_ctr = nullptr;
-    size_t tail_ctr_n = 0;
-    unsigned tail_epoch = 0;
-  };
-  std::vector<StreamWorkspace> workspaces;
-  std::vector<StreamWorkspace> call_workspaces;  // library_workspace's
+  Workspaces workspaces;       // fa_fwd's, for split partials
+  Workspaces call_workspaces;  // library_workspace's
 };
 
 std::mutex g_mu;
@@ -217,25 +215,11 @@ unsigned long long* sched_slot(const DeviceState& d, bool captured) {
 }
 
 // The workspace for `stream` among `all` (a device's), grown to `need` bytes.
-fa_status_t stream_workspace(std::vector<DeviceState::StreamWorkspace>& all, cudaStream_t stream,
-                             size_t need, void** out) {
+fa_status_t stream_workspace(Workspaces& all, cudaStream_t stream, size_t need, void** out) {
   std::lock_guard<std::mutex> lock(g_mu);
-  for (auto& w : all) {
-    if (w.stream != stream) continue;
-    if (w.bytes < need) {
-      cudaFree(w.ptr);  // waits for the work that used it
-      w.ptr = nullptr;
-      w.bytes = 0;
-      if (cudaMalloc(&w.ptr, need) != cudaSuccess) return FA_ERR_CUDA;
-      w.bytes = need;
-    }
-    *out = w.ptr;
-    return FA_OK;
-  }
-  void* ptr = nullptr;
-  if (cudaMalloc(&ptr, need) != cudaSuccess) return FA_ERR_CUDA;
-  all.push_back({stream, ptr, need});
-  *out = ptr;
+  const Workspaces::Entry* w = all.get(stream, need);
+  if (!w) return FA_ERR_CUDA;
+  *out = w->ptr;
   return FA_OK;
 }
 
@@ -246,29 +230,26 @@ fa_status_t stream_workspace(std::vector<DeviceState::StreamWorkspace>& all, cud
 fa_status_t stream_tail_state(DeviceState& d, cudaStream_t stream, size_t part_bytes,
                               size_t n_ctr, void** part, unsigned long long** ctr,
                               unsigned* epoch) {
-  fa_status_t st = stream_workspace(d.workspaces, stream, part_bytes, part);
-  if (st != FA_OK) return st;
   std::lock_guard<std::mutex> lock(g_mu);
-  for (auto& w : d.workspaces) {
-    if (w.stream != stream) continue;
-    if (w.tail_ctr_n < n_ctr) {
-      if (w.tail_ctr) cudaFree(w.tail_ctr);  // waits for the work that used it
-      w.tail_ctr = nullptr;
-      w.tail_ctr_n = 0;
-      void* p = nullptr;
-      if (cudaMalloc(&p, n_ctr * sizeof(unsigned long long)) != cudaSuccess) return FA_ERR_CUDA;
-      w.tail_ctr = static_cast<unsigned long long*>(p);
-      w.tail_ctr_n = n_ctr;
-      if (cudaMemsetAsync(p, 0, n_ctr * sizeof(unsigned long long), stream) != cudaSuccess)
-        return FA_ERR_CUDA;
-      w.tail_epoch = 0;
-    }
-    if (++w.tail_epoch == 0) w.tail_epoch = 1;
-    *ctr = w.tail_ctr;
-    *epoch = w.tail_epoch;
-    return FA_OK;
+  Workspaces::Entry* w = d.workspaces.get(stream, part_bytes);
+  if (!w) return FA_ERR_CUDA;
+  *part = w->ptr;
+  if (w->tail_ctr_n < n_ctr) {
+    if (w->tail_ctr) cudaFree(w->tail_ctr);  // waits for the work that used it
+    w->tail_ctr = nullptr;
+    w->tail_ctr_n = 0;
+    void* p = nullptr;
+    if (cudaMalloc(&p, n_ctr * sizeof(unsigned long long)) != cudaSuccess) return FA_ERR_CUDA;
+    w->tail_ctr = p;
+    w->tail_ctr_n = n_ctr;
+    if (cudaMemsetAsync(p, 0, n_ctr * sizeof(unsigned long long), stream) != cudaSuccess)
+      return FA_ERR_CUDA;
+    w->tail_epoch = 0;
   }
-  return FA_ERR_CUDA;  // stream_workspace made the entry
+  if (++w->tail_epoch == 0) w->tail_epoch = 1;
+  *ctr = static_cast<unsigned long long*>(w->tail_ctr);
+  *epoch = w->tail_epoch;
+  return FA_OK;
 }
 
 // Prefill key splits: only when the (query tile, head) items are fewer than
@@ -865,13 +846,8 @@ fa_status_t fa_release_workspaces(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
   std::lock_guard<std::mutex> lock(g_mu);
   fa_status_t out = FA_OK;
-  for (auto* all : {&d->workspaces, &d->call_workspaces}) {
-    for (auto& w : *all) {
-      if (cudaFree(w.ptr) != cudaSuccess) out = FA_ERR_CUDA;
-      if (w.tail_ctr && cudaFree(w.tail_ctr) != cudaSuccess) out = FA_ERR_CUDA;
-    }
-    all->clear();
-  }
+  for (Workspaces* all : {&d->workspaces, &d->call_workspaces})
+    if (!all->release()) out = FA_ERR_CUDA;
   return out;
 }
 

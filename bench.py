@@ -160,7 +160,7 @@ def load_peaks():
 # workspaces), the device self-check, and the operators that the bench does
 # not run (score-modified attention, the 4-bit cache): not part of what the
 # attention kernels' counters depend on.
-_HOST_ONLY = {"fa_api.cu", "fa_noalloc.cu", "fa_host.h", "fa_diag.cu",
+_HOST_ONLY = {"fa_api.cu", "fa_noalloc.cu", "fa_host.h", "fa_workspace.h", "fa_diag.cu",
               "fa_score.h", "fa_score.cuh", "fa_score_launch.cuh", "fa_score_d128_bf16.cu",
               "fa_score_d128_f16.cu", "fa_score_d64_bf16.cu", "fa_score_d64_f16.cu",
               "fa_score_docs.cu", "fa_score_api.cu",

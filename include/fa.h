@@ -182,14 +182,14 @@ typedef enum {
  * split item) and arrival counters go to the library's workspace for the
  * stream, as fa_fwd's key splits do.  The
  * partials go to a workspace that the library allocates on the first call
- * that needs one, one per (device, stream handle), and keeps until
+ * that needs one, one per (device, stream), and keeps until
  * fa_release_workspaces() or process exit (use fa_fwd_ex to supply your
  * own).  A call that needs a larger workspace than its stream's frees the
  * old one first (cudaFree, which synchronises the device) and allocates
- * the new one.  The cache is keyed on the stream handle: a stream created
- * after another was destroyed may receive the same handle, and would then
- * share that stream's workspace, so call fa_release_workspaces() after
- * destroying streams that fa_fwd used.
+ * the new one.  A stream is known by cudaStreamGetId: every thread's
+ * cudaStreamPerThread has a workspace of its own (kept when the thread ends),
+ * and a stream that received a destroyed one's handle gets a new workspace
+ * when the old one's work is done and its memory is freed.
  * Returns FA_OK once the work is enqueued.
  */
 fa_status_t fa_fwd(const void *q, const void *k, const void *v, void *o,
@@ -312,9 +312,9 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  *              doc_q and doc_k are given); used until the work on `stream`
  *              has finished.  Smaller: the keys are not split, and a call with
  *              documents, whose tile lists need their part of it, returns
- *              FA_ERR_WORKSPACE.  NULL: the library's own for the stream,
- *              also with calls of several host threads; inside a capture
- *              none.
+ *              FA_ERR_WORKSPACE.  NULL: the library's own for the stream
+ *              (kept as fa_fwd's are), also with calls of several host
+ *              threads; inside a capture none.
  * With a workspace it allocates nothing.  May be captured into a CUDA graph
  * (fa_fwd's limits on scheduler slots hold; the workspace is then the graph's to
  * keep).
@@ -416,8 +416,8 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
 
 /*
  * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score and
- * fa_fwd_cache keep for split partials on the current device (one per stream handle it was called
- * with), after synchronising the device.  The next fa_fwd that needs one
+ * fa_fwd_cache keep on the current device (one per stream that they were called
+ * on), after synchronising the device.  The next fa_fwd that needs one
  * allocates it again.  Returns FA_ERR_CUDA if the synchronisation or a free
  * failed (the cache is emptied either way).
  */
