@@ -67,6 +67,7 @@ constexpr int kMaxDevices = 64;
 constexpr unsigned long long kDefaultWatchdogNs = 1000000000ull;
 std::atomic<unsigned long long> g_watchdog_ns{kDefaultWatchdogNs};
 
+// The CUDA calls of the workspaces.
 struct CudaStreams {
   using Stream = cudaStream_t;
   static bool id(cudaStream_t s, unsigned long long* out) {
@@ -76,8 +77,6 @@ struct CudaStreams {
   static bool alloc(void** p, size_t n) { return cudaMalloc(p, n) == cudaSuccess; }
   static bool free(void* p) { return cudaFree(p) == cudaSuccess; }
 };
-using Workspaces = fa::StreamWorkspaces<CudaStreams>;
-
 struct DeviceState {
   bool probed = false;
   unsigned long long ctx_id = 0;  // the context the addresses below belong to
@@ -95,13 +94,14 @@ struct DeviceState {
   int pair64_slots[2] = {};  // the 64-key pair kernel; 0: not usable
   bool d64x3_checked[2] = {};
   bool d64x3_ok[2] = {};     // the three-stage D = 64 kernel, per dtype
-  Workspaces workspaces;       // fa_fwd's, for split partials
-  Workspaces call_workspaces;  // library_workspace's
 };
 
 std::mutex g_mu;
-std::mutex g_call_mu;  // taken before g_mu: see library_workspace
 DeviceState g_dev[kMaxDevices];
+// A device's locks are not held where g_mu is taken.
+using Workspaces = fa::DeviceWorkspaces<CudaStreams, kMaxDevices>;
+Workspaces g_fwd_workspaces;   // fa_fwd's, for split partials
+Workspaces g_call_workspaces;  // library_workspace's
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 
@@ -133,7 +133,11 @@ fa_status_t current_device(DeviceState** out, int* dev_out) {
   const unsigned long long ctx = fa::context_id();
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& d = g_dev[dev];
-  if (d.probed && d.usable == FA_OK && ctx != d.ctx_id) d = DeviceState{};
+  if (d.probed && d.usable == FA_OK && ctx != d.ctx_id) {
+    d = DeviceState{};
+    g_fwd_workspaces.forget(dev);
+    g_call_workspaces.forget(dev);
+  }
   if (!d.probed) {
     int major = 0, minor = 0, sms = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
@@ -165,6 +169,8 @@ fa_status_t current_device(DeviceState** out, int* dev_out) {
   if (dev_out) *dev_out = dev;
   return FA_OK;
 }
+
+int device_index(const DeviceState& d) { return static_cast<int>(&d - g_dev); }
 
 bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
@@ -214,10 +220,10 @@ unsigned long long* sched_slot(const DeviceState& d, bool captured) {
   return next_slot(d.sched, captured);
 }
 
-// The workspace for `stream` among `all` (a device's), grown to `need` bytes.
-fa_status_t stream_workspace(Workspaces& all, cudaStream_t stream, size_t need, void** out) {
-  std::lock_guard<std::mutex> lock(g_mu);
-  const Workspaces::Entry* w = all.get(stream, need);
+// fa_fwd's workspace for `stream` of this device, grown to `need` bytes.
+fa_status_t stream_workspace(const DeviceState& d, cudaStream_t stream, size_t need, void** out) {
+  std::unique_lock<std::mutex> hold;
+  const auto* w = g_fwd_workspaces.acquire(device_index(d), stream, need, &hold);
   if (!w) return FA_ERR_CUDA;
   *out = w->ptr;
   return FA_OK;
@@ -230,8 +236,8 @@ fa_status_t stream_workspace(Workspaces& all, cudaStream_t stream, size_t need, 
 fa_status_t stream_tail_state(DeviceState& d, cudaStream_t stream, size_t part_bytes,
                               size_t n_ctr, void** part, unsigned long long** ctr,
                               unsigned* epoch) {
-  std::lock_guard<std::mutex> lock(g_mu);
-  Workspaces::Entry* w = d.workspaces.get(stream, part_bytes);
+  std::unique_lock<std::mutex> hold;
+  auto* w = g_fwd_workspaces.acquire(device_index(d), stream, part_bytes, &hold);
   if (!w) return FA_ERR_CUDA;
   *part = w->ptr;
   if (w->tail_ctr_n < n_ctr) {
@@ -527,7 +533,7 @@ fa_status_t run_prefill(DeviceState& d, const void* q, const void* k, const void
   p.n_splits = n_splits;
   if (need > 0) {
     if (own_ws) {
-      if ((st = stream_workspace(d.workspaces, stream, need, &ws)) != FA_OK) return st;
+      if ((st = stream_workspace(d, stream, need, &ws)) != FA_OK) return st;
     } else if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) {
       return FA_ERR_WORKSPACE;
     }
@@ -594,7 +600,7 @@ fa_status_t run_decode(DeviceState& d, const void* q, const void* k, const void*
   const size_t need = decode_ws_bytes(BH, n_splits, D);
   if (need > 0) {
     if (own_ws) {
-      const fa_status_t wst = stream_workspace(d.workspaces, stream, need, &ws);
+      const fa_status_t wst = stream_workspace(d, stream, need, &ws);
       if (wst != FA_OK) return wst;
     } else {
       if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
@@ -727,8 +733,10 @@ fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out,
   DeviceState* d = nullptr;
   const fa_status_t st = current_device(&d, nullptr);
   if (st != FA_OK) return st;
-  *hold = std::unique_lock<std::mutex>(g_call_mu);
-  return stream_workspace(d->call_workspaces, stream, need, out);
+  const auto* w = g_call_workspaces.acquire(device_index(*d), stream, need, hold);
+  if (!w) return FA_ERR_CUDA;
+  *out = w->ptr;
+  return FA_OK;
 }
 
 int device_sms() {
@@ -842,12 +850,13 @@ fa_status_t fa_release_workspaces(void) {
   DeviceState* d = nullptr;
   const fa_status_t st = current_device(&d, nullptr);
   if (st != FA_OK) return st;
-  std::lock_guard<std::mutex> calls(g_call_mu);
+  const int dev = device_index(*d);
+  auto calls = g_call_workspaces.lock(dev);
   if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
-  std::lock_guard<std::mutex> lock(g_mu);
+  auto fwd = g_fwd_workspaces.lock(dev);
   fa_status_t out = FA_OK;
-  for (Workspaces* all : {&d->workspaces, &d->call_workspaces})
-    if (!all->release()) out = FA_ERR_CUDA;
+  for (Workspaces* all : {&g_fwd_workspaces, &g_call_workspaces})
+    if (!all->release(dev)) out = FA_ERR_CUDA;
   return out;
 }
 

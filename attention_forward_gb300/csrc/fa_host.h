@@ -50,8 +50,9 @@ unsigned long long* take_sched_slot(const LaunchEnv& env);
 
 // The library's workspace for the score and cache calls on `stream` of the
 // current device, grown to `need` bytes.  Not for captured calls.  `hold` is
-// locked: keep it until the call's launches are all in the stream, so that no
-// other thread's call comes between them or grows the workspace under them.
+// locked (the device's lock): keep it until the call's launches are all in the
+// stream, so that no other thread's call comes between them or grows the workspace
+// under them.
 fa_status_t library_workspace(cudaStream_t stream, size_t need, void** out,
                               std::unique_lock<std::mutex>* hold);
 

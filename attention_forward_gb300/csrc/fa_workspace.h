@@ -2,6 +2,7 @@
 // called on (internal; host only, no CUDA header: Api makes the calls).
 #pragma once
 #include <cstddef>
+#include <mutex>
 #include <vector>
 
 namespace fa {
@@ -63,6 +64,9 @@ class StreamWorkspaces {
     return ok;
   }
 
+  // The memory went away with its context.
+  void forget() { all_.clear(); }
+
  private:
   static bool grow(Entry& e, size_t need) {
     if (e.bytes >= need) return true;
@@ -84,6 +88,37 @@ class StreamWorkspaces {
   }
 
   std::vector<Entry> all_;
+};
+
+// Every device's, each behind a lock of its own: an allocation or a free, which
+// waits for its device, keeps no call on another device waiting.
+template <class Api, int kDevices>
+class DeviceWorkspaces {
+ public:
+  using Streams = StreamWorkspaces<Api>;
+
+  // The entry of a stream of device `dev` (see StreamWorkspaces::get).  `hold` is
+  // locked on return, and no other call gets at the device's entries until it is
+  // given up.
+  typename Streams::Entry* acquire(int dev, typename Api::Stream stream, size_t need,
+                                   std::unique_lock<std::mutex>* hold) {
+    *hold = std::unique_lock<std::mutex>(at_[dev].mu);
+    return at_[dev].streams.get(stream, need);
+  }
+  std::unique_lock<std::mutex> lock(int dev) { return std::unique_lock<std::mutex>(at_[dev].mu); }
+  // With the device's lock held: frees its memory; false if a free failed.
+  bool release(int dev) { return at_[dev].streams.release(); }
+  void forget(int dev) {
+    std::lock_guard<std::mutex> lock(at_[dev].mu);
+    at_[dev].streams.forget();
+  }
+
+ private:
+  struct Device {
+    std::mutex mu;
+    Streams streams;
+  };
+  Device at_[kDevices];
 };
 
 }  // namespace fa

@@ -100,14 +100,74 @@ int main() {
 """
 
 
-def test_one_block_a_stream_known_by_its_id(tmp_path):
+def compile_and_run(tmp_path, program):
     cxx = shutil.which("g++")
     if cxx is None:
         pytest.skip("g++ not found")
     src, exe = tmp_path / "w.cpp", tmp_path / "w"
-    src.write_text(PROGRAM)
-    subprocess.run([cxx, "-std=c++17", "-Wall", "-Wextra", "-Werror", "-I",
+    src.write_text(program)
+    subprocess.run([cxx, "-std=c++17", "-Wall", "-Wextra", "-Werror", "-pthread", "-I",
                     os.path.join(ROOT, "attention_forward_gb300", "csrc"), str(src), "-o", str(exe)],
                    check=True)
-    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_one_block_a_stream_known_by_its_id(tmp_path):
+    compile_and_run(tmp_path, PROGRAM)
+
+
+DEVICES = r"""
+#include <atomic>
+#include <chrono>
+#include <cstdio>
+#include <cstdlib>
+#include <future>
+#include "fa_workspace.h"
+
+static std::atomic<int> frees{0};
+struct Fake {
+  using Stream = long;
+  static bool id(long s, unsigned long long* out) { *out = 1000 + s; return true; }
+  static bool shared(long) { return false; }
+  static bool alloc(void** p, size_t n) { *p = std::malloc(n); return *p != nullptr; }
+  static bool free(void* p) { ++frees; std::free(p); return true; }
+};
+
+#define CHECK(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); std::_Exit(1); } } while (0)
+
+int main() {
+  using namespace std::chrono_literals;
+  static fa::DeviceWorkspaces<Fake, 2> w;
+  auto call = [](int dev) {
+    return std::async(std::launch::async, [dev] {
+      std::unique_lock<std::mutex> hold;
+      CHECK(w.acquire(dev, 7, 100, &hold) != nullptr && hold.owns_lock());
+    });
+  };
+  std::future<void> second;
+  {
+    // a call in progress on device 0: device 1 does not wait, device 0 does
+    std::unique_lock<std::mutex> hold;
+    CHECK(w.acquire(0, 7, 100, &hold) != nullptr && hold.owns_lock());
+    CHECK(call(1).wait_for(20s) == std::future_status::ready);
+    second = call(0);
+    CHECK(second.wait_for(200ms) == std::future_status::timeout);
+  }
+  CHECK(second.wait_for(20s) == std::future_status::ready);
+  // a device's memory alone is freed
+  {
+    auto lock = w.lock(0);
+    CHECK(call(1).wait_for(20s) == std::future_status::ready);
+    CHECK(w.release(0) && frees == 1);
+  }
+  w.forget(1);
+  CHECK(call(1).wait_for(20s) == std::future_status::ready && frees == 1);
+  std::puts("ok");
+  return 0;
+}
+"""
+
+
+def test_a_call_on_one_device_keeps_none_on_another_waiting(tmp_path):
+    compile_and_run(tmp_path, DEVICES)
