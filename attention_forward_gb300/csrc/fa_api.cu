@@ -133,7 +133,8 @@ fa_status_t current_device(DeviceState** out, int* dev_out) {
   const unsigned long long ctx = fa::context_id();
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& d = g_dev[dev];
-  if (d.probed && d.usable == FA_OK && ctx != d.ctx_id) {
+  // (an id of 0 tells nothing: other threads may be using what would be forgotten)
+  if (d.probed && d.usable == FA_OK && ctx != 0 && ctx != d.ctx_id) {
     d = DeviceState{};
     g_fwd_workspaces.forget(dev);
     g_call_workspaces.forget(dev);
@@ -157,8 +158,7 @@ fa_status_t current_device(DeviceState** out, int* dev_out) {
         d.probed = false;
         return FA_ERR_CUDA;
       }
-      // the lookup made the device's context current if it was not yet
-      d.ctx_id = fa::context_id();
+      d.ctx_id = ctx != 0 ? ctx : fa::context_id();
       d.status = static_cast<unsigned*>(addr);
       d.sched = static_cast<unsigned long long*>(sched);
       d.usable = FA_OK;
@@ -687,10 +687,16 @@ unsigned long long context_id() {
   });
   CUcontext ctx = nullptr;
   unsigned long long id = 0;
-  if (!g_ctx_current || !g_ctx_get_id || g_ctx_current(&ctx) != CUDA_SUCCESS || !ctx ||
-      g_ctx_get_id(ctx, &id) != CUDA_SUCCESS)
-    return 0;
-  return id;
+  if (!g_ctx_current || !g_ctx_get_id || g_ctx_current(&ctx) != CUDA_SUCCESS) return 0;
+  if (!ctx) {
+    // a host thread's first call: the runtime makes its device's context current
+    // on the first call that needs one, which cudaGetDevice is not
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess ||
+        g_ctx_current(&ctx) != CUDA_SUCCESS || !ctx)
+      return 0;
+  }
+  return g_ctx_get_id(ctx, &id) == CUDA_SUCCESS ? id : 0;
 }
 
 fa_status_t check_device() {

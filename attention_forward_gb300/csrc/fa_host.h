@@ -28,8 +28,8 @@ inline bool softcap_ok(float c) { return c == 0.f || (c >= 1e-6f && c <= 1e6f); 
 // The current device's support check alone (compute capability 10.3).
 fa_status_t check_device();
 
-// Process-unique id of the calling thread's current CUDA context (0 when
-// there is none).  Device addresses of the library's static __device__
+// Process-unique id of the calling thread's current CUDA context; a thread that
+// has none yet gets its device's (0 when that fails).  Device addresses of the library's static __device__
 // arrays belong to the context that loaded the module: after
 // cudaDeviceReset the primary context is a new one, with a new id, and every
 // cached address must be looked up again.

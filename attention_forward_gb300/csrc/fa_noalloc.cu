@@ -45,7 +45,7 @@ fa_status_t scratch_for_current_device(void** out) {
   const unsigned long long ctx = fa::context_id();
   std::lock_guard<std::mutex> lock(g_mu);
   ScratchAddr& a = g_scratch[dev];
-  if (!a.ptr || a.ctx != ctx) {
+  if (!a.ptr || (ctx != 0 && a.ctx != ctx)) {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_decode_scratch) != cudaSuccess || !p) {
       cudaGetLastError();  // leave no pending error behind
