@@ -49,7 +49,8 @@ cudaError_t launch_prefill(int D, bool bf16, bool corr, const CUtensorMap& q,
 
 namespace {
 
-// Device status word: kernels record FA_ERR_TIMEOUT here.
+// Device status word: kernels record FA_ERR_TIMEOUT here, and the cache's
+// FA_ERR_INVALID_ARG where there is no timeout.
 __device__ unsigned g_status_word;
 
 // Slots of the prefill kernel's item scheduler (see PrefillParams::sched);

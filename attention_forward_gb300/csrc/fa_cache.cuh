@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kCacheCopyThreads, kCacheWriteBlocks)
                           : make_uint4(0u, 0u, 0u, 0u);
     const long long row =
         i < end ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
-    if (i < end && row < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+    if (i < end && row < 0 && lane == 0) atomicMax(p.status, kStatusBadIndex);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       float x[2][8];
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kCacheCopyThreads) fa_cache_read_kernel(const 
     const int i = i0 + k * kRows;
     const long long row =
         i < count ? cache_row(p, b, hk, static_cast<uint32_t>(start) + static_cast<uint32_t>(i)) : -1;
-    if (i < count && row < 0 && lane == 0) atomicExch(p.status, kStatusBadIndex);
+    if (i < count && row < 0 && lane == 0) atomicMax(p.status, kStatusBadIndex);
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       word[k][n] = param[k][n] = 0u;  // a place that does not exist reads as zeros

@@ -13,7 +13,9 @@ constexpr int kCacheGroup = 32;
 // Values beyond this magnitude are held as it: 15 scales above the smallest
 // minimum stay within fp16.
 constexpr float kCacheLimit = 61440.f;
-constexpr unsigned kStatusBadIndex = 1;  // FA_ERR_INVALID_ARG, from a kernel
+// FA_ERR_INVALID_ARG, from a kernel.  Recorded by a maximum: a timeout (5) that
+// another kernel left in the status word is the worse news and stays.
+constexpr unsigned kStatusBadIndex = 1;
 
 // The four arrays of a cache: rows of (page, kv head, slot).
 struct CachePool {

@@ -221,7 +221,7 @@ __device__ __forceinline__ int cache_scan(const CacheAttnParams& p, CacheScan& s
   int sum = 0;
   for (int b = b0; b < b1; ++b) {
     const int len = cache_length(p, b);
-    if (report && len != p.length[b]) atomicExch(p.status, kStatusBadIndex);
+    if (report && len != p.length[b]) atomicMax(p.status, kStatusBadIndex);
     sum += cache_chunks(len);
   }
   int inc = sum;
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kCacheAttnThreads, cache_attn_occupancy(8 * NT
   for (int cur = first; cur < last;) {
   if (p.whole) b = cur / units;
   if (p.whole || cur != first) len = cache_length(p, b);
-  if (p.whole && threadIdx.x == 0 && len != p.length[b]) atomicExch(p.status, kStatusBadIndex);
+  if (p.whole && threadIdx.x == 0 && len != p.length[b]) atomicMax(p.status, kStatusBadIndex);
   const int seq_chunks = cache_chunks(len);
   const int unit = p.whole ? cur - b * units : (cur - before) / seq_chunks;
   const int chunk0 = p.whole ? 0 : cur - before - unit * seq_chunks;
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kCacheAttnThreads, cache_attn_occupancy(8 * NT
       const int key = piece + 16 * i;  // a 16-key tile lies within one page
       const int pg = pages[key >> p.page_shift];
       const bool bad = pg < 0 || pg >= p.num_pages;
-      if (bad) atomicExch(p.status, kStatusBadIndex);
+      if (bad) atomicMax(p.status, kStatusBadIndex);
       sm.rows[i] = bad ? -1
                        : ((static_cast<long long>(pg) * p.Hkv + hk) << p.page_shift) +
                              (key & ((1 << p.page_shift) - 1));

@@ -425,9 +425,12 @@ fa_status_t fa_release_workspaces(void);
 
 /*
  * fa_get_device_status -- synchronises `stream`, then returns and clears the
- * device status word of the current device: FA_OK, or FA_ERR_TIMEOUT if a
- * kernel's bounded wait ran out since the last call.  FA_ERR_CUDA if the
- * synchronisation itself failed.
+ * device status word of the current device.  Since the last call:
+ *   FA_ERR_TIMEOUT      a kernel's bounded wait ran out
+ *   FA_ERR_INVALID_ARG  else, a cache call met a page, position or length
+ *                       that does not exist (the 4-bit cache, above)
+ *   FA_OK               neither
+ * FA_ERR_CUDA if the synchronisation itself failed.
  */
 fa_status_t fa_get_device_status(fa_stream_t stream);
 
