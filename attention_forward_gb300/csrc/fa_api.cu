@@ -221,10 +221,12 @@ unsigned long long* sched_slot(const DeviceState& d, bool captured) {
   return next_slot(d.sched, captured);
 }
 
-// fa_fwd's workspace for `stream` of this device, grown to `need` bytes.
-fa_status_t stream_workspace(const DeviceState& d, cudaStream_t stream, size_t need, void** out) {
-  std::unique_lock<std::mutex> hold;
-  const auto* w = g_fwd_workspaces.acquire(device_index(d), stream, need, &hold);
+// fa_fwd's workspace for `stream` of this device, grown to `need` bytes.  `hold`
+// is locked: keep it until the call's launches are all in the stream, as with
+// library_workspace.
+fa_status_t stream_workspace(const DeviceState& d, cudaStream_t stream, size_t need, void** out,
+                             std::unique_lock<std::mutex>* hold) {
+  const auto* w = g_fwd_workspaces.acquire(device_index(d), stream, need, hold);
   if (!w) return FA_ERR_CUDA;
   *out = w->ptr;
   return FA_OK;
@@ -233,12 +235,11 @@ fa_status_t stream_workspace(const DeviceState& d, cudaStream_t stream, size_t n
 // The tail split's memory for `stream`: its partials in the stream's
 // workspace (grown to `part_bytes`) and `n_ctr` arrival counters, with the
 // launch's epoch.  A new counter block is zeroed on the stream and its
-// epochs start again at 1.
+// epochs start again at 1.  `hold` as in stream_workspace.
 fa_status_t stream_tail_state(DeviceState& d, cudaStream_t stream, size_t part_bytes,
                               size_t n_ctr, void** part, unsigned long long** ctr,
-                              unsigned* epoch) {
-  std::unique_lock<std::mutex> hold;
-  auto* w = g_fwd_workspaces.acquire(device_index(d), stream, part_bytes, &hold);
+                              unsigned* epoch, std::unique_lock<std::mutex>* hold) {
+  auto* w = g_fwd_workspaces.acquire(device_index(d), stream, part_bytes, hold);
   if (!w) return FA_ERR_CUDA;
   *part = w->ptr;
   if (w->tail_ctr_n < n_ctr) {
@@ -397,11 +398,12 @@ fa_status_t run_prefill_pair(DeviceState& d, const void* q, const void* k, const
   const int tail = k64 || captured || !(flags & FA_FLAG_TAIL_SPLIT) ||
                            (flags & FA_FLAG_CORRECTION_WG)
                        ? 0 : pair_tail_items(n_items, n_pairs, causal, Skv);
+  std::unique_lock<std::mutex> hold;
   if (tail > 0) {
     if (n_items + 3LL * tail > 0x7fffffffLL) return FA_ERR_INVALID_ARG;
     void* part = nullptr;
     if ((st = stream_tail_state(d, stream, tail_part_bytes(tail), static_cast<size_t>(tail) * 16,
-                                &part, &p.tail_count, &p.tail_epoch)) != FA_OK)
+                                &part, &p.tail_count, &p.tail_epoch, &hold)) != FA_OK)
       return st;
     p.part_o = static_cast<float*>(part);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(part) + tail_part_o_bytes(tail));
@@ -532,9 +534,10 @@ fa_status_t run_prefill(DeviceState& d, const void* q, const void* k, const void
     need = 0;
   }
   p.n_splits = n_splits;
+  std::unique_lock<std::mutex> hold;
   if (need > 0) {
     if (own_ws) {
-      if ((st = stream_workspace(d, stream, need, &ws)) != FA_OK) return st;
+      if ((st = stream_workspace(d, stream, need, &ws, &hold)) != FA_OK) return st;
     } else if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) {
       return FA_ERR_WORKSPACE;
     }
@@ -599,9 +602,10 @@ fa_status_t run_decode(DeviceState& d, const void* q, const void* k, const void*
   const int kps = decode_keys_per_split(BH, Skv, d.sm_count, num_splits);
   const int n_splits = (Skv + kps - 1) / kps;
   const size_t need = decode_ws_bytes(BH, n_splits, D);
+  std::unique_lock<std::mutex> hold;
   if (need > 0) {
     if (own_ws) {
-      const fa_status_t wst = stream_workspace(d, stream, need, &ws);
+      const fa_status_t wst = stream_workspace(d, stream, need, &ws, &hold);
       if (wst != FA_OK) return wst;
     } else {
       if (!ws || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))
