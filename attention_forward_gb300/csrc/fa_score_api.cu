@@ -174,6 +174,16 @@ extern "C" size_t fa_score_workspace_bytes(int B, int H, int Hkv, int Sq, int Sk
   return p.doc_bytes + p.split_bytes;
 }
 
+extern "C" int fa_score_item_rows(int B, int H, int Hkv, int Sq, int Skv, int D) {
+  if (!sizes_ok(B, H, Hkv, Sq, Skv) || (D != 64 && D != 128)) return 0;
+  return make_plan(B, H, Hkv, Sq, Skv, D, false, fa::device_sms()).halves ? fa::kBM : fa::kRowsPerCta;
+}
+
+extern "C" int fa_score_key_ranges(int B, int H, int Hkv, int Sq, int Skv, int D) {
+  if (!sizes_ok(B, H, Hkv, Sq, Skv) || (D != 64 && D != 128)) return 0;
+  return make_plan(B, H, Hkv, Sq, Skv, D, false, fa::device_sms()).n_splits;
+}
+
 extern "C" fa_status_t fa_fwd_score(const void* q, const void* k, const void* v, void* o,
                                     float* lse, int B, int H, int Hkv, int Sq, int Skv, int D,
                                     float scale, int causal, int dtype, float softcap,

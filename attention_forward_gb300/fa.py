@@ -94,6 +94,10 @@ def load_path(path: str) -> ctypes.CDLL:
     L.fa_prefill_tail_items.restype = ci
     L.fa_score_workspace_bytes.argtypes = [ci] * 7
     L.fa_score_workspace_bytes.restype = sz
+    L.fa_score_item_rows.argtypes = [ci] * 6
+    L.fa_score_item_rows.restype = ci
+    L.fa_score_key_ranges.argtypes = [ci] * 6
+    L.fa_score_key_ranges.restype = ci
     L.fa_fwd_score.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, ci, cf,
                                vp, vp, vp, vp, vp, sz, vp]
     L.fa_fwd_score.restype = ci
@@ -325,6 +329,17 @@ def _graph_workspace(call, need: int, device, stream) -> int:
 def fa_score_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, Skv: int, D: int,
                              documents: bool = False) -> int:
     return int(load().fa_score_workspace_bytes(B, H, Hkv, Sq, Skv, D, int(bool(documents))))
+
+
+def fa_score_item_rows(B: int, H: int, Hkv: int, Sq: int, Skv: int, D: int) -> int:
+    """Rows of a work item of fa_fwd_score at these sizes: 256, or 128 whose key
+    tiles an item's two stages share."""
+    return int(load().fa_score_item_rows(B, H, Hkv, Sq, Skv, D))
+
+
+def fa_score_key_ranges(B: int, H: int, Hkv: int, Sq: int, Skv: int, D: int) -> int:
+    """Ranges that fa_fwd_score splits an item's keys into at these sizes."""
+    return int(load().fa_score_key_ranges(B, H, Hkv, Sq, Skv, D))
 
 
 def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,

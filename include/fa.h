@@ -328,6 +328,15 @@ fa_status_t fa_fwd_score(const void *q, const void *k, const void *v, void *o,
                          const int *doc_k, const int *prefix, void *workspace,
                          size_t workspace_bytes, fa_stream_t stream);
 
+/* How fa_fwd_score runs a call of these sizes (argument values that it refuses
+ * give 0).  fa_score_item_rows: the rows of a work item, 256 (a stage of 128
+ * each) or, where 256 would leave multiprocessors idle, 128 whose key tiles the
+ * two stages share.  fa_score_key_ranges: the ranges that an item's keys are
+ * split into when the workspace has room for their partials; 1: not split.
+ * Read the current device's SM count (152 without a device); launch nothing. */
+int fa_score_item_rows(int B, int H, int Hkv, int Sq, int Skv, int D);
+int fa_score_key_ranges(int B, int H, int Hkv, int Sq, int Skv, int D);
+
 /*
  * The 4-bit key/value cache: fa_cache_write, fa_cache_read, fa_fwd_cache.
  *
