@@ -439,10 +439,11 @@ __global__ void __launch_bounds__(kCacheAttnThreads, cache_attn_occupancy(8 * NT
     }
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // up = 2^e with top * up in [2^13, 2^14), an all-zero row's 1.  The bounds
-    // keep up and 2^24 / up floats; a row past 2^113 overflows to NaN
-    int e2 = top > 0.f && top < INFINITY ? 13 - ilogbf(top) : 0;
-    e2 = min(max(e2, -100), 120);
+    // up = 2^e with top * up in [2^13, 2^14); e is at least 13 - 127, and at most
+    // 120, as for an all-zero row, so that 1 / up is a float and its scores are 0
+    // under any scale
+    int e2 = top > 0.f ? (top < INFINITY ? 13 - ilogbf(top) : 0) : 120;
+    e2 = min(e2, 120);
     const float up = __int_as_float((127 + e2) << 23);
     float part[G];
 #pragma unroll
@@ -471,13 +472,15 @@ __global__ void __launch_bounds__(kCacheAttnThreads, cache_attn_occupancy(8 * NT
     const __half lo = __float2half_rn(sum - __half2float(hi));
     qs[n][0] = static_cast<uint32_t>(__half_as_ushort(hi)) << 16;
     qs[n][1] = static_cast<uint32_t>(__half_as_ushort(lo)) << 16;
-    // what a sum is multiplied by: 2^24 (the codes') / up, the scale, and
-    // log2(e) unless the cap comes between
-    const float down = __int_as_float((127 + 24 - e2) << 23);
+    // what a sum is multiplied by: 1 / up, the scale, then 2^24 (the codes') and
+    // log2(e) unless the cap comes between; in this order it overflows only where
+    // the scores do
+    const float down = __int_as_float((127 - e2) << 23);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int rc = 8 * n + 2 * t + c;
-      fac[n][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * (kMod && p.cap > 0.f ? p.scale : p.scale * kLog2e);
+      fac[n][c] = __shfl_sync(0xffffffffu, down, (2 * t + c) * 4) * p.scale *
+                  (kMod && p.cap > 0.f ? 16777216.f : 16777216.f * kLog2e);
       const int rr = min(rc, n_rows - 1) + row0;
       const int h = hk * (p.H / p.Hkv) + rr / p.Sq, i = rr % p.Sq;
       slope[n][c] = kMod && p.slopes ? p.slopes[h] * kLog2e : 0.f;
