@@ -15,7 +15,7 @@
 // by its instructions (16 a value at first, most of them of the ALU pipe): a
 // thread takes 16 channels, so that two lanes share a group's parameters.
 // 32 x 8 heads of 4096 tokens, D = 128, 705 MB: write 144 us in bf16 (4.9 TB/s of
-// 6.8), 126 in fp16, whose grid has fewer ties; read 111 us (6.3 TB/s).  With 8
+// 6.8), 126 in fp16, whose grid has fewer ties; read 112 us (6.3 TB/s), 108 in fp16.  With 8
 // channels a lane, every tie and limit looked at in place: 218 us.
 #pragma once
 #include <cuda_bf16.h>
@@ -223,31 +223,65 @@ __device__ __forceinline__ void cache_quantise(const float (&x)[2][8], uint32_t 
                                  x[h][7], z, s);
 }
 
+// Two codes at a time are cut out as fp16 pairs (channels e, e + 4): a code
+// masked into the low or high nibble of a fp16 mantissa is 1024 or 64 too large.
+__device__ __forceinline__ __half2 cache_code_pair(uint32_t word, int e) {
+  const uint32_t w = e & 2 ? word >> 8 : word;
+  const uint32_t bits = e & 1 ? (w & 0x00f000f0u) | 0x54005400u : (w & 0x000f000fu) | 0x64006400u;
+  return __hsub2(*reinterpret_cast<const __half2*>(&bits), __float2half2_rn(e & 1 ? 64.f : 1024.f));
+}
+
+// Pairs (e, e + 4) in the order of their channels.
+__device__ __forceinline__ uint4 cache_in_order(const uint32_t (&v)[4]) {
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
+                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+}
+
+// c s + z rounded to odd: rounded again to bf16, that is c s + z rounded once,
+// where rounding it to nearest first could make a tie of it.
+__device__ __forceinline__ float fma_odd(float c, float s, float z) {
+  const float lo = __fmaf_rd(c, s, z), hi = __fmaf_ru(c, s, z);
+  return (__float_as_uint(lo) & 1u) ? lo : hi;
+}
+
+// cache_values in bf16 where fp32 does not hold the sums.  (Out of line: its
+// registers are not the kernel's.  A template, for the linker.)
+template <int kUnused = 0>
+__device__ __noinline__ uint4 cache_values_odd(uint32_t word, float s, float z) {
+  uint32_t v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2 c = cache_code_pair(word, e);
+    v[e] = cache_pack<true>(fma_odd(__low2float(c), s, z), fma_odd(__high2float(c), s, z));
+  }
+  return cache_in_order(v);
+}
+
 // The 8 values of a word, rounded once to 16 bits, in the order of their
-// channels.  Two codes at a time are cut out as fp16 pairs (channels e, e + 4):
-// a code masked into the low or high nibble of a fp16 mantissa is 1024 or 64
-// too large.
+// channels.
 template <bool BF16>
 __device__ __forceinline__ uint4 cache_values(uint32_t word, uint32_t param) {
   const __half2 sz = *reinterpret_cast<const __half2*>(&param);
-  const uint32_t y = word >> 8;
-  const uint32_t bits[4] = {(word & 0x000f000fu) | 0x64006400u, (word & 0x00f000f0u) | 0x54005400u,
-                            (y & 0x000f000fu) | 0x64006400u, (y & 0x00f000f0u) | 0x54005400u};
   uint32_t v[4];  // channels (e, e + 4)
+  if constexpr (BF16) {
+    const float s = __low2float(sz), z = __high2float(sz);
+    // c s + z is exact in fp32 where its last place, at least 2^-11 of the smaller
+    // of s and |z|, is within 2^-23 of |z| + 16 s: nearly always (705 MB in 112 us;
+    // 121 with every group by fma_odd, 114 with both in line, 110 rounding twice)
+    if (fminf(s, fabsf(z)) * 4096.f < fmaf(16.f, s, fabsf(z))) return cache_values_odd<>(word, s, z);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&bits[e]),
-                              __float2half2_rn(e & 1 ? 64.f : 1024.f));
-    if constexpr (BF16) {
-      const float s = __low2float(sz), z = __high2float(sz);
+    for (int e = 0; e < 4; ++e) {
+      const __half2 c = cache_code_pair(word, e);
       v[e] = cache_pack<true>(fmaf(__low2float(c), s, z), fmaf(__high2float(c), s, z));
-    } else {
-      const __half2 r = __hfma2(c, __low2half2(sz), __high2half2(sz));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 r = __hfma2(cache_code_pair(word, e), __low2half2(sz), __high2half2(sz));
       v[e] = *reinterpret_cast<const uint32_t*>(&r);
     }
   }
-  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                    __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
+  return cache_in_order(v);
 }
 
 // Rows per block: the lanes of a row lie side by side.  blockIdx.y is the
