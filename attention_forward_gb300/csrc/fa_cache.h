@@ -64,6 +64,7 @@ int cache_attn_row_block(int rows);
 constexpr int kCacheAttnWarps = 4;
 constexpr int kCacheAttnKeys = 16 * kCacheAttnWarps;  // a chunk of the work: a tile for each warp
 constexpr int kCacheAttnStages = 3;                   // tiles of a warp's ring
+constexpr long long kCacheMaxChunks = 0x7fffff00;     // of a call: an int's, and room to round up
 constexpr int kCachePiece = 4096;  // keys whose tiles' places are in shared memory at once
 // CTAs an SM holds: the registers of 16 accumulated rows are more.
 constexpr int cache_attn_occupancy(int row_block) { return row_block == 8 ? 4 : 3; }

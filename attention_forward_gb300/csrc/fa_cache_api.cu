@@ -82,6 +82,16 @@ fa_status_t copy(bool write, const void* const (&pool)[4], const void* k, const 
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// The attention counts chunks of keys in an int, by the table's room: the lengths
+// are the device's to read.
+bool chunks_ok(int B, int H, int Hkv, int Sq, const PageShape& s) {
+  const long long rows = static_cast<long long>(H / Hkv) * Sq;
+  const int block = fa::cache_attn_row_block(static_cast<int>(rows));
+  const long long chunks = (static_cast<long long>(s.max_pages) * s.page_size +
+                            fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys;
+  return static_cast<long long>(B) * Hkv * ((rows + block - 1) / block) * chunks <= fa::kCacheMaxChunks;
+}
+
 // The attention's persistent CTAs and the memory for their parts.
 struct AttnPlan {
   int row_blocks, grid, whole;
@@ -129,7 +139,7 @@ size_t fa_cache_workspace_bytes(int B, int H, int Hkv, int Sq, int D, int page_s
                                 int max_pages) {
   const PageShape s{1, page_size, max_pages};
   if (B < 1 || H < 1 || Hkv < 1 || Sq < 1 || Sq > 256 || H % Hkv != 0 || (D != 64 && D != 128) ||
-      static_cast<long long>(B) * H >= 65536 || !pages_ok(s))
+      static_cast<long long>(B) * H >= 65536 || !pages_ok(s) || !chunks_ok(B, H, Hkv, Sq, s))
     return 0;
   return plan_attn(B, H, Hkv, Sq, D, s, fa::device_sms()).bytes;
 }
@@ -147,17 +157,13 @@ fa_status_t fa_fwd_cache(const void* q, const void* k_codes, const void* k_param
   if (!q || !o || !lse || !length || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16) ||
       !aligned(length, 4) || !aligned(slopes, 4))
     return FA_ERR_INVALID_ARG;
-  if (Sq > 256) return FA_ERR_INVALID_ARG;
+  if (Sq > 256 || !chunks_ok(B, H, Hkv, Sq, s)) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   if (!fa::softcap_ok(softcap)) return FA_ERR_INVALID_ARG;
   cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
   fa::LaunchEnv env{};
   if ((st = fa::launch_env(strm, &env)) != FA_OK) return st;
   const AttnPlan plan = plan_attn(B, H, Hkv, Sq, D, s, env.sm_count);
-  // the kernel counts chunks of keys in an int
-  if (static_cast<long long>(B) * Hkv * plan.row_blocks *
-          ((max_pages * page_size + fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys) > 0x7fffff00LL)
-    return FA_ERR_INVALID_ARG;
   std::unique_lock<std::mutex> hold;
   if (plan.bytes > 0 && !workspace && !env.captured) {
     if ((st = fa::library_workspace(strm, plan.bytes, &workspace, &hold)) != FA_OK) return st;

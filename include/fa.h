@@ -393,7 +393,13 @@ fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
 
 /*
  * fa_fwd_cache -- attention of the newest tokens over the cache.
- *   q, o [B, H, Sq, D], lse [B, H, Sq]; Hkv divides H; 1 <= Sq <= 256
+ *   q, o [B, H, Sq, D], lse [B, H, Sq]; Hkv divides H; 1 <= Sq <= 256.
+ *   The keys are dealt in chunks of 64, counted in 31 bits by the room of the
+ *   page table: with rows = (H / Hkv) * Sq,
+ *   B * Hkv * ceil(rows / (rows <= 8 ? 8 : 16)) * ceil(max_pages * page_size / 64)
+ *   is at most 2^31 - 256 (beyond it FA_ERR_INVALID_ARG, and
+ *   fa_cache_workspace_bytes returns 0): 8191 blocks of rows at room for 2^24
+ *   keys.
  *   length  [B] int32: tokens of sequence b in the cache, these Sq included;
  *           query row i sees keys j <= length[b] - Sq + i.  A length of 0, or
  *           a row that comes before key 0, sees nothing (O = 0, LSE = -inf).
