@@ -349,7 +349,9 @@ def fa_fwd_score(q, k, v, causal: bool = False, scale: float | None = None,
     v [B, Hkv, Skv, D].  ``softcap`` caps the scores by a tanh, ``slopes``
     (float32 [H]) takes slope * distance off them, ``doc_q`` / ``doc_k``
     (int32 [B, Sq], [B, Skv]) keep rows to keys of their document, ``prefix``
-    (int32 [B], causal only) shows the first keys to every row.  Without
+    (int32 [B], causal only) shows the first keys to every row.  In bfloat16
+    under a cap of at most 50, v is taken up to 2^30 in magnitude (below 2^-50 it
+    may count as 0), unless ``slopes``, zeros if need be, are given.  Without
     ``workspace`` the library's own for the stream serves (a captured call gets
     one of the graph's memory).  Returns (o, lse)."""
     dev, (B, H, Sq, D) = _rows16(q, "q")

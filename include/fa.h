@@ -292,6 +292,8 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  *   softcap  0: no cap; else 1e-6 ... 1e6.  With bf16, no slopes and a cap up
  *            to 50 (its probabilities are summed unshifted) values of V are
  *            taken up to 2^30 in magnitude, and below 2^-50 may count as 0.
+ *            Slopes of 0 give such a call the running maximum of the other
+ *            forms, and V the range that it has in fa_fwd.
  *   slopes   [H] fp32 (finite), or NULL
  *   doc_q    [B, Sq] int32, doc_k [B, Skv] int32: the document of every query
  *            and key, both given or both NULL.  A negative id belongs to no
