@@ -72,9 +72,13 @@ constexpr int cache_attn_occupancy(int row_block) { return row_block == 8 ? 4 : 
 // sequence of 2048 keys, 8 kv heads: 7.4 us by 4 chunks, 9.0 by 8, 12.8 by 12; of
 // 32768: 18.6, 17.3, 18.7).
 constexpr int kCacheMinChunks = 4;
-// Page tables of at most this many keys are not split: 4 x 16 heads of 701 keys
-// took 10.3 us split and merged, 10.0 whole, and one launch less; 8 heads of 2048
-// keys 7.4 us split, 17.2 whole.
+// Page tables of at most this many keys are not split, which saves the merge's
+// launch.  On the GPU, units of 4 rows, us, whole and split: 512 keys 7.0 and 7.1
+// (1 unit), 7.2 and 8.1 (64), 8.9 and 11.7 (256); 1000 keys 10.6 and 7.0 (1), 10.3
+// and 7.5 (8), 10.7 and 9.2 (64), 10.9 and 12.0 (128), 13.6 and 17.3 (256); 4 x 16
+// heads of 701 keys 10.0 and 10.3; 2048 keys, 8 units, 17.2 and 7.4.  So few units of
+// more than 512 keys lose up to 3.5 us in a graph; called from the host, one launch
+// less pays for it (8 units of 1000 keys: 17.3 us a call whole, 19.7 split).
 constexpr int kCacheWholeKeys = 1024;
 // CTAs for `units` row blocks of up to `room` keys.
 int cache_attn_grid(int rows, long long units, int room, int sm_count);

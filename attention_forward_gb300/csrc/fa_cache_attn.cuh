@@ -10,19 +10,20 @@
 //     c 2^-24 (bits 0-3) or c 2^-20 (bits 4-7), exact, so a word of 8 codes
 //     becomes four A registers with one shift and four ANDs.  B is the query
 //     row, scaled by a power of two that puts its largest element in
-//     [2^13, 2^14) (bf16 queries become fp16 exactly), times 2^-4 opposite the
-//     2^-20 codes.  A group's 32 channels are two such products; its scale
+//     [2^13, 2^14), times 2^-4 opposite the 2^-20 codes.  (Exact down to 2^-26 of
+//     the row's largest channel in bf16 and 2^-23 in fp16, off by at most 2^-34 of
+//     that below.)  A group's 32 channels are two such products; its scale
 //     multiplies their fp32 sums.  The minima come from one more product:
 //     A = the stored (scale, minimum) pairs, B = (0, sum of the group's query
-//     channels), that sum in two fp16 parts.  The scores lose nothing to
-//     rounding before the fp32 sums.
+//     channels), that sum in two fp16 parts, to 2^-22 of itself.
 //   softmax: fp32, log2 domain, one reference maximum per row, raised when a
 //     score passes it by 15: p = 2^(t - m) <= 2^15 with m set 8 below the
 //     maximum, so that fp16 holds p over 2^-24 ... 2^15 around it.
 //   output, channels x rows: A = the values, dequantised to fp16 pairs of two
 //     tokens ((1024 + c) - 1024 or (64 + c) - 64, then one fma with scale and
 //     minimum: a rounding of 2^-11 of the value, an eighth of bf16's), B = p
-//     in fp16 (2^-11), turned from the score layout by movmatrix.
+//     in fp16 (2^-11), turned from the score layout by movmatrix.  Both are what
+//     the product's 16-bit operands hold; the sums are fp32.
 //
 // A warp copies its tiles (16 keys: 2560 bytes at D = 128) into a ring of its own
 // in shared memory with 16-byte asynchronous copies, kCacheAttnStages tiles

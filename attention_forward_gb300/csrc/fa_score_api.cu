@@ -55,7 +55,12 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 // causal, with a cap: 8 heads of one token over 700 keys 12.6 whole, 9.9 split; of
 // 128 over 2048 23.0 and 12.8; 2 x 8 heads of 1021 x 1500 27.6 with 256 rows, 19.9
 // in halves; 16 of 1024 x 4096 52.6 (in 2 ranges) and 39.0; 8 of 2048 x 2048 34.1
-// and 23.5 (105 in 16 ranges).
+// and 23.5 (105 in 16 ranges).  Several items an SM, D = 128, 256 rows and halves:
+// 352 heads of 300 42.4 and 35.7; 128 of 800 47.5 and 45.4; 640 of 300 x 1000 167 and
+// 169 (D = 64 153 and 118); and where 256 rows are taken, 1024 heads of 400 111 and
+// 138, 1024 of 148 x 1000 138 and 183, but 1024 of 300 102 and 90: a last item of few
+// rows costs more than the rounds say.  Every key tile counts as visible, those that
+// documents rule out included: their ids are the device's to read.
 struct Cut {
   int halves, splits;
   long long cost;

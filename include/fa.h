@@ -304,7 +304,8 @@ fa_status_t fa_fwd_decode_static(const void *q, const void *k, const void *v,
  * These arrays are device memory, 4-byte aligned.  A row with no visible key
  * gets O = 0 and LSE = -inf.  A masked key's K may hold anything; V must be
  * finite in every row (a masked key's weight is an exact 0, and 0 * inf is
- * NaN).
+ * NaN).  As in fa_fwd, a probability is rounded to the type of V for its
+ * product with V, but not in the row's sum; scores and statistics are fp32.
  * Supported: fa_fwd's D, types and limits (B * H < 65536, Sq, Skv <= 2^24).
  * Up to 128 query tokens, the heads of a group run as rows of one tile, so a
  * single token of H heads reads K and V once.  Few row tiles split the keys,
@@ -416,6 +417,8 @@ fa_status_t fa_cache_read(const void *k_codes, const void *k_params,
  *           returns FA_ERR_WORKSPACE without.
  * The keys of all sequences are dealt evenly to the GPU's multiprocessors by
  * the lengths that the device finds, ragged batches and replays included.
+ * For the product with V, values and probabilities are rounded to fp16; scores
+ * and statistics are fp32.
  * Meant for single tokens and the few of a draft: every 8 or 16 query rows of
  * a kv head read its keys again.  For longer blocks read the cache back and
  * call fa_fwd_score.
