@@ -34,11 +34,11 @@ class Server:
         fa.fa_cache_write(k, v, self.cache, self.table)
         self.host = [torch.empty((B, n, 1, D), dtype=torch.bfloat16, pin_memory=True) for n in (H, Hkv, Hkv)]
         self.q, self.k, self.v = (torch.empty_like(t, device="cuda") for t in self.host)
-        self.o, self.lse = torch.empty_like(self.q), torch.empty((B, H, 1), device="cuda")
-        self.back = torch.empty((B, H, 1, D), dtype=torch.bfloat16, pin_memory=True)
-        self.part = [torch.empty((B, Hkv, L, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        self.o, self.lse = torch.zeros_like(self.q), torch.zeros((B, H, 1), device="cuda")
+        self.back = torch.zeros((B, H, 1, D), dtype=torch.bfloat16, pin_memory=True)
+        self.part = [torch.zeros((B, Hkv, L, D), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
         self.qp = rand(3, B, H, 40, D).cuda()
-        self.op, self.lp = torch.empty_like(self.qp), torch.empty((B, H, 40), device="cuda")
+        self.op, self.lp = torch.zeros_like(self.qp), torch.zeros((B, H, 40), device="cuda")
         self.ids = torch.arange(L, device="cuda").div(200, rounding_mode="floor").int().expand(B, L).contiguous()
         self.dq = self.ids[:, L - 40:].contiguous()
         torch.cuda.synchronize()
@@ -89,7 +89,6 @@ def same(a, b):
 def test_copies_and_memsets_between_captured_calls():
     direct, replayed = Server(), Server()
     for s in (direct, replayed):
-        s.back.zero_(), s.op.zero_(), s.lp.zero_()
         s.inputs(0)
         s.step()
     assert same(direct.outputs(), replayed.outputs())
