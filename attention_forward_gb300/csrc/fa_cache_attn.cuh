@@ -41,6 +41,7 @@
 
 #include "fa_cache.cuh"
 #include "fa_cache.h"
+#include "fa_keys.cuh"
 #include "fa_merge.cuh"
 #include "sm103_ptx.cuh"
 
@@ -106,18 +107,6 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t b
   return d;
 }
 
-// cap tanh(x / cap): for |y| = |x / cap| < 1/4 the odd series through y^7 (its
-// next term is 3e-7 of the value), else 1 - 2 / (1 + e^(2 y)), which is off by
-// a few 2^-24 of the cap and saturates to +-cap as the exponential reaches
-// infinity or 0.
-__device__ __forceinline__ float cap_score(float x, const CacheAttnParams& p) {
-  const float y = x * p.inv_cap, u = y * y;
-  const float small = fmaf(u, fmaf(u, fmaf(u, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f) * x;
-  const float e = ex2_approx(x * p.cap_arg);
-  const float large = fmaf(-2.f * p.cap, __fdividef(1.f, 1.f + e), p.cap);
-  return u < 0.0625f ? small : large;
-}
-
 // A 16-key tile in shared memory: the 16 rows' codes and parameters of K, then
 // of V, as they lie in the pool.
 template <int D>
@@ -171,100 +160,8 @@ __device__ __forceinline__ void copy_tile(uint32_t dst, const CacheLane& c, long
   if (c.has_par) cp_async16(dst + c.par_dst, c.par + row * T::kPar);
 }
 
-// ---- how the work is dealt to the CTAs (the merge kernel uses it too) ----
-
-// A sequence's length, limited to what its page table can hold.
-__device__ __forceinline__ int cache_length(const CacheAttnParams& p, int b) {
-  return max(0, min(p.length[b], p.max_pages << p.page_shift));
-}
-
-// Chunks of a unit of that length; one without keys is a chunk all the same.
-__device__ __forceinline__ int cache_chunks(int len) {
-  return max(1, (len + kCacheAttnKeys - 1) / kCacheAttnKeys);
-}
-
-// All C chunks dealt to n CTAs: C / n each, the first C % n one more.  C < 2^31
-// (fa_fwd_cache checks it).
-struct CacheDeal {
-  int n, per, more;
-  __device__ __forceinline__ int begin(int x) const { return x * per + min(x, more); }
-  __device__ __forceinline__ int cta_of(int c) const {
-    const int big = more * (per + 1);  // chunks of the CTAs that have one more
-    return c < big ? c / (per + 1) : more + (c - big) / per;
-  }
-};
-
-// At least kCacheMinChunks chunks to a CTA.
-__device__ __forceinline__ CacheDeal cache_deal(int all, int grid) {
-  CacheDeal d;
-  d.n = min((all + kCacheMinChunks - 1) / kCacheMinChunks, grid);
-  d.per = all / d.n;
-  d.more = all - d.per * d.n;
-  return d;
-}
-
 constexpr int kCacheAttnThreads = kCacheAttnWarps * 32;
-
-struct CacheScan {
-  int warp_sum[kCacheAttnWarps];
-  int before, b, len;
-};
-
-// The block's threads take the sequences in runs of equal length and add up
-// their chunks.  Returns the chunks of all units, and a unit's of the sequences
-// before the thread's run (`upto`); `report` records lengths that had to be
-// limited.
-__device__ __forceinline__ int cache_scan(const CacheAttnParams& p, CacheScan& s, bool report,
-                                          int& upto) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
-  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) {
-    const int len = cache_length(p, b);
-    if (report && len != p.length[b]) atomicMax(p.status, kStatusBadIndex);
-    sum += cache_chunks(len);
-  }
-  int inc = sum;
-#pragma unroll
-  for (int k = 1; k < 32; k <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, inc, k);
-    if (lane >= k) inc += o;
-  }
-  if (lane == 31) s.warp_sum[warp] = inc;
-  __syncthreads();
-  int base = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kCacheAttnWarps; ++w) {
-    if (w < warp) base += s.warp_sum[w];
-    all += s.warp_sum[w];
-  }
-  upto = base + inc - sum;
-  return all * (p.Hkv * p.n_row_blocks);
-}
-
-// The sequence of chunk c, its length, and the chunks before it (all units').
-__device__ __forceinline__ void cache_find(const CacheAttnParams& p, CacheScan& s, int upto, int c,
-                                           int& b, int& len, int& before) {
-  const int run = (p.B + kCacheAttnThreads - 1) / kCacheAttnThreads;
-  const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
-  const int units = p.Hkv * p.n_row_blocks;
-  int at = upto * units;
-  for (int k = b0; k < b1 && at <= c; ++k) {
-    const int l = cache_length(p, k);
-    const int n = cache_chunks(l) * units;
-    if (c < at + n) {
-      s.before = at;
-      s.b = k;
-      s.len = l;
-    }
-    at += n;
-  }
-  __syncthreads();
-  b = s.b;
-  len = s.len;
-  before = s.before;
-}
+using CacheScan = KeyScan<kCacheAttnWarps>;
 
 template <int D, int NT>
 struct CacheAttnSmem {

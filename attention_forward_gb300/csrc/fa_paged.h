@@ -1,0 +1,83 @@
+// fa_paged.h -- parameter blocks and launch entry points of the 16-bit paged
+// caches: keys and values, and latent rows (internal).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+#include "fa_cache.h"
+
+namespace fa {
+
+// A latent row: the latent vector, which is the value too, then the rotated part
+// of the key.
+constexpr int kLatent = 512, kLatentRope = 64, kLatentRow = kLatent + kLatentRope;
+// Latent attention's heads where they are expanded: keys of kNope channels of
+// their own and the shared rotated ones, values of kNope.
+constexpr int kNope = 128;
+
+// A write: new rows into the pages, rotated to their positions.  Keys and values:
+// k and v [B, Hkv, S, D] go to the two pools, q [B, H, S, D] to q_out.  Latent: v
+// [B, S, 512] and k [B, S, 64] go to one pool, q [B, H, S, 64] to the last channels
+// of q_out's rows.
+struct PagedWriteParams {
+  const void *q, *k, *v;  // q: null for none
+  void* q_out;
+  void* pool[2];
+  const float* freqs;     // [rot / 2] radians a position, or null
+  const int* page_table;
+  const int* start;       // [B] or null (0)
+  const int* count;       // [B] or null (S)
+  unsigned* status;
+  int B, H, Hkv, S, D;    // H: 0 without q
+  int rot;                // channels that are rotated, 0 for none
+  int q_width;            // channels of a row of q_out
+  int num_pages, page_shift, max_pages;
+  int token_shift;        // tokens of a block: 1 << token_shift
+};
+
+// A read: positions start ... into rows of out[0], out[1] (keys and values, or the
+// latent and the rotated part).
+struct PagedReadParams {
+  const void* pool[2];
+  void* out[2];
+  const int *page_table, *start, *count;
+  unsigned* status;
+  int B, Hkv, S, D;
+  int num_pages, page_shift, max_pages;
+};
+
+struct PagedAttnParams {
+  void* o;            // [B, H, Sq, values' width]
+  float* lse;         // [B, H, Sq]
+  float* part_o;      // [2 * grid, rows of a CTA, values' width] fp32, O / l of a segment
+  float* part_lse;    // [2 * grid, rows of a CTA]
+  const int* page_table;
+  const int* length;  // [B]
+  const float* slopes;
+  unsigned* status;
+  unsigned long long timeout_ns;
+  int B, H, Hkv, Sq;
+  int rows;           // (H / Hkv) * Sq query rows per kv head
+  int n_row_blocks;
+  int sms;
+  int whole;          // CTAs take whole units: no parts, no merge
+  int num_pages, page_shift, max_pages;
+  int pool_rows;      // rows of the pool: the coordinate of what does not exist
+  float scale, cap, inv_cap, cap_arg;
+};
+
+cudaError_t launch_paged_write(bool latent, bool bf16, bool pairs, const PagedWriteParams& p,
+                               int slices, cudaStream_t stream);
+cudaError_t launch_paged_read(bool latent, const PagedReadParams& p, cudaStream_t stream);
+
+// Query rows that one pass of the attention over the keys takes, and the CTAs that
+// an SM holds.  kind: 64 or 128, a head's channels; kLatent, latent rows.
+int paged_attn_row_block(int kind, int rows);
+int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
+cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const PagedAttnParams& p, int grid,
+                              cudaStream_t stream);
+
+}  // namespace fa

@@ -1,0 +1,262 @@
+// fa_paged_copy.cuh -- the 16-bit paged caches: rotating write, and read back.
+//
+// Rotation of a pair (x, y) of channels at position n with frequency f (radians a
+// position):  (x cos a - y sin a, y cos a + x sin a),  a = n f.
+// The angle is held in turns as a 64-bit fraction: f / 2 pi is rounded once to
+// 2^-64 of a turn (through 53 bits), its product with n is exact modulo a turn, and
+// 32 bits of it go to the sine and cosine.  At n = 2^24 and f = 1 the angle is off by
+// 2^-28 of a radian; n f in fp32 would be off by half a radian.
+//
+// Both kernels only move bytes.  Write: a block takes 2^token_shift tokens of a
+// sequence.  Its threads make the tokens' sines and cosines, one each, then take
+// 16 channels at a time: the pairs of 8 frequencies (two 16-byte words that lie
+// apart by half of what is rotated, or side by side), or 16 channels as they are.
+// Neighbouring threads take neighbouring words of a row, then the next token's, whose
+// row follows in the input.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cache.cuh"
+#include "fa_paged.h"
+
+namespace fa {
+
+constexpr int kPagedCopyThreads = 256;
+constexpr int kPagedMaxTokenShift = 3;
+constexpr int kPagedAtOnce = 4;  // tasks of a thread whose loads go out together
+constexpr int kPagedMaxPairs = 64;
+
+// Cosine and sine of position n times f.
+__device__ __forceinline__ float2 rope_unit(int n, float f) {
+  constexpr double kPerTurn = 0.15915494309189533577;  // 1 / 2 pi
+  double turns = static_cast<double>(f) * kPerTurn;
+  turns -= floor(turns);
+  const unsigned long long step = __double2ull_rn(turns * 18446744073709551616.0);
+  const unsigned long long at = step * static_cast<unsigned long long>(static_cast<long long>(n));
+  // the upper half as a signed number: half turns in [-1, 1)
+  const float half = static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f;
+  float2 u;
+  sincospif(half, &u.y, &u.x);
+  return u;
+}
+
+// Two 16-byte words of 16-bit channels: the pairs (e, e) of both words, or (2 e, 2 e
+// + 1) of one, rotated by unit[0 ... 7].
+template <bool BF16, bool kPairs>
+__device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float2* unit) {
+  uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+  auto turn = [](float& x, float& y, float2 u) {
+    const float t = fmaf(x, u.x, -y * u.y);
+    y = fmaf(y, u.x, x * u.y);
+    x = t;
+  };
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float2 x = cache_unpack<BF16>(wa[e]), y = cache_unpack<BF16>(wb[e]);
+    if constexpr (kPairs) {
+      turn(x.x, x.y, unit[e]);
+      turn(y.x, y.y, unit[e + 4]);
+    } else {
+      turn(x.x, y.x, unit[2 * e]);
+      turn(x.y, y.y, unit[2 * e + 1]);
+    }
+    wa[e] = cache_pack<BF16>(x.x, x.y);
+    wb[e] = cache_pack<BF16>(y.x, y.y);
+  }
+}
+
+// The slot of the token at position `pos` of sequence b as a row of kv head 0; -1
+// when its place does not exist.
+template <class P>
+__device__ __forceinline__ long long paged_slot(const P& p, int b, uint32_t pos) {
+  const uint32_t n = pos >> p.page_shift;
+  if (n >= static_cast<uint32_t>(p.max_pages)) return -1;
+  const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + n];
+  if (page < 0 || page >= p.num_pages) return -1;
+  return ((static_cast<long long>(page) * p.Hkv) << p.page_shift) +
+         (pos & ((1u << p.page_shift) - 1u));
+}
+
+template <bool kLat, bool BF16, bool kPairs>
+__global__ void __launch_bounds__(kPagedCopyThreads, 4)
+    fa_paged_write_kernel(const PagedWriteParams p) {
+  __shared__ float2 unit[kPagedMaxPairs << kPagedMaxTokenShift];  // [token][pair]
+  __shared__ long long slot[1 << kPagedMaxTokenShift];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int b = static_cast<int>(blockIdx.y);
+  const int first = static_cast<int>(blockIdx.x) << p.token_shift;
+  const int start = p.start ? p.start[b] : 0;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  if (first >= count) return;
+  const int tokens = min(1 << p.token_shift, count - first);
+  const int half = p.rot >> 1;
+
+  // a row's tasks: 16 channels each; rows of q, of k, then of v
+  const int d_shift = kLat ? 2 : (p.D == 128 ? 3 : 2);  // tasks of a row of q or k
+  const int v_shift = kLat ? 5 : d_shift;
+  const int ts = p.token_shift;
+  const int n_q = p.H << (ts + d_shift), n_k = p.Hkv << (ts + d_shift);
+  const int n_v = p.Hkv << (ts + v_shift);
+  const int all = n_q + n_k + n_v;
+  const int per = (all + static_cast<int>(gridDim.z) - 1) / static_cast<int>(gridDim.z);
+  const int t0 = per * static_cast<int>(blockIdx.z), t1 = min(all, t0 + per);
+
+  struct Task {
+    const uint4 *in0, *in1;
+    uint4 *out0, *out1;
+    int token, pair;  // pair: the first of its 8, or -1
+  };
+  const int D = kLat ? kLatentRope : p.D;
+  // where a task's words are; `out` is ready once the slots are
+  auto source = [&](int id, Task& t) {
+    t.pair = -1;
+    t.token = tokens;
+    if (id >= t1) return;
+    int r = id, shift = d_shift, heads = p.H;
+    const void* in = p.q;
+    bool turned = p.rot > 0;
+    if (r >= n_q) {
+      r -= n_q;
+      heads = p.Hkv;
+      in = p.k;
+      if (r >= n_k) {
+        r -= n_k;
+        shift = v_shift;
+        in = p.v;
+        turned = false;
+      }
+    }
+    const int u = r & ((1 << shift) - 1);
+    t.token = (r >> shift) & ((1 << ts) - 1);
+    if (t.token >= tokens) {
+      t.token = tokens;
+      return;
+    }
+    const int head = r >> (shift + ts);
+    turned = turned && 16 * u < p.rot;
+    const int w0 = turned && !kPairs ? u : 2 * u;
+    const uint4* row = static_cast<const uint4*>(in) +
+                       (((static_cast<long long>(b) * heads + head) * p.S + first + t.token)
+                        << (shift + 1));
+    t.in0 = row + w0;
+    t.in1 = row + (turned && !kPairs ? w0 + (half >> 3) : w0 + 1);
+    if (turned) t.pair = 8 * u;
+  };
+  auto target = [&](int id, Task& t) -> bool {
+    int r = id;
+    const bool is_q = r < n_q, is_v = r >= n_q + n_k;
+    const int shift = is_v ? v_shift : d_shift;
+    r -= is_q ? 0 : (is_v ? n_q + n_k : n_q);
+    const int head = r >> (shift + ts), u = r & ((1 << shift) - 1);
+    const int w0 = t.pair >= 0 && !kPairs ? u : 2 * u;
+    uint4* row;
+    if (is_q) {
+      row = static_cast<uint4*>(p.q_out) +
+            ((static_cast<long long>(b) * p.H + head) * p.S + first + t.token) * (p.q_width >> 3) +
+            ((p.q_width - D) >> 3);
+    } else {
+      const long long s = slot[t.token];
+      if (s < 0) return false;
+      if constexpr (kLat) {
+        row = static_cast<uint4*>(p.pool[0]) + s * (kLatentRow / 8) + (is_v ? 0 : kLatent / 8);
+      } else {
+        row = static_cast<uint4*>(p.pool[is_v ? 1 : 0]) +
+              ((s + (static_cast<long long>(head) << p.page_shift)) << (d_shift + 1));
+      }
+    }
+    t.out0 = row + w0;
+    t.out1 = row + (t.pair >= 0 && !kPairs ? w0 + (half >> 3) : w0 + 1);
+    return true;
+  };
+
+  bool ready = false;
+#pragma unroll 1
+  for (int base = t0; base < t1 || !ready; base += kPagedCopyThreads * kPagedAtOnce) {
+    Task t[kPagedAtOnce];
+    uint4 x[kPagedAtOnce], y[kPagedAtOnce];
+#pragma unroll
+    for (int k = 0; k < kPagedAtOnce; ++k) {
+      source(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k]);
+      if (t[k].token < tokens) {
+        x[k] = __ldcs(t[k].in0);
+        y[k] = __ldcs(t[k].in1);
+      }
+    }
+    if (!ready) {  // while the first words are on their way
+      if (static_cast<int>(threadIdx.x) < tokens) {
+        const uint32_t pos = static_cast<uint32_t>(start) + static_cast<uint32_t>(first) + threadIdx.x;
+        const long long s = paged_slot(p, b, pos);
+        slot[threadIdx.x] = s;
+        if (s < 0 && blockIdx.z == 0) atomicMax(p.status, kStatusBadIndex);
+      }
+      for (int i = threadIdx.x; i < tokens * half; i += kPagedCopyThreads) {
+        const int tok = i / half;
+        unit[i] = rope_unit(static_cast<int>(static_cast<uint32_t>(start) +
+                                             static_cast<uint32_t>(first + tok)),
+                            p.freqs[i - tok * half]);
+      }
+      __syncthreads();
+      ready = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kPagedAtOnce; ++k) {
+      if (t[k].token >= tokens) continue;
+      if (t[k].pair >= 0) rope_turn<BF16, kPairs>(x[k], y[k], unit + t[k].token * half + t[k].pair);
+      if (!target(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k])) continue;
+      *t[k].out0 = x[k];
+      *t[k].out1 = y[k];
+    }
+  }
+}
+
+// A thread takes the same 16 bytes of kPagedAtOnce rows.  blockIdx.y: the (sequence,
+// kv head), blockIdx.z: keys or values; latent rows (72 words) are taken whole.
+template <bool kLat>
+__global__ void __launch_bounds__(kPagedCopyThreads) fa_paged_read_kernel(const PagedReadParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int bh = static_cast<int>(blockIdx.y);
+  const int b = bh / p.Hkv, hk = bh - b * p.Hkv;
+  const int start = p.start ? p.start[b] : 0;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  const int words = kLat ? kLatentRow / 8 : p.D / 8;
+  const int lanes = kPagedCopyThreads / words;  // rows at once
+  const int row_of = static_cast<int>(threadIdx.x) / words;
+  const int w = static_cast<int>(threadIdx.x) - row_of * words;
+  const int i0 = static_cast<int>(blockIdx.x) * lanes * kPagedAtOnce + row_of;
+  if (row_of >= lanes || i0 >= count) return;
+  const uint4* pool = static_cast<const uint4*>(kLat || blockIdx.z == 0 ? p.pool[0] : p.pool[1]);
+  uint4 x[kPagedAtOnce];
+#pragma unroll
+  for (int k = 0; k < kPagedAtOnce; ++k) {
+    const int i = i0 + k * lanes;
+    x[k] = make_uint4(0u, 0u, 0u, 0u);  // a place that does not exist reads as zeros
+    if (i >= count) continue;
+    const long long s = paged_slot(p, b, static_cast<uint32_t>(start) + static_cast<uint32_t>(i));
+    if (s < 0) {
+      if (w == 0) atomicMax(p.status, kStatusBadIndex);
+    } else {
+      // from L2: the kernel may have started while the write before it ran
+      x[k] = __ldcg(pool + (s + (static_cast<long long>(hk) << p.page_shift)) * words + w);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPagedAtOnce; ++k) {
+    const int i = i0 + k * lanes;
+    if (i >= count) continue;
+    const long long row = static_cast<long long>(bh) * p.S + i;
+    if constexpr (kLat) {
+      if (w < kLatent / 8)
+        static_cast<uint4*>(p.out[0])[row * (kLatent / 8) + w] = x[k];
+      else
+        static_cast<uint4*>(p.out[1])[row * (kLatentRope / 8) + w - kLatent / 8] = x[k];
+    } else {
+      static_cast<uint4*>(blockIdx.z == 0 ? p.out[0] : p.out[1])[row * words + w] = x[k];
+    }
+  }
+}
+
+}  // namespace fa

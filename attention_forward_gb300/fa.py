@@ -109,6 +109,22 @@ def load_path(path: str) -> ctypes.CDLL:
     L.fa_cache_workspace_bytes.restype = sz
     L.fa_fwd_cache.argtypes = [vp] * 9 + [ci] * 8 + [cf, ci, cf, vp, vp, sz, vp]
     L.fa_fwd_cache.restype = ci
+    L.fa_paged_write.argtypes = [vp] * 10 + [ci] * 11 + [vp]
+    L.fa_paged_write.restype = ci
+    L.fa_paged_read.argtypes = [vp] * 7 + [ci] * 8 + [vp]
+    L.fa_paged_read.restype = ci
+    L.fa_paged_workspace_bytes.argtypes = [ci] * 7
+    L.fa_paged_workspace_bytes.restype = sz
+    L.fa_fwd_paged.argtypes = [vp] * 7 + [ci] * 8 + [cf, ci, cf, vp, vp, sz, vp]
+    L.fa_fwd_paged.restype = ci
+    L.fa_latent_write.argtypes = [vp] * 9 + [ci] * 9 + [vp]
+    L.fa_latent_write.restype = ci
+    L.fa_latent_read.argtypes = [vp] * 6 + [ci] * 6 + [vp]
+    L.fa_latent_read.restype = ci
+    L.fa_latent_workspace_bytes.argtypes = [ci] * 5
+    L.fa_latent_workspace_bytes.restype = sz
+    L.fa_fwd_latent.argtypes = [vp] * 6 + [ci] * 6 + [cf, ci, vp, sz, vp]
+    L.fa_fwd_latent.restype = ci
     L.fa_version.argtypes = []
     L.fa_version.restype = ci
     return L
@@ -574,6 +590,286 @@ def fa_fwd_cache(q, cache, page_table, length, scale: float | None = None,
                               stream)
     if st:
         _check(st, "fa_fwd_cache")
+    return out, lse
+
+
+# ------------------------------------------------------------ 16-bit paged caches
+
+LATENT, LATENT_ROPE = 512, 64  # channels of a latent row, and of its rotated part
+
+
+def _on(dev: int, call, *args):
+    """The call again with its tensors' device current."""
+    with torch.cuda.device(dev):
+        return call(*args)
+
+
+def _opt(t, name: str, dev: int, dtype, shape):
+    return None if t is None else _ptr(t, name, dev, dtype, shape)
+
+
+def _places(page_table, start, count, dev: int, B: int):
+    """(page_table, start, count) as pointers, and max_pages."""
+    table, per = _pages(page_table, dev, B)
+    return (table, _opt(start, "start", dev, torch.int32, (B,)),
+            _opt(count, "count", dev, torch.int32, (B,))), per
+
+
+def fa_paged_empty(num_pages: int, Hkv: int, page_size: int, D: int, dtype=torch.bfloat16,
+                   device="cuda"):
+    """The arrays (k_pages, v_pages) of a 16-bit cache of that many pages, zeroed;
+    any tensors of this shape and type serve."""
+    if D not in (64, 128) or dtype not in _DTYPE:
+        raise ValueError("D must be 64 or 128, dtype float16 or bfloat16")
+    one = lambda: torch.zeros((num_pages, Hkv, page_size, D), dtype=dtype, device=device)  # noqa: E731
+    return one(), one()
+
+
+def _paged(cache, dev: int, dtype, Hkv: int, D: int):
+    """A 16-bit cache's pointers, num_pages and page_size, checked."""
+    if len(cache) != 2 or not isinstance(cache[0], torch.Tensor) or cache[0].dim() != 4:
+        raise ValueError("a cache is (k_pages, v_pages), [num_pages, Hkv, page_size, D] each")
+    shape = (cache[0].shape[0], Hkv, cache[0].shape[2], D)
+    return (_ptr(cache[0], "k_pages", dev, dtype, shape),
+            _ptr(cache[1], "v_pages", dev, dtype, shape), shape[0], shape[2])
+
+
+def _freqs(freqs, dev: int):
+    if freqs is None:
+        return None, 0
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be a 1-d float32 tensor")
+    return _ptr(freqs, "freqs", dev, torch.float32, freqs.shape), 2 * freqs.shape[0]
+
+
+def _rotated(out, shape, like, count, stream):
+    """A new tensor for rotated queries; zeros where a count may leave rows out."""
+    if out is not None:
+        return out
+    out = (torch.empty if count is None else torch.zeros)(shape, dtype=like.dtype,
+                                                          device=like.device)
+    if stream is not None:
+        _own_memory([out], stream)
+    return out
+
+
+def fa_paged_write(k, v, cache, page_table, start=None, count=None, freqs=None,
+                   interleaved: bool = False, q=None, q_out=None, stream=None):
+    """k, v [B, Hkv, S, D] into the 16-bit cache: token i < count[b] (default S) of
+    sequence b goes to position start[b] + i (default i) of the pages that page_table
+    [B, max_pages] lists.  ``freqs`` (float32 [rotary / 2], radians a position) rotates
+    the first channels of keys and of ``q`` [B, H, S, D], as halves or interleaved
+    pairs.  Returns the rotated queries (``q_out``, which may be q; None without q)."""
+    dev, (B, Hkv, S, D) = _rows16(k, "k")
+    if _current_device() != dev:
+        return _on(dev, fa_paged_write, k, v, cache, page_table, start, count, freqs, interleaved,
+                   q, q_out, stream)
+    vp = _ptr(v, "v", dev, k.dtype, k.shape)
+    kp, vpp, pages, page = _paged(cache, dev, k.dtype, Hkv, D)
+    where, per = _places(page_table, start, count, dev, B)
+    fp, rotary = _freqs(freqs, dev)
+    qp = op = None
+    H = Hkv
+    if q is not None:
+        _, shape = _rows16(q, "q")
+        H = shape[1]
+        _group_check(H, Hkv)
+        qp = _ptr(q, "q", dev, k.dtype, (B, H, S, D))
+        q_out = _rotated(q_out, q.shape, q, count, stream)
+        op = _ptr(q_out, "q_out", dev, k.dtype, q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check((_lib or load()).fa_paged_write(
+        qp, k.data_ptr(), vp, op, kp, vpp, *where, fp, rotary, bool(interleaved), B, H, Hkv, S, D,
+        pages, page, per, _DTYPE[k.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_paged_write")
+    return q_out
+
+
+def fa_paged_read(cache, page_table, start=None, count=None, out=None, stream=None):
+    """Positions start[b] ... start[b] + count[b] - 1 of the 16-bit cache into the
+    first rows of ``out`` = (k, v), [B, Hkv, S, D] each; rows past count[b] are left as
+    they were.  Returns (k, v)."""
+    if out is None or len(out) != 2:
+        raise ValueError("out must be the pair (k, v) to read into")
+    k, v = out
+    dev, (B, Hkv, S, D) = _rows16(k, "k")
+    if _current_device() != dev:
+        return _on(dev, fa_paged_read, cache, page_table, start, count, out, stream)
+    vp = _ptr(v, "v", dev, k.dtype, k.shape)
+    kp, vpp, pages, page = _paged(cache, dev, k.dtype, Hkv, D)
+    where, per = _places(page_table, start, count, dev, B)
+    _check((_lib or load()).fa_paged_read(
+        kp, vpp, *where, k.data_ptr(), vp, B, Hkv, S, D, pages, page, per, _DTYPE[k.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_paged_read")
+    return k, v
+
+
+def fa_paged_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, D: int, page_size: int,
+                             max_pages: int) -> int:
+    return int(load().fa_paged_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages))
+
+
+def _attend_pages(name: str, call, need, dev: int, q, stream, workspace):
+    """A cache attention's call(workspace, bytes, stream handle); a captured one that
+    has no workspace gets one of the graph's memory."""
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    st = call(ws, ws_bytes, handle)
+    if st == FA_ERR_WORKSPACE and ws is None:
+        st = _graph_workspace(lambda p, n: call(p, n, handle), need(), q.device, stream)
+    if st:
+        _check(st, name)
+
+
+def fa_fwd_paged(q, cache, page_table, length, scale: float | None = None, softcap: float = 0.0,
+                 slopes=None, workspace=None, out=None, lse=None, stream=None):
+    """Attention of the newest Sq tokens, q [B, H, Sq, D], over the 16-bit cache:
+    length[b] (int32) tokens of sequence b are in it, these included.  Returns
+    (o, lse)."""
+    dev, (B, H, Sq, D) = _rows16(q, "q")
+    if _current_device() != dev:
+        return _on(dev, fa_fwd_paged, q, cache, page_table, length, scale, softcap, slopes,
+                   workspace, out, lse, stream)
+    Hkv = cache[0].shape[1] if isinstance(cache[0], torch.Tensor) and cache[0].dim() == 4 else 0
+    _group_check(H, Hkv)
+    kp, vp, pages, page = _paged(cache, dev, q.dtype, Hkv, D)
+    table, per = _pages(page_table, dev, B)
+    lp = _ptr(length, "length", dev, torch.int32, (B,))
+    sp = _opt(slopes, "slopes", dev, torch.float32, (H,))
+    sc = float(D) ** -0.5 if scale is None else float(scale)
+    L = _lib or load()
+    out, lse = _outputs_on(q, dev, out, lse, stream)
+    args = (q.data_ptr(), kp, vp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, D,
+            pages, page, per, sc, _DTYPE[q.dtype], softcap, sp)
+    _attend_pages("fa_fwd_paged", lambda *ws: L.fa_fwd_paged(*args, *ws),
+                  lambda: L.fa_paged_workspace_bytes(B, H, Hkv, Sq, D, page, per), dev, q, stream,
+                  workspace)
+    return out, lse
+
+
+def fa_latent_empty(num_pages: int, page_size: int, dtype=torch.bfloat16, device="cuda"):
+    """A latent cache [num_pages, page_size, 576], zeroed; any tensor of this shape and
+    type serves."""
+    if dtype not in _DTYPE:
+        raise ValueError("dtype must be float16 or bfloat16")
+    return torch.zeros((num_pages, page_size, LATENT + LATENT_ROPE), dtype=dtype, device=device)
+
+
+def _latent_pages(cache, dev: int, dtype):
+    if not isinstance(cache, torch.Tensor) or cache.dim() != 3:
+        raise ValueError("a latent cache is [num_pages, page_size, 576]")
+    n, page, _ = cache.shape
+    return _ptr(cache, "cache", dev, dtype, (n, page, LATENT + LATENT_ROPE)), n, page
+
+
+def _latent_rows(c, k_rope):
+    """(device, B, S) of latent rows and their rotated part."""
+    if not isinstance(c, torch.Tensor) or c.dim() != 3 or c.dtype not in _DTYPE:
+        raise ValueError("c must be a [B, S, 512] float16 or bfloat16 tensor")
+    dev, (B, S, _) = c.get_device(), c.shape
+    _ptr(c, "c", dev if dev >= 0 else -2, c.dtype, (B, S, LATENT))
+    _ptr(k_rope, "k_rope", dev, c.dtype, (B, S, LATENT_ROPE))
+    return dev, B, S
+
+
+def fa_latent_write(c, k_rope, cache, page_table, start=None, count=None, freqs=None,
+                    interleaved: bool = False, q_rope=None, q=None, stream=None):
+    """Latent rows c [B, S, 512] and k_rope [B, S, 64] into the cache, k_rope rotated by
+    ``freqs`` (float32 [32]; None: as it is), as fa_paged_write.  ``q_rope`` [B, H, S,
+    64] goes rotated into the last 64 channels of ``q`` [B, H, S, width], whose others
+    stay.  Returns q."""
+    dev, B, S = _latent_rows(c, k_rope)
+    if _current_device() != dev:
+        return _on(dev, fa_latent_write, c, k_rope, cache, page_table, start, count, freqs,
+                   interleaved, q_rope, q, stream)
+    cp, pages, page = _latent_pages(cache, dev, c.dtype)
+    where, per = _places(page_table, start, count, dev, B)
+    fp = _opt(freqs, "freqs", dev, torch.float32, (LATENT_ROPE // 2,))
+    qp = op = None
+    H = width = 0
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q go together")
+    if q is not None:
+        _, shape = _rows16(q, "q")
+        H, width = shape[1], shape[3]
+        op = _ptr(q, "q", dev, c.dtype, (B, H, S, width))
+        qp = _ptr(q_rope, "q_rope", dev, c.dtype, (B, H, S, LATENT_ROPE))
+    _check((_lib or load()).fa_latent_write(
+        c.data_ptr(), k_rope.data_ptr(), cp, qp, op, *where, fp, bool(interleaved), B, H, S, width,
+        pages, page, per, _DTYPE[c.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_latent_write")
+    return q
+
+
+def fa_latent_read(cache, page_table, start=None, count=None, out=None, stream=None):
+    """Positions start[b] ... of the latent cache into the first rows of ``out`` = (c,
+    k_rope), [B, S, 512] and [B, S, 64]; rows past count[b] are left as they were.
+    Returns (c, k_rope)."""
+    if out is None or len(out) != 2:
+        raise ValueError("out must be the pair (c, k_rope) to read into")
+    c, k_rope = out
+    dev, B, S = _latent_rows(c, k_rope)
+    if _current_device() != dev:
+        return _on(dev, fa_latent_read, cache, page_table, start, count, out, stream)
+    cp, pages, page = _latent_pages(cache, dev, c.dtype)
+    where, per = _places(page_table, start, count, dev, B)
+    _check((_lib or load()).fa_latent_read(
+        cp, *where, c.data_ptr(), k_rope.data_ptr(), B, S, pages, page, per, _DTYPE[c.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_latent_read")
+    return c, k_rope
+
+
+def fa_latent_workspace_bytes(B: int, H: int, Sq: int, page_size: int, max_pages: int) -> int:
+    return int(load().fa_latent_workspace_bytes(B, H, Sq, page_size, max_pages))
+
+
+def _outputs_wide(q, width: int, dev: int, out, lse, stream):
+    """As _outputs_on, with output rows of another width than q's."""
+    B, H, Sq, _ = q.shape
+    made = []
+    if out is None:
+        out = torch.empty((B, H, Sq, width), dtype=q.dtype, device=q.device)
+        made.append(out)
+    else:
+        _ptr(out, "out", dev, q.dtype, (B, H, Sq, width))
+    if lse is None:
+        lse = torch.empty((B, H, Sq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    else:
+        _ptr(lse, "lse", dev, torch.float32, (B, H, Sq))
+    if stream is not None and made:
+        _own_memory(made, stream)
+    return out, lse
+
+
+# the width of a head's keys where they are expanded, 128 + 64: what the scores of
+# latent attention are scaled by unless the call says
+_LATENT_SCALE = 192.0 ** -0.5
+
+
+def fa_fwd_latent(q, cache, page_table, length, scale: float | None = None, workspace=None,
+                  out=None, lse=None, stream=None):
+    """Latent attention, absorbed: the newest Sq tokens' q [B, H, Sq, 576] over the
+    cache's rows, whose first 512 channels are the values too.  length as for
+    fa_fwd_paged; scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 512], lse)."""
+    dev, (B, H, Sq, D) = _rows16(q, "q")
+    if D != LATENT + LATENT_ROPE:
+        raise ValueError("q must be [B, H, Sq, 576]")
+    if _current_device() != dev:
+        return _on(dev, fa_fwd_latent, q, cache, page_table, length, scale, workspace, out, lse,
+                   stream)
+    cp, pages, page = _latent_pages(cache, dev, q.dtype)
+    table, per = _pages(page_table, dev, B)
+    lp = _ptr(length, "length", dev, torch.int32, (B,))
+    sc = _LATENT_SCALE if scale is None else float(scale)
+    L = _lib or load()
+    out, lse = _outputs_wide(q, LATENT, dev, out, lse, stream)
+    args = (q.data_ptr(), cp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Sq, pages, page, per,
+            sc, _DTYPE[q.dtype])
+    _attend_pages("fa_fwd_latent", lambda *ws: L.fa_fwd_latent(*args, *ws),
+                  lambda: L.fa_latent_workspace_bytes(B, H, Sq, page, per), dev, q, stream,
+                  workspace)
     return out, lse
 
 

@@ -435,8 +435,112 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
                          size_t workspace_bytes, fa_stream_t stream);
 
 /*
- * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score and
- * fa_fwd_cache keep on the current device (one per stream that they were called
+ * The 16-bit paged caches.
+ *
+ * Keys and values: fa_paged_write, fa_paged_read, fa_fwd_paged.
+ *   k_pages, v_pages  [num_pages, Hkv, page_size, D], fp16 or bf16, 16-byte
+ *                     aligned
+ * page_table, page_size, start, count, length and what happens to places that
+ * do not exist are as for the 4-bit cache, whose limits hold too, and
+ * num_pages * Hkv * page_size < 2^31.  All may be captured into CUDA graphs.
+ *
+ * fa_paged_write -- new tokens into the pages, queries and keys rotated on the
+ * way.
+ *   k, v   [B, Hkv, S, D]: token i of sequence b goes to position n = start[b]
+ *          + i, for i < count[b]
+ *   q      [B, H, S, D], written rotated to q_out (which may be q; tokens past
+ *          count[b] are left as they were there); both NULL for none, and H is
+ *          then not looked at
+ *   freqs  [rotary / 2] fp32 radians a position: the first `rotary` channels
+ *          of a query's or key's head (a multiple of 16, up to D) are pairs
+ *          (x, y) that become (x cos a - y sin a, y cos a + x sin a), a = n *
+ *          freqs[j].  NULL with rotary 0: nothing is rotated.
+ *   interleaved  0: pair j is channels j, j + rotary / 2; 1: 2 j, 2 j + 1
+ * The angle is exact to 2^-28 radian up to n = 2^24 and freqs[j] = 1 (and in
+ * proportion above); a rotated value is rounded once to its type behind fp32
+ * work.  No two tokens of a call may go to the same slot.
+ *
+ * fa_paged_read -- positions start[b] ... start[b] + count[b] - 1 into rows 0 ...
+ * of k, v [B, Hkv, S, D], as fa_cache_read.
+ *
+ * fa_fwd_paged -- attention of the newest tokens over the pages: fa_fwd_cache
+ * with 16-bit keys and values.  Its arguments, limits (row blocks of 16 rows up
+ * to (H / Hkv) * Sq = 16, else of 64), workspace rules and masks are
+ * fa_fwd_cache's; a probability is rounded to the type of V for the product.  V
+ * must be finite within a sequence's length; what lies past it may be anything.
+ */
+fa_status_t fa_paged_write(const void *q, const void *k, const void *v,
+                           void *q_out, void *k_pages, void *v_pages,
+                           const int *page_table, const int *start,
+                           const int *count, const float *freqs, int rotary,
+                           int interleaved, int B, int H, int Hkv, int S, int D,
+                           int num_pages, int page_size, int max_pages,
+                           int dtype, fa_stream_t stream);
+fa_status_t fa_paged_read(const void *k_pages, const void *v_pages,
+                          const int *page_table, const int *start,
+                          const int *count, void *k, void *v, int B, int Hkv,
+                          int S, int D, int num_pages, int page_size,
+                          int max_pages, int dtype, fa_stream_t stream);
+size_t fa_paged_workspace_bytes(int B, int H, int Hkv, int Sq, int D,
+                                int page_size, int max_pages);
+fa_status_t fa_fwd_paged(const void *q, const void *k_pages,
+                         const void *v_pages, const int *page_table,
+                         const int *length, void *o, float *lse, int B, int H,
+                         int Hkv, int Sq, int D, int num_pages, int page_size,
+                         int max_pages, float scale, int dtype, float softcap,
+                         const float *slopes, void *workspace,
+                         size_t workspace_bytes, fa_stream_t stream);
+
+/*
+ * Latent attention: keys and values of all heads come from one latent row a
+ * token, of 512 channels and 64 more that are rotated.
+ *   pages  [num_pages, page_size, 576], fp16 or bf16, 16-byte aligned: the
+ *          latent, then the rotated part
+ * Limits as above with Hkv = 1.
+ *
+ * fa_latent_write -- new rows into the pages.
+ *   c, k_rope  [B, S, 512], [B, S, 64]; k_rope is rotated (all 64 channels,
+ *              freqs of 32; NULL: not rotated)
+ *   q_rope     [B, H, S, 64], written rotated to the last 64 channels of the rows
+ *              of q [B, H, S, q_width] (q_width a multiple of 8, 64 ... 65536; 192
+ *              for fa_fwd_expanded, 576 for fa_fwd_latent), whose other channels
+ *              are left as they were; both NULL for none
+ *
+ * fa_latent_read -- positions start[b] ... into rows of c and k_rope.
+ *
+ * fa_fwd_latent -- the absorbed form: attention of the newest tokens over the
+ * pages, all heads against the same rows.
+ *   q [B, H, Sq, 576]: a head's query through its key expansion (512), and the
+ *   rotated part; o [B, H, Sq, 512]: sums of latents, to go through the head's
+ *   value expansion; lse [B, H, Sq]
+ *   O = sum_j softmax_j(scale <q, row_j>) row_j[0 ... 511]
+ * length, workspace and masks as for fa_fwd_paged (row blocks of 16, 32 or 64 of
+ * the H * Sq rows).  Latent rows must be finite within a sequence's length.
+ */
+fa_status_t fa_latent_write(const void *c, const void *k_rope, void *pages,
+                            const void *q_rope, void *q, const int *page_table,
+                            const int *start, const int *count,
+                            const float *freqs, int interleaved, int B, int H,
+                            int S, int q_width, int num_pages, int page_size,
+                            int max_pages, int dtype, fa_stream_t stream);
+fa_status_t fa_latent_read(const void *pages, const int *page_table,
+                           const int *start, const int *count, void *c,
+                           void *k_rope, int B, int S, int num_pages,
+                           int page_size, int max_pages, int dtype,
+                           fa_stream_t stream);
+size_t fa_latent_workspace_bytes(int B, int H, int Sq, int page_size,
+                                 int max_pages);
+fa_status_t fa_fwd_latent(const void *q, const void *pages,
+                          const int *page_table, const int *length, void *o,
+                          float *lse, int B, int H, int Sq, int num_pages,
+                          int page_size, int max_pages, float scale, int dtype,
+                          void *workspace, size_t workspace_bytes,
+                          fa_stream_t stream);
+
+/*
+ * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score,
+ * fa_fwd_cache, fa_fwd_paged and fa_fwd_latent keep on the current device (one
+ * per stream that they were called
  * on), after synchronising the device.  The next fa_fwd that needs one
  * allocates it again.  Returns FA_ERR_CUDA if the synchronisation or a free
  * failed (the cache is emptied either way).
@@ -447,8 +551,8 @@ fa_status_t fa_release_workspaces(void);
  * fa_get_device_status -- synchronises `stream`, then returns and clears the
  * device status word of the current device.  Since the last call:
  *   FA_ERR_TIMEOUT      a kernel's bounded wait ran out
- *   FA_ERR_INVALID_ARG  else, a cache call met a page, position or length
- *                       that does not exist (the 4-bit cache, above)
+ *   FA_ERR_INVALID_ARG  else, a call on a paged cache met a page, position or
+ *                       length that does not exist
  *   FA_OK               neither
  * FA_ERR_CUDA if the synchronisation itself failed.
  */
