@@ -31,7 +31,7 @@ SOURCES = ["fa_prefill_d128.cu", "fa_prefill_d64.cu", "fa_prefill_d64x3.cu", "fa
            "fa_score_d64_bf16.cu", "fa_score_d64_f16.cu", "fa_score_docs.cu", "fa_score_api.cu",
            "fa_cache.cu", "fa_cache_attn.cu", "fa_cache_api.cu", "fa_merge.cu",
            "fa_paged_copy.cu", "fa_paged_attn_d64.cu", "fa_paged_attn_d128.cu",
-           "fa_paged_attn_latent.cu", "fa_paged_api.cu"]
+           "fa_paged_attn_latent.cu", "fa_paged_api.cu", "fa_expanded.cu"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,431 @@
+// fa_expanded.cuh -- latent attention with its heads expanded (prompts): scores over
+// 192 channels, of which 128 are a head's own and 64 the heads share, values of 128.
+// sm_103a.
+//
+//   S = scale (Q[:, :128] K^T + Q[:, 128:] R^T),  O = softmax(S) V
+// with K and V the halves of the head's rows of kv [Skv, 256], as one product with
+// the expansion's weights leaves them, and R = k_rope [Skv, 64]: neither is ever put
+// together with the other or repeated by heads in memory.
+//
+// The prefill kernel's pipeline (its header): items of two stages of 128 rows, the
+// same warps, softmax, register split and tensor memory.  What differs follows from
+// shared memory: Q takes 2 x 48 KB, a key tile 48 KB and a value tile 32 KB, so that
+// two tiles do not fit.  Keys and values therefore go through one ring of eight
+// 16 KB chunks, five a tile in the order of their use:
+//   K chunk c (3): 128 keys x 64 channels;  V chunk h (2): 64 keys x 128 channels
+// each with its own barriers, so that a product starts with its first chunk and
+// frees each as it is done with it; the ring runs 1.6 tiles ahead.  O goes from
+// registers to global memory (its staging's 32 KB are the ring's).
+#pragma once
+#include "fa_paged.h"
+#include "fa_prefill.cuh"
+
+namespace fa {
+
+struct ExpandedParams {
+  PrefillParams a;  // lse, scheduler, sizes, masks, split keys; o in a.o
+  int H;
+};
+
+struct ExpandedLayout {
+  static constexpr int kDq = kNope + kLatentRope;    // 192
+  static constexpr int kChunk = 128 * 64 * 2;        // 16 KB
+  static constexpr int kQBytes = 3 * kChunk;         // one stage of Q
+  static constexpr int kSlots = 8;
+  static constexpr int kPerTile = 5;                 // chunks: K 3, V 2
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffRing = kStages * kQBytes;
+  static constexpr int kOffBars = kOffRing + kSlots * kChunk;
+  // mbarrier indices, as the prefill kernel's
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, PV_READY = 6, O_READY = 8, ML_FULL = 10,
+                       O_FREE = 12, DRAIN = 14, ITEM_FULL = 15, ITEM_EMPTY = 19, KV_FULL = 23,
+                       KV_EMPTY = KV_FULL + kSlots, kNumBars = KV_EMPTY + kSlots;
+  static constexpr int kOffInvL = kOffBars + ((kNumBars * 8 + 15) / 16) * 16;
+  static constexpr int kOffItems = kOffInvL + kStages * kBM * 4;
+  static constexpr int kOffTmemSlot = kOffItems + kItemRing * 4;
+  static constexpr int kOffAbort = kOffTmemSlot + 4;
+  static constexpr int kSmemBytes = kOffAbort + 4 + 1024;  // + align
+  static constexpr int kTmemCols = 512;
+  static constexpr int kTmemO = 256;  // O_s at column 256 + 128 s
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+};
+
+template <bool BF16, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    fa_expanded_kernel(const __grid_constant__ CUtensorMap tmQ,
+                       const __grid_constant__ CUtensorMap tmKV,
+                       const __grid_constant__ CUtensorMap tmR, const ExpandedParams ep) {
+  using L = ExpandedLayout;
+  constexpr int D = kNope;
+  const PrefillParams& p = ep.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + L::kOffQ, sRing = sbase + L::kOffRing, bars = sbase + L::kOffBars;
+  float* inv_l_smem = reinterpret_cast<float*>(smem + L::kOffInvL);
+  volatile int* item_ring = reinterpret_cast<volatile int*>(smem + L::kOffItems);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffTmemSlot);
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + L::kOffAbort);
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(L::Q_FULL + s), 1);
+      mbar_init(bar(L::Q_EMPTY + s), 1);
+      mbar_init(bar(L::S_FULL + s), 1);
+      mbar_init(bar(L::PV_READY + s), 4);  // the stage's 4 softmax warps
+      mbar_init(bar(L::O_READY + s), 1);
+      mbar_init(bar(L::ML_FULL + s), 4);
+      mbar_init(bar(L::O_FREE + s), 4);    // the 4 epilogue warps
+    }
+    mbar_init(bar(L::DRAIN), 1);
+    for (int i = 0; i < kItemRing; ++i) {
+      mbar_init(bar(L::ITEM_FULL + i), 1);
+      mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers);
+    }
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bar(L::KV_FULL + i), 1);
+      mbar_init(bar(L::KV_EMPTY + i), 1);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 13 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmKV);
+    tma_prefetch_desc(&tmR);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctl ctl{abort_flag, p.status, p.timeout_ns};
+  grid_dependency_wait();  // the setup overlapped the end of the kernel before
+
+  const int wg = warp >> 2;
+  if (wg < 2) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmaxSingle));
+  } else if (wg == 2) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpilogueSingle));
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControlSingle));
+  }
+
+  if (wg < 2) {
+    // =========================== softmax, stage s ===========================
+    const int s = wg, rq = warp & 3, r = rq * 32 + lane;
+    const uint32_t t_lane = static_cast<uint32_t>(rq * 32) << 16;
+    const uint32_t tS = tmem + t_lane + static_cast<uint32_t>(s * kBN);
+    const uint32_t tO = tmem + t_lane + static_cast<uint32_t>(L::kTmemO + s * D);
+    uint32_t n_s = 0;  // tiles of this stage so far (S_FULL / O_READY phase)
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t k = 0; ok; ++k) {
+      const int idx = take_item<0>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
+      if (!ok || idx < 0) break;
+      const ItemT<kSplit> it = get_item<kSplit>(p, idx);
+      const int nT = s == 0 ? it.nT0 : it.nT1;
+      const int stage_row0 = it.row0 + s * kBM, row_g = stage_row0 + r;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < nT; ++j, ++n_s) {
+        if (!wait_bar_warp(bar(L::S_FULL + s), n_s & 1, ctl)) { ok = false; break; }
+        tc_fence_after();
+        softmax_tile<D, BF16>(tS, tO, (it.t0 + j) * kBN, stage_row0, row_g, p, j > 0, m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::PV_READY + s));
+      }
+      if (!ok) break;
+      if (row_g < p.Sq) {
+        const float lse = l > 0.f ? (m + log2f(l)) * 0.69314718055994530942f : l == 0.f ? -INFINITY : l;
+        if constexpr (kSplit)
+          p.part_lse[(static_cast<size_t>(it.split) * p.BH + it.bh) * p.Sq + row_g] = lse;
+        else
+          p.lse[static_cast<size_t>(it.bh) * p.Sq + row_g] = lse;
+      }
+      if (nT > 0) {
+        if (!wait_bar_warp(bar(L::O_READY + s), (n_s - 1) & 1, ctl)) { ok = false; break; }
+        inv_l_smem[s * kBM + r] = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::ML_FULL + s));
+      }
+    }
+    __syncwarp();
+  } else if (wg == 2) {
+    // =============================== epilogue ===============================
+    const int rq = warp & 3, r = rq * 32 + lane;
+    const uint32_t t_lane = static_cast<uint32_t>(rq * 32) << 16;
+    uint32_t n_t[2] = {0u, 0u}, n_e[2] = {0u, 0u};  // O_READY and ML_FULL phases
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t k = 0; ok; ++k) {
+      const int idx = take_item<kSleepEpilogueNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k,
+                                                  ctl, ok);
+      if (!ok || idx < 0) break;
+      const ItemT<kSplit> it = get_item<kSplit>(p, idx);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!ok) continue;
+        const int nT = s == 0 ? it.nT0 : it.nT1;
+        float inv_l = 0.f;
+        if (nT > 0) {
+          n_t[s] += static_cast<uint32_t>(nT);
+          ok = wait_bar_warp<kSleepEpilogueNs>(bar(L::ML_FULL + s), n_e[s] & 1, ctl);
+          ++n_e[s];
+          ok = ok && wait_bar_warp<kSleepEpilogueNs>(bar(L::O_READY + s), (n_t[s] - 1) & 1, ctl);
+          if (!ok) continue;
+          inv_l = inv_l_smem[s * kBM + r];
+          tc_fence_after();
+        }
+        const uint32_t tO = tmem + t_lane + static_cast<uint32_t>(L::kTmemO + s * D);
+        const int row_g = it.row0 + s * kBM + r;
+        const size_t row = static_cast<size_t>(it.bh) * p.Sq + row_g;
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t v[2][16];
+          if (nT > 0) {
+            tmem_ld32(tO + cc * 32, v[0], v[1]);
+            tmem_wait_ld();
+            reg_fence16(v[0]);
+            reg_fence16(v[1]);
+          } else {  // no visible key: O = 0
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[0][e] = v[1][e] = 0u;
+          }
+          if (row_g >= p.Sq) continue;
+          float x[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(v[e >> 4][e & 15]) * inv_l;
+          if constexpr (kSplit) {
+            float4* out = reinterpret_cast<float4*>(
+                p.part_o + ((static_cast<size_t>(it.split) * p.BH) * p.Sq + row) * D + cc * 32);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              out[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+          } else {
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row * D + cc * 32);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              out[e] = make_uint4(pack2<BF16>(x[8 * e], x[8 * e + 1]),
+                                  pack2<BF16>(x[8 * e + 2], x[8 * e + 3]),
+                                  pack2<BF16>(x[8 * e + 4], x[8 * e + 5]),
+                                  pack2<BF16>(x[8 * e + 6], x[8 * e + 7]));
+          }
+        }
+        if (nT > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::O_FREE + s));
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 12) {
+    // ============================== MMA issuer ==============================
+    // per key tile PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1); at an item's last tile the
+    // next item's QK_s(0) take the place of QK_s(j+1)
+    constexpr uint32_t kIdescQK = idesc_f16(BF16, false, false, kBM, kBN);
+    constexpr uint32_t kIdescPV = idesc_f16(BF16, false, true, kBM, D);
+    const uint32_t tS[2] = {tmem, tmem + kBN};
+    const uint32_t tO[2] = {tmem + L::kTmemO, tmem + L::kTmemO + D};
+    bool issued = false;
+    auto slot_of = [&](uint32_t fill) { return static_cast<int>(fill % L::kSlots); };
+    auto full = [&](uint32_t fill) {
+      return wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fill)), (fill / L::kSlots) & 1u, ctl);
+    };
+    auto at = [&](uint32_t fill) { return sRing + static_cast<uint32_t>(slot_of(fill) * L::kChunk); };
+    // QK_s of tile `tile` (counted over the CTA's items); stage 1 is its last user
+    auto qk = [&](int s, uint32_t tile, bool last_of_stage) -> bool {
+#pragma unroll
+      for (uint32_t c = 0; c < 3; ++c) {
+        const uint32_t fill = L::kPerTile * tile + c;
+        if (!full(fill)) return false;
+        tc_fence_after();
+        umma_f16_ss_k64(tS[s], smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes) + c * L::kChunk, 16, 1024),
+                        smem_desc_sw128(at(fill), 16, 1024), kIdescQK, c > 0 ? 1u : 0u);
+        issued = true;
+        if (s == 1) umma_commit(bar(L::KV_EMPTY + slot_of(fill)));
+      }
+      umma_commit(bar(L::S_FULL + s));
+      if (last_of_stage) umma_commit(bar(L::Q_EMPTY + s));
+      return true;
+    };
+    auto pv = [&](int s, uint32_t tile, bool acc) -> bool {
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) {
+        const uint32_t fill = L::kPerTile * tile + 3 + h;
+        if (!full(fill)) return false;
+        tc_fence_after();
+        umma_f16_ts_k64(tO[s], tS[s] + h * 32, smem_desc_sw128(at(fill), L::kChunk / 2, 1024), kIdescPV,
+                        acc || h > 0 ? 1u : 0u);
+        if (s == 1) umma_commit(bar(L::KV_EMPTY + slot_of(fill)));
+      }
+      umma_commit(bar(L::O_READY + s));
+      return true;
+    };
+    auto q_full = [&](int s, uint32_t kq) {
+      return wait_bar_warp<kSleepMmaNs>(bar(L::Q_FULL + s), kq & 1u, ctl);
+    };
+    // an item's first scores of stage s
+    auto begin = [&](int s, const ItemT<kSplit>& it, uint32_t kq, uint32_t tile) -> bool {
+      if (!q_full(s, kq)) return false;
+      const int nT = s == 0 ? it.nT0 : it.nT1;
+      if (nT > 0) return qk(s, tile, nT == 1);
+      umma_commit(bar(L::Q_EMPTY + s));
+      return true;
+    };
+    uint32_t n_pv[2] = {0u, 0u};  // PV_s issued so far (PV_READY phase)
+    uint32_t n_o[2] = {0u, 0u};   // items so far with a PV_s (O_FREE phase)
+    uint32_t kq = 0, tile0 = 0;   // items begun (Q_FULL phase); the item's first tile
+    bool ok = true;
+    const int first = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), 0, ctl, ok);
+    ItemT<kSplit> cur = first >= 0 ? get_item<kSplit>(p, first) : ItemT<kSplit>{0, 0, 0, 0};
+    ok = ok && first >= 0 && begin(0, cur, 0, 0) && begin(1, cur, 0, 0);
+#pragma unroll 1
+    while (ok) {
+      bool taken = false, has_next = false;
+      ItemT<kSplit> nxt{0, 0, 0, 0};
+      auto take_next = [&]() {
+        if (taken) return;
+        taken = true;
+        const int nidx = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), kq + 1,
+                                                ctl, ok);
+        has_next = ok && nidx >= 0;
+        if (has_next) nxt = get_item<kSplit>(p, nidx);
+      };
+      const uint32_t tileN = tile0 + static_cast<uint32_t>(cur.nT1);  // the next item's first
+#pragma unroll 1
+      for (int j = 0; ok && j < cur.nT1; ++j) {
+        const bool last = j + 1 == cur.nT1;
+        if (last) take_next();
+        const uint32_t tile = tile0 + static_cast<uint32_t>(j);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int nT = s == 0 ? cur.nT0 : cur.nT1;
+          if (ok && j < nT) {
+            ok = wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + s), n_pv[s] & 1u, ctl);
+            ++n_pv[s];
+            if (ok && j == 0 && n_o[s] > 0)
+              ok = wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + s), (n_o[s] - 1) & 1u, ctl);
+            tc_fence_after();
+            ok = ok && pv(s, tile, j > 0);
+          }
+          if (ok && !last && j + 1 < nT) ok = qk(s, tile + 1, j + 2 == nT);
+          if (ok && last && has_next) ok = begin(s, nxt, kq + 1, tileN);
+        }
+      }
+      if (ok) take_next();  // an item without key tiles
+      if (!ok || !has_next) break;
+      if (cur.nT0 > 0) ++n_o[0];
+      if (cur.nT1 > 0) ++n_o[1];
+      if (cur.nT1 == 0) ok = begin(0, nxt, kq + 1, tileN) && begin(1, nxt, kq + 1, tileN);
+      ++kq;
+      cur = nxt;
+      tile0 = tileN;
+    }
+    if (issued) {  // every MMA issued so far completes before TMEM is freed
+      umma_commit(bar(L::DRAIN));
+      wait_drain(bar(L::DRAIN), 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 13) {
+    // ============================== TMA producer =============================
+    if (lane == 0) {
+      uint32_t fill = 0;
+      uint32_t nq[2] = {0u, 0u};  // Q loads issued per stage
+      bool ok = true;
+      auto load_q = [&](const ItemT<kSplit>& it, int s) -> bool {
+        if (nq[s] > 0 && !wait_bar<kSleepProducerNs>(bar(L::Q_EMPTY + s), (nq[s] - 1) & 1u, ctl)) return false;
+        mbar_arrive_expect_tx(bar(L::Q_FULL + s), L::kQBytes);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + c * L::kChunk), &tmQ,
+                      bar(L::Q_FULL + s), c * 64, it.row0 + s * kBM, it.bh);
+        ++nq[s];
+        return true;
+      };
+      // the next chunk: of K (c = 0, 1 own, 2 shared), or of V (c = 3, 4)
+      auto load = [&](const ItemT<kSplit>& it, int c, int j) -> bool {
+        const int slot = static_cast<int>(fill % L::kSlots);
+        if (!wait_bar<kSleepProducerNs>(bar(L::KV_EMPTY + slot), ((fill / L::kSlots) & 1u) ^ 1u, ctl))
+          return false;
+        const uint32_t b = bar(L::KV_FULL + slot);
+        const uint32_t dst = sRing + static_cast<uint32_t>(slot * L::kChunk);
+        const int key = (it.t0 + j) * kBN;
+        mbar_arrive_expect_tx(b, L::kChunk);
+        if (c == 2) {
+          tma_load_3d(dst, &tmR, b, 0, key, it.bh / ep.H);
+        } else if (c < 2) {
+          tma_load_3d(dst, &tmKV, b, c * 64, key, it.bh);
+          tma_load_3d(dst + L::kChunk / 2, &tmKV, b, c * 64, key + 64, it.bh);
+        } else {
+          const int k0 = key + (c - 3) * 64;
+          tma_load_3d(dst, &tmKV, b, kNope, k0, it.bh);
+          tma_load_3d(dst + L::kChunk / 2, &tmKV, b, kNope + 64, k0, it.bh);
+        }
+        ++fill;
+        return true;
+      };
+      int idx = static_cast<int>(blockIdx.x);  // the grid never exceeds the items
+#pragma unroll 1
+      for (uint32_t k = 0; ok; ++k) {
+        const uint32_t slot = k % kItemRing;
+        if (k >= kItemRing &&
+            !wait_bar<kSleepProducerNs>(bar(L::ITEM_EMPTY + slot), (k / kItemRing - 1) & 1u, ctl)) {
+          ok = false;
+          break;
+        }
+        item_ring[slot] = idx;
+        mbar_arrive(bar(L::ITEM_FULL + slot));
+        if (idx < 0) break;
+        const ItemT<kSplit> it = get_item<kSplit>(p, idx);
+        ok = load_q(it, 0);
+#pragma unroll 1
+        for (int j = 0; ok && j < it.nT1; ++j) {
+#pragma unroll 1
+          for (int c = 0; ok && c < L::kPerTile; ++c) {
+            if (j == 0 && c == 3) ok = load_q(it, 1);
+            if (ok) ok = load(it, c, j);
+          }
+        }
+        if (ok && it.nT1 == 0) ok = load_q(it, 1);
+        idx = claim_item(p);
+        if (idx < 0) grid_launch_dependents();  // the next grid may take the SMs
+      }
+      // drain: every load issued lands before shared memory goes away
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (nq[s] > 0) wait_drain(bar(L::Q_FULL + s), (nq[s] - 1) & 1u, p.timeout_ns);
+#pragma unroll 1
+      for (uint32_t i = fill > L::kSlots ? fill - L::kSlots : 0u; i < fill; ++i)
+        wait_drain(bar(L::KV_FULL + static_cast<int>(i % L::kSlots)), (i / L::kSlots) & 1u, p.timeout_ns);
+    }
+    __syncwarp();
+  }
+
+  // ---- teardown ----
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, L::kTmemCols);
+  }
+  if (threadIdx.x == 0) {
+    // the launch's last CTA clears the scheduler slot
+    __threadfence();
+    if (atomicAdd(&p.sched[1], 1ull) == gridDim.x - 1) {
+      p.sched[0] = 0ull;
+      p.sched[1] = 0ull;
+      __threadfence();
+    }
+  }
+}
+
+}  // namespace fa

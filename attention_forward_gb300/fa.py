@@ -125,6 +125,10 @@ def load_path(path: str) -> ctypes.CDLL:
     L.fa_latent_workspace_bytes.restype = sz
     L.fa_fwd_latent.argtypes = [vp] * 6 + [ci] * 6 + [cf, ci, vp, sz, vp]
     L.fa_fwd_latent.restype = ci
+    L.fa_expanded_workspace_bytes.argtypes = [ci] * 4
+    L.fa_expanded_workspace_bytes.restype = sz
+    L.fa_fwd_expanded.argtypes = [vp] * 5 + [ci] * 4 + [cf, ci, ci, vp, sz, vp]
+    L.fa_fwd_expanded.restype = ci
     L.fa_version.argtypes = []
     L.fa_version.restype = ci
     return L
@@ -870,6 +874,42 @@ def fa_fwd_latent(q, cache, page_table, length, scale: float | None = None, work
     _attend_pages("fa_fwd_latent", lambda *ws: L.fa_fwd_latent(*args, *ws),
                   lambda: L.fa_latent_workspace_bytes(B, H, Sq, page, per), dev, q, stream,
                   workspace)
+    return out, lse
+
+
+def fa_expanded_workspace_bytes(B: int, H: int, Sq: int, Skv: int) -> int:
+    return int(load().fa_expanded_workspace_bytes(B, H, Sq, Skv))
+
+
+def fa_fwd_expanded(q, kv, k_rope, causal: bool = False, scale: float | None = None,
+                    workspace=None, out=None, lse=None, stream=None):
+    """Latent attention, expanded: q [B, H, Sq, 192], kv [B, H, Skv, 256] (a head's key
+    of 128 channels, then its value), k_rope [B, Skv, 64] (the keys' shared part).
+    scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 128], lse)."""
+    dev, (B, H, Sq, D) = _rows16(q, "q")
+    _, shape = _rows16(kv, "kv")
+    Skv = shape[2]
+    if D != 192:
+        raise ValueError("q must be [B, H, Sq, 192]")
+    kvp = _ptr(kv, "kv", dev, q.dtype, (B, H, Skv, 256))
+    rp = _ptr(k_rope, "k_rope", dev, q.dtype, (B, Skv, LATENT_ROPE))
+    if _current_device() != dev:
+        return _on(dev, fa_fwd_expanded, q, kv, k_rope, causal, scale, workspace, out, lse, stream)
+    sc = _LATENT_SCALE if scale is None else float(scale)
+    L = _lib or load()
+    out, lse = _outputs_wide(q, 128, dev, out, lse, stream)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    args = (q.data_ptr(), kvp, rp, out.data_ptr(), lse.data_ptr(), B, H, Sq, Skv, sc, bool(causal),
+            _DTYPE[q.dtype])
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        need = L.fa_expanded_workspace_bytes(B, H, Sq, Skv)
+        st = _graph_workspace(lambda p, n: L.fa_fwd_expanded(*args, p, n, handle), need, q.device,
+                              stream)
+    else:
+        st = L.fa_fwd_expanded(*args, ws, ws_bytes, handle)
+    if st:
+        _check(st, "fa_fwd_expanded")
     return out, lse
 
 

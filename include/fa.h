@@ -538,8 +538,28 @@ fa_status_t fa_fwd_latent(const void *q, const void *pages,
                           fa_stream_t stream);
 
 /*
+ * fa_fwd_expanded -- the expanded form, for prompts: every head's keys and values
+ * made from the latents by one product, the rotated part shared.
+ *   q [B, H, Sq, 192]: 128 channels, then the 64 rotated ones
+ *   kv [B, H, Skv, 256]: a head's key (128), then its value (128)
+ *   k_rope [B, Skv, 64]: what the heads' keys share
+ *   o [B, H, Sq, 128], lse [B, H, Sq]
+ *   x = scale * (<q[0 ... 127], key_j> + <q[128 ... 191], k_rope_j>)
+ * with fa_fwd's masks and limits.  A masked key may hold anything; values must be
+ * finite in every row.  A call whose items are fewer than the multiprocessors
+ * splits the keys when it has fa_expanded_workspace_bytes(...) of workspace
+ * (256-byte aligned; NULL: the library's own for the stream, inside a capture
+ * none).  Captured as fa_fwd_score is (fa_fwd's limits on scheduler slots hold).
+ */
+size_t fa_expanded_workspace_bytes(int B, int H, int Sq, int Skv);
+fa_status_t fa_fwd_expanded(const void *q, const void *kv, const void *k_rope,
+                            void *o, float *lse, int B, int H, int Sq, int Skv,
+                            float scale, int causal, int dtype, void *workspace,
+                            size_t workspace_bytes, fa_stream_t stream);
+
+/*
  * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score,
- * fa_fwd_cache, fa_fwd_paged and fa_fwd_latent keep on the current device (one
+ * fa_fwd_cache, fa_fwd_paged, fa_fwd_latent and fa_fwd_expanded keep on the current device (one
  * per stream that they were called
  * on), after synchronising the device.  The next fa_fwd that needs one
  * allocates it again.  Returns FA_ERR_CUDA if the synchronisation or a free

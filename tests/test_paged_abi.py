@@ -101,7 +101,24 @@ def test_latent_attention_refusals(lib, kw, want):
                              a["dtype"], None, 0, None) == want
 
 
+@pytest.mark.parametrize("kw,want", [
+    (dict(q=0), 1), (dict(q=8), 1), (dict(k=0), 1), (dict(k=8), 1), (dict(v=0), 1), (dict(v=8), 1),
+    (dict(o=0), 1), (dict(o=8), 1), (dict(lse=0), 1), (dict(lse=4), 1), (dict(B=0), 1),
+    (dict(H=0), 1), (dict(B=1 << 14), 1), (dict(Sq=0), 1), (dict(S=0), 1), (dict(S=(1 << 24) + 1), 1),
+    (dict(Sq=(1 << 24) + 1), 1), (dict(scale=0.0), 1), (dict(scale=NAN), 1), (dict(scale=INF), 1),
+    (dict(dtype=2), 2), (dict(ws=128), 4)])
+def test_expanded_refusals(lib, kw, want):
+    a = base(ws=None, **kw) if "ws" not in kw else base(**kw)
+    assert lib.fa_fwd_expanded(a["q"], a["v"], a["k"], a["o"], a["lse"], a["B"], a["H"], a["Sq"],
+                               a["S"], F(a["scale"]), 1, a["dtype"], a["ws"], 0, None) == want
+
+
 def test_workspace_sizes():
+    assert fa.fa_expanded_workspace_bytes(0, 4, 8, 8) == 0
+    assert fa.fa_expanded_workspace_bytes(1, 4, 100, 100) == 0        # one key tile
+    assert fa.fa_expanded_workspace_bytes(8, 32, 4096, 4096) == 0     # items enough
+    n = fa.fa_expanded_workspace_bytes(1, 4, 100, 16384)
+    assert n >= 2 * 4 * 100 * 129 * 4 and n % 256 == 0
     assert fa.fa_paged_workspace_bytes(1, 4, 3, 1, 64, 16, 4) == 0    # refused sizes need none
     assert fa.fa_paged_workspace_bytes(1, 4, 1, 257, 64, 16, 400) == 0
     assert fa.fa_paged_workspace_bytes(1, 4, 1, 1, 64, 16, 4) == 0    # short: not split
@@ -150,6 +167,8 @@ def test_binding_refusals():
                  lambda: fa.fa_latent_read(latent, table),
                  lambda: fa.fa_latent_read(latent, table, out=[c, r]),
                  lambda: fa.fa_fwd_latent(q, latent, table, length),
-                 lambda: fa.fa_fwd_latent(wide, latent, table, length)):
+                 lambda: fa.fa_fwd_latent(wide, latent, table, length),
+                 lambda: fa.fa_fwd_expanded(torch.zeros(1, 4, 8, 192, dtype=bf),
+                                            torch.zeros(1, 4, 8, 256, dtype=bf), r)):
         with pytest.raises(ValueError):
             call()
