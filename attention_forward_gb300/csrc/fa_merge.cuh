@@ -25,9 +25,8 @@ struct MergeSmem {
 // A warp's share of a row: parts first, first + step, ... of n_parts.  Returns
 // their largest LSE, against which o and sum are weighted (-inf: none has a
 // key).  part_row(s): the row of part s in part_o [., D] (fp32, O / l) and
-// part_lse [.]; LSE = -inf with O = 0 where a part has no visible key.  kStride: the
-// channels of a row, of which D are merged (part_o and o_out begin at the first).
-template <int D, int kStride = D, class PartRow>
+// part_lse [.]; LSE = -inf with O = 0 where a part has no visible key.
+template <int D, class PartRow>
 __device__ __forceinline__ float merge_parts(const float* part_o, const float* part_lse,
                                              int n_parts, int first, int step, PartRow part_row,
                                              float (&o)[D / 32], float& sum) {
@@ -49,7 +48,7 @@ __device__ __forceinline__ float merge_parts(const float* part_o, const float* p
       if (s < n_parts) {
         const long long at = part_row(s);
         lse[k] = part_lse[at];
-        const float* po = part_o + at * kStride + lane * kDims;
+        const float* po = part_o + at * D + lane * kDims;
         if constexpr (kDims == 4) {
           const float4 v = *reinterpret_cast<const float4*>(po);
           x[k][0] = v.x; x[k][1] = v.y; x[k][2] = v.z; x[k][3] = v.w;
@@ -90,15 +89,15 @@ __device__ __forceinline__ uint32_t merge_pack(float a, float b) {
   }
 }
 
-// The row by the whole block.  lse_out: null where another block writes it.
-template <int D, bool BF16, int kStride = D, class PartRow>
+// The row by the whole block.
+template <int D, bool BF16, class PartRow>
 __device__ __forceinline__ void merge_row(const float* part_o, const float* part_lse, int n_parts,
                                           PartRow part_row, void* o_out, float* lse_out,
                                           long long row, MergeSmem<D>& sm) {
   constexpr int kDims = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float o[kDims], sum;
-  float top = merge_parts<D, kStride>(part_o, part_lse, n_parts, warp, kMergeWarps, part_row, o, sum);
+  float top = merge_parts<D>(part_o, part_lse, n_parts, warp, kMergeWarps, part_row, o, sum);
 #pragma unroll
   for (int d = 0; d < kDims; ++d) sm.part[warp][lane * kDims + d] = o[d];
   if (lane == 0) {
@@ -123,28 +122,28 @@ __device__ __forceinline__ void merge_row(const float* part_o, const float* part
   }
   // no part has a key: 0; a NaN stays one
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  reinterpret_cast<uint32_t*>(o_out)[(row * kStride + ch) / 2] = merge_pack<BF16>(a * inv, b * inv);
-  if (ch == 0 && lse_out) lse_out[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+  reinterpret_cast<uint32_t*>(o_out)[(row * D + ch) / 2] = merge_pack<BF16>(a * inv, b * inv);
+  if (ch == 0) lse_out[row] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 // The row by one warp.
-template <int D, bool BF16, int kStride = D, class PartRow>
+template <int D, bool BF16, class PartRow>
 __device__ __forceinline__ void merge_row_warp(const float* part_o, const float* part_lse,
                                                int n_parts, PartRow part_row, void* o_out,
                                                float* lse_out, long long row) {
   constexpr int kDims = D / 32;
   const int lane = threadIdx.x & 31;
   float o[kDims], sum;
-  const float top = merge_parts<D, kStride>(part_o, part_lse, n_parts, 0, 1, part_row, o, sum);
+  const float top = merge_parts<D>(part_o, part_lse, n_parts, 0, 1, part_row, o, sum);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint32_t* out = reinterpret_cast<uint32_t*>(o_out) + (row * kStride + lane * kDims) / 2;
+  uint32_t* out = reinterpret_cast<uint32_t*>(o_out) + (row * D + lane * kDims) / 2;
   if constexpr (kDims == 4) {
     *reinterpret_cast<uint2*>(out) = make_uint2(merge_pack<BF16>(o[0] * inv, o[1] * inv),
                                                 merge_pack<BF16>(o[2] * inv, o[3] * inv));
   } else {
     *out = merge_pack<BF16>(o[0] * inv, o[1] * inv);
   }
-  if (lane == 0 && lse_out) lse_out[row] = sum == 0.f ? -INFINITY : top + logf(sum);
+  if (lane == 0) lse_out[row] = sum == 0.f ? -INFINITY : top + logf(sum);
 }
 
 }  // namespace fa

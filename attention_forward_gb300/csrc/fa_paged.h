@@ -49,9 +49,10 @@ struct PagedReadParams {
 };
 
 struct PagedAttnParams {
+  const void* q;      // [B, H, Sq, keys' width]
   void* o;            // [B, H, Sq, values' width]
   float* lse;         // [B, H, Sq]
-  float* part_o;      // [2 * grid, rows of a CTA, values' width] fp32, O / l of a segment
+  float* part_o;      // [2 * grid, values' width, part_rows] fp32, O / l of a segment
   float* part_lse;    // [2 * grid, rows of a CTA]
   const int* page_table;
   const int* length;  // [B]
@@ -60,11 +61,13 @@ struct PagedAttnParams {
   unsigned long long timeout_ns;
   int B, H, Hkv, Sq;
   int rows;           // (H / Hkv) * Sq query rows per kv head
+  int part_rows;      // rows that a part holds: a CTA's, up to a multiple of 4
   int n_row_blocks;
   int sms;
   int whole;          // CTAs take whole units: no parts, no merge
   int num_pages, page_shift, max_pages;
   int pool_rows;      // rows of the pool: the coordinate of what does not exist
+  int k_at, v_at;     // the arrays' places in their descriptors
   float scale, cap, inv_cap, cap_arg;
 };
 
@@ -76,8 +79,7 @@ cudaError_t launch_paged_read(bool latent, const PagedReadParams& p, cudaStream_
 // an SM holds.  kind: 64 or 128, a head's channels; kLatent, latent rows.
 int paged_attn_row_block(int kind, int rows);
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
-cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
-                              const CUtensorMap& v, const PagedAttnParams& p, int grid,
-                              cudaStream_t stream);
+cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,
+                              const PagedAttnParams& p, int grid, cudaStream_t stream);
 
 }  // namespace fa

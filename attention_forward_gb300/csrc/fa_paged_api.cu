@@ -9,19 +9,18 @@
 
 namespace fa {
 
-cudaError_t launch_paged_attn_d64(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+cudaError_t launch_paged_attn_d64(bool, const CUtensorMap&, const CUtensorMap&,
                                   const PagedAttnParams&, int, cudaStream_t);
-cudaError_t launch_paged_attn_d128(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+cudaError_t launch_paged_attn_d128(bool, const CUtensorMap&, const CUtensorMap&,
                                    const PagedAttnParams&, int, cudaStream_t);
-cudaError_t launch_paged_attn_latent(bool, const CUtensorMap&, const CUtensorMap&,
+cudaError_t launch_paged_attn_latent(bool, const CUtensorMap&,
                                      const PagedAttnParams&, int, cudaStream_t);
 
-cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
-                              const CUtensorMap& v, const PagedAttnParams& p, int grid,
-                              cudaStream_t stream) {
-  if (kind == kLatent) return launch_paged_attn_latent(bf16, q, k, p, grid, stream);
-  return kind == 128 ? launch_paged_attn_d128(bf16, q, k, v, p, grid, stream)
-                     : launch_paged_attn_d64(bf16, q, k, v, p, grid, stream);
+cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,
+                              const PagedAttnParams& p, int grid, cudaStream_t stream) {
+  if (kind == kLatent) return launch_paged_attn_latent(bf16, k, p, grid, stream);
+  return kind == 128 ? launch_paged_attn_d128(bf16, k, v, p, grid, stream)
+                     : launch_paged_attn_d64(bf16, k, v, p, grid, stream);
 }
 
 int paged_attn_row_block(int kind, int rows) {
@@ -32,7 +31,7 @@ int paged_attn_row_block(int kind, int rows) {
 // CTAs an SM holds (PagedShape's last number).
 static int paged_attn_ctas(int kind, int block) {
   if (kind == kLatent) return 1;
-  return block == 16 || kind == 64 ? 2 : 1;
+  return block == 16 ? 2 : 1;
 }
 
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count) {
@@ -141,7 +140,7 @@ bool chunks_ok(int kind, int B, int H, int Hkv, int Sq, const PageShape& s) {
 
 // The attention's persistent CTAs and the memory for their parts.
 struct AttnPlan {
-  int row_blocks, grid, whole;
+  int row_blocks, part_rows, grid, whole;
   size_t o_bytes, bytes;
 };
 
@@ -150,13 +149,14 @@ AttnPlan plan_attn(int kind, int B, int H, int Hkv, int Sq, const PageShape& s, 
   const int rows = (H / Hkv) * Sq, block = fa::paged_attn_row_block(kind, rows);
   const int room = s.max_pages * s.page_size;
   a.row_blocks = (rows + block - 1) / block;
+  a.part_rows = (std::min(rows, block) + 3) & ~3;
   a.grid = fa::paged_attn_grid(kind, rows, static_cast<long long>(B) * Hkv * a.row_blocks, room,
                                sm_count);
   a.whole = room <= fa::kCacheWholeKeys ? 1 : 0;
   if (!a.whole) {
-    const size_t n = 2u * static_cast<size_t>(a.grid) * block;
-    a.o_bytes = up256(n * kind * sizeof(float));
-    a.bytes = a.o_bytes + up256(n * sizeof(float));
+    const size_t parts = 2u * static_cast<size_t>(a.grid);
+    a.o_bytes = up256(parts * a.part_rows * kind * sizeof(float));
+    a.bytes = a.o_bytes + up256(parts * block * sizeof(float));
   }
   return a;
 }
@@ -190,6 +190,7 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
     return FA_ERR_WORKSPACE;
 
   fa::PagedAttnParams p{};
+  p.q = q;
   p.o = o;
   p.lse = lse;
   if (plan.bytes > 0) {
@@ -206,6 +207,7 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
   p.Hkv = Hkv;
   p.Sq = Sq;
   p.rows = (H / Hkv) * Sq;
+  p.part_rows = plan.part_rows;
   p.n_row_blocks = plan.row_blocks;
   p.sms = env.sm_count;
   p.whole = plan.whole;
@@ -221,16 +223,24 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
   }
   const bool bf16 = dtype == FA_BF16;
   const int k_chunks = kind == fa::kLatent ? fa::kLatentRow / 64 : kind / 64;
-  CUtensorMap tq, tk, tv;
-  if ((st = fa::encode_chunks(&tq, q, static_cast<long long>(B) * H * Sq, k_chunks,
-                              fa::paged_attn_row_block(kind, p.rows), bf16)) != FA_OK)
-    return st;
-  if ((st = fa::encode_chunks(&tk, k, p.pool_rows, k_chunks, 8, bf16)) != FA_OK) return st;
+  // one descriptor for both pools, two where they lie too far apart (each takes the
+  // host over a microsecond)
+  CUtensorMap tk, tv;
+  const bool one = kind == fa::kLatent || k == v;
+  const char *kb = static_cast<const char*>(k), *vb = static_cast<const char*>(v);
+  st = fa::encode_pools(&tk, std::min(kb, vb), one ? nullptr : std::max(kb, vb), p.pool_rows, k_chunks,
+                        bf16);
   tv = tk;
-  if (kind != fa::kLatent && (st = fa::encode_chunks(&tv, v, p.pool_rows, k_chunks, 8, bf16)) != FA_OK)
-    return st;
-  return fa::launch_paged_attn(kind, bf16, tq, tk, tv, p, plan.grid, stream) == cudaSuccess ? FA_OK
-                                                                                            : FA_ERR_CUDA;
+  if (st == FA_OK && !one) {
+    p.k_at = kb > vb ? 1 : 0;
+    p.v_at = 1 - p.k_at;
+  } else if (st == FA_ERR_UNSUPPORTED) {
+    if ((st = fa::encode_pools(&tk, k, nullptr, p.pool_rows, k_chunks, bf16)) == FA_OK)
+      st = fa::encode_pools(&tv, v, nullptr, p.pool_rows, k_chunks, bf16);
+  }
+  if (st != FA_OK) return st;
+  return fa::launch_paged_attn(kind, bf16, tk, tv, p, plan.grid, stream) == cudaSuccess ? FA_OK
+                                                                                        : FA_ERR_CUDA;
 }
 
 }  // namespace

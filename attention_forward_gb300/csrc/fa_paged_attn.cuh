@@ -18,9 +18,9 @@
 //        one reference maximum a row, raised for the whole CTA when a score passes it
 //        by 15 (log2 units; then O is rescaled in place), set 8 below the maximum so
 //        that fp16 holds p over 2^-24 ... 2^15 around it; p goes to shared memory
-//        transposed (stmatrix).  At a segment's end they write O.
-//   4    MMA issue, the queries' load, tensor memory
-//   5    TMA producer: a ring of tiles, by boxes of 8 rows (all channels): any page
+//        transposed (stmatrix).  They also load a segment's queries and write its O.
+//   4    MMA issue, tensor memory
+//   5, 6 TMA producers, of K and of V (one for latent rows): rings of tiles, by boxes of 8 rows (all channels): any page
 //        size is a multiple of them.  A box past the sequence or of a page that does
 //        not exist is fetched from past the pool's end, as zeros.
 // The tensor core runs S(j + 1) while the softmax works on S(j), when the tile is
@@ -29,25 +29,26 @@
 // Every wait is bounded by the watchdog, as in the prefill kernels.
 #pragma once
 #include "fa_keys.cuh"
-#include "fa_merge.cuh"
 #include "fa_paged.h"
 #include "fa_prefill.cuh"
 
 namespace fa {
 
-constexpr int kPagedThreads = 192;
 constexpr int kPagedKeys = kCacheAttnKeys;  // 64 keys: a tile, and a chunk of the deal
 
 // kKC, kVC: 64-channel chunks of a key and of a value; kShared: the value is the
 // key's first chunks.  kN: query rows of a CTA.
-template <int kKC_, int kVC_, bool kShared_, int kN_, int kStages_, int kCtas_>
+template <int kKC_, int kVC_, bool kShared_, int kN_, int kStages_, int kCtas_, int kPs_ = 2>
 struct PagedShape {
   static constexpr int kKC = kKC_, kVC = kVC_, kN = kN_, kStages = kStages_, kCtas = kCtas_;
+  static constexpr int kPs = kPs_;  // buffers for P
   static constexpr bool kShared = kShared_;
+  static constexpr int kWarps = kShared ? 6 : 7, kThreads = 32 * kWarps;
   static constexpr int kDv = 64 * kVC;
   static constexpr int kTileK = kPagedKeys * 128 * kKC;
   static constexpr int kTileV = kShared ? 0 : kPagedKeys * 128 * kVC;
   static constexpr int kStageBytes = kTileK + kTileV;
+  static constexpr int kVTile = kShared ? kTileK : kTileV;       // from a tile's V to the next
   static constexpr int kVStride = (kShared ? kKC : kVC) * 1024;  // from 8 keys to the next 8
   static constexpr int kQBytes = kN * 128 * kKC;
   static constexpr int kPBytes = kN * 128;
@@ -56,25 +57,33 @@ struct PagedShape {
   static constexpr int kCols = kColO + kBlocks * kN;
   static constexpr int kTmemCols =
       kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static constexpr int kOffP = kQBytes, kOffRing = kOffP + kPBytes;
+  static constexpr int kOffP = kQBytes, kOffRing = kOffP + kPs * kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kStageBytes;
   static_assert(kVC == 1 || kVC % 2 == 0, "values of 64 channels, or of 128 a block");
   static_assert(kOffP % 1024 == 0 && kOffRing % 1024 == 0, "128-byte swizzled tiles");
   static_assert(kCols <= 512 && kCtas * kTmemCols <= 512, "tensor memory");
 };
 
+// K and V have rings of their own.  A latent stage is given back 16 keys at a time:
+// k_empty[4 stage + 16-key block].
 struct PagedMiscBars {
-  static constexpr int kMaxStages = 12;
-  alignas(8) unsigned long long kv_full[kMaxStages], kv_empty[kMaxStages];
-  unsigned long long s_full[2], p_ready, o_done, q_full, q_empty, drain;
+  static constexpr int kMaxStages = 8;
+  alignas(8) unsigned long long k_full[kMaxStages], k_empty[kMaxStages];
+  unsigned long long v_full[kMaxStages], v_empty[kMaxStages];
+  unsigned long long s_full[2], p_ready[2], o_done[2], q_full, drain;
 };
 
-template <int kN, bool kSlopes>
+constexpr int kPagedBad = 16;
+static_assert(kPagedBad >= PagedMiscBars::kMaxStages + 3, "notes of the tiles in flight");
+
+template <int kN, int kWarps, bool kSlopes>
 struct PagedMisc {
   PagedMiscBars bars;
-  KeyScan<kPagedThreads / 32> scan;
+  KeyScan<kWarps> scan;
   uint32_t tmem, abort;
-  uint32_t bad[PagedMiscBars::kMaxStages];  // a bit for each 8 keys whose page does not exist
+  // of a tile, a bit for each 8 keys whose page does not exist: written before its keys
+  // are sent for, read after their scores, at most a ring and three tiles later
+  volatile uint32_t bad[kPagedBad];
   float red[4][kN];
   float factor[kN];  // a rescale's, then a row's 1 / l
   union {
@@ -86,7 +95,7 @@ struct PagedMisc {
 
 template <class S>
 constexpr int paged_smem_bytes() {
-  return S::kOffMisc + static_cast<int>(sizeof(PagedMisc<S::kN, !S::kShared>)) + 1024;  // + alignment
+  return S::kOffMisc + static_cast<int>(sizeof(PagedMisc<S::kN, S::kWarps, !S::kShared>)) + 1024;  // + alignment
 }
 
 // The CTA's segments: ranges of one unit's keys.
@@ -95,7 +104,7 @@ struct PagedWalk {
   int b, len, before;    // the sequence, its length, the chunks of those before it
 };
 struct PagedSeg {
-  int hk, row0, n_rows, len, k_begin, k_end, n_tiles, part;
+  int seq, hk, row0, n_rows, len, k_begin, k_end, n_tiles, part;
   bool whole;
   long long out_row0;
   const int* pages;
@@ -118,6 +127,7 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
   s.row0 = rb * kN;
   s.n_rows = min(kN, p.rows - s.row0);
   s.out_row0 = (static_cast<long long>(w.b) * p.Hkv + s.hk) * p.rows + s.row0;
+  s.seq = w.b;
   s.len = w.len;
   s.k_begin = chunk0 * kPagedKeys;
   s.k_end = min(w.len, s.k_begin + n_chunks * kPagedKeys);
@@ -136,9 +146,8 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
 }
 
 template <class S, bool BF16, bool kMod>
-__global__ void __launch_bounds__(kPagedThreads, S::kCtas)
-    fa_paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
-                         const __grid_constant__ CUtensorMap tmK,
+__global__ void __launch_bounds__(S::kThreads, S::kCtas)
+    fa_paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
   constexpr int kN = S::kN, kNB = kN / 8, kStages = S::kStages;
   constexpr float kLog2e = 1.4426950408889634f;
@@ -147,26 +156,31 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sQ = smem_u32(smem), sP = sQ + S::kOffP, sRing = sQ + S::kOffRing;
-  using Misc = PagedMisc<kN, !S::kShared>;
+  const uint32_t sQ = smem_u32(smem), sP = sQ + S::kOffP, sK = sQ + S::kOffRing;
+  const uint32_t sV = S::kShared ? sK : sK + kStages * S::kTileK;  // V's ring
+  using Misc = PagedMisc<kN, S::kWarps, !S::kShared>;
   Misc& sm = *reinterpret_cast<Misc*>(smem + S::kOffMisc);
-  const uint32_t kv_full = smem_u32(sm.bars.kv_full), kv_empty = smem_u32(sm.bars.kv_empty);
-  const uint32_t s_full = smem_u32(sm.bars.s_full), p_ready = smem_u32(&sm.bars.p_ready);
-  const uint32_t o_done = smem_u32(&sm.bars.o_done), q_full = smem_u32(&sm.bars.q_full);
-  const uint32_t q_empty = smem_u32(&sm.bars.q_empty), drain = smem_u32(&sm.bars.drain);
+  const uint32_t k_full = smem_u32(sm.bars.k_full), k_empty = smem_u32(sm.bars.k_empty);
+  const uint32_t v_full = smem_u32(sm.bars.v_full), v_empty = smem_u32(sm.bars.v_empty);
+  const uint32_t s_full = smem_u32(sm.bars.s_full), p_ready = smem_u32(sm.bars.p_ready);
+  const uint32_t o_done = smem_u32(sm.bars.o_done), q_full = smem_u32(&sm.bars.q_full);
+  const uint32_t drain = smem_u32(&sm.bars.drain);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(kv_full + 8 * i, 1);
-      mbar_init(kv_empty + 8 * i, 1);
+    for (int i = 0; i < PagedMiscBars::kMaxStages; ++i) {
+      mbar_init(k_full + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(v_full + 8 * i, 1);
+      mbar_init(v_empty + 8 * i, 1);
     }
     mbar_init(s_full, 1);
     mbar_init(s_full + 8, 1);
     mbar_init(p_ready, 4);
+    mbar_init(p_ready + 8, 4);
     mbar_init(o_done, 1);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(o_done + 8, 1);
+    mbar_init(q_full, 4);
     mbar_init(drain, 1);
     sm.abort = 0u;
     fence_mbar_init();
@@ -176,7 +190,6 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
     tmem_relinquish();
   }
   if (warp == 5 && lane == 0) {
-    tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     if constexpr (!S::kShared) tma_prefetch_desc(&tmV);
   }
@@ -216,9 +229,38 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
     const float fac = kMod && p.cap > 0.f ? p.scale : p.scale * kLog2e;
     uint32_t t = 0;  // tiles so far
     bool ok = true;
+    // a segment's queries, K-major and 128-byte swizzled, zeros past its rows; the
+    // scores of the segment before are all read
+    auto load_q = [&](const PagedSeg& s) {
+      if (s.n_tiles == 0) return;
+      constexpr int kWords = 8 * S::kKC, kAtOnce = kN * kWords / 128 < 9 ? kN * kWords / 128 : 9;
+      static_assert(kN * kWords % (128 * kAtOnce) == 0, "words of the queries");
+      const uint4* q = static_cast<const uint4*>(p.q) + s.out_row0 * kWords;
 #pragma unroll 1
-    while (ok && paged_next<kN>(p, walk, seg)) {
-      if (p.whole && threadIdx.x == 0 && seg.len != p.length[walk.b])
+      for (int i0 = threadIdx.x; i0 < kN * kWords; i0 += 128 * kAtOnce) {
+        uint4 x[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int i = i0 + 128 * k;
+          x[k] = i / kWords < s.n_rows ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int i = i0 + 128 * k, n = i / kWords, w = i - n * kWords;
+          st_shared_v4(sQ + static_cast<uint32_t>((w >> 3) * (kN * 128) + n * 128 + (((w ^ n) & 7) << 4)),
+                       x[k].x, x[k].y, x[k].z, x[k].w);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+    PagedSeg next;
+    bool more = paged_next<kN>(p, walk, seg);
+    if (more) load_q(seg);
+#pragma unroll 1
+    while (more) {
+      if (p.whole && threadIdx.x == 0 && seg.len != p.length[seg.seq])
         atomicMax(p.status, kStatusBadIndex);
       for (int n = threadIdx.x; n < kN; n += 128) {
         const int rr = min(n, seg.n_rows - 1) + seg.row0;
@@ -238,12 +280,10 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
         const uint32_t stage = t % kStages, buf = t & 1u;
         const int key0 = seg.k_begin + j * kPagedKeys;
         ok = ok && wait_bar_warp(s_full + 8 * buf, (t >> 1) & 1u, ctl);
-        // (long since complete: makes the producer's note of bad pages visible)
-        ok = ok && wait_bar_warp(kv_full + 8 * stage, (t / kStages) & 1u, ctl);
         tc_fence_after();
         uint32_t raw[kNB][4];
         tmem_ld_frag(tmem + t_lane + buf * kN, raw);
-        const uint32_t bad = sm.bad[stage];
+        const uint32_t bad = sm.bad[t % kPagedBad];
         tmem_wait_ld();
         float s[kNB][4];
 #pragma unroll
@@ -279,7 +319,8 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
           // rows with its last (their scores are read, whose operand they were)
           const int tail = (key0 + kPagedKeys > seg.len ? seg.len - key0 : 0) & 7;
           if (tail != 0) {
-            const uint32_t rows = sRing + stage * S::kStageBytes + (S::kShared ? 0 : S::kTileK) +
+            if constexpr (!S::kShared) ok = ok && wait_bar_warp(v_full + 8 * stage, (t / kStages) & 1u, ctl);
+            const uint32_t rows = sV + stage * S::kVTile +
                                   static_cast<uint32_t>((seg.len - key0) >> 3) * S::kVStride;
             for (int i = threadIdx.x; i < (8 - tail) * S::kVC * 8; i += 128) {
               const int r = tail + i / (S::kVC * 8), c = i % (S::kVC * 8);
@@ -327,7 +368,7 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
             }
           named_bar_sync(1, 128);
           if (j > 0) {
-            ok = wait_bar_warp(o_done, (t - 1) & 1u, ctl);
+            ok = wait_bar_warp(o_done + 8 * ((t - 1) & 1u), ((t - 1) >> 1) & 1u, ctl);
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < S::kBlocks * kN; c += 16) {
@@ -355,20 +396,26 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
           pk[n][0] = pack2<BF16>(e[0], e[1]);
           pk[n][1] = pack2<BF16>(e[2], e[3]);
         }
-        // the product before has read its P (a segment's first: its end waited)
-        if (j > 0) ok = ok && wait_bar_warp(o_done, (t - 1) & 1u, ctl);
+        // the product that had this buffer has read it (a segment's first ones: its end
+        // waited)
+        if (j >= S::kPs)
+          ok = ok && wait_bar_warp(o_done + 8 * ((t - S::kPs) & 1u), ((t - S::kPs) >> 1) & 1u, ctl);
+        const uint32_t p_buf = p_at + (S::kPs > 1 ? buf * S::kPBytes : 0u);
 #pragma unroll
         for (int n = 0; n < kNB; n += 2)
-          stmatrix_trans4(p_at + n * 1024, pk[n][0], pk[n][1], pk[n + 1][0], pk[n + 1][1]);
+          stmatrix_trans4(p_buf + n * 1024, pk[n][0], pk[n][1], pk[n + 1][0], pk[n + 1][1]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready);
+        if (lane == 0) mbar_arrive(p_ready + 8 * buf);
       }
 
       // ---- the segment's end: sums over the keys, then O^T out ----
       ok = !named_bar_or(1, 128, !ok);
       if (!ok) break;
+      // the next segment's queries first: its scores run beside what follows
+      more = paged_next<kN>(p, walk, next);
+      if (more) load_q(next);
 #pragma unroll
       for (int n = 0; n < kNB; ++n)
 #pragma unroll
@@ -396,42 +443,71 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
       }
       named_bar_sync(1, 128);
       if (seg.n_tiles > 0) {
-        ok = wait_bar_warp(o_done, (t - 1) & 1u, ctl);
+        ok = wait_bar_warp(o_done + 8 * ((t - 1) & 1u), ((t - 1) >> 1) & 1u, ctl);
         tc_fence_after();
       }
-      // a lane's channel of each block; with 64 channels a warp has 16
-      const int ch = S::kVC == 1 ? 16 * warp + lane : 32 * warp + lane;
-#pragma unroll 1
-      for (int blk = 0; blk < S::kBlocks; ++blk)
-#pragma unroll 1
-        for (int c = 0; c < kN; c += 16) {
-          uint32_t v[16];
-          if (seg.n_tiles > 0) {
-            tmem_ld16(tmem + t_lane + S::kColO + blk * kN + c, v);
-            tmem_wait_ld();
-            reg_fence16(v);
-          } else {
+      // 16 channels at a time as fragments.  O: transposed through the warp's share of
+      // P's memory, 32 bytes a row; parts: as they are, [channel, row].
+      float inv[kNB][2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = 0u;
-          }
-          if (ok && (S::kVC > 1 || lane < 16)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = sm.factor[c + e] == 0.f ? 0.f : __uint_as_float(v[e]) * sm.factor[c + e];
-              if (c + e < seg.n_rows) {
-                if (seg.whole) {
-                  const uint32_t w = pack2<BF16>(x, x);
-                  reinterpret_cast<uint16_t*>(p.o)[(seg.out_row0 + c + e) * S::kDv + blk * 128 + ch] =
-                      static_cast<uint16_t>(w);
-                } else {
-                  p.part_o[(static_cast<long long>(seg.part) * kN + c + e) * S::kDv + blk * 128 + ch] = x;
-                }
-              }
-            }
-          }
+      for (int n = 0; n < kNB; ++n) {
+        inv[n][0] = sm.factor[8 * n + 2 * t4];
+        inv[n][1] = sm.factor[8 * n + 2 * t4 + 1];
+      }
+      const uint32_t out_at = sP + static_cast<uint32_t>(warp * kN * 32);
+      constexpr int kHalves = S::kVC == 1 ? 1 : 2;  // with 64 channels a warp has 16
+#pragma unroll 1
+      for (int i = 0; i < S::kBlocks * kHalves; ++i) {
+        const int blk = i / kHalves, half = i % kHalves;
+        const int ch0 = blk * 128 + 16 * (kHalves * warp + half);
+        uint32_t v[kNB][4];
+        if (seg.n_tiles > 0) {
+          tmem_ld_frag(tmem + t_lane + (static_cast<uint32_t>(half) << 20) + S::kColO + blk * kN, v);
+          tmem_wait_ld();
         }
+        float x[kNB][4];
+#pragma unroll
+        for (int n = 0; n < kNB; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            asm volatile("" : "+r"(v[n][e]));  // not before the wait
+            x[n][e] = inv[n][e & 1] == 0.f ? 0.f : __uint_as_float(v[n][e]) * inv[n][e & 1];
+          }
+        if (!ok) continue;
+        if (seg.whole) {
+          const uint32_t row8 = static_cast<uint32_t>((lane >> 4) * 8 + (lane & 7));
+          const uint32_t to = out_at + row8 * 32 + ((((lane >> 3) ^ (row8 >> 2)) & 1u) << 4);
+#pragma unroll
+          for (int n = 0; n < kNB; n += 2)
+            stmatrix_trans4(to + n * 256, pack2<BF16>(x[n][0], x[n][1]), pack2<BF16>(x[n][2], x[n][3]),
+                            pack2<BF16>(x[n + 1][0], x[n + 1][1]), pack2<BF16>(x[n + 1][2], x[n + 1][3]));
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < kN / 16; ++k) {
+            const int row = 16 * k + (lane >> 1), c = lane & 1;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(out_at + row * 32 + ((c ^ ((row >> 2) & 1)) << 4)));
+            if (row < seg.n_rows)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (seg.out_row0 + row) * S::kDv +
+                                        ch0 + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+        } else {
+          float* part = p.part_o + (static_cast<long long>(seg.part) * S::kDv + ch0 + g) * p.part_rows +
+                        2 * t4;
+#pragma unroll
+          for (int n = 0; n < kNB; ++n)
+            if (8 * n + 2 * t4 < p.part_rows) {
+              *reinterpret_cast<float2*>(part + 8 * n) = make_float2(x[n][0], x[n][1]);
+              *reinterpret_cast<float2*>(part + 8 * n + 8 * p.part_rows) = make_float2(x[n][2], x[n][3]);
+            }
+        }
+      }
       tc_fence_before();
-      ok = !named_bar_or(1, 128, !ok);
+      if (named_bar_or(1, 128, !ok)) break;
+      seg = next;
     }
   } else if (warp == 4) {
     // =============================== MMA issue ===============================
@@ -443,83 +519,101 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
     while (ok && paged_next<kN>(p, walk, seg)) {
       const uint32_t n = static_cast<uint32_t>(seg.n_tiles);
       if (n == 0) continue;
-      // the queries, once the scores of the segment before are done
-      if (nq > 0 && !wait_bar_warp<kSleepMmaNs>(q_empty, (nq - 1) & 1u, ctl)) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, S::kQBytes);
-        tma_load_3d(sQ, &tmQ, q_full, 0, static_cast<int>(seg.out_row0), 0);
-      }
-      __syncwarp();
-      issued = true;
-      const bool q_ok = wait_bar_warp<kSleepMmaNs>(q_full, nq & 1u, ctl);
+      if (!wait_bar_warp(q_full, nq & 1u, ctl)) break;
       ++nq;
-      if (!q_ok) break;
+      issued = true;
       uint32_t s = 0, o = 0;  // products issued in this segment
-      uint64_t since = 0;
-      uint32_t polls = 0;
-#pragma unroll 1
-      while (o < n) {
-        if (o < s && __all_sync(0xffffffffu, mbar_test_wait(p_ready, (t0 + o) & 1u))) {
-          tc_fence_after();
-          const uint32_t stage = (t0 + o) % kStages;
-          const uint64_t a = smem_desc_sw128(
-              sRing + stage * S::kStageBytes + (S::kShared ? 0 : S::kTileK), 1024, S::kVStride);
-          const uint64_t b = smem_desc_sw128(sP, 16, 1024);
+      auto score = [&]() {
+        const uint32_t ts = t0 + s;
+        tc_fence_after();
+        const uint64_t a = smem_desc_sw128(sK + (ts % kStages) * S::kTileK, 16, S::kKC * 1024);
+        const uint64_t b = smem_desc_sw128(sQ, 16, 1024);
+#pragma unroll
+        for (int c = 0; c < S::kKC; ++c)
+          umma_f16_ss_k64(tmem + (ts & 1u) * kN, a + c * (1024 >> 4), b + c * (kN * 128 >> 4), kIdescS,
+                          c > 0 ? 1u : 0u);
+        umma_commit(s_full + 8 * (ts & 1u));
+        if constexpr (!S::kShared) umma_commit(k_empty + 8 * (ts % kStages));
+        ++s;
+      };
+      auto output = [&]() {
+        const uint32_t stage = (t0 + o) % kStages;
+        if constexpr (!S::kShared) {
+          ok = wait_bar_warp(v_full + 8 * stage, ((t0 + o) / kStages) & 1u, ctl);
+          if (!ok) return;
+        }
+        tc_fence_after();
+        const uint64_t a = smem_desc_sw128(sV + stage * S::kVTile, 1024, S::kVStride);
+        const uint64_t b =
+            smem_desc_sw128(sP + (S::kPs > 1 ? ((t0 + o) & 1u) * S::kPBytes : 0u), 16, 1024);
+#pragma unroll
+        for (int k = 0; k < kPagedKeys / 16; ++k) {
 #pragma unroll
           for (int blk = 0; blk < S::kBlocks; ++blk)
-#pragma unroll
-            for (int k = 0; k < kPagedKeys / 16; ++k)
-              umma_f16_ss(tmem + S::kColO + blk * kN, a + blk * (2048 >> 4) + k * (2 * S::kVStride >> 4),
-                          b + 2 * k, kIdescO, (o > 0 || k > 0) ? 1u : 0u);
-          umma_commit(kv_empty + 8 * stage);
-          umma_commit(o_done);
-          ++o;
-          since = 0;
-          continue;
+            umma_f16_ss(tmem + S::kColO + blk * kN, a + blk * (2048 >> 4) + k * (2 * S::kVStride >> 4),
+                        b + 2 * k, kIdescO, (o > 0 || k > 0) ? 1u : 0u);
+          if constexpr (S::kShared) umma_commit(k_empty + 8 * (4 * stage + k));
         }
-        const uint32_t ts = t0 + s;
-        if (s < n && s < o + 2 &&
-            __all_sync(0xffffffffu, mbar_test_wait(kv_full + 8 * (ts % kStages), (ts / kStages) & 1u))) {
-          tc_fence_after();
-          const uint64_t a = smem_desc_sw128(sRing + (ts % kStages) * S::kStageBytes, 16, S::kKC * 1024);
-          const uint64_t b = smem_desc_sw128(sQ, 16, 1024);
-#pragma unroll
-          for (int c = 0; c < S::kKC; ++c)
-            umma_f16_ss_k64(tmem + (ts & 1u) * kN, a + c * (1024 >> 4), b + c * (kN * 128 >> 4), kIdescS,
-                            c > 0 ? 1u : 0u);
-          umma_commit(s_full + 8 * (ts & 1u));
-          if (s + 1 == n) umma_commit(q_empty);
-          ++s;
-          since = 0;
-          continue;
-        }
-        if ((++polls & 31u) == 0) {
-          const uint64_t now = globaltimer_ns();
-          bool stop = *ctl.abort != 0u;
-          if (since == 0) {
-            since = now;
-          } else if (now - since > p.timeout_ns) {
-            *ctl.abort = 1u;
-            atomicExch(p.status, kStatusTimeout);
-            stop = true;
+        if constexpr (!S::kShared) umma_commit(v_empty + 8 * stage);
+        umma_commit(o_done + 8 * ((t0 + o) & 1u));
+        ++o;
+      };
+#pragma unroll 1
+      while (ok && o < n) {
+        const uint32_t full = k_full + 8 * ((t0 + s) % kStages), full_par = ((t0 + s) / kStages) & 1u;
+        const uint32_t ready = p_ready + 8 * ((t0 + o) & 1u), p_par = ((t0 + o) >> 1) & 1u;
+        if (s == n || s == o + 2) {  // nothing but the product with P can come next
+          ok = wait_bar_warp(ready, p_par, ctl);
+          if (ok) output();
+        } else if (s == o) {  // nothing but scores
+          ok = wait_bar_warp(full, full_par, ctl);
+          if (ok) score();
+        } else {  // whichever is ready first
+          uint64_t since = 0;
+#pragma unroll 1
+          for (uint32_t polls = 1;; ++polls) {
+            if (__all_sync(0xffffffffu, mbar_test_wait(ready, p_par))) {
+              output();
+              break;
+            }
+            if (__all_sync(0xffffffffu, mbar_test_wait(full, full_par))) {
+              score();
+              break;
+            }
+            if ((polls & 31u) == 0) {
+              const uint64_t now = globaltimer_ns();
+              bool stop = *ctl.abort != 0u;
+              if (since == 0) {
+                since = now;
+              } else if (now - since > p.timeout_ns) {
+                *ctl.abort = 1u;
+                atomicExch(p.status, kStatusTimeout);
+                stop = true;
+              }
+              if (__any_sync(0xffffffffu, stop)) {
+                ok = false;
+                break;
+              }
+            }
           }
-          if (__any_sync(0xffffffffu, stop)) {
-            ok = false;
-            break;
-          }
         }
-        __nanosleep(kSleepMmaNs);
       }
       t0 += n;
     }
-    if (nq > 0) wait_drain(q_full, (nq - 1) & 1u, p.timeout_ns);
     if (issued) {  // every MMA issued completes before tensor memory is freed
       umma_commit(drain);
       wait_drain(drain, 0, p.timeout_ns);
     }
     __syncwarp();
   } else {
-    // =============================== producer ================================
+    // =============================== producers ===============================
+    // warp 5 the keys, warp 6 the values
+    const bool is_k = warp == 5;
+    const uint32_t full0 = is_k ? k_full : v_full, empty0 = is_k ? k_empty : v_empty;
+    const uint32_t bytes = is_k ? S::kTileK : S::kTileV;
+    const uint32_t ring = (is_k ? sK : sV) + (lane & 7) * ((is_k ? S::kKC : S::kVC) * 1024);
+    const CUtensorMap* tm = is_k ? &tmK : &tmV;
+    const int at = is_k ? p.k_at : p.v_at;
     uint32_t t = 0;
     bool ok = true;
 #pragma unroll 1
@@ -534,38 +628,41 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
         const int key = seg.k_begin + j0 * kPagedKeys + 8 * lane;
         const int page = ahead;
         ahead = page_of(key + 4 * kPagedKeys);
-        const bool here = key < seg.k_end;
-        const bool is_bad = here && (page < 0 || page >= p.num_pages);
+        // the row of this lane's keys, past the pool where there are none
+        auto row_of = [&](int k, int pg) {
+          return k < seg.k_end && pg >= 0 && pg < p.num_pages
+                     ? ((pg * p.Hkv + seg.hk) << p.page_shift) + (k & (page_keys - 1))
+                     : p.pool_rows;
+        };
+        const int row = row_of(key, page);
+        const bool is_bad = key < seg.k_end && row == p.pool_rows;
         if (is_bad) atomicMax(p.status, kStatusBadIndex);
         const uint32_t bad = __ballot_sync(0xffffffffu, is_bad);
-        const int row = here && !is_bad
-                            ? ((page * p.Hkv + seg.hk) << p.page_shift) + (key & (page_keys - 1))
-                            : p.pool_rows;
 #pragma unroll 1
-        for (int k = 0; k < 4 && j0 + k < seg.n_tiles; ++k, ++t) {
-          const uint32_t stage = t % kStages, full = kv_full + 8 * stage;
-          if (!wait_bar_warp<kSleepProducerNs>(kv_empty + 8 * stage, ((t / kStages) & 1u) ^ 1u, ctl)) {
-            ok = false;
-            break;
+        for (int k = 0; ok && k < 4 && j0 + k < seg.n_tiles; ++k, ++t) {
+          const uint32_t stage = t % kStages, full = full0 + 8 * stage, par = ((t / kStages) & 1u) ^ 1u;
+          const uint32_t dst = ring + stage * bytes;
+          constexpr int kTurns = S::kShared ? 4 : 1;  // a latent stage 16 keys at a time
+#pragma unroll 1
+          for (int i = 0; ok && i < kTurns; ++i) {
+            ok = wait_bar_warp(empty0 + 8 * (kTurns * stage + i), par, ctl);
+            if (!ok) break;
+            if (i == 0 && lane == 0) {
+              if (is_k) sm.bad[t % kPagedBad] = (bad >> (8 * k)) & 0xffu;
+              mbar_arrive_expect_tx(full, bytes);
+            }
+            __syncwarp();
+            if ((lane >> 3) == k && (kTurns == 1 || ((lane & 7) >> 1) == i))
+              tma_load_4d(dst, tm, full, 0, row, 0, at);
+            __syncwarp();
           }
-          if (lane == 0) {
-            sm.bad[stage] = (bad >> (8 * k)) & 0xffu;
-            mbar_arrive_expect_tx(full, S::kStageBytes);
-          }
-          __syncwarp();
-          if ((lane >> 3) == k) {
-            const uint32_t dst = sRing + stage * S::kStageBytes;
-            tma_load_3d(dst + (lane & 7) * (S::kKC * 1024), &tmK, full, 0, row, 0);
-            if constexpr (!S::kShared)
-              tma_load_3d(dst + S::kTileK + (lane & 7) * (S::kVC * 1024), &tmV, full, 0, row, 0);
-          }
-          __syncwarp();
         }
       }
     }
-    // every load issued lands before shared memory goes away
+    // every load issued lands before shared memory goes away (an abort may have left
+    // the last tile's unsent: the wait is bounded)
     for (uint32_t i = t > kStages ? t - kStages : 0u; i < t; ++i)
-      wait_drain(kv_full + 8 * (i % kStages), (i / kStages) & 1u, p.timeout_ns);
+      wait_drain(full0 + 8 * (i % kStages), (i / kStages) & 1u, p.timeout_ns);
     __syncwarp();
   }
 
@@ -577,74 +674,165 @@ __global__ void __launch_bounds__(kPagedThreads, S::kCtas)
   }
 }
 
-// The units that several CTAs shared, as the 4-bit cache's merge: a slice of 128
-// channels (64) of a row by the four warps of a block (few units of many parts), or
-// by one warp, the rows of a unit eight to a block (many units of few parts).
-constexpr int kPagedMergeRows = 8;
+// The units that several CTAs shared: O = sum_s w_s O_s / sum_s w_s over their parts,
+// w_s = exp(LSE_s - max LSE).  A block takes kCh channels of a unit: it makes the
+// weights of all the unit's rows once, then its threads take four rows of a channel
+// each, which lie together in the parts, the parts dealt to groups of threads where
+// those are few.  As many channels as leave every multiprocessor a block.
+constexpr int kPagedMergeThreads = 256;
 
-template <class S, bool BF16, bool kByUnit>
-__global__ void __launch_bounds__(32 * kMergeWarps)
+template <class S, bool BF16, int kCh>
+__global__ void __launch_bounds__(kPagedMergeThreads)
     fa_paged_merge_kernel(const PagedAttnParams p, int attn_grid) {
-  constexpr int kN = S::kN, kSlice = S::kVC == 1 ? 64 : 128, kSlices = S::kDv / kSlice;
-  __shared__ KeyScan<kMergeWarps> scan;
-  const int slice = static_cast<int>(blockIdx.y);
-  int b, hk, rb, r;  // r: the block's first row within the kv head's
-  if constexpr (kByUnit) {
-    const int units = p.Hkv * p.n_row_blocks;
-    const int groups = (min(kN, p.rows) + kPagedMergeRows - 1) / kPagedMergeRows;
-    const int all = static_cast<int>(blockIdx.x) / groups;
-    b = all / units;
-    const int unit = all - b * units;
-    hk = unit / p.n_row_blocks;
-    rb = unit - hk * p.n_row_blocks;
-    r = rb * kN + (static_cast<int>(blockIdx.x) - all * groups) * kPagedMergeRows;
-  } else {
-    const int bh = static_cast<int>(blockIdx.x) / p.rows;
-    r = static_cast<int>(blockIdx.x) - bh * p.rows;
-    b = bh / p.Hkv;
-    hk = bh - b * p.Hkv;
-    rb = r / kN;
-  }
+  constexpr int kN = S::kN, kThr = kPagedMergeThreads, kWarps = kThr / 32;
+  constexpr int kParts = 64;                                // whose weights are held at once
+  constexpr int kItems = (kCh * kN / 4 + kThr - 1) / kThr;  // of a thread
+  constexpr int kAhead = kItems == 1 ? 4 : 2;               // its parts fetched before the weights
+  constexpr int kPer = kThr / kN;                           // threads that share a row's weights
+  constexpr int kW = kN + 4;
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ KeyScan<kWarps> scan;
+  __shared__ alignas(16) float w[kParts * kW];
+  __shared__ alignas(16) float old[kN];
+  __shared__ float sums[kN];
+  __shared__ union {
+    float4 acc[kThr];
+    alignas(16) uint16_t out[kN * kCh];
+  } end;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int units = p.Hkv * p.n_row_blocks;
+  const int b = static_cast<int>(blockIdx.x) / units, unit = static_cast<int>(blockIdx.x) - b * units;
+  const int hk = unit / p.n_row_blocks, rb = unit - hk * p.n_row_blocks;
+  const int ch0 = static_cast<int>(blockIdx.y) * kCh;
   int upto;
   const int all = cache_scan(p, scan, false, upto);
   const CacheDeal deal = cache_deal(all, attn_grid);
   // chunks per unit of the sequences before b: the thread with b in its run
-  const int run = (p.B + 32 * kMergeWarps - 1) / (32 * kMergeWarps);
-  if (b / run == static_cast<int>(threadIdx.x)) {
-    for (int k = static_cast<int>(threadIdx.x) * run; k < b; ++k)
-      upto += cache_chunks(cache_length(p, k));
+  const int run = (p.B + kThr - 1) / kThr;
+  if (b / run == tid) {
+    for (int k = tid * run; k < b; ++k) upto += cache_chunks(cache_length(p, k));
     scan.before = upto;
   }
   __syncthreads();
   const int chunks = cache_chunks(cache_length(p, b));
-  const int start = scan.before * (p.Hkv * p.n_row_blocks) + (hk * p.n_row_blocks + rb) * chunks;
+  const int start = scan.before * units + unit * chunks;
   const int x0 = deal.cta_of(start), x1 = deal.cta_of(start + chunks - 1);
   grid_dependency_wait();  // all blocks: this grid's end is then the attention's too
   if (x0 == x1) return;
   // a CTA's first segment, except where the unit begins inside x0
   const int inside = deal.begin(x0) < start ? 1 : 0;
-  const long long row0 = (static_cast<long long>(b) * p.Hkv + hk) * p.rows;
-  const float* part_o = p.part_o + slice * kSlice;
-  void* o = static_cast<uint16_t*>(p.o) + slice * kSlice;
-  float* lse = slice == 0 ? p.lse : nullptr;
-  const int n_parts = x1 - x0 + 1;
-  if constexpr (kByUnit) {
-    const int end = min(min(p.rows, (rb + 1) * kN), r + kPagedMergeRows);
-    for (int row = r + (static_cast<int>(threadIdx.x) >> 5); row < end; row += kMergeWarps)
-      merge_row_warp<kSlice, BF16, S::kDv>(
-          part_o, p.part_lse, n_parts,
-          [&](int s) -> long long {
-            return (2ll * (x0 + s) + (s == 0 ? inside : 0)) * kN + row - rb * kN;
-          },
-          o, lse, row0 + row);
-  } else {
-    __shared__ MergeSmem<kSlice> sm;
-    merge_row<kSlice, BF16, S::kDv>(
-        part_o, p.part_lse, n_parts,
-        [&](int s) -> long long { return (2ll * (x0 + s) + (s == 0 ? inside : 0)) * kN + r - rb * kN; },
-        o, lse, row0 + r, sm);
+  auto part_of = [&](int s) { return 2 * (x0 + s) + (s == 0 ? inside : 0); };
+  const int n_parts = x1 - x0 + 1, n_rows = min(kN, p.rows - rb * kN);
+  const int quads = p.part_rows / 4, items = kCh * quads;  // four rows of a channel each
+  const int groups = items < kThr ? kThr / items : 1;
+  const int group = items < kThr ? tid / items : 0;
+  const int item0 = items < kThr ? tid - group * items : tid;
+  const bool busy = group < groups && item0 < items;
+  const float* from = p.part_o + static_cast<long long>(ch0) * p.part_rows;
+  const long long step = static_cast<long long>(S::kDv) * p.part_rows;
+  auto load = [&](int s, int item) {
+    return *reinterpret_cast<const float4*>(from + part_of(s) * step + 4 * item);
+  };
+  float4 acc[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int row = tid / kPer, j = tid % kPer;
+  float top = -INFINITY, sum = 0.f;  // the row's, over the parts so far
+
+#pragma unroll 1
+  for (int s0 = 0; s0 < n_parts; s0 += kParts) {
+    const int now = min(kParts, n_parts - s0);
+    float4 ahead[kItems][kAhead];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i)
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (busy && item0 + i * kThr < items && group + k * groups < now)
+          ahead[i][k] = load(s0 + group + k * groups, item0 + i * kThr);
+    if (s0 > 0) __syncthreads();  // the weights before are done with
+    for (int i = tid; i < now * kN; i += kThr) {
+      const int s = i / kN, n = i % kN;
+      w[s * kW + n] = n < n_rows ? p.part_lse[static_cast<long long>(part_of(s0 + s)) * kN + n] * kLog2e
+                                 : -INFINITY;
+    }
+    __syncthreads();
+    float m = top, part_sum = 0.f;
+    for (int s = j; s < now; s += kPer) m = fmaxf(m, w[s * kW + row]);
+#pragma unroll
+    for (int k = kPer / 2; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float base = m == -INFINITY ? 0.f : m;
+    for (int s = j; s < now; s += kPer) {
+      const float x = ex2_approx(w[s * kW + row] - base);
+      w[s * kW + row] = x;
+      part_sum += x;
+    }
+#pragma unroll
+    for (int k = kPer / 2; k > 0; k >>= 1) part_sum += __shfl_xor_sync(0xffffffffu, part_sum, k);
+    const float f = ex2_approx(top - base);
+    sum = fmaf(sum, f, part_sum);
+    top = m;
+    if (j == 0) {
+      old[row] = f;
+      sums[row] = sum;
+    }
+    __syncthreads();
+    if (busy) {
+#pragma unroll
+      for (int i = 0; i < kItems; ++i) {
+        const int item = item0 + i * kThr;
+        if (item >= items) break;
+        const int r = 4 * (item % quads);
+        const float4 q = *reinterpret_cast<const float4*>(old + r);
+        acc[i].x *= q.x, acc[i].y *= q.y, acc[i].z *= q.z, acc[i].w *= q.w;
+        auto add = [&](int s, const float4& v) {
+          const float4 x = *reinterpret_cast<const float4*>(w + s * kW + r);
+          acc[i].x = fmaf(x.x, v.x, acc[i].x);
+          acc[i].y = fmaf(x.y, v.y, acc[i].y);
+          acc[i].z = fmaf(x.z, v.z, acc[i].z);
+          acc[i].w = fmaf(x.w, v.w, acc[i].w);
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+          if (group + k * groups < now) add(group + k * groups, ahead[i][k]);
+#pragma unroll 4
+        for (int s = group + kAhead * groups; s < now; s += groups) add(s, load(s0 + s, item));
+      }
+    }
   }
-  static_assert(kSlices * kSlice == S::kDv, "slices");
+  if (groups > 1) {
+    end.acc[tid] = acc[0];
+    __syncthreads();
+    if (group == 0 && busy)
+      for (int k = 1; k < groups; ++k) {
+        const float4 v = end.acc[k * items + item0];
+        acc[0].x += v.x, acc[0].y += v.y, acc[0].z += v.z, acc[0].w += v.w;
+      }
+    __syncthreads();  // the memory is the output's
+  }
+  if (group == 0 && busy) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int item = item0 + i * kThr;
+      if (item >= items) break;
+      const int r = 4 * (item % quads), c = item / quads;
+      const float v[4] = {acc[i].x, acc[i].y, acc[i].z, acc[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        // no part has a key: 0; a NaN stays one
+        const float x = sums[r + k] == 0.f ? 0.f : v[k] / sums[r + k];
+        end.out[(r + k) * kCh + c] = static_cast<uint16_t>(pack2<BF16>(x, x));
+      }
+    }
+  }
+  __syncthreads();
+  const long long row0 = (static_cast<long long>(b) * p.Hkv + hk) * p.rows + rb * kN;
+  for (int i = tid; i < n_rows * (kCh / 8); i += kThr) {
+    const int r = i / (kCh / 8), c = i % (kCh / 8);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (row0 + r) * S::kDv + ch0 + 8 * c) =
+        *reinterpret_cast<const uint4*>(end.out + r * kCh + 8 * c);
+  }
+  if (blockIdx.y == 0 && j == 0 && row < n_rows)
+    p.lse[row0 + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace fa

@@ -2,14 +2,15 @@
 // shared by its translation units (one per kind of cache and type).
 #pragma once
 #include <mutex>
+#include <type_traits>
 
 #include "fa_paged_attn.cuh"
 
 namespace fa {
 
 template <class S, bool BF16, bool kMod>
-cudaError_t paged_launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
-                             const PagedAttnParams& p, int grid, cudaStream_t stream) {
+cudaError_t paged_launch_one(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnParams& p,
+                             int grid, cudaStream_t stream) {
   static_assert(paged_smem_bytes<S>() <= 232448 && S::kStages <= PagedMiscBars::kMaxStages,
                 "shared memory budget");
   static_assert(S::kCtas * (paged_smem_bytes<S>() + 1024) <= 233472, "CTAs an SM");
@@ -32,7 +33,7 @@ cudaError_t paged_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
   // merge overlaps this one's (programmatic dependent launch)
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-  cfg.blockDim = dim3(kPagedThreads, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = paged_smem_bytes<S>();
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -40,18 +41,19 @@ cudaError_t paged_launch_one(const CUtensorMap& q, const CUtensorMap& k, const C
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_attn_kernel<S, BF16, kMod>, q, k, v, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_attn_kernel<S, BF16, kMod>, k, v, p);
   if (e != cudaSuccess || p.whole) return e;
   const long long units = static_cast<long long>(p.B) * p.Hkv * p.n_row_blocks;
-  const bool by_unit = units >= p.sms;
-  const int rows = p.rows < S::kN ? p.rows : S::kN;
-  const long long blocks = by_unit ? units * ((rows + kPagedMergeRows - 1) / kPagedMergeRows)
-                                   : static_cast<long long>(p.B) * p.Hkv * p.rows;
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks), S::kDv <= 128 ? 1 : S::kDv / 128, 1);
-  cfg.blockDim = dim3(32 * kMergeWarps, 1, 1);
+  cfg.blockDim = dim3(kPagedMergeThreads, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return by_unit ? cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<S, BF16, true>, p, grid)
-                 : cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<S, BF16, false>, p, grid);
+  auto with = [&](auto channels) {
+    constexpr int kCh = decltype(channels)::value;
+    cfg.gridDim = dim3(static_cast<unsigned>(units), S::kDv / kCh, 1);
+    return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<S, BF16, kCh>, p, grid);
+  };
+  if (units * (S::kDv / 64) >= p.sms) return with(std::integral_constant<int, 64>{});
+  if (units * (S::kDv / 32) >= p.sms) return with(std::integral_constant<int, 32>{});
+  return with(std::integral_constant<int, 8>{});
 }
 
 }  // namespace fa

@@ -2,10 +2,11 @@
 //
 // Rotation of a pair (x, y) of channels at position n with frequency f (radians a
 // position):  (x cos a - y sin a, y cos a + x sin a),  a = n f.
-// The angle is held in turns as a 64-bit fraction: f / 2 pi is rounded once to
-// 2^-64 of a turn (through 53 bits), its product with n is exact modulo a turn, and
-// 32 bits of it go to the sine and cosine.  At n = 2^24 and f = 1 the angle is off by
-// 2^-28 of a radian; n f in fp32 would be off by half a radian.
+// The angle is held in turns as a 64-bit fraction: f / 2 pi to 2^-61 of a turn, whose
+// product with n is exact modulo a turn; its upper 32 bits go to the sine and cosine.
+// All in integers: the GPU makes two double-precision products a cycle and
+// multiprocessor.  At n = 2^24 and f = 1 the angle is off by 2^-28 of a radian; n f in
+// fp32 would be off by half a radian.
 //
 // Both kernels only move bytes.  Write: a block takes 2^token_shift tokens of a
 // sequence.  Its threads make the tokens' sines and cosines, one each, then take
@@ -27,12 +28,21 @@ constexpr int kPagedMaxTokenShift = 3;
 constexpr int kPagedAtOnce = 4;  // tasks of a thread whose loads go out together
 constexpr int kPagedMaxPairs = 64;
 
-// Cosine and sine of position n times f.
-__device__ __forceinline__ float2 rope_unit(int n, float f) {
-  constexpr double kPerTurn = 0.15915494309189533577;  // 1 / 2 pi
-  double turns = static_cast<double>(f) * kPerTurn;
-  turns -= floor(turns);
-  const unsigned long long step = __double2ull_rn(turns * 18446744073709551616.0);
+// f / 2 pi as a fraction of a turn in 2^-64ths: f's 24 bits times 1 / 2 pi in 64.  Off
+// by 2^-61 of f's power of two, or 2^-64.
+__device__ __forceinline__ unsigned long long rope_step(float f) {
+  const uint32_t bits = __float_as_uint(f);
+  const int e = static_cast<int>((bits >> 23) & 0xffu) - 127;  // |f| = 1.m 2^e
+  if (e < -64 || e > 63) return 0ull;  // no angle at 2^24 positions, or no fp32 angle
+  const unsigned long long m = static_cast<unsigned long long>((bits & 0x7fffffu) | 0x800000u) << 40;
+  // 2^64 / 2 pi; the product's upper half is 2^63 1.m / 2 pi
+  const unsigned long long half = __umul64hi(m, 0x28be60db9391054aull);
+  const unsigned long long step = e >= 0 ? half << 1 << e : half >> (-e - 1);
+  return bits >> 31 ? 0ull - step : step;
+}
+
+// Cosine and sine of the angle n steps.
+__device__ __forceinline__ float2 rope_unit(int n, unsigned long long step) {
   const unsigned long long at = step * static_cast<unsigned long long>(static_cast<long long>(n));
   // the upper half as a signed number: half turns in [-1, 1)
   const float half = static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f;
@@ -88,11 +98,9 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
   grid_launch_dependents();
   const int b = static_cast<int>(blockIdx.y);
   const int first = static_cast<int>(blockIdx.x) << p.token_shift;
-  const int start = p.start ? p.start[b] : 0;
-  const int count = p.count ? min(p.count[b], p.S) : p.S;
-  if (first >= count) return;
-  const int tokens = min(1 << p.token_shift, count - first);
   const int half = p.rot >> 1;
+  // those there are, before the count is known: the first words are on their way by then
+  int tokens = min(1 << p.token_shift, p.S - first);
 
   // a row's tasks: 16 channels each; rows of q, of k, then of v
   const int d_shift = kLat ? 2 : (p.D == 128 ? 3 : 2);  // tasks of a row of q or k
@@ -105,15 +113,13 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
   const int t0 = per * static_cast<int>(blockIdx.z), t1 = min(all, t0 + per);
 
   struct Task {
-    const uint4 *in0, *in1;
-    uint4 *out0, *out1;
     int token, pair;  // pair: the first of its 8, or -1
   };
   const int D = kLat ? kLatentRope : p.D;
-  // where a task's words are; `out` is ready once the slots are
-  auto source = [&](int id, Task& t) {
+  // a task, and its words; past the end, a token that there is not
+  auto source = [&](int id, Task& t, uint4& x, uint4& y) {
     t.pair = -1;
-    t.token = tokens;
+    t.token = 1 << kPagedMaxTokenShift;
     if (id >= t1) return;
     int r = id, shift = d_shift, heads = p.H;
     const void* in = p.q;
@@ -129,29 +135,26 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
         turned = false;
       }
     }
-    const int u = r & ((1 << shift) - 1);
-    t.token = (r >> shift) & ((1 << ts) - 1);
-    if (t.token >= tokens) {
-      t.token = tokens;
-      return;
-    }
+    const int u = r & ((1 << shift) - 1), token = (r >> shift) & ((1 << ts) - 1);
+    if (token >= tokens) return;
+    t.token = token;
     const int head = r >> (shift + ts);
-    turned = turned && 16 * u < p.rot;
-    const int w0 = turned && !kPairs ? u : 2 * u;
+    if (turned && 16 * u < p.rot) t.pair = 8 * u;
+    const bool halves = t.pair >= 0 && !kPairs;
     const uint4* row = static_cast<const uint4*>(in) +
-                       (((static_cast<long long>(b) * heads + head) * p.S + first + t.token)
-                        << (shift + 1));
-    t.in0 = row + w0;
-    t.in1 = row + (turned && !kPairs ? w0 + (half >> 3) : w0 + 1);
-    if (turned) t.pair = 8 * u;
+                       (((static_cast<long long>(b) * heads + head) * p.S + first + token)
+                        << (shift + 1)) + (halves ? u : 2 * u);
+    x = __ldcs(row);
+    y = __ldcs(row + (halves ? half >> 3 : 1));
   };
-  auto target = [&](int id, Task& t) -> bool {
+  // its words to their place
+  auto target = [&](int id, const Task& t, const uint4& x, const uint4& y) {
     int r = id;
     const bool is_q = r < n_q, is_v = r >= n_q + n_k;
     const int shift = is_v ? v_shift : d_shift;
     r -= is_q ? 0 : (is_v ? n_q + n_k : n_q);
     const int head = r >> (shift + ts), u = r & ((1 << shift) - 1);
-    const int w0 = t.pair >= 0 && !kPairs ? u : 2 * u;
+    const bool halves = t.pair >= 0 && !kPairs;
     uint4* row;
     if (is_q) {
       row = static_cast<uint4*>(p.q_out) +
@@ -159,17 +162,17 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
             ((p.q_width - D) >> 3);
     } else {
       const long long s = slot[t.token];
-      if (s < 0) return false;
+      if (s < 0) return;
       if constexpr (kLat) {
         row = static_cast<uint4*>(p.pool[0]) + s * (kLatentRow / 8) + (is_v ? 0 : kLatent / 8);
       } else {
-        row = static_cast<uint4*>(p.pool[is_v ? 1 : 0]) +
+        row = static_cast<uint4*>(is_v ? p.pool[1] : p.pool[0]) +
               ((s + (static_cast<long long>(head) << p.page_shift)) << (d_shift + 1));
       }
     }
-    t.out0 = row + w0;
-    t.out1 = row + (t.pair >= 0 && !kPairs ? w0 + (half >> 3) : w0 + 1);
-    return true;
+    row += halves ? u : 2 * u;
+    row[0] = x;
+    row[halves ? half >> 3 : 1] = y;
   };
 
   bool ready = false;
@@ -179,13 +182,13 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
     uint4 x[kPagedAtOnce], y[kPagedAtOnce];
 #pragma unroll
     for (int k = 0; k < kPagedAtOnce; ++k) {
-      source(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k]);
-      if (t[k].token < tokens) {
-        x[k] = __ldcs(t[k].in0);
-        y[k] = __ldcs(t[k].in1);
-      }
+      source(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k], x[k], y[k]);
     }
-    if (!ready) {  // while the first words are on their way
+    if (!ready) {
+      const int start = p.start ? p.start[b] : 0;
+      const int count = p.count ? min(p.count[b], p.S) : p.S;
+      if (first >= count) return;
+      tokens = min(tokens, count - first);
       if (static_cast<int>(threadIdx.x) < tokens) {
         const uint32_t pos = static_cast<uint32_t>(start) + static_cast<uint32_t>(first) + threadIdx.x;
         const long long s = paged_slot(p, b, pos);
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
         const int tok = i / half;
         unit[i] = rope_unit(static_cast<int>(static_cast<uint32_t>(start) +
                                              static_cast<uint32_t>(first + tok)),
-                            p.freqs[i - tok * half]);
+                            rope_step(p.freqs[i - tok * half]));
       }
       __syncthreads();
       ready = true;
@@ -205,9 +208,7 @@ __global__ void __launch_bounds__(kPagedCopyThreads, 4)
     for (int k = 0; k < kPagedAtOnce; ++k) {
       if (t[k].token >= tokens) continue;
       if (t[k].pair >= 0) rope_turn<BF16, kPairs>(x[k], y[k], unit + t[k].token * half + t[k].pair);
-      if (!target(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k])) continue;
-      *t[k].out0 = x[k];
-      *t[k].out1 = y[k];
+      target(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k], x[k], y[k]);
     }
   }
 }

@@ -608,15 +608,11 @@ def _on(dev: int, call, *args):
         return call(*args)
 
 
-def _opt(t, name: str, dev: int, dtype, shape):
-    return None if t is None else _ptr(t, name, dev, dtype, shape)
-
-
-def _places(page_table, start, count, dev: int, B: int):
+def _places(page_table, start, count, dev: int, B: int, name: str = "start"):
     """(page_table, start, count) as pointers, and max_pages."""
     table, per = _pages(page_table, dev, B)
-    return (table, _opt(start, "start", dev, torch.int32, (B,)),
-            _opt(count, "count", dev, torch.int32, (B,))), per
+    return (table, None if start is None else _ptr(start, name, dev, torch.int32, (B,)),
+            None if count is None else _ptr(count, "count", dev, torch.int32, (B,))), per
 
 
 def fa_paged_empty(num_pages: int, Hkv: int, page_size: int, D: int, dtype=torch.bfloat16,
@@ -646,15 +642,43 @@ def _freqs(freqs, dev: int):
     return _ptr(freqs, "freqs", dev, torch.float32, freqs.shape), 2 * freqs.shape[0]
 
 
-def _rotated(out, shape, like, count, stream):
+def _rotated(q, count, stream):
     """A new tensor for rotated queries; zeros where a count may leave rows out."""
-    if out is not None:
-        return out
-    out = (torch.empty if count is None else torch.zeros)(shape, dtype=like.dtype,
-                                                          device=like.device)
+    out = torch.empty_like(q) if count is None else torch.zeros_like(q)
     if stream is not None:
         _own_memory([out], stream)
     return out
+
+
+def _pool_args(cache, page_table, start, count, dev: int, dtype, Hkv: int, D: int, B: int,
+               name: str = "start"):
+    """Pointers of a 16-bit cache, of its places, and (num_pages, page_size, max_pages):
+    the checks in one expression, for their time beside the kernels'; what it refuses is
+    named one by one."""
+    try:
+        kp, vp = cache
+        pool = kp.shape
+        pages, heads, page, width = pool
+        n, per = page_table.shape
+        i32 = torch.int32
+        if (heads == Hkv and width == D and n == B
+                and kp.dtype is dtype and kp.get_device() == dev and kp.is_contiguous()
+                and vp.dtype is dtype and vp.shape == pool and vp.get_device() == dev
+                and vp.is_contiguous()
+                and page_table.dtype is i32 and page_table.get_device() == dev
+                and page_table.is_contiguous()
+                and (start is None or start.dtype is i32 and start.shape == (B,)
+                     and start.get_device() == dev and start.is_contiguous())
+                and (count is None or count.dtype is i32 and count.shape == (B,)
+                     and count.get_device() == dev and count.is_contiguous())):
+            return (kp.data_ptr(), vp.data_ptr(), page_table.data_ptr(),
+                    None if start is None else start.data_ptr(),
+                    None if count is None else count.data_ptr()), (pages, page, per)
+    except (AttributeError, IndexError, TypeError, ValueError):
+        pass
+    kp, vp, pages, page = _paged(cache, dev, dtype, Hkv, D)
+    where, per = _places(page_table, start, count, dev, B, name)
+    return (kp, vp, *where), (pages, page, per)
 
 
 def fa_paged_write(k, v, cache, page_table, start=None, count=None, freqs=None,
@@ -664,29 +688,34 @@ def fa_paged_write(k, v, cache, page_table, start=None, count=None, freqs=None,
     [B, max_pages] lists.  ``freqs`` (float32 [rotary / 2], radians a position) rotates
     the first channels of keys and of ``q`` [B, H, S, D], as halves or interleaved
     pairs.  Returns the rotated queries (``q_out``, which may be q; None without q)."""
-    dev, (B, Hkv, S, D) = _rows16(k, "k")
+    dev, shape = _rows16(k, "k")
+    B, Hkv, S, D = shape
+    dt = k.dtype
     if _current_device() != dev:
         return _on(dev, fa_paged_write, k, v, cache, page_table, start, count, freqs, interleaved,
                    q, q_out, stream)
-    vp = _ptr(v, "v", dev, k.dtype, k.shape)
-    kp, vpp, pages, page = _paged(cache, dev, k.dtype, Hkv, D)
-    where, per = _places(page_table, start, count, dev, B)
+    vp = _ptr(v, "v", dev, dt, shape)
+    (kp, vpp, *where), pages = _pool_args(cache, page_table, start, count, dev, dt, Hkv, D, B)
     fp, rotary = _freqs(freqs, dev)
     qp = op = None
     H = Hkv
     if q is not None:
-        _, shape = _rows16(q, "q")
-        H = shape[1]
+        _, rows = _rows16(q, "q")
+        H = rows[1]
         _group_check(H, Hkv)
-        qp = _ptr(q, "q", dev, k.dtype, (B, H, S, D))
-        q_out = _rotated(q_out, q.shape, q, count, stream)
-        op = _ptr(q_out, "q_out", dev, k.dtype, q.shape)
+        if rows[0] != B or rows[2] != S or rows[3] != D or q.dtype is not dt or q.get_device() != dev:
+            _bad(q, "q", dev, dt, (B, H, S, D))
+        qp = q.data_ptr()
+        if q_out is None:
+            q_out = _rotated(q, count, stream)
+        op = _ptr(q_out, "q_out", dev, dt, rows)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _check((_lib or load()).fa_paged_write(
+    st = (_lib or load()).fa_paged_write(
         qp, k.data_ptr(), vp, op, kp, vpp, *where, fp, rotary, bool(interleaved), B, H, Hkv, S, D,
-        pages, page, per, _DTYPE[k.dtype],
-        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_paged_write")
+        *pages, _DTYPE[dt], _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_paged_write")
     return q_out
 
 
@@ -697,33 +726,23 @@ def fa_paged_read(cache, page_table, start=None, count=None, out=None, stream=No
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (k, v) to read into")
     k, v = out
-    dev, (B, Hkv, S, D) = _rows16(k, "k")
+    dev, shape = _rows16(k, "k")
+    B, Hkv, S, D = shape
     if _current_device() != dev:
         return _on(dev, fa_paged_read, cache, page_table, start, count, out, stream)
-    vp = _ptr(v, "v", dev, k.dtype, k.shape)
-    kp, vpp, pages, page = _paged(cache, dev, k.dtype, Hkv, D)
-    where, per = _places(page_table, start, count, dev, B)
-    _check((_lib or load()).fa_paged_read(
-        kp, vpp, *where, k.data_ptr(), vp, B, Hkv, S, D, pages, page, per, _DTYPE[k.dtype],
-        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_paged_read")
+    vp = _ptr(v, "v", dev, k.dtype, shape)
+    pool, pages = _pool_args(cache, page_table, start, count, dev, k.dtype, Hkv, D, B)
+    st = (_lib or load()).fa_paged_read(
+        *pool, k.data_ptr(), vp, B, Hkv, S, D, *pages, _DTYPE[k.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_paged_read")
     return k, v
 
 
 def fa_paged_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, D: int, page_size: int,
                              max_pages: int) -> int:
     return int(load().fa_paged_workspace_bytes(B, H, Hkv, Sq, D, page_size, max_pages))
-
-
-def _attend_pages(name: str, call, need, dev: int, q, stream, workspace):
-    """A cache attention's call(workspace, bytes, stream handle); a captured one that
-    has no workspace gets one of the graph's memory."""
-    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
-    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
-    st = call(ws, ws_bytes, handle)
-    if st == FA_ERR_WORKSPACE and ws is None:
-        st = _graph_workspace(lambda p, n: call(p, n, handle), need(), q.device, stream)
-    if st:
-        _check(st, name)
 
 
 def fa_fwd_paged(q, cache, page_table, length, scale: float | None = None, softcap: float = 0.0,
@@ -737,18 +756,24 @@ def fa_fwd_paged(q, cache, page_table, length, scale: float | None = None, softc
                    workspace, out, lse, stream)
     Hkv = cache[0].shape[1] if isinstance(cache[0], torch.Tensor) and cache[0].dim() == 4 else 0
     _group_check(H, Hkv)
-    kp, vp, pages, page = _paged(cache, dev, q.dtype, Hkv, D)
-    table, per = _pages(page_table, dev, B)
-    lp = _ptr(length, "length", dev, torch.int32, (B,))
-    sp = _opt(slopes, "slopes", dev, torch.float32, (H,))
-    sc = float(D) ** -0.5 if scale is None else float(scale)
+    (kp, vp, table, lp, _), (pages, page, per) = _pool_args(cache, page_table, length, None, dev,
+                                                            q.dtype, Hkv, D, B, "length")
+    if lp is None:
+        _bad(length, "length", dev, torch.int32, (B,))
+    sp = None if slopes is None else _ptr(slopes, "slopes", dev, torch.float32, (H,))
     L = _lib or load()
     out, lse = _outputs_on(q, dev, out, lse, stream)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
     args = (q.data_ptr(), kp, vp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Hkv, Sq, D,
-            pages, page, per, sc, _DTYPE[q.dtype], softcap, sp)
-    _attend_pages("fa_fwd_paged", lambda *ws: L.fa_fwd_paged(*args, *ws),
-                  lambda: L.fa_paged_workspace_bytes(B, H, Hkv, Sq, D, page, per), dev, q, stream,
-                  workspace)
+            pages, page, per, D ** -0.5 if scale is None else float(scale), _DTYPE[q.dtype], softcap, sp)
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    st = L.fa_fwd_paged(*args, ws, ws_bytes, handle)
+    if st == FA_ERR_WORKSPACE and ws is None:
+        need = L.fa_paged_workspace_bytes(B, H, Hkv, Sq, D, page, per)
+        st = _graph_workspace(lambda p, n: L.fa_fwd_paged(*args, p, n, handle), need, q.device,
+                              stream)
+    if st:
+        _check(st, "fa_fwd_paged")
     return out, lse
 
 
@@ -767,14 +792,40 @@ def _latent_pages(cache, dev: int, dtype):
     return _ptr(cache, "cache", dev, dtype, (n, page, LATENT + LATENT_ROPE)), n, page
 
 
-def _latent_rows(c, k_rope):
-    """(device, B, S) of latent rows and their rotated part."""
+def _latent_args(c, k_rope, cache, page_table, start, count):
+    """(device, rows' pointers, the cache's and its places' pointers, sizes) of a latent
+    copy, checked as in _pool_args."""
+    try:
+        dt, dev = c.dtype, c.get_device()
+        B, S, width = c.shape
+        pages, page, row = cache.shape
+        n, per = page_table.shape
+        i32 = torch.int32
+        if (dev >= 0 and dt in _DTYPE and width == LATENT and row == LATENT + LATENT_ROPE and n == B
+                and c.is_contiguous()
+                and k_rope.dtype is dt and k_rope.shape == (B, S, LATENT_ROPE)
+                and k_rope.get_device() == dev and k_rope.is_contiguous()
+                and cache.dtype is dt and cache.get_device() == dev and cache.is_contiguous()
+                and page_table.dtype is i32 and page_table.get_device() == dev
+                and page_table.is_contiguous()
+                and (start is None or start.dtype is i32 and start.shape == (B,)
+                     and start.get_device() == dev and start.is_contiguous())
+                and (count is None or count.dtype is i32 and count.shape == (B,)
+                     and count.get_device() == dev and count.is_contiguous())):
+            return (dev, (c.data_ptr(), k_rope.data_ptr()),
+                    (cache.data_ptr(), page_table.data_ptr(),
+                     None if start is None else start.data_ptr(),
+                     None if count is None else count.data_ptr()), (B, S, pages, page, per))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        pass
     if not isinstance(c, torch.Tensor) or c.dim() != 3 or c.dtype not in _DTYPE:
         raise ValueError("c must be a [B, S, 512] float16 or bfloat16 tensor")
     dev, (B, S, _) = c.get_device(), c.shape
-    _ptr(c, "c", dev if dev >= 0 else -2, c.dtype, (B, S, LATENT))
-    _ptr(k_rope, "k_rope", dev, c.dtype, (B, S, LATENT_ROPE))
-    return dev, B, S
+    cp = _ptr(c, "c", dev if dev >= 0 else -2, c.dtype, (B, S, LATENT))
+    rp = _ptr(k_rope, "k_rope", dev, c.dtype, (B, S, LATENT_ROPE))
+    pool, pages, page = _latent_pages(cache, dev, c.dtype)
+    where, per = _places(page_table, start, count, dev, B)
+    return dev, (cp, rp), (pool, *where), (B, S, pages, page, per)
 
 
 def fa_latent_write(c, k_rope, cache, page_table, start=None, count=None, freqs=None,
@@ -783,13 +834,12 @@ def fa_latent_write(c, k_rope, cache, page_table, start=None, count=None, freqs=
     ``freqs`` (float32 [32]; None: as it is), as fa_paged_write.  ``q_rope`` [B, H, S,
     64] goes rotated into the last 64 channels of ``q`` [B, H, S, width], whose others
     stay.  Returns q."""
-    dev, B, S = _latent_rows(c, k_rope)
+    dev, rows, (pool, *where), (B, S, *pages) = _latent_args(c, k_rope, cache, page_table, start,
+                                                             count)
     if _current_device() != dev:
         return _on(dev, fa_latent_write, c, k_rope, cache, page_table, start, count, freqs,
                    interleaved, q_rope, q, stream)
-    cp, pages, page = _latent_pages(cache, dev, c.dtype)
-    where, per = _places(page_table, start, count, dev, B)
-    fp = _opt(freqs, "freqs", dev, torch.float32, (LATENT_ROPE // 2,))
+    fp = None if freqs is None else _ptr(freqs, "freqs", dev, torch.float32, (LATENT_ROPE // 2,))
     qp = op = None
     H = width = 0
     if (q_rope is None) != (q is None):
@@ -799,10 +849,11 @@ def fa_latent_write(c, k_rope, cache, page_table, start=None, count=None, freqs=
         H, width = shape[1], shape[3]
         op = _ptr(q, "q", dev, c.dtype, (B, H, S, width))
         qp = _ptr(q_rope, "q_rope", dev, c.dtype, (B, H, S, LATENT_ROPE))
-    _check((_lib or load()).fa_latent_write(
-        c.data_ptr(), k_rope.data_ptr(), cp, qp, op, *where, fp, bool(interleaved), B, H, S, width,
-        pages, page, per, _DTYPE[c.dtype],
-        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_latent_write")
+    st = (_lib or load()).fa_latent_write(
+        *rows, pool, qp, op, *where, fp, bool(interleaved), B, H, S, width, *pages,
+        _DTYPE[c.dtype], _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_latent_write")
     return q
 
 
@@ -813,14 +864,14 @@ def fa_latent_read(cache, page_table, start=None, count=None, out=None, stream=N
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (c, k_rope) to read into")
     c, k_rope = out
-    dev, B, S = _latent_rows(c, k_rope)
+    dev, rows, pool, sizes = _latent_args(c, k_rope, cache, page_table, start, count)
     if _current_device() != dev:
         return _on(dev, fa_latent_read, cache, page_table, start, count, out, stream)
-    cp, pages, page = _latent_pages(cache, dev, c.dtype)
-    where, per = _places(page_table, start, count, dev, B)
-    _check((_lib or load()).fa_latent_read(
-        cp, *where, c.data_ptr(), k_rope.data_ptr(), B, S, pages, page, per, _DTYPE[c.dtype],
-        _raw_stream(dev) if stream is None else _stream_handle(stream)), "fa_latent_read")
+    st = (_lib or load()).fa_latent_read(
+        *pool, *rows, *sizes, _DTYPE[c.dtype],
+        _raw_stream(dev) if stream is None else _stream_handle(stream))
+    if st:
+        _check(st, "fa_latent_read")
     return c, k_rope
 
 
@@ -831,6 +882,8 @@ def fa_latent_workspace_bytes(B: int, H: int, Sq: int, page_size: int, max_pages
 def _outputs_wide(q, width: int, dev: int, out, lse, stream):
     """As _outputs_on, with output rows of another width than q's."""
     B, H, Sq, _ = q.shape
+    if out is None and lse is None and stream is None:
+        return q.new_empty((B, H, Sq, width)), q.new_empty((B, H, Sq), dtype=torch.float32)
     made = []
     if out is None:
         out = torch.empty((B, H, Sq, width), dtype=q.dtype, device=q.device)
@@ -866,14 +919,19 @@ def fa_fwd_latent(q, cache, page_table, length, scale: float | None = None, work
     cp, pages, page = _latent_pages(cache, dev, q.dtype)
     table, per = _pages(page_table, dev, B)
     lp = _ptr(length, "length", dev, torch.int32, (B,))
-    sc = _LATENT_SCALE if scale is None else float(scale)
     L = _lib or load()
     out, lse = _outputs_wide(q, LATENT, dev, out, lse, stream)
+    ws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
     args = (q.data_ptr(), cp, table, lp, out.data_ptr(), lse.data_ptr(), B, H, Sq, pages, page, per,
-            sc, _DTYPE[q.dtype])
-    _attend_pages("fa_fwd_latent", lambda *ws: L.fa_fwd_latent(*args, *ws),
-                  lambda: L.fa_latent_workspace_bytes(B, H, Sq, page, per), dev, q, stream,
-                  workspace)
+            _LATENT_SCALE if scale is None else float(scale), _DTYPE[q.dtype])
+    handle = _raw_stream(dev) if stream is None else _stream_handle(stream)
+    st = L.fa_fwd_latent(*args, ws, ws_bytes, handle)
+    if st == FA_ERR_WORKSPACE and ws is None:
+        need = L.fa_latent_workspace_bytes(B, H, Sq, page, per)
+        st = _graph_workspace(lambda p, n: L.fa_fwd_latent(*args, p, n, handle), need, q.device,
+                              stream)
+    if st:
+        _check(st, "fa_fwd_latent")
     return out, lse
 
 
