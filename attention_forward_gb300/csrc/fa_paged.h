@@ -62,7 +62,7 @@ struct PagedAttnParams {
   int B, H, Hkv, Sq;
   int rows;           // (H / Hkv) * Sq query rows per kv head
   int part_rows;      // rows that a part holds: a CTA's, up to a multiple of 4
-  int n_row_blocks;
+  int n_row_blocks;   // of a CTA's rows, or a cluster's
   int sms;
   int whole;          // CTAs take whole units: no parts, no merge
   int num_pages, page_shift, max_pages;
@@ -78,6 +78,10 @@ cudaError_t launch_paged_read(bool latent, const PagedReadParams& p, cudaStream_
 // Query rows that one pass of the attention over the keys takes, and the CTAs that
 // an SM holds.  kind: 64 or 128, a head's channels; kLatent, latent rows.
 int paged_attn_row_block(int kind, int rows);
+// CTAs of a cluster, which share the keys: 2 for latent rows where there are more query
+// rows than a CTA takes.
+int paged_attn_cluster(int kind, int rows);
+// CTAs for `units` (of a cluster's rows).
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
 cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,
                               const PagedAttnParams& p, int grid, cudaStream_t stream);

@@ -28,7 +28,9 @@ int paged_attn_row_block(int kind, int rows) {
   return kind == kLatent && rows <= 32 ? 32 : 64;
 }
 
-// CTAs an SM holds (PagedShape's last number).
+int paged_attn_cluster(int kind, int rows) { return kind == kLatent && rows > 64 ? 2 : 1; }
+
+// CTAs an SM holds (PagedShape's kCtas).
 static int paged_attn_ctas(int kind, int block) {
   if (kind == kLatent) return 1;
   return block == 16 ? 2 : 1;
@@ -38,9 +40,10 @@ int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count)
   const long long chunks = units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys);
   const long long most = room <= kCacheWholeKeys ? units
                                                  : (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
+  const int cluster = paged_attn_cluster(kind, rows);
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
-                          paged_attn_ctas(kind, paged_attn_row_block(kind, rows));
-  return static_cast<int>(most < slots ? most : slots);
+                          paged_attn_ctas(kind, paged_attn_row_block(kind, rows)) / cluster;
+  return static_cast<int>(most < slots ? most : slots) * cluster;
 }
 
 }  // namespace fa
@@ -148,7 +151,8 @@ AttnPlan plan_attn(int kind, int B, int H, int Hkv, int Sq, const PageShape& s, 
   AttnPlan a{};
   const int rows = (H / Hkv) * Sq, block = fa::paged_attn_row_block(kind, rows);
   const int room = s.max_pages * s.page_size;
-  a.row_blocks = (rows + block - 1) / block;
+  const int cluster_rows = block * fa::paged_attn_cluster(kind, rows);
+  a.row_blocks = (rows + cluster_rows - 1) / cluster_rows;
   a.part_rows = (std::min(rows, block) + 3) & ~3;
   a.grid = fa::paged_attn_grid(kind, rows, static_cast<long long>(B) * Hkv * a.row_blocks, room,
                                sm_count);

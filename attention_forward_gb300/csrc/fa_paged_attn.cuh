@@ -38,10 +38,14 @@ constexpr int kPagedKeys = kCacheAttnKeys;  // 64 keys: a tile, and a chunk of t
 
 // kKC, kVC: 64-channel chunks of a key and of a value; kShared: the value is the
 // key's first chunks.  kN: query rows of a CTA.
-template <int kKC_, int kVC_, bool kShared_, int kN_, int kStages_, int kCtas_, int kPs_ = 2>
+// kCluster: CTAs that share the keys, each with a block of query rows (latent rows
+// only).
+template <int kKC_, int kVC_, bool kShared_, int kN_, int kStages_, int kCtas_, int kPs_ = 2,
+          int kCluster_ = 1>
 struct PagedShape {
   static constexpr int kKC = kKC_, kVC = kVC_, kN = kN_, kStages = kStages_, kCtas = kCtas_;
   static constexpr int kPs = kPs_;  // buffers for P
+  static constexpr int kCluster = kCluster_;
   static constexpr bool kShared = kShared_;
   static constexpr int kWarps = kShared ? 6 : 7, kThreads = 32 * kWarps;
   static constexpr int kDv = 64 * kVC;
@@ -59,6 +63,7 @@ struct PagedShape {
       kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr int kOffP = kQBytes, kOffRing = kOffP + kPs * kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kStageBytes;
+  static_assert(kCluster == 1 || (kCluster == 2 && kShared), "pairs over latent rows");
   static_assert(kVC == 1 || kVC % 2 == 0, "values of 64 channels, or of 128 a block");
   static_assert(kOffP % 1024 == 0 && kOffRing % 1024 == 0, "128-byte swizzled tiles");
   static_assert(kCols <= 512 && kCtas * kTmemCols <= 512, "tensor memory");
@@ -100,6 +105,7 @@ constexpr int paged_smem_bytes() {
 
 // The CTA's segments: ranges of one unit's keys.
 struct PagedWalk {
+  int cta, ctas, rank;   // of the deal: a CTA, or a cluster; the CTA's rank in it
   int cur, first, last;  // chunks, or units where they are not split
   int b, len, before;    // the sequence, its length, the chunks of those before it
 };
@@ -110,7 +116,7 @@ struct PagedSeg {
   const int* pages;
 };
 
-template <int kN>
+template <int kN, int kCluster>
 __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& w, PagedSeg& s) {
   if (w.cur >= w.last) return false;
   const int units = p.Hkv * p.n_row_blocks;
@@ -121,11 +127,10 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
   const int chunk0 = p.whole ? 0 : w.cur - w.before - unit * seq_chunks;
   const int n_chunks = p.whole ? seq_chunks : min(seq_chunks - chunk0, w.last - w.cur);
   s.whole = n_chunks == seq_chunks;
-  s.part = 2 * static_cast<int>(blockIdx.x) + (w.cur == w.first ? 0 : 1);
+  s.part = (2 * w.cta + (w.cur == w.first ? 0 : 1)) * kCluster + w.rank;
   s.hk = unit / p.n_row_blocks;
-  const int rb = unit - s.hk * p.n_row_blocks;
-  s.row0 = rb * kN;
-  s.n_rows = min(kN, p.rows - s.row0);
+  s.row0 = ((unit - s.hk * p.n_row_blocks) * kCluster + w.rank) * kN;
+  s.n_rows = max(0, min(kN, p.rows - s.row0));  // a cluster's last may have none
   s.out_row0 = (static_cast<long long>(w.b) * p.Hkv + s.hk) * p.rows + s.row0;
   s.seq = w.b;
   s.len = w.len;
@@ -134,7 +139,7 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
   s.n_tiles = (s.k_end - s.k_begin + kPagedKeys - 1) / kPagedKeys;
   s.pages = p.page_table + static_cast<long long>(w.b) * p.max_pages;
   if (p.whole) {
-    w.cur += static_cast<int>(gridDim.x);
+    w.cur += w.ctas;
   } else {
     w.cur += n_chunks;
     if (chunk0 + n_chunks == seq_chunks && unit == units - 1) {
@@ -170,7 +175,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   if (threadIdx.x == 0) {
     for (int i = 0; i < PagedMiscBars::kMaxStages; ++i) {
       mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, 1);
+      mbar_init(k_empty + 8 * i, S::kCluster);
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
     }
@@ -194,6 +199,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     if constexpr (!S::kShared) tma_prefetch_desc(&tmV);
   }
   tc_fence_before();
+  if constexpr (S::kCluster > 1) cluster_sync_all();  // its barriers are there
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
@@ -202,16 +208,19 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   grid_launch_dependents();  // this grid's CTAs have their tensor memory
 
   PagedWalk walk{};
+  walk.cta = static_cast<int>(blockIdx.x) / S::kCluster;
+  walk.ctas = static_cast<int>(gridDim.x) / S::kCluster;
+  walk.rank = S::kCluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   if (p.whole) {
-    walk.first = static_cast<int>(blockIdx.x);
+    walk.first = walk.cta;
     walk.last = p.B * p.Hkv * p.n_row_blocks;
   } else {
     int upto;
     const int all = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
-    const CacheDeal deal = cache_deal(all, static_cast<int>(gridDim.x));
-    if (static_cast<int>(blockIdx.x) < deal.n) {
-      walk.first = deal.begin(static_cast<int>(blockIdx.x));
-      walk.last = deal.begin(static_cast<int>(blockIdx.x) + 1);
+    const CacheDeal deal = cache_deal(all, walk.ctas);
+    if (walk.cta < deal.n) {
+      walk.first = deal.begin(walk.cta);
+      walk.last = deal.begin(walk.cta + 1);
       cache_find(p, sm.scan, upto, walk.first, walk.b, walk.len, walk.before);
     }
   }
@@ -256,14 +265,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       if (lane == 0) mbar_arrive(q_full);
     };
     PagedSeg next;
-    bool more = paged_next<kN>(p, walk, seg);
+    bool more = paged_next<kN, S::kCluster>(p, walk, seg);
     if (more) load_q(seg);
 #pragma unroll 1
     while (more) {
       if (p.whole && threadIdx.x == 0 && seg.len != p.length[seg.seq])
         atomicMax(p.status, kStatusBadIndex);
       for (int n = threadIdx.x; n < kN; n += 128) {
-        const int rr = min(n, seg.n_rows - 1) + seg.row0;
+        const int rr = min(min(n, seg.n_rows - 1) + seg.row0, p.rows - 1);
         const int h = rr / p.Sq, i = rr - h * p.Sq;
         sm.limit[n] = n < seg.n_rows ? seg.len - (p.Sq - 1 - i) : seg.len;
         if constexpr (kMod)
@@ -414,7 +423,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       ok = !named_bar_or(1, 128, !ok);
       if (!ok) break;
       // the next segment's queries first: its scores run beside what follows
-      more = paged_next<kN>(p, walk, next);
+      more = paged_next<kN, S::kCluster>(p, walk, next);
       if (more) load_q(next);
 #pragma unroll
       for (int n = 0; n < kNB; ++n)
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     uint32_t t0 = 0, nq = 0;  // tiles, and segments with tiles, before this one
     bool ok = true, issued = false;
 #pragma unroll 1
-    while (ok && paged_next<kN>(p, walk, seg)) {
+    while (ok && paged_next<kN, S::kCluster>(p, walk, seg)) {
       const uint32_t n = static_cast<uint32_t>(seg.n_tiles);
       if (n == 0) continue;
       if (!wait_bar_warp(q_full, nq & 1u, ctl)) break;
@@ -552,7 +561,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           for (int blk = 0; blk < S::kBlocks; ++blk)
             umma_f16_ss(tmem + S::kColO + blk * kN, a + blk * (2048 >> 4) + k * (2 * S::kVStride >> 4),
                         b + 2 * k, kIdescO, (o > 0 || k > 0) ? 1u : 0u);
-          if constexpr (S::kShared) umma_commit(k_empty + 8 * (4 * stage + k));
+          if constexpr (S::kCluster > 1)
+            umma_commit_multicast(k_empty + 8 * (4 * stage + k), 3);
+          else if constexpr (S::kShared)
+            umma_commit(k_empty + 8 * (4 * stage + k));
         }
         if constexpr (!S::kShared) umma_commit(v_empty + 8 * stage);
         umma_commit(o_done + 8 * ((t0 + o) & 1u));
@@ -617,7 +629,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     uint32_t t = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && paged_next<kN>(p, walk, seg)) {
+    while (ok && paged_next<kN, S::kCluster>(p, walk, seg)) {
       // four tiles' places at a time, a lane for each 8 keys, the next four's fetched
       // ahead
       const int page_keys = 1 << p.page_shift;
@@ -642,18 +654,25 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int k = 0; ok && k < 4 && j0 + k < seg.n_tiles; ++k, ++t) {
           const uint32_t stage = t % kStages, full = full0 + 8 * stage, par = ((t / kStages) & 1u) ^ 1u;
           const uint32_t dst = ring + stage * bytes;
-          constexpr int kTurns = S::kShared ? 4 : 1;  // a latent stage 16 keys at a time
+          // a latent stage 16 keys at a time; in a cluster of two half of them, which go to
+          // both CTAs (an mbarrier may count the other's bytes before its own expects them)
+          constexpr int kTurns = S::kShared ? 4 / S::kCluster : 1;
 #pragma unroll 1
           for (int i = 0; ok && i < kTurns; ++i) {
-            ok = wait_bar_warp(empty0 + 8 * (kTurns * stage + i), par, ctl);
+            const int block = walk.rank * kTurns + i;
+            ok = wait_bar_warp(empty0 + 8 * (S::kShared ? 4 * stage + block : stage), par, ctl);
             if (!ok) break;
             if (i == 0 && lane == 0) {
               if (is_k) sm.bad[t % kPagedBad] = (bad >> (8 * k)) & 0xffu;
               mbar_arrive_expect_tx(full, bytes);
             }
             __syncwarp();
-            if ((lane >> 3) == k && (kTurns == 1 || ((lane & 7) >> 1) == i))
-              tma_load_4d(dst, tm, full, 0, row, 0, at);
+            if ((lane >> 3) == k && (!S::kShared || ((lane & 7) >> 1) == block)) {
+              if constexpr (S::kCluster > 1)
+                tma_load_4d_multicast(dst, tm, full, 0, row, 0, at, 3);
+              else
+                tma_load_4d(dst, tm, full, 0, row, 0, at);
+            }
             __syncwarp();
           }
         }
@@ -663,6 +682,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     // the last tile's unsent: the wait is bounded)
     for (uint32_t i = t > kStages ? t - kStages : 0u; i < t; ++i)
       wait_drain(full0 + 8 * (i % kStages), (i / kStages) & 1u, p.timeout_ns);
+    // and so does every arrival that the other CTA's products make here
+    if constexpr (S::kCluster > 1)
+      for (uint32_t i = t > kStages ? t - kStages : 0u; ok && i < t; ++i)
+        for (uint32_t k = 0; k < 4; ++k)
+          wait_drain(k_empty + 8 * (4 * (i % kStages) + k), (i / kStages) & 1u, p.timeout_ns);
     __syncwarp();
   }
 
@@ -672,6 +696,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
+  if constexpr (S::kCluster > 1) cluster_sync_all();  // the other CTA writes here no more
 }
 
 // The units that several CTAs shared: O = sum_s w_s O_s / sum_s w_s over their parts,
@@ -700,9 +725,11 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
     alignas(16) uint16_t out[kN * kCh];
   } end;
   const int tid = static_cast<int>(threadIdx.x);
-  const int units = p.Hkv * p.n_row_blocks;
+  // a unit of the deal and, in clusters, the rank of the CTA whose rows these are
+  const int units = p.Hkv * p.n_row_blocks, rank = static_cast<int>(blockIdx.z);
   const int b = static_cast<int>(blockIdx.x) / units, unit = static_cast<int>(blockIdx.x) - b * units;
-  const int hk = unit / p.n_row_blocks, rb = unit - hk * p.n_row_blocks;
+  const int hk = unit / p.n_row_blocks;
+  const int rb = (unit - hk * p.n_row_blocks) * S::kCluster + rank;
   const int ch0 = static_cast<int>(blockIdx.y) * kCh;
   int upto;
   const int all = cache_scan(p, scan, false, upto);
@@ -721,8 +748,8 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
   if (x0 == x1) return;
   // a CTA's first segment, except where the unit begins inside x0
   const int inside = deal.begin(x0) < start ? 1 : 0;
-  auto part_of = [&](int s) { return 2 * (x0 + s) + (s == 0 ? inside : 0); };
-  const int n_parts = x1 - x0 + 1, n_rows = min(kN, p.rows - rb * kN);
+  auto part_of = [&](int s) { return (2 * (x0 + s) + (s == 0 ? inside : 0)) * S::kCluster + rank; };
+  const int n_parts = x1 - x0 + 1, n_rows = max(0, min(kN, p.rows - rb * kN));
   const int quads = p.part_rows / 4, items = kCh * quads;  // four rows of a channel each
   const int groups = items < kThr ? kThr / items : 1;
   const int group = items < kThr ? tid / items : 0;
