@@ -298,9 +298,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 #pragma unroll
         for (int n = 0; n < kNB; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            asm volatile("" : "+r"(raw[n][e]));  // not before the wait
-            s[n][e] = __uint_as_float(raw[n][e]) * fac;
+          for (int e = 0; e < 4; e += 2) {
+            asm volatile("" : "+r"(raw[n][e]), "+r"(raw[n][e + 1]));  // not before the wait
+            ffma2(s[n][e], s[n][e + 1], __uint_as_float(raw[n][e]), __uint_as_float(raw[n][e + 1]), fac,
+                  fac, 0.f, 0.f);
           }
         const int k0 = key0 + 16 * warp + g;  // this lane's keys: k0, k0 + 8
         if constexpr (kMod) {
@@ -338,12 +339,23 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             }
           }
         }
-        bool over = false;
+        // above the references, and the largest of this lane's
+        float x[kNB][4], over = -INFINITY;
+        auto above = [&]() {
 #pragma unroll
-        for (int n = 0; n < kNB; ++n)
-          over = over || fmaxf(s[n][0], s[n][2]) > m[n][0] + kTau ||
-                 fmaxf(s[n][1], s[n][3]) > m[n][1] + kTau;
-        if (named_bar_or(1, 128, over || !ok)) {
+          for (int n = 0; n < kNB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              fadd2(x[n][e], x[n][e + 1], s[n][e], s[n][e + 1], -m[n][0], -m[n][1]);
+              over = fmax3(over, x[n][e], x[n][e + 1]);
+            }
+        };
+        above();
+        // whether the product that had P's buffer has read it, asked before the
+        // exponentials (a segment's first ones: its end waited)
+        const uint32_t p_free = o_done + 8 * ((t - S::kPs) & 1u), p_par = ((t - S::kPs) >> 1) & 1u;
+        const bool free_now = j < S::kPs || mbar_test_wait(p_free, p_par);
+        if (named_bar_or(1, 128, over > kTau || !ok)) {
           // rare: a row's reference rises, or a wait ran out somewhere
           if (named_bar_or(1, 128, !ok)) {
             ok = false;
@@ -392,23 +404,20 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             }
             tmem_wait_st();
           }
+          above();
         }
         uint32_t pk[kNB][2];
 #pragma unroll
         for (int n = 0; n < kNB; ++n) {
           float e[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            e[k] = ex2_approx(s[n][k] - m[n][k & 1]);
-            l[n][k & 1] += e[k];
-          }
+          for (int k = 0; k < 4; ++k) e[k] = ex2_approx(x[n][k]);
+          fadd2(l[n][0], l[n][1], l[n][0], l[n][1], e[0], e[1]);
+          fadd2(l[n][0], l[n][1], l[n][0], l[n][1], e[2], e[3]);
           pk[n][0] = pack2<BF16>(e[0], e[1]);
           pk[n][1] = pack2<BF16>(e[2], e[3]);
         }
-        // the product that had this buffer has read it (a segment's first ones: its end
-        // waited)
-        if (j >= S::kPs)
-          ok = ok && wait_bar_warp(o_done + 8 * ((t - S::kPs) & 1u), ((t - S::kPs) >> 1) & 1u, ctl);
+        if (!__all_sync(0xffffffffu, free_now)) ok = ok && wait_bar_warp(p_free, p_par, ctl);
         const uint32_t p_buf = p_at + (S::kPs > 1 ? buf * S::kPBytes : 0u);
 #pragma unroll
         for (int n = 0; n < kNB; n += 2)
@@ -675,6 +684,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             }
             __syncwarp();
           }
+          // two latent tiles in flight are not enough for HBM's latency: the next four
+          // come to L2 meanwhile
+          if constexpr (S::kCluster > 1)
+            if (k == 1) {
+              const int next_row = row_of(key + 4 * kPagedKeys, ahead);
+              if (next_row != p.pool_rows && ((lane & 7) >> 2) == walk.rank)
+                tma_prefetch_l2_4d(tm, 0, next_row, 0, at);
+              __syncwarp();
+            }
         }
       }
     }

@@ -163,6 +163,15 @@ __device__ __forceinline__ void tma_prefetch_l2_3d(const void* desc, int32_t x,
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_l2_4d(const void* desc, int32_t x, int32_t y, int32_t z,
+                                                   int32_t w) {
+  asm volatile(
+      "cp.async.bulk.prefetch.tensor.4d.L2.global [%0, {%1, %2, %3, %4}];" ::"l"(
+          reinterpret_cast<uint64_t>(desc)),
+      "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
 // 3-D tiled store shared -> global (bulk-group completion).
 __device__ __forceinline__ void tma_store_3d(const void* desc, uint32_t src,
                                              int32_t x, int32_t y, int32_t z) {
