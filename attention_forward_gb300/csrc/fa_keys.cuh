@@ -44,10 +44,10 @@ struct CacheDeal {
   }
 };
 
-// At least kCacheMinChunks chunks to a CTA.
-__device__ __forceinline__ CacheDeal cache_deal(int all, int grid) {
+// At least `least` chunks to a CTA.
+__device__ __forceinline__ CacheDeal cache_deal(int all, int grid, int least = kCacheMinChunks) {
   CacheDeal d;
-  d.n = min((all + kCacheMinChunks - 1) / kCacheMinChunks, grid);
+  d.n = min((all + least - 1) / least, grid);
   d.per = all / d.n;
   d.more = all - d.per * d.n;
   return d;

@@ -81,6 +81,17 @@ int paged_attn_row_block(int kind, int rows);
 // CTAs of a cluster, which share the keys: 2 for latent rows where there are more query
 // rows than a CTA takes.
 int paged_attn_cluster(int kind, int rows);
+// A CTA's least share of the keys, in chunks: the whole pipeline starts in one chunk's
+// time, and the merge's is the same for any number of parts.  By 1, 2 and 4 chunks, us:
+// 3 sequences of 704 latent keys 10.3, 12.5, 14.9; 8 units of 704 keys (128 channels)
+// 8.6, 10.7, 11.4, of 2048 9.2, 10.1, 10.1, of 4096 11.1, 10.6, 10.2.
+constexpr int kPagedMinChunks = 1;
+// Whether page tables with room for that many keys are dealt in whole units, without a
+// merge.  Whole and split, us: 8 units of 128 channels 8.5 and 8.4 at 512 keys, 10.2 and
+// 8.6 at 704; 64 units 10.3 and 12.3 at 704, 13.3 and 12.6 at 1024; latent rows, 1 unit
+// 6.9 and 9.4 at 128 keys, 9.6 and 9.4 at 256, 64 units 14.7 and 15.3 at 512, 18.9 and
+// 17.9 at 704, 152 units 26.6 and 31.1 at 704.
+bool paged_attn_whole(int kind, long long units, int room, int sm_count);
 // CTAs for `units` (of a cluster's rows).
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
 cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,

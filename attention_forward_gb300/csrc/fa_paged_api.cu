@@ -36,10 +36,20 @@ static int paged_attn_ctas(int kind, int block) {
   return block == 16 ? 2 : 1;
 }
 
+bool paged_attn_whole(int kind, long long units, int room, int sm_count) {
+  const int sms = sm_count > 0 ? sm_count : 152;
+  int most = kind == kLatent ? 256 : 512;
+  if (units >= sms)
+    most = 1024;
+  else if (5 * units >= 2 * sms)
+    most *= 2;
+  return room <= most;
+}
+
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count) {
   const long long chunks = units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys);
-  const long long most = room <= kCacheWholeKeys ? units
-                                                 : (chunks + kCacheMinChunks - 1) / kCacheMinChunks;
+  const long long most = paged_attn_whole(kind, units, room, sm_count)
+                             ? units : (chunks + kPagedMinChunks - 1) / kPagedMinChunks;
   const int cluster = paged_attn_cluster(kind, rows);
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
                           paged_attn_ctas(kind, paged_attn_row_block(kind, rows)) / cluster;
@@ -89,8 +99,8 @@ fa_status_t check(const void* pool0, const void* pool1, const int* page_table, i
   return FA_OK;
 }
 
-// Tokens of a block and slices of its tasks: 8 tokens whole where they make blocks
-// enough for the GPU, else a task a thread.
+// Tokens of a block and slices of its heads: 8 tokens with all heads where they make
+// blocks enough for the GPU, else a head a thread.
 fa_status_t write(bool latent, fa::PagedWriteParams& p, int pairs, const PageShape& s, int dtype,
                   cudaStream_t stream) {
   if (!aligned(p.q, 16) || !aligned(p.q_out, 16) || !aligned(p.k, 16) || !aligned(p.v, 16) ||
@@ -109,9 +119,9 @@ fa_status_t write(bool latent, fa::PagedWriteParams& p, int pairs, const PageSha
   const long long blocks = ((static_cast<long long>(p.S) + (1 << p.token_shift) - 1) >> p.token_shift) * p.B;
   int slices = 1;
   if (blocks < 4LL * env.sm_count) {
-    const int per_head = latent ? 4 : p.D / 16;
-    const int tasks = ((p.H + p.Hkv) * per_head + p.Hkv * (latent ? 32 : per_head)) << p.token_shift;
-    slices = (tasks + 255) / 256;
+    const int heads = p.H + p.Hkv + (latent ? fa::kLatent / fa::kLatentRope : p.Hkv);
+    const int at_once = 256 / ((latent ? 4 : p.D / 16) << p.token_shift);
+    slices = (heads + at_once - 1) / at_once;
   }
   const cudaError_t e = fa::launch_paged_write(latent, dtype == FA_BF16, pairs != 0, p, slices, stream);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
@@ -154,9 +164,9 @@ AttnPlan plan_attn(int kind, int B, int H, int Hkv, int Sq, const PageShape& s, 
   const int cluster_rows = block * fa::paged_attn_cluster(kind, rows);
   a.row_blocks = (rows + cluster_rows - 1) / cluster_rows;
   a.part_rows = (std::min(rows, block) + 3) & ~3;
-  a.grid = fa::paged_attn_grid(kind, rows, static_cast<long long>(B) * Hkv * a.row_blocks, room,
-                               sm_count);
-  a.whole = room <= fa::kCacheWholeKeys ? 1 : 0;
+  const long long units = static_cast<long long>(B) * Hkv * a.row_blocks;
+  a.grid = fa::paged_attn_grid(kind, rows, units, room, sm_count);
+  a.whole = fa::paged_attn_whole(kind, units, room, sm_count) ? 1 : 0;
   if (!a.whole) {
     const size_t parts = 2u * static_cast<size_t>(a.grid);
     a.o_bytes = up256(parts * a.part_rows * kind * sizeof(float));

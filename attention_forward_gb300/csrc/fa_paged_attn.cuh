@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   } else {
     int upto;
     const int all = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
-    const CacheDeal deal = cache_deal(all, walk.ctas);
+    const CacheDeal deal = cache_deal(all, walk.ctas, kPagedMinChunks);
     if (walk.cta < deal.n) {
       walk.first = deal.begin(walk.cta);
       walk.last = deal.begin(walk.cta + 1);
@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
   const int ch0 = static_cast<int>(blockIdx.y) * kCh;
   int upto;
   const int all = cache_scan(p, scan, false, upto);
-  const CacheDeal deal = cache_deal(all, attn_grid);
+  const CacheDeal deal = cache_deal(all, attn_grid, kPagedMinChunks);
   // chunks per unit of the sequences before b: the thread with b in its run
   const int run = (p.B + kThr - 1) / kThr;
   if (b / run == tid) {

@@ -9,11 +9,10 @@
 // fp32 would be off by half a radian.
 //
 // Both kernels only move bytes.  Write: a block takes 2^token_shift tokens of a
-// sequence.  Its threads make the tokens' sines and cosines, one each, then take
-// 16 channels at a time: the pairs of 8 frequencies (two 16-byte words that lie
-// apart by half of what is rotated, or side by side), or 16 channels as they are.
-// Neighbouring threads take neighbouring words of a row, then the next token's, whose
-// row follows in the input.
+// sequence and a slice of their heads.  A thread keeps to 16 channels of one token:
+// two 16-byte words of a row, the halves of 8 pairs (which lie apart by half of what is
+// rotated, or side by side), and goes through the heads with the 8 sines and cosines in
+// registers, made once by the block.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -54,9 +53,8 @@ __device__ __forceinline__ float2 rope_unit(int n, unsigned long long step) {
 // Two 16-byte words of 16-bit channels: the pairs (e, e) of both words, or (2 e, 2 e
 // + 1) of one, rotated by unit[0 ... 7].
 template <bool BF16, bool kPairs>
-__device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float2* unit) {
-  uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-  uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+__device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float2 (&unit)[8]) {
+  uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wb[4] = {b.x, b.y, b.z, b.w};
   auto turn = [](float& x, float& y, float2 u) {
     const float t = fmaf(x, u.x, -y * u.y);
     y = fmaf(y, u.x, x * u.y);
@@ -75,6 +73,8 @@ __device__ __forceinline__ void rope_turn(uint4& a, uint4& b, const float2* unit
     wa[e] = cache_pack<BF16>(x.x, x.y);
     wb[e] = cache_pack<BF16>(y.x, y.y);
   }
+  a = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+  b = make_uint4(wb[0], wb[1], wb[2], wb[3]);
 }
 
 // The slot of the token at position `pos` of sequence b as a row of kv head 0; -1
@@ -90,126 +90,98 @@ __device__ __forceinline__ long long paged_slot(const P& p, int b, uint32_t pos)
 }
 
 template <bool kLat, bool BF16, bool kPairs>
-__global__ void __launch_bounds__(kPagedCopyThreads, 4)
+__global__ void __launch_bounds__(kPagedCopyThreads, 3)
     fa_paged_write_kernel(const PagedWriteParams p) {
-  __shared__ float2 unit[kPagedMaxPairs << kPagedMaxTokenShift];  // [token][pair]
-  __shared__ long long slot[1 << kPagedMaxTokenShift];
+  __shared__ float2 units[kPagedMaxPairs << kPagedMaxTokenShift];  // [token][pair]
   grid_dependency_wait();
   grid_launch_dependents();
-  const int b = static_cast<int>(blockIdx.y);
-  const int first = static_cast<int>(blockIdx.x) << p.token_shift;
+  const int b = static_cast<int>(blockIdx.y), tid = static_cast<int>(threadIdx.x);
+  const int ts = p.token_shift, first = static_cast<int>(blockIdx.x) << ts;
+  // the thread's 16 channels of every row, its token, and the first of its heads
+  const int d_shift = kLat ? 2 : (p.D == 128 ? 3 : 2), d = kLat ? kLatentRope : p.D;
+  const int u = tid & ((1 << d_shift) - 1);
+  const int token = first + ((tid >> d_shift) & ((1 << ts) - 1));
+  const int step = kPagedCopyThreads >> (d_shift + ts);
   const int half = p.rot >> 1;
-  // those there are, before the count is known: the first words are on their way by then
-  int tokens = min(1 << p.token_shift, p.S - first);
-
-  // a row's tasks: 16 channels each; rows of q, of k, then of v
-  const int d_shift = kLat ? 2 : (p.D == 128 ? 3 : 2);  // tasks of a row of q or k
-  const int v_shift = kLat ? 5 : d_shift;
-  const int ts = p.token_shift;
-  const int n_q = p.H << (ts + d_shift), n_k = p.Hkv << (ts + d_shift);
-  const int n_v = p.Hkv << (ts + v_shift);
-  const int all = n_q + n_k + n_v;
+  const bool turned = 16 * u < p.rot, halves = turned && !kPairs;
+  const int w0 = halves ? u : 2 * u, w1 = halves ? u + (half >> 3) : 2 * u + 1;
+  // heads of q, of k, then of v (the latent as eight of 64 channels)
+  constexpr int kLatHeads = kLatent / kLatentRope;
+  const int h_v = p.H + p.Hkv, all = h_v + (kLat ? kLatHeads : p.Hkv);
   const int per = (all + static_cast<int>(gridDim.z) - 1) / static_cast<int>(gridDim.z);
-  const int t0 = per * static_cast<int>(blockIdx.z), t1 = min(all, t0 + per);
-
-  struct Task {
-    int token, pair;  // pair: the first of its 8, or -1
-  };
-  const int D = kLat ? kLatentRope : p.D;
-  // a task, and its words; past the end, a token that there is not
-  auto source = [&](int id, Task& t, uint4& x, uint4& y) {
-    t.pair = -1;
-    t.token = 1 << kPagedMaxTokenShift;
-    if (id >= t1) return;
-    int r = id, shift = d_shift, heads = p.H;
-    const void* in = p.q;
-    bool turned = p.rot > 0;
-    if (r >= n_q) {
-      r -= n_q;
-      heads = p.Hkv;
-      in = p.k;
-      if (r >= n_k) {
-        r -= n_k;
-        shift = v_shift;
-        in = p.v;
-        turned = false;
-      }
-    }
-    const int u = r & ((1 << shift) - 1), token = (r >> shift) & ((1 << ts) - 1);
-    if (token >= tokens) return;
-    t.token = token;
-    const int head = r >> (shift + ts);
-    if (turned && 16 * u < p.rot) t.pair = 8 * u;
-    const bool halves = t.pair >= 0 && !kPairs;
-    const uint4* row = static_cast<const uint4*>(in) +
-                       (((static_cast<long long>(b) * heads + head) * p.S + first + token)
-                        << (shift + 1)) + (halves ? u : 2 * u);
-    x = __ldcs(row);
-    y = __ldcs(row + (halves ? half >> 3 : 1));
-  };
-  // its words to their place
-  auto target = [&](int id, const Task& t, const uint4& x, const uint4& y) {
-    int r = id;
-    const bool is_q = r < n_q, is_v = r >= n_q + n_k;
-    const int shift = is_v ? v_shift : d_shift;
-    r -= is_q ? 0 : (is_v ? n_q + n_k : n_q);
-    const int head = r >> (shift + ts), u = r & ((1 << shift) - 1);
-    const bool halves = t.pair >= 0 && !kPairs;
-    uint4* row;
-    if (is_q) {
-      row = static_cast<uint4*>(p.q_out) +
-            ((static_cast<long long>(b) * p.H + head) * p.S + first + t.token) * (p.q_width >> 3) +
-            ((p.q_width - D) >> 3);
-    } else {
-      const long long s = slot[t.token];
-      if (s < 0) return;
-      if constexpr (kLat) {
-        row = static_cast<uint4*>(p.pool[0]) + s * (kLatentRow / 8) + (is_v ? 0 : kLatent / 8);
-      } else {
-        row = static_cast<uint4*>(is_v ? p.pool[1] : p.pool[0]) +
-              ((s + (static_cast<long long>(head) << p.page_shift)) << (d_shift + 1));
-      }
-    }
-    row += halves ? u : 2 * u;
-    row[0] = x;
-    row[halves ? half >> 3 : 1] = y;
+  const int h1 = min(all, per * (static_cast<int>(blockIdx.z) + 1));
+  int h = per * static_cast<int>(blockIdx.z) + (tid >> (d_shift + ts));
+  auto source = [&](int i) -> const uint4* {
+    const bool is_q = i < p.H, is_v = i >= h_v;
+    const uint4* in = static_cast<const uint4*>(is_q ? p.q : (is_v ? p.v : p.k));
+    if (kLat && is_v)
+      return in + (static_cast<long long>(b) * p.S + token) * (kLatent / 8) + (i - h_v) * 8;
+    const int heads = is_q ? p.H : p.Hkv, head = is_q ? i : i - (is_v ? h_v : p.H);
+    return in + (((static_cast<long long>(b) * heads + head) * p.S + token) << (d_shift + 1));
   };
 
-  bool ready = false;
+  uint4 x[kPagedAtOnce], y[kPagedAtOnce];
+  // (rows past the count are there all the same: the first words need not wait for it)
+  auto load = [&]() {
+#pragma unroll
+    for (int k = 0; k < kPagedAtOnce; ++k)
+      if (h + k * step < h1 && token < p.S) {
+        const uint4* in = source(h + k * step);
+        x[k] = __ldcs(in + w0);
+        y[k] = __ldcs(in + w1);
+      }
+  };
+  load();
+  const int start = p.start ? p.start[b] : 0;
+  const int count = p.count ? min(p.count[b], p.S) : p.S;
+  if (first >= count) return;
+  float2 unit[8];
+  if (half > 0) {
+    for (int i = tid; i < half << ts; i += kPagedCopyThreads) {
+      const int tok = i / half;
+      units[i] = rope_unit(static_cast<int>(static_cast<uint32_t>(start) +
+                                            static_cast<uint32_t>(first + tok)),
+                           rope_step(p.freqs[i - tok * half]));
+    }
+    __syncthreads();
+    if (turned) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) unit[e] = units[(token - first) * half + 8 * u + e];
+    }
+  }
+  if (token >= count) return;
+  const long long slot =
+      paged_slot(p, b, static_cast<uint32_t>(start) + static_cast<uint32_t>(token));
+  if (slot < 0 && u == 0 && h == 0) atomicMax(p.status, kStatusBadIndex);
 #pragma unroll 1
-  for (int base = t0; base < t1 || !ready; base += kPagedCopyThreads * kPagedAtOnce) {
-    Task t[kPagedAtOnce];
-    uint4 x[kPagedAtOnce], y[kPagedAtOnce];
+  for (;;) {
 #pragma unroll
     for (int k = 0; k < kPagedAtOnce; ++k) {
-      source(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k], x[k], y[k]);
-    }
-    if (!ready) {
-      const int start = p.start ? p.start[b] : 0;
-      const int count = p.count ? min(p.count[b], p.S) : p.S;
-      if (first >= count) return;
-      tokens = min(tokens, count - first);
-      if (static_cast<int>(threadIdx.x) < tokens) {
-        const uint32_t pos = static_cast<uint32_t>(start) + static_cast<uint32_t>(first) + threadIdx.x;
-        const long long s = paged_slot(p, b, pos);
-        slot[threadIdx.x] = s;
-        if (s < 0 && blockIdx.z == 0) atomicMax(p.status, kStatusBadIndex);
+      const int i = h + k * step;
+      if (i >= h1) break;
+      const bool is_q = i < p.H, is_v = i >= h_v;
+      if (turned && !is_v) rope_turn<BF16, kPairs>(x[k], y[k], unit);
+      uint4* out;
+      if (is_q) {
+        out = static_cast<uint4*>(p.q_out) +
+              ((static_cast<long long>(b) * p.H + i) * p.S + token) * (p.q_width >> 3) +
+              ((p.q_width - d) >> 3);
+      } else if (slot < 0) {
+        continue;
+      } else if constexpr (kLat) {
+        out = static_cast<uint4*>(p.pool[0]) + slot * (kLatentRow / 8) +
+              (is_v ? 8 * (i - h_v) : kLatent / 8);
+      } else {
+        const long long head = i - (is_v ? h_v : p.H);
+        out = static_cast<uint4*>(is_v ? p.pool[1] : p.pool[0]) +
+              ((slot + (head << p.page_shift)) << (d_shift + 1));
       }
-      for (int i = threadIdx.x; i < tokens * half; i += kPagedCopyThreads) {
-        const int tok = i / half;
-        unit[i] = rope_unit(static_cast<int>(static_cast<uint32_t>(start) +
-                                             static_cast<uint32_t>(first + tok)),
-                            rope_step(p.freqs[i - tok * half]));
-      }
-      __syncthreads();
-      ready = true;
+      out[w0] = x[k];
+      out[w1] = y[k];
     }
-#pragma unroll
-    for (int k = 0; k < kPagedAtOnce; ++k) {
-      if (t[k].token >= tokens) continue;
-      if (t[k].pair >= 0) rope_turn<BF16, kPairs>(x[k], y[k], unit + t[k].token * half + t[k].pair);
-      target(base + k * kPagedCopyThreads + static_cast<int>(threadIdx.x), t[k], x[k], y[k]);
-    }
+    h += kPagedAtOnce * step;
+    if (h >= h1) break;
+    load();
   }
 }
 
