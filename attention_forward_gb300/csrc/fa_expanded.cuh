@@ -13,8 +13,9 @@
 // two tiles do not fit.  Keys and values therefore go through one ring of eight
 // 16 KB chunks, five a tile in the order of their use:
 //   K chunk c (3): 128 keys x 64 channels;  V chunk h (2): 64 keys x 128 channels
-// each with its own barriers, so that a product starts with its first chunk and
-// frees each as it is done with it; the ring runs 1.6 tiles ahead.  O goes from
+// The ring runs 1.6 tiles ahead.  A tile's K, and its V, have one pair of barriers each:
+// with a pair for every chunk, the issuing warp's waits and commits took 4430 cycles a
+// tile of two stages, whose products take 2560.  O goes from
 // registers to global memory (its staging's 32 KB are the ring's).
 #pragma once
 #include "fa_paged.h"
@@ -38,8 +39,9 @@ struct ExpandedLayout {
   static constexpr int kOffBars = kOffRing + kSlots * kChunk;
   // mbarrier indices, as the prefill kernel's
   static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, PV_READY = 6, O_READY = 8, ML_FULL = 10,
-                       O_FREE = 12, DRAIN = 14, ITEM_FULL = 15, ITEM_EMPTY = 19, KV_FULL = 23,
-                       KV_EMPTY = KV_FULL + kSlots, kNumBars = KV_EMPTY + kSlots;
+                       O_FREE = 12, DRAIN = 14, ITEM_FULL = 15, ITEM_EMPTY = 19,
+                       // of the K and V of a tile, by the tile's parity
+                       K_FULL = 23, K_EMPTY = 25, V_FULL = 27, V_EMPTY = 29, kNumBars = 31;
   static constexpr int kOffInvL = kOffBars + ((kNumBars * 8 + 15) / 16) * 16;
   static constexpr int kOffItems = kOffInvL + kStages * kBM * 4;
   static constexpr int kOffTmemSlot = kOffItems + kItemRing * 4;
@@ -85,10 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(L::ITEM_FULL + i), 1);
       mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers);
     }
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(bar(L::KV_FULL + i), 1);
-      mbar_init(bar(L::KV_EMPTY + i), 1);
-    }
+    for (int i = L::K_FULL; i < L::kNumBars; ++i) mbar_init(bar(i), 1);
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -236,38 +235,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS[2] = {tmem, tmem + kBN};
     const uint32_t tO[2] = {tmem + L::kTmemO, tmem + L::kTmemO + D};
     bool issued = false;
-    auto slot_of = [&](uint32_t fill) { return static_cast<int>(fill % L::kSlots); };
-    auto full = [&](uint32_t fill) {
-      return wait_bar_warp<kSleepMmaNs>(bar(L::KV_FULL + slot_of(fill)), (fill / L::kSlots) & 1u, ctl);
-    };
-    auto at = [&](uint32_t fill) { return sRing + static_cast<uint32_t>(slot_of(fill) * L::kChunk); };
+    // the chunk of fill `fill` as an operand
+    auto at = [&](uint32_t fill) { return sRing + (fill % L::kSlots) * L::kChunk; };
+    uint32_t k_seen = 0, v_seen = 0;  // tiles whose K and V were waited for
+    auto by_tile = [&](int first, uint32_t tile) { return bar(first + static_cast<int>(tile & 1u)); };
     // QK_s of tile `tile` (counted over the CTA's items); stage 1 is its last user
     auto qk = [&](int s, uint32_t tile, bool last_of_stage) -> bool {
-#pragma unroll
-      for (uint32_t c = 0; c < 3; ++c) {
-        const uint32_t fill = L::kPerTile * tile + c;
-        if (!full(fill)) return false;
+      if (tile >= k_seen) {
+        if (!wait_bar_warp<kSleepMmaNs>(by_tile(L::K_FULL, tile), (tile >> 1) & 1u, ctl)) return false;
+        k_seen = tile + 1;
         tc_fence_after();
-        umma_f16_ss_k64(tS[s], smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes) + c * L::kChunk, 16, 1024),
-                        smem_desc_sw128(at(fill), 16, 1024), kIdescQK, c > 0 ? 1u : 0u);
-        issued = true;
-        if (s == 1) umma_commit(bar(L::KV_EMPTY + slot_of(fill)));
       }
+      const uint32_t fill = L::kPerTile * tile;
+      umma_f16_ss_3k64(tS[s], smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes), 16, 1024),
+                       smem_desc_sw128(at(fill), 16, 1024), smem_desc_sw128(at(fill + 1), 16, 1024),
+                       smem_desc_sw128(at(fill + 2), 16, 1024), kIdescQK);
+      issued = true;
       umma_commit(bar(L::S_FULL + s));
+      if (s == 1) umma_commit(by_tile(L::K_EMPTY, tile));
       if (last_of_stage) umma_commit(bar(L::Q_EMPTY + s));
       return true;
     };
-    auto pv = [&](int s, uint32_t tile, bool acc) -> bool {
-#pragma unroll
-      for (uint32_t h = 0; h < 2; ++h) {
-        const uint32_t fill = L::kPerTile * tile + 3 + h;
-        if (!full(fill)) return false;
-        tc_fence_after();
-        umma_f16_ts_k64(tO[s], tS[s] + h * 32, smem_desc_sw128(at(fill), L::kChunk / 2, 1024), kIdescPV,
-                        acc || h > 0 ? 1u : 0u);
-        if (s == 1) umma_commit(bar(L::KV_EMPTY + slot_of(fill)));
-      }
+    // PV_s, once P_s is ready
+    auto pv = [&](int s, uint32_t tile, uint32_t n, bool acc) -> bool {
+      // both probed together: usually both are complete
+      bool rdy = mbar_try_wait(bar(L::PV_READY + s), n & 1u);
+      if (tile >= v_seen) rdy &= mbar_try_wait(by_tile(L::V_FULL, tile), (tile >> 1) & 1u);
+      if (!__all_sync(0xffffffffu, rdy) &&
+          (!wait_bar_warp<kSleepMmaNs>(by_tile(L::V_FULL, tile), (tile >> 1) & 1u, ctl) ||
+           !wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + s), n & 1u, ctl)))
+        return false;
+      v_seen = tile + 1;
+      tc_fence_after();
+      const uint32_t fill = L::kPerTile * tile + 3;
+      umma_f16_ts_2k64(tO[s], tS[s], smem_desc_sw128(at(fill), L::kChunk / 2, 1024),
+                       smem_desc_sw128(at(fill + 1), L::kChunk / 2, 1024), kIdescPV, acc ? 1u : 0u);
       umma_commit(bar(L::O_READY + s));
+      if (s == 1) umma_commit(by_tile(L::V_EMPTY, tile));
       return true;
     };
     auto q_full = [&](int s, uint32_t kq) {
@@ -310,12 +314,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
           const int nT = s == 0 ? cur.nT0 : cur.nT1;
           if (ok && j < nT) {
-            ok = wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + s), n_pv[s] & 1u, ctl);
-            ++n_pv[s];
-            if (ok && j == 0 && n_o[s] > 0)
+            if (j == 0 && n_o[s] > 0)
               ok = wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + s), (n_o[s] - 1) & 1u, ctl);
-            tc_fence_after();
-            ok = ok && pv(s, tile, j > 0);
+            ok = ok && pv(s, tile, n_pv[s]++, j > 0);
           }
           if (ok && !last && j + 1 < nT) ok = qk(s, tile + 1, j + 2 == nT);
           if (ok && last && has_next) ok = begin(s, nxt, kq + 1, tileN);
@@ -351,15 +352,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq[s];
         return true;
       };
-      // the next chunk: of K (c = 0, 1 own, 2 shared), or of V (c = 3, 4)
+      // the next chunk: of K (c = 0, 1 own, 2 shared), or of V (c = 3, 4).  Its slot's
+      // last one was eight fills back; barriers of two tiles serve: K and V of tile i are
+      // done with before the first chunk of those of i + 2 finds its slot free.
       auto load = [&](const ItemT<kSplit>& it, int c, int j) -> bool {
-        const int slot = static_cast<int>(fill % L::kSlots);
-        if (!wait_bar<kSleepProducerNs>(bar(L::KV_EMPTY + slot), ((fill / L::kSlots) & 1u) ^ 1u, ctl))
-          return false;
-        const uint32_t b = bar(L::KV_FULL + slot);
-        const uint32_t dst = sRing + static_cast<uint32_t>(slot * L::kChunk);
+        if (fill >= L::kSlots) {
+          const uint32_t was = fill - L::kSlots, tile = was / L::kPerTile;
+          const int empty = (was - tile * L::kPerTile < 3 ? L::K_EMPTY : L::V_EMPTY) + static_cast<int>(tile & 1u);
+          if (!wait_bar<kSleepProducerNs>(bar(empty), (tile >> 1) & 1u, ctl)) return false;
+        }
+        const uint32_t tile = fill / L::kPerTile;
+        const uint32_t b = bar((c < 3 ? L::K_FULL : L::V_FULL) + static_cast<int>(tile & 1u));
+        const uint32_t dst = sRing + (fill % L::kSlots) * L::kChunk;
         const int key = (it.t0 + j) * kBN;
-        mbar_arrive_expect_tx(b, L::kChunk);
+        if (c == 0) mbar_arrive_expect_tx(b, 3 * L::kChunk);
+        if (c == 3) mbar_arrive_expect_tx(b, 2 * L::kChunk);
         if (c == 2) {
           tma_load_3d(dst, &tmR, b, 0, key, it.bh / ep.H);
         } else if (c < 2) {
@@ -403,9 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int s = 0; s < 2; ++s)
         if (nq[s] > 0) wait_drain(bar(L::Q_FULL + s), (nq[s] - 1) & 1u, p.timeout_ns);
-#pragma unroll 1
-      for (uint32_t i = fill > L::kSlots ? fill - L::kSlots : 0u; i < fill; ++i)
-        wait_drain(bar(L::KV_FULL + static_cast<int>(i % L::kSlots)), (i / L::kSlots) & 1u, p.timeout_ns);
+      // (an abort may have left a tile's last chunks unsent: the waits are bounded)
+      const uint32_t tiles = (fill + L::kPerTile - 1) / L::kPerTile;
+      for (uint32_t i = tiles > 2 ? tiles - 2 : 0u; i < tiles; ++i) {
+        wait_drain(bar(L::K_FULL + static_cast<int>(i & 1u)), (i >> 1) & 1u, p.timeout_ns);
+        if (fill > L::kPerTile * i + 3)
+          wait_drain(bar(L::V_FULL + static_cast<int>(i & 1u)), (i >> 1) & 1u, p.timeout_ns);
+      }
     }
     __syncwarp();
   }

@@ -23,7 +23,7 @@
 namespace fa {
 
 constexpr int kPagedCopyThreads = 256;
-constexpr int kPagedMaxTokenShift = 3;
+constexpr int kPagedMaxTokenShift = 4;
 constexpr int kPagedAtOnce = 4;  // tasks of a thread whose loads go out together
 constexpr int kPagedMaxPairs = 64;
 
@@ -90,7 +90,7 @@ __device__ __forceinline__ long long paged_slot(const P& p, int b, uint32_t pos)
 }
 
 template <bool kLat, bool BF16, bool kPairs>
-__global__ void __launch_bounds__(kPagedCopyThreads, 3)
+__global__ void __launch_bounds__(kPagedCopyThreads, kLat ? 4 : 3)
     fa_paged_write_kernel(const PagedWriteParams p) {
   __shared__ float2 units[kPagedMaxPairs << kPagedMaxTokenShift];  // [token][pair]
   grid_dependency_wait();

@@ -363,25 +363,73 @@ __device__ __forceinline__ void umma_f16_ts_k128(uint32_t d_tmem, uint32_t a_tme
       : "memory");
 }
 
-// Four K=16 steps of D (+)= A * B for a K = 64 contraction: A (128 rows x 64 K of
-// 16-bit pairs) in tensor memory, 8 columns per step; B as above.
-__device__ __forceinline__ void umma_f16_ts_k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                uint32_t idesc, uint32_t accumulate) {
+// Eight K=16 steps of D (+)= A * B for a K = 128 contraction: A (128 rows x 128 K of
+// 16-bit pairs) in tensor memory; B's first 64 K rows at b0, the others at b1, MN-major
+// as above.
+__device__ __forceinline__ void umma_f16_ts_2k64(uint32_t d_tmem, uint32_t a_tmem, uint64_t b0,
+                                                 uint64_t b1, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e, t;\n\t"
-      ".reg .b32 a1, a2, a3;\n\t"
-      ".reg .b64 b1, b2, b3;\n\t"
+      ".reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+      ".reg .b64 b1, b2, b3, b5, b6, b7;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
       "setp.eq.b32 t, 0, 0;\n\t"
       "add.s32 a1, %1, 8;\n\t  add.s64 b1, %2, 128;\n\t"
       "add.s32 a2, %1, 16;\n\t add.s64 b2, %2, 256;\n\t"
       "add.s32 a3, %1, 24;\n\t add.s64 b3, %2, 384;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "add.s32 a4, %1, 32;\n\t"
+      "add.s32 a5, %1, 40;\n\t add.s64 b5, %3, 128;\n\t"
+      "add.s32 a6, %1, 48;\n\t add.s64 b6, %3, 256;\n\t"
+      "add.s32 a7, %1, 56;\n\t add.s64 b7, %3, 384;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %3, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %4, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %4, t;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b0), "l"(b1), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Twelve K=16 steps of D = A * B for a K = 192 contraction, both operands K-major,
+// 128-byte swizzled, in boxes of 64 columns: A's three follow one another (16 KB
+// apart), B's lie where b0, b1 and b2 say.
+__device__ __forceinline__ void umma_f16_ss_3k64(uint32_t d_tmem, uint64_t a_desc, uint64_t b0,
+                                                 uint64_t b1, uint64_t b2, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred f, e, t;\n\t"
+      ".reg .b64 a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11;\n\t"
+      ".reg .b64 b1, b2, b3, b5, b6, b7, b9, b10, b11;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, 0, 0;\n\t"
+      "setp.eq.b32 t, 0, 0;\n\t"
+      "add.s64 a1, %1, 2;\n\t add.s64 b1, %2, 2;\n\t"
+      "add.s64 a2, %1, 4;\n\t add.s64 b2, %2, 4;\n\t"
+      "add.s64 a3, %1, 6;\n\t add.s64 b3, %2, 6;\n\t"
+      "add.s64 a4, %1, 1024;\n\t"
+      "add.s64 a5, %1, 1026;\n\t add.s64 b5, %3, 2;\n\t"
+      "add.s64 a6, %1, 1028;\n\t add.s64 b6, %3, 4;\n\t"
+      "add.s64 a7, %1, 1030;\n\t add.s64 b7, %3, 6;\n\t"
+      "add.s64 a8, %1, 2048;\n\t"
+      "add.s64 a9, %1, 2050;\n\t add.s64 b9, %4, 2;\n\t"
+      "add.s64 a10, %1, 2052;\n\t add.s64 b10, %4, 4;\n\t"
+      "add.s64 a11, %1, 2054;\n\t add.s64 b11, %4, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, f;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, %3, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a8, %4, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a9, b9, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a10, b10, %5, t;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a11, b11, %5, t;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b0), "l"(b1), "l"(b2), "r"(idesc)
       : "memory");
 }
 
