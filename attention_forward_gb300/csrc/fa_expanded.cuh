@@ -237,15 +237,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool issued = false;
     // the chunk of fill `fill` as an operand
     auto at = [&](uint32_t fill) { return sRing + (fill % L::kSlots) * L::kChunk; };
-    uint32_t k_seen = 0, v_seen = 0;  // tiles whose K and V were waited for
     auto by_tile = [&](int first, uint32_t tile) { return bar(first + static_cast<int>(tile & 1u)); };
+    // A wait costs this warp over 100 cycles even when it is over, and the tensor core
+    // holds little more work than that: each is asked for ahead of the products before
+    // it, and waited for only where the answer was no.
+    auto ask = [&](uint32_t b, uint32_t parity) { return mbar_test_wait(b, parity & 1u); };
+    auto wait = [&](bool asked, uint32_t b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, asked) || wait_bar_warp<kSleepMmaNs>(b, parity & 1u, ctl);
+    };
     // QK_s of tile `tile` (counted over the CTA's items); stage 1 is its last user
-    auto qk = [&](int s, uint32_t tile, bool last_of_stage) -> bool {
-      if (tile >= k_seen) {
-        if (!wait_bar_warp<kSleepMmaNs>(by_tile(L::K_FULL, tile), (tile >> 1) & 1u, ctl)) return false;
-        k_seen = tile + 1;
-        tc_fence_after();
-      }
+    auto qk = [&](int s, uint32_t tile, bool last_of_stage) {
+      tc_fence_after();
       const uint32_t fill = L::kPerTile * tile;
       umma_f16_ss_3k64(tS[s], smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes), 16, 1024),
                        smem_desc_sw128(at(fill), 16, 1024), smem_desc_sw128(at(fill + 1), 16, 1024),
@@ -254,82 +256,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(bar(L::S_FULL + s));
       if (s == 1) umma_commit(by_tile(L::K_EMPTY, tile));
       if (last_of_stage) umma_commit(bar(L::Q_EMPTY + s));
-      return true;
     };
-    // PV_s, once P_s is ready
-    auto pv = [&](int s, uint32_t tile, uint32_t n, bool acc) -> bool {
-      // both probed together: usually both are complete
-      bool rdy = mbar_try_wait(bar(L::PV_READY + s), n & 1u);
-      if (tile >= v_seen) rdy &= mbar_try_wait(by_tile(L::V_FULL, tile), (tile >> 1) & 1u);
-      if (!__all_sync(0xffffffffu, rdy) &&
-          (!wait_bar_warp<kSleepMmaNs>(by_tile(L::V_FULL, tile), (tile >> 1) & 1u, ctl) ||
-           !wait_bar_warp<kSleepMmaNs>(bar(L::PV_READY + s), n & 1u, ctl)))
-        return false;
-      v_seen = tile + 1;
+    auto pv = [&](int s, uint32_t tile, bool acc) {
       tc_fence_after();
       const uint32_t fill = L::kPerTile * tile + 3;
       umma_f16_ts_2k64(tO[s], tS[s], smem_desc_sw128(at(fill), L::kChunk / 2, 1024),
                        smem_desc_sw128(at(fill + 1), L::kChunk / 2, 1024), kIdescPV, acc ? 1u : 0u);
       umma_commit(bar(L::O_READY + s));
       if (s == 1) umma_commit(by_tile(L::V_EMPTY, tile));
-      return true;
     };
-    auto q_full = [&](int s, uint32_t kq) {
-      return wait_bar_warp<kSleepMmaNs>(bar(L::Q_FULL + s), kq & 1u, ctl);
-    };
-    // an item's first scores of stage s
-    auto begin = [&](int s, const ItemT<kSplit>& it, uint32_t kq, uint32_t tile) -> bool {
-      if (!q_full(s, kq)) return false;
-      const int nT = s == 0 ? it.nT0 : it.nT1;
-      if (nT > 0) return qk(s, tile, nT == 1);
-      umma_commit(bar(L::Q_EMPTY + s));
-      return true;
-    };
-    uint32_t n_pv[2] = {0u, 0u};  // PV_s issued so far (PV_READY phase)
-    uint32_t n_o[2] = {0u, 0u};   // items so far with a PV_s (O_FREE phase)
-    uint32_t kq = 0, tile0 = 0;   // items begun (Q_FULL phase); the item's first tile
+    uint32_t n_pv0 = 0, n_pv1 = 0;  // PV_s issued so far (PV_READY phase)
+    uint32_t n_o0 = 0, n_o1 = 0;    // items so far with a PV_s (O_FREE phase)
+    uint32_t kq = 0, tile = 0;      // items begun (Q_FULL phase); the next tile with a PV
     bool ok = true;
-    const int first = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), 0, ctl, ok);
-    ItemT<kSplit> cur = first >= 0 ? get_item<kSplit>(p, first) : ItemT<kSplit>{0, 0, 0, 0};
-    ok = ok && first >= 0 && begin(0, cur, 0, 0) && begin(1, cur, 0, 0);
+    ItemT<kSplit> cur{0, 0, 0, 0}, nxt{0, 0, 0, 0};
+    bool has_next = false;
+    // the item after `kq`, if there is one
+    auto take_next = [&](uint32_t k) {
+      const int idx = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
+      has_next = ok && idx >= 0;
+      if (has_next) nxt = get_item<kSplit>(p, idx);
+    };
+    // an item's first scores, where no tile before issued them
+    auto begin = [&]() {
+      const bool some = nxt.nT1 > 0;
+      ok = wait(false, bar(L::Q_FULL), kq) && wait(false, bar(L::Q_FULL + 1), kq) &&
+           (!some || wait(false, by_tile(L::K_FULL, tile), tile >> 1));
+      if (!ok) return;
+      if (nxt.nT0 > 0) qk(0, tile, nxt.nT0 == 1); else umma_commit(bar(L::Q_EMPTY));
+      if (some) qk(1, tile, nxt.nT1 == 1); else umma_commit(bar(L::Q_EMPTY + 1));
+    };
+    take_next(0);
+    if (has_next) begin();
 #pragma unroll 1
-    while (ok) {
-      bool taken = false, has_next = false;
-      ItemT<kSplit> nxt{0, 0, 0, 0};
-      auto take_next = [&]() {
-        if (taken) return;
-        taken = true;
-        const int nidx = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), kq + 1,
-                                                ctl, ok);
-        has_next = ok && nidx >= 0;
-        if (has_next) nxt = get_item<kSplit>(p, nidx);
-      };
-      const uint32_t tileN = tile0 + static_cast<uint32_t>(cur.nT1);  // the next item's first
-#pragma unroll 1
-      for (int j = 0; ok && j < cur.nT1; ++j) {
-        const bool last = j + 1 == cur.nT1;
-        if (last) take_next();
-        const uint32_t tile = tile0 + static_cast<uint32_t>(j);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int nT = s == 0 ? cur.nT0 : cur.nT1;
-          if (ok && j < nT) {
-            if (j == 0 && n_o[s] > 0)
-              ok = wait_bar_warp<kSleepMmaNs>(bar(L::O_FREE + s), (n_o[s] - 1) & 1u, ctl);
-            ok = ok && pv(s, tile, n_pv[s]++, j > 0);
-          }
-          if (ok && !last && j + 1 < nT) ok = qk(s, tile + 1, j + 2 == nT);
-          if (ok && last && has_next) ok = begin(s, nxt, kq + 1, tileN);
-        }
-      }
-      if (ok) take_next();  // an item without key tiles
-      if (!ok || !has_next) break;
-      if (cur.nT0 > 0) ++n_o[0];
-      if (cur.nT1 > 0) ++n_o[1];
-      if (cur.nT1 == 0) ok = begin(0, nxt, kq + 1, tileN) && begin(1, nxt, kq + 1, tileN);
-      ++kq;
+    while (ok && has_next) {
       cur = nxt;
-      tile0 = tileN;
+      has_next = false;
+      bool got_pv0 = false, got_v = false;  // asked ahead: P_0 and V of the next tile
+#pragma unroll 1
+      for (int j = 0; ok && j < cur.nT1; ++j, ++tile) {
+        const bool last = j + 1 == cur.nT1;
+        if (last) take_next(kq + 1);
+        // the scores that come after PV_s(j): of this item, or the next one's first
+        const int left0 = last ? (has_next ? nxt.nT0 : 0) : cur.nT0 - j - 1;
+        const int left1 = last ? (has_next ? nxt.nT1 : 0) : cur.nT1 - j - 1;
+        ok = ok && wait(got_v, by_tile(L::V_FULL, tile), tile >> 1);
+        bool got_k = false, got_pv1 = false;
+        if (ok && j < cur.nT0) {
+          ok = wait(got_pv0, bar(L::PV_READY), n_pv0++) &&
+               (j > 0 || n_o0 == 0 || wait(false, bar(L::O_FREE), n_o0 - 1));
+          if (left1 > 0) got_k = ask(by_tile(L::K_FULL, tile + 1), (tile + 1) >> 1);
+          if (ok) pv(0, tile, j > 0);
+        }
+        if (ok && last && has_next)
+          ok = wait(false, bar(L::Q_FULL), kq + 1) && wait(false, bar(L::Q_FULL + 1), kq + 1);
+        if (ok && left1 > 0) ok = wait(got_k, by_tile(L::K_FULL, tile + 1), (tile + 1) >> 1);
+        got_pv1 = ask(bar(L::PV_READY + 1), n_pv1);
+        if (ok && left0 > 0) qk(0, tile + 1, left0 == 1);
+        else if (ok && last && has_next) umma_commit(bar(L::Q_EMPTY));
+        ok = ok && wait(got_pv1, bar(L::PV_READY + 1), n_pv1++) &&
+             (j > 0 || n_o1 == 0 || wait(false, bar(L::O_FREE + 1), n_o1 - 1));
+        if (ok) pv(1, tile, j > 0);
+        got_pv0 = ask(bar(L::PV_READY), n_pv0);
+        got_v = left1 > 0 && ask(by_tile(L::V_FULL, tile + 1), (tile + 1) >> 1);
+        if (ok && left1 > 0) qk(1, tile + 1, left1 == 1);
+        else if (ok && last && has_next) umma_commit(bar(L::Q_EMPTY + 1));
+      }
+      if (!ok) break;
+      if (cur.nT1 == 0) take_next(kq + 1);  // an item without key tiles
+      if (!ok || !has_next) break;
+      if (cur.nT0 > 0) ++n_o0;
+      if (cur.nT1 > 0) ++n_o1;
+      ++kq;
+      if (cur.nT1 == 0) begin();
     }
     if (issued) {  // every MMA issued so far completes before TMEM is freed
       umma_commit(bar(L::DRAIN));
