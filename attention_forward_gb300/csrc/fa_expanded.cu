@@ -13,8 +13,8 @@ namespace fa {
 namespace {
 
 template <bool BF16, bool kSplit>
-cudaError_t launch(const CUtensorMap& q, const CUtensorMap& kv, const CUtensorMap& r,
-                   const ExpandedParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                   const CUtensorMap& r, const ExpandedParams& p, int grid, cudaStream_t stream) {
   {  // the shared-memory opt-in, and the registers that the kernel's split is made
      // for, once per device
     static std::mutex mu;
@@ -46,7 +46,7 @@ cudaError_t launch(const CUtensorMap& q, const CUtensorMap& kv, const CUtensorMa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fa_expanded_kernel<BF16, kSplit>, q, kv, r, p);
+  return cudaLaunchKernelEx(&cfg, fa_expanded_kernel<BF16, kSplit>, q, k, v, r, p);
 }
 
 }  // namespace
@@ -156,17 +156,18 @@ fa_status_t fa_fwd_expanded(const void* q, const void* kv, const void* k_rope, v
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
   }
   const bool bf16 = dtype == FA_BF16;
-  CUtensorMap tq, tkv, tr;
+  CUtensorMap tq, tk, tv, tr;
   if ((st = fa::encode_rows(&tq, q, fa::ExpandedLayout::kDq, Sq, B * H, fa::kBM, bf16)) != FA_OK) return st;
-  if ((st = fa::encode_rows(&tkv, kv, 2 * fa::kNope, Skv, B * H, 64, bf16)) != FA_OK) return st;
+  if ((st = fa::encode_rows(&tk, kv, 2 * fa::kNope, Skv, B * H, fa::kBN, bf16)) != FA_OK) return st;
+  if ((st = fa::encode_rows(&tv, kv, 2 * fa::kNope, Skv, B * H, 64, bf16)) != FA_OK) return st;
   if ((st = fa::encode_rows(&tr, k_rope, fa::kLatentRope, Skv, B, fa::kBN, bf16)) != FA_OK) return st;
   p.sched = fa::take_sched_slot(env);
   const int grid = static_cast<int>(std::min<long long>(items, env.sm_count > 0 ? env.sm_count : 1));
   const cudaError_t e =
-      plan.n_splits > 1 ? (bf16 ? fa::launch<true, true>(tq, tkv, tr, ep, grid, s)
-                                : fa::launch<false, true>(tq, tkv, tr, ep, grid, s))
-                        : (bf16 ? fa::launch<true, false>(tq, tkv, tr, ep, grid, s)
-                                : fa::launch<false, false>(tq, tkv, tr, ep, grid, s));
+      plan.n_splits > 1 ? (bf16 ? fa::launch<true, true>(tq, tk, tv, tr, ep, grid, s)
+                                : fa::launch<false, true>(tq, tk, tv, tr, ep, grid, s))
+                        : (bf16 ? fa::launch<true, false>(tq, tk, tv, tr, ep, grid, s)
+                                : fa::launch<false, false>(tq, tk, tv, tr, ep, grid, s));
   if (e != cudaSuccess) return FA_ERR_CUDA;
   if (plan.n_splits > 1) {
     const fa::MergeParams m{p.part_o, p.part_lse, o, lse, static_cast<long long>(rows), plan.n_splits};

@@ -15,7 +15,9 @@
 //   K chunk c (3): 128 keys x 64 channels;  V chunk h (2): 64 keys x 128 channels
 // The ring runs 1.6 tiles ahead.  A tile's K, and its V, have one pair of barriers each:
 // with a pair for every chunk, the issuing warp's waits and commits took 4430 cycles a
-// tile of two stages, whose products take 2560.  O goes from
+// tile of two stages, whose products take 2560.  Keys, values and queries are sent for
+// by warps 13, 14 and 15: by one, beside the softmax warps of its SM sub-partition, a
+// chunk took 860 cycles (4200 a tile).  O goes from
 // registers to global memory (its staging's 32 KB are the ring's).
 #pragma once
 #include "fa_paged.h"
@@ -55,7 +57,8 @@ struct ExpandedLayout {
 template <bool BF16, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_expanded_kernel(const __grid_constant__ CUtensorMap tmQ,
-                       const __grid_constant__ CUtensorMap tmKV,
+                       const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ CUtensorMap tmR, const ExpandedParams ep) {
   using L = ExpandedLayout;
   constexpr int D = kNope;
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(L::DRAIN), 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(bar(L::ITEM_FULL + i), 1);
-      mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers);
+      mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers + 2);  // and the other producers
     }
     for (int i = L::K_FULL; i < L::kNumBars; ++i) mbar_init(bar(i), 1);
     *abort_flag = 0u;
@@ -97,7 +100,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 13 && lane == 0) {
     tma_prefetch_desc(&tmQ);
-    tma_prefetch_desc(&tmKV);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmR);
   }
   tc_fence_before();
@@ -336,49 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else if (warp == 13) {
-    // ============================== TMA producer =============================
+    // ================= scheduler, and TMA producer of the keys ================
+    // A K chunk's slot was that of a chunk eight fills back: c 0 the last of K(T - 2), c 1
+    // and 2 those of V(T - 2); V's were the first two of K(T - 1).  Barriers of two tiles
+    // serve: K and V of a tile are done with before those of the next but one arrive.
     if (lane == 0) {
-      uint32_t fill = 0;
-      uint32_t nq[2] = {0u, 0u};  // Q loads issued per stage
+      uint32_t tile = 0;
       bool ok = true;
-      auto load_q = [&](const ItemT<kSplit>& it, int s) -> bool {
-        if (nq[s] > 0 && !wait_bar<kSleepProducerNs>(bar(L::Q_EMPTY + s), (nq[s] - 1) & 1u, ctl)) return false;
-        mbar_arrive_expect_tx(bar(L::Q_FULL + s), L::kQBytes);
-#pragma unroll
-        for (int c = 0; c < 3; ++c)
-          tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + c * L::kChunk), &tmQ,
-                      bar(L::Q_FULL + s), c * 64, it.row0 + s * kBM, it.bh);
-        ++nq[s];
-        return true;
-      };
-      // the next chunk: of K (c = 0, 1 own, 2 shared), or of V (c = 3, 4).  Its slot's
-      // last one was eight fills back; barriers of two tiles serve: K and V of tile i are
-      // done with before the first chunk of those of i + 2 finds its slot free.
-      auto load = [&](const ItemT<kSplit>& it, int c, int j) -> bool {
-        if (fill >= L::kSlots) {
-          const uint32_t was = fill - L::kSlots, tile = was / L::kPerTile;
-          const int empty = (was - tile * L::kPerTile < 3 ? L::K_EMPTY : L::V_EMPTY) + static_cast<int>(tile & 1u);
-          if (!wait_bar<kSleepProducerNs>(bar(empty), (tile >> 1) & 1u, ctl)) return false;
-        }
-        const uint32_t tile = fill / L::kPerTile;
-        const uint32_t b = bar((c < 3 ? L::K_FULL : L::V_FULL) + static_cast<int>(tile & 1u));
-        const uint32_t dst = sRing + (fill % L::kSlots) * L::kChunk;
-        const int key = (it.t0 + j) * kBN;
-        if (c == 0) mbar_arrive_expect_tx(b, 3 * L::kChunk);
-        if (c == 3) mbar_arrive_expect_tx(b, 2 * L::kChunk);
-        if (c == 2) {
-          tma_load_3d(dst, &tmR, b, 0, key, it.bh / ep.H);
-        } else if (c < 2) {
-          tma_load_3d(dst, &tmKV, b, c * 64, key, it.bh);
-          tma_load_3d(dst + L::kChunk / 2, &tmKV, b, c * 64, key + 64, it.bh);
-        } else {
-          const int k0 = key + (c - 3) * 64;
-          tma_load_3d(dst, &tmKV, b, kNope, k0, it.bh);
-          tma_load_3d(dst + L::kChunk / 2, &tmKV, b, kNope + 64, k0, it.bh);
-        }
-        ++fill;
-        return true;
-      };
       int idx = static_cast<int>(blockIdx.x);  // the grid never exceeds the items
 #pragma unroll 1
       for (uint32_t k = 0; ok; ++k) {
@@ -392,31 +360,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(L::ITEM_FULL + slot));
         if (idx < 0) break;
         const ItemT<kSplit> it = get_item<kSplit>(p, idx);
-        ok = load_q(it, 0);
+        const int batch = it.bh / ep.H;
+        int key = it.t0 * kBN;
 #pragma unroll 1
-        for (int j = 0; ok && j < it.nT1; ++j) {
-#pragma unroll 1
-          for (int c = 0; ok && c < L::kPerTile; ++c) {
-            if (j == 0 && c == 3) ok = load_q(it, 1);
-            if (ok) ok = load(it, c, j);
+        for (int j = 0; j < it.nT1; ++j, ++tile, key += kBN) {
+          const int odd = static_cast<int>(tile & 1u);
+          const uint32_t free_par = ((tile >> 1) & 1u) ^ 1u, full = bar(L::K_FULL + odd);
+          const uint32_t fill = L::kPerTile * tile;
+          if (tile >= 2 && !wait_bar<kSleepProducerNs>(bar(L::K_EMPTY + odd), free_par, ctl)) {
+            ok = false;
+            break;
           }
+          mbar_arrive_expect_tx(full, 3 * L::kChunk);
+          tma_load_3d(sRing + (fill % L::kSlots) * L::kChunk, &tmK, full, 0, key, it.bh);
+          if (tile >= 2 && !wait_bar<kSleepProducerNs>(bar(L::V_EMPTY + odd), free_par, ctl)) {
+            ok = false;
+            break;
+          }
+          tma_load_3d(sRing + ((fill + 1) % L::kSlots) * L::kChunk, &tmK, full, 64, key, it.bh);
+          tma_load_3d(sRing + ((fill + 2) % L::kSlots) * L::kChunk, &tmR, full, 0, key, batch);
         }
-        if (ok && it.nT1 == 0) ok = load_q(it, 1);
         idx = claim_item(p);
         if (idx < 0) grid_launch_dependents();  // the next grid may take the SMs
       }
-      // drain: every load issued lands before shared memory goes away
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-        if (nq[s] > 0) wait_drain(bar(L::Q_FULL + s), (nq[s] - 1) & 1u, p.timeout_ns);
-      // (an abort may have left a tile's last chunks unsent: the waits are bounded)
-      const uint32_t tiles = (fill + L::kPerTile - 1) / L::kPerTile;
-      for (uint32_t i = tiles > 2 ? tiles - 2 : 0u; i < tiles; ++i) {
+      // drain: every load issued lands before shared memory goes away (an abort may have
+      // left a tile's last chunks unsent: the waits are bounded)
+      for (uint32_t i = tile > 2 ? tile - 2 : 0u; i < tile + (ok ? 0u : 1u); ++i)
         wait_drain(bar(L::K_FULL + static_cast<int>(i & 1u)), (i >> 1) & 1u, p.timeout_ns);
-        if (fill > L::kPerTile * i + 3)
-          wait_drain(bar(L::V_FULL + static_cast<int>(i & 1u)), (i >> 1) & 1u, p.timeout_ns);
+    }
+    __syncwarp();
+  } else {
+    // ============ TMA producers of the values (warp 14) and of Q (15) =========
+    uint32_t tile = 0, items = 0;
+    bool ok = true;
+#pragma unroll 1
+    for (uint32_t k = 0; ok; ++k) {
+      const int idx = take_item<kSleepProducerNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
+      if (!ok || idx < 0) break;
+      const ItemT<kSplit> it = get_item<kSplit>(p, idx);
+      if (warp == 15) {
+#pragma unroll 1
+        for (int s = 0; ok && s < 2; ++s) {
+          ok = items == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::Q_EMPTY + s), (items - 1) & 1u, ctl);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(bar(L::Q_FULL + s), L::kQBytes);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + c * L::kChunk), &tmQ,
+                          bar(L::Q_FULL + s), c * 64, it.row0 + s * kBM, it.bh);
+          }
+          __syncwarp();
+        }
+        if (ok) ++items;
+      } else {
+        int key = it.t0 * kBN;
+#pragma unroll 1
+        for (int j = 0; ok && j < it.nT1; ++j, ++tile, key += kBN) {
+          const uint32_t before = tile - 1, fill = L::kPerTile * tile + 3;
+          ok = tile == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::K_EMPTY + static_cast<int>(before & 1u)),
+                                                            (before >> 1) & 1u, ctl);
+          if (!ok) break;
+          if (lane == 0) {
+            const uint32_t full = bar(L::V_FULL + static_cast<int>(tile & 1u));
+            mbar_arrive_expect_tx(full, 2 * L::kChunk);
+#pragma unroll
+            for (uint32_t h = 0; h < 2; ++h) {
+              const uint32_t dst = sRing + ((fill + h) % L::kSlots) * L::kChunk;
+              tma_load_3d(dst, &tmV, full, kNope, key + static_cast<int>(h) * 64, it.bh);
+              tma_load_3d(dst + L::kChunk / 2, &tmV, full, kNope + 64, key + static_cast<int>(h) * 64, it.bh);
+            }
+          }
+          __syncwarp();
+        }
       }
     }
+    // drain, as above
+    if (items > 0)
+      for (int s = 0; s < 2; ++s) wait_drain(bar(L::Q_FULL + s), (items - 1) & 1u, p.timeout_ns);
+    for (uint32_t i = tile > 2 ? tile - 2 : 0u; i < tile; ++i)
+      wait_drain(bar(L::V_FULL + static_cast<int>(i & 1u)), (i >> 1) & 1u, p.timeout_ns);
     __syncwarp();
   }
 
