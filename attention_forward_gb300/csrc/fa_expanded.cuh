@@ -15,9 +15,9 @@
 //   K chunk c (3): 128 keys x 64 channels;  V chunk h (2): 64 keys x 128 channels
 // The ring runs 1.6 tiles ahead.  A tile's K, and its V, have one pair of barriers each:
 // with a pair for every chunk, the issuing warp's waits and commits took 4430 cycles a
-// tile of two stages, whose products take 2560.  Keys, values and queries are sent for
-// by warps 13, 14 and 15: by one, beside the softmax warps of its SM sub-partition, a
-// chunk took 860 cycles (4200 a tile).  O goes from
+// tile of two stages, whose products take 2560.  Warps 12 and 13 issue a stage's products
+// each, warp 14 claims the items and sends for the keys, warp 15 for queries and values:
+// by one warp, a chunk took 860 cycles (4200 a tile).  O goes from
 // registers to global memory (its staging's 32 KB are the ring's).
 #pragma once
 #include "fa_paged.h"
@@ -41,9 +41,10 @@ struct ExpandedLayout {
   static constexpr int kOffBars = kOffRing + kSlots * kChunk;
   // mbarrier indices, as the prefill kernel's
   static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, PV_READY = 6, O_READY = 8, ML_FULL = 10,
-                       O_FREE = 12, DRAIN = 14, ITEM_FULL = 15, ITEM_EMPTY = 19,
+                       O_FREE = 12, ITEM_FULL = 15, ITEM_EMPTY = 19,
                        // of the K and V of a tile, by the tile's parity
-                       K_FULL = 23, K_EMPTY = 25, V_FULL = 27, V_EMPTY = 29, kNumBars = 31;
+                       K_FULL = 23, K_EMPTY = 25, V_FULL = 27, V_EMPTY = 29, DRAIN = 31,
+                       kNumBars = 33;
   static constexpr int kOffInvL = kOffBars + ((kNumBars * 8 + 15) / 16) * 16;
   static constexpr int kOffItems = kOffInvL + kStages * kBM * 4;
   static constexpr int kOffTmemSlot = kOffItems + kItemRing * 4;
@@ -85,12 +86,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(L::ML_FULL + s), 4);
       mbar_init(bar(L::O_FREE + s), 4);    // the 4 epilogue warps
     }
-    mbar_init(bar(L::DRAIN), 1);
     for (int i = 0; i < kItemRing; ++i) {
       mbar_init(bar(L::ITEM_FULL + i), 1);
-      mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers + 2);  // and the other producers
+      mbar_init(bar(L::ITEM_EMPTY + i), kItemTakers + 2);  // two that issue, two that load
     }
-    for (int i = L::K_FULL; i < L::kNumBars; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(L::K_FULL + i), 1);
+      mbar_init(bar(L::K_EMPTY + i), 2);  // both stages
+      mbar_init(bar(L::V_FULL + i), 1);
+      mbar_init(bar(L::V_EMPTY + i), 2);
+      mbar_init(bar(L::DRAIN + i), 1);
+    }
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -230,116 +236,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 12) {
-    // ============================== MMA issuer ==============================
-    // per key tile PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1); at an item's last tile the
-    // next item's QK_s(0) take the place of QK_s(j+1)
+  } else if (warp < 14) {
+    // ======================= MMA issuers, a warp a stage =====================
+    // per key tile PV_s(j - 1), QK_s(j): in this order, for the scores overwrite P.  (By
+    // one warp for both stages, its waits and commits left the tensor core idle for 1400
+    // of a tile's 4000 cycles.)
     constexpr uint32_t kIdescQK = idesc_f16(BF16, false, false, kBM, kBN);
     constexpr uint32_t kIdescPV = idesc_f16(BF16, false, true, kBM, D);
-    const uint32_t tS[2] = {tmem, tmem + kBN};
-    const uint32_t tO[2] = {tmem + L::kTmemO, tmem + L::kTmemO + D};
-    bool issued = false;
+    const int s = warp - 12;
+    const uint32_t tS = tmem + static_cast<uint32_t>(s * kBN);
+    const uint32_t tO = tmem + static_cast<uint32_t>(L::kTmemO + s * D);
+    const uint64_t q = smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes), 16, 1024);
     // the chunk of fill `fill` as an operand
     auto at = [&](uint32_t fill) { return sRing + (fill % L::kSlots) * L::kChunk; };
-    auto by_tile = [&](int first, uint32_t tile) { return bar(first + static_cast<int>(tile & 1u)); };
-    // A wait costs this warp over 100 cycles even when it is over, and the tensor core
-    // holds little more work than that: each is asked for ahead of the products before
-    // it, and waited for only where the answer was no.
-    auto ask = [&](uint32_t b, uint32_t parity) { return mbar_test_wait(b, parity & 1u); };
+    auto by_tile = [&](int first, uint32_t t) { return bar(first + static_cast<int>(t & 1u)); };
     auto wait = [&](bool asked, uint32_t b, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, asked) || wait_bar_warp<kSleepMmaNs>(b, parity & 1u, ctl);
     };
-    // QK_s of tile `tile` (counted over the CTA's items); stage 1 is its last user
-    auto qk = [&](int s, uint32_t tile, bool last_of_stage) {
-      tc_fence_after();
-      const uint32_t fill = L::kPerTile * tile;
-      umma_f16_ss_3k64(tS[s], smem_desc_sw128(sQ + static_cast<uint32_t>(s * L::kQBytes), 16, 1024),
-                       smem_desc_sw128(at(fill), 16, 1024), smem_desc_sw128(at(fill + 1), 16, 1024),
-                       smem_desc_sw128(at(fill + 2), 16, 1024), kIdescQK);
-      issued = true;
-      umma_commit(bar(L::S_FULL + s));
-      if (s == 1) umma_commit(by_tile(L::K_EMPTY, tile));
-      if (last_of_stage) umma_commit(bar(L::Q_EMPTY + s));
-    };
-    auto pv = [&](int s, uint32_t tile, bool acc) {
-      tc_fence_after();
-      const uint32_t fill = L::kPerTile * tile + 3;
-      umma_f16_ts_2k64(tO[s], tS[s], smem_desc_sw128(at(fill), L::kChunk / 2, 1024),
-                       smem_desc_sw128(at(fill + 1), L::kChunk / 2, 1024), kIdescPV, acc ? 1u : 0u);
-      umma_commit(bar(L::O_READY + s));
-      if (s == 1) umma_commit(by_tile(L::V_EMPTY, tile));
-    };
-    uint32_t n_pv0 = 0, n_pv1 = 0;  // PV_s issued so far (PV_READY phase)
-    uint32_t n_o0 = 0, n_o1 = 0;    // items so far with a PV_s (O_FREE phase)
-    uint32_t kq = 0, tile = 0;      // items begun (Q_FULL phase); the next tile with a PV
-    bool ok = true;
-    ItemT<kSplit> cur{0, 0, 0, 0}, nxt{0, 0, 0, 0};
-    bool has_next = false;
-    // the item after `kq`, if there is one
-    auto take_next = [&](uint32_t k) {
+    uint32_t n_pv = 0, n_o = 0;  // PV_s so far, and items with one (PV_READY, O_FREE phases)
+    uint32_t tile = 0;           // the item's first tile, counted over the CTA's items
+    bool ok = true, issued = false;
+#pragma unroll 1
+    for (uint32_t k = 0; ok; ++k) {
       const int idx = take_item<kSleepMmaNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
-      has_next = ok && idx >= 0;
-      if (has_next) nxt = get_item<kSplit>(p, idx);
-    };
-    // an item's first scores, where no tile before issued them
-    auto begin = [&]() {
-      const bool some = nxt.nT1 > 0;
-      ok = wait(false, bar(L::Q_FULL), kq) && wait(false, bar(L::Q_FULL + 1), kq) &&
-           (!some || wait(false, by_tile(L::K_FULL, tile), tile >> 1));
-      if (!ok) return;
-      if (nxt.nT0 > 0) qk(0, tile, nxt.nT0 == 1); else umma_commit(bar(L::Q_EMPTY));
-      if (some) qk(1, tile, nxt.nT1 == 1); else umma_commit(bar(L::Q_EMPTY + 1));
-    };
-    take_next(0);
-    if (has_next) begin();
+      if (!ok || idx < 0) break;
+      const ItemT<kSplit> it = get_item<kSplit>(p, idx);
+      const int n = s == 0 ? it.nT0 : it.nT1;
+      ok = wait(false, bar(L::Q_FULL + s), k);
+      if (ok && n == 0) umma_commit(bar(L::Q_EMPTY + s));
+      bool got_k = false;
 #pragma unroll 1
-    while (ok && has_next) {
-      cur = nxt;
-      has_next = false;
-      bool got_pv0 = false, got_v = false;  // asked ahead: P_0 and V of the next tile
-#pragma unroll 1
-      for (int j = 0; ok && j < cur.nT1; ++j, ++tile) {
-        const bool last = j + 1 == cur.nT1;
-        if (last) take_next(kq + 1);
-        // the scores that come after PV_s(j): of this item, or the next one's first
-        const int left0 = last ? (has_next ? nxt.nT0 : 0) : cur.nT0 - j - 1;
-        const int left1 = last ? (has_next ? nxt.nT1 : 0) : cur.nT1 - j - 1;
-        ok = ok && wait(got_v, by_tile(L::V_FULL, tile), tile >> 1);
-        bool got_k = false, got_pv1 = false;
-        if (ok && j < cur.nT0) {
-          ok = wait(got_pv0, bar(L::PV_READY), n_pv0++) &&
-               (j > 0 || n_o0 == 0 || wait(false, bar(L::O_FREE), n_o0 - 1));
-          if (left1 > 0) got_k = ask(by_tile(L::K_FULL, tile + 1), (tile + 1) >> 1);
-          if (ok) pv(0, tile, j > 0);
+      for (int j = 0; ok && j <= n && n > 0; ++j) {
+        const uint32_t t = tile + static_cast<uint32_t>(j);
+        if (j > 0) {
+          // both probed together: usually both are there
+          bool rdy = mbar_try_wait(by_tile(L::V_FULL, t - 1), ((t - 1) >> 1) & 1u);
+          rdy &= mbar_try_wait(bar(L::PV_READY + s), n_pv & 1u);
+          ok = __all_sync(0xffffffffu, rdy) ||
+               (wait(false, by_tile(L::V_FULL, t - 1), (t - 1) >> 1) &&
+                wait(false, bar(L::PV_READY + s), n_pv));
+          ++n_pv;
+          if (ok && j == 1 && n_o > 0) ok = wait(false, bar(L::O_FREE + s), n_o - 1);
+          if (!ok) break;
+          got_k = j < n && mbar_test_wait(by_tile(L::K_FULL, t), (t >> 1) & 1u);
+          tc_fence_after();
+          const uint32_t fill = L::kPerTile * (t - 1) + 3;
+          umma_f16_ts_2k64(tO, tS, smem_desc_sw128(at(fill), L::kChunk / 2, 1024),
+                           smem_desc_sw128(at(fill + 1), L::kChunk / 2, 1024), kIdescPV, j > 1 ? 1u : 0u);
+          umma_commit(by_tile(L::V_EMPTY, t - 1));
+          umma_commit(bar(L::O_READY + s));
         }
-        if (ok && last && has_next)
-          ok = wait(false, bar(L::Q_FULL), kq + 1) && wait(false, bar(L::Q_FULL + 1), kq + 1);
-        if (ok && left1 > 0) ok = wait(got_k, by_tile(L::K_FULL, tile + 1), (tile + 1) >> 1);
-        got_pv1 = ask(bar(L::PV_READY + 1), n_pv1);
-        if (ok && left0 > 0) qk(0, tile + 1, left0 == 1);
-        else if (ok && last && has_next) umma_commit(bar(L::Q_EMPTY));
-        ok = ok && wait(got_pv1, bar(L::PV_READY + 1), n_pv1++) &&
-             (j > 0 || n_o1 == 0 || wait(false, bar(L::O_FREE + 1), n_o1 - 1));
-        if (ok) pv(1, tile, j > 0);
-        got_pv0 = ask(bar(L::PV_READY), n_pv0);
-        got_v = left1 > 0 && ask(by_tile(L::V_FULL, tile + 1), (tile + 1) >> 1);
-        if (ok && left1 > 0) qk(1, tile + 1, left1 == 1);
-        else if (ok && last && has_next) umma_commit(bar(L::Q_EMPTY + 1));
+        if (j < n) {
+          ok = wait(got_k, by_tile(L::K_FULL, t), t >> 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t fill = L::kPerTile * t;
+          umma_f16_ss_3k64(tS, q, smem_desc_sw128(at(fill), 16, 1024), smem_desc_sw128(at(fill + 1), 16, 1024),
+                           smem_desc_sw128(at(fill + 2), 16, 1024), kIdescQK);
+          issued = true;
+          umma_commit(bar(L::S_FULL + s));
+          umma_commit(by_tile(L::K_EMPTY, t));
+          if (j + 1 == n) umma_commit(bar(L::Q_EMPTY + s));
+        }
       }
-      if (!ok) break;
-      if (cur.nT1 == 0) take_next(kq + 1);  // an item without key tiles
-      if (!ok || !has_next) break;
-      if (cur.nT0 > 0) ++n_o0;
-      if (cur.nT1 > 0) ++n_o1;
-      ++kq;
-      if (cur.nT1 == 0) begin();
+      if (n > 0) ++n_o;
+      // tiles that the other stage alone uses
+#pragma unroll 1
+      for (int j = n; ok && j < it.nT1; ++j) {
+        const uint32_t t = tile + static_cast<uint32_t>(j);
+        ok = wait(false, by_tile(L::K_FULL, t), t >> 1) && wait(false, by_tile(L::V_FULL, t), t >> 1);
+        if (ok && lane == 0) {
+          mbar_arrive(by_tile(L::K_EMPTY, t));
+          mbar_arrive(by_tile(L::V_EMPTY, t));
+        }
+        __syncwarp();
+      }
+      tile += static_cast<uint32_t>(it.nT1);
     }
     if (issued) {  // every MMA issued so far completes before TMEM is freed
-      umma_commit(bar(L::DRAIN));
-      wait_drain(bar(L::DRAIN), 0, p.timeout_ns);
+      umma_commit(bar(L::DRAIN + s));
+      wait_drain(bar(L::DRAIN + s), 0, p.timeout_ns);
     }
     __syncwarp();
-  } else if (warp == 13) {
+  } else if (warp == 14) {
     // ================= scheduler, and TMA producer of the keys ================
     // A K chunk's slot was that of a chunk eight fills back: c 0 the last of K(T - 2), c 1
     // and 2 those of V(T - 2); V's were the first two of K(T - 1).  Barriers of two tiles
@@ -390,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // ============ TMA producers of the values (warp 14) and of Q (15) =========
+    // ================ TMA producer of the queries and the values ==============
     uint32_t tile = 0, items = 0;
     bool ok = true;
 #pragma unroll 1
@@ -398,40 +377,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int idx = take_item<kSleepProducerNs>(item_ring, bar(L::ITEM_FULL), bar(L::ITEM_EMPTY), k, ctl, ok);
       if (!ok || idx < 0) break;
       const ItemT<kSplit> it = get_item<kSplit>(p, idx);
-      if (warp == 15) {
 #pragma unroll 1
-        for (int s = 0; ok && s < 2; ++s) {
-          ok = items == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::Q_EMPTY + s), (items - 1) & 1u, ctl);
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(bar(L::Q_FULL + s), L::kQBytes);
+      for (int s = 0; ok && s < 2; ++s) {
+        ok = items == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::Q_EMPTY + s), (items - 1) & 1u, ctl);
+        if (ok && lane == 0) {
+          mbar_arrive_expect_tx(bar(L::Q_FULL + s), L::kQBytes);
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + c * L::kChunk), &tmQ,
-                          bar(L::Q_FULL + s), c * 64, it.row0 + s * kBM, it.bh);
-          }
-          __syncwarp();
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d(sQ + static_cast<uint32_t>(s * L::kQBytes + c * L::kChunk), &tmQ,
+                        bar(L::Q_FULL + s), c * 64, it.row0 + s * kBM, it.bh);
         }
-        if (ok) ++items;
-      } else {
-        int key = it.t0 * kBN;
+        __syncwarp();
+      }
+      if (!ok) break;
+      ++items;
+      int key = it.t0 * kBN;
 #pragma unroll 1
-        for (int j = 0; ok && j < it.nT1; ++j, ++tile, key += kBN) {
-          const uint32_t before = tile - 1, fill = L::kPerTile * tile + 3;
-          ok = tile == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::K_EMPTY + static_cast<int>(before & 1u)),
-                                                            (before >> 1) & 1u, ctl);
-          if (!ok) break;
-          if (lane == 0) {
-            const uint32_t full = bar(L::V_FULL + static_cast<int>(tile & 1u));
-            mbar_arrive_expect_tx(full, 2 * L::kChunk);
+      for (int j = 0; j < it.nT1; ++j, ++tile, key += kBN) {
+        const uint32_t before = tile - 1, fill = L::kPerTile * tile + 3;
+        ok = tile == 0 || wait_bar_warp<kSleepProducerNs>(bar(L::K_EMPTY + static_cast<int>(before & 1u)),
+                                                          (before >> 1) & 1u, ctl);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t full = bar(L::V_FULL + static_cast<int>(tile & 1u));
+          mbar_arrive_expect_tx(full, 2 * L::kChunk);
 #pragma unroll
-            for (uint32_t h = 0; h < 2; ++h) {
-              const uint32_t dst = sRing + ((fill + h) % L::kSlots) * L::kChunk;
-              tma_load_3d(dst, &tmV, full, kNope, key + static_cast<int>(h) * 64, it.bh);
-              tma_load_3d(dst + L::kChunk / 2, &tmV, full, kNope + 64, key + static_cast<int>(h) * 64, it.bh);
-            }
+          for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t dst = sRing + ((fill + h) % L::kSlots) * L::kChunk;
+            tma_load_3d(dst, &tmV, full, kNope, key + static_cast<int>(h) * 64, it.bh);
+            tma_load_3d(dst + L::kChunk / 2, &tmV, full, kNope + 64, key + static_cast<int>(h) * 64, it.bh);
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
     }
     // drain, as above
