@@ -62,8 +62,10 @@ bool sizes_ok(int B, int H, int Sq, int Skv) {
          Sq <= (1 << 24) && Skv <= (1 << 24);
 }
 
-// Keys split where the items are fewer than the SMs, by fa_fwd's estimate in key
-// tiles: rounds of items times the tiles of a range, and eight tiles for the merge.
+// Keys split where the items are fewer than the SMs, by the smallest estimate of the
+// time in ns: rounds of items, each its start and end and its key tiles, and the merge's
+// start and its parts through L2.  (16 heads, 509 rows, us by ranges: 1500 keys 32.3
+// whole, 25.1 by 3, 23.9 by 4; 4096 keys 76.0 whole, 36.6 by 4, 91.9 by 32.)
 struct Plan {
   int n_qtiles, n_splits, tiles_per_split;
   size_t o_bytes, bytes;
@@ -78,11 +80,13 @@ Plan make_plan(int B, int H, int Sq, int Skv, int sm_count) {
   p.n_splits = 1;
   p.tiles_per_split = n_tiles;
   if (items < sms && static_cast<long long>(B) * H * Sq <= 0x7fffffffLL) {
-    constexpr long long kMergeTiles = 8;
-    long long best = n_tiles;
+    constexpr long long kItem = 4000, kTile = 2200, kMerge = 6000;
+    const long long rows = static_cast<long long>(B) * H * Sq;
+    long long best = kItem + kTile * n_tiles;
     for (int s = 2; s <= std::min(n_tiles, 64); ++s) {
       const int per = (n_tiles + s - 1) / s, n = (n_tiles + per - 1) / per;
-      const long long cost = (items * n + sms - 1) / sms * per + kMergeTiles;
+      const long long cost = (items * n + sms - 1) / sms * (kItem + kTile * per) + kMerge +
+                             rows * n * (fa::kNope + 1) * 8 / 7000;
       if (cost < best) {
         best = cost;
         p.n_splits = n;
