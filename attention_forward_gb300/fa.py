@@ -1,4 +1,5 @@
-"""ctypes binding of libfa_gb300.so -- argument marshalling only.
+"""Binding of libfa_gb300.so -- argument marshalling only, by ctypes; the plain calls
+of the 16-bit caches and of latent attention by compiled code (csrc/fa_torch.cpp).
 
 Every function here has the name of the C entry point it calls (declared in
 include/fa.h).  Tensors are torch tensors used as device (or pinned host)
@@ -8,6 +9,7 @@ fallback: if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -15,6 +17,7 @@ import torch
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                          "libfa_gb300.so")
 _lib = None
+_native = None  # the compiled calls, once bound to the library
 
 FA_F16, FA_BF16 = 0, 1
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED = 0, 1, 2
@@ -50,6 +53,26 @@ def load() -> ctypes.CDLL:
     if _lib is None:
         _lib = load_path(_LIB_PATH)
     return _lib
+
+
+def _load_native():
+    """The compiled calls, bound to the library's; raises if they have not been built."""
+    global _native
+    if _native is None:
+        path = os.path.join(os.path.dirname(_LIB_PATH), "_fa_torch.so")
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        L = load()
+        spec = importlib.util.spec_from_file_location("_fa_torch", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.fa_paged_write, L.fa_paged_read, L.fa_fwd_paged, L.fa_latent_write,
+            L.fa_latent_read, L.fa_fwd_latent, L.fa_fwd_expanded)))
+        _native = module
+    return _native
 
 
 def load_path(path: str) -> ctypes.CDLL:
@@ -652,30 +675,8 @@ def _rotated(q, count, stream):
 
 def _pool_args(cache, page_table, start, count, dev: int, dtype, Hkv: int, D: int, B: int,
                name: str = "start"):
-    """Pointers of a 16-bit cache, of its places, and (num_pages, page_size, max_pages):
-    the checks in one expression, for their time beside the kernels'; what it refuses is
-    named one by one."""
-    try:
-        kp, vp = cache
-        pool = kp.shape
-        pages, heads, page, width = pool
-        n, per = page_table.shape
-        i32 = torch.int32
-        if (heads == Hkv and width == D and n == B
-                and kp.dtype is dtype and kp.get_device() == dev and kp.is_contiguous()
-                and vp.dtype is dtype and vp.shape == pool and vp.get_device() == dev
-                and vp.is_contiguous()
-                and page_table.dtype is i32 and page_table.get_device() == dev
-                and page_table.is_contiguous()
-                and (start is None or start.dtype is i32 and start.shape == (B,)
-                     and start.get_device() == dev and start.is_contiguous())
-                and (count is None or count.dtype is i32 and count.shape == (B,)
-                     and count.get_device() == dev and count.is_contiguous())):
-            return (kp.data_ptr(), vp.data_ptr(), page_table.data_ptr(),
-                    None if start is None else start.data_ptr(),
-                    None if count is None else count.data_ptr()), (pages, page, per)
-    except (AttributeError, IndexError, TypeError, ValueError):
-        pass
+    """Pointers of a 16-bit cache and of its places, and (num_pages, page_size,
+    max_pages)."""
     kp, vp, pages, page = _paged(cache, dev, dtype, Hkv, D)
     where, per = _places(page_table, start, count, dev, B, name)
     return (kp, vp, *where), (pages, page, per)
@@ -688,6 +689,9 @@ def fa_paged_write(k, v, cache, page_table, start=None, count=None, freqs=None,
     [B, max_pages] lists.  ``freqs`` (float32 [rotary / 2], radians a position) rotates
     the first channels of keys and of ``q`` [B, H, S, D], as halves or interleaved
     pairs.  Returns the rotated queries (``q_out``, which may be q; None without q)."""
+    if stream is None and (_native or _load_native()).paged_write(
+            k, v, cache, page_table, start, count, freqs, interleaved, q, q_out) is None:
+        return q_out
     dev, shape = _rows16(k, "k")
     B, Hkv, S, D = shape
     dt = k.dtype
@@ -726,6 +730,9 @@ def fa_paged_read(cache, page_table, start=None, count=None, out=None, stream=No
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (k, v) to read into")
     k, v = out
+    if stream is None and (_native or _load_native()).paged_read(
+            cache, page_table, start, count, out) is None:
+        return k, v
     dev, shape = _rows16(k, "k")
     B, Hkv, S, D = shape
     if _current_device() != dev:
@@ -750,6 +757,11 @@ def fa_fwd_paged(q, cache, page_table, length, scale: float | None = None, softc
     """Attention of the newest Sq tokens, q [B, H, Sq, D], over the 16-bit cache:
     length[b] (int32) tokens of sequence b are in it, these included.  Returns
     (o, lse)."""
+    if out is None and lse is None and workspace is None and stream is None:
+        got = (_native or _load_native()).fwd_paged(q, cache, page_table, length, scale, softcap,
+                                                    slopes)
+        if got is not NotImplemented:
+            return got
     dev, (B, H, Sq, D) = _rows16(q, "q")
     if _current_device() != dev:
         return _on(dev, fa_fwd_paged, q, cache, page_table, length, scale, softcap, slopes,
@@ -794,30 +806,7 @@ def _latent_pages(cache, dev: int, dtype):
 
 def _latent_args(c, k_rope, cache, page_table, start, count):
     """(device, rows' pointers, the cache's and its places' pointers, sizes) of a latent
-    copy, checked as in _pool_args."""
-    try:
-        dt, dev = c.dtype, c.get_device()
-        B, S, width = c.shape
-        pages, page, row = cache.shape
-        n, per = page_table.shape
-        i32 = torch.int32
-        if (dev >= 0 and dt in _DTYPE and width == LATENT and row == LATENT + LATENT_ROPE and n == B
-                and c.is_contiguous()
-                and k_rope.dtype is dt and k_rope.shape == (B, S, LATENT_ROPE)
-                and k_rope.get_device() == dev and k_rope.is_contiguous()
-                and cache.dtype is dt and cache.get_device() == dev and cache.is_contiguous()
-                and page_table.dtype is i32 and page_table.get_device() == dev
-                and page_table.is_contiguous()
-                and (start is None or start.dtype is i32 and start.shape == (B,)
-                     and start.get_device() == dev and start.is_contiguous())
-                and (count is None or count.dtype is i32 and count.shape == (B,)
-                     and count.get_device() == dev and count.is_contiguous())):
-            return (dev, (c.data_ptr(), k_rope.data_ptr()),
-                    (cache.data_ptr(), page_table.data_ptr(),
-                     None if start is None else start.data_ptr(),
-                     None if count is None else count.data_ptr()), (B, S, pages, page, per))
-    except (AttributeError, IndexError, TypeError, ValueError):
-        pass
+    copy."""
     if not isinstance(c, torch.Tensor) or c.dim() != 3 or c.dtype not in _DTYPE:
         raise ValueError("c must be a [B, S, 512] float16 or bfloat16 tensor")
     dev, (B, S, _) = c.get_device(), c.shape
@@ -834,6 +823,9 @@ def fa_latent_write(c, k_rope, cache, page_table, start=None, count=None, freqs=
     ``freqs`` (float32 [32]; None: as it is), as fa_paged_write.  ``q_rope`` [B, H, S,
     64] goes rotated into the last 64 channels of ``q`` [B, H, S, width], whose others
     stay.  Returns q."""
+    if stream is None and (_native or _load_native()).latent_write(
+            c, k_rope, cache, page_table, start, count, freqs, interleaved, q_rope, q) is None:
+        return q
     dev, rows, (pool, *where), (B, S, *pages) = _latent_args(c, k_rope, cache, page_table, start,
                                                              count)
     if _current_device() != dev:
@@ -864,6 +856,9 @@ def fa_latent_read(cache, page_table, start=None, count=None, out=None, stream=N
     if out is None or len(out) != 2:
         raise ValueError("out must be the pair (c, k_rope) to read into")
     c, k_rope = out
+    if stream is None and (_native or _load_native()).latent_read(
+            cache, page_table, start, count, out) is None:
+        return c, k_rope
     dev, rows, pool, sizes = _latent_args(c, k_rope, cache, page_table, start, count)
     if _current_device() != dev:
         return _on(dev, fa_latent_read, cache, page_table, start, count, out, stream)
@@ -882,8 +877,6 @@ def fa_latent_workspace_bytes(B: int, H: int, Sq: int, page_size: int, max_pages
 def _outputs_wide(q, width: int, dev: int, out, lse, stream):
     """As _outputs_on, with output rows of another width than q's."""
     B, H, Sq, _ = q.shape
-    if out is None and lse is None and stream is None:
-        return q.new_empty((B, H, Sq, width)), q.new_empty((B, H, Sq), dtype=torch.float32)
     made = []
     if out is None:
         out = torch.empty((B, H, Sq, width), dtype=q.dtype, device=q.device)
@@ -910,6 +903,10 @@ def fa_fwd_latent(q, cache, page_table, length, scale: float | None = None, work
     """Latent attention, absorbed: the newest Sq tokens' q [B, H, Sq, 576] over the
     cache's rows, whose first 512 channels are the values too.  length as for
     fa_fwd_paged; scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 512], lse)."""
+    if out is None and lse is None and workspace is None and stream is None:
+        got = (_native or _load_native()).fwd_latent(q, cache, page_table, length, scale)
+        if got is not NotImplemented:
+            return got
     dev, (B, H, Sq, D) = _rows16(q, "q")
     if D != LATENT + LATENT_ROPE:
         raise ValueError("q must be [B, H, Sq, 576]")
@@ -944,6 +941,10 @@ def fa_fwd_expanded(q, kv, k_rope, causal: bool = False, scale: float | None = N
     """Latent attention, expanded: q [B, H, Sq, 192], kv [B, H, Skv, 256] (a head's key
     of 128 channels, then its value), k_rope [B, Skv, 64] (the keys' shared part).
     scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 128], lse)."""
+    if out is None and lse is None and workspace is None and stream is None:
+        got = (_native or _load_native()).fwd_expanded(q, kv, k_rope, causal, scale)
+        if got is not NotImplemented:
+            return got
     dev, (B, H, Sq, D) = _rows16(q, "q")
     _, shape = _rows16(kv, "kv")
     Skv = shape[2]
