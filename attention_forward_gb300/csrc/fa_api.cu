@@ -761,6 +761,22 @@ fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int h
   return st != FA_OK ? st : encode_3d(m, base, D, rows, heads, box_rows, bf16);
 }
 
+fa_status_t encode_rows_of_chunks(CUtensorMap* m, const void* base, long long rows, int chunks,
+                                  int box_rows, bool bf16) {
+  const fa_status_t st = get_encoder();
+  if (st != FA_OK) return st;
+  const cuuint64_t dims[3] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(chunks)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(chunks) * 128u, 128u};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(chunks)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = g_encode(
+      m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+      const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
+
 fa_status_t encode_pools(CUtensorMap* m, const void* base, const void* second, long long rows,
                          int chunks, bool bf16) {
   const fa_status_t st = get_encoder();

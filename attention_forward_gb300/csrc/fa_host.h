@@ -64,6 +64,11 @@ int device_sms();
 fa_status_t encode_rows(CUtensorMap* m, const void* base, int D, int rows, int heads,
                         int box_rows, bool bf16);
 
+// TMA descriptor of a [rows, 64 chunks] 16-bit array as [chunks, rows, 64]: a box of
+// box_rows rows lands chunk by chunk.
+fa_status_t encode_rows_of_chunks(CUtensorMap* m, const void* base, long long rows, int chunks,
+                                  int box_rows, bool bf16);
+
 // TMA descriptor of one or two [rows, 64 chunks] 16-bit arrays as [array, chunks,
 // rows, 64]: a box of 8 rows lands chunk by chunk.  `second`, which may be null, is
 // where the other array begins, above `base`; FA_ERR_UNSUPPORTED where they lie too

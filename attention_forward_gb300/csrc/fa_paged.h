@@ -49,7 +49,6 @@ struct PagedReadParams {
 };
 
 struct PagedAttnParams {
-  const void* q;      // [B, H, Sq, keys' width]
   void* o;            // [B, H, Sq, values' width]
   float* lse;         // [B, H, Sq]
   float* part_o;      // [2 * grid, values' width, part_rows] fp32, O / l of a segment
@@ -61,7 +60,7 @@ struct PagedAttnParams {
   unsigned long long timeout_ns;
   int B, H, Hkv, Sq;
   int rows;           // (H / Hkv) * Sq query rows per kv head
-  int part_rows;      // rows that a part holds: a CTA's, up to a multiple of 4
+  int part_rows;      // rows that a part holds: a CTA's, up to 4, 8, 16 or a multiple of 32
   int n_row_blocks;   // of a CTA's rows, or a cluster's
   int sms;
   int whole;          // CTAs take whole units: no parts, no merge
@@ -94,7 +93,8 @@ constexpr int kPagedMinChunks = 1;
 bool paged_attn_whole(int kind, long long units, int room, int sm_count);
 // CTAs for `units` (of a cluster's rows).
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
-cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,
-                              const PagedAttnParams& p, int grid, cudaStream_t stream);
+cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const PagedAttnParams& p, int grid,
+                              cudaStream_t stream);
 
 }  // namespace fa

@@ -9,18 +9,19 @@
 
 namespace fa {
 
-cudaError_t launch_paged_attn_d64(bool, const CUtensorMap&, const CUtensorMap&,
+cudaError_t launch_paged_attn_d64(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                   const PagedAttnParams&, int, cudaStream_t);
-cudaError_t launch_paged_attn_d128(bool, const CUtensorMap&, const CUtensorMap&,
+cudaError_t launch_paged_attn_d128(bool, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
                                    const PagedAttnParams&, int, cudaStream_t);
-cudaError_t launch_paged_attn_latent(bool, const CUtensorMap&,
+cudaError_t launch_paged_attn_latent(bool, const CUtensorMap&, const CUtensorMap&,
                                      const PagedAttnParams&, int, cudaStream_t);
 
-cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& k, const CUtensorMap& v,
-                              const PagedAttnParams& p, int grid, cudaStream_t stream) {
-  if (kind == kLatent) return launch_paged_attn_latent(bf16, k, p, grid, stream);
-  return kind == 128 ? launch_paged_attn_d128(bf16, k, v, p, grid, stream)
-                     : launch_paged_attn_d64(bf16, k, v, p, grid, stream);
+cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
+                              const CUtensorMap& v, const PagedAttnParams& p, int grid,
+                              cudaStream_t stream) {
+  if (kind == kLatent) return launch_paged_attn_latent(bf16, q, k, p, grid, stream);
+  return kind == 128 ? launch_paged_attn_d128(bf16, q, k, v, p, grid, stream)
+                     : launch_paged_attn_d64(bf16, q, k, v, p, grid, stream);
 }
 
 int paged_attn_row_block(int kind, int rows) {
@@ -165,7 +166,10 @@ AttnPlan plan_attn(int kind, int B, int H, int Hkv, int Sq, const PageShape& s, 
   const int room = s.max_pages * s.page_size;
   const int cluster_rows = block * fa::paged_attn_cluster(kind, rows);
   a.row_blocks = (rows + cluster_rows - 1) / cluster_rows;
-  a.part_rows = (std::min(rows, block) + 3) & ~3;
+  a.part_rows = std::min(rows, block);
+  a.part_rows = a.part_rows > 16   ? (a.part_rows + 31) & ~31
+                : a.part_rows > 8 ? 16
+                                  : (a.part_rows + 3) & ~3;  // as paged_part_row has them
   const long long units = static_cast<long long>(B) * Hkv * a.row_blocks;
   a.grid = fa::paged_attn_grid(kind, rows, units, room, sm_count);
   a.whole = fa::paged_attn_whole(kind, units, room, sm_count) ? 1 : 0;
@@ -206,7 +210,6 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
     return FA_ERR_WORKSPACE;
 
   fa::PagedAttnParams p{};
-  p.q = q;
   p.o = o;
   p.lse = lse;
   if (plan.bytes > 0) {
@@ -239,9 +242,11 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
   }
   const bool bf16 = dtype == FA_BF16;
   const int k_chunks = kind == fa::kLatent ? fa::kLatentRow / 64 : kind / 64;
-  // one descriptor for both pools, two where they lie too far apart (each takes the
-  // host over a microsecond)
-  CUtensorMap tk, tv;
+  CUtensorMap tq, tk, tv;
+  st = fa::encode_rows_of_chunks(&tq, q, static_cast<long long>(B) * H * Sq, k_chunks,
+                                 fa::paged_attn_row_block(kind, p.rows), bf16);
+  if (st != FA_OK) return st;
+  // one descriptor for both pools, two where they lie too far apart
   const bool one = kind == fa::kLatent || k == v;
   const char *kb = static_cast<const char*>(k), *vb = static_cast<const char*>(v);
   st = fa::encode_pools(&tk, std::min(kb, vb), one ? nullptr : std::max(kb, vb), p.pool_rows, k_chunks,
@@ -255,8 +260,8 @@ fa_status_t attend(int kind, const void* q, const void* k, const void* v, const 
       st = fa::encode_pools(&tv, v, nullptr, p.pool_rows, k_chunks, bf16);
   }
   if (st != FA_OK) return st;
-  return fa::launch_paged_attn(kind, bf16, tk, tv, p, plan.grid, stream) == cudaSuccess ? FA_OK
-                                                                                        : FA_ERR_CUDA;
+  return fa::launch_paged_attn(kind, bf16, tq, tk, tv, p, plan.grid, stream) == cudaSuccess ? FA_OK
+                                                                                            : FA_ERR_CUDA;
 }
 
 }  // namespace

@@ -18,11 +18,13 @@
 //        one reference maximum a row, raised for the whole CTA when a score passes it
 //        by 15 (log2 units; then O is rescaled in place), set 8 below the maximum so
 //        that fp16 holds p over 2^-24 ... 2^15 around it; p goes to shared memory
-//        transposed (stmatrix).  They also load a segment's queries and write its O.
+//        transposed (stmatrix).  They also send for a segment's queries (TMA: by the warps
+//        themselves 128 rows of 576 channels took 9 us) and write its O.
 //   4    MMA issue, tensor memory
-//   5, 6 TMA producers, of K and of V (one for latent rows): rings of tiles, by boxes of 8 rows (all channels): any page
-//        size is a multiple of them.  A box past the sequence or of a page that does
-//        not exist is fetched from past the pool's end, as zeros.
+//   5, 6 TMA producers, of K and of V (one for latent rows): rings of tiles, by boxes of
+//        8 rows (all channels): any page size is a multiple of them.  A box past the
+//        sequence or of a page that does not exist is fetched from past the pool's end,
+//        as zeros.
 // The tensor core runs S(j + 1) while the softmax works on S(j), when the tile is
 // there: warp 4 takes whichever of S(j + 1) and O(j) is ready first.
 //
@@ -103,6 +105,17 @@ constexpr int paged_smem_bytes() {
   return S::kOffMisc + static_cast<int>(sizeof(PagedMisc<S::kN, S::kWarps, !S::kShared>)) + 1024;  // + alignment
 }
 
+// The row of place i of a channel's in the parts.  A lane of the attention holds rows
+// 2 t4, 2 t4 + 1 of every 8: those of 32 rows (of 16) lie next to each other, so that
+// four lanes write a line (half) with one store each.  Parts of 4 or 8 rows: in order.
+template <int kN>
+__device__ __forceinline__ int paged_part_row(int i, int part_rows) {
+  if constexpr (kN >= 32)
+    return (i & ~31) + ((i >> 1) & 3) * 8 + ((i >> 3) & 3) * 2 + (i & 1);
+  else
+    return part_rows < 16 ? i : ((i >> 1) & 1) * 8 + (i >> 2) * 2 + (i & 1);
+}
+
 // The CTA's segments: ranges of one unit's keys.
 struct PagedWalk {
   int cta, ctas, rank;   // of the deal: a CTA, or a cluster; the CTA's rank in it
@@ -152,7 +165,8 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
 
 template <class S, bool BF16, bool kMod>
 __global__ void __launch_bounds__(S::kThreads, S::kCtas)
-    fa_paged_attn_kernel(const __grid_constant__ CUtensorMap tmK,
+    fa_paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
+                         const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
   constexpr int kN = S::kN, kNB = kN / 8, kStages = S::kStages;
   constexpr float kLog2e = 1.4426950408889634f;
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     mbar_init(p_ready + 8, 4);
     mbar_init(o_done, 1);
     mbar_init(o_done + 8, 1);
-    mbar_init(q_full, 4);
+    mbar_init(q_full, 1);
     mbar_init(drain, 1);
     sm.abort = 0u;
     fence_mbar_init();
@@ -195,6 +209,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     tmem_relinquish();
   }
   if (warp == 5 && lane == 0) {
+    tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     if constexpr (!S::kShared) tma_prefetch_desc(&tmV);
   }
@@ -236,33 +251,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     const uint32_t p_at = sP + static_cast<uint32_t>(((lane >> 4) * 8 + (lane & 7)) * 128 +
                                                      (((2 * warp + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
     const float fac = kMod && p.cap > 0.f ? p.scale : p.scale * kLog2e;
-    uint32_t t = 0;  // tiles so far
+    uint32_t t = 0, nq = 0;  // tiles, and loads of queries, so far
     bool ok = true;
-    // a segment's queries, K-major and 128-byte swizzled, zeros past its rows; the
-    // scores of the segment before are all read
+    // a segment's queries (the rows behind them, where it has fewer than kN, are nobody's);
+    // the scores of the segment before are all there
     auto load_q = [&](const PagedSeg& s) {
       if (s.n_tiles == 0) return;
-      constexpr int kWords = 8 * S::kKC, kAtOnce = kN * kWords / 128 < 9 ? kN * kWords / 128 : 9;
-      static_assert(kN * kWords % (128 * kAtOnce) == 0, "words of the queries");
-      const uint4* q = static_cast<const uint4*>(p.q) + s.out_row0 * kWords;
-#pragma unroll 1
-      for (int i0 = threadIdx.x; i0 < kN * kWords; i0 += 128 * kAtOnce) {
-        uint4 x[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const int i = i0 + 128 * k;
-          x[k] = i / kWords < s.n_rows ? __ldg(q + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const int i = i0 + 128 * k, n = i / kWords, w = i - n * kWords;
-          st_shared_v4(sQ + static_cast<uint32_t>((w >> 3) * (kN * 128) + n * 128 + (((w ^ n) & 7) << 4)),
-                       x[k].x, x[k].y, x[k].z, x[k].w);
-        }
+      ++nq;
+      if (threadIdx.x == 0) {
+        mbar_arrive_expect_tx(q_full, S::kQBytes);
+        tma_load_3d(sQ, &tmQ, q_full, 0, static_cast<int>(s.out_row0), 0);
       }
-      fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
     };
     PagedSeg next;
     bool more = paged_next<kN, S::kCluster>(p, walk, seg);
@@ -513,20 +513,34 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           }
           __syncwarp();
         } else {
-          float* part = p.part_o + (static_cast<long long>(seg.part) * S::kDv + ch0 + g) * p.part_rows +
-                        2 * t4;
+          // a lane's values of a channel next to each other (paged_part_row)
+          float* part = p.part_o + (static_cast<long long>(seg.part) * S::kDv + ch0 + g) * p.part_rows;
+          const int down = 8 * p.part_rows;
+          if constexpr (kN >= 32) {
 #pragma unroll
-          for (int n = 0; n < kNB; ++n)
-            if (8 * n + 2 * t4 < p.part_rows) {
-              *reinterpret_cast<float2*>(part + 8 * n) = make_float2(x[n][0], x[n][1]);
-              *reinterpret_cast<float2*>(part + 8 * n + 8 * p.part_rows) = make_float2(x[n][2], x[n][3]);
-            }
+            for (int n = 0; n < kNB; n += 4)
+              if (8 * n < p.part_rows) {
+                st_global_v8(part + 8 * n + 8 * t4, x[n][0], x[n][1], x[n + 1][0], x[n + 1][1],
+                             x[n + 2][0], x[n + 2][1], x[n + 3][0], x[n + 3][1]);
+                st_global_v8(part + down + 8 * n + 8 * t4, x[n][2], x[n][3], x[n + 1][2], x[n + 1][3],
+                             x[n + 2][2], x[n + 2][3], x[n + 3][2], x[n + 3][3]);
+              }
+          } else if (p.part_rows == 16) {
+            *reinterpret_cast<float4*>(part + 4 * t4) = make_float4(x[0][0], x[0][1], x[1][0], x[1][1]);
+            *reinterpret_cast<float4*>(part + down + 4 * t4) =
+                make_float4(x[0][2], x[0][3], x[1][2], x[1][3]);
+          } else if (2 * t4 < p.part_rows) {
+            *reinterpret_cast<float2*>(part + 2 * t4) = make_float2(x[0][0], x[0][1]);
+            *reinterpret_cast<float2*>(part + down + 2 * t4) = make_float2(x[0][2], x[0][3]);
+          }
         }
       }
       tc_fence_before();
       if (named_bar_or(1, 128, !ok)) break;
       seg = next;
     }
+    // queries sent for land before shared memory goes away
+    if (nq > 0) wait_drain(q_full, (nq - 1) & 1u, p.timeout_ns);
   } else if (warp == 4) {
     // =============================== MMA issue ===============================
     constexpr uint32_t kIdescS = idesc_f16(BF16, false, false, 64, kN);
@@ -722,10 +736,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 // weights of all the unit's rows once, then its threads take four rows of a channel
 // each, which lie together in the parts, the parts dealt to groups of threads where
 // those are few.  As many channels as leave every multiprocessor a block.
-constexpr int kPagedMergeThreads = 256;
+constexpr int kPagedMergeThreads = 256;  // 128: H 128 slower by 6 us
 
+// Four blocks an SM (three: 32 sequences of 8192 keys 138 to 141 us), or no limit for the
+// narrow slices that few units have.
 template <class S, bool BF16, int kCh>
-__global__ void __launch_bounds__(kPagedMergeThreads)
+__global__ void __launch_bounds__(kPagedMergeThreads, kCh > 8 ? 4 : 1)
     fa_paged_merge_kernel(const PagedAttnParams p, int attn_grid) {
   constexpr int kN = S::kN, kThr = kPagedMergeThreads, kWarps = kThr / 32;
   constexpr int kParts = 64;                                // whose weights are held at once
@@ -740,7 +756,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
   __shared__ float sums[kN];
   __shared__ union {
     float4 acc[kThr];
-    alignas(16) uint16_t out[kN * kCh];
+    alignas(16) uint16_t out[kN * (kCh + 8) + kN / 2];
   } end;
   const int tid = static_cast<int>(threadIdx.x);
   // a unit of the deal and, in clusters, the rank of the CTA whose rows these are
@@ -781,7 +797,9 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
   float4 acc[kItems];
 #pragma unroll
   for (int i = 0; i < kItems; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int row = tid / kPer, j = tid % kPer;
+  const int row = tid / kPer, j = tid % kPer;  // a row by its place in the parts
+  // the output's rows, so that the threads that write a channel's meet few banks twice
+  auto out_at = [](int r) { return r * (kCh + 8) + (r >> 4) * 8; };
   float top = -INFINITY, sum = 0.f;  // the row's, over the parts so far
 
 #pragma unroll 1
@@ -796,9 +814,9 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
           ahead[i][k] = load(s0 + group + k * groups, item0 + i * kThr);
     if (s0 > 0) __syncthreads();  // the weights before are done with
     for (int i = tid; i < now * kN; i += kThr) {
-      const int s = i / kN, n = i % kN;
-      w[s * kW + n] = n < n_rows ? p.part_lse[static_cast<long long>(part_of(s0 + s)) * kN + n] * kLog2e
-                                 : -INFINITY;
+      const int s = i / kN, at = i % kN, n = paged_part_row<kN>(at, p.part_rows);
+      w[s * kW + at] = n < n_rows ? p.part_lse[static_cast<long long>(part_of(s0 + s)) * kN + n] * kLog2e
+                                  : -INFINITY;
     }
     __syncthreads();
     float m = top, part_sum = 0.f;
@@ -865,7 +883,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
       for (int k = 0; k < 4; ++k) {
         // no part has a key: 0; a NaN stays one
         const float x = sums[r + k] == 0.f ? 0.f : v[k] / sums[r + k];
-        end.out[(r + k) * kCh + c] = static_cast<uint16_t>(pack2<BF16>(x, x));
+        end.out[out_at(paged_part_row<kN>(r + k, p.part_rows)) + c] = static_cast<uint16_t>(pack2<BF16>(x, x));
       }
     }
   }
@@ -874,10 +892,11 @@ __global__ void __launch_bounds__(kPagedMergeThreads)
   for (int i = tid; i < n_rows * (kCh / 8); i += kThr) {
     const int r = i / (kCh / 8), c = i % (kCh / 8);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (row0 + r) * S::kDv + ch0 + 8 * c) =
-        *reinterpret_cast<const uint4*>(end.out + r * kCh + 8 * c);
+        *reinterpret_cast<const uint4*>(end.out + out_at(r) + 8 * c);
   }
-  if (blockIdx.y == 0 && j == 0 && row < n_rows)
-    p.lse[row0 + row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  const int out_row = paged_part_row<kN>(row, p.part_rows);
+  if (blockIdx.y == 0 && j == 0 && out_row < n_rows)
+    p.lse[row0 + out_row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace fa

@@ -3,12 +3,12 @@
 
 namespace fa {
 
-cudaError_t launch_paged_attn_latent(bool bf16, const CUtensorMap& k,
+cudaError_t launch_paged_attn_latent(bool bf16, const CUtensorMap& q, const CUtensorMap& k,
                                      const PagedAttnParams& p, int grid, cudaStream_t stream) {
   auto with = [&](auto shape) {
     using S = decltype(shape);
-    return bf16 ? paged_launch_one<S, true, false>(k, k, p, grid, stream)
-                : paged_launch_one<S, false, false>(k, k, p, grid, stream);
+    return bf16 ? paged_launch_one<S, true, false>(q, k, k, p, grid, stream)
+                : paged_launch_one<S, false, false>(q, k, k, p, grid, stream);
   };
   switch (paged_attn_row_block(kLatent, p.rows)) {
     case 16: return with(PagedShape<9, 8, true, 16, 2, 1>{});

@@ -10,8 +10,8 @@
 namespace fa {
 
 template <class S, bool BF16, bool kMod>
-cudaError_t paged_launch_one(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnParams& p,
-                             int grid, cudaStream_t stream) {
+cudaError_t paged_launch_one(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v,
+                             const PagedAttnParams& p, int grid, cudaStream_t stream) {
   static_assert(paged_smem_bytes<S>() <= 232448 && S::kStages <= PagedMiscBars::kMaxStages,
                 "shared memory budget");
   static_assert(S::kCtas * (paged_smem_bytes<S>() + 1024) <= 233472, "CTAs an SM");
@@ -57,7 +57,7 @@ cudaError_t paged_launch_one(const CUtensorMap& k, const CUtensorMap& v, const P
   }
   cfg.gridDim = dim3(static_cast<unsigned>(grid * S::kCluster), 1, 1);
   cfg.numAttrs = S::kCluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_attn_kernel<S, BF16, kMod>, k, v, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_attn_kernel<S, BF16, kMod>, q, k, v, p);
   if (e != cudaSuccess || p.whole) return e;
   const long long units = static_cast<long long>(p.B) * p.Hkv * p.n_row_blocks;
   const long long blocks = units * S::kCluster;
@@ -69,7 +69,10 @@ cudaError_t paged_launch_one(const CUtensorMap& k, const CUtensorMap& v, const P
     cfg.gridDim = dim3(static_cast<unsigned>(units), S::kDv / kCh, S::kCluster);
     return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<S, BF16, kCh>, p, grid);
   };
-  if (blocks * (S::kDv / 64) >= p.sms) return with(std::integral_constant<int, 64>{});
+  // (64 channels of 64 rows are four float4 a thread and part, and 168 registers: 128
+  // heads, 32 sequences of 8192 keys 108 us, 32 channels 101 us)
+  if constexpr (S::kN < 64)
+    if (blocks * (S::kDv / 64) >= p.sms) return with(std::integral_constant<int, 64>{});
   if (blocks * (S::kDv / 32) >= p.sms) return with(std::integral_constant<int, 32>{});
   return with(std::integral_constant<int, 8>{});
 }

@@ -814,6 +814,14 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&v)[8][4]
       : "memory");
 }
 
+// eight floats to a 32-byte boundary
+__device__ __forceinline__ void st_global_v8(float* to, float a, float b, float c, float d, float e,
+                                             float f, float g, float h) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(a), "f"(b),
+               "f"(c), "f"(d), "f"(e), "f"(f), "f"(g), "f"(h)
+               : "memory");
+}
+
 // Four 8 x 8 matrices of 16-bit elements (fragments as above, packed in pairs) to
 // shared memory, transposed: lane i gives the address of column i % 8 of matrix i / 8.
 __device__ __forceinline__ void stmatrix_trans4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
