@@ -63,9 +63,10 @@ struct KeyScan {
 // The block's threads take the sequences in runs of equal length and add up
 // their chunks.  Returns the chunks of all units, and a unit's of the sequences
 // before the thread's run (`upto`); `report` records lengths that had to be
-// limited.
+// limited.  `extra`: chunks more that every unit is dealt as, behind its own.
 template <class P, int kWarps>
-__device__ __forceinline__ int cache_scan(const P& p, KeyScan<kWarps>& s, bool report, int& upto) {
+__device__ __forceinline__ int cache_scan(const P& p, KeyScan<kWarps>& s, bool report, int& upto,
+                                          int extra = 0) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int run = (p.B + 32 * kWarps - 1) / (32 * kWarps);
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
@@ -73,7 +74,7 @@ __device__ __forceinline__ int cache_scan(const P& p, KeyScan<kWarps>& s, bool r
   for (int b = b0; b < b1; ++b) {
     const int len = cache_length(p, b);
     if (report && len != p.length[b]) atomicMax(p.status, kStatusBadIndex);
-    sum += cache_chunks(len);
+    sum += cache_chunks(len) + extra;
   }
   int inc = sum;
 #pragma unroll
@@ -96,14 +97,14 @@ __device__ __forceinline__ int cache_scan(const P& p, KeyScan<kWarps>& s, bool r
 // The sequence of chunk c, its length, and the chunks before it (all units').
 template <class P, int kWarps>
 __device__ __forceinline__ void cache_find(const P& p, KeyScan<kWarps>& s, int upto, int c, int& b,
-                                           int& len, int& before) {
+                                           int& len, int& before, int extra = 0) {
   const int run = (p.B + 32 * kWarps - 1) / (32 * kWarps);
   const int b0 = min(p.B, static_cast<int>(threadIdx.x) * run), b1 = min(p.B, b0 + run);
   const int units = p.Hkv * p.n_row_blocks;
   int at = upto * units;
   for (int k = b0; k < b1 && at <= c; ++k) {
     const int l = cache_length(p, k);
-    const int n = cache_chunks(l) * units;
+    const int n = (cache_chunks(l) + extra) * units;
     if (c < at + n) {
       s.before = at;
       s.b = k;

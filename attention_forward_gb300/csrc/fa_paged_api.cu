@@ -150,7 +150,7 @@ bool chunks_ok(int kind, int B, int H, int Hkv, int Sq, const PageShape& s) {
   const long long rows = static_cast<long long>(H / Hkv) * Sq;
   const int block = fa::paged_attn_row_block(kind, static_cast<int>(rows));
   const long long chunks = (static_cast<long long>(s.max_pages) * s.page_size +
-                            fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys;
+                            fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys + fa::kPagedMaxSegment;
   return static_cast<long long>(B) * Hkv * ((rows + block - 1) / block) * chunks <= fa::kCacheMaxChunks;
 }
 

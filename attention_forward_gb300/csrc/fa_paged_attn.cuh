@@ -56,6 +56,11 @@ struct PagedShape {
   static constexpr int kStageBytes = kTileK + kTileV;
   static constexpr int kVTile = kShared ? kTileK : kTileV;       // from a tile's V to the next
   static constexpr int kVStride = (kShared ? kKC : kVC) * 1024;  // from 8 keys to the next 8
+  // The end of a segment takes as long as so many chunks: a unit is dealt as so many more,
+  // behind its own, so that a CTA with two segments has fewer chunks (pairs, 32 sequences
+  // of 8192 rows: 98.5 to 96 us; one sequence of 16384 keys: 20.3 to 19.7 us).
+  static constexpr int kSegment = kCluster == 2 ? 3 : 1;
+  static_assert(kSegment <= kPagedMaxSegment, "the check of the deal's chunks");
   static constexpr int kQBytes = kN * 128 * kKC;
   static constexpr int kPBytes = kN * 128;
   static constexpr int kBlocks = kVC == 1 ? 1 : kVC / 2;  // O^T in blocks of 128 channels (64)
@@ -129,15 +134,32 @@ struct PagedSeg {
   const int* pages;
 };
 
-template <int kN, int kCluster>
+template <class S>
 __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& w, PagedSeg& s) {
-  if (w.cur >= w.last) return false;
+  constexpr int kN = S::kN, kCluster = S::kCluster;
   const int units = p.Hkv * p.n_row_blocks;
-  if (p.whole) w.b = w.cur / units;
-  if (p.whole || w.cur != w.first) w.len = cache_length(p, w.b);
-  const int seq_chunks = cache_chunks(w.len);
-  const int unit = p.whole ? w.cur - w.b * units : (w.cur - w.before) / seq_chunks;
-  const int chunk0 = p.whole ? 0 : w.cur - w.before - unit * seq_chunks;
+  int seq_chunks, unit, chunk0;
+  while (true) {
+    if (w.cur >= w.last) return false;
+    if (p.whole) w.b = w.cur / units;
+    if (p.whole || w.cur != w.first) w.len = cache_length(p, w.b);
+    seq_chunks = cache_chunks(w.len);
+    if (p.whole) {
+      unit = w.cur - w.b * units;
+      chunk0 = 0;
+      break;
+    }
+    const int dealt = seq_chunks + S::kSegment;
+    unit = (w.cur - w.before) / dealt;
+    chunk0 = w.cur - w.before - unit * dealt;
+    if (chunk0 < seq_chunks) break;
+    // nothing but what stands for the unit's end
+    w.cur += dealt - chunk0;
+    if (unit == units - 1) {
+      w.before += dealt * units;
+      ++w.b;
+    }
+  }
   const int n_chunks = p.whole ? seq_chunks : min(seq_chunks - chunk0, w.last - w.cur);
   s.whole = n_chunks == seq_chunks;
   s.part = (2 * w.cta + (w.cur == w.first ? 0 : 1)) * kCluster + w.rank;
@@ -153,10 +175,12 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
   s.pages = p.page_table + static_cast<long long>(w.b) * p.max_pages;
   if (p.whole) {
     w.cur += w.ctas;
-  } else {
+  } else if (chunk0 + n_chunks < seq_chunks) {
     w.cur += n_chunks;
-    if (chunk0 + n_chunks == seq_chunks && unit == units - 1) {
-      w.before += seq_chunks * units;
+  } else {
+    w.cur += n_chunks + S::kSegment;
+    if (unit == units - 1) {
+      w.before += (seq_chunks + S::kSegment) * units;
       ++w.b;
     }
   }
@@ -231,12 +255,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     walk.last = p.B * p.Hkv * p.n_row_blocks;
   } else {
     int upto;
-    const int all = cache_scan(p, sm.scan, blockIdx.x == 0, upto);
+    const int all = cache_scan(p, sm.scan, blockIdx.x == 0, upto, S::kSegment);
     const CacheDeal deal = cache_deal(all, walk.ctas, kPagedMinChunks);
     if (walk.cta < deal.n) {
       walk.first = deal.begin(walk.cta);
       walk.last = deal.begin(walk.cta + 1);
-      cache_find(p, sm.scan, upto, walk.first, walk.b, walk.len, walk.before);
+      cache_find(p, sm.scan, upto, walk.first, walk.b, walk.len, walk.before,
+                 S::kSegment);
     }
   }
   walk.cur = walk.first;
@@ -265,7 +290,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       __syncwarp();
     };
     PagedSeg next;
-    bool more = paged_next<kN, S::kCluster>(p, walk, seg);
+    bool more = paged_next<S>(p, walk, seg);
     if (more) load_q(seg);
 #pragma unroll 1
     while (more) {
@@ -432,7 +457,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       ok = !named_bar_or(1, 128, !ok);
       if (!ok) break;
       // the next segment's queries first: its scores run beside what follows
-      more = paged_next<kN, S::kCluster>(p, walk, next);
+      more = paged_next<S>(p, walk, next);
       if (more) load_q(next);
 #pragma unroll
       for (int n = 0; n < kNB; ++n)
@@ -548,7 +573,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     uint32_t t0 = 0, nq = 0;  // tiles, and segments with tiles, before this one
     bool ok = true, issued = false;
 #pragma unroll 1
-    while (ok && paged_next<kN, S::kCluster>(p, walk, seg)) {
+    while (ok && paged_next<S>(p, walk, seg)) {
       const uint32_t n = static_cast<uint32_t>(seg.n_tiles);
       if (n == 0) continue;
       if (!wait_bar_warp(q_full, nq & 1u, ctl)) break;
@@ -652,7 +677,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     uint32_t t = 0;
     bool ok = true;
 #pragma unroll 1
-    while (ok && paged_next<kN, S::kCluster>(p, walk, seg)) {
+    while (ok && paged_next<S>(p, walk, seg)) {
       // four tiles' places at a time, a lane for each 8 keys, the next four's fetched
       // ahead
       const int page_keys = 1 << p.page_shift;
@@ -766,17 +791,17 @@ __global__ void __launch_bounds__(kPagedMergeThreads, kCh > 8 ? 4 : 1)
   const int rb = (unit - hk * p.n_row_blocks) * S::kCluster + rank;
   const int ch0 = static_cast<int>(blockIdx.y) * kCh;
   int upto;
-  const int all = cache_scan(p, scan, false, upto);
+  const int all = cache_scan(p, scan, false, upto, S::kSegment);
   const CacheDeal deal = cache_deal(all, attn_grid, kPagedMinChunks);
   // chunks per unit of the sequences before b: the thread with b in its run
   const int run = (p.B + kThr - 1) / kThr;
   if (b / run == tid) {
-    for (int k = tid * run; k < b; ++k) upto += cache_chunks(cache_length(p, k));
+    for (int k = tid * run; k < b; ++k) upto += cache_chunks(cache_length(p, k)) + S::kSegment;
     scan.before = upto;
   }
   __syncthreads();
   const int chunks = cache_chunks(cache_length(p, b));
-  const int start = scan.before * units + unit * chunks;
+  const int start = scan.before * units + unit * (chunks + S::kSegment);
   const int x0 = deal.cta_of(start), x1 = deal.cta_of(start + chunks - 1);
   grid_dependency_wait();  // all blocks: this grid's end is then the attention's too
   if (x0 == x1) return;
