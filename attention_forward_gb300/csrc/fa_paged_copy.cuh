@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(kPagedCopyThreads, kLat ? 4 : 3)
   const int start = p.start ? p.start[b] : 0;
   const int count = p.count ? min(p.count[b], p.S) : p.S;
   if (first >= count) return;
+  // (before the angles, which its latency then hides)
+  const long long slot =
+      paged_slot(p, b, static_cast<uint32_t>(start) + static_cast<uint32_t>(token));
   float2 unit[8];
   if (half > 0) {
     for (int i = tid; i < half << ts; i += kPagedCopyThreads) {
@@ -150,8 +153,6 @@ __global__ void __launch_bounds__(kPagedCopyThreads, kLat ? 4 : 3)
     }
   }
   if (token >= count) return;
-  const long long slot =
-      paged_slot(p, b, static_cast<uint32_t>(start) + static_cast<uint32_t>(token));
   if (slot < 0 && u == 0 && h == 0) atomicMax(p.status, kStatusBadIndex);
 #pragma unroll 1
   for (;;) {
