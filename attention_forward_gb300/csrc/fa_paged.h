@@ -85,7 +85,11 @@ int paged_attn_cluster(int kind, int rows);
 // 3 sequences of 704 latent keys 10.3, 12.5, 14.9; 8 units of 704 keys (128 channels)
 // 8.6, 10.7, 11.4, of 2048 9.2, 10.1, 10.1, of 4096 11.1, 10.6, 10.2.
 constexpr int kPagedMinChunks = 1;
-constexpr int kPagedMaxSegment = 3;  // chunks that a unit is dealt as behind its own
+// The end of a segment (a range of one unit's keys) takes as long as so many chunks: a unit
+// is dealt as so many more, behind its own, so that a CTA with two segments has fewer
+// chunks (pairs, 32 sequences of 8192 rows: 98.4 to 96.4 us; 8 units of 16384 keys: 20.0 to
+// 19.5 us).
+constexpr int paged_segment(int cluster) { return cluster == 2 ? 3 : 1; }
 // Whether page tables with room for that many keys are dealt in whole units, without a
 // merge.  Whole and split, us: 8 units of 128 channels 8.5 and 8.4 at 512 keys, 10.2 and
 // 8.6 at 704; 64 units 10.3 and 12.3 at 704, 13.3 and 12.6 at 1024; latent rows, 1 unit

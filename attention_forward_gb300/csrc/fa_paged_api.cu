@@ -48,10 +48,11 @@ bool paged_attn_whole(int kind, long long units, int room, int sm_count) {
 }
 
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count) {
-  const long long chunks = units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys);
+  const int cluster = paged_attn_cluster(kind, rows);
+  const long long chunks =
+      units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys + paged_segment(cluster));
   const long long most = paged_attn_whole(kind, units, room, sm_count)
                              ? units : (chunks + kPagedMinChunks - 1) / kPagedMinChunks;
-  const int cluster = paged_attn_cluster(kind, rows);
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
                           paged_attn_ctas(kind, paged_attn_row_block(kind, rows)) / cluster;
   return static_cast<int>(most < slots ? most : slots) * cluster;
@@ -150,7 +151,8 @@ bool chunks_ok(int kind, int B, int H, int Hkv, int Sq, const PageShape& s) {
   const long long rows = static_cast<long long>(H / Hkv) * Sq;
   const int block = fa::paged_attn_row_block(kind, static_cast<int>(rows));
   const long long chunks = (static_cast<long long>(s.max_pages) * s.page_size +
-                            fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys + fa::kPagedMaxSegment;
+                            fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys +
+                           fa::paged_segment(fa::paged_attn_cluster(kind, static_cast<int>(rows)));
   return static_cast<long long>(B) * Hkv * ((rows + block - 1) / block) * chunks <= fa::kCacheMaxChunks;
 }
 

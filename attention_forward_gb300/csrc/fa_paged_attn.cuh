@@ -56,11 +56,7 @@ struct PagedShape {
   static constexpr int kStageBytes = kTileK + kTileV;
   static constexpr int kVTile = kShared ? kTileK : kTileV;       // from a tile's V to the next
   static constexpr int kVStride = (kShared ? kKC : kVC) * 1024;  // from 8 keys to the next 8
-  // The end of a segment takes as long as so many chunks: a unit is dealt as so many more,
-  // behind its own, so that a CTA with two segments has fewer chunks (pairs, 32 sequences
-  // of 8192 rows: 98.5 to 96 us; one sequence of 16384 keys: 20.3 to 19.7 us).
-  static constexpr int kSegment = kCluster == 2 ? 3 : 1;
-  static_assert(kSegment <= kPagedMaxSegment, "the check of the deal's chunks");
+  static constexpr int kSegment = paged_segment(kCluster);
   static constexpr int kQBytes = kN * 128 * kKC;
   static constexpr int kPBytes = kN * 128;
   static constexpr int kBlocks = kVC == 1 ? 1 : kVC / 2;  // O^T in blocks of 128 channels (64)

@@ -465,7 +465,7 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
  *
  * fa_fwd_paged -- attention of the newest tokens over the pages: fa_fwd_cache
  * with 16-bit keys and values.  Its arguments, limits (row blocks of 16 rows up
- * to (H / Hkv) * Sq = 16, else of 64, each counted with three chunks more),
+ * to (H / Hkv) * Sq = 16, else of 64, each counted with one chunk more),
  * workspace rules and masks are fa_fwd_cache's; a probability is rounded to the type of V for the product.  V
  * must be finite within a sequence's length; what lies past it may be anything.
  */
