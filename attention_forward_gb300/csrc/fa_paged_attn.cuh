@@ -28,6 +28,12 @@
 // The tensor core runs S(j + 1) while the softmax works on S(j), when the tile is
 // there: warp 4 takes whichever of S(j + 1) and O(j) is ready first.
 //
+// Bound, and measured (in a CUDA graph, merge included): 32 sequences of 8192 keys, 8 kv
+// heads of 128 channels, by HBM: 139 us, 6.4 TB/s; latent rows, 64 sequences of 4096 and
+// 16 heads, by HBM between 13 us of start, end and merge: 54.5 us; 32 of 8192 and 128
+// heads 96.5 us: a tile of 64 keys takes 2700 cycles where its products take 2040, for two
+// tiles and the queries fill shared memory and a tile is reloaded only behind its product.
+//
 // Every wait is bounded by the watchdog, as in the prefill kernels.
 #pragma once
 #include "fa_keys.cuh"

@@ -454,7 +454,8 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
  *   freqs  [rotary / 2] fp32 radians a position: the first `rotary` channels
  *          of a query's or key's head (a multiple of 16, up to D) are pairs
  *          (x, y) that become (x cos a - y sin a, y cos a + x sin a), a = n *
- *          freqs[j].  NULL with rotary 0: nothing is rotated.
+ *          freqs[j].  NULL with rotary 0: nothing is rotated.  Finite, and below
+ *          2^64 in magnitude: what is not turns nothing.
  *   interleaved  0: pair j is channels j, j + rotary / 2; 1: 2 j, 2 j + 1
  * The angle is exact to 2^-28 radian up to n = 2^24 and freqs[j] = 1 (and in
  * proportion above); a rotated value is rounded once to its type behind fp32
