@@ -127,14 +127,15 @@ __global__ void __launch_bounds__(kPagedCopyThreads, kLat ? 4 : 3)
   };
 
   uint4 x[kPagedAtOnce], y[kPagedAtOnce];
-  // (rows past the count are there all the same: the first words need not wait for it)
+  // (rows past the count are there all the same: the first words need not wait for it.
+  // From L2: the kernel may have started while the one that wrote them ran.)
   auto load = [&]() {
 #pragma unroll
     for (int k = 0; k < kPagedAtOnce; ++k)
       if (h + k * step < h1 && token < p.S) {
         const uint4* in = source(h + k * step);
-        x[k] = __ldcs(in + w0);
-        y[k] = __ldcs(in + w1);
+        x[k] = __ldcg(in + w0);
+        y[k] = __ldcg(in + w1);
       }
   };
   load();

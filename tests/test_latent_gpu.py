@@ -243,3 +243,21 @@ def test_two_streams_and_a_graph_at_once():
     ok()
     for o, lse in got:
         assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("H,L", [(5, 70), (20, 900), (40, 100), (80, 900), (65, 100)])
+def test_rows_of_other_sequences_stay_out(H, L, value):
+    """The heads are fewer than a tile (or a pair's two) holds, whose other rows are the
+    next sequence's: whatever they are, a row has the same bits."""
+    B = 3
+    cache, table, _, _ = cache_of(B, L, 16, "bf16", 40)
+    length = ints([L, L - 7, L // 3])
+    q = normal(41, B, H, 1, 576).bfloat16()
+    o, lse = fa.fa_fwd_latent(q, cache, table, length)
+    for b in range(B):
+        other = torch.full_like(q, value)
+        other[b] = q[b]
+        o2, lse2 = fa.fa_fwd_latent(other, cache, table, length)
+        assert torch.equal(o2[b], o[b]) and torch.equal(lse2[b], lse[b])
+    ok()

@@ -442,3 +442,43 @@ def test_prompt_decode_and_a_further_chunk(D, dt):
             paged_ref.close(cache[0][pg, :, slot:slot + 1], *paged_ref.rotate(k1[b], at, freqs, False))
         ops_ref.check(o1, l1, paged_ref.newest(q1r, *cache, table, length, D ** -0.5, cap))
     assert length.tolist() == [S + 21, 122]
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("H,Hkv,Sq,L", [(5, 1, 1, 70), (6, 2, 1, 1500), (10, 2, 3, 1500), (20, 1, 1, 900)])
+def test_rows_of_other_heads_stay_out(H, Hkv, Sq, L, value):
+    """The rows of a head group are fewer than a tile holds, whose others are the next
+    group's or sequence's: whatever they are, a row has the same bits."""
+    B = 3
+    cache, table, _, _ = cache_of(B, L, Hkv, 16, 64, "bf16", 40)
+    length = ints([L, L - 7, L // 3])
+    q = normal(41, B, H, Sq, 64).bfloat16()
+    o, lse = fa.fa_fwd_paged(q, cache, table, length)
+    for b in range(B):
+        for g in range(Hkv):
+            heads = slice(g * H // Hkv, (g + 1) * H // Hkv)
+            other = torch.full_like(q, value)
+            other[b, heads] = q[b, heads]
+            o2, lse2 = fa.fa_fwd_paged(other, cache, table, length)
+            assert torch.equal(o2[b, heads], o[b, heads]) and torch.equal(lse2[b, heads], lse[b, heads])
+    ok()
+
+
+def test_copies_that_follow_each_other():
+    """A write, a read into a buffer, a write of the buffer and its read, over and over on
+    one stream with other values: each sees what the one before it wrote."""
+    B, Hkv, S, n = 2, 2, 200, 30
+    a, b = (fa.fa_paged_empty(32, Hkv, 16, 64, torch.float16) for _ in range(2))
+    table = table_of(B, 13, 32)
+    rows = [[normal(50 + 2 * i + j, B, Hkv, S, 64).half() for j in range(2)] for i in range(n)]
+    got = [[torch.empty_like(x) for x in r] for r in rows]
+    buf = [torch.empty_like(x) for x in rows[0]]
+    torch.cuda.synchronize()
+    for i in range(n):
+        fa.fa_paged_write(*rows[i], a, table)
+        fa.fa_paged_read(a, table, out=buf)
+        fa.fa_paged_write(*buf, b, table)
+        fa.fa_paged_read(b, table, out=got[i])
+    ok()
+    for r, g in zip(rows, got):
+        assert torch.equal(r[0], g[0]) and torch.equal(r[1], g[1])
