@@ -562,8 +562,9 @@ fa_status_t fa_fwd_expanded(const void *q, const void *kv, const void *k_rope,
  * fa_release_workspaces -- frees the workspaces that fa_fwd, fa_fwd_score,
  * fa_fwd_cache, fa_fwd_paged, fa_fwd_latent and fa_fwd_expanded keep on the
  * current device (one per stream that they were called on), after
- * synchronising the device.  The next call that needs one allocates it again.  Returns FA_ERR_CUDA if the synchronisation or a free
- * failed (the cache is emptied either way).
+ * synchronising the device.  The next call that needs one allocates it again.
+ * Returns FA_ERR_CUDA if the synchronisation or a free failed (the cache is
+ * emptied either way).
  */
 fa_status_t fa_release_workspaces(void);
 
