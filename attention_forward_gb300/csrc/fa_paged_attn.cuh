@@ -14,25 +14,28 @@
 // type of V for its product.
 //
 // Warps:
-//   0-3  softmax: a warp's 16 keys of the tile as mma fragments (16x256b loads),
-//        one reference maximum a row, raised for the whole CTA when a score passes it
-//        by 15 (log2 units; then O is rescaled in place), set 8 below the maximum so
-//        that fp16 holds p over 2^-24 ... 2^15 around it; p goes to shared memory
-//        transposed (stmatrix).  They also send for a segment's queries (TMA: by the warps
-//        themselves 128 rows of 576 channels took 9 us) and write its O.
-//   4    MMA issue, tensor memory
-//   5, 6 TMA producers, of K and of V (one for latent rows): rings of tiles, by boxes of
-//        8 rows (all channels): any page size is a multiple of them.  A box past the
+//   4 softmax, a group, or 8, two groups with half of 64 rows each (one group: 64 latent
+//        heads over 1024 keys 13.7 us, two 12.2): a warp's 16 keys of the tile as mma
+//        fragments (16x256b loads), one reference maximum a row, raised for the whole
+//        group when a score passes it by 15 (log2 units; then O is rescaled in place),
+//        set 8 below the maximum so that fp16 holds p over 2^-24 ... 2^15 around it; p
+//        goes to shared memory transposed (stmatrix).  They also send for a segment's
+//        queries (TMA: by the warps themselves 128 rows of 576 channels took 9 us) and
+//        write its O.
+//   1 MMA issue, tensor memory
+//   1 or 2 TMA producers, of K and of V (one for latent rows): rings of tiles, by boxes
+//        of 8 rows (all channels): any page size is a multiple of them.  A box past the
 //        sequence or of a page that does not exist is fetched from past the pool's end,
 //        as zeros.
 // The tensor core runs S(j + 1) while the softmax works on S(j), when the tile is
-// there: warp 4 takes whichever of S(j + 1) and O(j) is ready first.
+// there: the issuing warp takes whichever of S(j + 1) and O(j) is ready first.
 //
 // Bound, and measured (in a CUDA graph, merge included): 32 sequences of 8192 keys, 8 kv
 // heads of 128 channels, by HBM: 139 us, 6.4 TB/s; latent rows, 64 sequences of 4096 and
 // 16 heads, by HBM between 13 us of start, end and merge: 54.5 us; 32 of 8192 and 128
-// heads 96.5 us: a tile of 64 keys takes 2700 cycles where its products take 2040, for two
-// tiles and the queries fill shared memory and a tile is reloaded only behind its product.
+// heads 95.5 us: a tile of 64 keys takes 2700 cycles where its products take 2040, for two
+// tiles and the queries fill shared memory, a tile is reloaded only behind its product, and
+// arrives 1500 cycles later.
 //
 // Every wait is bounded by the watchdog, as in the prefill kernels.
 #pragma once
@@ -55,7 +58,10 @@ struct PagedShape {
   static constexpr int kPs = kPs_;  // buffers for P
   static constexpr int kCluster = kCluster_;
   static constexpr bool kShared = kShared_;
-  static constexpr int kWarps = kShared ? 6 : 7, kThreads = 32 * kWarps;
+  // groups of four softmax warps, each with its share of the query rows
+  static constexpr int kGroups = kN == 64 ? 2 : 1, kRows = kN / kGroups;
+  static constexpr int kMmaWarp = 4 * kGroups;
+  static constexpr int kWarps = kMmaWarp + (kShared ? 2 : 3), kThreads = 32 * kWarps;
   static constexpr int kDv = 64 * kVC;
   static constexpr int kTileK = kPagedKeys * 128 * kKC;
   static constexpr int kTileV = kShared ? 0 : kPagedKeys * 128 * kVC;
@@ -194,7 +200,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     fa_paged_attn_kernel(const __grid_constant__ CUtensorMap tmQ,
                          const __grid_constant__ CUtensorMap tmK,
                          const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
-  constexpr int kN = S::kN, kNB = kN / 8, kStages = S::kStages;
+  constexpr int kN = S::kN, kRows = S::kRows, kNB = kRows / 8, kStages = S::kStages;
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kBelow = 8.f, kTau = 15.f;
   constexpr float kNone = -3.0e38f;  // below every score that counts; -inf - kNone is -inf
@@ -221,8 +227,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     }
     mbar_init(s_full, 1);
     mbar_init(s_full + 8, 1);
-    mbar_init(p_ready, 4);
-    mbar_init(p_ready + 8, 4);
+    mbar_init(p_ready, 4 * S::kGroups);
+    mbar_init(p_ready + 8, 4 * S::kGroups);
     mbar_init(o_done, 1);
     mbar_init(o_done + 8, 1);
     mbar_init(q_full, 1);
@@ -230,11 +236,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     sm.abort = 0u;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == S::kMmaWarp) {
     tmem_alloc(smem_u32(&sm.tmem), S::kTmemCols);
     tmem_relinquish();
   }
-  if (warp == 5 && lane == 0) {
+  if (warp == S::kMmaWarp + 1 && lane == 0) {
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     if constexpr (!S::kShared) tma_prefetch_desc(&tmV);
@@ -269,14 +275,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   walk.cur = walk.first;
   PagedSeg seg;
 
-  if (warp < 4) {
+  if (warp < S::kMmaWarp) {
     // ================================ softmax ================================
+    // rows row0 ... row0 + kRows of the CTA's are this group's; they meet at its barrier
     const int g = lane >> 2, t4 = lane & 3;
-    const uint32_t t_lane = static_cast<uint32_t>(warp * 32) << 16;
+    const int wq = warp & 3, tid = static_cast<int>(threadIdx.x) & 127, row0 = (warp >> 2) * kRows;
+    const uint32_t group_bar = 1u + static_cast<uint32_t>(warp >> 2);
+    const uint32_t t_lane = static_cast<uint32_t>(wq * 32) << 16;
     // this lane's address of a transposed store of two blocks of 8 rows: row (lane /
-    // 16) * 8 + lane % 8, keys 16 warp + 8 (lane / 8 % 2)
-    const uint32_t p_at = sP + static_cast<uint32_t>(((lane >> 4) * 8 + (lane & 7)) * 128 +
-                                                     (((2 * warp + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+    // 16) * 8 + lane % 8, keys 16 wq + 8 (lane / 8 % 2)
+    const uint32_t p_at = sP + static_cast<uint32_t>((row0 + (lane >> 4) * 8 + (lane & 7)) * 128 +
+                                                     (((2 * wq + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
     const float fac = kMod && p.cap > 0.f ? p.scale : p.scale * kLog2e;
     uint32_t t = 0, nq = 0;  // tiles, and loads of queries, so far
     bool ok = true;
@@ -298,14 +307,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     while (more) {
       if (p.whole && threadIdx.x == 0 && seg.len != p.length[seg.seq])
         atomicMax(p.status, kStatusBadIndex);
-      for (int n = threadIdx.x; n < kN; n += 128) {
+      for (int n = row0 + tid; n < row0 + kRows; n += 128) {
         const int rr = min(min(n, seg.n_rows - 1) + seg.row0, p.rows - 1);
         const int h = rr / p.Sq, i = rr - h * p.Sq;
         sm.limit[n] = n < seg.n_rows ? seg.len - (p.Sq - 1 - i) : seg.len;
         if constexpr (kMod)
           sm.slope[n] = p.slopes ? p.slopes[seg.hk * (p.H / p.Hkv) + h] * kLog2e : 0.f;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(group_bar, 128);
       const int least = seg.len - (p.Sq - 1);
       float m[kNB][2], l[kNB][2];
 #pragma unroll
@@ -318,7 +327,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         ok = ok && wait_bar_warp(s_full + 8 * buf, (t >> 1) & 1u, ctl);
         tc_fence_after();
         uint32_t raw[kNB][4];
-        tmem_ld_frag(tmem + t_lane + buf * kN, raw);
+        tmem_ld_frag(tmem + t_lane + buf * kN + row0, raw);
         const uint32_t bad = sm.bad[t % kPagedBad];
         tmem_wait_ld();
         float s[kNB][4];
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             ffma2(s[n][e], s[n][e + 1], __uint_as_float(raw[n][e]), __uint_as_float(raw[n][e + 1]), fac,
                   fac, 0.f, 0.f);
           }
-        const int k0 = key0 + 16 * warp + g;  // this lane's keys: k0, k0 + 8
+        const int k0 = key0 + 16 * wq + g;  // this lane's keys: k0, k0 + 8
         if constexpr (kMod) {
 #pragma unroll
           for (int n = 0; n < kNB; ++n)
@@ -338,19 +347,19 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             for (int e = 0; e < 4; ++e) {
               if (p.cap > 0.f) s[n][e] = cap_score(s[n][e], p) * kLog2e;
               if (p.slopes) {
-                const int row = 8 * n + 2 * t4 + (e & 1);
+                const int row = row0 + 8 * n + 2 * t4 + (e & 1);
                 s[n][e] = fmaf(-sm.slope[row],
                                static_cast<float>(abs(sm.limit[row] - 1 - k0 - 8 * (e >> 1))), s[n][e]);
               }
             }
         }
         if (key0 + kPagedKeys > least || bad != 0u) {
-          const bool off[2] = {((bad >> (2 * warp)) & 1u) != 0u, ((bad >> (2 * warp + 1)) & 1u) != 0u};
+          const bool off[2] = {((bad >> (2 * wq)) & 1u) != 0u, ((bad >> (2 * wq + 1)) & 1u) != 0u};
 #pragma unroll
           for (int n = 0; n < kNB; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (off[e >> 1] || k0 + 8 * (e >> 1) >= sm.limit[8 * n + 2 * t4 + (e & 1)])
+              if (off[e >> 1] || k0 + 8 * (e >> 1) >= sm.limit[row0 + 8 * n + 2 * t4 + (e & 1)])
                 s[n][e] = -INFINITY;
           // slots past the sequence may hold anything: zeros where they share 8
           // rows with its last (their scores are read, whose operand they were)
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             if constexpr (!S::kShared) ok = ok && wait_bar_warp(v_full + 8 * stage, (t / kStages) & 1u, ctl);
             const uint32_t rows = sV + stage * S::kVTile +
                                   static_cast<uint32_t>((seg.len - key0) >> 3) * S::kVStride;
-            for (int i = threadIdx.x; i < (8 - tail) * S::kVC * 8; i += 128) {
+            for (int i = threadIdx.x; i < (8 - tail) * S::kVC * 8; i += 128 * S::kGroups) {
               const int r = tail + i / (S::kVC * 8), c = i % (S::kVC * 8);
               st_shared_v4(rows + static_cast<uint32_t>((c >> 3) * 1024 + r * 128 + (c & 7) * 16), 0u,
                            0u, 0u, 0u);
@@ -382,9 +391,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         // exponentials (a segment's first ones: its end waited)
         const uint32_t p_free = o_done + 8 * ((t - S::kPs) & 1u), p_par = ((t - S::kPs) >> 1) & 1u;
         const bool free_now = j < S::kPs || mbar_test_wait(p_free, p_par);
-        if (named_bar_or(1, 128, over > kTau || !ok)) {
+        if (named_bar_or(group_bar, 128, over > kTau || !ok)) {
           // rare: a row's reference rises, or a wait ran out somewhere
-          if (named_bar_or(1, 128, !ok)) {
+          if (named_bar_or(group_bar, 128, !ok)) {
             ok = false;
             break;
           }
@@ -396,14 +405,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-              if (g == 0) sm.red[warp][8 * n + 2 * t4 + c] = top;
+              if (g == 0) sm.red[wq][row0 + 8 * n + 2 * t4 + c] = top;
             }
-          named_bar_sync(1, 128);
+          named_bar_sync(group_bar, 128);
 #pragma unroll
           for (int n = 0; n < kNB; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              const int row = 8 * n + 2 * t4 + c;
+              const int row = row0 + 8 * n + 2 * t4 + c;
               const float top = fmaxf(fmaxf(sm.red[0][row], sm.red[1][row]),
                                       fmaxf(sm.red[2][row], sm.red[3][row]));
               float a = 1.f;
@@ -412,22 +421,24 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
                 m[n][c] = top - kBelow;
                 l[n][c] *= a;
               }
-              if (warp == 0 && g == 0) sm.factor[row] = a;
+              if (wq == 0 && g == 0) sm.factor[row] = a;
             }
-          named_bar_sync(1, 128);
+          named_bar_sync(group_bar, 128);
           if (j > 0) {
             ok = wait_bar_warp(o_done + 8 * ((t - 1) & 1u), ((t - 1) >> 1) & 1u, ctl);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < S::kBlocks * kN; c += 16) {
+            for (int c = 0; c < S::kBlocks * kRows; c += 16) {
+              const int row = row0 + c % kRows;
+              const uint32_t at = tmem + t_lane + S::kColO + c / kRows * kN + row;
               uint32_t v[16];
-              tmem_ld16(tmem + t_lane + S::kColO + c, v);
+              tmem_ld16(at, v);
               tmem_wait_ld();
               reg_fence16(v);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
-                v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.factor[(c + e) % kN]);
-              tmem_st16(tmem + t_lane + S::kColO + c, v);
+                v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.factor[row + e]);
+              tmem_st16(at, v);
             }
             tmem_wait_st();
           }
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       }
 
       // ---- the segment's end: sums over the keys, then O^T out ----
-      ok = !named_bar_or(1, 128, !ok);
+      ok = !named_bar_or(group_bar, 128, !ok);
       if (!ok) break;
       // the next segment's queries first: its scores run beside what follows
       more = paged_next<S>(p, walk, next);
@@ -470,12 +481,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           sum += __shfl_xor_sync(0xffffffffu, sum, 8);
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
           if (g == 0) {
-            sm.red[warp][8 * n + 2 * t4 + c] = sum;
-            if (warp == 0) sm.top[8 * n + 2 * t4 + c] = m[n][c];
+            sm.red[wq][row0 + 8 * n + 2 * t4 + c] = sum;
+            if (wq == 0) sm.top[row0 + 8 * n + 2 * t4 + c] = m[n][c];
           }
         }
-      named_bar_sync(1, 128);
-      for (int n = threadIdx.x; n < kN; n += 128) {
+      named_bar_sync(group_bar, 128);
+      for (int n = row0 + tid; n < row0 + kRows; n += 128) {
         const float sum = (sm.red[0][n] + sm.red[1][n]) + (sm.red[2][n] + sm.red[3][n]);
         sm.factor[n] = sum == 0.f ? 0.f : 1.f / sum;  // no visible key: 0; a NaN stays one
         if (n < seg.n_rows) {
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
             p.part_lse[static_cast<long long>(seg.part) * kN + n] = lse;
         }
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(group_bar, 128);
       if (seg.n_tiles > 0) {
         ok = wait_bar_warp(o_done + 8 * ((t - 1) & 1u), ((t - 1) >> 1) & 1u, ctl);
         tc_fence_after();
@@ -496,18 +507,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
       float inv[kNB][2];
 #pragma unroll
       for (int n = 0; n < kNB; ++n) {
-        inv[n][0] = sm.factor[8 * n + 2 * t4];
-        inv[n][1] = sm.factor[8 * n + 2 * t4 + 1];
+        inv[n][0] = sm.factor[row0 + 8 * n + 2 * t4];
+        inv[n][1] = sm.factor[row0 + 8 * n + 2 * t4 + 1];
       }
-      const uint32_t out_at = sP + static_cast<uint32_t>(warp * kN * 32);
+      const uint32_t out_at = sP + static_cast<uint32_t>(warp * kRows * 32);
       constexpr int kHalves = S::kVC == 1 ? 1 : 2;  // with 64 channels a warp has 16
 #pragma unroll 1
       for (int i = 0; i < S::kBlocks * kHalves; ++i) {
         const int blk = i / kHalves, half = i % kHalves;
-        const int ch0 = blk * 128 + 16 * (kHalves * warp + half);
+        const int ch0 = blk * 128 + 16 * (kHalves * wq + half);
         uint32_t v[kNB][4];
         if (seg.n_tiles > 0) {
-          tmem_ld_frag(tmem + t_lane + (static_cast<uint32_t>(half) << 20) + S::kColO + blk * kN, v);
+          tmem_ld_frag(tmem + t_lane + (static_cast<uint32_t>(half) << 20) + S::kColO + blk * kN + row0, v);
           tmem_wait_ld();
         }
         float x[kNB][4];
@@ -528,25 +539,26 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
                             pack2<BF16>(x[n + 1][0], x[n + 1][1]), pack2<BF16>(x[n + 1][2], x[n + 1][3]));
           __syncwarp();
 #pragma unroll
-          for (int k = 0; k < kN / 16; ++k) {
+          for (int k = 0; k < kRows / 16; ++k) {
             const int row = 16 * k + (lane >> 1), c = lane & 1;
             uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
                          : "r"(out_at + row * 32 + ((c ^ ((row >> 2) & 1)) << 4)));
-            if (row < seg.n_rows)
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (seg.out_row0 + row) * S::kDv +
-                                        ch0 + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (row0 + row < seg.n_rows)
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) +
+                                        (seg.out_row0 + row0 + row) * S::kDv + ch0 + 8 * c) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
         } else {
           // a lane's values of a channel next to each other (paged_part_row)
-          float* part = p.part_o + (static_cast<long long>(seg.part) * S::kDv + ch0 + g) * p.part_rows;
+          float* part =
+              p.part_o + (static_cast<long long>(seg.part) * S::kDv + ch0 + g) * p.part_rows + row0;
           const int down = 8 * p.part_rows;
           if constexpr (kN >= 32) {
 #pragma unroll
             for (int n = 0; n < kNB; n += 4)
-              if (8 * n < p.part_rows) {
+              if (row0 + 8 * n < p.part_rows) {
                 st_global_v8(part + 8 * n + 8 * t4, x[n][0], x[n][1], x[n + 1][0], x[n + 1][1],
                              x[n + 2][0], x[n + 2][1], x[n + 3][0], x[n + 3][1]);
                 st_global_v8(part + down + 8 * n + 8 * t4, x[n][2], x[n][3], x[n + 1][2], x[n + 1][3],
@@ -563,12 +575,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         }
       }
       tc_fence_before();
-      if (named_bar_or(1, 128, !ok)) break;
+      if (named_bar_or(group_bar, 128, !ok)) break;
       seg = next;
     }
     // queries sent for land before shared memory goes away
     if (nq > 0) wait_drain(q_full, (nq - 1) & 1u, p.timeout_ns);
-  } else if (warp == 4) {
+  } else if (warp == S::kMmaWarp) {
     // =============================== MMA issue ===============================
     constexpr uint32_t kIdescS = idesc_f16(BF16, false, false, 64, kN);
     constexpr uint32_t kIdescO = idesc_f16(BF16, true, false, S::kVC == 1 ? 64 : 128, kN);
@@ -669,8 +681,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     __syncwarp();
   } else {
     // =============================== producers ===============================
-    // warp 5 the keys, warp 6 the values
-    const bool is_k = warp == 5;
+    // the first the keys, the second the values
+    const bool is_k = warp == S::kMmaWarp + 1;
     const uint32_t full0 = is_k ? k_full : v_full, empty0 = is_k ? k_empty : v_empty;
     const uint32_t bytes = is_k ? S::kTileK : S::kTileV;
     const uint32_t ring = (is_k ? sK : sV) + (lane & 7) * ((is_k ? S::kKC : S::kVC) * 1024);
@@ -751,7 +763,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == S::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
