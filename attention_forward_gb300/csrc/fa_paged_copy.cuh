@@ -15,10 +15,10 @@
 // registers, made once by the block.
 //
 // Measured, 4 x 4096 tokens, in a graph: 32 + 8 + 8 heads of 128 channels written and read
-// back in 55.2 us (5.5 TB/s), latent rows and 16 heads in 22.7 (3.6 TB/s: 1024 blocks,
+// back in 54.1 us (5.6 TB/s), latent rows and 16 heads in 22.7 (3.6 TB/s: 1024 blocks,
 // of which 608 run at once).  Rows in flight a thread, write and latent write: 2 at five
 // and six blocks an SM 63 and 28 us, 3 at four and five 54.5 and 26, 4 at three and four
-// 55.3 and 22.6.  A token of 32 sequences: 2.5 us, three loads one behind the other.
+// 55.3 and 22.6.  A token of 32 sequences: 2.2 us, three loads one behind the other.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
