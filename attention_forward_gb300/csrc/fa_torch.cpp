@@ -151,14 +151,19 @@ bool latent_rows(const at::Tensor* c, const at::Tensor* r) {
          is(r, c->scalar_type(), c->get_device(), {c->size(0), c->size(1), kRope});
 }
 
-// The call without the interpreter's lock; true where its work is in the stream.
-template <class Call>
-bool launched(Call call) {
-  fa_status_t st;
-  Py_BEGIN_ALLOW_THREADS
-  st = call();
-  Py_END_ALLOW_THREADS
-  return st == FA_OK;
+// The interpreter's lock given up, and back however the scope is left.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// A call of the library without the interpreter's lock; true where its work is in the
+// stream.  The arguments are evaluated by the caller, under the lock: a tensor without
+// storage (under torch.vmap and the like) throws where its address is asked for.
+template <class Call, class... Args>
+bool launched(Call call, Args... args) {
+  Unlocked unlocked;
+  return call(args...) == FA_OK;
 }
 
 // Torch's errors (no memory, tensors without storage) are fa.py's to meet again.
@@ -207,12 +212,10 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else if (!number(a[4], &scale))
       return not_taken();
     at::Tensor o = at::empty_like(*q), lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched([&] {
-      return lib.fwd_paged(q->data_ptr(), k, v, p.table, p.start, o.data_ptr(),
-                           static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Hkv), n32(Sq), n32(D),
-                           p.num, p.size, p.max, static_cast<float>(scale), dtype_of(*q),
-                           static_cast<float>(cap), slopes, nullptr, 0, stream_of(*q));
-    });
+    const bool ok = launched(lib.fwd_paged, q->data_ptr(), k, v, p.table, p.start, o.data_ptr(),
+                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Hkv), n32(Sq), n32(D),
+                             p.num, p.size, p.max, static_cast<float>(scale), dtype_of(*q),
+                             static_cast<float>(cap), slopes, nullptr, 0, stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
   });
 }
@@ -231,11 +234,9 @@ PyObject* fwd_latent(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return not_taken();
     at::Tensor o = at::empty({B, H, Sq, kLatent}, q->options());
     at::Tensor lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched([&] {
-      return lib.fwd_latent(q->data_ptr(), pool, p.table, p.start, o.data_ptr(),
-                            static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), p.num, p.size,
-                            p.max, static_cast<float>(scale), dtype_of(*q), nullptr, 0, stream_of(*q));
-    });
+    const bool ok = launched(lib.fwd_latent, q->data_ptr(), pool, p.table, p.start, o.data_ptr(),
+                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), p.num, p.size,
+                             p.max, static_cast<float>(scale), dtype_of(*q), nullptr, 0, stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
   });
 }
@@ -255,12 +256,10 @@ PyObject* fwd_expanded(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return not_taken();
     at::Tensor o = at::empty({B, H, Sq, kNope}, q->options());
     at::Tensor lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched([&] {
-      return lib.fwd_expanded(q->data_ptr(), kv->data_ptr(), r->data_ptr(), o.data_ptr(),
-                              static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), n32(Skv),
-                              static_cast<float>(scale), a[3] == Py_True, dtype_of(*q), nullptr, 0,
-                              stream_of(*q));
-    });
+    const bool ok = launched(lib.fwd_expanded, q->data_ptr(), kv->data_ptr(), r->data_ptr(), o.data_ptr(),
+                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), n32(Skv),
+                             static_cast<float>(scale), a[3] == Py_True, dtype_of(*q), nullptr, 0,
+                             stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
   });
 }
@@ -300,11 +299,9 @@ PyObject* paged_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
       q = t->data_ptr();
       q_out = o->data_ptr();
     }
-    const bool ok = launched([&] {
-      return lib.paged_write(q, k->data_ptr(), v->data_ptr(), q_out, kp, vp, p.table, p.start, p.count, freqs,
-                             n32(rotary), a[7] == Py_True, n32(B), n32(H), n32(Hkv), n32(S), n32(D), p.num,
-                             p.size, p.max, dtype_of(*k), stream_of(*k));
-    });
+    const bool ok = launched(lib.paged_write, q, k->data_ptr(), v->data_ptr(), q_out, kp, vp, p.table,
+                             p.start, p.count, freqs, n32(rotary), a[7] == Py_True, n32(B), n32(H),
+                             n32(Hkv), n32(S), n32(D), p.num, p.size, p.max, dtype_of(*k), stream_of(*k));
     if (!ok) return not_taken();
     Py_RETURN_NONE;
   });
@@ -324,10 +321,9 @@ PyObject* paged_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!is(v, k->scalar_type(), dev, k->sizes()) || !pools(a[0], *k, Hkv, D, &kp, &vp, &p) ||
         !places(a[1], a[2], a[3], dev, B, &p))
       return not_taken();
-    const bool ok = launched([&] {
-      return lib.paged_read(kp, vp, p.table, p.start, p.count, k->data_ptr(), v->data_ptr(), n32(B), n32(Hkv),
-                            n32(S), n32(D), p.num, p.size, p.max, dtype_of(*k), stream_of(*k));
-    });
+    const bool ok = launched(lib.paged_read, kp, vp, p.table, p.start, p.count, k->data_ptr(),
+                             v->data_ptr(), n32(B), n32(Hkv), n32(S), n32(D), p.num, p.size, p.max,
+                             dtype_of(*k), stream_of(*k));
     if (!ok) return not_taken();
     Py_RETURN_NONE;
   });
@@ -360,11 +356,9 @@ PyObject* latent_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
       q_rope = t->data_ptr();
       q = o->data_ptr();
     }
-    const bool ok = launched([&] {
-      return lib.latent_write(c->data_ptr(), r->data_ptr(), pool, q_rope, q, p.table, p.start, p.count, freqs,
-                              a[7] == Py_True, n32(B), n32(H), n32(S), n32(width), p.num, p.size, p.max,
-                              dtype_of(*c), stream_of(*c));
-    });
+    const bool ok = launched(lib.latent_write, c->data_ptr(), r->data_ptr(), pool, q_rope, q, p.table,
+                             p.start, p.count, freqs, a[7] == Py_True, n32(B), n32(H), n32(S), n32(width),
+                             p.num, p.size, p.max, dtype_of(*c), stream_of(*c));
     if (!ok) return not_taken();
     Py_RETURN_NONE;
   });
@@ -381,10 +375,9 @@ PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pool;
     if (!latent_pool(a[0], *c, &pool, &p) || !places(a[1], a[2], a[3], c->get_device(), c->size(0), &p))
       return not_taken();
-    const bool ok = launched([&] {
-      return lib.latent_read(pool, p.table, p.start, p.count, c->data_ptr(), r->data_ptr(), n32(c->size(0)),
-                             n32(c->size(1)), p.num, p.size, p.max, dtype_of(*c), stream_of(*c));
-    });
+    const bool ok = launched(lib.latent_read, pool, p.table, p.start, p.count, c->data_ptr(), r->data_ptr(),
+                             n32(c->size(0)), n32(c->size(1)), p.num, p.size, p.max, dtype_of(*c),
+                             stream_of(*c));
     if (!ok) return not_taken();
     Py_RETURN_NONE;
   });
