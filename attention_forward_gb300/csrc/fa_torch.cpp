@@ -18,6 +18,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
+#include <stdexcept>
 
 #include "../../include/fa.h"
 
@@ -41,6 +42,14 @@ PyObject* not_taken() { Py_RETURN_NOTIMPLEMENTED; }
 // The tensor behind an argument; null where it is none of torch's own.
 const at::Tensor* tensor(PyObject* o) {
   return THPVariable_CheckExact(o) ? &THPVariable_Unpack(o) : nullptr;
+}
+
+// A tensor's memory.  Throws where it has none: its address would be taken for that of an
+// argument left out (a tensor under torch.func.functionalize is at 0).
+void* memory(const at::Tensor& t) {
+  void* at = t.data_ptr();
+  if (!at && t.numel() > 0) throw std::invalid_argument("a tensor without memory");
+  return at;
 }
 
 // A contiguous tensor of that type, device and shape.
@@ -72,7 +81,7 @@ bool optional(PyObject* o, c10::ScalarType type, int dev, int64_t n, const T** o
   if (o == Py_None) return true;
   const at::Tensor* t = tensor(o);
   if (!is(t, type, dev, {n})) return false;
-  *out = static_cast<const T*>(t->data_ptr());
+  *out = static_cast<const T*>(memory(*t));
   return true;
 }
 
@@ -113,7 +122,7 @@ struct Pages {
 bool places(PyObject* table, PyObject* start, PyObject* count, int dev, int64_t B, Pages* p) {
   const at::Tensor* t = tensor(table);
   if (!t || t->dim() != 2 || !is(t, at::kInt, dev, {B, t->size(1)}) || !all_fit(*t)) return false;
-  p->table = static_cast<const int*>(t->data_ptr());
+  p->table = static_cast<const int*>(memory(*t));
   p->max = static_cast<int>(t->size(1));
   return optional(start, at::kInt, dev, B, &p->start) && optional(count, at::kInt, dev, B, &p->count);
 }
@@ -127,8 +136,8 @@ bool pools(PyObject* cache, const at::Tensor& like, int64_t Hkv, int64_t D, void
   const int64_t shape[4] = {kp->size(0), Hkv, kp->size(2), D};
   const int dev = like.get_device();
   if (!is(kp, like.scalar_type(), dev, shape) || !is(vp, like.scalar_type(), dev, shape)) return false;
-  *k = kp->data_ptr();
-  *v = vp->data_ptr();
+  *k = memory(*kp);
+  *v = memory(*vp);
   p->num = static_cast<int>(shape[0]);
   p->size = static_cast<int>(shape[2]);
   return true;
@@ -139,7 +148,7 @@ bool latent_pool(PyObject* cache, const at::Tensor& like, void** pool, Pages* p)
   if (!t || t->dim() != 3 || !all_fit(*t) ||
       !is(t, like.scalar_type(), like.get_device(), {t->size(0), t->size(1), kRow}))
     return false;
-  *pool = t->data_ptr();
+  *pool = memory(*t);
   p->num = static_cast<int>(t->size(0));
   p->size = static_cast<int>(t->size(1));
   return true;
@@ -212,8 +221,8 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     else if (!number(a[4], &scale))
       return not_taken();
     at::Tensor o = at::empty_like(*q), lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched(lib.fwd_paged, q->data_ptr(), k, v, p.table, p.start, o.data_ptr(),
-                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Hkv), n32(Sq), n32(D),
+    const bool ok = launched(lib.fwd_paged, memory(*q), k, v, p.table, p.start, memory(o),
+                             static_cast<float*>(memory(lse)), n32(B), n32(H), n32(Hkv), n32(Sq), n32(D),
                              p.num, p.size, p.max, static_cast<float>(scale), dtype_of(*q),
                              static_cast<float>(cap), slopes, nullptr, 0, stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
@@ -234,8 +243,8 @@ PyObject* fwd_latent(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return not_taken();
     at::Tensor o = at::empty({B, H, Sq, kLatent}, q->options());
     at::Tensor lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched(lib.fwd_latent, q->data_ptr(), pool, p.table, p.start, o.data_ptr(),
-                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), p.num, p.size,
+    const bool ok = launched(lib.fwd_latent, memory(*q), pool, p.table, p.start, memory(o),
+                             static_cast<float*>(memory(lse)), n32(B), n32(H), n32(Sq), p.num, p.size,
                              p.max, static_cast<float>(scale), dtype_of(*q), nullptr, 0, stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
   });
@@ -256,8 +265,8 @@ PyObject* fwd_expanded(PyObject*, PyObject* const* a, Py_ssize_t n) {
       return not_taken();
     at::Tensor o = at::empty({B, H, Sq, kNope}, q->options());
     at::Tensor lse = at::empty({B, H, Sq}, q->options().dtype(at::kFloat));
-    const bool ok = launched(lib.fwd_expanded, q->data_ptr(), kv->data_ptr(), r->data_ptr(), o.data_ptr(),
-                             static_cast<float*>(lse.data_ptr()), n32(B), n32(H), n32(Sq), n32(Skv),
+    const bool ok = launched(lib.fwd_expanded, memory(*q), memory(*kv), memory(*r), memory(o),
+                             static_cast<float*>(memory(lse)), n32(B), n32(H), n32(Sq), n32(Skv),
                              static_cast<float>(scale), a[3] == Py_True, dtype_of(*q), nullptr, 0,
                              stream_of(*q));
     return ok ? outputs(o, lse) : not_taken();
@@ -296,10 +305,10 @@ PyObject* paged_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (Hkv < 1 || H % Hkv != 0 || !is(t, k->scalar_type(), dev, {B, H, S, D}) ||
           !is(o, k->scalar_type(), dev, t->sizes()))
         return not_taken();
-      q = t->data_ptr();
-      q_out = o->data_ptr();
+      q = memory(*t);
+      q_out = memory(*o);
     }
-    const bool ok = launched(lib.paged_write, q, k->data_ptr(), v->data_ptr(), q_out, kp, vp, p.table,
+    const bool ok = launched(lib.paged_write, q, memory(*k), memory(*v), q_out, kp, vp, p.table,
                              p.start, p.count, freqs, n32(rotary), a[7] == Py_True, n32(B), n32(H),
                              n32(Hkv), n32(S), n32(D), p.num, p.size, p.max, dtype_of(*k), stream_of(*k));
     if (!ok) return not_taken();
@@ -321,8 +330,8 @@ PyObject* paged_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!is(v, k->scalar_type(), dev, k->sizes()) || !pools(a[0], *k, Hkv, D, &kp, &vp, &p) ||
         !places(a[1], a[2], a[3], dev, B, &p))
       return not_taken();
-    const bool ok = launched(lib.paged_read, kp, vp, p.table, p.start, p.count, k->data_ptr(),
-                             v->data_ptr(), n32(B), n32(Hkv), n32(S), n32(D), p.num, p.size, p.max,
+    const bool ok = launched(lib.paged_read, kp, vp, p.table, p.start, p.count, memory(*k),
+                             memory(*v), n32(B), n32(Hkv), n32(S), n32(D), p.num, p.size, p.max,
                              dtype_of(*k), stream_of(*k));
     if (!ok) return not_taken();
     Py_RETURN_NONE;
@@ -353,10 +362,10 @@ PyObject* latent_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
       width = o->size(3);
       if (!is(o, c->scalar_type(), dev, {B, H, S, width}) || !is(t, c->scalar_type(), dev, {B, H, S, kRope}))
         return not_taken();
-      q_rope = t->data_ptr();
-      q = o->data_ptr();
+      q_rope = memory(*t);
+      q = memory(*o);
     }
-    const bool ok = launched(lib.latent_write, c->data_ptr(), r->data_ptr(), pool, q_rope, q, p.table,
+    const bool ok = launched(lib.latent_write, memory(*c), memory(*r), pool, q_rope, q, p.table,
                              p.start, p.count, freqs, a[7] == Py_True, n32(B), n32(H), n32(S), n32(width),
                              p.num, p.size, p.max, dtype_of(*c), stream_of(*c));
     if (!ok) return not_taken();
@@ -375,7 +384,7 @@ PyObject* latent_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* pool;
     if (!latent_pool(a[0], *c, &pool, &p) || !places(a[1], a[2], a[3], c->get_device(), c->size(0), &p))
       return not_taken();
-    const bool ok = launched(lib.latent_read, pool, p.table, p.start, p.count, c->data_ptr(), r->data_ptr(),
+    const bool ok = launched(lib.latent_read, pool, p.table, p.start, p.count, memory(*c), memory(*r),
                              n32(c->size(0)), n32(c->size(1)), p.num, p.size, p.max, dtype_of(*c),
                              stream_of(*c));
     if (!ok) return not_taken();

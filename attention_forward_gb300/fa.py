@@ -310,7 +310,11 @@ def _ptr(t, name: str, dev: int, dtype, shape) -> int:
     try:
         if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
                 and t.is_contiguous()):
-            return t.data_ptr()
+            at = t.data_ptr()
+            if at or not t.numel():
+                return at
+            # 0 would stand for an argument left out
+            raise ValueError(f"{name} must be a tensor with memory (it is under a function transform)")
     except AttributeError:
         pass  # not a tensor
     _bad(t, name, dev, dtype, shape)
@@ -493,9 +497,9 @@ def _copy_args(k, v, cache, page_table, start, count):
                 and page_table.dtype is i32 and page_table.get_device() == dev
                 and page_table.is_contiguous()
                 and (start is None or start.dtype is i32 and start.shape == (B,)
-                     and start.get_device() == dev and start.is_contiguous())
+                     and start.get_device() == dev and start.is_contiguous() and start.data_ptr())
                 and (count is None or count.dtype is i32 and count.shape == (B,)
-                     and count.get_device() == dev and count.is_contiguous())):
+                     and count.get_device() == dev and count.is_contiguous() and count.data_ptr())):
             return (dev, (k.data_ptr(), v.data_ptr()),
                     (kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr()),
                     (page_table.data_ptr(), None if start is None else start.data_ptr(),

@@ -85,6 +85,50 @@ def child(transform):
     print("alive")
 
 
+def left_out():
+    """Arguments that may be left out are not taken for that where they have no memory."""
+    import torch
+
+    import test_native_binding_gpu as plain
+    from attention_forward_gb300 import fa
+
+    x = plain.Inputs()
+    one = x.q[:, :, :1].contiguous()
+    four = fa.fa_cache_empty(8, 2, 16, 64)
+    doc = torch.zeros((2, 30), dtype=torch.int32, device="cuda")
+    calls = [
+        (lambda q: fa.fa_paged_write(x.k, x.v, x.cache, x.table, q=q, q_out=q), x.q),
+        (lambda s: fa.fa_paged_write(x.k, x.v, x.cache, x.table, s), x.start),
+        (lambda n: fa.fa_paged_write(x.k, x.v, x.cache, x.table, None, n), x.count),
+        (lambda f: fa.fa_paged_write(x.k, x.v, x.cache, x.table, freqs=f), x.freqs),
+        (lambda s: fa.fa_paged_read(x.cache, x.table, s, None, x.out), x.start),
+        (lambda n: fa.fa_paged_read(x.cache, x.table, None, n, x.out), x.count),
+        (lambda s: fa.fa_fwd_paged(one, x.cache, x.table, x.length, slopes=s), x.slopes),
+        (lambda s: fa.fa_latent_write(x.c, x.r, x.latent, x.table, s), x.start),
+        (lambda n: fa.fa_latent_write(x.c, x.r, x.latent, x.table, None, n), x.count),
+        (lambda f: fa.fa_latent_write(x.c, x.r, x.latent, x.table, freqs=f), x.freqs),
+        (lambda q: fa.fa_latent_write(x.c, x.r, x.latent, x.table, q_rope=q, q=q),
+         x.wide[..., :64].contiguous()),
+        (lambda s: fa.fa_latent_read(x.latent, x.table, s, None, x.lout), x.start),
+        (lambda n: fa.fa_latent_read(x.latent, x.table, None, n, x.lout), x.count),
+        (lambda s: fa.fa_cache_write(x.k, x.v, four, x.table, s), x.start),
+        (lambda n: fa.fa_cache_write(x.k, x.v, four, x.table, None, n), x.count),
+        (lambda s: fa.fa_fwd_score(x.q, x.k, x.v, slopes=s), x.slopes),
+        (lambda d: fa.fa_fwd_score(x.q, x.k, x.v, doc_q=d, doc_k=d), doc),
+    ]
+    kept = (*x.cache, x.latent, *x.out, *x.lout, *four)
+    before = [t.clone() for t in kept]
+    for i, (call, t) in enumerate(calls):
+        assert under("functionalize", call, t), f"call {i} was not refused"
+    torch.cuda.synchronize()
+    for a, b in zip(before, kept):
+        assert torch.equal(a, b)
+
+
+def test_an_argument_without_memory_is_not_one_left_out():
+    left_out()
+
+
 @pytest.mark.parametrize("transform", TRANSFORMS)
 def test_refused_with_an_exception(transform):
     r = subprocess.run([sys.executable, os.path.abspath(__file__), transform], cwd=os.path.dirname(TESTS),
