@@ -61,7 +61,7 @@ struct PagedAttnParams {
   int B, H, Hkv, Sq;
   int rows;           // (H / Hkv) * Sq query rows per kv head
   int part_rows;      // rows that a part holds: a CTA's, up to 4, 8, 16 or a multiple of 32
-  int n_row_blocks;   // of a CTA's rows, or a cluster's
+  int n_row_blocks;   // of a CTA's rows, or a pair's
   int sms;
   int whole;          // CTAs take whole units: no parts, no merge
   int num_pages, page_shift, max_pages;
@@ -77,9 +77,10 @@ cudaError_t launch_paged_read(bool latent, const PagedReadParams& p, cudaStream_
 // Query rows that one pass of the attention over the keys takes, and the CTAs that
 // an SM holds.  kind: 64 or 128, a head's channels; kLatent, latent rows.
 int paged_attn_row_block(int kind, int rows);
-// CTAs of a cluster, which share the keys: 2 for latent rows where there are more query
-// rows than a CTA takes.
-int paged_attn_cluster(int kind, int rows);
+// CTAs that take the same keys side by side: 2 for latent rows where there are more query
+// rows than a CTA takes (128 heads, 32 sequences of up to 8192 rows: 96.2 us; each block of
+// rows as a unit of its own, whose keys are read at another time, 107.9).
+int paged_attn_peers(int kind, int rows);
 // A CTA's least share of the keys, in chunks: the whole pipeline starts in one chunk's
 // time, and the merge's is the same for any number of parts.  By 1, 2 and 4 chunks, us:
 // 3 sequences of 704 latent keys 10.3, 12.5, 14.9; 8 units of 704 keys (128 channels)
@@ -87,16 +88,16 @@ int paged_attn_cluster(int kind, int rows);
 constexpr int kPagedMinChunks = 1;
 // The end of a segment (a range of one unit's keys) takes as long as so many chunks: a unit
 // is dealt as so many more, behind its own, so that a CTA with two segments has fewer
-// chunks (pairs, 32 sequences of 8192 rows: 98.4 to 96.4 us; 8 units of 16384 keys: 20.0 to
-// 19.5 us).
-constexpr int paged_segment(int cluster) { return cluster == 2 ? 3 : 1; }
+// chunks (pairs, by 1 and 3: 32 sequences of 8192 rows 112 and 111 us, 4 of 2048 and
+// 4 tokens 27.9 and 27.0; by 0 and 1, 8 units of 16384 keys: 20.0 and 19.5 us).
+constexpr int paged_segment(int peers) { return peers == 2 ? 3 : 1; }
 // Whether page tables with room for that many keys are dealt in whole units, without a
 // merge.  Whole and split, us: 8 units of 128 channels 8.5 and 8.4 at 512 keys, 10.2 and
 // 8.6 at 704; 64 units 10.3 and 12.3 at 704, 13.3 and 12.6 at 1024; latent rows, 1 unit
 // 6.9 and 9.4 at 128 keys, 9.6 and 9.4 at 256, 64 units 14.7 and 15.3 at 512, 18.9 and
 // 17.9 at 704, 152 units 26.6 and 31.1 at 704.
 bool paged_attn_whole(int kind, long long units, int room, int sm_count);
-// CTAs for `units` (of a cluster's rows).
+// CTAs for `units` (of a CTA's rows, or a pair's).
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
 cudaError_t launch_paged_attn(int kind, bool bf16, const CUtensorMap& q, const CUtensorMap& k,
                               const CUtensorMap& v, const PagedAttnParams& p, int grid,

@@ -29,7 +29,7 @@ int paged_attn_row_block(int kind, int rows) {
   return kind == kLatent && rows <= 32 ? 32 : 64;
 }
 
-int paged_attn_cluster(int kind, int rows) { return kind == kLatent && rows > 64 ? 2 : 1; }
+int paged_attn_peers(int kind, int rows) { return kind == kLatent && rows > 64 ? 2 : 1; }
 
 // CTAs an SM holds (PagedShape's kCtas).
 static int paged_attn_ctas(int kind, int block) {
@@ -48,14 +48,14 @@ bool paged_attn_whole(int kind, long long units, int room, int sm_count) {
 }
 
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count) {
-  const int cluster = paged_attn_cluster(kind, rows);
+  const int peers = paged_attn_peers(kind, rows);
   const long long chunks =
-      units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys + paged_segment(cluster));
+      units * ((room + kCacheAttnKeys - 1) / kCacheAttnKeys + paged_segment(peers));
   const long long most = paged_attn_whole(kind, units, room, sm_count)
                              ? units : (chunks + kPagedMinChunks - 1) / kPagedMinChunks;
   const long long slots = static_cast<long long>(sm_count > 0 ? sm_count : 152) *
-                          paged_attn_ctas(kind, paged_attn_row_block(kind, rows)) / cluster;
-  return static_cast<int>(most < slots ? most : slots) * cluster;
+                          paged_attn_ctas(kind, paged_attn_row_block(kind, rows)) / peers;
+  return static_cast<int>(most < slots ? most : slots) * peers;
 }
 
 }  // namespace fa
@@ -152,7 +152,7 @@ bool chunks_ok(int kind, int B, int H, int Hkv, int Sq, const PageShape& s) {
   const int block = fa::paged_attn_row_block(kind, static_cast<int>(rows));
   const long long chunks = (static_cast<long long>(s.max_pages) * s.page_size +
                             fa::kCacheAttnKeys - 1) / fa::kCacheAttnKeys +
-                           fa::paged_segment(fa::paged_attn_cluster(kind, static_cast<int>(rows)));
+                           fa::paged_segment(fa::paged_attn_peers(kind, static_cast<int>(rows)));
   return static_cast<long long>(B) * Hkv * ((rows + block - 1) / block) * chunks <= fa::kCacheMaxChunks;
 }
 
@@ -166,8 +166,8 @@ AttnPlan plan_attn(int kind, int B, int H, int Hkv, int Sq, const PageShape& s, 
   AttnPlan a{};
   const int rows = (H / Hkv) * Sq, block = fa::paged_attn_row_block(kind, rows);
   const int room = s.max_pages * s.page_size;
-  const int cluster_rows = block * fa::paged_attn_cluster(kind, rows);
-  a.row_blocks = (rows + cluster_rows - 1) / cluster_rows;
+  const int unit_rows = block * fa::paged_attn_peers(kind, rows);
+  a.row_blocks = (rows + unit_rows - 1) / unit_rows;
   a.part_rows = std::min(rows, block);
   a.part_rows = a.part_rows > 16   ? (a.part_rows + 31) & ~31
                 : a.part_rows > 8 ? 16

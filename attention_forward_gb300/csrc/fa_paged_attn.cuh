@@ -32,10 +32,15 @@
 //
 // Bound, and measured (in a CUDA graph, merge included): 32 sequences of 8192 keys, 8 kv
 // heads of 128 channels, by HBM: 139 us, 6.4 TB/s; latent rows, 64 sequences of 4096 and
-// 16 heads, by HBM between 13 us of start, end and merge: 54.5 us; 32 of 8192 and 128
-// heads 95.5 us: a tile of 64 keys takes 2700 cycles where its products take 2040, for two
-// tiles and the queries fill shared memory, a tile is reloaded only behind its product, and
-// arrives 1500 cycles later.
+// 16 heads, by HBM between 13 us of start, end and merge: 54.5 us; 32 of up to
+// 8192 and 128 heads 96 us: a tile of 64 keys takes 2700 cycles where its products take 2040,
+// for two tiles and the queries fill shared memory, and a tile is reloaded only behind its
+// product.
+//
+// More than 64 rows of latent attention are dealt to pairs of CTAs, neighbours in the grid,
+// which go through the same keys at about the same time, each for 64 rows and each with
+// loads of its own: the second to ask finds a tile in L2.  Nothing makes them wait for one
+// another (started as a cluster of two they are no faster).
 //
 // Every wait is bounded by the watchdog, as in the prefill kernels.
 #pragma once
@@ -49,14 +54,14 @@ constexpr int kPagedKeys = kCacheAttnKeys;  // 64 keys: a tile, and a chunk of t
 
 // kKC, kVC: 64-channel chunks of a key and of a value; kShared: the value is the
 // key's first chunks.  kN: query rows of a CTA.
-// kCluster: CTAs that share the keys, each with a block of query rows (latent rows
-// only).
+// kPeers: CTAs, next to each other in the grid, that take the same keys, each for a block of
+// query rows (latent rows only).
 template <int kKC_, int kVC_, bool kShared_, int kN_, int kStages_, int kCtas_, int kPs_ = 2,
-          int kCluster_ = 1>
+          int kPeers_ = 1>
 struct PagedShape {
   static constexpr int kKC = kKC_, kVC = kVC_, kN = kN_, kStages = kStages_, kCtas = kCtas_;
   static constexpr int kPs = kPs_;  // buffers for P
-  static constexpr int kCluster = kCluster_;
+  static constexpr int kPeers = kPeers_;
   static constexpr bool kShared = kShared_;
   // groups of four softmax warps, each with its share of the query rows
   static constexpr int kGroups = kN == 64 ? 2 : 1, kRows = kN / kGroups;
@@ -68,7 +73,7 @@ struct PagedShape {
   static constexpr int kStageBytes = kTileK + kTileV;
   static constexpr int kVTile = kShared ? kTileK : kTileV;       // from a tile's V to the next
   static constexpr int kVStride = (kShared ? kKC : kVC) * 1024;  // from 8 keys to the next 8
-  static constexpr int kSegment = paged_segment(kCluster);
+  static constexpr int kSegment = paged_segment(kPeers);
   static constexpr int kQBytes = kN * 128 * kKC;
   static constexpr int kPBytes = kN * 128;
   static constexpr int kBlocks = kVC == 1 ? 1 : kVC / 2;  // O^T in blocks of 128 channels (64)
@@ -78,7 +83,7 @@ struct PagedShape {
       kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr int kOffP = kQBytes, kOffRing = kOffP + kPs * kPBytes;
   static constexpr int kOffMisc = kOffRing + kStages * kStageBytes;
-  static_assert(kCluster == 1 || (kCluster == 2 && kShared), "pairs over latent rows");
+  static_assert(kPeers == 1 || (kPeers == 2 && kShared), "pairs over latent rows");
   static_assert(kVC == 1 || kVC % 2 == 0, "values of 64 channels, or of 128 a block");
   static_assert(kOffP % 1024 == 0 && kOffRing % 1024 == 0, "128-byte swizzled tiles");
   static_assert(kCols <= 512 && kCtas * kTmemCols <= 512, "tensor memory");
@@ -131,7 +136,7 @@ __device__ __forceinline__ int paged_part_row(int i, int part_rows) {
 
 // The CTA's segments: ranges of one unit's keys.
 struct PagedWalk {
-  int cta, ctas, rank;   // of the deal: a CTA, or a cluster; the CTA's rank in it
+  int cta, ctas, rank;   // of the deal: a CTA, or a pair; the CTA's rank in it
   int cur, first, last;  // chunks, or units where they are not split
   int b, len, before;    // the sequence, its length, the chunks of those before it
 };
@@ -144,7 +149,7 @@ struct PagedSeg {
 
 template <class S>
 __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& w, PagedSeg& s) {
-  constexpr int kN = S::kN, kCluster = S::kCluster;
+  constexpr int kN = S::kN, kPeers = S::kPeers;
   const int units = p.Hkv * p.n_row_blocks;
   int seq_chunks, unit, chunk0;
   while (true) {
@@ -170,10 +175,10 @@ __device__ __forceinline__ bool paged_next(const PagedAttnParams& p, PagedWalk& 
   }
   const int n_chunks = p.whole ? seq_chunks : min(seq_chunks - chunk0, w.last - w.cur);
   s.whole = n_chunks == seq_chunks;
-  s.part = (2 * w.cta + (w.cur == w.first ? 0 : 1)) * kCluster + w.rank;
+  s.part = (2 * w.cta + (w.cur == w.first ? 0 : 1)) * kPeers + w.rank;
   s.hk = unit / p.n_row_blocks;
-  s.row0 = ((unit - s.hk * p.n_row_blocks) * kCluster + w.rank) * kN;
-  s.n_rows = max(0, min(kN, p.rows - s.row0));  // a cluster's last may have none
+  s.row0 = ((unit - s.hk * p.n_row_blocks) * kPeers + w.rank) * kN;
+  s.n_rows = max(0, min(kN, p.rows - s.row0));  // a pair's last may have none
   s.out_row0 = (static_cast<long long>(w.b) * p.Hkv + s.hk) * p.rows + s.row0;
   s.seq = w.b;
   s.len = w.len;
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   if (threadIdx.x == 0) {
     for (int i = 0; i < PagedMiscBars::kMaxStages; ++i) {
       mbar_init(k_full + 8 * i, 1);
-      mbar_init(k_empty + 8 * i, S::kCluster);
+      mbar_init(k_empty + 8 * i, 1);
       mbar_init(v_full + 8 * i, 1);
       mbar_init(v_empty + 8 * i, 1);
     }
@@ -246,7 +251,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     if constexpr (!S::kShared) tma_prefetch_desc(&tmV);
   }
   tc_fence_before();
-  if constexpr (S::kCluster > 1) cluster_sync_all();  // its barriers are there
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
@@ -255,9 +259,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
   grid_launch_dependents();  // this grid's CTAs have their tensor memory
 
   PagedWalk walk{};
-  walk.cta = static_cast<int>(blockIdx.x) / S::kCluster;
-  walk.ctas = static_cast<int>(gridDim.x) / S::kCluster;
-  walk.rank = S::kCluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  walk.cta = static_cast<int>(blockIdx.x) / S::kPeers;
+  walk.ctas = static_cast<int>(gridDim.x) / S::kPeers;
+  walk.rank = static_cast<int>(blockIdx.x) % S::kPeers;
   if (p.whole) {
     walk.first = walk.cta;
     walk.last = p.B * p.Hkv * p.n_row_blocks;
@@ -623,10 +627,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
           for (int blk = 0; blk < S::kBlocks; ++blk)
             umma_f16_ss(tmem + S::kColO + blk * kN, a + blk * (2048 >> 4) + k * (2 * S::kVStride >> 4),
                         b + 2 * k, kIdescO, (o > 0 || k > 0) ? 1u : 0u);
-          if constexpr (S::kCluster > 1)
-            umma_commit_multicast(k_empty + 8 * (4 * stage + k), 3);
-          else if constexpr (S::kShared)
-            umma_commit(k_empty + 8 * (4 * stage + k));
+          if constexpr (S::kShared) umma_commit(k_empty + 8 * (4 * stage + k));
         }
         if constexpr (!S::kShared) umma_commit(v_empty + 8 * stage);
         umma_commit(o_done + 8 * ((t0 + o) & 1u));
@@ -716,34 +717,28 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
         for (int k = 0; ok && k < 4 && j0 + k < seg.n_tiles; ++k, ++t) {
           const uint32_t stage = t % kStages, full = full0 + 8 * stage, par = ((t / kStages) & 1u) ^ 1u;
           const uint32_t dst = ring + stage * bytes;
-          // a latent stage 16 keys at a time; in a cluster of two half of them, which go to
-          // both CTAs (an mbarrier may count the other's bytes before its own expects them)
-          constexpr int kTurns = S::kShared ? 4 / S::kCluster : 1;
+          // a latent stage 16 keys at a time
+          constexpr int kBlocks = S::kShared ? 4 : 1;
 #pragma unroll 1
-          for (int i = 0; ok && i < kTurns; ++i) {
-            const int block = walk.rank * kTurns + i;
-            ok = wait_bar_warp(empty0 + 8 * (S::kShared ? 4 * stage + block : stage), par, ctl);
+          for (int block = 0; ok && block < kBlocks; ++block) {
+            ok = wait_bar_warp(empty0 + 8 * (kBlocks * stage + block), par, ctl);
             if (!ok) break;
-            if (i == 0 && lane == 0) {
+            if (block == 0 && lane == 0) {
               if (is_k) sm.bad[t % kPagedBad] = (bad >> (8 * k)) & 0xffu;
               mbar_arrive_expect_tx(full, bytes);
             }
             __syncwarp();
-            if ((lane >> 3) == k && (!S::kShared || ((lane & 7) >> 1) == block)) {
-              if constexpr (S::kCluster > 1)
-                tma_load_4d_multicast(dst, tm, full, 0, row, 0, at, 3);
-              else
-                tma_load_4d(dst, tm, full, 0, row, 0, at);
-            }
+            if ((lane >> 3) == k && (!S::kShared || ((lane & 7) >> 1) == block))
+              tma_load_4d(dst, tm, full, 0, row, 0, at);
             __syncwarp();
           }
-          // two latent tiles in flight are not enough for HBM's latency: the next four
-          // come to L2 meanwhile
-          if constexpr (S::kCluster > 1)
+          // two latent tiles in flight are not enough for HBM's latency: the next four come
+          // to L2 meanwhile.  (128 heads, 32 sequences of up to 8192 rows: 96.2 us, without
+          // 102.6; half of them by each of a pair, whose CTAs may have drifted apart, 96.9.)
+          if constexpr (S::kPeers > 1)
             if (k == 1) {
               const int next_row = row_of(key + 4 * kPagedKeys, ahead);
-              if (next_row != p.pool_rows && ((lane & 7) >> 2) == walk.rank)
-                tma_prefetch_l2_4d(tm, 0, next_row, 0, at);
+              if (next_row != p.pool_rows) tma_prefetch_l2_4d(tm, 0, next_row, 0, at);
               __syncwarp();
             }
         }
@@ -753,11 +748,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     // the last tile's unsent: the wait is bounded)
     for (uint32_t i = t > kStages ? t - kStages : 0u; i < t; ++i)
       wait_drain(full0 + 8 * (i % kStages), (i / kStages) & 1u, p.timeout_ns);
-    // and so does every arrival that the other CTA's products make here
-    if constexpr (S::kCluster > 1)
-      for (uint32_t i = t > kStages ? t - kStages : 0u; ok && i < t; ++i)
-        for (uint32_t k = 0; k < 4; ++k)
-          wait_drain(k_empty + 8 * (4 * (i % kStages) + k), (i / kStages) & 1u, p.timeout_ns);
     __syncwarp();
   }
 
@@ -767,7 +757,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kCtas)
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
-  if constexpr (S::kCluster > 1) cluster_sync_all();  // the other CTA writes here no more
 }
 
 // The units that several CTAs shared: O = sum_s w_s O_s / sum_s w_s over their parts,
@@ -798,11 +787,11 @@ __global__ void __launch_bounds__(kPagedMergeThreads, kCh > 8 ? 4 : 1)
     alignas(16) uint16_t out[kN * (kCh + 8) + kN / 2];
   } end;
   const int tid = static_cast<int>(threadIdx.x);
-  // a unit of the deal and, in clusters, the rank of the CTA whose rows these are
+  // a unit of the deal and, in pairs, the rank of the CTA whose rows these are
   const int units = p.Hkv * p.n_row_blocks, rank = static_cast<int>(blockIdx.z);
   const int b = static_cast<int>(blockIdx.x) / units, unit = static_cast<int>(blockIdx.x) - b * units;
   const int hk = unit / p.n_row_blocks;
-  const int rb = (unit - hk * p.n_row_blocks) * S::kCluster + rank;
+  const int rb = (unit - hk * p.n_row_blocks) * S::kPeers + rank;
   const int ch0 = static_cast<int>(blockIdx.y) * kCh;
   int upto;
   const int all = cache_scan(p, scan, false, upto, S::kSegment);
@@ -821,7 +810,7 @@ __global__ void __launch_bounds__(kPagedMergeThreads, kCh > 8 ? 4 : 1)
   if (x0 == x1) return;
   // a CTA's first segment, except where the unit begins inside x0
   const int inside = deal.begin(x0) < start ? 1 : 0;
-  auto part_of = [&](int s) { return (2 * (x0 + s) + (s == 0 ? inside : 0)) * S::kCluster + rank; };
+  auto part_of = [&](int s) { return (2 * (x0 + s) + (s == 0 ? inside : 0)) * S::kPeers + rank; };
   const int n_parts = x1 - x0 + 1, n_rows = max(0, min(kN, p.rows - rb * kN));
   const int quads = p.part_rows / 4, items = kCh * quads;  // four rows of a channel each
   const int groups = items < kThr ? kThr / items : 1;

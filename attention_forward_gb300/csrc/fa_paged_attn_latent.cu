@@ -14,7 +14,7 @@ cudaError_t launch_paged_attn_latent(bool bf16, const CUtensorMap& q, const CUte
     case 16: return with(PagedShape<9, 8, true, 16, 2, 1>{});
     case 32: return with(PagedShape<9, 8, true, 32, 2, 1>{});
     default:
-      return paged_attn_cluster(kLatent, p.rows) == 2 ? with(PagedShape<9, 8, true, 64, 2, 1, 1, 2>{})
+      return paged_attn_peers(kLatent, p.rows) == 2 ? with(PagedShape<9, 8, true, 64, 2, 1, 1, 2>{})
                                                       : with(PagedShape<9, 8, true, 64, 2, 1, 1>{});
   }
 }

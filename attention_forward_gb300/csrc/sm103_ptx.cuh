@@ -141,18 +141,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* desc, uint
       : "memory");
 }
 
-// The same into the CTAs of `mask` of this cluster, at the same offset in each, every
-// one's share signalled on its own mbarrier at the same offset.
-__device__ __forceinline__ void tma_load_4d_multicast(uint32_t dst, const void* desc, uint32_t bar,
-                                                      int32_t x, int32_t y, int32_t z, int32_t w,
-                                                      uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes."
-      "multicast::cluster [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(desc)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w), "h"(mask)
-      : "memory");
-}
-
 // Prefetch a 3-D tile into L2 (no shared memory, no completion signal).
 __device__ __forceinline__ void tma_prefetch_l2_3d(const void* desc, int32_t x,
                                                    int32_t y, int32_t z) {
@@ -470,17 +458,6 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
       "[%0];\n\t}" ::"r"(bar)
-      : "memory");
-}
-
-// As umma_commit, arriving on the mbarrier at this offset in each CTA of `mask`.
-__device__ __forceinline__ void umma_commit_multicast(uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster."
-      "multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-      "h"(mask)
       : "memory");
 }
 
