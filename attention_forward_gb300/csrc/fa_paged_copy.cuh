@@ -3,10 +3,11 @@
 // Rotation of a pair (x, y) of channels at position n with frequency f (radians a
 // position):  (x cos a - y sin a, y cos a + x sin a),  a = n f.
 // The angle is held in turns as a 64-bit fraction: f / 2 pi to 2^-61 of a turn, whose
-// product with n is exact modulo a turn; its upper 32 bits go to the sine and cosine.
-// All in integers: the GPU makes two double-precision products a cycle and
-// multiprocessor.  At n = 2^24 and f = 1 the angle is off by 2^-28 of a radian; n f in
-// fp32 would be off by half a radian.
+// product with n is exact modulo a turn; its upper 32 bits, rounded to fp32, go to the sine
+// and cosine.  All in integers: the GPU makes two double-precision products a cycle and
+// multiprocessor.  That rounding is nearly all of the angle's error: half turns in [-1, 1)
+// are off by 2^-25, which is 2^-23.3 radian; f's fraction adds 2^-35 f at n = 2^24.  n f in
+// fp32 would be off by half a radian there.
 //
 // Both kernels only move bytes.  Write: a block takes 2^token_shift tokens of a
 // sequence and a slice of their heads.  A thread keeps to 16 channels of one token:
@@ -49,7 +50,8 @@ __device__ __forceinline__ unsigned long long rope_step(float f) {
 // Cosine and sine of the angle n steps.
 __device__ __forceinline__ float2 rope_unit(int n, unsigned long long step) {
   const unsigned long long at = step * static_cast<unsigned long long>(static_cast<long long>(n));
-  // the upper half as a signed number: half turns in [-1, 1)
+  // the upper half as a signed number: half turns in [-1, 1), rounded to 24 bits as sine and
+  // cosine are
   const float half = static_cast<float>(static_cast<int>(at >> 32)) * 4.656612873077393e-10f;
   float2 u;
   sincospif(half, &u.y, &u.x);

@@ -457,9 +457,9 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
  *          freqs[j].  NULL with rotary 0: nothing is rotated.  Finite, and below
  *          2^64 in magnitude: what is not turns nothing.
  *   interleaved  0: pair j is channels j, j + rotary / 2; 1: 2 j, 2 j + 1
- * The angle is exact to 2^-28 radian up to n = 2^24 and freqs[j] = 1 (and in
- * proportion above); a rotated value is rounded once to its type behind fp32
- * work.  No two tokens of a call may go to the same slot.
+ * The angle is off by 2^-23 radian at most for n up to 2^24 and freqs[j] up to
+ * 2^8 in magnitude (above, by 2^-35 freqs[j] more): sine and cosine take it as
+ * fp32 half turns.  A rotated value is rounded once to its type behind fp32 work.  No two tokens of a call may go to the same slot.
  *
  * fa_paged_read -- positions start[b] ... start[b] + count[b] - 1 into rows 0 ...
  * of k, v [B, Hkv, S, D], as fa_cache_read.
