@@ -64,8 +64,9 @@ bool sizes_ok(int B, int H, int Sq, int Skv) {
 
 // Keys split where the items are fewer than the SMs, by the smallest estimate of the
 // time in ns: rounds of items, each its start and end and its key tiles, and the merge's
-// start and its parts through L2.  (16 heads, 509 rows, us by ranges: 1500 keys 32.3
-// whole, 25.1 by 3, 23.9 by 4; 4096 keys 76.0 whole, 36.6 by 4, 91.9 by 32.)
+// start and its parts through L2.  (16 heads, 509 rows, in a graph, us by ranges: 1500 keys
+// 32.3 whole, 29.6 by 2, 25.8 by 3, 24.1 by 4, 28.7 by 6; 4096 keys 76.1 whole, 36.7 by 4, 49.6
+// by 6, 91.9 by 32.  The plan takes 4 in both.)
 struct Plan {
   int n_qtiles, n_splits, tiles_per_split;
   size_t o_bytes, bytes;

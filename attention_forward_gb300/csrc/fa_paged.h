@@ -95,7 +95,9 @@ constexpr int paged_segment(int peers) { return peers == 2 ? 3 : 1; }
 // merge.  Whole and split, us: 8 units of 128 channels 8.5 and 8.4 at 512 keys, 10.2 and
 // 8.6 at 704; 64 units 10.3 and 12.3 at 704, 13.3 and 12.6 at 1024; latent rows, 1 unit
 // 6.9 and 9.4 at 128 keys, 9.6 and 9.4 at 256, 64 units 14.7 and 15.3 at 512, 18.9 and
-// 17.9 at 704, 152 units 26.6 and 31.1 at 704.
+// 17.9 at 704, 152 units 26.6 and 31.1 at 704.  17 to 64 rows of 128 channels: 8 units 10.2 and
+// 10.6 at 512 keys, 64 units 16.7 and 22.5 at 1024, 160 units 24.4 and 26.0 at 704, 31.2 and
+// 30.1 at 1024.
 bool paged_attn_whole(int kind, long long units, int room, int sm_count);
 // CTAs for `units` (of a CTA's rows, or a pair's).
 int paged_attn_grid(int kind, int rows, long long units, int room, int sm_count);
