@@ -759,8 +759,8 @@ def fa_paged_workspace_bytes(B: int, H: int, Hkv: int, Sq: int, D: int, page_siz
 def fa_fwd_paged(q, cache, page_table, length, scale: float | None = None, softcap: float = 0.0,
                  slopes=None, workspace=None, out=None, lse=None, stream=None):
     """Attention of the newest Sq tokens, q [B, H, Sq, D], over the 16-bit cache:
-    length[b] (int32) tokens of sequence b are in it, these included.  Returns
-    (o, lse)."""
+    length[b] (int32) tokens of sequence b are in it, these included.  Values are
+    finite, in bfloat16 below 2^88 in magnitude.  Returns (o, lse)."""
     if out is None and lse is None and workspace is None and stream is None:
         got = (_native or _load_native()).fwd_paged(q, cache, page_table, length, scale, softcap,
                                                     slopes)
@@ -906,7 +906,8 @@ def fa_fwd_latent(q, cache, page_table, length, scale: float | None = None, work
                   out=None, lse=None, stream=None):
     """Latent attention, absorbed: the newest Sq tokens' q [B, H, Sq, 576] over the
     cache's rows, whose first 512 channels are the values too.  length as for
-    fa_fwd_paged; scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 512], lse)."""
+    fa_fwd_paged, and the range of the rows' values; scale defaults to 192 ** -0.5.
+    Returns (o [B, H, Sq, 512], lse)."""
     if out is None and lse is None and workspace is None and stream is None:
         got = (_native or _load_native()).fwd_latent(q, cache, page_table, length, scale)
         if got is not NotImplemented:
@@ -944,7 +945,8 @@ def fa_fwd_expanded(q, kv, k_rope, causal: bool = False, scale: float | None = N
                     workspace=None, out=None, lse=None, stream=None):
     """Latent attention, expanded: q [B, H, Sq, 192], kv [B, H, Skv, 256] (a head's key
     of 128 channels, then its value), k_rope [B, Skv, 64] (the keys' shared part).
-    scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq, 128], lse)."""
+    Values as for fa_fwd_paged; scale defaults to 192 ** -0.5.  Returns (o [B, H, Sq,
+    128], lse)."""
     if out is None and lse is None and workspace is None and stream is None:
         got = (_native or _load_native()).fwd_expanded(q, kv, k_rope, causal, scale)
         if got is not NotImplemented:

@@ -459,7 +459,8 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
  *   interleaved  0: pair j is channels j, j + rotary / 2; 1: 2 j, 2 j + 1
  * The angle is off by 2^-23 radian at most for n up to 2^24 and freqs[j] up to
  * 2^8 in magnitude (above, by 2^-35 freqs[j] more): sine and cosine take it as
- * fp32 half turns.  A rotated value is rounded once to its type behind fp32 work.  No two tokens of a call may go to the same slot.
+ * fp32 half turns.  A rotated value is rounded once to its type behind fp32
+ * work.  No two tokens of a call may go to the same slot.
  *
  * fa_paged_read -- positions start[b] ... start[b] + count[b] - 1 into rows 0 ...
  * of k, v [B, Hkv, S, D], as fa_cache_read.
@@ -467,8 +468,10 @@ fa_status_t fa_fwd_cache(const void *q, const void *k_codes,
  * fa_fwd_paged -- attention of the newest tokens over the pages: fa_fwd_cache
  * with 16-bit keys and values.  Its arguments, limits (row blocks of 16 rows up
  * to (H / Hkv) * Sq = 16, else of 64, each counted with one chunk more),
- * workspace rules and masks are fa_fwd_cache's; a probability is rounded to the type of V for the product.  V
- * must be finite within a sequence's length; what lies past it may be anything.
+ * workspace rules and masks are fa_fwd_cache's; a probability is rounded to the
+ * type of V for the product.  V must be finite within a sequence's length, in
+ * bf16 below 2^88 in magnitude (unnormalised probabilities, up to 2^15 for each
+ * of 2^24 keys, times V are summed in fp32); what lies past it may be anything.
  */
 fa_status_t fa_paged_write(const void *q, const void *k, const void *v,
                            void *q_out, void *k_pages, void *v_pages,
@@ -516,7 +519,8 @@ fa_status_t fa_fwd_paged(const void *q, const void *k_pages,
  *   value expansion; lse [B, H, Sq]
  *   O = sum_j softmax_j(scale <q, row_j>) row_j[0 ... 511]
  * length, workspace and masks as for fa_fwd_paged (row blocks of 16, 32 or 64 of
- * the H * Sq rows).  Latent rows must be finite within a sequence's length.
+ * the H * Sq rows; of more than 64 rows, each counted with three chunks more).
+ * Latent rows must be finite within a sequence's length, in bf16 below 2^88.
  */
 fa_status_t fa_latent_write(const void *c, const void *k_rope, void *pages,
                             const void *q_rope, void *q, const int *page_table,
@@ -547,7 +551,7 @@ fa_status_t fa_fwd_latent(const void *q, const void *pages,
  *   o [B, H, Sq, 128], lse [B, H, Sq]
  *   x = scale * (<q[0 ... 127], key_j> + <q[128 ... 191], k_rope_j>)
  * with fa_fwd's masks and limits.  A masked key may hold anything; values must be
- * finite in every row.  A call whose items are fewer than the multiprocessors
+ * finite in every row, in bf16 below 2^88 in magnitude.  A call whose items are fewer than the multiprocessors
  * splits the keys when it has fa_expanded_workspace_bytes(...) of workspace
  * (256-byte aligned; NULL: the library's own for the stream, inside a capture
  * none).  Captured as fa_fwd_score is (fa_fwd's limits on scheduler slots hold).
