@@ -300,6 +300,9 @@ def _own_memory(tensors, stream) -> None:
             t.record_stream(stream)
 
 
+_INT = 0x7fffffff  # the largest size that the library is given
+
+
 def _bad(t, name: str, dev: int, dtype, shape):
     if not isinstance(t, torch.Tensor) or t.get_device() != dev or dev < 0:
         raise ValueError(f"{name} must be a tensor on the call's CUDA device")
@@ -469,6 +472,8 @@ def _pages(page_table, dev: int, B: int):
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
     n = page_table.shape[1]
+    if n > _INT:  # the library would take it for another number
+        raise ValueError("page_table must have fewer than 2^31 pages a sequence")
     return _ptr(page_table, "page_table", dev, torch.int32, (B, n)), n
 
 
@@ -495,7 +500,7 @@ def _copy_args(k, v, cache, page_table, start, count):
                 and vp.dtype is f16 and vp.shape == params and vp.get_device() == dev
                 and vp.is_contiguous()
                 and page_table.dtype is i32 and page_table.get_device() == dev
-                and page_table.is_contiguous()
+                and page_table.is_contiguous() and per <= _INT
                 and (start is None or start.dtype is i32 and start.shape == (B,)
                      and start.get_device() == dev and start.is_contiguous() and start.data_ptr())
                 and (count is None or count.dtype is i32 and count.shape == (B,)
@@ -576,7 +581,7 @@ def _attn_args(cache, page_table, length, dev: int, B: int, H: int, D: int):
                 and vp.dtype is f16 and vp.shape == params and vp.get_device() == dev
                 and vp.is_contiguous()
                 and page_table.dtype is i32 and page_table.get_device() == dev
-                and page_table.is_contiguous()
+                and page_table.is_contiguous() and per <= _INT
                 and length.dtype is i32 and length.shape == (B,)
                 and length.get_device() == dev and length.is_contiguous()):
             return (Hkv, kc.data_ptr(), kp.data_ptr(), vc.data_ptr(), vp.data_ptr(), pages, page,
